@@ -165,6 +165,108 @@ bam_status bam_attn_decode_paged(const void* q, const void* k_pages, const void*
                                  int num_pages, int D, const bam_params* p, void* ws,
                                  size_t ws_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving over a paged cache with drafted tokens
+ *
+ * Pages, block table and cache_lens are those of bam_attn_decode_paged, except
+ * that Hkv heads of keys and values may serve H = Hkv * group query heads
+ * (query head h reads key head h / group; k_pages, v_pages are
+ * [num_pages, Hkv, page, D]) and that a committed length may be 0.
+ *
+ * A draft of sequence b is a tree (or forest) of draft_lens[b] <= N nodes.
+ * Node i has its key and value in cache slot cache_lens[b] + i, behind the
+ * committed ones.  parents: device int32 [B, N]; parents[b][i] < i is the
+ * node that node i follows, -1 if it follows the committed sequence.  A NULL
+ * parents is a chain (node i follows node i - 1).  The depth of a node is its
+ * number of ancestors, and its position is cache_lens[b] + depth: siblings
+ * share a position, whatever their slots are.
+ *
+ * What only the device reads is checked there.  A length outside its range
+ * is clamped into it (cache_lens to [0, max_blocks*page], draft lengths to
+ * [0, N] and to the room behind the committed keys), a parent outside
+ * [-1, i) counts as -1, and each such case is recorded:
+ * bam_attn_check_status then returns BAM_ERR_INVALID_ARG.  Sequences share
+ * pages only if no call writes them.
+ * ------------------------------------------------------------------------- */
+
+/* Rotation by position of the first `dims` dimensions of a head vector, in
+ * pairs: pair f turns by the angle position * base^(-2 f / dims).  dims is a
+ * multiple of 16 from 0 (no rotation) to 64.  Angles are reduced exactly (a
+ * 64-bit fraction of a turn), so far positions keep their accuracy. */
+typedef struct {
+  double base;     /* > 0, finite; for example 10000                         */
+  int dims;
+  int interleaved; /* 0: pair f is (x[f], x[f + dims/2]); 1: (x[2f], x[2f+1]) */
+} bam_rope;
+
+/* Bytes of workspace of bam_kv_append_paged and bam_kv_keep_paged (their
+ * status words). */
+#define BAM_CACHE_WORKSPACE_BYTES 256u
+
+/* Appends keys and values behind the committed ones.  k, v: bf16
+ * [B, Hkv, N, D]; token i < new_lens[b] goes to slot cache_lens[b] + i (all N
+ * tokens when new_lens is NULL).  Keys, and the queries q [B, H, N, D] if
+ * given, are rotated by their positions when rope is given (NULL or dims 0:
+ * copied); values are copied.  q_out: bf16 [B, H, N, D], dense; it may be q
+ * itself if q is dense.  With parents (N <= 128) positions follow the tree,
+ * else token i has position cache_lens[b] + i.
+ *
+ * strides: element strides of k, v and q over batch, head and token (nine
+ * values, multiples of 8, >= 0), so that slices of a projection's output need
+ * no copy; NULL when all are dense.  The rows of tokens behind new_lens[b]
+ * are not written, in the pages nor in q_out.  A token whose slot lies behind
+ * the block table or whose page number is out of range is not written to the
+ * pages and is reported by bam_attn_check_status as BAM_ERR_INVALID_ARG.
+ * cache_lens is not changed.  One launch. */
+bam_status bam_kv_append_paged(const void* k, const void* v, const void* q, void* q_out,
+                               const int64_t* strides, void* k_pages, void* v_pages,
+                               const int* block_table, const int* cache_lens,
+                               const int* new_lens, const int* parents, int B, int H, int Hkv,
+                               int N, int page, int max_blocks, int num_pages, int D,
+                               const bam_rope* rope, void* ws, size_t ws_bytes,
+                               cudaStream_t stream);
+
+/* Attention of drafted tokens over the paged cache.  q: bf16 [B, H, N, D];
+ * node t < draft_lens[b] (all N when draft_lens is NULL) sees the committed
+ * keys, itself and its ancestors; 1 <= N <= 128.  Its query sits at position
+ * cache_lens[b] + depth(t): a committed key j is at distance
+ * cache_lens[b] + depth(t) - j, an ancestor i at depth(t) - depth(i), and
+ * n = cache_lens[b] + depth(t) + 1 for Scalable-Softmax.  A key that a node
+ * does not see has no effect on it, whatever it holds (NaN and infinities
+ * included).  A tree of one node is bam_attn_decode_paged with that token's
+ * length counted.  o: [B, H, N, D], fp32 when o_fp32 != 0, else bf16; lse:
+ * fp32 [B, H, N] or NULL; rows behind draft_lens[b] are left as they were.
+ * The weights enter the product with V as sums of bf16 parts: one part for
+ * bf16 output, three (24 bits) for fp32 output.  A page number out of range
+ * reads page 0 and is reported.  If a device wait of the call gives up, the
+ * rows of o and lse are written as NaN. */
+bam_status bam_attn_decode_tree_paged(const void* q, const void* k_pages, const void* v_pages,
+                                      const int* block_table, const int* cache_lens,
+                                      const int* draft_lens, const int* parents, void* o,
+                                      int o_fp32, float* lse, int B, int H, int Hkv, int N,
+                                      int page, int max_blocks, int num_pages, int D,
+                                      const bam_params* p, void* ws, size_t ws_bytes,
+                                      cudaStream_t stream);
+
+/* Bytes of workspace of bam_attn_decode_tree_paged (Tmax = max_blocks*page).
+ * Returns 0 for invalid sizes.  Host-only. */
+size_t bam_attn_tree_workspace_size(int B, int H, int Hkv, int N, int Tmax, int D);
+
+/* Keeps an accepted path.  accepted: device int32 [B], the last accepted node
+ * of each sequence's draft (-1: none).  The keys and values of the nodes from
+ * the root to it move, in order, to the slots behind the committed ones; their
+ * rotation stays right, since positions follow depth.  new_lens: device int32
+ * [B], cache_lens[b] plus the nodes kept; it may be cache_lens itself.  Slots
+ * behind the kept ones hold what is left of the draft.  1 <= N <= 128.  An
+ * accepted node outside [-1, draft_lens[b]) counts as -1, and a sequence with
+ * a page number out of range on its path keeps its pages as they were and its
+ * length; both are reported.  One launch. */
+bam_status bam_kv_keep_paged(void* k_pages, void* v_pages, const int* block_table,
+                             const int* cache_lens, const int* draft_lens, const int* parents,
+                             const int* accepted, int* new_lens, int B, int Hkv, int N, int page,
+                             int max_blocks, int num_pages, int D, void* ws, size_t ws_bytes,
+                             cudaStream_t stream);
+
 /* Synchronises `stream`, then reads and clears the device status word of
  * `ws`.  Returns BAM_OK, BAM_ERR_TIMEOUT (a device wait gave up),
  * BAM_ERR_INVALID_ARG (a device-read argument was out of range: a ragged or
@@ -261,7 +363,12 @@ enum {
   BAM_KERNEL_BWD_FINAL = 4,  /* dq conversion and scalar-gradient finish    */
   BAM_KERNEL_DECODE = 5,     /* split-KV decode                             */
   BAM_KERNEL_DECODE_COMBINE = 6,
-  BAM_KERNEL_COUNT = 7
+  BAM_KERNEL_KV_APPEND = 7,
+  BAM_KERNEL_TREE_PREP = 8,    /* tree attention: lengths, distance table     */
+  BAM_KERNEL_TREE = 9,         /* tree attention                              */
+  BAM_KERNEL_TREE_COMBINE = 10,
+  BAM_KERNEL_KV_KEEP = 11,
+  BAM_KERNEL_COUNT = 12
 };
 
 /* Instrumentation: while set, every launch of kernel `which` is bracketed

@@ -48,7 +48,12 @@ BAM_KERNEL_BWD = 3
 BAM_KERNEL_BWD_FINAL = 4
 BAM_KERNEL_DECODE = 5
 BAM_KERNEL_DECODE_COMBINE = 6
-BAM_KERNEL_COUNT = 7
+BAM_KERNEL_KV_APPEND = 7
+BAM_KERNEL_TREE_PREP = 8
+BAM_KERNEL_TREE = 9
+BAM_KERNEL_TREE_COMBINE = 10
+BAM_KERNEL_KV_KEEP = 11
+BAM_KERNEL_COUNT = 12
 
 # Every symbol that include/bam_attn.h declares.
 EXPORTED = (
@@ -69,10 +74,18 @@ EXPORTED = (
     "bam_attn_debug_arm_giveup",
     "bam_attn_debug_arm_giveup_noalloc",
     "bam_attn_bwd_schedule",
+    "bam_kv_append_paged",
+    "bam_attn_decode_tree_paged",
+    "bam_attn_tree_workspace_size",
+    "bam_kv_keep_paged",
 )
 
 # Size of the fixed device scratch of bam_attn_decode_noalloc.
 BAM_DECODE_NOALLOC_SCRATCH_BYTES = 4 << 20
+# Workspace of bam_kv_append_paged and bam_kv_keep_paged (status words only).
+BAM_CACHE_WORKSPACE_BYTES = 256
+# Most nodes of a draft with parents (tree attention, keep).
+BAM_TREE_MAX_NODES = 128
 
 
 class BamError(RuntimeError):
@@ -91,6 +104,14 @@ class BamParams(ctypes.Structure):
         ("causal", ctypes.c_int),
         ("ssmax", ctypes.c_int),
         ("prior", ctypes.c_int),
+    ]
+
+
+class BamRope(ctypes.Structure):
+    _fields_ = [
+        ("base", ctypes.c_double),
+        ("dims", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
     ]
 
 
@@ -148,6 +169,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         ip = ctypes.POINTER(ctypes.c_int)
         lib.bam_attn_bwd_schedule.restype = i
         lib.bam_attn_bwd_schedule.argtypes = [i, i, i, i, i, ip, ip, i]
+        lp = ctypes.POINTER(ctypes.c_int64)
+        lib.bam_kv_append_paged.restype = i
+        lib.bam_kv_append_paged.argtypes = [vp] * 4 + [lp] + [vp] * 6 + [i] * 8 + [
+            ctypes.POINTER(BamRope), vp, sz, vp]
+        lib.bam_attn_decode_tree_paged.restype = i
+        lib.bam_attn_decode_tree_paged.argtypes = [vp] * 8 + [i, vp] + [i] * 8 + [pp, vp, sz, vp]
+        lib.bam_attn_tree_workspace_size.restype = sz
+        lib.bam_attn_tree_workspace_size.argtypes = [i] * 6
+        lib.bam_kv_keep_paged.restype = i
+        lib.bam_kv_keep_paged.argtypes = [vp] * 8 + [i] * 7 + [vp, sz, vp]
         _lib = lib
         return lib
 
@@ -211,14 +242,14 @@ def _require(t, name, shape, dtypes, device, optional=False):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _device(q):
-    """The CUDA device of q, which must be the current device (the library
+def _device(q, name="q"):
+    """The CUDA device of q (called `name` in errors), which must be the current device (the library
     launches there, on that device's stream)."""
     import torch
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise ValueError("q must be a CUDA tensor")
+        raise ValueError(f"{name} must be a CUDA tensor")
     if q.device.index != torch.cuda.current_device():
-        raise ValueError(f"q is on {q.device}, but cuda:{torch.cuda.current_device()} is "
+        raise ValueError(f"{name} is on {q.device}, but cuda:{torch.cuda.current_device()} is "
                          "the current device")
     return q.device
 
@@ -283,6 +314,10 @@ def _check(status: int, where: str):
 
 def bam_status_string(status: int) -> str:
     return load_library().bam_status_string(int(status)).decode()
+
+
+def bam_attn_tree_workspace_size(B: int, H: int, Hkv: int, N: int, Tmax: int, D: int = 64) -> int:
+    return int(load_library().bam_attn_tree_workspace_size(B, H, Hkv, N, Tmax, D))
 
 
 def bam_attn_workspace_size(op: int, B: int, H: int, T: int, D: int = 64) -> int:
@@ -423,6 +458,130 @@ def bam_attn_decode_noalloc(q, kc, vc, o, lse, params: BamParams, stream=None,
     _check(st, "bam_attn_decode_noalloc")
 
 
+# ---------------------------------------------------------------- drafted tokens, paged cache
+
+def make_rope(base=10000.0, dims=64, interleaved=False) -> BamRope:
+    """Rotation by position of the first `dims` dimensions (a multiple of 16
+    up to 64; 0: none).  interleaved: pairs (2f, 2f+1) instead of
+    (f, f + dims/2)."""
+    if not 0 <= int(dims) <= 64 or int(dims) % 16:
+        raise ValueError("dims must be a multiple of 16 from 0 to 64")
+    if not 0.0 < float(base) < float("inf"):
+        raise ValueError("base must be positive and finite")
+    return BamRope(float(base), int(dims), int(bool(interleaved)))
+
+
+def _cache_specs(k_pages, v_pages, block_table, cache_lens, draft_lens, parents, B, N):
+    """Specs of a paged cache and the drafts behind its committed keys."""
+    if k_pages.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("k_pages must be [num_pages, Hkv, page, 64] and block_table "
+                         "[B, max_blocks]")
+    bf, _, _, i32 = _dt()
+    pages = k_pages.shape[:3] + (64,)
+    return (("k_pages", k_pages, pages, bf, False), ("v_pages", v_pages, pages, bf, False),
+            ("block_table", block_table, (B, block_table.shape[1]), i32, False),
+            ("cache_lens", cache_lens, (B,), i32, False),
+            ("draft_lens", draft_lens, (B,), i32, True),
+            ("parents", parents, (B, N), i32, True))
+
+
+def _check_rows(t, name, shape, device):
+    """A bf16 input whose rows of 64 are contiguous and 16-byte aligned; the
+    other strides are free."""
+    import torch
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(3) != 1 or any(x % 8 for x in t.stride()[:3]) or t.data_ptr() % 16:
+        raise ValueError(f"{name} must have contiguous, 16-byte aligned rows")
+
+
+def bam_kv_append_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_lens, parents, q,
+                        q_out, rope, ws, stream=None, check=True) -> None:
+    """Append k, v [B, Hkv, N, 64] (any batch, head and token strides) to the
+    pages [num_pages, Hkv, page, 64] behind cache_lens [B] committed keys, the
+    keys rotated by their positions.  new_lens int32 [B] or None: tokens of
+    each sequence; parents int32 [B, N] or None: the tree that positions
+    follow; q [B, H, N, 64] -> q_out (contiguous) or both None: queries rotated
+    on the way; rope: make_rope(...) or None."""
+    B, Hkv, N, D = k.shape
+    num_pages, _, page, _ = k_pages.shape
+    H = q.shape[1] if q is not None else Hkv
+    if check:
+        dev = _device(k, "k")
+        bf = _dt()[0]
+        _check_rows(k, "k", (B, k_pages.shape[1], N, 64), dev)
+        _check_rows(v, "v", k.shape, dev)
+        if (q is None) != (q_out is None):
+            raise ValueError("q and q_out go together")
+        if q is not None:
+            _check_rows(q, "q", (B, H, N, 64), dev)
+        _check_tensors(_cache_specs(k_pages, v_pages, block_table, cache_lens, new_lens, parents,
+                                    B, N)
+                       + (("q_out", q_out, (B, H, N, 64), bf, True),), dev)
+        _check_ws(ws, dev)
+    strides = k.stride()[:3] + v.stride()[:3] + (q.stride()[:3] if q is not None else (0, 0, 0))
+    st = load_library().bam_kv_append_paged(
+        _ptr(k), _ptr(v), _ptr(q), _ptr(q_out), (ctypes.c_int64 * 9)(*strides), _ptr(k_pages),
+        _ptr(v_pages), _ptr(block_table), _ptr(cache_lens), _ptr(new_lens), _ptr(parents), B, H,
+        Hkv, N, page, block_table.shape[1], num_pages, D,
+        None if rope is None else ctypes.byref(rope), _ptr(ws), ws.numel(), _stream(stream))
+    _check(st, "bam_kv_append_paged")
+
+
+def bam_attn_decode_tree_paged(q, k_pages, v_pages, block_table, cache_lens, draft_lens, parents,
+                               o, lse, params: BamParams, ws, stream=None, check=True) -> None:
+    """q, o: [B, H, N, 64]; pages [num_pages, Hkv, page, 64] that hold each
+    sequence's committed keys and, behind them, its draft's; cache_lens int32
+    [B] (committed keys); draft_lens int32 [B] or None (N each); parents int32
+    [B, N] or None (a chain); lse [B, H, N] or None."""
+    import torch
+    B, H, N, D = q.shape
+    num_pages, Hkv, page, _ = k_pages.shape
+    if check:
+        dev = _device(q)
+        bf, f32, out, _ = _dt()
+        _check_tensors((("q", q, (B, H, N, 64), bf, False), ("o", o, (B, H, N, 64), out, False),
+                        ("lse", lse, (B, H, N), f32, True))
+                       + _cache_specs(k_pages, v_pages, block_table, cache_lens, draft_lens,
+                                      parents, B, N) + _param_specs(params, H), dev)
+        _check_ws(ws, dev)
+    o_fp32 = 1 if o.dtype == torch.float32 else 0
+    st = load_library().bam_attn_decode_tree_paged(
+        _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(cache_lens),
+        _ptr(draft_lens), _ptr(parents), _ptr(o), o_fp32, _ptr(lse), B, H, Hkv, N, page,
+        block_table.shape[1], num_pages, D, ctypes.byref(params), _ptr(ws), ws.numel(),
+        _stream(stream))
+    _check(st, "bam_attn_decode_tree_paged")
+
+
+def bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, parents, accepted,
+                      new_lens, ws, stream=None, check=True) -> None:
+    """Keep the path from the root to node accepted[b] (int32 [B], -1: none)
+    of each draft; new_lens int32 [B] (may be cache_lens) gets the lengths."""
+    num_pages, Hkv, page, D = k_pages.shape
+    B = block_table.shape[0]
+    N = parents.shape[1] if parents is not None else BAM_TREE_MAX_NODES
+    if check:
+        dev = _device(k_pages, "k_pages")
+        i32 = _dt()[3]
+        if parents is None and draft_lens is None:
+            raise ValueError("draft_lens is required without parents")
+        _check_tensors(_cache_specs(k_pages, v_pages, block_table, cache_lens, draft_lens, parents,
+                                    B, N)
+                       + (("accepted", accepted, (B,), i32, False),
+                          ("new_lens", new_lens, (B,), i32, False)), dev)
+        _check_ws(ws, dev)
+    st = load_library().bam_kv_keep_paged(
+        _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(cache_lens), _ptr(draft_lens),
+        _ptr(parents), _ptr(accepted), _ptr(new_lens), B, Hkv, N, page, block_table.shape[1],
+        num_pages, D, _ptr(ws), ws.numel(), _stream(stream))
+    _check(st, "bam_kv_keep_paged")
+
+
 def bam_attn_selftest_wait(ws, stream=None) -> None:
     """Launch the failure-detection self-test: a bounded wait that runs out
     and records BAM_ERR_TIMEOUT in the status word of `ws` (about 2 s)."""
@@ -494,6 +653,21 @@ def workspace(op: int, B: int, H: int, T: int, device="cuda"):
     if n == 0:
         raise BamError(BAM_ERR_INVALID_ARG, "bam_attn_workspace_size")
     return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def tree_workspace(B: int, H: int, Hkv: int, N: int, Tmax: int, device="cuda"):
+    """Workspace of bam_attn_decode_tree_paged (Tmax = max_blocks * page)."""
+    import torch
+    n = bam_attn_tree_workspace_size(B, H, Hkv, N, Tmax, 64)
+    if n == 0:
+        raise BamError(BAM_ERR_INVALID_ARG, "bam_attn_tree_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def cache_workspace(device="cuda"):
+    """Workspace of bam_kv_append_paged and bam_kv_keep_paged."""
+    import torch
+    return torch.zeros(BAM_CACHE_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
 
 
 def attention_forward(q, k, v, alpha, beta, mu, s=None, eps=1e-5, causal=True, ssmax=False,
@@ -571,3 +745,55 @@ def attention_decode_paged(q, k_pages, v_pages, block_table, cache_lens, alpha, 
     prm = make_params(alpha, beta, mu, s, eps, True, ssmax, prior)
     bam_attn_decode_paged(q, k_pages, v_pages, block_table, cache_lens, o, lse, prm, ws, stream)
     return o, lse
+
+
+def kv_append_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_lens=None, parents=None,
+                    q=None, rope=None, ws=None, stream=None):
+    """Append k, v [B, Hkv, N, 64] to the pages behind cache_lens committed
+    keys, rotated by position when rope is given; returns the rotated q (None
+    without q).  cache_lens is not changed."""
+    import torch
+    q_out = None
+    if q is not None:
+        # rows behind new_lens are not written: no uninitialised memory in them
+        make = torch.empty if new_lens is None else torch.zeros
+        q_out = make(q.shape, dtype=q.dtype, device=q.device)
+    if ws is None:
+        ws = cache_workspace(k_pages.device)
+    bam_kv_append_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_lens, parents, q,
+                        q_out, rope, ws, stream)
+    return q_out
+
+
+def attention_decode_tree_paged(q, k_pages, v_pages, block_table, cache_lens, alpha, beta, mu,
+                                s=None, draft_lens=None, parents=None, eps=1e-5, ssmax=False,
+                                o_dtype=None, ws=None, stream=None, prior=BAM_PRIOR_ALPHA):
+    """Attention of drafted tokens q bf16 [B,H,N,64] over a paged cache that
+    already holds their keys and values behind cache_lens committed ones ->
+    (o [B,H,N,64], lse [B,H,N]); rows behind draft_lens are zero."""
+    import torch
+    B, H, N, D = q.shape
+    make = torch.empty if draft_lens is None else torch.zeros
+    o = make((B, H, N, D), dtype=o_dtype or torch.float32, device=q.device)
+    lse = make((B, H, N), dtype=torch.float32, device=q.device)
+    if ws is None:
+        ws = tree_workspace(B, H, k_pages.shape[1], N, k_pages.shape[2] * block_table.shape[1],
+                            q.device)
+    prm = make_params(alpha, beta, mu, s, eps, True, ssmax, prior)
+    bam_attn_decode_tree_paged(q, k_pages, v_pages, block_table, cache_lens, draft_lens, parents,
+                               o, lse, prm, ws, stream)
+    return o, lse
+
+
+def kv_keep_paged(k_pages, v_pages, block_table, cache_lens, accepted, parents, draft_lens=None,
+                  new_lens=None, ws=None, stream=None):
+    """Keep the accepted path of each draft; returns the new lengths (written
+    to new_lens, which may be cache_lens, if given)."""
+    import torch
+    if new_lens is None:
+        new_lens = torch.empty_like(cache_lens)
+    if ws is None:
+        ws = cache_workspace(k_pages.device)
+    bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, parents, accepted,
+                      new_lens, ws, stream)
+    return new_lens

@@ -11,6 +11,7 @@
 
 #include "../../include/bam_attn.h"
 #include "bam_common.cuh"
+#include "tree_common.cuh"
 
 static_assert(BAM_PRIOR_THETA == bam::kPriorTheta, "prior codes of the ABI and the kernels");
 
@@ -167,8 +168,34 @@ DecWs dec_ws(int B, int H, int Tkv) {
   return w;
 }
 
+// Tree attention: status words only.
+size_t tree_ws(int B, int H, int N, int Tmax) {
+  (void)B;
+  (void)H;
+  (void)N;
+  (void)Tmax;
+  return kStatusBytes;
+}
+
 bam_status check_ws(void* ws, size_t ws_bytes, size_t need) {
   if (!ws || !aligned(ws, 256) || ws_bytes < need) return BAM_ERR_WORKSPACE;
+  return BAM_OK;
+}
+
+// Sizes and pointers of a paged cache with drafts behind its committed keys.
+bam_status check_cache(int B, int H, int Hkv, int N, int page, int max_blocks, int num_pages,
+                       int D, const void* block_table, const void* cache_lens,
+                       const void* draft_lens, const void* parents) {
+  if (B < 1 || H < 1 || Hkv < 1 || N < 1 || D < 1 || max_blocks < 1 || num_pages < 1)
+    return BAM_ERR_INVALID_ARG;
+  if (page < 64 || page % 64 != 0 || H % Hkv != 0) return BAM_ERR_INVALID_ARG;
+  if (!block_table || !aligned(block_table, 4) || !cache_lens || !aligned(cache_lens, 4) ||
+      !aligned(draft_lens, 4) || !aligned(parents, 4))
+    return BAM_ERR_INVALID_ARG;
+  if (D != kHeadDim) return BAM_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(page) * max_blocks > (1 << 28) || N > (1 << 28) || B > 65535 ||
+      H > 65535 || static_cast<int64_t>(num_pages) * Hkv > 0x7FFFFFFF)
+    return BAM_ERR_UNSUPPORTED;
   return BAM_OK;
 }
 
@@ -410,6 +437,130 @@ bam_status bam_attn_decode_varlen(const void* q, const void* kc, const void* vc,
   if (!cache_lens || !aligned(cache_lens, 4)) return BAM_ERR_INVALID_ARG;
   return decode_impl(q, kc, vc, cache_lens, o, o_fp32, lse, B, H, Tmax, D, p, ws, ws_bytes,
                      stream);
+}
+
+bam_status bam_kv_append_paged(const void* k, const void* v, const void* q, void* q_out,
+                               const int64_t* strides, void* k_pages, void* v_pages,
+                               const int* block_table, const int* cache_lens,
+                               const int* new_lens, const int* parents, int B, int H, int Hkv,
+                               int N, int page, int max_blocks, int num_pages, int D,
+                               const bam_rope* rope, void* ws, size_t ws_bytes,
+                               cudaStream_t stream) {
+  bam_status s = check_cache(B, H, Hkv, N, page, max_blocks, num_pages, D, block_table, cache_lens,
+                             new_lens, parents);
+  if (s != BAM_OK) return s;
+  if (!k || !v || !k_pages || !v_pages || !q != !q_out) return BAM_ERR_INVALID_ARG;
+  for (const void* x : {k, v, q, static_cast<const void*>(q_out),
+                        static_cast<const void*>(k_pages), static_cast<const void*>(v_pages)})
+    if (!aligned(x, 16)) return BAM_ERR_INVALID_ARG;
+  if (parents && N > kTreeMax) return BAM_ERR_UNSUPPORTED;
+  AppendArgs a = {};
+  if (rope && rope->dims != 0) {
+    if (rope->dims < 0 || rope->dims > kHeadDim || rope->dims % 16 != 0 ||
+        (rope->interleaved != 0 && rope->interleaved != 1) || !(rope->base > 0.0) ||
+        !std::isfinite(rope->base))
+      return BAM_ERR_INVALID_ARG;
+    a.dims = rope->dims;
+    a.interleaved = rope->interleaved;
+    for (int f = 0; f < rope->dims / 2; ++f) {
+      double turns = std::pow(rope->base, -2.0 * f / rope->dims) / 6.283185307179586477;
+      turns -= std::floor(turns);  // only the fraction of a turn per position matters
+      if (!(turns < 1.0)) turns = 0.0;
+      a.freq[f] = static_cast<uint64_t>(turns * 18446744073709551616.0);
+    }
+  }
+  for (int x = 0; x < 9; ++x) {
+    const int h = x < 6 ? Hkv : H;
+    const int64_t dense[3] = {static_cast<int64_t>(h) * N * kHeadDim,
+                              static_cast<int64_t>(N) * kHeadDim, kHeadDim};
+    const int64_t v64 = strides ? strides[x] : dense[x % 3];
+    if (x >= 6 && !q) break;
+    if (v64 < 0 || v64 % 8 != 0) return BAM_ERR_INVALID_ARG;
+    (x < 3 ? a.ks : x < 6 ? a.vs : a.qs)[x % 3] = v64;
+  }
+  if ((s = check_ws(ws, ws_bytes, BAM_CACHE_WORKSPACE_BYTES)) != BAM_OK) return s;
+  a.c = CacheArgs{block_table, cache_lens, new_lens, parents, static_cast<DevStatus*>(ws),
+                  B, Hkv, N, page, max_blocks, num_pages};
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_pages = static_cast<uint16_t*>(k_pages);
+  a.v_pages = static_cast<uint16_t*>(v_pages);
+  a.H = q ? H : 0;
+  return cuda_status(
+      launch_kernel(BAM_KERNEL_KV_APPEND, stream, [&] { return launch_append(a, stream); }));
+}
+
+size_t bam_attn_tree_workspace_size(int B, int H, int Hkv, int N, int Tmax, int D) {
+  if (B < 1 || H < 1 || Hkv < 1 || N < 1 || Tmax < 1 || D != kHeadDim || H % Hkv != 0 ||
+      N > kTreeMax || B > 65535 || H > 65535 || Tmax > (1 << 28))
+    return 0;
+  return tree_ws(B, H, N, Tmax);
+}
+
+bam_status bam_attn_decode_tree_paged(const void* q, const void* k_pages, const void* v_pages,
+                                      const int* block_table, const int* cache_lens,
+                                      const int* draft_lens, const int* parents, void* o,
+                                      int o_fp32, float* lse, int B, int H, int Hkv, int N,
+                                      int page, int max_blocks, int num_pages, int D,
+                                      const bam_params* p, void* ws, size_t ws_bytes,
+                                      cudaStream_t stream) {
+  bam_status s = check_cache(B, H, Hkv, N, page, max_blocks, num_pages, D, block_table, cache_lens,
+                             draft_lens, parents);
+  if (s != BAM_OK) return s;
+  if (N > kTreeMax) return BAM_ERR_UNSUPPORTED;
+  if ((s = check_params(p)) != BAM_OK) return s;
+  if (!q || !k_pages || !v_pages || !o) return BAM_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16) ||
+      (lse && !aligned(lse, 4)))
+    return BAM_ERR_INVALID_ARG;
+  if ((s = check_ws(ws, ws_bytes, tree_ws(B, H, N, page * max_blocks))) != BAM_OK) return s;
+  TreeArgs a = {};
+  a.c = CacheArgs{block_table, cache_lens, draft_lens, parents, static_cast<DevStatus*>(ws),
+                  B, Hkv, N, page, max_blocks, num_pages};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k_pages = static_cast<const uint16_t*>(k_pages);
+  a.v_pages = static_cast<const uint16_t*>(v_pages);
+  a.alpha = p->alpha;
+  a.beta = p->beta;
+  a.mu = p->mu;
+  a.s = p->s;
+  a.o = o;
+  a.lse = lse;
+  a.eps = p->eps;
+  a.H = H;
+  a.prior = p->prior;
+  a.ssmax = p->ssmax;
+  a.o_fp32 = o_fp32 ? 1 : 0;
+  cudaError_t e =
+      launch_kernel(BAM_KERNEL_TREE_PREP, stream, [&] { return launch_tree_prep(a, stream); });
+  if (e != cudaSuccess) return BAM_ERR_CUDA;
+  return cuda_status(launch_kernel(BAM_KERNEL_TREE, stream, [&] { return launch_tree(a, stream); }));
+}
+
+bam_status bam_kv_keep_paged(void* k_pages, void* v_pages, const int* block_table,
+                             const int* cache_lens, const int* draft_lens, const int* parents,
+                             const int* accepted, int* new_lens, int B, int Hkv, int N, int page,
+                             int max_blocks, int num_pages, int D, void* ws, size_t ws_bytes,
+                             cudaStream_t stream) {
+  bam_status s = check_cache(B, Hkv, Hkv, N, page, max_blocks, num_pages, D, block_table,
+                             cache_lens, draft_lens, parents);
+  if (s != BAM_OK) return s;
+  if (N > kTreeMax) return BAM_ERR_UNSUPPORTED;
+  if (!k_pages || !v_pages || !accepted || !new_lens || !aligned(k_pages, 16) ||
+      !aligned(v_pages, 16) || !aligned(accepted, 4) || !aligned(new_lens, 4))
+    return BAM_ERR_INVALID_ARG;
+  if ((s = check_ws(ws, ws_bytes, BAM_CACHE_WORKSPACE_BYTES)) != BAM_OK) return s;
+  KeepArgs a;
+  a.c = CacheArgs{block_table, cache_lens, draft_lens, parents, static_cast<DevStatus*>(ws),
+                  B, Hkv, N, page, max_blocks, num_pages};
+  a.k_pages = static_cast<uint16_t*>(k_pages);
+  a.v_pages = static_cast<uint16_t*>(v_pages);
+  a.accepted = accepted;
+  a.new_lens = new_lens;
+  return cuda_status(
+      launch_kernel(BAM_KERNEL_KV_KEEP, stream, [&] { return launch_keep(a, stream); }));
 }
 
 bam_status bam_attn_bwd(const void* q, const void* k, const void* v, const void* o, int o_fp32,

@@ -1,0 +1,142 @@
+// Shared by the paged-cache operators for drafted tokens (append, tree
+// attention, keep): kernel argument blocks, checks of what only the device
+// reads, and the depths and ancestors of a draft's nodes.
+#pragma once
+
+#include "bam_common.cuh"
+
+namespace bam {
+
+constexpr int kTreeMax = 128;  // nodes of a draft with parents
+
+// A paged cache and the drafts behind its committed keys.
+struct CacheArgs {
+  const int* block_table;  // [B, max_blocks]
+  const int* lens;         // [B] committed keys
+  const int* draft_lens;   // [B] or null: N each
+  const int* parents;      // [B, N] or null: a chain
+  DevStatus* status;
+  int B, Hkv, N, page, max_blocks, num_pages;
+};
+
+struct AppendArgs {
+  CacheArgs c;
+  const uint16_t* k;
+  const uint16_t* v;
+  const uint16_t* q;
+  uint16_t* q_out;
+  uint16_t* k_pages;
+  uint16_t* v_pages;
+  int64_t ks[3], vs[3], qs[3];  // element strides over batch, head, token
+  int H;                        // query heads (0 without q)
+  int dims, interleaved;
+  int tokens, heads;            // tokens and heads of one CTA
+  uint64_t freq[kHeadDim / 2];  // turns per position of pair f, times 2^64
+};
+
+struct KeepArgs {
+  CacheArgs c;
+  uint16_t* k_pages;
+  uint16_t* v_pages;
+  const int* accepted;
+  int* new_lens;
+};
+
+struct TreeArgs {
+  CacheArgs c;
+  const uint16_t* q;  // [B, H, N, 64]
+  const uint16_t* k_pages;
+  const uint16_t* v_pages;
+  const float* alpha;
+  const float* beta;
+  const float* mu;
+  const float* s;
+  void* o;
+  float* lse;
+  float eps;
+  int H, prior, ssmax, o_fp32;
+};
+
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t st);
+cudaError_t launch_keep(const KeepArgs& a, cudaStream_t st);
+cudaError_t launch_tree_prep(const TreeArgs& a, cudaStream_t st);
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t st);
+
+#ifdef __CUDACC__
+
+enum : int { kSiteCacheArg = 50 };
+
+// Records an argument that only the device reads and that was out of range.
+// The operators of one launch have no earlier kernel that initialises a fresh
+// status area, so the recording thread does; every thread that gets here
+// writes the same words, so their order does not matter.
+__device__ __forceinline__ void record_bad_arg(DevStatus* st) {
+  volatile DevStatus* v = st;
+  if (v->magic[0] == kStatusMagic0 && v->magic[1] == kStatusMagic1) {
+    if (atomicCAS(&st->code, BAM_DEV_OK, BAM_DEV_BAD_ARG) == BAM_DEV_OK) v->site = kSiteCacheArg;
+    return;
+  }
+  v->abort = 0;
+  v->code = BAM_DEV_BAD_ARG;
+  v->site = kSiteCacheArg;
+  v->block = 0;
+  v->giveup = 0;
+  __threadfence();
+  v->magic[0] = kStatusMagic0;
+  v->magic[1] = kStatusMagic1;
+}
+
+// Committed length and draft nodes of sequence b, clamped into their ranges.
+// Returns false when a value was out of range.
+__device__ __forceinline__ bool cache_lengths(const CacheArgs& c, int b, int* len, int* n) {
+  const int cap = c.page * c.max_blocks;
+  const int raw = __ldg(c.lens + b);
+  const int rawn = c.draft_lens ? __ldg(c.draft_lens + b) : c.N;
+  *len = min(max(raw, 0), cap);
+  *n = min(min(max(rawn, 0), c.N), cap - *len);
+  return raw == *len && rawn == *n;
+}
+
+// Depths of the first n <= kTreeMax nodes, by all threads of a block of at
+// least kTreeMax threads: each round doubles the distance that a node's jump
+// pointer spans, so the deepest chain takes log2(depth) rounds.  `jump` holds
+// kTreeMax ints of shared memory, as `depth`.  Ends with a block barrier.
+// Returns false in a thread whose node had a parent outside [-1, i).
+__device__ __forceinline__ bool tree_depths(const int* parents, int n, int* jump, int* depth) {
+  const int i = threadIdx.x;
+  bool ok = true;
+  int p = -1;
+  if (i < n) {
+    p = parents ? __ldg(parents + i) : i - 1;
+    ok = p >= -1 && p < i;
+    if (!ok) p = -1;
+  }
+  int d = p >= 0 ? 1 : 0;
+  if (!parents) {
+    d = i;
+    p = -1;
+  }
+  if (i < kTreeMax) {
+    jump[i] = p;
+    depth[i] = d;
+  }
+  while (__syncthreads_or(p >= 0)) {
+    int dp = 0, pp = -1;
+    if (p >= 0) {
+      dp = depth[p];
+      pp = jump[p];
+    }
+    __syncthreads();
+    d += dp;
+    p = pp;
+    if (i < kTreeMax) {
+      jump[i] = p;
+      depth[i] = d;
+    }
+  }
+  return ok;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace bam
