@@ -141,6 +141,27 @@ def test_tree_long_and_split(lens):
     _tree_case(3, B, 4, 2, 6, 64, lens, [6] * B, parents, True, False, "fp32")
 
 
+@pytest.mark.parametrize("H,Hkv,N,out", [(16, 8, 2, "bf16"), (8, 8, 3, "fp32"), (16, 8, 12, "bf16"),
+                                         (8, 8, 40, "bf16"), (8, 8, 100, "fp32")])
+def test_tree_many_tiles_a_cta(H, Hkv, N, out):
+    """Enough tiles that every CTA goes around its ring many times, at the pace
+    of several streams; repeated calls give the same bits."""
+    rng = np.random.default_rng(N)
+    lens, new = [16000, 9000, 15001, 12345, 7, 16100], [1, N, 2, 1, N, 1]
+    parents = [random_tree(rng, n) for n in new]
+    c, q, o, lse = _tree_case(N, 6, H, Hkv, N, 64, lens, new, parents, True, False, out)
+    t = [dev_f32(_prm(np.random.default_rng(1), H, False)[n]) for n in ("alpha", "beta", "mu", "s")]
+    par, ln, nw = _i32(pack_trees(parents, 6, N)), _i32(lens), _i32(new)
+    ws = ba.tree_workspace(6, H, Hkv, N, c.k.shape[2] * c.table.shape[1])
+    first = None
+    for _ in range(40):
+        got = ba.attention_decode_tree_paged(q, c.k, c.v, c.table, ln, *t, draft_lens=nw,
+                                             parents=par, ssmax=True, ws=ws)
+        first = got if first is None else first
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+    assert ba.bam_attn_check_status(ws) == ba.BAM_OK
+
+
 def test_tree_many_sequences():
     """More sequences than a block has threads, most of them short."""
     rng = np.random.default_rng(5)

@@ -168,13 +168,19 @@ DecWs dec_ws(int B, int H, int Tkv) {
   return w;
 }
 
-// Tree attention: status words only.
-size_t tree_ws(int B, int H, int N, int Tmax) {
-  (void)B;
-  (void)H;
-  (void)N;
-  (void)Tmax;
-  return kStatusBytes;
+struct TreeWs {
+  size_t plan, table, ml, part, total;
+  int rows;
+};
+TreeWs tree_ws(int B, int H, int Hkv, int N, int Tmax) {
+  TreeWs w;
+  w.rows = tree_rows(H / Hkv * N);
+  w.plan = kStatusBytes;
+  w.table = w.plan + align256((static_cast<size_t>(B) + 1) * 8);
+  w.ml = w.table + align256(static_cast<size_t>(H) * tree_table_len(Tmax) * 4);
+  w.part = w.ml + align256(2 * kTreeCtas * static_cast<size_t>(w.rows) * 8);
+  w.total = w.part + align256(2 * kTreeCtas * static_cast<size_t>(w.rows) * kHeadDim * 4);
+  return w;
 }
 
 bam_status check_ws(void* ws, size_t ws_bytes, size_t need) {
@@ -496,7 +502,7 @@ size_t bam_attn_tree_workspace_size(int B, int H, int Hkv, int N, int Tmax, int 
   if (B < 1 || H < 1 || Hkv < 1 || N < 1 || Tmax < 1 || D != kHeadDim || H % Hkv != 0 ||
       N > kTreeMax || B > 65535 || H > 65535 || Tmax > (1 << 28))
     return 0;
-  return tree_ws(B, H, N, Tmax);
+  return tree_ws(B, H, Hkv, N, Tmax).total;
 }
 
 bam_status bam_attn_decode_tree_paged(const void* q, const void* k_pages, const void* v_pages,
@@ -515,28 +521,46 @@ bam_status bam_attn_decode_tree_paged(const void* q, const void* k_pages, const 
   if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16) ||
       (lse && !aligned(lse, 4)))
     return BAM_ERR_INVALID_ARG;
-  if ((s = check_ws(ws, ws_bytes, tree_ws(B, H, N, page * max_blocks))) != BAM_OK) return s;
+  const int Tmax = page * max_blocks;
+  const TreeWs w = tree_ws(B, H, Hkv, N, Tmax);
+  if ((s = check_ws(ws, ws_bytes, w.total)) != BAM_OK) return s;
+  // Pages as rows of 64 dimensions, in boxes of one tile of 64 keys.
+  CUtensorMap tk, tv;
+  if (!encode_rows(&tk, k_pages, num_pages * Hkv, page, kTreeTile) ||
+      !encode_rows(&tv, v_pages, num_pages * Hkv, page, kTreeTile))
+    return BAM_ERR_CUDA;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
   TreeArgs a = {};
   a.c = CacheArgs{block_table, cache_lens, draft_lens, parents, static_cast<DevStatus*>(ws),
                   B, Hkv, N, page, max_blocks, num_pages};
   a.q = static_cast<const uint16_t*>(q);
-  a.k_pages = static_cast<const uint16_t*>(k_pages);
-  a.v_pages = static_cast<const uint16_t*>(v_pages);
   a.alpha = p->alpha;
   a.beta = p->beta;
   a.mu = p->mu;
   a.s = p->s;
   a.o = o;
   a.lse = lse;
+  a.plan = reinterpret_cast<int64_t*>(wsb + w.plan);
+  a.table = reinterpret_cast<float*>(wsb + w.table);
+  a.part_ml = reinterpret_cast<float2*>(wsb + w.ml);
+  a.part = reinterpret_cast<float*>(wsb + w.part);
   a.eps = p->eps;
   a.H = H;
+  a.group = H / Hkv;
   a.prior = p->prior;
   a.ssmax = p->ssmax;
   a.o_fp32 = o_fp32 ? 1 : 0;
+  a.tab_len = tree_table_len(Tmax);
+  a.tab_zero = tree_table_zero(Tmax);
+  a.rows = w.rows;
+  if (!tree_config(&a, sm_count())) return BAM_ERR_CUDA;
   cudaError_t e =
       launch_kernel(BAM_KERNEL_TREE_PREP, stream, [&] { return launch_tree_prep(a, stream); });
   if (e != cudaSuccess) return BAM_ERR_CUDA;
-  return cuda_status(launch_kernel(BAM_KERNEL_TREE, stream, [&] { return launch_tree(a, stream); }));
+  e = launch_kernel(BAM_KERNEL_TREE, stream, [&] { return launch_tree(tk, tv, a, stream); });
+  if (e != cudaSuccess) return BAM_ERR_CUDA;
+  return cuda_status(launch_kernel(BAM_KERNEL_TREE_COMBINE, stream,
+                                   [&] { return launch_tree_combine(a, stream); }));
 }
 
 bam_status bam_kv_keep_paged(void* k_pages, void* v_pages, const int* block_table,

@@ -42,25 +42,51 @@ struct KeepArgs {
   int* new_lens;
 };
 
+// Tree attention: the rows of a (sequence, key head) are its group * n
+// (query head, node) pairs, row r = (head r / n, node r % n), taken `rows` at
+// a time; such an item reads the tiles of 64 keys that hold the sequence's
+// len + n keys.  The plan is the running sum of the sequences' tiles over all
+// their items, and CTA c of `active` takes tiles [W c / active, W (c+1) /
+// active) of the W in all.
+constexpr int kTreeTile = 64;    // keys of a tile
+constexpr int kTreeCtas = 304;   // most CTAs (two per SM)
+
 struct TreeArgs {
   CacheArgs c;
   const uint16_t* q;  // [B, H, N, 64]
-  const uint16_t* k_pages;
-  const uint16_t* v_pages;
   const float* alpha;
   const float* beta;
   const float* mu;
   const float* s;
   void* o;
   float* lse;
+  int64_t* plan;      // [B + 1] first tile of each sequence, and W
+  float* table;       // [H, tab_len]: entry y is b_h(tab_zero - y) * log2(e)
+  float* part;        // [2 * kTreeCtas, rows, 64] partial outputs
+  float2* part_ml;    // [2 * kTreeCtas, rows]: maximum (log2 units), sum
   float eps;
-  int H, prior, ssmax, o_fp32;
+  int H, group, prior, ssmax, o_fp32;
+  int tab_len, tab_zero;
+  int rows;           // rows of an item: 16, 32, 64 or 128
+  int ctas, least;    // CTAs of the launch; tiles that one gets at least
+  int stages;         // ring stages
+  int win_stage;      // floats of a stage's table windows
 };
+
+// Rows of an item for `rows` (head, node) pairs.
+inline int tree_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// Table row: distances 0 .. Tmax at entries Tmax .. 0 and, behind entry
+// Tmax, room for windows that reach past the last key.
+inline int tree_table_zero(int Tmax) { return (Tmax + 63) / 64 * 64; }
+inline int tree_table_len(int Tmax) { return tree_table_zero(Tmax) + 64 + kTreeMax + kTreeTile; }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st);
 cudaError_t launch_keep(const KeepArgs& a, cudaStream_t st);
+bool tree_config(TreeArgs* a, int sms);
 cudaError_t launch_tree_prep(const TreeArgs& a, cudaStream_t st);
-cudaError_t launch_tree(const TreeArgs& a, cudaStream_t st);
+cudaError_t launch_tree(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a,
+                        cudaStream_t st);
+cudaError_t launch_tree_combine(const TreeArgs& a, cudaStream_t st);
 
 #ifdef __CUDACC__
 
