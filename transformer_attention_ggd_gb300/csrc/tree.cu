@@ -40,6 +40,8 @@ struct __align__(16) TreeSmem {
   uint32_t seen[kTreeMax][kTreeMax / 32];  // ancestors of each node, and itself
   int jump[kTreeMax];
   int depth[kTreeMax];
+  int node[kTreeMax];  // of the item's rows: node (-1: no row) and query head
+  int head[kTreeMax];
   int abort_flag;
   int find;
 };
@@ -239,12 +241,14 @@ __host__ __device__ __forceinline__ int window_floats(int n) {
 
 // ---------------------------------------------------------------- attention
 
-// A consumer warp holds 16 * MT rows of an item (row group warp % RG) and
-// takes every (kConsumers / RG)-th tile of the CTA: the warps that share a
-// tile are the row groups, the others work on other tiles at the same time.
-// Its products are bf16 m16n8k16 with fp32 accumulators: S = Q K^T over 32
-// keys at a time, the softmax on the accumulators, and O += P V with the
-// weights as the next product's left operand, without leaving registers.
+// A consumer warp holds 16 * MT rows of an item (row group warp % RG) and one
+// of kConsumers / RG equal parts of the keys of every tile.  Its products are
+// bf16 m16n8k16 with fp32 accumulators: S = Q K^T, the softmax on the
+// accumulators, and O += P V with the weights as the next product's left
+// operand, without leaving registers.  (Whole tiles dealt out to the warps in
+// turn were slower, 915 against 746 us at B64 H12 N32 T32768: a slot of the
+// ring may then serve one warp only, since a wait names a phase by its parity,
+// and each warp had a single slot.)
 //
 // The running maximum is only raised when a logit exceeds it by more than 8
 // (a weight is at most 2^8), so most tiles need no exchange between lanes.
@@ -255,8 +259,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     bam_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                     const TreeArgs a) {
   constexpr int kRows = 16 * MT * RG;
-  constexpr int kStreams = kConsumers / RG;
-  constexpr int NT = MT == 1 ? 8 : 4;  // 8-key column tiles of S at a time
+  constexpr int kStreams = kConsumers / RG;  // parts of a tile's keys
+  constexpr int kKeys = kTreeTile / kStreams;
+  constexpr int NT = kKeys < 32 ? kKeys / 8 : 4;  // 8-key column tiles of S at a time
   extern __shared__ __align__(16) uint8_t smem_raw[];
   uint8_t* const kv = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // [stages][K, V]
   float* const win = reinterpret_cast<float*>(kv + a.stages * 2 * kKvBytes);
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     prefetch_tmap(&tv);
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], RG);
+      mbar_init(&sm.empty[s], kConsumers);
     }
     fence_barrier_init();
     sm.find = 0;
@@ -358,6 +363,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   // ------------------------------------------------------------------ consumers
   const int rg = warp % RG, stream = warp / RG;
   const int quad = lane & 3;
+  const int key0 = stream * kKeys;  // first key of this warp in a tile
+  int s = 0, phase = 0;
   bool ok = *ab == 0, args_ok = true;
   int last_b = -1;
   for (int64_t x = beg; x < end;) {
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     const int rem = (a.tab_zero - (len + n - 1)) & 3;
     // This lane's rows: 2 of each 16.
     float cs[MT][2], m[MT][2], l[MT][2], o[MT][8][4];
-    int woff[MT][2], node[MT][2], head[MT][2];
+    int woff[MT][2];
     uint32_t q[MT][4][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -384,15 +391,19 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         const int t = live ? r - g * n : 0;
         const int pos = len + sm.depth[t];
         float cl = 0.125f;
-        head[mt][hf] = it.hk * a.group + g;
-        if (a.ssmax) cl *= __ldg(a.s + head[mt][hf]) * logf(static_cast<float>(pos + 1));
+        const int head = it.hk * a.group + g;
+        if (a.ssmax) cl *= __ldg(a.s + head) * logf(static_cast<float>(pos + 1));
         cs[mt][hf] = cl * static_cast<float>(kLog2e);
         woff[mt][hf] = (g - g0) * nwin + rem + (len + n - 1 - pos) + 2 * quad;
-        node[mt][hf] = live ? t : -1;
+        if (quad == 0 && stream == 0) {
+          const int rr = 16 * (MT * rg + mt) + 8 * hf + (lane >> 2);
+          sm.node[rr] = live ? t : -1;
+          sm.head[rr] = head;
+        }
         m[mt][hf] = kNoMax;
         l[mt][hf] = 0.0f;
         const uint32_t* qr = reinterpret_cast<const uint32_t*>(
-            a.q + ((static_cast<size_t>(it.b) * a.H + head[mt][hf]) * c.N + t) * kHeadDim);
+            a.q + ((static_cast<size_t>(it.b) * a.H + head) * c.N + t) * kHeadDim);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           q[mt][kk][hf] = live ? __ldg(qr + 8 * kk + quad) : 0u;
@@ -404,23 +415,20 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.0f;
     }
+    consumer_sync();  // rows' nodes and heads; the previous item's join is over
     const bool rows_live = r0 + 16 * MT * rg < r1;
 
-    // Tiles of the CTA's run whose number is this stream's.
-    const int i0 = static_cast<int>(x - beg) - it.t0;  // number of the item's tile 0
-    int t = it.t0 + (stream + kStreams - (i0 + it.t0) % kStreams) % kStreams;
-    for (; t < it.t1; t += kStreams) {
-      const int i = i0 + t, s = i % a.stages;
-      if (ok) ok = mbar_wait(&sm.full[s], (i / a.stages) & 1, c.status, ab, kSiteTreeConsumer);
+    for (int t = it.t0; t < it.t1; ++t) {
+      if (ok) ok = mbar_wait(&sm.full[s], phase, c.status, ab, kSiteTreeConsumer);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const uint32_t ks = smem_u32(kv + s * 2 * kKvBytes), vs = ks + kKvBytes;
-      const float* w = win + s * a.win_stage;
-      const int j0 = t * kTreeTile;
-      const bool tail = j0 + kTreeTile > len;  // holds keys that not every row sees
+      const float* w = win + s * a.win_stage + key0;
+      const int j0 = t * kTreeTile + key0;
+      const bool tail = j0 + kKeys > len;  // holds keys that not every row sees
       bool odd = false;
 #pragma unroll 1
-      for (int ch = 0; rows_live && ch < 8 / NT; ++ch) {
+      for (int ch = 0; rows_live && ch < kKeys / (8 * NT); ++ch) {
         float z[MT][NT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -433,7 +441,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk) {
             uint32_t kb[4];
-            ldsm_x4(ks + ((ch * NT + nt) * 8 + (lane & 7)) * 128 +
+            ldsm_x4(ks + (key0 + (ch * NT + nt) * 8 + (lane & 7)) * 128 +
                         (((4 * kk + (lane >> 3)) ^ (lane & 7)) << 4),
                     kb);
 #pragma unroll
@@ -467,10 +475,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              const int nd = node[mt][hf];
+              const int rr = 16 * (MT * rg + mt) + 8 * hf + (lane >> 2);
+              const int nd = sm.node[rr];
               const float* wr = w + woff[mt][hf] + ch * NT * 8;
               // table entry of an ancestor at depth x: near + x
-              const float* near = a.table + static_cast<size_t>(head[mt][hf]) * a.tab_len +
+              const float* near = a.table + static_cast<size_t>(sm.head[rr]) * a.tab_len +
                                   a.tab_zero - (nd >= 0 ? sm.depth[nd] : 0);
               float mx = kNoMax;
 #pragma unroll
@@ -545,11 +554,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
               }
             }
           }
-          const int kb = (ch * NT + 2 * k2) * 8;  // first key within the tile
+          const int kb = (ch * NT + 2 * k2) * 8;  // first key, from this warp's
 #pragma unroll
           for (int dp = 0; dp < 4; ++dp) {
             uint32_t vb[4];
-            ldsm_x4_t(vs + (kb + (lane & 15)) * 128 + (((2 * dp + (lane >> 4)) ^ (lane & 7)) << 4),
+            ldsm_x4_t(vs + (key0 + kb + (lane & 15)) * 128 + (((2 * dp + (lane >> 4)) ^ (lane & 7)) << 4),
                       vb);
             if (tail) {
               // Rows behind the draft hold anything: zeros.  A drafted value
@@ -580,8 +589,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       if (tail && __any_sync(0xffffffffu, odd)) {
         const uint8_t* vt = kv + s * 2 * kKvBytes + kKvBytes;
 #pragma unroll 1
-        for (int j = max(len, j0); j < min(len + n, j0 + kTreeTile); ++j) {
-          const int row = j - j0, i = j - len;
+        for (int j = max(len, j0); j < min(len + n, j0 + kKeys); ++j) {
+          const int row = j - t * kTreeTile, i = j - len;
 #pragma unroll
           for (int nt = 0; nt < 8; ++nt) {
             const uint32_t v =
@@ -590,7 +599,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf) {
-                const int nd = node[mt][hf];
+                const int nd = sm.node[16 * (MT * rg + mt) + 8 * hf + (lane >> 2)];
                 if (nd >= 0 && (sm.seen[nd][i >> 5] >> (i & 31) & 1)) {
                   if (odd_exp(v)) o[mt][nt][2 * hf] += bf16_lo(v);
                   if (odd_exp(v >> 16)) o[mt][nt][2 * hf + 1] += bf16_hi(v);
@@ -602,11 +611,14 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[s]);
+      if (++s == a.stages) {
+        s = 0;
+        phase ^= 1;
+      }
     }
 
-    // Join the streams in shared memory.  After a give-up the values mean
+    // Join the parts of the keys in shared memory.  After a give-up the values mean
     // nothing, but every warp comes here for every item, so the barriers match.
-    consumer_sync();  // the previous item's rows have been read
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -780,21 +792,16 @@ bool tree_config(TreeArgs* a, int sms) {
     if (heads * window_floats(n) > a->win_stage) a->win_stage = heads * window_floats(n);
   }
   const size_t fixed = smem_fixed(a->rows), stage = smem_stage(*a);
-  const int streams = a->rows <= 32 ? kConsumers : kConsumers * 32 / a->rows;
   int per_sm = 2;
   size_t budget = kSmemTwo;
-  if (fixed + (streams < 3 ? 3 : streams) * stage > budget) {
+  if (fixed + 3 * stage > budget) {
     per_sm = 1;
     budget = kSmemOne;
   }
   a->stages = static_cast<int>((budget - fixed) / stage);
   if (a->stages > kMaxStages) a->stages = kMaxStages;
-  // A slot serves one stream only.  Streams run at their own pace, and a wait
-  // names a phase by its parity: a warp that was ahead on a slot of another
-  // stream would take the phase before the one that is still open for its own.
-  a->stages -= a->stages % streams;
   a->ctas = per_sm * sms < kTreeCtas ? per_sm * sms : kTreeCtas;
-  a->least = streams;
+  a->least = 2;
   return a->stages >= 2 && a->ctas >= 1;
 }
 
