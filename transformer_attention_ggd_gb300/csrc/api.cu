@@ -174,11 +174,11 @@ struct TreeWs {
 };
 TreeWs tree_ws(int B, int H, int Hkv, int N, int Tmax) {
   TreeWs w;
-  w.rows = tree_rows(H / Hkv * N);
+  w.rows = tree_rows(static_cast<int64_t>(H / Hkv) * N);
   w.plan = kStatusBytes;
   w.table = w.plan + align256((static_cast<size_t>(B) + 1) * 8);
   w.ml = w.table + align256(static_cast<size_t>(H) * tree_table_len(Tmax) * 4);
-  w.part = w.ml + align256(2 * kTreeCtas * static_cast<size_t>(w.rows) * 8);
+  w.part = w.ml + align256(2 * kTreeCtas * static_cast<size_t>(w.rows) * 16);
   w.total = w.part + align256(2 * kTreeCtas * static_cast<size_t>(w.rows) * kHeadDim * 4);
   return w;
 }
@@ -534,6 +534,7 @@ bam_status bam_attn_decode_tree_paged(const void* q, const void* k_pages, const 
   a.c = CacheArgs{block_table, cache_lens, draft_lens, parents, static_cast<DevStatus*>(ws),
                   B, Hkv, N, page, max_blocks, num_pages};
   a.q = static_cast<const uint16_t*>(q);
+  a.v_pages = static_cast<const uint16_t*>(v_pages);
   a.alpha = p->alpha;
   a.beta = p->beta;
   a.mu = p->mu;
@@ -542,7 +543,7 @@ bam_status bam_attn_decode_tree_paged(const void* q, const void* k_pages, const 
   a.lse = lse;
   a.plan = reinterpret_cast<int64_t*>(wsb + w.plan);
   a.table = reinterpret_cast<float*>(wsb + w.table);
-  a.part_ml = reinterpret_cast<float2*>(wsb + w.ml);
+  a.part_ml = reinterpret_cast<float4*>(wsb + w.ml);
   a.part = reinterpret_cast<float*>(wsb + w.part);
   a.eps = p->eps;
   a.H = H;

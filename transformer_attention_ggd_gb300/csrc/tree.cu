@@ -20,28 +20,48 @@
 namespace bam {
 namespace {
 
-constexpr int kConsumers = 4;  // warps
-constexpr int kTreeThreads = 32 * (kConsumers + 1);
+constexpr int kTreeThreads = 192;  // softmax warps (at most 4), producer, MMA issuer
+constexpr int kRowsMax = 128;      // rows of an item: lanes of Tensor Memory
 constexpr int kKvBytes = kTreeTile * kHeadDim * 2;  // 8 KB of K (and of V) a tile
+constexpr int kQBytes = kRowsMax * kHeadDim * 2;
 constexpr int kMaxStages = 8;
-constexpr int kMergeStride = 72;  // floats of a merge row: 8-byte stores of 8 rows hit all banks
 constexpr float kRescale = 8.0f;  // log2 units by which a weight may exceed 1
 constexpr float kNoMax = -3.4e38f;  // below every logit (the table is clamped at -3e38)
 
+// Tensor Memory columns of a CTA (256): S, the parts of P, O.
+constexpr uint32_t kTmemCols = 256, kColP = 64, kColO = 192;
+
 enum : int {
   kSiteTreeProducer = 60,
-  kSiteTreeConsumer = 61,
-  kSiteTreeTable = 62
+  kSiteTreeTable = 61,
+  kSiteTreeMmaQ = 62,
+  kSiteTreeMmaS = 63,
+  kSiteTreeMmaK = 64,
+  kSiteTreeMmaP = 65,
+  kSiteTreeSoftS = 66,
+  kSiteTreeSoftK = 67,
+  kSiteTreeSoftPV = 68,
+  kSiteTreeSoftEnd = 69
+};
+
+// Depths and ancestors of a sequence's nodes; every softmax warp has its own,
+// so that the warps need no barrier among themselves.
+struct TreeInfo {
+  uint32_t seen[kTreeMax][kTreeMax / 32];  // a node's ancestors, and itself
+  int jump[kTreeMax];
+  int depth[kTreeMax];
 };
 
 struct __align__(16) TreeSmem {
-  uint64_t full[kMaxStages];
-  uint64_t empty[kMaxStages];
-  uint32_t seen[kTreeMax][kTreeMax / 32];  // ancestors of each node, and itself
-  int jump[kTreeMax];
-  int depth[kTreeMax];
-  int node[kTreeMax];  // of the item's rows: node (-1: no row) and query head
-  int head[kTreeMax];
+  TreeInfo info[kRowsMax / 32];
+  uint64_t full[kMaxStages];   // K, V and table windows of a stage have arrived
+  uint64_t empty[kMaxStages];  // its P V is done
+  uint64_t q_full;             // the item's queries are in shared memory
+  uint64_t s_full, s_free;     // S is complete; S is in registers
+  uint64_t p_full, pv_done;    // P is in Tensor Memory; P V is done
+  uint64_t mma_final;
+  uint32_t odd[2][kTreeMax / 32];  // nodes whose value is not finite, by item parity
+  uint32_t tmem_base;
   int abort_flag;
   int find;
 };
@@ -148,89 +168,68 @@ __device__ __forceinline__ Item item_at(const TreeArgs& a, int b, int64_t x, int
   return it;
 }
 
-// ---------------------------------------------------------------- matrix instructions
-
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t* r) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma_bf16(float* d, const uint32_t* a, const uint32_t* b) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-
-__device__ __forceinline__ void consumer_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
-}
-__device__ __forceinline__ bool consumer_or(bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n"
-      " selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(x ? 1u : 0u), "n"(32 * kConsumers)
-      : "memory");
-  return r != 0;
-}
-
-// Depth and ancestors of the nodes of sequence b, by the consumer threads
-// (one node each).  Each round doubles the chains that the jump pointers
-// span.  Returns false in a thread whose node had a parent outside [-1, i).
-__device__ __forceinline__ bool tree_seen(const CacheArgs& c, int b, int n, TreeSmem& sm) {
-  const int i = threadIdx.x;
-  bool ok = true;
-  int p = -1, d = 0;
-  uint32_t w[kTreeMax / 32];
+// Depth and ancestors of the n nodes of sequence b, by one warp (four nodes a
+// lane).  Each round doubles the chains that the jump pointers span.  Returns
+// false in a lane that met a parent outside [-1, i).
+__device__ __forceinline__ bool tree_info(const CacheArgs& c, int b, int n, TreeInfo& ti) {
+  constexpr int kPer = kTreeMax / 32;
+  const int lane = threadIdx.x & 31;
+  bool ok = true, more = false;
+  __syncwarp();
 #pragma unroll
-  for (int x = 0; x < kTreeMax / 32; ++x) w[x] = i / 32 == x ? 1u << (i & 31) : 0u;
-  if (!c.parents) {
-    d = i;
+  for (int x = 0; x < kPer; ++x) {
+    const int i = 32 * x + lane;
+    uint32_t w[kPer];
+    int p = -1, d = 0;
 #pragma unroll
-    for (int x = 0; x < kTreeMax / 32; ++x)
-      w[x] = i / 32 > x ? 0xFFFFFFFFu : i / 32 == x ? 0xFFFFFFFFu >> (31 - (i & 31)) : 0u;
-  } else if (i < n) {
-    p = __ldg(c.parents + static_cast<size_t>(b) * c.N + i);
-    ok = p >= -1 && p < i;
-    if (!ok) p = -1;
-    d = p >= 0;
-  }
-  consumer_sync();  // the previous sequence's words are no longer read
-  for (;;) {
-    sm.jump[i] = p;
-    sm.depth[i] = d;
-    *reinterpret_cast<uint4*>(sm.seen[i]) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (!consumer_or(p >= 0)) break;
-    int dp = 0, pp = -1;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (p >= 0) {
-      dp = sm.depth[p];
-      pp = sm.jump[p];
-      v = *reinterpret_cast<const uint4*>(sm.seen[p]);
+    for (int y = 0; y < kPer; ++y) w[y] = x == y ? 1u << lane : 0u;
+    if (!c.parents) {
+      d = i;
+#pragma unroll
+      for (int y = 0; y < kPer; ++y) w[y] = x > y ? ~0u : x == y ? ~0u >> (31 - lane) : 0u;
+    } else if (i < n) {
+      p = __ldg(c.parents + static_cast<size_t>(b) * c.N + i);
+      ok &= p >= -1 && p < i;
+      if (p < -1 || p >= i) p = -1;
+      d = p >= 0;
     }
-    consumer_sync();
-    d += dp;
-    p = pp;
-    w[0] |= v.x;
-    w[1] |= v.y;
-    w[2] |= v.z;
-    w[3] |= v.w;
+    more |= p >= 0;
+    ti.jump[i] = p;
+    ti.depth[i] = d;
+    *reinterpret_cast<uint4*>(ti.seen[i]) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __syncwarp();
+  while (__any_sync(0xffffffffu, more)) {
+    int p[kPer], dp[kPer];
+    uint4 v[kPer];
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const int j = ti.jump[32 * x + lane];
+      p[x] = -1;
+      dp[x] = 0;
+      v[x] = make_uint4(0, 0, 0, 0);
+      if (j >= 0) {
+        p[x] = ti.jump[j];
+        dp[x] = ti.depth[j];
+        v[x] = *reinterpret_cast<const uint4*>(ti.seen[j]);
+      }
+    }
+    __syncwarp();
+    more = false;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const int i = 32 * x + lane;
+      uint4* w = reinterpret_cast<uint4*>(ti.seen[i]);
+      *w = make_uint4(w->x | v[x].x, w->y | v[x].y, w->z | v[x].z, w->w | v[x].w);
+      ti.depth[i] += dp[x];
+      ti.jump[i] = p[x];
+      more |= p[x] >= 0;
+    }
+    __syncwarp();
   }
   return ok;
 }
 
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ bool odd_exp(uint32_t half) { return (half & 0x7F80u) == 0x7F80u; }
 
 // Floats of one head's table window for a tile and n nodes: 64 keys against
@@ -241,35 +240,62 @@ __host__ __device__ __forceinline__ int window_floats(int n) {
 
 // ---------------------------------------------------------------- attention
 
-// A consumer warp holds 16 * MT rows of an item (row group warp % RG) and one
-// of kConsumers / RG equal parts of the keys of every tile.  Its products are
-// bf16 m16n8k16 with fp32 accumulators: S = Q K^T, the softmax on the
-// accumulators, and O += P V with the weights as the next product's left
-// operand, without leaving registers.  (Whole tiles dealt out to the warps in
-// turn were slower, 915 against 746 us at B64 H12 N32 T32768: a slot of the
-// ring may then serve one warp only, since a wait names a phase by its parity,
-// and each warp had a single slot.)
-//
-// The running maximum is only raised when a logit exceeds it by more than 8
-// (a weight is at most 2^8), so most tiles need no exchange between lanes.
-// PARTS: bf16 parts of a weight in the product with V (1: its rounding, at
-// most 2^-8 of the weight, is of the size of the output's own; 3: 24 bits).
-template <int MT, int RG, int PARTS>
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, DevStatus* st,
+                                          volatile int* ab, int site) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, st, ab, site));
+}
+
+// The softmax state of one row (the thread's lane of Tensor Memory).
+struct TreeRow {
+  float m, l, le;     // maximum (log2 units), sum of the rounded weights, exact sum
+  float c;            // logit scale, log2 units
+  int node;           // -1: no row
+  int head;
+  const float* near;  // table entry of an ancestor at depth 0
+};
+
+// Visibility of the 64 keys of a tile that starts at j0 to a node: committed
+// keys, then the bits of its ancestors.
+__device__ __forceinline__ uint64_t tile_mask(const uint32_t* seen, int j0, int len) {
+  const uint64_t lo = static_cast<uint64_t>(seen[1]) << 32 | seen[0];
+  const uint64_t hi = static_cast<uint64_t>(seen[3]) << 32 | seen[2];
+  const int i = j0 - len;  // node of the tile's first key
+  if (i <= 0) {
+    const int k = -i;  // 0 .. 63 committed keys in the tile
+    return k ? (lo << k) | ((1ull << k) - 1) : lo;
+  }
+  if (i >= 128) return 0;
+  if (i >= 64) return hi >> (i - 64);
+  return lo >> i | hi << (64 - i);
+}
+
+// One CTA walks its run of tiles; two CTAs share an SM, so that one's
+// hand-offs are covered by the other's work.  Roles: a softmax warp per 32
+// rows, a producer warp (TMA loads of K and V, bulk copies of the table
+// windows of the item's heads, into a ring), and a thread that issues the
+// products:
+//   S = Q K^T   128 x 64 x 64, Q and K from shared memory (K-major),
+//   O += P V    128 x 64 x 64, P from Tensor Memory, V from shared memory.
+// All 128 rows are computed whatever their number: at 64 keys a tile the two
+// products take 256 cycles of an SM's tensor core, its share of HBM delivers
+// the tile's 16 KB in about 700.  The next tile's S runs while the softmax
+// works on this tile's.  One thread owns one row, so the softmax needs no
+// exchange; O is rescaled only when a row's maximum grows by more than 8.
+// PARTS: bf16 parts of a weight in the product with V.  With one, the sum
+// that normalises is that of the rounded weights, so that the rounding of a
+// weight that dominates its row cancels; three carry 24 bits.
+template <int PARTS>
 __global__ void __launch_bounds__(kTreeThreads, 2)
     bam_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                     const TreeArgs a) {
-  constexpr int kRows = 16 * MT * RG;
-  constexpr int kStreams = kConsumers / RG;  // parts of a tile's keys
-  constexpr int kKeys = kTreeTile / kStreams;
-  constexpr int NT = kKeys < 32 ? kKeys / 8 : 4;  // 8-key column tiles of S at a time
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  uint8_t* const kv = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // [stages][K, V]
+  uint8_t* const sq = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
+  uint8_t* const kv = sq + kQBytes;  // [stages][K, V]
   float* const win = reinterpret_cast<float*>(kv + a.stages * 2 * kKvBytes);
-  float* const merge = win + a.stages * a.win_stage;  // [streams][rows][kMergeStride]
-  float2* const merge_ml = reinterpret_cast<float2*>(merge + kStreams * kRows * kMergeStride);
-  TreeSmem& sm = *reinterpret_cast<TreeSmem*>(merge_ml + kStreams * kRows);
+  TreeSmem& sm = *reinterpret_cast<TreeSmem*>(win + a.stages * a.win_stage);
   const CacheArgs& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nw = a.rows / 32;  // softmax warps
   volatile int* ab = &sm.abort_flag;
 
   if (threadIdx.x == 0) {
@@ -277,10 +303,20 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     prefetch_tmap(&tv);
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], kConsumers);
+      mbar_init(&sm.empty[s], 1);
     }
+    mbar_init(&sm.q_full, nw);
+    mbar_init(&sm.s_full, 1);
+    mbar_init(&sm.s_free, nw);
+    mbar_init(&sm.p_full, nw);
+    mbar_init(&sm.pv_done, 1);
+    mbar_init(&sm.mma_final, 1);
     fence_barrier_init();
     sm.find = 0;
+  }
+  if (warp == nw + 1) {
+    tmem_alloc(&sm.tmem_base, kTmemCols);
+    tmem_relinquish();
   }
   grid_dep_wait();  // plan and table
   grid_dep_trigger();
@@ -288,25 +324,31 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   const int64_t all = __ldcg(a.plan + c.B);
   const int active = active_ctas(all, a.ctas, a.least);
   const int cta = blockIdx.x;
-  if (all == 0 || cta >= active) return;
-  const int64_t beg = range_beg(all, active, cta), end = range_beg(all, active, cta + 1);
+  int64_t beg = 0, end = 0;
+  if (all > 0 && cta < active) {
+    beg = range_beg(all, active, cta);
+    end = range_beg(all, active, cta + 1);
+  }
+  tc_fence_before();
   __syncthreads();
-  {
+  tc_fence_after();
+  if (beg < end) {
     int before = 0;
-    for (int b = threadIdx.x; b < c.B; b += kTreeThreads) before += __ldcg(a.plan + b + 1) <= beg;
+    for (int b = threadIdx.x; b < c.B; b += blockDim.x) before += __ldcg(a.plan + b + 1) <= beg;
     if (before) atomicAdd(&sm.find, before);
   }
   __syncthreads();
+  const uint32_t tm = sm.tmem_base;
   int b = sm.find;
 
-  if (warp == kConsumers) {
+  if (warp == nw) {
     // ---------------------------------------------------------------- producer
     bool ok = *ab == 0, bad_page = false;
     int issued = 0, s = 0, phase = 1;
     for (int64_t x = beg; ok && x < end;) {
       const Item it = item_at(a, b, x, end);
       b = it.b;
-      const int r0 = it.rb * kRows, r1 = min(r0 + kRows, a.group * it.n);
+      const int r0 = it.rb * a.rows, r1 = min(r0 + a.rows, a.group * it.n);
       const int g0 = r0 / it.n, heads = (r1 - 1) / it.n - g0 + 1;
       const int y0 = a.tab_zero - (it.len + it.n - 1);  // entry of key 0 for the last position
       const int nwin = window_floats(it.n);
@@ -325,8 +367,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         }
         const int pg = __shfl_sync(0xffffffffu, pages, ahead);
         if (issued >= a.stages) {
-          ok = mbar_wait(&sm.empty[s], phase, c.status, ab, kSiteTreeProducer);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = warp_wait(&sm.empty[s], phase, c.status, ab, kSiteTreeProducer);
           if (!ok) break;
         }
         uint8_t* dst = kv + s * 2 * kKvBytes;
@@ -348,335 +389,361 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           s = 0;
           phase ^= 1;
         }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
       }
       x += it.t1 - it.t0;
     }
-    // On the give-up path consumers may not have waited for every copy.
-    if (!__all_sync(0xffffffffu, ok) || *ab) {
-      for (int i = max(0, issued - a.stages); i < issued; ++i)
-        mbar_drain(&sm.full[i % a.stages], (i / a.stages) & 1);
-    }
+    // Copies in flight land before the CTA leaves.
+    for (int i = max(0, issued - a.stages); i < issued; ++i)
+      mbar_drain(&sm.full[i % a.stages], (i / a.stages) & 1);
     if (bad_page) record_bad_arg(c.status);
-    return;
-  }
-
-  // ------------------------------------------------------------------ consumers
-  const int rg = warp % RG, stream = warp / RG;
-  const int quad = lane & 3;
-  const int key0 = stream * kKeys;  // first key of this warp in a tile
-  int s = 0, phase = 0;
-  bool ok = *ab == 0, args_ok = true;
-  int last_b = -1;
-  for (int64_t x = beg; x < end;) {
-    const Item it = item_at(a, b, x, end);
-    b = it.b;
-    if (it.b != last_b) args_ok &= tree_seen(c, it.b, it.n, sm);
-    last_b = it.b;
-    const int n = it.n, len = it.len;
-    const int r0 = it.rb * kRows, r1 = min(r0 + kRows, a.group * n);
-    const int g0 = r0 / n;
-    const int nwin = window_floats(n);
-    const int rem = (a.tab_zero - (len + n - 1)) & 3;
-    // This lane's rows: 2 of each 16.
-    float cs[MT][2], m[MT][2], l[MT][2], o[MT][8][4];
-    int woff[MT][2];
-    uint32_t q[MT][4][4];
+  } else if (warp == nw + 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint32_t id_s = idesc_bf16(128, 64, false, false), id_o = idesc_bf16(128, 64, false, true);
+      const uint64_t qd = sdesc_sw128(smem_u32(sq), 16, 1024);
+      const uint64_t kd = sdesc_sw128(smem_u32(kv), 16, 1024);
+      const uint64_t vd = sdesc_sw128(smem_u32(kv + kKvBytes), 16384, 1024);
+      constexpr uint64_t kStageDesc = 2 * kKvBytes >> 4;
+      bool ok = *ab == 0;
+      int g = 0, item = 0;     // tiles and items so far
+      int s = 0, phase = 0;    // ring slot of the tile whose S comes next
+      auto issue_s = [&]() {
+        if (g > 0) ok = ok && mbar_wait(&sm.s_free, (g - 1) & 1, c.status, ab, kSiteTreeMmaS);
+        ok = ok && mbar_wait(&sm.full[s], phase, c.status, ab, kSiteTreeMmaK);
+        if (!ok) return;
+        tc_fence_after();
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int r = r0 + 16 * (MT * rg + mt) + 8 * hf + (lane >> 2);
-        const bool live = r < r1;
-        const int g = live ? r / n : g0;
-        const int t = live ? r - g * n : 0;
-        const int pos = len + sm.depth[t];
-        float cl = 0.125f;
-        const int head = it.hk * a.group + g;
-        if (a.ssmax) cl *= __ldg(a.s + head) * logf(static_cast<float>(pos + 1));
-        cs[mt][hf] = cl * static_cast<float>(kLog2e);
-        woff[mt][hf] = (g - g0) * nwin + rem + (len + n - 1 - pos) + 2 * quad;
-        if (quad == 0 && stream == 0) {
-          const int rr = 16 * (MT * rg + mt) + 8 * hf + (lane >> 2);
-          sm.node[rr] = live ? t : -1;
-          sm.head[rr] = head;
+        for (int kk = 0; kk < 4; ++kk)
+          umma_ss(tm, qd + 2 * kk, kd + kStageDesc * s + 2 * kk, id_s, kk > 0 ? 1u : 0u);
+        umma_commit(&sm.s_full);
+        ++g;
+        if (++s == a.stages) {
+          s = 0;
+          phase ^= 1;
         }
-        m[mt][hf] = kNoMax;
-        l[mt][hf] = 0.0f;
-        const uint32_t* qr = reinterpret_cast<const uint32_t*>(
-            a.q + ((static_cast<size_t>(it.b) * a.H + head) * c.N + t) * kHeadDim);
+      };
+      for (int64_t x = beg; ok && x < end; ++item) {
+        const Item it = item_at(a, b, x, end);
+        b = it.b;
+        ok = mbar_wait(&sm.q_full, item & 1, c.status, ab, kSiteTreeMmaQ);
+        if (!ok) break;
+        issue_s();
+        for (int t = it.t0; ok && t < it.t1; ++t) {
+          const int sv = (s == 0 ? a.stages : s) - 1, gv = g - 1;  // this tile
+          if (t + 1 < it.t1) issue_s();
+          ok = ok && mbar_wait(&sm.p_full, gv & 1, c.status, ab, kSiteTreeMmaP);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          q[mt][kk][hf] = live ? __ldg(qr + 8 * kk + quad) : 0u;
-          q[mt][kk][2 + hf] = live ? __ldg(qr + 8 * kk + 4 + quad) : 0u;
+          for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_ts(tm + kColO, tm + kColP + 32 * part + 8 * kk, vd + kStageDesc * sv + 128 * kk,
+                      id_o, (t > it.t0 || part > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&sm.pv_done);
+          umma_commit(&sm.empty[sv]);
         }
+        x += it.t1 - it.t0;
       }
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.0f;
+      umma_commit(&sm.mma_final);
+      mbar_drain(&sm.mma_final, 0);
     }
-    consumer_sync();  // rows' nodes and heads; the previous item's join is over
-    const bool rows_live = r0 + 16 * MT * rg < r1;
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const uint32_t tS = tm + tmem_lane_base(warp), tP = tS + kColP, tO = tS + kColO;
+    TreeInfo& ti = sm.info[warp];
+    bool ok = *ab == 0, args_ok = true;
+    int last_b = -1, g = 0, item = 0, s = 0, phase = 0;
+    for (int64_t x = beg; ok && x < end; ++item) {
+      const Item it = item_at(a, b, x, end);
+      b = it.b;
+      if (it.b != last_b) args_ok &= tree_info(c, it.b, it.n, ti);
+      last_b = it.b;
+      const int n = it.n, len = it.len;
+      const int r0 = it.rb * a.rows, r1 = min(r0 + a.rows, a.group * n);
+      const int g0 = r0 / n, nwin = window_floats(n);
+      const int r = r0 + threadIdx.x;
+      const bool live = r < r1, warp_live = r0 + 32 * warp < r1;
+      TreeRow row;
+      row.m = kNoMax;
+      row.l = row.le = 0.0f;
+      const int hg = live ? r / n : g0;
+      const int t_node = live ? r - hg * n : 0;
+      row.node = live ? t_node : -1;
+      row.head = it.hk * a.group + hg;
+      const int pos = len + ti.depth[t_node];
+      row.c = 0.125f * static_cast<float>(kLog2e);
+      if (a.ssmax) row.c *= __ldg(a.s + row.head) * logf(static_cast<float>(pos + 1));
+      row.near = a.table + static_cast<size_t>(row.head) * a.tab_len + a.tab_zero - ti.depth[t_node];
+      const int woff = (hg - g0) * nwin + ((a.tab_zero - (len + n - 1)) & 3) + (len + n - 1 - pos);
+      const size_t orow = (static_cast<size_t>(it.b) * a.H + row.head) * c.N + t_node;
+      // This thread's query row, 16-byte chunks swizzled as the product reads
+      // them.  The previous item's last S is done: its warps waited for it.
+      if (warp_live) {
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + orow * kHeadDim);
+        uint4 w[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) w[y] = live ? __ldg(src + y) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+          *reinterpret_cast<uint4*>(sq + threadIdx.x * 128 + ((y ^ (threadIdx.x & 7)) << 4)) = w[y];
+      }
+      if (warp == 0 && lane < kTreeMax / 32) sm.odd[item & 1][lane] = 0;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full);
 
-    for (int t = it.t0; t < it.t1; ++t) {
-      if (ok) ok = mbar_wait(&sm.full[s], phase, c.status, ab, kSiteTreeConsumer);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint32_t ks = smem_u32(kv + s * 2 * kKvBytes), vs = ks + kKvBytes;
-      const float* w = win + s * a.win_stage + key0;
-      const int j0 = t * kTreeTile + key0;
-      const bool tail = j0 + kKeys > len;  // holds keys that not every row sees
-      bool odd = false;
-#pragma unroll 1
-      for (int ch = 0; rows_live && ch < kKeys / (8 * NT); ++ch) {
-        float z[MT][NT][4];
+      for (int t = it.t0; ok && t < it.t1; ++t, ++g) {
+        const int j0 = t * kTreeTile;
+        const bool tail = j0 + kTreeTile > len;  // holds keys that not every row sees
+        ok = warp_wait(&sm.s_full, g & 1, c.status, ab, kSiteTreeSoftS) &&
+             warp_wait(&sm.full[s], phase, c.status, ab, kSiteTreeSoftK);
+        if (!ok) break;
+        tc_fence_after();
+        const float* w = win + s * a.win_stage + woff;
+        uint64_t z[32];
+        if (warp_live) {
+          uint32_t sv[64];
+          tmem_ld_32x32b_x32(tS, sv);
+          tmem_ld_32x32b_x32(tS + 32, sv + 32);
+          tmem_ld_wait();
+          reg_fence32(sv);
+          reg_fence32(sv + 32);
+          const uint64_t c2 = f2_pack(row.c, row.c);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+          for (int y = 0; y < 32; ++y)
+            z[y] = f2_pack(__uint_as_float(sv[2 * y]), __uint_as_float(sv[2 * y + 1]));
+          if (!tail) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int y = 0; y < 32; ++y) z[y] = ffma2(z[y], c2, f2_pack(w[2 * y], w[2 * y + 1]));
+          } else {
+            const uint64_t vis = row.node >= 0 ? tile_mask(ti.seen[row.node], j0, len) : 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[mt][nt][e] = 0.0f;
+            for (int y = 0; y < 32; ++y) {
+              float e[2];
+              f2_unpack(z[y], e[0], e[1]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk) {
-            uint32_t kb[4];
-            ldsm_x4(ks + (key0 + (ch * NT + nt) * 8 + (lane & 7)) * 128 +
-                        (((4 * kk + (lane >> 3)) ^ (lane & 7)) << 4),
-                    kb);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma_bf16(z[mt][nt], q[mt][2 * kk], kb);
-              mma_bf16(z[mt][nt], q[mt][2 * kk + 1], kb + 2);
+              for (int h = 0; h < 2; ++h) {
+                const int k = 2 * y + h, i = j0 + k - len;
+                float bias = 0.0f;
+                const bool sees = vis >> k & 1;
+                if (sees) bias = i < 0 ? w[k] : __ldcg(row.near + ti.depth[i]);
+                e[h] = sees ? fmaf(e[h], row.c, bias) : -INFINITY;
+              }
+              z[y] = f2_pack(e[0], e[1]);
             }
           }
         }
-        bool raise = false;
-        if (!tail) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.s_free);
+
+        if (tail && warp == 0) {
+          // Rows of V behind the draft hold anything, and a drafted value that
+          // is not finite must not meet the weight 0 of a row that does not
+          // see it: zeros here.  The latter are added to O at the item's end.
+          uint8_t* vt = kv + s * 2 * kKvBytes + kKvBytes;
+          bool any = false;
+#pragma unroll 4
+          for (int y = 0; y < kKvBytes / 512; ++y) {
+            const int chunk = 32 * y + lane, i = j0 + (chunk >> 3) - len;
+            if (i < 0) continue;
+            uint4* p = reinterpret_cast<uint4*>(vt + chunk * 16);
+            uint4 v = *p;
+            uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+            bool fix = i >= n;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const float* wr = w + woff[mt][hf] + ch * NT * 8;
-              float mx = kNoMax;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float& z0 = z[mt][nt][2 * hf];
-                float& z1 = z[mt][nt][2 * hf + 1];
-                z0 = fmaf(z0, cs[mt][hf], wr[8 * nt]);
-                z1 = fmaf(z1, cs[mt][hf], wr[8 * nt + 1]);
-                mx = fmax3(mx, z0, z1);
-              }
-              raise |= mx > m[mt][hf] + kRescale;
+            for (int h = 0; h < 4; ++h) {
+              uint32_t keep = i >= n ? 0u : 0xFFFFFFFFu;
+              if (odd_exp(u[h])) keep &= 0xFFFF0000u;
+              if (odd_exp(u[h] >> 16)) keep &= 0x0000FFFFu;
+              fix |= keep != 0xFFFFFFFFu;
+              if (i < n && keep != 0xFFFFFFFFu) atomicOr(&sm.odd[item & 1][i >> 5], 1u << (i & 31));
+              u[h] &= keep;
             }
+            if (fix) *p = v;
+            any |= fix;
           }
-        } else {
+          if (any) fence_proxy_async_smem();
+          __syncwarp();
+        }
+
+        bool resc = false;
+        float scale = 1.0f;
+        if (warp_live) {
+          float mq[4];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
+          for (int y = 0; y < 4; ++y) {
+            float lo, hi;
+            f2_unpack(z[y], lo, hi);
+            mq[y] = fmaxf(lo, hi);
+          }
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const int rr = 16 * (MT * rg + mt) + 8 * hf + (lane >> 2);
-              const int nd = sm.node[rr];
-              const float* wr = w + woff[mt][hf] + ch * NT * 8;
-              // table entry of an ancestor at depth x: near + x
-              const float* near = a.table + static_cast<size_t>(sm.head[rr]) * a.tab_len +
-                                  a.tab_zero - (nd >= 0 ? sm.depth[nd] : 0);
-              float mx = kNoMax;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float& zz = z[mt][nt][2 * hf + e];
-                  const int j = j0 + (ch * NT + nt) * 8 + 2 * quad + e, i = j - len;
-                  if (i < 0) {
-                    zz = fmaf(zz, cs[mt][hf], wr[8 * nt + e]);
-                  } else if (nd >= 0 && i < n && (sm.seen[nd][i >> 5] >> (i & 31) & 1)) {
-                    zz = fmaf(zz, cs[mt][hf], __ldcg(near + sm.depth[i]));
-                  } else {
-                    zz = -INFINITY;
-                  }
-                  mx = fmaxf(mx, zz);
-                }
-              }
-              raise |= mx > m[mt][hf] + kRescale;
-            }
+          for (int y = 4; y < 32; ++y) {
+            float lo, hi;
+            f2_unpack(z[y], lo, hi);
+            mq[y & 3] = fmax3(mq[y & 3], lo, hi);
+          }
+          const float m_new = fmaxf(row.m, fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])));
+          resc = m_new > row.m + kRescale;
+          if (resc) {
+            scale = ex2_approx(row.m - m_new);
+            row.l *= scale;
+            row.le *= scale;
+            row.m = m_new;
           }
         }
-        if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              float mx = kNoMax;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mx = fmax3(mx, z[mt][nt][2 * hf], z[mt][nt][2 * hf + 1]);
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-              if (mx > m[mt][hf]) {
-                const float corr = ex2_approx(m[mt][hf] - mx);
-                l[mt][hf] *= corr;
-#pragma unroll
-                for (int nt = 0; nt < 8; ++nt) {
-                  o[mt][nt][2 * hf] *= corr;
-                  o[mt][nt][2 * hf + 1] *= corr;
-                }
-                m[mt][hf] = mx;
-              }
-            }
-          }
+        if (g > 0) {
+          // The previous P V is done: P may be overwritten, O is at rest.
+          ok = warp_wait(&sm.pv_done, (g - 1) & 1, c.status, ab, kSiteTreeSoftPV);
+          if (!ok) break;
+          tc_fence_after();
         }
+        if (warp_live) {
+          const uint64_t negm2 = f2_pack(-row.m, -row.m);
+          float lr[4] = {0.f, 0.f, 0.f, 0.f};
+          uint64_t le2[2] = {0ull, 0ull};
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[PARTS][16];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float p = ex2_approx(z[mt][nt][e] - m[mt][e >> 1]);
-              z[mt][nt][e] = p;
-              l[mt][e >> 1] += p;
-            }
-        // 16 keys at a time: two column tiles of S are the left operand.
-#pragma unroll
-        for (int k2 = 0; k2 < NT / 2; ++k2) {
-          uint32_t pa[MT][PARTS][4];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float lo = z[mt][2 * k2 + (e >> 1)][2 * (e & 1)];
-              float hi = z[mt][2 * k2 + (e >> 1)][2 * (e & 1) + 1];
+            for (int y = 0; y < 16; ++y) {
+              float p0, p1;
+              f2_unpack(fadd2(z[16 * q + y], negm2), p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              le2[y & 1] = fadd2(le2[y & 1], f2_pack(p0, p1));
 #pragma unroll
               for (int part = 0; part < PARTS; ++part) {
-                const uint32_t pk = pack_bf16x2(lo, hi);
-                pa[mt][part][e] = pk;
-                lo -= bf16_lo(pk);
-                hi -= bf16_hi(pk);
+                const uint32_t u = pack_bf16x2(p0, p1);
+                pk[part][y] = u;
+                if (PARTS == 1) {
+                  add_bf16x2_f32(u, lr[2 * (y & 1)], lr[2 * (y & 1) + 1]);
+                } else {
+                  p0 -= __uint_as_float(u << 16);
+                  p1 -= __uint_as_float(u & 0xFFFF0000u);
+                }
+              }
+            }
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part)
+              tmem_st_32x32b_x16(tP + 32 * part + 16 * q, pk[part]);
+          }
+          float b0, b1;
+          f2_unpack(fadd2(le2[0], le2[1]), b0, b1);
+          row.le += b0 + b1;
+          row.l += (lr[0] + lr[1]) + (lr[2] + lr[3]);
+          if (t > it.t0 && __any_sync(0xffffffffu, resc)) {
+            uint32_t ov[64];
+            tmem_ld_32x32b_x32(tO, ov);
+            tmem_ld_32x32b_x32(tO + 32, ov + 32);
+            tmem_ld_wait();
+            reg_fence32(ov);
+            reg_fence32(ov + 32);
+#pragma unroll
+            for (int y = 0; y < 64; ++y) ov[y] = __float_as_uint(__uint_as_float(ov[y]) * scale);
+            tmem_st_32x32b_x32(tO, ov);
+            tmem_st_32x32b_x32(tO + 32, ov + 32);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full);
+        if (++s == a.stages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      ok = warp_wait(&sm.pv_done, (g - 1) & 1, c.status, ab, kSiteTreeSoftEnd);
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole = it.t0 == 0 && it.t1 == it.tiles;
+      if (warp_live) {
+        const uint32_t* odd = sm.odd[item & 1];
+        const bool any_odd = (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
+        const float norm = PARTS == 1 ? row.l : row.le;
+        const size_t prow = static_cast<size_t>(2 * cta + (it.t0 == 0 ? 1 : 0)) * a.rows + threadIdx.x;
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb) {
+          uint32_t ov[32];
+          tmem_ld_32x32b_x32(tO + 32 * hb, ov);
+          tmem_ld_wait();
+          reg_fence32(ov);
+          float* o = reinterpret_cast<float*>(ov);
+          if (!live) continue;
+          if (any_odd) {
+            // Values that are not finite, for the nodes that see them.
+            for (int i = 0; i < n; ++i) {
+              if (!(odd[i >> 5] >> (i & 31) & 1) || !(ti.seen[row.node][i >> 5] >> (i & 31) & 1))
+                continue;
+              const int slot = len + i;
+              int pg = __ldg(c.block_table + static_cast<size_t>(it.b) * c.max_blocks + slot / c.page);
+              if (pg < 0 || pg >= c.num_pages) pg = 0;
+              const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                  a.v_pages +
+                  ((static_cast<size_t>(pg) * c.Hkv + it.hk) * c.page + slot % c.page) * kHeadDim +
+                  32 * hb);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) {
+                const uint32_t u = __ldg(v + y);
+                if (odd_exp(u)) o[2 * y] += __uint_as_float(u << 16);
+                if (odd_exp(u >> 16)) o[2 * y + 1] += __uint_as_float(u & 0xFFFF0000u);
               }
             }
           }
-          const int kb = (ch * NT + 2 * k2) * 8;  // first key, from this warp's
+          if (!whole) {
+            float4* dst = reinterpret_cast<float4*>(a.part + prow * kHeadDim + 32 * hb);
 #pragma unroll
-          for (int dp = 0; dp < 4; ++dp) {
-            uint32_t vb[4];
-            ldsm_x4_t(vs + (key0 + kb + (lane & 15)) * 128 + (((2 * dp + (lane >> 4)) ^ (lane & 7)) << 4),
-                      vb);
-            if (tail) {
-              // Rows behind the draft hold anything: zeros.  A drafted value
-              // that is not finite is zero here (a weight of 0 would turn it
-              // into NaN for the rows that do not see it) and is added below
-              // to those that do.
+            for (int y = 0; y < 8; ++y)
+              dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          } else {
+            const float inv = 1.0f / norm;
+            if (PARTS > 1) {
+              float4* dst =
+                  reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kHeadDim + 32 * hb);
+#pragma unroll
+              for (int y = 0; y < 8; ++y)
+                dst[y] = make_float4(o[4 * y] * inv, o[4 * y + 1] * inv, o[4 * y + 2] * inv,
+                                     o[4 * y + 3] * inv);
+            } else {
+              uint4* dst =
+                  reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * kHeadDim + 32 * hb);
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
-                const int i = j0 + kb + 8 * (y & 1) + 2 * quad - len;
-                uint32_t keep = 0xFFFFFFFFu;
-                if (i >= n || (i >= 0 && odd_exp(vb[y]))) keep &= 0xFFFF0000u;
-                if (i + 1 >= n || (i + 1 >= 0 && odd_exp(vb[y] >> 16))) keep &= 0x0000FFFFu;
-                odd |= (i >= 0 && i < n && !(keep & 1u)) || (i + 1 >= 0 && i + 1 < n && !(keep >> 31));
-                vb[y] &= keep;
-              }
-            }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-              for (int part = 0; part < PARTS; ++part) {
-                mma_bf16(o[mt][2 * dp], pa[mt][part], vb);
-                mma_bf16(o[mt][2 * dp + 1], pa[mt][part], vb + 2);
+                float* e = o + 8 * y;
+                dst[y] = make_uint4(pack_bf16x2(e[0] * inv, e[1] * inv),
+                                    pack_bf16x2(e[2] * inv, e[3] * inv),
+                                    pack_bf16x2(e[4] * inv, e[5] * inv),
+                                    pack_bf16x2(e[6] * inv, e[7] * inv));
               }
             }
           }
         }
-      }
-      if (tail && __any_sync(0xffffffffu, odd)) {
-        const uint8_t* vt = kv + s * 2 * kKvBytes + kKvBytes;
-#pragma unroll 1
-        for (int j = max(len, j0); j < min(len + n, j0 + kKeys); ++j) {
-          const int row = j - t * kTreeTile, i = j - len;
-#pragma unroll
-          for (int nt = 0; nt < 8; ++nt) {
-            const uint32_t v =
-                *reinterpret_cast<const uint32_t*>(vt + row * 128 + ((nt ^ (row & 7)) << 4) + 4 * quad);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                const int nd = sm.node[16 * (MT * rg + mt) + 8 * hf + (lane >> 2)];
-                if (nd >= 0 && (sm.seen[nd][i >> 5] >> (i & 31) & 1)) {
-                  if (odd_exp(v)) o[mt][nt][2 * hf] += bf16_lo(v);
-                  if (odd_exp(v >> 16)) o[mt][nt][2 * hf + 1] += bf16_hi(v);
-                }
-              }
-            }
-          }
+        if (live) {
+          if (!whole)
+            a.part_ml[prow] = make_float4(row.m, norm, row.le, 0.0f);
+          else if (a.lse)
+            a.lse[orow] = (row.m + log2f(row.le)) * kLn2f;
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.empty[s]);
-      if (++s == a.stages) {
-        s = 0;
-        phase ^= 1;
-      }
+      // O has been read before the next item's products overwrite it: they
+      // wait for its p_full, on which every warp arrives after this.
+      tc_fence_before();
+      x += it.t1 - it.t0;
     }
-
-    // Join the parts of the keys in shared memory.  After a give-up the values mean
-    // nothing, but every warp comes here for every item, so the barriers match.
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 1);
-        l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 2);
-        const int rr = stream * kRows + 16 * (MT * rg + mt) + 8 * hf + (lane >> 2);
-        if (quad == 0) merge_ml[rr] = make_float2(m[mt][hf], l[mt][hf]);
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
-          *reinterpret_cast<float2*>(merge + rr * kMergeStride + 8 * nt + 2 * quad) =
-              make_float2(o[mt][nt][2 * hf], o[mt][nt][2 * hf + 1]);
-      }
-    }
-    consumer_sync();
-    const bool whole = it.t0 == 0 && it.t1 == it.tiles;
-    const int slot = 2 * cta + (it.t0 == 0 ? 1 : 0);
-    for (int e = threadIdx.x; e < kRows * 16; e += 32 * kConsumers) {
-      const int rr = e >> 4, col = (e & 15) * 4, r = r0 + rr;
-      if (r >= r1) break;
-      float M = kNoMax, L = 0.0f;
-#pragma unroll
-      for (int st = 0; st < kStreams; ++st) M = fmaxf(M, merge_ml[st * kRows + rr].x);
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int st = 0; st < kStreams; ++st) {
-        const float2 ml = merge_ml[st * kRows + rr];
-        const float4 y = *reinterpret_cast<const float4*>(merge + (st * kRows + rr) * kMergeStride + col);
-        const float f = ex2_approx(ml.x - M);
-        L += ml.y * f;
-        v.x += y.x * f;
-        v.y += y.y * f;
-        v.z += y.z * f;
-        v.w += y.w * f;
-      }
-      if (whole) {
-        const int g = r / n, nd = r - g * n;
-        const size_t row = (static_cast<size_t>(it.b) * a.H + it.hk * a.group + g) * c.N + nd;
-        v.x /= L;
-        v.y /= L;
-        v.z /= L;
-        v.w /= L;
-        if (PARTS > 1) {
-          *reinterpret_cast<float4*>(static_cast<float*>(a.o) + row * kHeadDim + col) = v;
-        } else {
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + row * kHeadDim + col) =
-              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-        }
-        if (a.lse && col == 0) a.lse[row] = (M + log2f(L)) * kLn2f;
-      } else {
-        const size_t row = static_cast<size_t>(slot) * kRows + rr;
-        *reinterpret_cast<float4*>(a.part + row * kHeadDim + col) = v;
-        if (col == 0) a.part_ml[row] = make_float2(M, L);
-      }
-    }
-    x += it.t1 - it.t0;
+    if (!args_ok) record_bad_arg(c.status);
   }
-  if (!args_ok) record_bad_arg(c.status);
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == nw + 1) {
+    tc_fence_after();
+    tmem_dealloc(tm, kTmemCols);
+  }
 }
 
 // One warp per row (b, h, t): joins the parts of an item that was cut.
@@ -713,7 +780,7 @@ __global__ void __launch_bounds__(256) bam_tree_combine_kernel(const TreeArgs a)
       auto part_row = [&](int cta) {
         return static_cast<size_t>(2 * cta + (cta == c0 ? 1 : 0)) * a.rows + rr;
       };
-      float M = kNoMax, L = 0.0f;
+      float M = kNoMax, L = 0.0f, LE = 0.0f;
       for (int x = c0 + lane; x <= c1; x += 32) M = fmaxf(M, __ldcg(a.part_ml + part_row(x)).x);
 #pragma unroll
       for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
@@ -721,16 +788,17 @@ __global__ void __launch_bounds__(256) bam_tree_combine_kernel(const TreeArgs a)
 #pragma unroll 4
       for (int x = c0; x <= c1; ++x) {
         const size_t pr = part_row(x);
-        const float2 ml = __ldcg(a.part_ml + pr);
+        const float4 ml = __ldcg(a.part_ml + pr);
         const float2 y = __ldcg(reinterpret_cast<const float2*>(a.part + pr * kHeadDim) + lane);
         const float f = ex2_approx(ml.x - M);
         L += ml.y * f;
+        LE += ml.z * f;
         v.x += y.x * f;
         v.y += y.y * f;
       }
       v.x /= L;
       v.y /= L;
-      lse = (M + log2f(L)) * kLn2f;
+      lse = (M + log2f(LE)) * kLn2f;
     }
     if (a.o_fp32)
       reinterpret_cast<float2*>(static_cast<float*>(a.o) + row * kHeadDim)[lane] = v;
@@ -745,38 +813,20 @@ constexpr size_t kSmemTwo = 113 * 1024;  // a CTA's share when two fit an SM
 constexpr size_t kSmemOne = 227 * 1024;
 
 // Shared memory of a CTA besides its ring stages, and of one stage.
-size_t smem_fixed(int rows) {
-  const int streams = rows <= 32 ? kConsumers : kConsumers * 32 / rows;
-  return 1024 + static_cast<size_t>(streams) * rows * (kMergeStride * 4 + 8) + sizeof(TreeSmem);
-}
+constexpr size_t kSmemFixed = 1024 + kQBytes + sizeof(TreeSmem);
 size_t smem_stage(const TreeArgs& a) {
   return 2 * kKvBytes + static_cast<size_t>(a.win_stage) * 4;
-}
-
-template <int MT, int RG, int PARTS>
-cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a,
-                        cudaStream_t st) {
-  static bool limit_set[64] = {};
-  auto kernel = bam_tree_kernel<MT, RG, PARTS>;
-  const cudaError_t e = smem_limit_once(kernel, kSmemOne, limit_set);
-  if (e != cudaSuccess) return e;
-  return launch_k(kernel, dim3(a.ctas), dim3(kTreeThreads),
-                  smem_fixed(a.rows) + a.stages * smem_stage(a), st, true, tk, tv, a);
 }
 
 template <int PARTS>
 cudaError_t launch_parts(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a,
                          cudaStream_t st) {
-  switch (a.rows) {
-    case 16:
-      return launch_rows<1, 1, PARTS>(tk, tv, a, st);
-    case 32:
-      return launch_rows<2, 1, PARTS>(tk, tv, a, st);
-    case 64:
-      return launch_rows<2, 2, PARTS>(tk, tv, a, st);
-    default:
-      return launch_rows<2, 4, PARTS>(tk, tv, a, st);
-  }
+  static bool limit_set[64] = {};
+  auto kernel = bam_tree_kernel<PARTS>;
+  const cudaError_t e = smem_limit_once(kernel, kSmemOne, limit_set);
+  if (e != cudaSuccess) return e;
+  return launch_k(kernel, dim3(a.ctas), dim3(a.rows + 64), kSmemFixed + a.stages * smem_stage(a),
+                  st, true, tk, tv, a);
 }
 
 }  // namespace
@@ -791,7 +841,7 @@ bool tree_config(TreeArgs* a, int sms) {
     if (heads > a->group) heads = a->group;
     if (heads * window_floats(n) > a->win_stage) a->win_stage = heads * window_floats(n);
   }
-  const size_t fixed = smem_fixed(a->rows), stage = smem_stage(*a);
+  const size_t fixed = kSmemFixed, stage = smem_stage(*a);
   int per_sm = 2;
   size_t budget = kSmemTwo;
   if (fixed + 3 * stage > budget) {
@@ -801,7 +851,7 @@ bool tree_config(TreeArgs* a, int sms) {
   a->stages = static_cast<int>((budget - fixed) / stage);
   if (a->stages > kMaxStages) a->stages = kMaxStages;
   a->ctas = per_sm * sms < kTreeCtas ? per_sm * sms : kTreeCtas;
-  a->least = 2;
+  a->least = 1;
   return a->stages >= 2 && a->ctas >= 1;
 }
 

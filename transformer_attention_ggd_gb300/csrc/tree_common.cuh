@@ -54,6 +54,7 @@ constexpr int kTreeCtas = 304;   // most CTAs (two per SM)
 struct TreeArgs {
   CacheArgs c;
   const uint16_t* q;  // [B, H, N, 64]
+  const uint16_t* v_pages;
   const float* alpha;
   const float* beta;
   const float* mu;
@@ -63,18 +64,18 @@ struct TreeArgs {
   int64_t* plan;      // [B + 1] first tile of each sequence, and W
   float* table;       // [H, tab_len]: entry y is b_h(tab_zero - y) * log2(e)
   float* part;        // [2 * kTreeCtas, rows, 64] partial outputs
-  float2* part_ml;    // [2 * kTreeCtas, rows]: maximum (log2 units), sum
+  float4* part_ml;    // [2 * kTreeCtas, rows]: maximum (log2 units), sum that normalises, exact sum
   float eps;
   int H, group, prior, ssmax, o_fp32;
   int tab_len, tab_zero;
-  int rows;           // rows of an item: 16, 32, 64 or 128
+  int rows;           // rows of an item, at most: 32, 64, 96 or 128
   int ctas, least;    // CTAs of the launch; tiles that one gets at least
   int stages;         // ring stages
   int win_stage;      // floats of a stage's table windows
 };
 
 // Rows of an item for `rows` (head, node) pairs.
-inline int tree_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+inline int tree_rows(int64_t rows) { return rows >= 128 ? 128 : static_cast<int>((rows + 31) / 32 * 32); }
 // Table row: distances 0 .. Tmax at entries Tmax .. 0 and, behind entry
 // Tmax, room for windows that reach past the last key.
 inline int tree_table_zero(int Tmax) { return (Tmax + 63) / 64 * 64; }
