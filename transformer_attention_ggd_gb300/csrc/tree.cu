@@ -20,10 +20,13 @@
 namespace bam {
 namespace {
 
-constexpr int kTreeThreads = 192;  // softmax warps (at most 4), producer, MMA issuer
+constexpr int kSoftWarps = 4;
+constexpr int kTreeThreads = 32 * (kSoftWarps + 2);  // and the producer and the MMA issuer
 constexpr int kRowsMax = 128;      // rows of an item: lanes of Tensor Memory
 constexpr int kKvBytes = kTreeTile * kHeadDim * 2;  // 8 KB of K (and of V) a tile
 constexpr int kQBytes = kRowsMax * kHeadDim * 2;
+constexpr int kMergeStride = 68;  // floats of a merge row: 16-byte reads of 32 rows spread over the banks
+constexpr int kNear = 32 + 2 * kTreeMax;  // a warp's table entries of the draft's distances
 constexpr int kMaxStages = 8;
 constexpr float kRescale = 8.0f;  // log2 units by which a weight may exceed 1
 constexpr float kNoMax = -3.4e38f;  // below every logit (the table is clamped at -3e38)
@@ -41,7 +44,8 @@ enum : int {
   kSiteTreeSoftS = 66,
   kSiteTreeSoftK = 67,
   kSiteTreeSoftPV = 68,
-  kSiteTreeSoftEnd = 69
+  kSiteTreeSoftEnd = 69,
+  kSiteTreeMerge = 70
 };
 
 // Depths and ancestors of a sequence's nodes; every softmax warp has its own,
@@ -50,15 +54,18 @@ struct TreeInfo {
   uint32_t seen[kTreeMax][kTreeMax / 32];  // a node's ancestors, and itself
   int jump[kTreeMax];
   int depth[kTreeMax];
+  float near[kNear];  // [head of the warp's rows][distance < n]
 };
 
 struct __align__(16) TreeSmem {
-  TreeInfo info[kRowsMax / 32];
+  TreeInfo info[kSoftWarps];
+  float4 merge_ml[kRowsMax];
   uint64_t full[kMaxStages];   // K, V and table windows of a stage have arrived
   uint64_t empty[kMaxStages];  // its P V is done
   uint64_t q_full;             // the item's queries are in shared memory
   uint64_t s_full, s_free;     // S is complete; S is in registers
   uint64_t p_full, pv_done;    // P is in Tensor Memory; P V is done
+  uint64_t merge_full, merge_free;  // the item's parts are in shared memory; are read
   uint64_t mma_final;
   uint32_t odd[2][kTreeMax / 32];  // nodes whose value is not finite, by item parity
   uint32_t tmem_base;
@@ -238,21 +245,52 @@ __host__ __device__ __forceinline__ int window_floats(int n) {
   return (3 + kTreeTile + n - 1 + 3) & ~3;
 }
 
+// Bytes of the query buffer, which also holds the copies' outputs at an
+// item's end (24.5 KB for three copies of 32 rows, 17 KB for one of 64).
+__host__ __device__ constexpr int q_bytes(int ks) {
+  return ks == 1 ? kQBytes : ((kRowsMax - kRowsMax / ks) * kMergeStride * 4 + 1023) / 1024 * 1024;
+}
+static_assert(q_bytes(2) >= kQBytes && q_bytes(4) >= kQBytes, "queries");
+
+// N columns (16, 32 or 64) of this warp's lanes of Tensor Memory.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
+  if constexpr (N == 16) {
+    tmem_ld_32x32b_x16(taddr, r);
+    tmem_ld_wait();
+    reg_fence16(r);
+  } else {
+    tmem_ld_32x32b_x32(taddr, r);
+    if (N == 64) tmem_ld_32x32b_x32(taddr + 32, r + 32);
+    tmem_ld_wait();
+    reg_fence32(r);
+    if (N == 64) reg_fence32(r + 32);
+  }
+}
+
+// D[tmem] (+)= A[tmem] * B[smem] for the 128 / KS lanes of one copy; the other
+// lanes of D keep their values.
+template <int KS>
+__device__ __forceinline__ void umma_ts_lanes(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                              uint32_t idesc, uint32_t accumulate, int copy) {
+  uint32_t off[4];  // a bit per lane: not written
+#pragma unroll
+  for (int x = 0; x < 4; ++x) off[x] = x / (4 / KS) == copy ? 0u : 0xFFFFFFFFu;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n}\n" ::"r"(
+          d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(off[0]), "r"(off[1]), "r"(off[2]),
+      "r"(off[3])
+      : "memory");
+}
+
 // ---------------------------------------------------------------- attention
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, DevStatus* st,
                                           volatile int* ab, int site) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, st, ab, site));
 }
-
-// The softmax state of one row (the thread's lane of Tensor Memory).
-struct TreeRow {
-  float m, l, le;     // maximum (log2 units), sum of the rounded weights, exact sum
-  float c;            // logit scale, log2 units
-  int node;           // -1: no row
-  int head;
-  const float* near;  // table entry of an ancestor at depth 0
-};
 
 // Visibility of the 64 keys of a tile that starts at j0 to a node: committed
 // keys, then the bits of its ancestors.
@@ -270,32 +308,43 @@ __device__ __forceinline__ uint64_t tile_mask(const uint32_t* seen, int j0, int 
 }
 
 // One CTA walks its run of tiles; two CTAs share an SM, so that one's
-// hand-offs are covered by the other's work.  Roles: a softmax warp per 32
-// rows, a producer warp (TMA loads of K and V, bulk copies of the table
-// windows of the item's heads, into a ring), and a thread that issues the
-// products:
+// hand-offs are covered by the other's work.  Roles: four softmax warps, a
+// producer warp (TMA loads of K and V, bulk copies of the table windows of
+// the item's heads, into a ring), and a thread that issues the products:
 //   S = Q K^T   128 x 64 x 64, Q and K from shared memory (K-major),
 //   O += P V    128 x 64 x 64, P from Tensor Memory, V from shared memory.
-// All 128 rows are computed whatever their number: at 64 keys a tile the two
-// products take 256 cycles of an SM's tensor core, its share of HBM delivers
-// the tile's 16 KB in about 700.  The next tile's S runs while the softmax
-// works on this tile's.  One thread owns one row, so the softmax needs no
-// exchange; O is rescaled only when a row's maximum grows by more than 8.
+// All 128 lanes are computed whatever the number of rows: at 64 keys a tile
+// the two products take 256 cycles of an SM's tensor core, its share of HBM
+// delivers the tile's 16 KB in about 700.  The next tile's S runs while the
+// softmax works on this tile's.
+//
+// KS (1, 2, 4): an item of at most 128 / KS rows fills Tensor Memory KS times
+// over, and each copy of a row works on its own 64 / KS keys of every tile,
+// with its own maximum, sum and output, which are joined at the item's end.
+// The products cost the same (a step of P V adds to the lanes of its keys'
+// copy only), and the softmax, a thread per row and copy, takes a KS-th of
+// the time.  The softmax needs no exchange between threads; O is rescaled
+// only when a row's maximum grows by more than 8.
+//
 // PARTS: bf16 parts of a weight in the product with V.  With one, the sum
 // that normalises is that of the rounded weights, so that the rounding of a
 // weight that dominates its row cancels; three carry 24 bits.
-template <int PARTS>
+template <int PARTS, int KS>
 __global__ void __launch_bounds__(kTreeThreads, 2)
     bam_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                     const TreeArgs a) {
+  constexpr int nw = kSoftWarps;
+  constexpr int kRows = kRowsMax / KS;   // rows of an item
+  constexpr int kGroups = kRows / 32;    // warps of a copy
+  constexpr int kCols = kTreeTile / KS;  // keys of a tile for one copy
   extern __shared__ __align__(16) uint8_t smem_raw[];
   uint8_t* const sq = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
-  uint8_t* const kv = sq + kQBytes;  // [stages][K, V]
+  float* const merge = reinterpret_cast<float*>(sq);  // [KS - 1][kRows][kMergeStride], after Q's use
+  uint8_t* const kv = sq + q_bytes(KS);  // [stages][K, V]
   float* const win = reinterpret_cast<float*>(kv + a.stages * 2 * kKvBytes);
   TreeSmem& sm = *reinterpret_cast<TreeSmem*>(win + a.stages * a.win_stage);
   const CacheArgs& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nw = a.rows / 32;  // softmax warps
   volatile int* ab = &sm.abort_flag;
 
   if (threadIdx.x == 0) {
@@ -310,6 +359,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     mbar_init(&sm.s_free, nw);
     mbar_init(&sm.p_full, nw);
     mbar_init(&sm.pv_done, 1);
+    mbar_init(&sm.merge_full, nw);
+    mbar_init(&sm.merge_free, nw);
     mbar_init(&sm.mma_final, 1);
     fence_barrier_init();
     sm.find = 0;
@@ -348,7 +399,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     for (int64_t x = beg; ok && x < end;) {
       const Item it = item_at(a, b, x, end);
       b = it.b;
-      const int r0 = it.rb * a.rows, r1 = min(r0 + a.rows, a.group * it.n);
+      const int r0 = it.rb * kRows, r1 = min(r0 + kRows, a.group * it.n);
       const int g0 = r0 / it.n, heads = (r1 - 1) / it.n - g0 + 1;
       const int y0 = a.tab_zero - (it.len + it.n - 1);  // entry of key 0 for the last position
       const int nwin = window_floats(it.n);
@@ -439,9 +490,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 #pragma unroll
           for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_ts(tm + kColO, tm + kColP + 32 * part + 8 * kk, vd + kStageDesc * sv + 128 * kk,
-                      id_o, (t > it.t0 || part > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) {
+              // 16 keys; they belong to copy kk / (4 / KS).
+              constexpr int kSteps = 4 / KS;
+              umma_ts_lanes<KS>(tm + kColO, tm + kColP + 32 * part + 8 * kk,
+                                vd + kStageDesc * sv + 128 * kk, id_o,
+                                (t > it.t0 || part > 0 || kk % kSteps > 0) ? 1u : 0u, kk / kSteps);
+            }
           umma_commit(&sm.pv_done);
           umma_commit(&sm.empty[sv]);
         }
@@ -452,7 +507,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    const uint32_t tS = tm + tmem_lane_base(warp), tP = tS + kColP, tO = tS + kColO;
+    const int rg = warp % kGroups, copy = warp / kGroups;
+    const int k0 = copy * kCols;  // first key of this copy in a tile
+    const uint32_t lanes = tm + tmem_lane_base(warp);
+    const uint32_t tS = lanes + k0, tP = lanes + kColP + k0 / 2, tO = lanes + kColO;
     TreeInfo& ti = sm.info[warp];
     bool ok = *ab == 0, args_ok = true;
     int last_b = -1, g = 0, item = 0, s = 0, phase = 0;
@@ -462,30 +520,38 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       if (it.b != last_b) args_ok &= tree_info(c, it.b, it.n, ti);
       last_b = it.b;
       const int n = it.n, len = it.len;
-      const int r0 = it.rb * a.rows, r1 = min(r0 + a.rows, a.group * n);
+      const int r0 = it.rb * kRows, r1 = min(r0 + kRows, a.group * n);
+      const int rw = r0 + 32 * rg;  // first row of the warp
       const int g0 = r0 / n, nwin = window_floats(n);
-      const int r = r0 + threadIdx.x;
-      const bool live = r < r1, warp_live = r0 + 32 * warp < r1;
-      TreeRow row;
-      row.m = kNoMax;
-      row.l = row.le = 0.0f;
-      const int hg = live ? r / n : g0;
-      const int t_node = live ? r - hg * n : 0;
-      row.node = live ? t_node : -1;
-      row.head = it.hk * a.group + hg;
-      const int pos = len + ti.depth[t_node];
-      row.c = 0.125f * static_cast<float>(kLog2e);
-      if (a.ssmax) row.c *= __ldg(a.s + row.head) * logf(static_cast<float>(pos + 1));
-      row.near = a.table + static_cast<size_t>(row.head) * a.tab_len + a.tab_zero - ti.depth[t_node];
-      const int woff = (hg - g0) * nwin + ((a.tab_zero - (len + n - 1)) & 3) + (len + n - 1 - pos);
-      const size_t orow = (static_cast<size_t>(it.b) * a.H + row.head) * c.N + t_node;
-      // This thread's query row, 16-byte chunks swizzled as the product reads
-      // them.  The previous item's last S is done: its warps waited for it.
+      const int r = rw + lane;
+      const bool live = r < r1, warp_live = rw < r1;
+      const int hg = (live ? r : warp_live ? rw : r0) / n;
+      const int node = live ? r - hg * n : 0;
+      const int head = it.hk * a.group + hg, depth = ti.depth[node];
+      float m = kNoMax, l = 0.0f, le = 0.0f;  // log2 units; sums of rounded and of exact weights
+      float cs = 0.125f * static_cast<float>(kLog2e);
+      if (a.ssmax) cs *= __ldg(a.s + head) * logf(static_cast<float>(len + depth + 1));
+      const int woff = (hg - g0) * nwin + ((a.tab_zero - (len + n - 1)) & 3) + (n - 1 - depth) + k0;
+      const size_t orow = (static_cast<size_t>(it.b) * a.H + head) * c.N + node;
+      const float* near = ti.near + depth;  // table entry of an ancestor: near[-its depth]
       if (warp_live) {
+        // This thread's query row, 16-byte chunks swizzled as the product
+        // reads them.  The previous item's last S is done: its warps waited
+        // for it.
         const uint4* src = reinterpret_cast<const uint4*>(a.q + orow * kHeadDim);
         uint4 w[8];
 #pragma unroll
         for (int y = 0; y < 8; ++y) w[y] = live ? __ldg(src + y) : make_uint4(0, 0, 0, 0);
+        if (it.t1 * kTreeTile > len) {
+          // Some tile holds drafted keys: their distances' table entries.
+          const int h0 = rw / n;
+          const int cnt = ((min(rw + 32, r1) - 1) / n - h0 + 1) * n;
+          const float* tab = a.table + static_cast<size_t>(it.hk * a.group + h0) * a.tab_len + a.tab_zero;
+          __syncwarp();
+          for (int y = lane; y < cnt; y += 32)
+            ti.near[y] = __ldcg(tab + static_cast<size_t>(y / n) * a.tab_len - y % n);
+          near += (hg - h0) * n;
+        }
 #pragma unroll
         for (int y = 0; y < 8; ++y)
           *reinterpret_cast<uint4*>(sq + threadIdx.x * 128 + ((y ^ (threadIdx.x & 7)) << 4)) = w[y];
@@ -503,34 +569,29 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         if (!ok) break;
         tc_fence_after();
         const float* w = win + s * a.win_stage + woff;
-        uint64_t z[32];
+        uint64_t z[kCols / 2];
         if (warp_live) {
-          uint32_t sv[64];
-          tmem_ld_32x32b_x32(tS, sv);
-          tmem_ld_32x32b_x32(tS + 32, sv + 32);
-          tmem_ld_wait();
-          reg_fence32(sv);
-          reg_fence32(sv + 32);
-          const uint64_t c2 = f2_pack(row.c, row.c);
-#pragma unroll
-          for (int y = 0; y < 32; ++y)
-            z[y] = f2_pack(__uint_as_float(sv[2 * y]), __uint_as_float(sv[2 * y + 1]));
+          uint32_t sv[kCols];
+          tmem_ld_cols<kCols>(tS, sv);
+          const uint64_t c2 = f2_pack(cs, cs);
           if (!tail) {
 #pragma unroll
-            for (int y = 0; y < 32; ++y) z[y] = ffma2(z[y], c2, f2_pack(w[2 * y], w[2 * y + 1]));
+            for (int y = 0; y < kCols / 2; ++y)
+              z[y] = ffma2(f2_pack(__uint_as_float(sv[2 * y]), __uint_as_float(sv[2 * y + 1])), c2,
+                           f2_pack(w[2 * y], w[2 * y + 1]));
           } else {
-            const uint64_t vis = row.node >= 0 ? tile_mask(ti.seen[row.node], j0, len) : 0;
+            const uint64_t vis = live ? tile_mask(ti.seen[node], j0, len) >> k0 : 0;
 #pragma unroll
-            for (int y = 0; y < 32; ++y) {
+            for (int y = 0; y < kCols / 2; ++y) {
               float e[2];
-              f2_unpack(z[y], e[0], e[1]);
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int k = 2 * y + h, i = j0 + k - len;
-                float bias = 0.0f;
-                const bool sees = vis >> k & 1;
-                if (sees) bias = i < 0 ? w[k] : __ldcg(row.near + ti.depth[i]);
-                e[h] = sees ? fmaf(e[h], row.c, bias) : -INFINITY;
+                const int k = 2 * y + h, i = j0 + k0 + k - len;
+                // Loads of keys out of sight stay in range and are not used.
+                const int back = min(ti.depth[min(max(i, 0), kTreeMax - 1)], depth);
+                const float bias = i < 0 ? w[k] : near[-back];
+                const float v = fmaf(__uint_as_float(sv[k]), cs, bias);
+                e[h] = vis >> k & 1 ? v : -INFINITY;
               }
               z[y] = f2_pack(e[0], e[1]);
             }
@@ -581,18 +642,18 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             mq[y] = fmaxf(lo, hi);
           }
 #pragma unroll
-          for (int y = 4; y < 32; ++y) {
+          for (int y = 4; y < kCols / 2; ++y) {
             float lo, hi;
             f2_unpack(z[y], lo, hi);
             mq[y & 3] = fmax3(mq[y & 3], lo, hi);
           }
-          const float m_new = fmaxf(row.m, fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])));
-          resc = m_new > row.m + kRescale;
+          const float m_new = fmaxf(m, fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])));
+          resc = m_new > m + kRescale;
           if (resc) {
-            scale = ex2_approx(row.m - m_new);
-            row.l *= scale;
-            row.le *= scale;
-            row.m = m_new;
+            scale = ex2_approx(m - m_new);
+            l *= scale;
+            le *= scale;
+            m = m_new;
           }
         }
         if (g > 0) {
@@ -602,16 +663,17 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           tc_fence_after();
         }
         if (warp_live) {
-          const uint64_t negm2 = f2_pack(-row.m, -row.m);
+          const uint64_t negm2 = f2_pack(-m, -m);
           float lr[4] = {0.f, 0.f, 0.f, 0.f};
           uint64_t le2[2] = {0ull, 0ull};
+          constexpr int kBatch = kCols / 2 < 16 ? kCols / 2 : 16;
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t pk[PARTS][16];
+          for (int q = 0; q < kCols / 2 / kBatch; ++q) {
+            uint32_t pk[PARTS][kBatch];
 #pragma unroll
-            for (int y = 0; y < 16; ++y) {
+            for (int y = 0; y < kBatch; ++y) {
               float p0, p1;
-              f2_unpack(fadd2(z[16 * q + y], negm2), p0, p1);
+              f2_unpack(fadd2(z[kBatch * q + y], negm2), p0, p1);
               p0 = ex2_approx(p0);
               p1 = ex2_approx(p1);
               le2[y & 1] = fadd2(le2[y & 1], f2_pack(p0, p1));
@@ -628,24 +690,26 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
               }
             }
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part)
-              tmem_st_32x32b_x16(tP + 32 * part + 16 * q, pk[part]);
+            for (int part = 0; part < PARTS; ++part) {
+              if (kBatch == 16)
+                tmem_st_32x32b_x16(tP + 32 * part + 16 * q, pk[part]);
+              else
+                tmem_st_32x32b_x8(tP + 32 * part, pk[part]);
+            }
           }
           float b0, b1;
           f2_unpack(fadd2(le2[0], le2[1]), b0, b1);
-          row.le += b0 + b1;
-          row.l += (lr[0] + lr[1]) + (lr[2] + lr[3]);
+          le += b0 + b1;
+          l += (lr[0] + lr[1]) + (lr[2] + lr[3]);
           if (t > it.t0 && __any_sync(0xffffffffu, resc)) {
-            uint32_t ov[64];
-            tmem_ld_32x32b_x32(tO, ov);
-            tmem_ld_32x32b_x32(tO + 32, ov + 32);
-            tmem_ld_wait();
-            reg_fence32(ov);
-            reg_fence32(ov + 32);
 #pragma unroll
-            for (int y = 0; y < 64; ++y) ov[y] = __float_as_uint(__uint_as_float(ov[y]) * scale);
-            tmem_st_32x32b_x32(tO, ov);
-            tmem_st_32x32b_x32(tO + 32, ov + 32);
+            for (int hb = 0; hb < 2; ++hb) {
+              uint32_t ov[32];
+              tmem_ld_cols<32>(tO + 32 * hb, ov);
+#pragma unroll
+              for (int y = 0; y < 32; ++y) ov[y] = __float_as_uint(__uint_as_float(ov[y]) * scale);
+              tmem_st_32x32b_x32(tO + 32 * hb, ov);
+            }
           }
           tmem_st_wait();
         }
@@ -661,25 +725,83 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       ok = warp_wait(&sm.pv_done, (g - 1) & 1, c.status, ab, kSiteTreeSoftEnd);
       if (!ok) break;
       tc_fence_after();
-      const bool whole = it.t0 == 0 && it.t1 == it.tiles;
-      if (warp_live) {
+      const float norm = PARTS == 1 ? l : le;
+      float M = m, L = norm, LE = le, f[KS];  // joined over the copies
+      f[0] = 1.0f;
+      if (KS > 1) {
+        // The other copies' outputs, maxima and sums go through the buffer of
+        // Q, which the item's products no longer read.
+        if (copy > 0) {
+          if (warp_live) {
+            const int mr = (copy - 1) * kRows + 32 * rg + lane;
+            sm.merge_ml[mr] = make_float4(m, norm, le, 0.0f);
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb) {
+              uint32_t ov[32];
+              tmem_ld_cols<32>(tO + 32 * hb, ov);
+#pragma unroll
+              for (int y = 0; y < 8; ++y)
+                *reinterpret_cast<uint4*>(merge + mr * kMergeStride + 32 * hb + 4 * y) =
+                    make_uint4(ov[4 * y], ov[4 * y + 1], ov[4 * y + 2], ov[4 * y + 3]);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.merge_full);
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.merge_full);
+          ok = warp_wait(&sm.merge_full, item & 1, c.status, ab, kSiteTreeMerge);
+          if (!ok) break;
+          float4 ml[KS];
+#pragma unroll
+          for (int y = 1; y < KS; ++y) {
+            ml[y] = sm.merge_ml[(y - 1) * kRows + 32 * rg + lane];
+            M = fmaxf(M, ml[y].x);
+          }
+          f[0] = ex2_approx(m - M);
+          L *= f[0];
+          LE *= f[0];
+#pragma unroll
+          for (int y = 1; y < KS; ++y) {
+            f[y] = ex2_approx(ml[y].x - M);
+            L += ml[y].y * f[y];
+            LE += ml[y].z * f[y];
+          }
+        }
+      }
+      if (copy == 0 && warp_live) {
+        const bool whole = it.t0 == 0 && it.t1 == it.tiles;
         const uint32_t* odd = sm.odd[item & 1];
         const bool any_odd = (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
-        const float norm = PARTS == 1 ? row.l : row.le;
-        const size_t prow = static_cast<size_t>(2 * cta + (it.t0 == 0 ? 1 : 0)) * a.rows + threadIdx.x;
+        const size_t prow =
+            static_cast<size_t>(2 * cta + (it.t0 == 0 ? 1 : 0)) * kRows + 32 * rg + lane;
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb) {
           uint32_t ov[32];
-          tmem_ld_32x32b_x32(tO + 32 * hb, ov);
-          tmem_ld_wait();
-          reg_fence32(ov);
+          tmem_ld_cols<32>(tO + 32 * hb, ov);
           float* o = reinterpret_cast<float*>(ov);
           if (!live) continue;
+          if (KS > 1) {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] *= f[0];
+#pragma unroll
+            for (int cp = 1; cp < KS; ++cp) {
+              const float4* src = reinterpret_cast<const float4*>(
+                  merge + ((cp - 1) * kRows + 32 * rg + lane) * kMergeStride + 32 * hb);
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
+                const float4 v = src[y];
+                o[4 * y] = fmaf(v.x, f[cp], o[4 * y]);
+                o[4 * y + 1] = fmaf(v.y, f[cp], o[4 * y + 1]);
+                o[4 * y + 2] = fmaf(v.z, f[cp], o[4 * y + 2]);
+                o[4 * y + 3] = fmaf(v.w, f[cp], o[4 * y + 3]);
+              }
+            }
+          }
           if (any_odd) {
             // Values that are not finite, for the nodes that see them.
             for (int i = 0; i < n; ++i) {
-              if (!(odd[i >> 5] >> (i & 31) & 1) || !(ti.seen[row.node][i >> 5] >> (i & 31) & 1))
-                continue;
+              if (!(odd[i >> 5] >> (i & 31) & 1) || !(ti.seen[node][i >> 5] >> (i & 31) & 1)) continue;
               const int slot = len + i;
               int pg = __ldg(c.block_table + static_cast<size_t>(it.b) * c.max_blocks + slot / c.page);
               if (pg < 0 || pg >= c.num_pages) pg = 0;
@@ -701,7 +823,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             for (int y = 0; y < 8; ++y)
               dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
           } else {
-            const float inv = 1.0f / norm;
+            const float inv = 1.0f / L;
             if (PARTS > 1) {
               float4* dst =
                   reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kHeadDim + 32 * hb);
@@ -725,10 +847,16 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         }
         if (live) {
           if (!whole)
-            a.part_ml[prow] = make_float4(row.m, norm, row.le, 0.0f);
+            a.part_ml[prow] = make_float4(M, L, LE, 0.0f);
           else if (a.lse)
-            a.lse[orow] = (row.m + log2f(row.le)) * kLn2f;
+            a.lse[orow] = (M + log2f(LE)) * kLn2f;
         }
+      }
+      if (KS > 1) {
+        // The next item's queries may overwrite the parts.
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.merge_free);
+        ok = warp_wait(&sm.merge_free, item & 1, c.status, ab, kSiteTreeMerge);
       }
       // O has been read before the next item's products overwrite it: they
       // wait for its p_full, on which every warp arrives after this.
@@ -813,20 +941,35 @@ constexpr size_t kSmemTwo = 113 * 1024;  // a CTA's share when two fit an SM
 constexpr size_t kSmemOne = 227 * 1024;
 
 // Shared memory of a CTA besides its ring stages, and of one stage.
-constexpr size_t kSmemFixed = 1024 + kQBytes + sizeof(TreeSmem);
+size_t smem_fixed(const TreeArgs& a) {
+  return 1024 + q_bytes(kRowsMax / a.rows) + sizeof(TreeSmem);
+}
 size_t smem_stage(const TreeArgs& a) {
   return 2 * kKvBytes + static_cast<size_t>(a.win_stage) * 4;
+}
+
+template <int PARTS, int KS>
+cudaError_t launch_copies(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a,
+                          cudaStream_t st) {
+  static bool limit_set[64] = {};
+  auto kernel = bam_tree_kernel<PARTS, KS>;
+  const cudaError_t e = smem_limit_once(kernel, kSmemOne, limit_set);
+  if (e != cudaSuccess) return e;
+  return launch_k(kernel, dim3(a.ctas), dim3(kTreeThreads), smem_fixed(a) + a.stages * smem_stage(a),
+                  st, true, tk, tv, a);
 }
 
 template <int PARTS>
 cudaError_t launch_parts(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a,
                          cudaStream_t st) {
-  static bool limit_set[64] = {};
-  auto kernel = bam_tree_kernel<PARTS>;
-  const cudaError_t e = smem_limit_once(kernel, kSmemOne, limit_set);
-  if (e != cudaSuccess) return e;
-  return launch_k(kernel, dim3(a.ctas), dim3(a.rows + 64), kSmemFixed + a.stages * smem_stage(a),
-                  st, true, tk, tv, a);
+  switch (a.rows) {
+    case 32:
+      return launch_copies<PARTS, 4>(tk, tv, a, st);
+    case 64:
+      return launch_copies<PARTS, 2>(tk, tv, a, st);
+    default:
+      return launch_copies<PARTS, 1>(tk, tv, a, st);
+  }
 }
 
 }  // namespace
@@ -841,7 +984,7 @@ bool tree_config(TreeArgs* a, int sms) {
     if (heads > a->group) heads = a->group;
     if (heads * window_floats(n) > a->win_stage) a->win_stage = heads * window_floats(n);
   }
-  const size_t fixed = kSmemFixed, stage = smem_stage(*a);
+  const size_t fixed = smem_fixed(*a), stage = smem_stage(*a);
   int per_sm = 2;
   size_t budget = kSmemTwo;
   if (fixed + 3 * stage > budget) {

@@ -68,14 +68,14 @@ struct TreeArgs {
   float eps;
   int H, group, prior, ssmax, o_fp32;
   int tab_len, tab_zero;
-  int rows;           // rows of an item, at most: 32, 64, 96 or 128
+  int rows;           // rows of an item, at most: 32, 64 or 128
   int ctas, least;    // CTAs of the launch; tiles that one gets at least
   int stages;         // ring stages
   int win_stage;      // floats of a stage's table windows
 };
 
 // Rows of an item for `rows` (head, node) pairs.
-inline int tree_rows(int64_t rows) { return rows >= 128 ? 128 : static_cast<int>((rows + 31) / 32 * 32); }
+inline int tree_rows(int64_t rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 // Table row: distances 0 .. Tmax at entries Tmax .. 0 and, behind entry
 // Tmax, room for windows that reach past the last key.
 inline int tree_table_zero(int Tmax) { return (Tmax + 63) / 64 * 64; }
