@@ -178,7 +178,7 @@ TreeWs tree_ws(int B, int H, int Hkv, int N, int Tmax) {
   w.plan = kStatusBytes;
   w.table = w.plan + align256((static_cast<size_t>(B) + 1) * 8);
   w.ml = w.table + align256(static_cast<size_t>(H) * tree_table_len(Tmax) * 4);
-  w.part = w.ml + align256(2 * kTreeCtas * static_cast<size_t>(w.rows) * 16);
+  w.part = w.ml + align256(2 * kTreeCtas * static_cast<size_t>(w.rows) * 8);
   w.total = w.part + align256(2 * kTreeCtas * static_cast<size_t>(w.rows) * kHeadDim * 4);
   return w;
 }
@@ -526,8 +526,8 @@ bam_status bam_attn_decode_tree_paged(const void* q, const void* k_pages, const 
   if ((s = check_ws(ws, ws_bytes, w.total)) != BAM_OK) return s;
   // Pages as rows of 64 dimensions, in boxes of one tile of 64 keys.
   CUtensorMap tk, tv;
-  if (!encode_rows(&tk, k_pages, num_pages * Hkv, page, kTreeTile) ||
-      !encode_rows(&tv, v_pages, num_pages * Hkv, page, kTreeTile))
+  if (!encode_rows(&tk, k_pages, num_pages * Hkv, page, 64) ||
+      !encode_rows(&tv, v_pages, num_pages * Hkv, page, 64))
     return BAM_ERR_CUDA;
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   TreeArgs a = {};
@@ -543,7 +543,7 @@ bam_status bam_attn_decode_tree_paged(const void* q, const void* k_pages, const 
   a.lse = lse;
   a.plan = reinterpret_cast<int64_t*>(wsb + w.plan);
   a.table = reinterpret_cast<float*>(wsb + w.table);
-  a.part_ml = reinterpret_cast<float4*>(wsb + w.ml);
+  a.part_ml = reinterpret_cast<float2*>(wsb + w.ml);
   a.part = reinterpret_cast<float*>(wsb + w.part);
   a.eps = p->eps;
   a.H = H;

@@ -23,54 +23,74 @@ namespace {
 constexpr int kSoftWarps = 4;
 constexpr int kTreeThreads = 32 * (kSoftWarps + 2);  // and the producer and the MMA issuer
 constexpr int kRowsMax = 128;      // rows of an item: lanes of Tensor Memory
-constexpr int kKvBytes = kTreeTile * kHeadDim * 2;  // 8 KB of K (and of V) a tile
+constexpr int kBox = 64;                             // keys of a TMA box: pages are multiples of it
+constexpr int kBoxBytes = kBox * kHeadDim * 2;
 constexpr int kQBytes = kRowsMax * kHeadDim * 2;
-constexpr int kMergeStride = 68;  // floats of a merge row: 16-byte reads of 32 rows spread over the banks
-constexpr int kNear = 32 + 2 * kTreeMax;  // a warp's table entries of the draft's distances
+constexpr int kNear = kRowsMax + 2 * kTreeMax;  // an item's table entries of the draft's distances
 constexpr int kMaxStages = 8;
 constexpr float kRescale = 8.0f;  // log2 units by which a weight may exceed 1
 constexpr float kNoMax = -3.4e38f;  // below every logit (the table is clamped at -3e38)
 
-// Tensor Memory columns of a CTA (256): S, the parts of P, O.
-constexpr uint32_t kTmemCols = 256, kColP = 64, kColO = 192;
+// Tensor Memory columns of a CTA: S, P, O.
+constexpr uint32_t kTmemCols = 256, kColO = 192;
 
 enum : int {
   kSiteTreeProducer = 60,
-  kSiteTreeTable = 61,
-  kSiteTreeMmaQ = 62,
-  kSiteTreeMmaS = 63,
-  kSiteTreeMmaK = 64,
-  kSiteTreeMmaP = 65,
-  kSiteTreeSoftS = 66,
-  kSiteTreeSoftK = 67,
-  kSiteTreeSoftPV = 68,
-  kSiteTreeSoftEnd = 69,
-  kSiteTreeMerge = 70
+  kSiteTreeItem = 61,
+  kSiteTreeTable = 62,
+  kSiteTreeMmaItem = 63,
+  kSiteTreeMmaS = 64,
+  kSiteTreeMmaK = 65,
+  kSiteTreeMmaP = 66,
+  kSiteTreeSoftItem = 67,
+  kSiteTreeSoftS = 68,
+  kSiteTreeSoftK = 69,
+  kSiteTreeSoftPV = 70,
+  kSiteTreeSoftEnd = 71,
+  kSiteTreeMerge = 72
 };
 
-// Depths and ancestors of a sequence's nodes; every softmax warp has its own,
-// so that the warps need no barrier among themselves.
+// One CTA's share of an item: rows r0 .. r1 - 1 of sequence b and key head
+// hk against tiles t0 .. t1 - 1 of its len + n keys.
+struct Item {
+  int b, hk, r0, r1;
+  int len, n;
+  int t0, t1, tiles;  // t1 == 0: no more items
+  int tree;           // which of the two TreeInfo buffers
+};
+
+// Depths and ancestors of a sequence's nodes.
 struct TreeInfo {
   uint32_t seen[kTreeMax][kTreeMax / 32];  // a node's ancestors, and itself
-  int jump[kTreeMax];
   int depth[kTreeMax];
-  float near[kNear];  // [head of the warp's rows][distance < n]
+};
+
+// What the producer prepares of an item besides its queries.
+struct ItemInfo {
+  Item it;
+  int row[kRowsMax];     // of each row: head within the item * kTreeMax + node; -1: no row
+  float scale[kRowsMax]; // logit scale, log2 units
+  float near[kNear];     // [head of the item's][distance < n]
 };
 
 struct __align__(16) TreeSmem {
-  TreeInfo info[kSoftWarps];
-  float4 merge_ml[kRowsMax];
-  uint64_t full[kMaxStages];   // K, V and table windows of a stage have arrived
-  uint64_t empty[kMaxStages];  // its P V is done
-  uint64_t q_full;             // the item's queries are in shared memory
-  uint64_t s_full, s_free;     // S is complete; S is in registers
+  TreeInfo tree[2];
+  ItemInfo info[2];
+  int jump[kTreeMax];  // scratch of tree_info
+  float2 merge_ml[kRowsMax];
+  uint64_t k_full[kMaxStages];   // a slot's K and table windows have arrived
+  uint64_t v_full[kMaxStages];   // its V has
+  uint64_t s_free[kMaxStages];   // its S and its windows are in registers
+  uint64_t v_empty[kMaxStages];  // its P V is done
+  uint64_t item_full[2];       // an item's queries and info are in shared memory
+  uint64_t item_empty[2];      // the softmax warps are done with them
+  uint64_t s_full;             // S is complete
   uint64_t p_full, pv_done;    // P is in Tensor Memory; P V is done
-  uint64_t merge_full, merge_free;  // the item's parts are in shared memory; are read
+  uint64_t merge_full, merge_free;  // half the item's parts are in shared memory; are read
   uint64_t mma_final;
   uint32_t odd[2][kTreeMax / 32];  // nodes whose value is not finite, by item parity
   uint32_t tmem_base;
   int abort_flag;
-  int find;
 };
 
 // ---------------------------------------------------------------- plan and table
@@ -97,7 +117,7 @@ __global__ void __launch_bounds__(256) bam_tree_prep_kernel(const TreeArgs a) {
         ok &= cache_lengths(c, b0 + tid, &len, &n);
         if (n > 0)
           x = static_cast<int64_t>(c.Hkv) * ((a.group * n + a.rows - 1) / a.rows) *
-              ((len + n + kTreeTile - 1) / kTreeTile);
+              ((len + n + a.tile - 1) / a.tile + kItemCost);
       }
       sum[tid] = x;
       __syncthreads();
@@ -137,7 +157,7 @@ __global__ void __launch_bounds__(256) bam_tree_prep_kernel(const TreeArgs a) {
 
 // ---------------------------------------------------------------- walking the plan
 
-// CTAs that take part: each gets at least `least` tiles.
+// CTAs that take part: each gets at least `least` units.
 __device__ __forceinline__ int active_ctas(int64_t all, int ctas, int least) {
   const int64_t n = (all + least - 1) / least;
   return n < 1 ? 1 : n < ctas ? static_cast<int>(n) : ctas;
@@ -145,40 +165,15 @@ __device__ __forceinline__ int active_ctas(int64_t all, int ctas, int least) {
 __device__ __forceinline__ int64_t range_beg(int64_t all, int active, int cta) {
   return all * cta / active;
 }
-// The CTA whose range holds tile x.
+// The CTA whose range holds unit x.
 __device__ __forceinline__ int range_owner(int64_t all, int active, int64_t x) {
   return static_cast<int>(((x + 1) * active - 1) / all);
-}
-
-struct Item {
-  int b, hk, rb;
-  int len, n, tiles;
-  int t0, t1;      // tiles of this CTA
-  int64_t first;   // global index of the item's tile 0
-};
-
-// The item that tile x belongs to; `b` is a sequence at or before it.
-__device__ __forceinline__ Item item_at(const TreeArgs& a, int b, int64_t x, int64_t end) {
-  while (__ldcg(a.plan + b + 1) <= x) ++b;
-  Item it;
-  it.b = b;
-  cache_lengths(a.c, b, &it.len, &it.n);
-  it.tiles = (it.len + it.n + kTreeTile - 1) / kTreeTile;
-  const int nrb = (a.group * it.n + a.rows - 1) / a.rows;
-  const int64_t local = x - __ldcg(a.plan + b);
-  const int idx = static_cast<int>(local / it.tiles);
-  it.hk = idx / nrb;
-  it.rb = idx - it.hk * nrb;
-  it.t0 = static_cast<int>(local - static_cast<int64_t>(idx) * it.tiles);
-  it.first = x - it.t0;
-  it.t1 = static_cast<int>(min(static_cast<int64_t>(it.tiles), it.t0 + (end - x)));
-  return it;
 }
 
 // Depth and ancestors of the n nodes of sequence b, by one warp (four nodes a
 // lane).  Each round doubles the chains that the jump pointers span.  Returns
 // false in a lane that met a parent outside [-1, i).
-__device__ __forceinline__ bool tree_info(const CacheArgs& c, int b, int n, TreeInfo& ti) {
+__device__ __noinline__ bool tree_info(const CacheArgs& c, int b, int n, TreeInfo& ti, int* jump) {
   constexpr int kPer = kTreeMax / 32;
   const int lane = threadIdx.x & 31;
   bool ok = true, more = false;
@@ -201,7 +196,7 @@ __device__ __forceinline__ bool tree_info(const CacheArgs& c, int b, int n, Tree
       d = p >= 0;
     }
     more |= p >= 0;
-    ti.jump[i] = p;
+    jump[i] = p;
     ti.depth[i] = d;
     *reinterpret_cast<uint4*>(ti.seen[i]) = make_uint4(w[0], w[1], w[2], w[3]);
   }
@@ -211,12 +206,12 @@ __device__ __forceinline__ bool tree_info(const CacheArgs& c, int b, int n, Tree
     uint4 v[kPer];
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
-      const int j = ti.jump[32 * x + lane];
+      const int j = jump[32 * x + lane];
       p[x] = -1;
       dp[x] = 0;
       v[x] = make_uint4(0, 0, 0, 0);
       if (j >= 0) {
-        p[x] = ti.jump[j];
+        p[x] = jump[j];
         dp[x] = ti.depth[j];
         v[x] = *reinterpret_cast<const uint4*>(ti.seen[j]);
       }
@@ -229,7 +224,7 @@ __device__ __forceinline__ bool tree_info(const CacheArgs& c, int b, int n, Tree
       uint4* w = reinterpret_cast<uint4*>(ti.seen[i]);
       *w = make_uint4(w->x | v[x].x, w->y | v[x].y, w->z | v[x].z, w->w | v[x].w);
       ti.depth[i] += dp[x];
-      ti.jump[i] = p[x];
+      jump[i] = p[x];
       more |= p[x] >= 0;
     }
     __syncwarp();
@@ -239,18 +234,11 @@ __device__ __forceinline__ bool tree_info(const CacheArgs& c, int b, int n, Tree
 
 __device__ __forceinline__ bool odd_exp(uint32_t half) { return (half & 0x7F80u) == 0x7F80u; }
 
-// Floats of one head's table window for a tile and n nodes: 64 keys against
+// Floats of one head's table window for a tile and n nodes: its keys against
 // n positions at most, from a 16-byte boundary.
-__host__ __device__ __forceinline__ int window_floats(int n) {
-  return (3 + kTreeTile + n - 1 + 3) & ~3;
+__host__ __device__ __forceinline__ int window_floats(int tile, int n) {
+  return (3 + tile + n - 1 + 3) & ~3;
 }
-
-// Bytes of the query buffer, which also holds the copies' outputs at an
-// item's end (24.5 KB for three copies of 32 rows, 17 KB for one of 64).
-__host__ __device__ constexpr int q_bytes(int ks) {
-  return ks == 1 ? kQBytes : ((kRowsMax - kRowsMax / ks) * kMergeStride * 4 + 1023) / 1024 * 1024;
-}
-static_assert(q_bytes(2) >= kQBytes && q_bytes(4) >= kQBytes, "queries");
 
 // N columns (16, 32 or 64) of this warp's lanes of Tensor Memory.
 template <int N>
@@ -292,215 +280,439 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, DevSta
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, st, ab, site));
 }
 
-// Visibility of the 64 keys of a tile that starts at j0 to a node: committed
-// keys, then the bits of its ancestors.
+// Visibility of the 64 keys from j0 on to a node: committed keys, then the
+// bits of its ancestors.
 __device__ __forceinline__ uint64_t tile_mask(const uint32_t* seen, int j0, int len) {
   const uint64_t lo = static_cast<uint64_t>(seen[1]) << 32 | seen[0];
   const uint64_t hi = static_cast<uint64_t>(seen[3]) << 32 | seen[2];
   const int i = j0 - len;  // node of the tile's first key
   if (i <= 0) {
-    const int k = -i;  // 0 .. 63 committed keys in the tile
-    return k ? (lo << k) | ((1ull << k) - 1) : lo;
+    const int k = -i;  // committed keys among them
+    return k >= 64 ? ~0ull : k ? (lo << k) | ((1ull << k) - 1) : lo;
   }
   if (i >= 128) return 0;
   if (i >= 64) return hi >> (i - 64);
   return lo >> i | hi << (64 - i);
 }
 
+// 16 bytes global -> shared, or zeros, asynchronously.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// True when phase `parity` is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // One CTA walks its run of tiles; two CTAs share an SM, so that one's
-// hand-offs are covered by the other's work.  Roles: four softmax warps, a
-// producer warp (TMA loads of K and V, bulk copies of the table windows of
-// the item's heads, into a ring), and a thread that issues the products:
-//   S = Q K^T   128 x 64 x 64, Q and K from shared memory (K-major),
-//   O += P V    128 x 64 x 64, P from Tensor Memory, V from shared memory.
-// All 128 lanes are computed whatever the number of rows: at 64 keys a tile
-// the two products take 256 cycles of an SM's tensor core, its share of HBM
-// delivers the tile's 16 KB in about 700.  The next tile's S runs while the
-// softmax works on this tile's.
+// hand-offs are covered by the other's work.  Roles:
+//   producer warp   walks the plan; prepares each item one ahead (queries,
+//                   the tree's ancestors, the rows' scales) in one of two
+//                   buffers, and loads K and V (TMA) and the table windows of
+//                   the item's heads (bulk copies) into a ring of tiles;
+//   MMA thread      S = Q K^T  (128 x 64 x 64, Q and K from shared memory),
+//                   O += P V   (128 x 64 x 64, P from Tensor Memory);
+//   softmax warps   four, a thread per lane of Tensor Memory.
+// All 128 lanes are computed whatever the number of rows: the two products of
+// 64 keys take 256 cycles of an SM's tensor core, its share of HBM delivers
+// their 16 KB in about 700.  S runs a tile ahead of the softmax.
 //
 // KS (1, 2, 4): an item of at most 128 / KS rows fills Tensor Memory KS times
-// over, and each copy of a row works on its own 64 / KS keys of every tile,
-// with its own maximum, sum and output, which are joined at the item's end.
-// The products cost the same (a step of P V adds to the lanes of its keys'
-// copy only), and the softmax, a thread per row and copy, takes a KS-th of
-// the time.  The softmax needs no exchange between threads; O is rescaled
-// only when a row's maximum grows by more than 8.
+// over, and each copy of a row works on its own KS-th of the keys of every
+// tile, with its own maximum, sum and output, which are joined at the item's
+// end.  The products cost the same (a step of P V adds to the lanes of its
+// keys' copy only), and the softmax takes a KS-th of the time.  With copies a
+// tile is 128 keys: a tile's hand-offs (about 1500 cycles) then weigh half.
+// The softmax needs no exchange between threads; O is rescaled only when a
+// row's maximum grows by more than 8.
 //
-// PARTS: bf16 parts of a weight in the product with V.  With one, the sum
-// that normalises is that of the rounded weights, so that the rounding of a
-// weight that dominates its row cancels; three carry 24 bits.
+// PARTS: bf16 parts of a weight in the product with V.  One rounds a weight by
+// at most 2^-8, which moves an output by as much as its own rounding to bf16
+// does; three carry 24 bits, for fp32 output.  Sums are of the exact weights.
 template <int PARTS, int KS>
 __global__ void __launch_bounds__(kTreeThreads, 2)
     bam_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                     const TreeArgs a) {
-  constexpr int nw = kSoftWarps;
-  constexpr int kRows = kRowsMax / KS;   // rows of an item
-  constexpr int kGroups = kRows / 32;    // warps of a copy
-  constexpr int kCols = kTreeTile / KS;  // keys of a tile for one copy
+  constexpr int kRows = kRowsMax / KS;     // rows of an item
+  constexpr int kGroups = kRows / 32;      // warps of a copy
+  constexpr int kTile = KS == 1 ? 64 : 128;  // keys of a tile
+  constexpr int kCols = kTile / KS;        // of which one copy's
+  constexpr int kTileBytes = kTile * kHeadDim * 2;
+  constexpr int kPCols = kTile / 2;        // columns of a part of P
+  // Where S and the parts of P do not fit side by side, P takes the place of
+  // S, and the next S waits for P V.
+  constexpr bool kOverlay = kTile + kPCols * PARTS > kColO;
+  constexpr uint32_t kColP = kOverlay ? 0 : kTile;
+  static_assert(kColP + kPCols * PARTS <= kColO, "Tensor Memory");
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  uint8_t* const sq = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
-  float* const merge = reinterpret_cast<float*>(sq);  // [KS - 1][kRows][kMergeStride], after Q's use
-  uint8_t* const kv = sq + q_bytes(KS);  // [stages][K, V]
-  float* const win = reinterpret_cast<float*>(kv + a.stages * 2 * kKvBytes);
+  uint8_t* const sq = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // two query tiles
+  uint8_t* const sk = sq + 2 * kQBytes;  // [stages] tiles of K, then of V
+  uint8_t* const sv_ring = sk + a.stages * kTileBytes;
+  float* const win = reinterpret_cast<float*>(sv_ring + a.stages * kTileBytes);
   TreeSmem& sm = *reinterpret_cast<TreeSmem*>(win + a.stages * a.win_stage);
   const CacheArgs& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kProducer = kSoftWarps, kMma = kSoftWarps + 1;
   volatile int* ab = &sm.abort_flag;
 
   if (threadIdx.x == 0) {
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.k_full[s], 1);
+      mbar_init(&sm.v_full[s], 1);
+      mbar_init(&sm.s_free[s], kSoftWarps);
+      mbar_init(&sm.v_empty[s], 1);
     }
-    mbar_init(&sm.q_full, nw);
     mbar_init(&sm.s_full, 1);
-    mbar_init(&sm.s_free, nw);
-    mbar_init(&sm.p_full, nw);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sm.item_full[x], 1);
+      mbar_init(&sm.item_empty[x], kSoftWarps);
+    }
+    mbar_init(&sm.p_full, kSoftWarps);
     mbar_init(&sm.pv_done, 1);
-    mbar_init(&sm.merge_full, nw);
-    mbar_init(&sm.merge_free, nw);
+    mbar_init(&sm.merge_full, kSoftWarps);
+    mbar_init(&sm.merge_free, kSoftWarps);
     mbar_init(&sm.mma_final, 1);
     fence_barrier_init();
-    sm.find = 0;
+    sm.abort_flag = 0;
   }
-  if (warp == nw + 1) {
+  if (warp == kMma) {
     tmem_alloc(&sm.tmem_base, kTmemCols);
     tmem_relinquish();
-  }
-  grid_dep_wait();  // plan and table
-  grid_dep_trigger();
-  if (threadIdx.x == 0) sm.abort_flag = *reinterpret_cast<volatile int*>(&c.status->abort);
-  const int64_t all = __ldcg(a.plan + c.B);
-  const int active = active_ctas(all, a.ctas, a.least);
-  const int cta = blockIdx.x;
-  int64_t beg = 0, end = 0;
-  if (all > 0 && cta < active) {
-    beg = range_beg(all, active, cta);
-    end = range_beg(all, active, cta + 1);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (beg < end) {
-    int before = 0;
-    for (int b = threadIdx.x; b < c.B; b += blockDim.x) before += __ldcg(a.plan + b + 1) <= beg;
-    if (before) atomicAdd(&sm.find, before);
-  }
-  __syncthreads();
   const uint32_t tm = sm.tmem_base;
-  int b = sm.find;
+  // The plan, the table and the status words come from the previous kernel
+  // (a wait that looks at an abort word before it is cleared would give up).
+  grid_dep_wait();
+  grid_dep_trigger();
 
-  if (warp == nw) {
+  if (warp == kProducer) {
     // ---------------------------------------------------------------- producer
-    bool ok = *ab == 0, bad_page = false;
-    int issued = 0, s = 0, phase = 1;
-    for (int64_t x = beg; ok && x < end;) {
-      const Item it = item_at(a, b, x, end);
-      b = it.b;
-      const int r0 = it.rb * kRows, r1 = min(r0 + kRows, a.group * it.n);
-      const int g0 = r0 / it.n, heads = (r1 - 1) / it.n - g0 + 1;
-      const int y0 = a.tab_zero - (it.len + it.n - 1);  // entry of key 0 for the last position
-      const int nwin = window_floats(it.n);
-      const float* trow = a.table + static_cast<size_t>(it.hk * a.group + g0) * a.tab_len;
-      int pages = 0;
-      for (int t = it.t0; t < it.t1; ++t) {
-        const int ahead = (t - it.t0) & 31;
-        if (ahead == 0 && t + lane < it.t1) {
-          // page numbers of the next 32 tiles, one a lane
-          pages = __ldg(c.block_table + static_cast<size_t>(it.b) * c.max_blocks +
-                        (t + lane) * kTreeTile / c.page);
-          if (pages < 0 || pages >= c.num_pages) {
-            bad_page = true;
-            pages = 0;
-          }
-        }
-        const int pg = __shfl_sync(0xffffffffu, pages, ahead);
-        if (issued >= a.stages) {
-          ok = warp_wait(&sm.empty[s], phase, c.status, ab, kSiteTreeProducer);
-          if (!ok) break;
-        }
-        uint8_t* dst = kv + s * 2 * kKvBytes;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&sm.full[s], 2 * kKvBytes + heads * nwin * 4);
-          const int row = t * kTreeTile % c.page, plane = pg * c.Hkv + it.hk;
-          tma_load_3d(dst, &tk, &sm.full[s], 0, row, plane);
-          tma_load_3d(dst + kKvBytes, &tv, &sm.full[s], 0, row, plane);
-        }
-        __syncwarp();
-        for (int g = lane; g < heads; g += 32) {
-          const float* tr = trow + static_cast<size_t>(g) * a.tab_len;
-          ok &= bulk_load_checked(win + s * a.win_stage + g * nwin, tr + ((y0 + t * kTreeTile) & ~3),
-                                  nwin * 4, &sm.full[s], tr, tr + a.tab_len, c.status, ab,
-                                  kSiteTreeTable);
-        }
-        ++issued;
-        if (++s == a.stages) {
-          s = 0;
-          phase ^= 1;
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-      }
-      x += it.t1 - it.t0;
+    bool ok = *reinterpret_cast<volatile int*>(&c.status->abort) == 0;
+    bool args_ok = true;
+    // 32 sequences a time, one a lane: where they begin and end, their lengths.
+    int b = 0, b0 = 0, len_l = 0, n_l = 0;
+    int64_t beg_l = 0, end_l = 0;
+    auto fetch = [&]() {
+      const int y = min(b0 + lane, c.B - 1);
+      beg_l = __ldcg(a.plan + y);
+      end_l = __ldcg(a.plan + y + 1);
+      cache_lengths(c, y, &len_l, &n_l);
+    };
+    if (c.B <= 32) fetch();
+    const int64_t all = __ldcg(a.plan + c.B);
+    const int active = active_ctas(all, a.ctas, a.least), cta = blockIdx.x;
+    int64_t x = 0, end = 0;
+    if (all > 0 && cta < active) {
+      x = range_beg(all, active, cta);
+      end = range_beg(all, active, cta + 1);
     }
-    // Copies in flight land before the CTA leaves.
-    for (int i = max(0, issued - a.stages); i < issued; ++i)
-      mbar_drain(&sm.full[i % a.stages], (i / a.stages) & 1);
-    if (bad_page) record_bad_arg(c.status);
-  } else if (warp == nw + 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t id_s = idesc_bf16(128, 64, false, false), id_o = idesc_bf16(128, 64, false, true);
-      const uint64_t qd = sdesc_sw128(smem_u32(sq), 16, 1024);
-      const uint64_t kd = sdesc_sw128(smem_u32(kv), 16, 1024);
-      const uint64_t vd = sdesc_sw128(smem_u32(kv + kKvBytes), 16384, 1024);
-      constexpr uint64_t kStageDesc = 2 * kKvBytes >> 4;
-      bool ok = *ab == 0;
-      int g = 0, item = 0;     // tiles and items so far
-      int s = 0, phase = 0;    // ring slot of the tile whose S comes next
-      auto issue_s = [&]() {
-        if (g > 0) ok = ok && mbar_wait(&sm.s_free, (g - 1) & 1, c.status, ab, kSiteTreeMmaS);
-        ok = ok && mbar_wait(&sm.full[s], phase, c.status, ab, kSiteTreeMmaK);
-        if (!ok) return;
-        tc_fence_after();
+    if (c.B > 32 && x < end) {
+      // The sequence that unit x lies in: how many end at or before it.
+      int hi = c.B;
+      while (hi - b > 32) {
+        const int step = (hi - b + 31) / 32, y = min(b + (lane + 1) * step, hi);
+        const int full = __popc(__ballot_sync(0xffffffffu, __ldcg(a.plan + y) <= x));
+        b += full * step;
+        hi = min(hi, b + step);
+      }
+      b += __popc(__ballot_sync(0xffffffffu, b + lane < hi && __ldcg(a.plan + b + lane + 1) <= x));
+      b0 = b;
+      fetch();
+    }
+    int issued = 0, s = 0, phase = 1, k = 0, last_b = -1, tree = 1;
+    for (;; ++k) {
+      ItemInfo& info = sm.info[k & 1];
+      if (!ok) break;
+      Item it;
+      it.t0 = it.t1 = 0;
+      while (x < end) {
+        // The sequence of unit x, at b or behind it.
+        for (;;) {
+          const unsigned ends = __ballot_sync(0xffffffffu, b0 + lane >= b && end_l > x);
+          if (ends) {
+            b = b0 + __ffs(ends) - 1;
+            break;
+          }
+          b = b0 += 32;
+          fetch();
+        }
+        it.b = b;
+        it.len = __shfl_sync(0xffffffffu, len_l, b - b0);
+        it.n = __shfl_sync(0xffffffffu, n_l, b - b0);
+        const int64_t local = x - __shfl_sync(0xffffffffu, beg_l, b - b0);
+        it.tiles = (it.len + it.n + kTile - 1) / kTile;
+        const int unit = it.tiles + kItemCost;
+        const int idx = static_cast<int>(local / unit);
+        const int at = static_cast<int>(local - static_cast<int64_t>(idx) * unit);
+        const int nrb = (a.group * it.n + kRows - 1) / kRows;
+        it.hk = idx / nrb;
+        it.r0 = (idx - it.hk * nrb) * kRows;
+        it.r1 = min(it.r0 + kRows, a.group * it.n);
+        const int stop = static_cast<int>(min(static_cast<int64_t>(unit), at + (end - x)));
+        it.t0 = max(at - kItemCost, 0);
+        it.t1 = max(stop - kItemCost, 0);
+        x += stop - at;
+        if (it.t1 > it.t0) break;
+        it.t1 = 0;  // only the fixed cost of an item whose tiles are another CTA's
+      }
+      const int n = it.n, len = it.len;
+      const int g0 = it.t1 ? it.r0 / n : 0, heads = it.t1 ? (it.r1 - 1) / n - g0 + 1 : 0;
+      const float* trow = a.table + static_cast<size_t>(it.hk * a.group + g0) * a.tab_len;
+      const int y0 = a.tab_zero - (len + n - 1);  // entry of key 0 for the last position
+      const int nwin = window_floats(kTile, n);
+      // Tiles are issued as slots are free; `wait` waits for them.
+      int t = it.t0, pages = 0;
+      auto issue_tiles = [&](bool wait) {
+        for (; t < it.t1; ++t) {
+          if (issued >= a.stages) {
+            if (!wait) {
+              const bool free = mbar_test(&sm.s_free[s], phase) && mbar_test(&sm.v_empty[s], phase);
+              if (!__all_sync(0xffffffffu, free)) return;
+            } else {
+              ok = warp_wait(&sm.s_free[s], phase, c.status, ab, kSiteTreeProducer);
+              if (!ok) return;
+            }
+          }
+          constexpr int kBoxes = kTile / kBox, kAhead = 32 / kBoxes;
+          const int ahead = (t - it.t0) % kAhead;
+          if (ahead == 0) {
+            // page numbers of the boxes of the next tiles, one a lane
+            const int key = t * kTile + lane * kBox;
+            pages = 0;
+            if (key < min(it.t1 * kTile, len + n)) {
+              pages = __ldg(c.block_table + static_cast<size_t>(it.b) * c.max_blocks + key / c.page);
+              if (pages < 0 || pages >= c.num_pages) {
+                args_ok = false;
+                pages = 0;
+              }
+            }
+          }
+          // Boxes that hold no key are not loaded: their rows of S are out of
+          // sight and their rows of V are made zero.
+          const int boxes = min(kBoxes, (len + n - t * kTile + kBox - 1) / kBox);
+          int plane[kBoxes];
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_ss(tm, qd + 2 * kk, kd + kStageDesc * s + 2 * kk, id_s, kk > 0 ? 1u : 0u);
-        umma_commit(&sm.s_full);
-        ++g;
-        if (++s == a.stages) {
-          s = 0;
-          phase ^= 1;
+          for (int x2 = 0; x2 < kBoxes; ++x2)
+            plane[x2] = __shfl_sync(0xffffffffu, pages, ahead * kBoxes + x2) * c.Hkv + it.hk;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.k_full[s], boxes * kBoxBytes + heads * nwin * 4);
+#pragma unroll
+            for (int x2 = 0; x2 < kBoxes; ++x2)
+              if (x2 < boxes)
+                tma_load_3d(sk + s * kTileBytes + x2 * kBoxBytes, &tk, &sm.k_full[s], 0,
+                            (t * kTile + x2 * kBox) % c.page, plane[x2]);
+          }
+          __syncwarp();
+          for (int g = lane; g < heads; g += 32) {
+            const float* tr = trow + static_cast<size_t>(g) * a.tab_len;
+            ok &= bulk_load_checked(win + s * a.win_stage + g * nwin, tr + ((y0 + t * kTile) & ~3),
+                                    nwin * 4, &sm.k_full[s], tr, tr + a.tab_len, c.status, ab,
+                                    kSiteTreeTable);
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok && wait && issued >= a.stages)
+            ok = warp_wait(&sm.v_empty[s], phase, c.status, ab, kSiteTreeProducer);
+          // (after a give-up the slot's V copy is still armed, so that the
+          // copies can be drained alike)
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.v_full[s], ok ? boxes * kBoxBytes : 0);
+#pragma unroll
+            for (int x2 = 0; x2 < kBoxes; ++x2)
+              if (ok && x2 < boxes)
+                tma_load_3d(sv_ring + s * kTileBytes + x2 * kBoxBytes, &tv, &sm.v_full[s], 0,
+                            (t * kTile + x2 * kBox) % c.page, plane[x2]);
+          }
+          __syncwarp();
+          ++issued;
+          if (++s == a.stages) {
+            s = 0;
+            phase ^= 1;
+          }
+          if (!ok) return;
         }
       };
-      for (int64_t x = beg; ok && x < end; ++item) {
-        const Item it = item_at(a, b, x, end);
-        b = it.b;
-        ok = mbar_wait(&sm.q_full, item & 1, c.status, ab, kSiteTreeMmaQ);
-        if (!ok) break;
-        issue_s();
-        for (int t = it.t0; ok && t < it.t1; ++t) {
-          const int sv = (s == 0 ? a.stages : s) - 1, gv = g - 1;  // this tile
-          if (t + 1 < it.t1) issue_s();
-          ok = ok && mbar_wait(&sm.p_full, gv & 1, c.status, ab, kSiteTreeMmaP);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              // 16 keys; they belong to copy kk / (4 / KS).
-              constexpr int kSteps = 4 / KS;
-              umma_ts_lanes<KS>(tm + kColO, tm + kColP + 32 * part + 8 * kk,
-                                vd + kStageDesc * sv + 128 * kk, id_o,
-                                (t > it.t0 || part > 0 || kk % kSteps > 0) ? 1u : 0u, kk / kSteps);
-            }
-          umma_commit(&sm.pv_done);
-          umma_commit(&sm.empty[sv]);
+      issue_tiles(false);
+      if (k >= 2) {
+        ok = ok && warp_wait(&sm.item_empty[k & 1], (k / 2 - 1) & 1, c.status, ab, kSiteTreeItem);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (!ok) break;
+      if (it.t1 == 0) {
+        if (lane == 0) {
+          info.it = it;
+          mbar_arrive(&sm.item_full[k & 1]);
         }
-        x += it.t1 - it.t0;
+        break;
+      }
+      const int nrows = it.r1 - it.r0;
+      // Queries: the item's rows, once for each copy, 16-byte chunks swizzled
+      // as the product reads them; eight lanes a row.
+      {
+        const uint32_t dst = smem_u32(sq + (k & 1) * kQBytes);
+        const uint16_t* base =
+            a.q + (static_cast<size_t>(it.b) * a.H + it.hk * a.group) * c.N * kHeadDim;
+        const int ch = lane & 7, padded = (nrows + 31) & ~31;
+        int hg = (it.r0 + (lane >> 3)) / n, node = it.r0 + (lane >> 3) - hg * n;
+        for (int rr = lane >> 3; rr < padded; rr += 4) {
+          const bool live = rr < nrows;
+          const uint16_t* src = base + (live ? static_cast<size_t>(hg) * c.N + node : 0) * kHeadDim + 8 * ch;
+#pragma unroll
+          for (int cp = 0; cp < KS; ++cp) {
+            const int row = cp * kRows + rr;
+            cp_async16(dst + row * 128 + ((ch ^ (row & 7)) << 4), src, live);
+          }
+          for (node += 4; node >= n; node -= n) ++hg;
+        }
+      }
+      // Some tile holds drafted keys: their distances' table entries.
+      if (it.t1 * kTile > len) {
+        for (int h = 0; h < heads; ++h)
+          for (int y = lane; y < n; y += 32)
+            cp_async4(smem_u32(info.near + h * n + y),
+                      trow + static_cast<size_t>(h) * a.tab_len + a.tab_zero - y);
+      }
+      if (it.b != last_b) {
+        tree ^= 1;
+        args_ok &= tree_info(c, it.b, n, sm.tree[tree], sm.jump);
+        last_b = it.b;
+      }
+      it.tree = tree;
+#pragma unroll
+      for (int rr = lane; rr < kRows; rr += 32) {
+        const int r = it.r0 + rr;
+        const bool live = rr < nrows;
+        const int hg = live ? r / n : g0, node = live ? r - hg * n : 0;
+        float sc = 0.125f * static_cast<float>(kLog2e);
+        if (a.ssmax)
+          sc *= __ldg(a.s + it.hk * a.group + hg) *
+                logf(static_cast<float>(len + sm.tree[tree].depth[node] + 1));
+        info.row[rr] = live ? (hg - g0) * kTreeMax + node : -1;
+        info.scale[rr] = sc;
+      }
+      if (lane == 0) info.it = it;
+      if (lane < kTreeMax / 32) sm.odd[k & 1][lane] = 0;
+      cp_async_wait();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_full[k & 1]);
+      issue_tiles(true);
+      if (!ok) break;
+    }
+    // Copies in flight land before the CTA leaves.
+    cp_async_wait();
+    for (int i = max(0, issued - a.stages); i < issued; ++i) {
+      mbar_drain(&sm.k_full[i % a.stages], (i / a.stages) & 1);
+      mbar_drain(&sm.v_full[i % a.stages], (i / a.stages) & 1);
+    }
+    if (!args_ok) record_bad_arg(c.status);
+  } else if (warp == kMma) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint32_t id_s = idesc_bf16(128, kTile, false, false);
+      const uint32_t id_o = idesc_bf16(128, 64, false, true);
+      const uint64_t qd = sdesc_sw128(smem_u32(sq), 16, 1024);
+      const uint64_t kd = sdesc_sw128(smem_u32(sk), 16, 1024);
+      const uint64_t vd = sdesc_sw128(smem_u32(sv_ring), 16384, 1024);
+      constexpr uint64_t kSlotDesc = kTileBytes >> 4, kQDesc = kQBytes >> 4;
+      // Two places in the same sequence of tiles: S runs ahead of P V.
+      struct Place {
+        int k, left, g, s, phase;  // item, its tiles to come, tile, ring slot and phase
+        bool first;
+      };
+      Place ps{-1, 0, 0, 0, 0, true}, pv{-1, 0, 0, 0, 0, true};
+      bool ok = true;
+      auto advance = [&](Place& p) {
+        --p.left;
+        ++p.g;
+        p.first = false;
+        if (++p.s == a.stages) {
+          p.s = 0;
+          p.phase ^= 1;
+        }
+      };
+      // Puts p on the next tile; false at the end or when a wait gave up.
+      auto enter = [&](Place& p) {
+        if (p.left > 0) return true;
+        ++p.k;
+        p.first = true;
+        ok = ok && mbar_wait(&sm.item_full[p.k & 1], (p.k >> 1) & 1, c.status, ab, kSiteTreeMmaItem);
+        if (!ok) return false;
+        const Item& it = sm.info[p.k & 1].it;
+        p.left = it.t1 - it.t0;
+        return it.t1 > 0;
+      };
+      auto issue_s = [&]() {
+        if (ps.g > 0) {  // the S before it has been read
+          const int q = (ps.s == 0 ? a.stages : ps.s) - 1;
+          ok = ok && mbar_wait(&sm.s_free[q], ps.s == 0 ? ps.phase ^ 1 : ps.phase, c.status, ab,
+                               kSiteTreeMmaS);
+          if (kOverlay)  // and so has the P that took its place
+            ok = ok && mbar_wait(&sm.pv_done, (ps.g - 1) & 1, c.status, ab, kSiteTreeMmaS);
+        }
+        ok = ok && mbar_wait(&sm.k_full[ps.s], ps.phase, c.status, ab, kSiteTreeMmaK);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t q0 = qd + kQDesc * (ps.k & 1), k0 = kd + kSlotDesc * ps.s;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_ss(tm, q0 + 2 * kk, k0 + 2 * kk, id_s, kk > 0 ? 1u : 0u);
+        umma_commit(&sm.s_full);
+        advance(ps);
+      };
+      bool more = enter(ps);  // tiles whose S is to come
+      if (more) issue_s();
+      while (ok && ps.g > pv.g) {
+        // The next tile's S goes first if its item and keys are there (the
+        // softmax reads this tile's S before it writes P).
+        if (!kOverlay && more &&
+            (ps.left > 0 || mbar_test(&sm.item_full[(ps.k + 1) & 1], ((ps.k + 1) >> 1) & 1))) {
+          more = enter(ps);
+          if (more && mbar_test(&sm.k_full[ps.s], ps.phase)) issue_s();
+        }
+        const bool behind = ps.g == pv.g + 1;
+        if (!enter(pv)) break;
+        ok = ok && mbar_wait(&sm.v_full[pv.s], pv.phase, c.status, ab, kSiteTreeMmaK) &&
+             mbar_wait(&sm.p_full, pv.g & 1, c.status, ab, kSiteTreeMmaP);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk) {
+            // 16 keys; they belong to copy kk / kSteps.
+            constexpr int kSteps = kTile / 16 / KS;
+            umma_ts_lanes<KS>(tm + kColO, tm + kColP + kPCols * part + 8 * kk,
+                              vd + kSlotDesc * pv.s + 128 * kk, id_o,
+                              (!pv.first || part > 0 || kk % kSteps > 0) ? 1u : 0u, kk / kSteps);
+          }
+        umma_commit(&sm.pv_done);
+        umma_commit(&sm.v_empty[pv.s]);
+        advance(pv);
+        if (behind && more) {
+          more = enter(ps);
+          if (more) issue_s();
+        }
       }
       umma_commit(&sm.mma_final);
       mbar_drain(&sm.mma_final, 0);
@@ -508,64 +720,34 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   } else {
     // ---------------------------------------------------------------- softmax
     const int rg = warp % kGroups, copy = warp / kGroups;
-    const int k0 = copy * kCols;  // first key of this copy in a tile
+    const int rr = 32 * rg + lane;  // row of the item
+    const int k0 = copy * kCols;    // first key of this copy in a tile
     const uint32_t lanes = tm + tmem_lane_base(warp);
     const uint32_t tS = lanes + k0, tP = lanes + kColP + k0 / 2, tO = lanes + kColO;
-    TreeInfo& ti = sm.info[warp];
-    bool ok = *ab == 0, args_ok = true;
-    int last_b = -1, g = 0, item = 0, s = 0, phase = 0;
-    for (int64_t x = beg; ok && x < end; ++item) {
-      const Item it = item_at(a, b, x, end);
-      b = it.b;
-      if (it.b != last_b) args_ok &= tree_info(c, it.b, it.n, ti);
-      last_b = it.b;
-      const int n = it.n, len = it.len;
-      const int r0 = it.rb * kRows, r1 = min(r0 + kRows, a.group * n);
-      const int rw = r0 + 32 * rg;  // first row of the warp
-      const int g0 = r0 / n, nwin = window_floats(n);
-      const int r = rw + lane;
-      const bool live = r < r1, warp_live = rw < r1;
-      const int hg = (live ? r : warp_live ? rw : r0) / n;
-      const int node = live ? r - hg * n : 0;
-      const int head = it.hk * a.group + hg, depth = ti.depth[node];
-      float m = kNoMax, l = 0.0f, le = 0.0f;  // log2 units; sums of rounded and of exact weights
-      float cs = 0.125f * static_cast<float>(kLog2e);
-      if (a.ssmax) cs *= __ldg(a.s + head) * logf(static_cast<float>(len + depth + 1));
-      const int woff = (hg - g0) * nwin + ((a.tab_zero - (len + n - 1)) & 3) + (n - 1 - depth) + k0;
-      const size_t orow = (static_cast<size_t>(it.b) * a.H + head) * c.N + node;
-      const float* near = ti.near + depth;  // table entry of an ancestor: near[-its depth]
-      if (warp_live) {
-        // This thread's query row, 16-byte chunks swizzled as the product
-        // reads them.  The previous item's last S is done: its warps waited
-        // for it.
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + orow * kHeadDim);
-        uint4 w[8];
-#pragma unroll
-        for (int y = 0; y < 8; ++y) w[y] = live ? __ldg(src + y) : make_uint4(0, 0, 0, 0);
-        if (it.t1 * kTreeTile > len) {
-          // Some tile holds drafted keys: their distances' table entries.
-          const int h0 = rw / n;
-          const int cnt = ((min(rw + 32, r1) - 1) / n - h0 + 1) * n;
-          const float* tab = a.table + static_cast<size_t>(it.hk * a.group + h0) * a.tab_len + a.tab_zero;
-          __syncwarp();
-          for (int y = lane; y < cnt; y += 32)
-            ti.near[y] = __ldcg(tab + static_cast<size_t>(y / n) * a.tab_len - y % n);
-          near += (hg - h0) * n;
-        }
-#pragma unroll
-        for (int y = 0; y < 8; ++y)
-          *reinterpret_cast<uint4*>(sq + threadIdx.x * 128 + ((y ^ (threadIdx.x & 7)) << 4)) = w[y];
-      }
-      if (warp == 0 && lane < kTreeMax / 32) sm.odd[item & 1][lane] = 0;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.q_full);
-
-      for (int t = it.t0; ok && t < it.t1; ++t, ++g) {
-        const int j0 = t * kTreeTile;
-        const bool tail = j0 + kTreeTile > len;  // holds keys that not every row sees
+    bool ok = true;
+    int g = 0, s = 0, phase = 0, merges = 0;
+    for (int k = 0;; ++k) {
+      ok = warp_wait(&sm.item_full[k & 1], (k >> 1) & 1, c.status, ab, kSiteTreeSoftItem);
+      if (!ok) break;
+      const ItemInfo& info = sm.info[k & 1];
+      const int t1 = info.it.t1;
+      if (t1 == 0) break;
+      const TreeInfo& ti = sm.tree[info.it.tree];
+      const int n = info.it.n, len = info.it.len, t0 = info.it.t0;
+      const int row = info.row[rr];
+      const bool live = row >= 0;
+      const int node = live ? row % kTreeMax : 0, hrel = live ? row / kTreeMax : 0;
+      const bool warp_live = info.it.r0 + 32 * rg < info.it.r1;
+      const int depth = ti.depth[node];
+      const float cs = info.scale[rr];
+      const int woff = hrel * window_floats(kTile, n) + ((a.tab_zero - (len + n - 1)) & 3) + (n - 1 - depth) + k0;
+      const float* near = info.near + hrel * n + depth;  // entry of an ancestor: near[-its depth]
+      float m = kNoMax, l = 0.0f;  // log2 units; sum of the weights
+      for (int t = t0; t < t1; ++t, ++g) {
+        const int j0 = t * kTile;
+        const bool tail = j0 + kTile > len;  // holds keys that not every row sees
         ok = warp_wait(&sm.s_full, g & 1, c.status, ab, kSiteTreeSoftS) &&
-             warp_wait(&sm.full[s], phase, c.status, ab, kSiteTreeSoftK);
+             warp_wait(&sm.k_full[s], phase, c.status, ab, kSiteTreeSoftK);
         if (!ok) break;
         tc_fence_after();
         const float* w = win + s * a.win_stage + woff;
@@ -580,18 +762,18 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
               z[y] = ffma2(f2_pack(__uint_as_float(sv[2 * y]), __uint_as_float(sv[2 * y + 1])), c2,
                            f2_pack(w[2 * y], w[2 * y + 1]));
           } else {
-            const uint64_t vis = live ? tile_mask(ti.seen[node], j0, len) >> k0 : 0;
+            const uint64_t vis = live ? tile_mask(ti.seen[node], j0 + k0, len) : 0;
 #pragma unroll
             for (int y = 0; y < kCols / 2; ++y) {
               float e[2];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int k = 2 * y + h, i = j0 + k0 + k - len;
+                const int kk = 2 * y + h, i = j0 + k0 + kk - len;
                 // Loads of keys out of sight stay in range and are not used.
                 const int back = min(ti.depth[min(max(i, 0), kTreeMax - 1)], depth);
-                const float bias = i < 0 ? w[k] : near[-back];
-                const float v = fmaf(__uint_as_float(sv[k]), cs, bias);
-                e[h] = vis >> k & 1 ? v : -INFINITY;
+                const float bias = i < 0 ? w[kk] : near[-back];
+                const float v = fmaf(__uint_as_float(sv[kk]), cs, bias);
+                e[h] = vis >> kk & 1 ? v : -INFINITY;
               }
               z[y] = f2_pack(e[0], e[1]);
             }
@@ -599,19 +781,21 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.s_free);
+        if (lane == 0) mbar_arrive(&sm.s_free[s]);
 
-        if (tail && warp == 0) {
+        if (tail) {
           // Rows of V behind the draft hold anything, and a drafted value that
           // is not finite must not meet the weight 0 of a row that does not
-          // see it: zeros here.  The latter are added to O at the item's end.
-          uint8_t* vt = kv + s * 2 * kKvBytes + kKvBytes;
+          // see it: zeros here, a quarter of the rows by each warp.  The
+          // latter are added to O at the item's end.
+          ok = warp_wait(&sm.v_full[s], phase, c.status, ab, kSiteTreeSoftK);
+          if (!ok) break;
           bool any = false;
 #pragma unroll 4
-          for (int y = 0; y < kKvBytes / 512; ++y) {
-            const int chunk = 32 * y + lane, i = j0 + (chunk >> 3) - len;
+          for (int y = 0; y < kTile / 16; ++y) {
+            const int row = kTile / kSoftWarps * warp + 4 * y + (lane >> 3), i = j0 + row - len;
             if (i < 0) continue;
-            uint4* p = reinterpret_cast<uint4*>(vt + chunk * 16);
+            uint4* p = reinterpret_cast<uint4*>(sv_ring + s * kTileBytes + row * 128 + 16 * (lane & 7));
             uint4 v = *p;
             uint32_t* u = reinterpret_cast<uint32_t*>(&v);
             bool fix = i >= n;
@@ -621,7 +805,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
               if (odd_exp(u[h])) keep &= 0xFFFF0000u;
               if (odd_exp(u[h] >> 16)) keep &= 0x0000FFFFu;
               fix |= keep != 0xFFFFFFFFu;
-              if (i < n && keep != 0xFFFFFFFFu) atomicOr(&sm.odd[item & 1][i >> 5], 1u << (i & 31));
+              if (i < n && keep != 0xFFFFFFFFu) atomicOr(&sm.odd[k & 1][i >> 5], 1u << (i & 31));
               u[h] &= keep;
             }
             if (fix) *p = v;
@@ -652,7 +836,6 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           if (resc) {
             scale = ex2_approx(m - m_new);
             l *= scale;
-            le *= scale;
             m = m_new;
           }
         }
@@ -664,8 +847,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         }
         if (warp_live) {
           const uint64_t negm2 = f2_pack(-m, -m);
-          float lr[4] = {0.f, 0.f, 0.f, 0.f};
-          uint64_t le2[2] = {0ull, 0ull};
+          uint64_t l2[2] = {0ull, 0ull};
           constexpr int kBatch = kCols / 2 < 16 ? kCols / 2 : 16;
 #pragma unroll
           for (int q = 0; q < kCols / 2 / kBatch; ++q) {
@@ -676,14 +858,12 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
               f2_unpack(fadd2(z[kBatch * q + y], negm2), p0, p1);
               p0 = ex2_approx(p0);
               p1 = ex2_approx(p1);
-              le2[y & 1] = fadd2(le2[y & 1], f2_pack(p0, p1));
+              l2[y & 1] = fadd2(l2[y & 1], f2_pack(p0, p1));
 #pragma unroll
               for (int part = 0; part < PARTS; ++part) {
                 const uint32_t u = pack_bf16x2(p0, p1);
                 pk[part][y] = u;
-                if (PARTS == 1) {
-                  add_bf16x2_f32(u, lr[2 * (y & 1)], lr[2 * (y & 1) + 1]);
-                } else {
+                if (part + 1 < PARTS) {
                   p0 -= __uint_as_float(u << 16);
                   p1 -= __uint_as_float(u & 0xFFFF0000u);
                 }
@@ -692,16 +872,15 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 #pragma unroll
             for (int part = 0; part < PARTS; ++part) {
               if (kBatch == 16)
-                tmem_st_32x32b_x16(tP + 32 * part + 16 * q, pk[part]);
+                tmem_st_32x32b_x16(tP + kPCols * part + 16 * q, pk[part]);
               else
-                tmem_st_32x32b_x8(tP + 32 * part, pk[part]);
+                tmem_st_32x32b_x8(tP + kPCols * part, pk[part]);
             }
           }
           float b0, b1;
-          f2_unpack(fadd2(le2[0], le2[1]), b0, b1);
-          le += b0 + b1;
-          l += (lr[0] + lr[1]) + (lr[2] + lr[3]);
-          if (t > it.t0 && __any_sync(0xffffffffu, resc)) {
+          f2_unpack(fadd2(l2[0], l2[1]), b0, b1);
+          l += b0 + b1;
+          if (t > t0 && __any_sync(0xffffffffu, resc)) {
 #pragma unroll
             for (int hb = 0; hb < 2; ++hb) {
               uint32_t ov[32];
@@ -725,72 +904,59 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       ok = warp_wait(&sm.pv_done, (g - 1) & 1, c.status, ab, kSiteTreeSoftEnd);
       if (!ok) break;
       tc_fence_after();
-      const float norm = PARTS == 1 ? l : le;
-      float M = m, L = norm, LE = le, f[KS];  // joined over the copies
+
+      // The item's end: the copies are joined, 32 columns at a time, through
+      // the buffer of its queries, which its products no longer read.
+      const int hk = info.it.hk, bb = info.it.b;
+      const bool whole = t0 == 0 && t1 == info.it.tiles;
+      const size_t orow =
+          (static_cast<size_t>(bb) * a.H + hk * a.group + info.it.r0 / n + hrel) * c.N + node;
+      const size_t prow = static_cast<size_t>(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * kRows + rr;
+      const uint32_t* odd = sm.odd[k & 1];
+      const bool any_odd = (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
+      uint8_t* const merge = sq + (k & 1) * kQBytes;  // [KS - 1][kRows] rows of 128 bytes, swizzled
+      float M = m, L = l, f[KS];
       f[0] = 1.0f;
-      if (KS > 1) {
-        // The other copies' outputs, maxima and sums go through the buffer of
-        // Q, which the item's products no longer read.
-        if (copy > 0) {
-          if (warp_live) {
-            const int mr = (copy - 1) * kRows + 32 * rg + lane;
-            sm.merge_ml[mr] = make_float4(m, norm, le, 0.0f);
 #pragma unroll
-            for (int hb = 0; hb < 2; ++hb) {
-              uint32_t ov[32];
-              tmem_ld_cols<32>(tO + 32 * hb, ov);
+      for (int hb = 0; hb < 2; ++hb) {
+        uint32_t ov[32];
+        float* o = reinterpret_cast<float*>(ov);
+        if (warp_live) tmem_ld_cols<32>(tO + 32 * hb, ov);
+        if (KS > 1) {
+          if (copy > 0 && warp_live) {
+            const int mr = (copy - 1) * kRows + rr;
+            if (hb == 0) sm.merge_ml[mr] = make_float2(m, l);
 #pragma unroll
-              for (int y = 0; y < 8; ++y)
-                *reinterpret_cast<uint4*>(merge + mr * kMergeStride + 32 * hb + 4 * y) =
-                    make_uint4(ov[4 * y], ov[4 * y + 1], ov[4 * y + 2], ov[4 * y + 3]);
-            }
+            for (int y = 0; y < 8; ++y)
+              *reinterpret_cast<uint4*>(merge + mr * 128 + ((y ^ (mr & 7)) << 4)) =
+                  make_uint4(ov[4 * y], ov[4 * y + 1], ov[4 * y + 2], ov[4 * y + 3]);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.merge_full);
-        } else {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.merge_full);
-          ok = warp_wait(&sm.merge_full, item & 1, c.status, ab, kSiteTreeMerge);
+          ok = warp_wait(&sm.merge_full, merges & 1, c.status, ab, kSiteTreeMerge);
           if (!ok) break;
-          float4 ml[KS];
+          if (copy == 0 && live) {
+            if (hb == 0) {
 #pragma unroll
-          for (int y = 1; y < KS; ++y) {
-            ml[y] = sm.merge_ml[(y - 1) * kRows + 32 * rg + lane];
-            M = fmaxf(M, ml[y].x);
-          }
-          f[0] = ex2_approx(m - M);
-          L *= f[0];
-          LE *= f[0];
+              for (int y = 1; y < KS; ++y) M = fmaxf(M, sm.merge_ml[(y - 1) * kRows + rr].x);
+              f[0] = ex2_approx(m - M);
+              L *= f[0];
 #pragma unroll
-          for (int y = 1; y < KS; ++y) {
-            f[y] = ex2_approx(ml[y].x - M);
-            L += ml[y].y * f[y];
-            LE += ml[y].z * f[y];
-          }
-        }
-      }
-      if (copy == 0 && warp_live) {
-        const bool whole = it.t0 == 0 && it.t1 == it.tiles;
-        const uint32_t* odd = sm.odd[item & 1];
-        const bool any_odd = (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
-        const size_t prow =
-            static_cast<size_t>(2 * cta + (it.t0 == 0 ? 1 : 0)) * kRows + 32 * rg + lane;
-#pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {
-          uint32_t ov[32];
-          tmem_ld_cols<32>(tO + 32 * hb, ov);
-          float* o = reinterpret_cast<float*>(ov);
-          if (!live) continue;
-          if (KS > 1) {
+              for (int y = 1; y < KS; ++y) {
+                const float2 ml = sm.merge_ml[(y - 1) * kRows + rr];
+                f[y] = ex2_approx(ml.x - M);
+                L += ml.y * f[y];
+              }
+            }
 #pragma unroll
             for (int y = 0; y < 32; ++y) o[y] *= f[0];
 #pragma unroll
             for (int cp = 1; cp < KS; ++cp) {
-              const float4* src = reinterpret_cast<const float4*>(
-                  merge + ((cp - 1) * kRows + 32 * rg + lane) * kMergeStride + 32 * hb);
+              const int mr = (cp - 1) * kRows + rr;
 #pragma unroll
               for (int y = 0; y < 8; ++y) {
-                const float4 v = src[y];
+                const float4 v =
+                    *reinterpret_cast<const float4*>(merge + mr * 128 + ((y ^ (mr & 7)) << 4));
                 o[4 * y] = fmaf(v.x, f[cp], o[4 * y]);
                 o[4 * y + 1] = fmaf(v.y, f[cp], o[4 * y + 1]);
                 o[4 * y + 2] = fmaf(v.z, f[cp], o[4 * y + 2]);
@@ -798,77 +964,76 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
               }
             }
           }
-          if (any_odd) {
-            // Values that are not finite, for the nodes that see them.
-            for (int i = 0; i < n; ++i) {
-              if (!(odd[i >> 5] >> (i & 31) & 1) || !(ti.seen[node][i >> 5] >> (i & 31) & 1)) continue;
-              const int slot = len + i;
-              int pg = __ldg(c.block_table + static_cast<size_t>(it.b) * c.max_blocks + slot / c.page);
-              if (pg < 0 || pg >= c.num_pages) pg = 0;
-              const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                  a.v_pages +
-                  ((static_cast<size_t>(pg) * c.Hkv + it.hk) * c.page + slot % c.page) * kHeadDim +
-                  32 * hb);
+          __syncwarp();
+          if (hb == 0) {
+            // The second half may overwrite the first.
+            if (lane == 0) mbar_arrive(&sm.merge_free);
+            ok = warp_wait(&sm.merge_free, k & 1, c.status, ab, kSiteTreeMerge);
+            if (!ok) break;
+          }
+          ++merges;
+        }
+        if (copy > 0 || !live) continue;
+        if (any_odd) {
+          // Values that are not finite, for the nodes that see them.
+          for (int i = 0; i < n; ++i) {
+            if (!(odd[i >> 5] >> (i & 31) & 1) || !(ti.seen[node][i >> 5] >> (i & 31) & 1)) continue;
+            const int slot = len + i;
+            int pg = __ldg(c.block_table + static_cast<size_t>(bb) * c.max_blocks + slot / c.page);
+            if (pg < 0 || pg >= c.num_pages) pg = 0;
+            const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                a.v_pages + ((static_cast<size_t>(pg) * c.Hkv + hk) * c.page + slot % c.page) * kHeadDim +
+                32 * hb);
 #pragma unroll
-              for (int y = 0; y < 16; ++y) {
-                const uint32_t u = __ldg(v + y);
-                if (odd_exp(u)) o[2 * y] += __uint_as_float(u << 16);
-                if (odd_exp(u >> 16)) o[2 * y + 1] += __uint_as_float(u & 0xFFFF0000u);
-              }
+            for (int y = 0; y < 16; ++y) {
+              const uint32_t u = __ldg(v + y);
+              if (odd_exp(u)) o[2 * y] += __uint_as_float(u << 16);
+              if (odd_exp(u >> 16)) o[2 * y + 1] += __uint_as_float(u & 0xFFFF0000u);
             }
           }
-          if (!whole) {
-            float4* dst = reinterpret_cast<float4*>(a.part + prow * kHeadDim + 32 * hb);
+        }
+        if (!whole) {
+          float4* dst = reinterpret_cast<float4*>(a.part + prow * kHeadDim + 32 * hb);
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          if (hb == 0) a.part_ml[prow] = make_float2(M, L);
+        } else {
+          const float inv = 1.0f / L;
+          if (PARTS > 1) {
+            float4* dst =
+                reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kHeadDim + 32 * hb);
 #pragma unroll
             for (int y = 0; y < 8; ++y)
-              dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+              dst[y] = make_float4(o[4 * y] * inv, o[4 * y + 1] * inv, o[4 * y + 2] * inv,
+                                   o[4 * y + 3] * inv);
           } else {
-            const float inv = 1.0f / L;
-            if (PARTS > 1) {
-              float4* dst =
-                  reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kHeadDim + 32 * hb);
+            uint4* dst =
+                reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * kHeadDim + 32 * hb);
 #pragma unroll
-              for (int y = 0; y < 8; ++y)
-                dst[y] = make_float4(o[4 * y] * inv, o[4 * y + 1] * inv, o[4 * y + 2] * inv,
-                                     o[4 * y + 3] * inv);
-            } else {
-              uint4* dst =
-                  reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * kHeadDim + 32 * hb);
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                float* e = o + 8 * y;
-                dst[y] = make_uint4(pack_bf16x2(e[0] * inv, e[1] * inv),
-                                    pack_bf16x2(e[2] * inv, e[3] * inv),
-                                    pack_bf16x2(e[4] * inv, e[5] * inv),
-                                    pack_bf16x2(e[6] * inv, e[7] * inv));
-              }
+            for (int y = 0; y < 4; ++y) {
+              float* e = o + 8 * y;
+              dst[y] = make_uint4(pack_bf16x2(e[0] * inv, e[1] * inv),
+                                  pack_bf16x2(e[2] * inv, e[3] * inv),
+                                  pack_bf16x2(e[4] * inv, e[5] * inv),
+                                  pack_bf16x2(e[6] * inv, e[7] * inv));
             }
           }
-        }
-        if (live) {
-          if (!whole)
-            a.part_ml[prow] = make_float4(M, L, LE, 0.0f);
-          else if (a.lse)
-            a.lse[orow] = (M + log2f(LE)) * kLn2f;
+          if (hb == 0 && a.lse) a.lse[orow] = (M + log2f(L)) * kLn2f;
         }
       }
-      if (KS > 1) {
-        // The next item's queries may overwrite the parts.
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.merge_free);
-        ok = warp_wait(&sm.merge_free, item & 1, c.status, ab, kSiteTreeMerge);
-      }
+      if (!ok) break;
       // O has been read before the next item's products overwrite it: they
       // wait for its p_full, on which every warp arrives after this.
       tc_fence_before();
-      x += it.t1 - it.t0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
     }
-    if (!args_ok) record_bad_arg(c.status);
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == nw + 1) {
+  if (warp == kMma) {
     tc_fence_after();
     tmem_dealloc(tm, kTmemCols);
   }
@@ -898,9 +1063,9 @@ __global__ void __launch_bounds__(256) bam_tree_combine_kernel(const TreeArgs a)
     } else {
       const int g = h % a.group, r = g * n + t, rb = r / a.rows;
       const int nrb = (a.group * n + a.rows - 1) / a.rows;
-      const int tiles = (len + n + kTreeTile - 1) / kTreeTile;
-      const int64_t first =
-          __ldcg(a.plan + b) + static_cast<int64_t>(h / a.group * nrb + rb) * tiles;
+      const int tiles = (len + n + a.tile - 1) / a.tile;
+      const int64_t first = __ldcg(a.plan + b) + kItemCost +
+                            static_cast<int64_t>(h / a.group * nrb + rb) * (tiles + kItemCost);
       const int c0 = range_owner(all, active, first);
       const int c1 = range_owner(all, active, first + tiles - 1);
       if (c0 == c1) continue;
@@ -908,7 +1073,7 @@ __global__ void __launch_bounds__(256) bam_tree_combine_kernel(const TreeArgs a)
       auto part_row = [&](int cta) {
         return static_cast<size_t>(2 * cta + (cta == c0 ? 1 : 0)) * a.rows + rr;
       };
-      float M = kNoMax, L = 0.0f, LE = 0.0f;
+      float M = kNoMax, L = 0.0f;
       for (int x = c0 + lane; x <= c1; x += 32) M = fmaxf(M, __ldcg(a.part_ml + part_row(x)).x);
 #pragma unroll
       for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
@@ -916,17 +1081,16 @@ __global__ void __launch_bounds__(256) bam_tree_combine_kernel(const TreeArgs a)
 #pragma unroll 4
       for (int x = c0; x <= c1; ++x) {
         const size_t pr = part_row(x);
-        const float4 ml = __ldcg(a.part_ml + pr);
+        const float2 ml = __ldcg(a.part_ml + pr);
         const float2 y = __ldcg(reinterpret_cast<const float2*>(a.part + pr * kHeadDim) + lane);
         const float f = ex2_approx(ml.x - M);
         L += ml.y * f;
-        LE += ml.z * f;
         v.x += y.x * f;
         v.y += y.y * f;
       }
       v.x /= L;
       v.y /= L;
-      lse = (M + log2f(LE)) * kLn2f;
+      lse = (M + log2f(L)) * kLn2f;
     }
     if (a.o_fp32)
       reinterpret_cast<float2*>(static_cast<float*>(a.o) + row * kHeadDim)[lane] = v;
@@ -942,10 +1106,11 @@ constexpr size_t kSmemOne = 227 * 1024;
 
 // Shared memory of a CTA besides its ring stages, and of one stage.
 size_t smem_fixed(const TreeArgs& a) {
-  return 1024 + q_bytes(kRowsMax / a.rows) + sizeof(TreeSmem);
+  (void)a;
+  return 1024 + 2 * kQBytes + sizeof(TreeSmem);
 }
 size_t smem_stage(const TreeArgs& a) {
-  return 2 * kKvBytes + static_cast<size_t>(a.win_stage) * 4;
+  return 2 * static_cast<size_t>(a.tile) * kHeadDim * 2 + static_cast<size_t>(a.win_stage) * 4;
 }
 
 template <int PARTS, int KS>
@@ -977,24 +1142,26 @@ cudaError_t launch_parts(const CUtensorMap& tk, const CUtensorMap& tv, const Tre
 // Ring and grid of the call, from its sizes.  Returns false when a stage does
 // not fit (more heads share a key head than its windows have room for).
 bool tree_config(TreeArgs* a, int sms) {
+  a->tile = a->rows == kRowsMax ? 64 : 128;
   // Most heads and floats that a stage's windows hold, over the node counts.
   a->win_stage = 0;
   for (int n = 1; n <= a->c.N; ++n) {
     int heads = (a->rows + n - 2) / n + 1;
     if (heads > a->group) heads = a->group;
-    if (heads * window_floats(n) > a->win_stage) a->win_stage = heads * window_floats(n);
+    const int floats = heads * window_floats(a->tile, n);
+    if (floats > a->win_stage) a->win_stage = floats;
   }
   const size_t fixed = smem_fixed(*a), stage = smem_stage(*a);
   int per_sm = 2;
   size_t budget = kSmemTwo;
-  if (fixed + 3 * stage > budget) {
+  if (fixed + 2 * stage > budget) {
     per_sm = 1;
     budget = kSmemOne;
   }
   a->stages = static_cast<int>((budget - fixed) / stage);
   if (a->stages > kMaxStages) a->stages = kMaxStages;
   a->ctas = per_sm * sms < kTreeCtas ? per_sm * sms : kTreeCtas;
-  a->least = 1;
+  a->least = 1 + kItemCost;
   return a->stages >= 2 && a->ctas >= 1;
 }
 

@@ -44,11 +44,12 @@ struct KeepArgs {
 
 // Tree attention: the rows of a (sequence, key head) are its group * n
 // (query head, node) pairs, row r = (head r / n, node r % n), taken `rows` at
-// a time; such an item reads the tiles of 64 keys that hold the sequence's
-// len + n keys.  The plan is the running sum of the sequences' tiles over all
-// their items, and CTA c of `active` takes tiles [W c / active, W (c+1) /
-// active) of the W in all.
-constexpr int kTreeTile = 64;    // keys of a tile
+// a time; such an item reads the tiles of 64 or 128 keys that hold the sequence's
+// len + n keys.  An item counts as its tiles and kItemCost units before them;
+// the plan is the running sum of the sequences' units over all their items,
+// and CTA c of `active` takes units [W c / active, W (c+1) / active) of the W
+// in all.
+constexpr int kItemCost = 1;     // an item's fixed cost, in tiles
 constexpr int kTreeCtas = 304;   // most CTAs (two per SM)
 
 struct TreeArgs {
@@ -61,15 +62,16 @@ struct TreeArgs {
   const float* s;
   void* o;
   float* lse;
-  int64_t* plan;      // [B + 1] first tile of each sequence, and W
+  int64_t* plan;      // [B + 1] first unit of each sequence, and W
   float* table;       // [H, tab_len]: entry y is b_h(tab_zero - y) * log2(e)
   float* part;        // [2 * kTreeCtas, rows, 64] partial outputs
-  float4* part_ml;    // [2 * kTreeCtas, rows]: maximum (log2 units), sum that normalises, exact sum
+  float2* part_ml;    // [2 * kTreeCtas, rows]: maximum (log2 units), sum
   float eps;
   int H, group, prior, ssmax, o_fp32;
   int tab_len, tab_zero;
   int rows;           // rows of an item, at most: 32, 64 or 128
-  int ctas, least;    // CTAs of the launch; tiles that one gets at least
+  int tile;           // keys of a tile: 64 with 128 rows, else 128
+  int ctas, least;    // CTAs of the launch; units that one gets at least
   int stages;         // ring stages
   int win_stage;      // floats of a stage's table windows
 };
@@ -79,7 +81,7 @@ inline int tree_rows(int64_t rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 
 // Table row: distances 0 .. Tmax at entries Tmax .. 0 and, behind entry
 // Tmax, room for windows that reach past the last key.
 inline int tree_table_zero(int Tmax) { return (Tmax + 63) / 64 * 64; }
-inline int tree_table_len(int Tmax) { return tree_table_zero(Tmax) + 64 + kTreeMax + kTreeTile; }
+inline int tree_table_len(int Tmax) { return tree_table_zero(Tmax) + 64 + kTreeMax + 128; }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st);
 cudaError_t launch_keep(const KeepArgs& a, cudaStream_t st);
