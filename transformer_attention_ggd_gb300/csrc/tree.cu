@@ -14,6 +14,8 @@
 // key head) that lies in one CTA is written by it; one that is cut leaves a
 // partial maximum, sum and output per CTA, which the combine kernel joins.
 // Ragged batches and a single long sequence keep every SM busy alike.
+#include <type_traits>
+
 #include "table_eval.cuh"
 #include "tree_common.cuh"
 
@@ -275,9 +277,37 @@ __device__ __forceinline__ void umma_ts_lanes(uint32_t d_tmem, uint32_t a_tmem, 
 
 // ---------------------------------------------------------------- attention
 
+// As mbar_wait, without its call: the slow path of a call would keep the
+// caller's live registers (a row of S, here) in local memory.
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, DevStatus* st,
+                                          volatile int* ab, int site) {
+#ifdef BAM_DEBUG
+  if (*reinterpret_cast<volatile int*>(&st->giveup) > 0 && atomicSub(&st->giveup, 1) == 1) {
+    raise_abort(st, ab, site);
+    return false;
+  }
+#endif
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t it = 1; !mbar_try_wait_sleep(bar, parity, kWaitSleepNs); ++it) {
+    if ((it & 3u) != 0) continue;
+    if (*ab) return false;
+    if (*reinterpret_cast<volatile int*>(&st->abort)) {
+      *ab = 1;
+      return false;
+    }
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      raise_abort(st, ab, site);
+      return false;
+    }
+  }
+  return true;
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, DevStatus* st,
                                           volatile int* ab, int site) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, st, ab, site));
+  return __all_sync(0xffffffffu, tree_wait(bar, parity, st, ab, site));
 }
 
 // Visibility of the 64 keys from j0 on to a node: committed keys, then the
@@ -320,6 +350,462 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Keys of a tile: as many as S and the parts of P leave room for, and no more
+// than 64 columns a thread.
+__host__ __device__ constexpr int tree_tile(int parts, int ks) {
+  return parts == 1 && ks > 1 ? 128 : 64;
+}
+
+// Sizes of a kernel with PARTS parts of a weight and KS copies of a row.
+template <int PARTS, int KS>
+struct Shape {
+  static constexpr int kRows = kRowsMax / KS;        // rows of an item
+  static constexpr int kGroups = kRows / 32;         // warps of a copy
+  static constexpr int kTile = tree_tile(PARTS, KS);  // keys of a tile
+  static constexpr int kCols = kTile / KS;           // of which one copy's
+  static constexpr int kTileBytes = kTile * kHeadDim * 2;
+  static constexpr int kPCols = kTile / 2;           // columns of a part of P
+  static constexpr uint32_t kColP = kTile;
+  static_assert(kColP + kPCols * PARTS <= kColO, "Tensor Memory");
+};
+
+// The CTA's shared memory.
+extern __shared__ __align__(16) uint8_t tree_smem_raw[];
+struct View {
+  uint8_t* sq;  // two query tiles
+  uint8_t* sk;  // [stages] tiles of K
+  uint8_t* sv;  // [stages] tiles of V
+  float* win;   // [stages] table windows
+  TreeSmem* sm;
+};
+template <class S>
+__device__ __forceinline__ View smem_view(const TreeArgs& a) {
+  View v;
+  v.sq = tree_smem_raw + ((0u - smem_u32(tree_smem_raw)) & 1023u);
+  v.sk = v.sq + 2 * kQBytes;
+  v.sv = v.sk + a.stages * S::kTileBytes;
+  v.win = reinterpret_cast<float*>(v.sv + a.stages * S::kTileBytes);
+  v.sm = reinterpret_cast<TreeSmem*>(v.win + a.stages * a.win_stage);
+  return v;
+}
+
+// What a softmax warp carries from tile to tile.
+struct SoftState {
+  int g, s, phase;  // tile of the CTA, its ring slot and phase
+  int t;            // tile of the item
+  float m, l;       // running maximum (log2 units) and sum of the weights
+  bool first;       // the item's first tile
+  bool ok;
+};
+
+// A softmax thread's row of the item in buffer k & 1.
+struct SoftRow {
+  int rr, copy, k0;  // row of the item, copy, the copy's first key in a tile
+  uint32_t lanes;    // the warp's lanes of Tensor Memory
+  bool live, warp_live;
+  int node, hrel, depth;  // hrel: head within the item
+  float cs;          // logit scale, log2 units
+  int woff;          // its place in a table window
+};
+template <class S>
+__device__ __forceinline__ SoftRow soft_row(const TreeArgs& a, const TreeSmem& sm, int k) {
+  const ItemInfo& info = sm.info[k & 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = info.it.n;
+  SoftRow r;
+  r.rr = 32 * (warp % S::kGroups) + lane;
+  r.copy = warp / S::kGroups;
+  r.k0 = r.copy * S::kCols;
+  r.lanes = sm.tmem_base + tmem_lane_base(warp);
+  r.warp_live = info.it.r0 + 32 * (warp % S::kGroups) < info.it.r1;
+  const int row = info.row[r.rr];
+  r.live = row >= 0;
+  r.node = r.live ? row % kTreeMax : 0;
+  r.hrel = r.live ? row / kTreeMax : 0;
+  r.depth = sm.tree[info.it.tree].depth[r.node];
+  r.cs = info.scale[r.rr];
+  r.woff = r.hrel * window_floats(S::kTile, n) + ((a.tab_zero - (info.it.len + n - 1)) & 3) +
+           (n - 1 - r.depth) + r.k0;
+  return r;
+}
+
+// N / 2 columns of P (bf16 pairs) of this warp's lanes.
+template <int N>
+__device__ __forceinline__ void tmem_st_pairs(uint32_t taddr, const uint32_t* r) {
+  if constexpr (N == 16)
+    tmem_st_32x32b_x8(taddr, r);
+  else
+    tmem_st_32x32b_x16(taddr, r);
+}
+
+// The start of a tile: S and the windows are there.
+__device__ __forceinline__ bool soft_begin(const TreeArgs& a, TreeSmem& sm, SoftState& st) {
+  volatile int* ab = &sm.abort_flag;
+  st.ok = warp_wait(&sm.s_full, st.g & 1, a.c.status, ab, kSiteTreeSoftS) &&
+          warp_wait(&sm.k_full[st.s], st.phase, a.c.status, ab, kSiteTreeSoftK);
+  if (st.ok) tc_fence_after();
+  return st.ok;
+}
+__device__ __forceinline__ void soft_free_s(TreeSmem& sm, const SoftState& st) {
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.s_free[st.s]);
+}
+// Takes the tile's maximum mx into account and waits until the previous P V
+// is done (P may then be overwritten, and O is at rest).  `scale`: what O has
+// to be multiplied by.
+__device__ __forceinline__ bool soft_max(const TreeArgs& a, TreeSmem& sm, const SoftRow& row,
+                                         SoftState& st, float mx, float& scale) {
+  volatile int* ab = &sm.abort_flag;
+  scale = 1.0f;
+  const float m_new = fmaxf(st.m, mx);
+  if (row.warp_live && m_new > st.m + kRescale) {
+    scale = ex2_approx(st.m - m_new);
+    st.l *= scale;
+    st.m = m_new;
+  }
+  if (st.g > 0) {
+    st.ok = warp_wait(&sm.pv_done, (st.g - 1) & 1, a.c.status, ab, kSiteTreeSoftPV);
+    if (st.ok) tc_fence_after();
+  }
+  return st.ok;
+}
+// The end of a tile: O scaled if need be, P complete.
+__device__ __forceinline__ void soft_finish(const TreeArgs& a, TreeSmem& sm, const SoftRow& row,
+                                            SoftState& st, float scale) {
+  if (row.warp_live) {
+    if (!st.first && __any_sync(0xffffffffu, scale != 1.0f)) {
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t ov[16];
+        tmem_ld_cols<16>(row.lanes + kColO + 16 * q, ov);
+#pragma unroll
+        for (int y = 0; y < 16; ++y) ov[y] = __float_as_uint(__uint_as_float(ov[y]) * scale);
+        tmem_st_32x32b_x16(row.lanes + kColO + 16 * q, ov);
+      }
+    }
+    tmem_st_wait();
+  }
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.p_full);
+  if (++st.s == a.stages) {
+    st.s = 0;
+    st.phase ^= 1;
+  }
+  ++st.g;
+  ++st.t;
+  st.first = false;
+}
+// Two weights and their bf16 parts; l2 gathers the exact ones.
+template <int PARTS, int N>
+__device__ __forceinline__ void soft_weights(uint64_t z, uint64_t negm2, uint64_t& l2,
+                                             uint32_t (*pk)[N], int y) {
+  float p0, p1;
+  f2_unpack(fadd2(z, negm2), p0, p1);
+  p0 = ex2_approx(p0);
+  p1 = ex2_approx(p1);
+  l2 = fadd2(l2, f2_pack(p0, p1));
+#pragma unroll
+  for (int part = 0; part < PARTS; ++part) {
+    const uint32_t u = pack_bf16x2(p0, p1);
+    pk[part][y] = u;
+    if (part + 1 < PARTS) {
+      p0 -= __uint_as_float(u << 16);
+      p1 -= __uint_as_float(u & 0xFFFF0000u);
+    }
+  }
+}
+
+// A tile of which every row sees every key.
+template <int PARTS, int KS>
+__device__ __forceinline__ void soft_tile(const TreeArgs& a, const View& v, const SoftRow& row,
+                                          SoftState& st) {
+  using S = Shape<PARTS, KS>;
+  TreeSmem& sm = *v.sm;
+  if (!soft_begin(a, sm, st)) return;
+  uint64_t z[S::kCols / 2];
+  float mx = kNoMax, scale;
+  if (row.warp_live) {
+    const float* w = v.win + st.s * a.win_stage + row.woff;
+    uint32_t sv[S::kCols];
+    tmem_ld_cols<S::kCols>(row.lanes + row.k0, sv);
+    const uint64_t c2 = f2_pack(row.cs, row.cs);
+#pragma unroll
+    for (int y = 0; y < S::kCols / 2; ++y)
+      z[y] = ffma2(f2_pack(__uint_as_float(sv[2 * y]), __uint_as_float(sv[2 * y + 1])), c2,
+                   f2_pack(w[2 * y], w[2 * y + 1]));
+  }
+  soft_free_s(sm, st);
+  if (row.warp_live) {
+    float mq[4];
+#pragma unroll
+    for (int y = 0; y < S::kCols / 2; ++y) {
+      float lo, hi;
+      f2_unpack(z[y], lo, hi);
+      mq[y & 3] = y < 4 ? fmaxf(lo, hi) : fmax3(mq[y & 3], lo, hi);
+    }
+    mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+  }
+  if (!soft_max(a, sm, row, st, mx, scale)) return;
+  if (row.warp_live) {
+    const uint64_t negm2 = f2_pack(-st.m, -st.m);
+    uint64_t l2[2] = {0ull, 0ull};
+    constexpr int kBatch = S::kCols < 32 ? S::kCols / 2 : 16;  // column pairs
+#pragma unroll
+    for (int q = 0; q < S::kCols / 2 / kBatch; ++q) {
+      uint32_t pk[PARTS][kBatch];
+#pragma unroll
+      for (int y = 0; y < kBatch; ++y)
+        soft_weights<PARTS, kBatch>(z[kBatch * q + y], negm2, l2[y & 1], pk, y);
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part)
+        tmem_st_pairs<2 * kBatch>(row.lanes + S::kColP + row.k0 / 2 + S::kPCols * part + kBatch * q,
+                                  pk[part]);
+    }
+    float b0, b1;
+    f2_unpack(fadd2(l2[0], l2[1]), b0, b1);
+    st.l += b0 + b1;
+  }
+  soft_finish(a, sm, row, st, scale);
+}
+
+// A tile with keys that not every row sees: 16 columns at a time, S read
+// twice, so that this rarer code takes few registers from the other.
+template <int PARTS, int KS>
+__device__ __forceinline__ void soft_tail(const TreeArgs& a, const View& v, const SoftRow& row,
+                                          SoftState& st, int k) {
+  using S = Shape<PARTS, KS>;
+  TreeSmem& sm = *v.sm;
+  volatile int* ab = &sm.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const ItemInfo& info = sm.info[k & 1];
+  const TreeInfo& ti = sm.tree[info.it.tree];
+  const int n = info.it.n, len = info.it.len, j0 = st.t * S::kTile;
+  if (!soft_begin(a, sm, st)) return;
+  const float* w = v.win + st.s * a.win_stage + row.woff;
+  const float* near = info.near + row.hrel * n + row.depth;  // of an ancestor: near[-its depth]
+  const uint64_t vis = row.live ? tile_mask(ti.seen[row.node], j0 + row.k0, len) : 0;
+  auto logits = [&](int q, uint64_t* z) __attribute__((always_inline)) {
+    uint32_t sv[16];
+    tmem_ld_cols<16>(row.lanes + row.k0 + 16 * q, sv);
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      float e[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int kk = 16 * q + 2 * y + h, i = j0 + row.k0 + kk - len;
+        // Loads of keys out of sight stay in range and are not used.
+        const int back = min(ti.depth[min(max(i, 0), kTreeMax - 1)], row.depth);
+        const float bias = i < 0 ? w[kk] : near[-back];
+        const float x = fmaf(__uint_as_float(sv[2 * y + h]), row.cs, bias);
+        e[h] = vis >> kk & 1 ? x : -INFINITY;
+      }
+      z[y] = f2_pack(e[0], e[1]);
+    }
+  };
+  float mx = kNoMax, scale;
+  if (row.warp_live) {
+#pragma unroll 1
+    for (int q = 0; q < S::kCols / 16; ++q) {
+      uint64_t z[8];
+      logits(q, z);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        float lo, hi;
+        f2_unpack(z[y], lo, hi);
+        mx = fmax3(mx, lo, hi);
+      }
+    }
+  }
+  // Rows of V behind the draft hold anything, and a drafted value that is not
+  // finite must not meet the weight 0 of a row that does not see it: zeros
+  // here, a quarter of the rows by each warp.  The latter are added to O at
+  // the item's end.
+  st.ok = warp_wait(&sm.v_full[st.s], st.phase, a.c.status, ab, kSiteTreeSoftK);
+  if (!st.ok) return;
+  bool any = false;
+#pragma unroll 2
+  for (int y = 0; y < S::kTile / 16; ++y) {
+    const int key = S::kTile / kSoftWarps * warp + 4 * y + (lane >> 3), i = j0 + key - len;
+    if (i < 0) continue;
+    uint4* p = reinterpret_cast<uint4*>(v.sv + st.s * S::kTileBytes + key * 128 + 16 * (lane & 7));
+    uint4 x = *p;
+    uint32_t* u = reinterpret_cast<uint32_t*>(&x);
+    bool fix = i >= n;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      uint32_t keep = i >= n ? 0u : 0xFFFFFFFFu;
+      if (odd_exp(u[h])) keep &= 0xFFFF0000u;
+      if (odd_exp(u[h] >> 16)) keep &= 0x0000FFFFu;
+      fix |= keep != 0xFFFFFFFFu;
+      if (i < n && keep != 0xFFFFFFFFu) atomicOr(&sm.odd[k & 1][i >> 5], 1u << (i & 31));
+      u[h] &= keep;
+    }
+    if (fix) *p = x;
+    any |= fix;
+  }
+  if (any) fence_proxy_async_smem();
+  __syncwarp();
+  if (!soft_max(a, sm, row, st, mx, scale)) return;
+  if (row.warp_live) {
+    const uint64_t negm2 = f2_pack(-st.m, -st.m);
+    uint64_t l2 = 0ull;
+#pragma unroll 1
+    for (int q = 0; q < S::kCols / 16; ++q) {
+      uint64_t z[8];
+      uint32_t pk[PARTS][8];
+      logits(q, z);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) soft_weights<PARTS, 8>(z[y], negm2, l2, pk, y);
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part)
+        tmem_st_pairs<16>(row.lanes + S::kColP + row.k0 / 2 + S::kPCols * part + 8 * q, pk[part]);
+    }
+    float b0, b1;
+    f2_unpack(l2, b0, b1);
+    st.l += b0 + b1;
+  }
+  soft_free_s(sm, st);
+  soft_finish(a, sm, row, st, scale);
+}
+
+// The item's end: the copies are joined, 32 columns at a time, through the
+// buffer of its queries, which its products no longer read.
+template <int PARTS, int KS>
+__device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const SoftRow& row,
+                                         const SoftState& st, int k) {
+  using S = Shape<PARTS, KS>;
+  TreeSmem& sm = *v.sm;
+  const CacheArgs& c = a.c;
+  volatile int* ab = &sm.abort_flag;
+  const int lane = threadIdx.x & 31;
+  const ItemInfo& info = sm.info[k & 1];
+  const TreeInfo& ti = sm.tree[info.it.tree];
+  const int n = info.it.n, hk = info.it.hk, bb = info.it.b, t0 = info.it.t0;
+  if (!warp_wait(&sm.pv_done, (st.g - 1) & 1, c.status, ab, kSiteTreeSoftEnd)) return false;
+  tc_fence_after();
+  const bool whole = t0 == 0 && info.it.t1 == info.it.tiles;
+  const size_t orow =
+      (static_cast<size_t>(bb) * a.H + hk * a.group + info.it.r0 / n + row.hrel) * c.N + row.node;
+  const size_t prow = static_cast<size_t>(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * S::kRows + row.rr;
+  const uint32_t* odd = sm.odd[k & 1];
+  const bool any_odd = (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
+  uint8_t* const merge = v.sq + (k & 1) * kQBytes;  // [KS - 1][kRows] rows of 128 bytes, swizzled
+  float M = st.m, L = st.l, f[KS];
+  f[0] = 1.0f;
+  if (KS > 1 && row.copy > 0 && row.warp_live)
+    sm.merge_ml[(row.copy - 1) * S::kRows + row.rr] = make_float2(st.m, st.l);
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    uint32_t ov[16];
+    float* o = reinterpret_cast<float*>(ov);
+    if (row.warp_live) tmem_ld_cols<16>(row.lanes + kColO + 16 * q, ov);
+    if (KS > 1) {
+      if ((q & 1) == 0) {
+        if (row.copy > 0 && row.warp_live) {
+          const int mr = (row.copy - 1) * S::kRows + row.rr;
+          uint32_t o2[16];
+          tmem_ld_cols<16>(row.lanes + kColO + 16 * q + 16, o2);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            *reinterpret_cast<uint4*>(merge + mr * 128 + ((y ^ (mr & 7)) << 4)) =
+                make_uint4(ov[4 * y], ov[4 * y + 1], ov[4 * y + 2], ov[4 * y + 3]);
+            *reinterpret_cast<uint4*>(merge + mr * 128 + (((y + 4) ^ (mr & 7)) << 4)) =
+                make_uint4(o2[4 * y], o2[4 * y + 1], o2[4 * y + 2], o2[4 * y + 3]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.merge_full);
+        if (!warp_wait(&sm.merge_full, q >> 1, c.status, ab, kSiteTreeMerge)) return false;
+        if (q == 0 && row.copy == 0 && row.live) {
+#pragma unroll
+          for (int y = 1; y < KS; ++y) M = fmaxf(M, sm.merge_ml[(y - 1) * S::kRows + row.rr].x);
+          f[0] = ex2_approx(st.m - M);
+          L *= f[0];
+#pragma unroll
+          for (int y = 1; y < KS; ++y) {
+            const float2 ml = sm.merge_ml[(y - 1) * S::kRows + row.rr];
+            f[y] = ex2_approx(ml.x - M);
+            L += ml.y * f[y];
+          }
+        }
+      }
+      if (row.copy == 0 && row.live) {
+#pragma unroll
+        for (int y = 0; y < 16; ++y) o[y] *= f[0];
+#pragma unroll
+        for (int cp = 1; cp < KS; ++cp) {
+          const int mr = (cp - 1) * S::kRows + row.rr;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float4 x = *reinterpret_cast<const float4*>(
+                merge + mr * 128 + (((y + 4 * (q & 1)) ^ (mr & 7)) << 4));
+            o[4 * y] = fmaf(x.x, f[cp], o[4 * y]);
+            o[4 * y + 1] = fmaf(x.y, f[cp], o[4 * y + 1]);
+            o[4 * y + 2] = fmaf(x.z, f[cp], o[4 * y + 2]);
+            o[4 * y + 3] = fmaf(x.w, f[cp], o[4 * y + 3]);
+          }
+        }
+      }
+      if (q == 1) {
+        // The second half may overwrite the first.
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.merge_free);
+        if (!warp_wait(&sm.merge_free, k & 1, c.status, ab, kSiteTreeMerge)) return false;
+      }
+    }
+    if (row.copy > 0 || !row.live) continue;
+    if (any_odd) {
+      // Values that are not finite, for the nodes that see them.
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        if (!(odd[i >> 5] >> (i & 31) & 1) || !(ti.seen[row.node][i >> 5] >> (i & 31) & 1)) continue;
+        const int slot = info.it.len + i;
+        int pg = __ldg(c.block_table + static_cast<size_t>(bb) * c.max_blocks + slot / c.page);
+        if (pg < 0 || pg >= c.num_pages) pg = 0;
+        const uint32_t* vr = reinterpret_cast<const uint32_t*>(
+            a.v_pages + ((static_cast<size_t>(pg) * c.Hkv + hk) * c.page + slot % c.page) * kHeadDim +
+            16 * q);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const uint32_t u = __ldg(vr + y);
+          if (odd_exp(u)) o[2 * y] += __uint_as_float(u << 16);
+          if (odd_exp(u >> 16)) o[2 * y + 1] += __uint_as_float(u & 0xFFFF0000u);
+        }
+      }
+    }
+    if (!whole) {
+      float4* dst = reinterpret_cast<float4*>(a.part + prow * kHeadDim + 16 * q);
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+      if (q == 0) a.part_ml[prow] = make_float2(M, L);
+    } else {
+      const float inv = 1.0f / L;
+      if (PARTS > 1) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kHeadDim + 16 * q);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          dst[y] = make_float4(o[4 * y] * inv, o[4 * y + 1] * inv, o[4 * y + 2] * inv,
+                               o[4 * y + 3] * inv);
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * kHeadDim + 16 * q);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float* e = o + 8 * y;
+          dst[y] = make_uint4(pack_bf16x2(e[0] * inv, e[1] * inv), pack_bf16x2(e[2] * inv, e[3] * inv),
+                              pack_bf16x2(e[4] * inv, e[5] * inv), pack_bf16x2(e[6] * inv, e[7] * inv));
+        }
+      }
+      if (q == 0 && a.lse) a.lse[orow] = (M + log2f(L)) * kLn2f;
+    }
+  }
+  // O has been read before the next item's products overwrite it: they wait
+  // for its p_full, on which every warp arrives after this.
+  tc_fence_before();
+  return true;
+}
+
 // One CTA walks its run of tiles; two CTAs share an SM, so that one's
 // hand-offs are covered by the other's work.  Roles:
 //   producer warp   walks the plan; prepares each item one ahead (queries,
@@ -348,24 +834,13 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 template <int PARTS, int KS>
 __global__ void __launch_bounds__(kTreeThreads, 2)
     bam_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                    const TreeArgs a) {
-  constexpr int kRows = kRowsMax / KS;     // rows of an item
-  constexpr int kGroups = kRows / 32;      // warps of a copy
-  constexpr int kTile = KS == 1 ? 64 : 128;  // keys of a tile
-  constexpr int kCols = kTile / KS;        // of which one copy's
-  constexpr int kTileBytes = kTile * kHeadDim * 2;
-  constexpr int kPCols = kTile / 2;        // columns of a part of P
-  // Where S and the parts of P do not fit side by side, P takes the place of
-  // S, and the next S waits for P V.
-  constexpr bool kOverlay = kTile + kPCols * PARTS > kColO;
-  constexpr uint32_t kColP = kOverlay ? 0 : kTile;
-  static_assert(kColP + kPCols * PARTS <= kColO, "Tensor Memory");
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  uint8_t* const sq = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // two query tiles
-  uint8_t* const sk = sq + 2 * kQBytes;  // [stages] tiles of K, then of V
-  uint8_t* const sv_ring = sk + a.stages * kTileBytes;
-  float* const win = reinterpret_cast<float*>(sv_ring + a.stages * kTileBytes);
-  TreeSmem& sm = *reinterpret_cast<TreeSmem*>(win + a.stages * a.win_stage);
+                    const __grid_constant__ TreeArgs a) {
+  using S = Shape<PARTS, KS>;
+  constexpr int kRows = S::kRows, kTile = S::kTile, kTileBytes = S::kTileBytes;
+  const View v = smem_view<S>(a);
+  uint8_t *const sq = v.sq, *const sk = v.sk, *const sv_ring = v.sv;
+  float* const win = v.win;
+  TreeSmem& sm = *v.sm;
   const CacheArgs& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kProducer = kSoftWarps, kMma = kSoftWarps + 1;
@@ -656,7 +1131,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         if (p.left > 0) return true;
         ++p.k;
         p.first = true;
-        ok = ok && mbar_wait(&sm.item_full[p.k & 1], (p.k >> 1) & 1, c.status, ab, kSiteTreeMmaItem);
+        ok = ok && tree_wait(&sm.item_full[p.k & 1], (p.k >> 1) & 1, c.status, ab, kSiteTreeMmaItem);
         if (!ok) return false;
         const Item& it = sm.info[p.k & 1].it;
         p.left = it.t1 - it.t0;
@@ -665,12 +1140,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       auto issue_s = [&]() {
         if (ps.g > 0) {  // the S before it has been read
           const int q = (ps.s == 0 ? a.stages : ps.s) - 1;
-          ok = ok && mbar_wait(&sm.s_free[q], ps.s == 0 ? ps.phase ^ 1 : ps.phase, c.status, ab,
+          ok = ok && tree_wait(&sm.s_free[q], ps.s == 0 ? ps.phase ^ 1 : ps.phase, c.status, ab,
                                kSiteTreeMmaS);
-          if (kOverlay)  // and so has the P that took its place
-            ok = ok && mbar_wait(&sm.pv_done, (ps.g - 1) & 1, c.status, ab, kSiteTreeMmaS);
         }
-        ok = ok && mbar_wait(&sm.k_full[ps.s], ps.phase, c.status, ab, kSiteTreeMmaK);
+        ok = ok && tree_wait(&sm.k_full[ps.s], ps.phase, c.status, ab, kSiteTreeMmaK);
         if (!ok) return;
         tc_fence_after();
         const uint64_t q0 = qd + kQDesc * (ps.k & 1), k0 = kd + kSlotDesc * ps.s;
@@ -685,15 +1158,15 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       while (ok && ps.g > pv.g) {
         // The next tile's S goes first if its item and keys are there (the
         // softmax reads this tile's S before it writes P).
-        if (!kOverlay && more &&
+        if (more &&
             (ps.left > 0 || mbar_test(&sm.item_full[(ps.k + 1) & 1], ((ps.k + 1) >> 1) & 1))) {
           more = enter(ps);
           if (more && mbar_test(&sm.k_full[ps.s], ps.phase)) issue_s();
         }
         const bool behind = ps.g == pv.g + 1;
         if (!enter(pv)) break;
-        ok = ok && mbar_wait(&sm.v_full[pv.s], pv.phase, c.status, ab, kSiteTreeMmaK) &&
-             mbar_wait(&sm.p_full, pv.g & 1, c.status, ab, kSiteTreeMmaP);
+        ok = ok && tree_wait(&sm.v_full[pv.s], pv.phase, c.status, ab, kSiteTreeMmaK) &&
+             tree_wait(&sm.p_full, pv.g & 1, c.status, ab, kSiteTreeMmaP);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -702,7 +1175,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           for (int kk = 0; kk < kTile / 16; ++kk) {
             // 16 keys; they belong to copy kk / kSteps.
             constexpr int kSteps = kTile / 16 / KS;
-            umma_ts_lanes<KS>(tm + kColO, tm + kColP + kPCols * part + 8 * kk,
+            umma_ts_lanes<KS>(tm + kColO, tm + S::kColP + S::kPCols * part + 8 * kk,
                               vd + kSlotDesc * pv.s + 128 * kk, id_o,
                               (!pv.first || part > 0 || kk % kSteps > 0) ? 1u : 0u, kk / kSteps);
           }
@@ -719,313 +1192,22 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    const int rg = warp % kGroups, copy = warp / kGroups;
-    const int rr = 32 * rg + lane;  // row of the item
-    const int k0 = copy * kCols;    // first key of this copy in a tile
-    const uint32_t lanes = tm + tmem_lane_base(warp);
-    const uint32_t tS = lanes + k0, tP = lanes + kColP + k0 / 2, tO = lanes + kColO;
-    bool ok = true;
-    int g = 0, s = 0, phase = 0, merges = 0;
+    SoftState st{0, 0, 0, 0, 0.0f, 0.0f, true, true};
     for (int k = 0;; ++k) {
-      ok = warp_wait(&sm.item_full[k & 1], (k >> 1) & 1, c.status, ab, kSiteTreeSoftItem);
-      if (!ok) break;
+      st.ok = warp_wait(&sm.item_full[k & 1], (k >> 1) & 1, c.status, ab, kSiteTreeSoftItem);
+      if (!st.ok) break;
       const ItemInfo& info = sm.info[k & 1];
       const int t1 = info.it.t1;
       if (t1 == 0) break;
-      const TreeInfo& ti = sm.tree[info.it.tree];
-      const int n = info.it.n, len = info.it.len, t0 = info.it.t0;
-      const int row = info.row[rr];
-      const bool live = row >= 0;
-      const int node = live ? row % kTreeMax : 0, hrel = live ? row / kTreeMax : 0;
-      const bool warp_live = info.it.r0 + 32 * rg < info.it.r1;
-      const int depth = ti.depth[node];
-      const float cs = info.scale[rr];
-      const int woff = hrel * window_floats(kTile, n) + ((a.tab_zero - (len + n - 1)) & 3) + (n - 1 - depth) + k0;
-      const float* near = info.near + hrel * n + depth;  // entry of an ancestor: near[-its depth]
-      float m = kNoMax, l = 0.0f;  // log2 units; sum of the weights
-      for (int t = t0; t < t1; ++t, ++g) {
-        const int j0 = t * kTile;
-        const bool tail = j0 + kTile > len;  // holds keys that not every row sees
-        ok = warp_wait(&sm.s_full, g & 1, c.status, ab, kSiteTreeSoftS) &&
-             warp_wait(&sm.k_full[s], phase, c.status, ab, kSiteTreeSoftK);
-        if (!ok) break;
-        tc_fence_after();
-        const float* w = win + s * a.win_stage + woff;
-        uint64_t z[kCols / 2];
-        if (warp_live) {
-          uint32_t sv[kCols];
-          tmem_ld_cols<kCols>(tS, sv);
-          const uint64_t c2 = f2_pack(cs, cs);
-          if (!tail) {
-#pragma unroll
-            for (int y = 0; y < kCols / 2; ++y)
-              z[y] = ffma2(f2_pack(__uint_as_float(sv[2 * y]), __uint_as_float(sv[2 * y + 1])), c2,
-                           f2_pack(w[2 * y], w[2 * y + 1]));
-          } else {
-            const uint64_t vis = live ? tile_mask(ti.seen[node], j0 + k0, len) : 0;
-#pragma unroll
-            for (int y = 0; y < kCols / 2; ++y) {
-              float e[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int kk = 2 * y + h, i = j0 + k0 + kk - len;
-                // Loads of keys out of sight stay in range and are not used.
-                const int back = min(ti.depth[min(max(i, 0), kTreeMax - 1)], depth);
-                const float bias = i < 0 ? w[kk] : near[-back];
-                const float v = fmaf(__uint_as_float(sv[kk]), cs, bias);
-                e[h] = vis >> kk & 1 ? v : -INFINITY;
-              }
-              z[y] = f2_pack(e[0], e[1]);
-            }
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.s_free[s]);
-
-        if (tail) {
-          // Rows of V behind the draft hold anything, and a drafted value that
-          // is not finite must not meet the weight 0 of a row that does not
-          // see it: zeros here, a quarter of the rows by each warp.  The
-          // latter are added to O at the item's end.
-          ok = warp_wait(&sm.v_full[s], phase, c.status, ab, kSiteTreeSoftK);
-          if (!ok) break;
-          bool any = false;
-#pragma unroll 4
-          for (int y = 0; y < kTile / 16; ++y) {
-            const int row = kTile / kSoftWarps * warp + 4 * y + (lane >> 3), i = j0 + row - len;
-            if (i < 0) continue;
-            uint4* p = reinterpret_cast<uint4*>(sv_ring + s * kTileBytes + row * 128 + 16 * (lane & 7));
-            uint4 v = *p;
-            uint32_t* u = reinterpret_cast<uint32_t*>(&v);
-            bool fix = i >= n;
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              uint32_t keep = i >= n ? 0u : 0xFFFFFFFFu;
-              if (odd_exp(u[h])) keep &= 0xFFFF0000u;
-              if (odd_exp(u[h] >> 16)) keep &= 0x0000FFFFu;
-              fix |= keep != 0xFFFFFFFFu;
-              if (i < n && keep != 0xFFFFFFFFu) atomicOr(&sm.odd[k & 1][i >> 5], 1u << (i & 31));
-              u[h] &= keep;
-            }
-            if (fix) *p = v;
-            any |= fix;
-          }
-          if (any) fence_proxy_async_smem();
-          __syncwarp();
-        }
-
-        bool resc = false;
-        float scale = 1.0f;
-        if (warp_live) {
-          float mq[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            float lo, hi;
-            f2_unpack(z[y], lo, hi);
-            mq[y] = fmaxf(lo, hi);
-          }
-#pragma unroll
-          for (int y = 4; y < kCols / 2; ++y) {
-            float lo, hi;
-            f2_unpack(z[y], lo, hi);
-            mq[y & 3] = fmax3(mq[y & 3], lo, hi);
-          }
-          const float m_new = fmaxf(m, fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])));
-          resc = m_new > m + kRescale;
-          if (resc) {
-            scale = ex2_approx(m - m_new);
-            l *= scale;
-            m = m_new;
-          }
-        }
-        if (g > 0) {
-          // The previous P V is done: P may be overwritten, O is at rest.
-          ok = warp_wait(&sm.pv_done, (g - 1) & 1, c.status, ab, kSiteTreeSoftPV);
-          if (!ok) break;
-          tc_fence_after();
-        }
-        if (warp_live) {
-          const uint64_t negm2 = f2_pack(-m, -m);
-          uint64_t l2[2] = {0ull, 0ull};
-          constexpr int kBatch = kCols / 2 < 16 ? kCols / 2 : 16;
-#pragma unroll
-          for (int q = 0; q < kCols / 2 / kBatch; ++q) {
-            uint32_t pk[PARTS][kBatch];
-#pragma unroll
-            for (int y = 0; y < kBatch; ++y) {
-              float p0, p1;
-              f2_unpack(fadd2(z[kBatch * q + y], negm2), p0, p1);
-              p0 = ex2_approx(p0);
-              p1 = ex2_approx(p1);
-              l2[y & 1] = fadd2(l2[y & 1], f2_pack(p0, p1));
-#pragma unroll
-              for (int part = 0; part < PARTS; ++part) {
-                const uint32_t u = pack_bf16x2(p0, p1);
-                pk[part][y] = u;
-                if (part + 1 < PARTS) {
-                  p0 -= __uint_as_float(u << 16);
-                  p1 -= __uint_as_float(u & 0xFFFF0000u);
-                }
-              }
-            }
-#pragma unroll
-            for (int part = 0; part < PARTS; ++part) {
-              if (kBatch == 16)
-                tmem_st_32x32b_x16(tP + kPCols * part + 16 * q, pk[part]);
-              else
-                tmem_st_32x32b_x8(tP + kPCols * part, pk[part]);
-            }
-          }
-          float b0, b1;
-          f2_unpack(fadd2(l2[0], l2[1]), b0, b1);
-          l += b0 + b1;
-          if (t > t0 && __any_sync(0xffffffffu, resc)) {
-#pragma unroll
-            for (int hb = 0; hb < 2; ++hb) {
-              uint32_t ov[32];
-              tmem_ld_cols<32>(tO + 32 * hb, ov);
-#pragma unroll
-              for (int y = 0; y < 32; ++y) ov[y] = __float_as_uint(__uint_as_float(ov[y]) * scale);
-              tmem_st_32x32b_x32(tO + 32 * hb, ov);
-            }
-          }
-          tmem_st_wait();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full);
-        if (++s == a.stages) {
-          s = 0;
-          phase ^= 1;
-        }
-      }
-      if (!ok) break;
-      ok = warp_wait(&sm.pv_done, (g - 1) & 1, c.status, ab, kSiteTreeSoftEnd);
-      if (!ok) break;
-      tc_fence_after();
-
-      // The item's end: the copies are joined, 32 columns at a time, through
-      // the buffer of its queries, which its products no longer read.
-      const int hk = info.it.hk, bb = info.it.b;
-      const bool whole = t0 == 0 && t1 == info.it.tiles;
-      const size_t orow =
-          (static_cast<size_t>(bb) * a.H + hk * a.group + info.it.r0 / n + hrel) * c.N + node;
-      const size_t prow = static_cast<size_t>(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * kRows + rr;
-      const uint32_t* odd = sm.odd[k & 1];
-      const bool any_odd = (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
-      uint8_t* const merge = sq + (k & 1) * kQBytes;  // [KS - 1][kRows] rows of 128 bytes, swizzled
-      float M = m, L = l, f[KS];
-      f[0] = 1.0f;
-#pragma unroll
-      for (int hb = 0; hb < 2; ++hb) {
-        uint32_t ov[32];
-        float* o = reinterpret_cast<float*>(ov);
-        if (warp_live) tmem_ld_cols<32>(tO + 32 * hb, ov);
-        if (KS > 1) {
-          if (copy > 0 && warp_live) {
-            const int mr = (copy - 1) * kRows + rr;
-            if (hb == 0) sm.merge_ml[mr] = make_float2(m, l);
-#pragma unroll
-            for (int y = 0; y < 8; ++y)
-              *reinterpret_cast<uint4*>(merge + mr * 128 + ((y ^ (mr & 7)) << 4)) =
-                  make_uint4(ov[4 * y], ov[4 * y + 1], ov[4 * y + 2], ov[4 * y + 3]);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.merge_full);
-          ok = warp_wait(&sm.merge_full, merges & 1, c.status, ab, kSiteTreeMerge);
-          if (!ok) break;
-          if (copy == 0 && live) {
-            if (hb == 0) {
-#pragma unroll
-              for (int y = 1; y < KS; ++y) M = fmaxf(M, sm.merge_ml[(y - 1) * kRows + rr].x);
-              f[0] = ex2_approx(m - M);
-              L *= f[0];
-#pragma unroll
-              for (int y = 1; y < KS; ++y) {
-                const float2 ml = sm.merge_ml[(y - 1) * kRows + rr];
-                f[y] = ex2_approx(ml.x - M);
-                L += ml.y * f[y];
-              }
-            }
-#pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] *= f[0];
-#pragma unroll
-            for (int cp = 1; cp < KS; ++cp) {
-              const int mr = (cp - 1) * kRows + rr;
-#pragma unroll
-              for (int y = 0; y < 8; ++y) {
-                const float4 v =
-                    *reinterpret_cast<const float4*>(merge + mr * 128 + ((y ^ (mr & 7)) << 4));
-                o[4 * y] = fmaf(v.x, f[cp], o[4 * y]);
-                o[4 * y + 1] = fmaf(v.y, f[cp], o[4 * y + 1]);
-                o[4 * y + 2] = fmaf(v.z, f[cp], o[4 * y + 2]);
-                o[4 * y + 3] = fmaf(v.w, f[cp], o[4 * y + 3]);
-              }
-            }
-          }
-          __syncwarp();
-          if (hb == 0) {
-            // The second half may overwrite the first.
-            if (lane == 0) mbar_arrive(&sm.merge_free);
-            ok = warp_wait(&sm.merge_free, k & 1, c.status, ab, kSiteTreeMerge);
-            if (!ok) break;
-          }
-          ++merges;
-        }
-        if (copy > 0 || !live) continue;
-        if (any_odd) {
-          // Values that are not finite, for the nodes that see them.
-          for (int i = 0; i < n; ++i) {
-            if (!(odd[i >> 5] >> (i & 31) & 1) || !(ti.seen[node][i >> 5] >> (i & 31) & 1)) continue;
-            const int slot = len + i;
-            int pg = __ldg(c.block_table + static_cast<size_t>(bb) * c.max_blocks + slot / c.page);
-            if (pg < 0 || pg >= c.num_pages) pg = 0;
-            const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                a.v_pages + ((static_cast<size_t>(pg) * c.Hkv + hk) * c.page + slot % c.page) * kHeadDim +
-                32 * hb);
-#pragma unroll
-            for (int y = 0; y < 16; ++y) {
-              const uint32_t u = __ldg(v + y);
-              if (odd_exp(u)) o[2 * y] += __uint_as_float(u << 16);
-              if (odd_exp(u >> 16)) o[2 * y + 1] += __uint_as_float(u & 0xFFFF0000u);
-            }
-          }
-        }
-        if (!whole) {
-          float4* dst = reinterpret_cast<float4*>(a.part + prow * kHeadDim + 32 * hb);
-#pragma unroll
-          for (int y = 0; y < 8; ++y)
-            dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-          if (hb == 0) a.part_ml[prow] = make_float2(M, L);
-        } else {
-          const float inv = 1.0f / L;
-          if (PARTS > 1) {
-            float4* dst =
-                reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kHeadDim + 32 * hb);
-#pragma unroll
-            for (int y = 0; y < 8; ++y)
-              dst[y] = make_float4(o[4 * y] * inv, o[4 * y + 1] * inv, o[4 * y + 2] * inv,
-                                   o[4 * y + 3] * inv);
-          } else {
-            uint4* dst =
-                reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * kHeadDim + 32 * hb);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              float* e = o + 8 * y;
-              dst[y] = make_uint4(pack_bf16x2(e[0] * inv, e[1] * inv),
-                                  pack_bf16x2(e[2] * inv, e[3] * inv),
-                                  pack_bf16x2(e[4] * inv, e[5] * inv),
-                                  pack_bf16x2(e[6] * inv, e[7] * inv));
-            }
-          }
-          if (hb == 0 && a.lse) a.lse[orow] = (M + log2f(L)) * kLn2f;
-        }
-      }
-      if (!ok) break;
-      // O has been read before the next item's products overwrite it: they
-      // wait for its p_full, on which every warp arrives after this.
-      tc_fence_before();
+      st.t = info.it.t0;
+      st.m = kNoMax;
+      st.l = 0.0f;
+      st.first = true;
+      const SoftRow row = soft_row<S>(a, sm, k);
+      for (const int plain = min(t1, info.it.len / S::kTile); st.ok && st.t < plain;)
+        soft_tile<PARTS, KS>(a, v, row, st);
+      while (st.ok && st.t < t1) soft_tail<PARTS, KS>(a, v, row, st, k);
+      if (!st.ok || !soft_end<PARTS, KS>(a, v, row, st, k)) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
     }
@@ -1142,7 +1324,7 @@ cudaError_t launch_parts(const CUtensorMap& tk, const CUtensorMap& tv, const Tre
 // Ring and grid of the call, from its sizes.  Returns false when a stage does
 // not fit (more heads share a key head than its windows have room for).
 bool tree_config(TreeArgs* a, int sms) {
-  a->tile = a->rows == kRowsMax ? 64 : 128;
+  a->tile = tree_tile(a->o_fp32 ? 3 : 1, kRowsMax / a->rows);
   // Most heads and floats that a stage's windows hold, over the node counts.
   a->win_stage = 0;
   for (int n = 1; n <= a->c.N; ++n) {
