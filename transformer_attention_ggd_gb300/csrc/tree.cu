@@ -28,7 +28,6 @@ constexpr int kRowsMax = 128;      // rows of an item: lanes of Tensor Memory
 constexpr int kBox = 64;                             // keys of a TMA box: pages are multiples of it
 constexpr int kBoxBytes = kBox * kHeadDim * 2;
 constexpr int kQBytes = kRowsMax * kHeadDim * 2;
-constexpr int kNear = kRowsMax + 2 * kTreeMax;  // an item's table entries of the draft's distances
 constexpr int kMaxStages = 8;
 constexpr float kRescale = 8.0f;  // log2 units by which a weight may exceed 1
 constexpr float kNoMax = -3.4e38f;  // below every logit (the table is clamped at -3e38)
@@ -61,25 +60,23 @@ struct Item {
   int tree;           // which of the two TreeInfo buffers
 };
 
-// Depths and ancestors of a sequence's nodes.
+// Ancestors of a sequence's nodes (a bit each, the node itself among them)
+// and their depths.
 struct TreeInfo {
-  uint32_t seen[kTreeMax][kTreeMax / 32];  // a node's ancestors, and itself
-  int depth[kTreeMax];
+  uint4* seen;
+  int* depth;
 };
 
 // What the producer prepares of an item besides its queries.
 struct ItemInfo {
-  Item it;
-  int row[kRowsMax];     // of each row: head within the item * kTreeMax + node; -1: no row
-  float scale[kRowsMax]; // logit scale, log2 units
-  float near[kNear];     // [head of the item's][distance < n]
+  Item* it;
+  int* row;      // of each row: head within the item * kTreeMax + node; -1: no row
+  float* scale;  // logit scale, log2 units
+  float* near;   // [head of the item's][distance < n] table entries
 };
 
 struct __align__(16) TreeSmem {
-  TreeInfo tree[2];
-  ItemInfo info[2];
-  int jump[kTreeMax];  // scratch of tree_info
-  float2 merge_ml[kRowsMax];
+  Item item[2];
   uint64_t k_full[kMaxStages];   // a slot's K and table windows have arrived
   uint64_t v_full[kMaxStages];   // its V has
   uint64_t s_free[kMaxStages];   // its S and its windows are in registers
@@ -172,27 +169,35 @@ __device__ __forceinline__ int range_owner(int64_t all, int active, int64_t x) {
   return static_cast<int>(((x + 1) * active - 1) / all);
 }
 
-// Depth and ancestors of the n nodes of sequence b, by one warp (four nodes a
-// lane).  Each round doubles the chains that the jump pointers span.  Returns
-// false in a lane that met a parent outside [-1, i).
-__device__ __noinline__ bool tree_info(const CacheArgs& c, int b, int n, TreeInfo& ti, int* jump) {
+// Depth and ancestors of the n nodes of sequence b, by one warp, for `nodes`
+// (a multiple of 32) entries, up to four a lane.  Each round doubles the
+// chains that the jump pointers span.  Returns false in a lane that met a
+// parent outside [-1, i).
+__device__ __noinline__ bool tree_info(const CacheArgs& c, int b, int n, int nodes,
+                                       const TreeInfo& ti, int* jump) {
   constexpr int kPer = kTreeMax / 32;
   const int lane = threadIdx.x & 31;
   bool ok = true, more = false;
+  int par[kPer];
+#pragma unroll
+  for (int x = 0; x < kPer; ++x)
+    par[x] = c.parents && 32 * x + lane < n
+                 ? __ldg(c.parents + static_cast<size_t>(b) * c.N + 32 * x + lane)
+                 : -1;
   __syncwarp();
 #pragma unroll
   for (int x = 0; x < kPer; ++x) {
     const int i = 32 * x + lane;
+    if (32 * x >= nodes) break;
     uint32_t w[kPer];
-    int p = -1, d = 0;
+    int p = par[x], d;
 #pragma unroll
     for (int y = 0; y < kPer; ++y) w[y] = x == y ? 1u << lane : 0u;
     if (!c.parents) {
       d = i;
 #pragma unroll
       for (int y = 0; y < kPer; ++y) w[y] = x > y ? ~0u : x == y ? ~0u >> (31 - lane) : 0u;
-    } else if (i < n) {
-      p = __ldg(c.parents + static_cast<size_t>(b) * c.N + i);
+    } else {
       ok &= p >= -1 && p < i;
       if (p < -1 || p >= i) p = -1;
       d = p >= 0;
@@ -200,7 +205,7 @@ __device__ __noinline__ bool tree_info(const CacheArgs& c, int b, int n, TreeInf
     more |= p >= 0;
     jump[i] = p;
     ti.depth[i] = d;
-    *reinterpret_cast<uint4*>(ti.seen[i]) = make_uint4(w[0], w[1], w[2], w[3]);
+    ti.seen[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __syncwarp();
   while (__any_sync(0xffffffffu, more)) {
@@ -208,6 +213,7 @@ __device__ __noinline__ bool tree_info(const CacheArgs& c, int b, int n, TreeInf
     uint4 v[kPer];
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
+      if (32 * x >= nodes) break;
       const int j = jump[32 * x + lane];
       p[x] = -1;
       dp[x] = 0;
@@ -215,16 +221,17 @@ __device__ __noinline__ bool tree_info(const CacheArgs& c, int b, int n, TreeInf
       if (j >= 0) {
         p[x] = jump[j];
         dp[x] = ti.depth[j];
-        v[x] = *reinterpret_cast<const uint4*>(ti.seen[j]);
+        v[x] = ti.seen[j];
       }
     }
     __syncwarp();
     more = false;
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
+      if (32 * x >= nodes) break;
       const int i = 32 * x + lane;
-      uint4* w = reinterpret_cast<uint4*>(ti.seen[i]);
-      *w = make_uint4(w->x | v[x].x, w->y | v[x].y, w->z | v[x].z, w->w | v[x].w);
+      const uint4 w = ti.seen[i];
+      ti.seen[i] = make_uint4(w.x | v[x].x, w.y | v[x].y, w.z | v[x].z, w.w | v[x].w);
       ti.depth[i] += dp[x];
       jump[i] = p[x];
       more |= p[x] >= 0;
@@ -232,6 +239,9 @@ __device__ __noinline__ bool tree_info(const CacheArgs& c, int b, int n, TreeInf
     __syncwarp();
   }
   return ok;
+}
+__device__ __forceinline__ bool tree_sees(const TreeInfo& ti, int node, int i) {
+  return reinterpret_cast<const uint32_t*>(ti.seen + node)[i >> 5] >> (i & 31) & 1;
 }
 
 __device__ __forceinline__ bool odd_exp(uint32_t half) { return (half & 0x7F80u) == 0x7F80u; }
@@ -312,9 +322,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, DevSta
 
 // Visibility of the 64 keys from j0 on to a node: committed keys, then the
 // bits of its ancestors.
-__device__ __forceinline__ uint64_t tile_mask(const uint32_t* seen, int j0, int len) {
-  const uint64_t lo = static_cast<uint64_t>(seen[1]) << 32 | seen[0];
-  const uint64_t hi = static_cast<uint64_t>(seen[3]) << 32 | seen[2];
+__device__ __forceinline__ uint64_t tile_mask(uint4 seen, int j0, int len) {
+  const uint64_t lo = static_cast<uint64_t>(seen.y) << 32 | seen.x;
+  const uint64_t hi = static_cast<uint64_t>(seen.w) << 32 | seen.z;
   const int i = j0 - len;  // node of the tile's first key
   if (i <= 0) {
     const int k = -i;  // committed keys among them
@@ -369,7 +379,8 @@ struct Shape {
   static_assert(kColP + kPCols * PARTS <= kColO, "Tensor Memory");
 };
 
-// The CTA's shared memory.
+// The CTA's shared memory.  What grows with the nodes of a draft is laid out
+// for the call's N, so that small drafts leave room for the ring.
 extern __shared__ __align__(16) uint8_t tree_smem_raw[];
 struct View {
   uint8_t* sq;  // two query tiles
@@ -377,6 +388,10 @@ struct View {
   uint8_t* sv;  // [stages] tiles of V
   float* win;   // [stages] table windows
   TreeSmem* sm;
+  uint8_t* nodes;   // TreeInfo [2], jump
+  float* near;      // [2][near]
+  int* rows;        // row and scale [2][kRows] each
+  float2* merge_ml; // [128 - kRows]
 };
 template <class S>
 __device__ __forceinline__ View smem_view(const TreeArgs& a) {
@@ -386,7 +401,24 @@ __device__ __forceinline__ View smem_view(const TreeArgs& a) {
   v.sv = v.sk + a.stages * S::kTileBytes;
   v.win = reinterpret_cast<float*>(v.sv + a.stages * S::kTileBytes);
   v.sm = reinterpret_cast<TreeSmem*>(v.win + a.stages * a.win_stage);
+  v.nodes = reinterpret_cast<uint8_t*>(v.sm + 1);
+  v.near = reinterpret_cast<float*>(v.nodes + a.nodes * 44);
+  v.rows = reinterpret_cast<int*>(v.near + 2 * a.near);
+  v.merge_ml = reinterpret_cast<float2*>(v.rows + 4 * S::kRows);
   return v;
+}
+__device__ __forceinline__ TreeInfo tree_view(const TreeArgs& a, const View& v, int which) {
+  return TreeInfo{reinterpret_cast<uint4*>(v.nodes) + which * a.nodes,
+                  reinterpret_cast<int*>(v.nodes + 32 * a.nodes) + which * a.nodes};
+}
+__device__ __forceinline__ int* jump_view(const TreeArgs& a, const View& v) {
+  return reinterpret_cast<int*>(v.nodes + 40 * a.nodes);
+}
+template <class S>
+__device__ __forceinline__ ItemInfo info_view(const TreeArgs& a, const View& v, int k) {
+  const int x = k & 1;
+  return ItemInfo{v.sm->item + x, v.rows + 2 * x * S::kRows,
+                  reinterpret_cast<float*>(v.rows + (2 * x + 1) * S::kRows), v.near + x * a.near};
 }
 
 // What a softmax warp carries from tile to tile.
@@ -408,22 +440,24 @@ struct SoftRow {
   int woff;          // its place in a table window
 };
 template <class S>
-__device__ __forceinline__ SoftRow soft_row(const TreeArgs& a, const TreeSmem& sm, int k) {
-  const ItemInfo& info = sm.info[k & 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = info.it.n;
+__device__ __forceinline__ SoftRow soft_row(const TreeArgs& a, const View& v, int k) {
+  const TreeSmem& sm = *v.sm;
+  const ItemInfo info = info_view<S>(a, v, k);
+  const Item& it = *info.it;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = it.n;
   SoftRow r;
   r.rr = 32 * (warp % S::kGroups) + lane;
   r.copy = warp / S::kGroups;
   r.k0 = r.copy * S::kCols;
   r.lanes = sm.tmem_base + tmem_lane_base(warp);
-  r.warp_live = info.it.r0 + 32 * (warp % S::kGroups) < info.it.r1;
+  r.warp_live = it.r0 + 32 * (warp % S::kGroups) < it.r1;
   const int row = info.row[r.rr];
   r.live = row >= 0;
   r.node = r.live ? row % kTreeMax : 0;
   r.hrel = r.live ? row / kTreeMax : 0;
-  r.depth = sm.tree[info.it.tree].depth[r.node];
+  r.depth = tree_view(a, v, it.tree).depth[r.node];
   r.cs = info.scale[r.rr];
-  r.woff = r.hrel * window_floats(S::kTile, n) + ((a.tab_zero - (info.it.len + n - 1)) & 3) +
+  r.woff = r.hrel * window_floats(S::kTile, n) + ((a.tab_zero - (it.len + n - 1)) & 3) +
            (n - 1 - r.depth) + r.k0;
   return r;
 }
@@ -493,7 +527,7 @@ __device__ __forceinline__ void soft_finish(const TreeArgs& a, TreeSmem& sm, con
     st.phase ^= 1;
   }
   ++st.g;
-  ++st.t;
+  --st.t;
   st.first = false;
 }
 // Two weights and their bf16 parts; l2 gathers the exact ones.
@@ -578,9 +612,9 @@ __device__ __forceinline__ void soft_tail(const TreeArgs& a, const View& v, cons
   TreeSmem& sm = *v.sm;
   volatile int* ab = &sm.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const ItemInfo& info = sm.info[k & 1];
-  const TreeInfo& ti = sm.tree[info.it.tree];
-  const int n = info.it.n, len = info.it.len, j0 = st.t * S::kTile;
+  const ItemInfo info = info_view<S>(a, v, k);
+  const TreeInfo ti = tree_view(a, v, info.it->tree);
+  const int n = info.it->n, len = info.it->len, j0 = st.t * S::kTile;
   if (!soft_begin(a, sm, st)) return;
   const float* w = v.win + st.s * a.win_stage + row.woff;
   const float* near = info.near + row.hrel * n + row.depth;  // of an ancestor: near[-its depth]
@@ -595,7 +629,7 @@ __device__ __forceinline__ void soft_tail(const TreeArgs& a, const View& v, cons
       for (int h = 0; h < 2; ++h) {
         const int kk = 16 * q + 2 * y + h, i = j0 + row.k0 + kk - len;
         // Loads of keys out of sight stay in range and are not used.
-        const int back = min(ti.depth[min(max(i, 0), kTreeMax - 1)], row.depth);
+        const int back = min(ti.depth[min(max(i, 0), n - 1)], row.depth);
         const float bias = i < 0 ? w[kk] : near[-back];
         const float x = fmaf(__uint_as_float(sv[2 * y + h]), row.cs, bias);
         e[h] = vis >> kk & 1 ? x : -INFINITY;
@@ -679,14 +713,14 @@ __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const
   const CacheArgs& c = a.c;
   volatile int* ab = &sm.abort_flag;
   const int lane = threadIdx.x & 31;
-  const ItemInfo& info = sm.info[k & 1];
-  const TreeInfo& ti = sm.tree[info.it.tree];
-  const int n = info.it.n, hk = info.it.hk, bb = info.it.b, t0 = info.it.t0;
+  const Item& it = sm.item[k & 1];
+  const TreeInfo ti = tree_view(a, v, it.tree);
+  const int n = it.n, hk = it.hk, bb = it.b, t0 = it.t0;
   if (!warp_wait(&sm.pv_done, (st.g - 1) & 1, c.status, ab, kSiteTreeSoftEnd)) return false;
   tc_fence_after();
-  const bool whole = t0 == 0 && info.it.t1 == info.it.tiles;
+  const bool whole = t0 == 0 && it.t1 == it.tiles;
   const size_t orow =
-      (static_cast<size_t>(bb) * a.H + hk * a.group + info.it.r0 / n + row.hrel) * c.N + row.node;
+      (static_cast<size_t>(bb) * a.H + hk * a.group + it.r0 / n + row.hrel) * c.N + row.node;
   const size_t prow = static_cast<size_t>(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * S::kRows + row.rr;
   const uint32_t* odd = sm.odd[k & 1];
   const bool any_odd = (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
@@ -694,7 +728,7 @@ __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const
   float M = st.m, L = st.l, f[KS];
   f[0] = 1.0f;
   if (KS > 1 && row.copy > 0 && row.warp_live)
-    sm.merge_ml[(row.copy - 1) * S::kRows + row.rr] = make_float2(st.m, st.l);
+    v.merge_ml[(row.copy - 1) * S::kRows + row.rr] = make_float2(st.m, st.l);
 #pragma unroll 1
   for (int q = 0; q < 4; ++q) {
     uint32_t ov[16];
@@ -719,12 +753,12 @@ __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const
         if (!warp_wait(&sm.merge_full, q >> 1, c.status, ab, kSiteTreeMerge)) return false;
         if (q == 0 && row.copy == 0 && row.live) {
 #pragma unroll
-          for (int y = 1; y < KS; ++y) M = fmaxf(M, sm.merge_ml[(y - 1) * S::kRows + row.rr].x);
+          for (int y = 1; y < KS; ++y) M = fmaxf(M, v.merge_ml[(y - 1) * S::kRows + row.rr].x);
           f[0] = ex2_approx(st.m - M);
           L *= f[0];
 #pragma unroll
           for (int y = 1; y < KS; ++y) {
-            const float2 ml = sm.merge_ml[(y - 1) * S::kRows + row.rr];
+            const float2 ml = v.merge_ml[(y - 1) * S::kRows + row.rr];
             f[y] = ex2_approx(ml.x - M);
             L += ml.y * f[y];
           }
@@ -759,8 +793,8 @@ __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const
       // Values that are not finite, for the nodes that see them.
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
-        if (!(odd[i >> 5] >> (i & 31) & 1) || !(ti.seen[row.node][i >> 5] >> (i & 31) & 1)) continue;
-        const int slot = info.it.len + i;
+        if (!(odd[i >> 5] >> (i & 31) & 1) || !tree_sees(ti, row.node, i)) continue;
+        const int slot = it.len + i;
         int pg = __ldg(c.block_table + static_cast<size_t>(bb) * c.max_blocks + slot / c.page);
         if (pg < 0 || pg >= c.num_pages) pg = 0;
         const uint32_t* vr = reinterpret_cast<const uint32_t*>(
@@ -917,7 +951,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     }
     int issued = 0, s = 0, phase = 1, k = 0, last_b = -1, tree = 1;
     for (;; ++k) {
-      ItemInfo& info = sm.info[k & 1];
+      const ItemInfo info = info_view<S>(a, v, k);
       if (!ok) break;
       Item it;
       it.t0 = it.t1 = 0;
@@ -956,10 +990,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const float* trow = a.table + static_cast<size_t>(it.hk * a.group + g0) * a.tab_len;
       const int y0 = a.tab_zero - (len + n - 1);  // entry of key 0 for the last position
       const int nwin = window_floats(kTile, n);
-      // Tiles are issued as slots are free; `wait` waits for them.
-      int t = it.t0, pages = 0;
+      // Tiles are issued as slots are free; `wait` waits for them.  The last
+      // tiles come first: where the prior falls off with distance, as it mostly
+      // does, the first tiles then hold the largest logits, and O is hardly
+      // ever rescaled.
+      int t = it.t1 - 1, pages = 0;
       auto issue_tiles = [&](bool wait) {
-        for (; t < it.t1; ++t) {
+        for (; t >= it.t0; --t) {
           if (issued >= a.stages) {
             if (!wait) {
               const bool free = mbar_test(&sm.s_free[s], phase) && mbar_test(&sm.v_empty[s], phase);
@@ -970,12 +1007,12 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             }
           }
           constexpr int kBoxes = kTile / kBox, kAhead = 32 / kBoxes;
-          const int ahead = (t - it.t0) % kAhead;
+          const int ahead = (it.t1 - 1 - t) % kAhead;
           if (ahead == 0) {
             // page numbers of the boxes of the next tiles, one a lane
-            const int key = t * kTile + lane * kBox;
+            const int tl = t - lane / kBoxes, key = tl * kTile + lane % kBoxes * kBox;
             pages = 0;
-            if (key < min(it.t1 * kTile, len + n)) {
+            if (tl >= it.t0 && key < len + n) {
               pages = __ldg(c.block_table + static_cast<size_t>(it.b) * c.max_blocks + key / c.page);
               if (pages < 0 || pages >= c.num_pages) {
                 args_ok = false;
@@ -1035,7 +1072,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       if (!ok) break;
       if (it.t1 == 0) {
         if (lane == 0) {
-          info.it = it;
+          *info.it = it;
           mbar_arrive(&sm.item_full[k & 1]);
         }
         break;
@@ -1069,7 +1106,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       }
       if (it.b != last_b) {
         tree ^= 1;
-        args_ok &= tree_info(c, it.b, n, sm.tree[tree], sm.jump);
+        args_ok &= tree_info(c, it.b, n, a.nodes, tree_view(a, v, tree), jump_view(a, v));
         last_b = it.b;
       }
       it.tree = tree;
@@ -1081,11 +1118,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         float sc = 0.125f * static_cast<float>(kLog2e);
         if (a.ssmax)
           sc *= __ldg(a.s + it.hk * a.group + hg) *
-                logf(static_cast<float>(len + sm.tree[tree].depth[node] + 1));
+                logf(static_cast<float>(len + tree_view(a, v, tree).depth[node] + 1));
         info.row[rr] = live ? (hg - g0) * kTreeMax + node : -1;
         info.scale[rr] = sc;
       }
-      if (lane == 0) info.it = it;
+      if (lane == 0) *info.it = it;
       if (lane < kTreeMax / 32) sm.odd[k & 1][lane] = 0;
       cp_async_wait();
       fence_proxy_async_smem();
@@ -1133,7 +1170,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         p.first = true;
         ok = ok && tree_wait(&sm.item_full[p.k & 1], (p.k >> 1) & 1, c.status, ab, kSiteTreeMmaItem);
         if (!ok) return false;
-        const Item& it = sm.info[p.k & 1].it;
+        const Item& it = sm.item[p.k & 1];
         p.left = it.t1 - it.t0;
         return it.t1 > 0;
       };
@@ -1196,17 +1233,16 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     for (int k = 0;; ++k) {
       st.ok = warp_wait(&sm.item_full[k & 1], (k >> 1) & 1, c.status, ab, kSiteTreeSoftItem);
       if (!st.ok) break;
-      const ItemInfo& info = sm.info[k & 1];
-      const int t1 = info.it.t1;
-      if (t1 == 0) break;
-      st.t = info.it.t0;
+      const Item& it = sm.item[k & 1];
+      const int t0 = it.t0, plain = it.len / S::kTile;  // tiles without drafted keys
+      st.t = it.t1 - 1;
+      if (st.t < 0) break;
       st.m = kNoMax;
       st.l = 0.0f;
       st.first = true;
-      const SoftRow row = soft_row<S>(a, sm, k);
-      for (const int plain = min(t1, info.it.len / S::kTile); st.ok && st.t < plain;)
-        soft_tile<PARTS, KS>(a, v, row, st);
-      while (st.ok && st.t < t1) soft_tail<PARTS, KS>(a, v, row, st, k);
+      const SoftRow row = soft_row<S>(a, v, k);
+      while (st.ok && st.t >= max(plain, t0)) soft_tail<PARTS, KS>(a, v, row, st, k);
+      while (st.ok && st.t >= t0) soft_tile<PARTS, KS>(a, v, row, st);
       if (!st.ok || !soft_end<PARTS, KS>(a, v, row, st, k)) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
@@ -1288,8 +1324,8 @@ constexpr size_t kSmemOne = 227 * 1024;
 
 // Shared memory of a CTA besides its ring stages, and of one stage.
 size_t smem_fixed(const TreeArgs& a) {
-  (void)a;
-  return 1024 + 2 * kQBytes + sizeof(TreeSmem);
+  return 1024 + 2 * kQBytes + sizeof(TreeSmem) + 44 * static_cast<size_t>(a.nodes) +
+         8 * static_cast<size_t>(a.near) + 16 * a.rows + 8 * (kRowsMax - a.rows);
 }
 size_t smem_stage(const TreeArgs& a) {
   return 2 * static_cast<size_t>(a.tile) * kHeadDim * 2 + static_cast<size_t>(a.win_stage) * 4;
@@ -1326,12 +1362,14 @@ cudaError_t launch_parts(const CUtensorMap& tk, const CUtensorMap& tv, const Tre
 bool tree_config(TreeArgs* a, int sms) {
   a->tile = tree_tile(a->o_fp32 ? 3 : 1, kRowsMax / a->rows);
   // Most heads and floats that a stage's windows hold, over the node counts.
-  a->win_stage = 0;
+  a->win_stage = a->near = 0;
+  a->nodes = (a->c.N + 31) & ~31;
   for (int n = 1; n <= a->c.N; ++n) {
     int heads = (a->rows + n - 2) / n + 1;
     if (heads > a->group) heads = a->group;
     const int floats = heads * window_floats(a->tile, n);
     if (floats > a->win_stage) a->win_stage = floats;
+    if (heads * n > a->near) a->near = (heads * n + 3) & ~3;
   }
   const size_t fixed = smem_fixed(*a), stage = smem_stage(*a);
   int per_sm = 2;

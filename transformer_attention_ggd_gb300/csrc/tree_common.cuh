@@ -74,6 +74,7 @@ struct TreeArgs {
   int ctas, least;    // CTAs of the launch; units that one gets at least
   int stages;         // ring stages
   int win_stage;      // floats of a stage's table windows
+  int nodes, near;    // nodes (a multiple of 32) and table entries that an item keeps
 };
 
 // Rows of an item for `rows` (head, node) pairs.
