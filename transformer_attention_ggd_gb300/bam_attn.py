@@ -115,6 +115,8 @@ class BamRope(ctypes.Structure):
     ]
 
 
+_Strides9 = ctypes.c_int64 * 9
+
 _lib = None
 _lock = threading.Lock()
 
@@ -122,6 +124,8 @@ _lock = threading.Lock()
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libbam_attn.so and declare its signatures (no GPU needed)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -477,7 +481,7 @@ def _cache_specs(k_pages, v_pages, block_table, cache_lens, draft_lens, parents,
         raise ValueError("k_pages must be [num_pages, Hkv, page, 64] and block_table "
                          "[B, max_blocks]")
     bf, _, _, i32 = _dt()
-    pages = k_pages.shape[:3] + (64,)
+    pages = tuple(k_pages.shape[:3]) + (64,)
     return (("k_pages", k_pages, pages, bf, False), ("v_pages", v_pages, pages, bf, False),
             ("block_table", block_table, (B, block_table.shape[1]), i32, False),
             ("cache_lens", cache_lens, (B,), i32, False),
@@ -489,6 +493,8 @@ def _check_rows(t, name, shape, device):
     """A bf16 input whose rows of 64 are contiguous and 16-byte aligned; the
     other strides are free."""
     import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != torch.bfloat16:
@@ -499,6 +505,56 @@ def _check_rows(t, name, shape, device):
         raise ValueError(f"{name} must have contiguous, 16-byte aligned rows")
 
 
+# A decoding step calls these operators once per layer and token, and a call of
+# theirs lasts a few microseconds on the GPU: the checks of a call in order are
+# a handful of attribute reads per tensor, and only a call that fails them goes
+# through the detailed ones above, which say what is wrong.
+
+def _raw_stream(stream, index):
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _plain(index, dtype, shape, *tensors):
+    """Every tensor is contiguous, on CUDA device `index`, of this dtype and shape."""
+    for t in tensors:
+        if not (t.dtype is dtype and t.get_device() == index and t.shape == shape
+                and t.is_contiguous()):
+            return False
+    return True
+
+
+def _cache_ok(index, k_pages, v_pages, block_table, cache_lens, draft_lens, parents, ws, B, N):
+    import torch
+    i32 = torch.int32
+    return (_plain(index, torch.bfloat16, k_pages.shape, k_pages, v_pages)
+            and k_pages.shape[3] == 64 and block_table.dim() == 2
+            and _plain(index, i32, (B, block_table.shape[1]), block_table)
+            and _plain(index, i32, (B,), cache_lens)
+            and (draft_lens is None or _plain(index, i32, (B,), draft_lens))
+            and (parents is None or _plain(index, i32, (B, N), parents))
+            and ws.dim() == 1 and _plain(index, torch.uint8, ws.shape, ws))
+
+
+def _rows_ok(index, shape, t):
+    import torch
+    if t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape:
+        return False
+    a, b, c, d = t.stride()
+    return d == 1 and not (a | b | c) & 7 and not t.data_ptr() & 15
+
+
+def _current_device():
+    import torch
+    return torch._C._cuda_getDevice()
+
+
 def bam_kv_append_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_lens, parents, q,
                         q_out, rope, ws, stream=None, check=True) -> None:
     """Append k, v [B, Hkv, N, 64] (any batch, head and token strides) to the
@@ -507,29 +563,47 @@ def bam_kv_append_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_len
     each sequence; parents int32 [B, N] or None: the tree that positions
     follow; q [B, H, N, 64] -> q_out (contiguous) or both None: queries rotated
     on the way; rope: make_rope(...) or None."""
-    B, Hkv, N, D = k.shape
-    num_pages, _, page, _ = k_pages.shape
-    H = q.shape[1] if q is not None else Hkv
+    B, Hkv, N, D = shape = k.shape
+    num_pages, pool_heads, page, _ = k_pages.shape
+    index = k.get_device()
+    H = Hkv
+    strides = k.stride()[:3] + v.stride()[:3]
+    if q is not None:
+        H = q.shape[1]
+        strides += q.stride()[:3]
     if check:
-        dev = _device(k, "k")
-        bf = _dt()[0]
-        _check_rows(k, "k", (B, k_pages.shape[1], N, 64), dev)
-        _check_rows(v, "v", k.shape, dev)
-        if (q is None) != (q_out is None):
-            raise ValueError("q and q_out go together")
-        if q is not None:
-            _check_rows(q, "q", (B, H, N, 64), dev)
-        _check_tensors(_cache_specs(k_pages, v_pages, block_table, cache_lens, new_lens, parents,
-                                    B, N)
-                       + (("q_out", q_out, (B, H, N, 64), bf, True),), dev)
-        _check_ws(ws, dev)
-    strides = k.stride()[:3] + v.stride()[:3] + (q.stride()[:3] if q is not None else (0, 0, 0))
+        import torch
+        try:
+            ok = (index >= 0 and index == _current_device() and D == 64 and pool_heads == Hkv
+                  and _rows_ok(index, shape, k) and _rows_ok(index, shape, v)
+                  and (q is None) == (q_out is None)
+                  and (q is None or (_rows_ok(index, (B, H, N, 64), q)
+                                     and _plain(index, torch.bfloat16, (B, H, N, 64), q_out)))
+                  and _cache_ok(index, k_pages, v_pages, block_table, cache_lens, new_lens,
+                                parents, ws, B, N))
+        except AttributeError:
+            ok = False
+        if not ok:
+            dev = _device(k, "k")
+            _check_rows(k, "k", (B, pool_heads, N, 64), dev)
+            _check_rows(v, "v", shape, dev)
+            if (q is None) != (q_out is None):
+                raise ValueError("q and q_out go together")
+            if q is not None:
+                _check_rows(q, "q", (B, H, N, 64), dev)
+            _check_tensors(_cache_specs(k_pages, v_pages, block_table, cache_lens, new_lens,
+                                        parents, B, N)
+                           + (("q_out", q_out, (B, H, N, 64), _dt()[0], True),), dev)
+            _check_ws(ws, dev)
+            raise ValueError("argument check failed")
     st = load_library().bam_kv_append_paged(
-        _ptr(k), _ptr(v), _ptr(q), _ptr(q_out), (ctypes.c_int64 * 9)(*strides), _ptr(k_pages),
-        _ptr(v_pages), _ptr(block_table), _ptr(cache_lens), _ptr(new_lens), _ptr(parents), B, H,
-        Hkv, N, page, block_table.shape[1], num_pages, D,
-        None if rope is None else ctypes.byref(rope), _ptr(ws), ws.numel(), _stream(stream))
-    _check(st, "bam_kv_append_paged")
+        k.data_ptr(), v.data_ptr(), _address(q), _address(q_out),
+        _Strides9(*strides), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+        cache_lens.data_ptr(), _address(new_lens), _address(parents), B, H, Hkv, N, page,
+        block_table.shape[1], num_pages, D, None if rope is None else ctypes.byref(rope),
+        ws.data_ptr(), ws.numel(), _raw_stream(stream, index))
+    if st:
+        _check(st, "bam_kv_append_paged")
 
 
 def bam_attn_decode_tree_paged(q, k_pages, v_pages, block_table, cache_lens, draft_lens, parents,
@@ -539,23 +613,42 @@ def bam_attn_decode_tree_paged(q, k_pages, v_pages, block_table, cache_lens, dra
     [B] (committed keys); draft_lens int32 [B] or None (N each); parents int32
     [B, N] or None (a chain); lse [B, H, N] or None."""
     import torch
-    B, H, N, D = q.shape
+    B, H, N, D = shape = q.shape
     num_pages, Hkv, page, _ = k_pages.shape
+    index = q.get_device()
+    out = o.dtype
     if check:
-        dev = _device(q)
-        bf, f32, out, _ = _dt()
-        _check_tensors((("q", q, (B, H, N, 64), bf, False), ("o", o, (B, H, N, 64), out, False),
-                        ("lse", lse, (B, H, N), f32, True))
-                       + _cache_specs(k_pages, v_pages, block_table, cache_lens, draft_lens,
-                                      parents, B, N) + _param_specs(params, H), dev)
-        _check_ws(ws, dev)
-    o_fp32 = 1 if o.dtype == torch.float32 else 0
+        f32 = torch.float32
+        try:
+            prm = getattr(params, "tensors", None)
+            ok = (index >= 0 and index == _current_device() and D == 64
+                  and (out is torch.bfloat16 or out is f32)
+                  and _plain(index, torch.bfloat16, shape, q) and _plain(index, out, shape, o)
+                  and (lse is None or _plain(index, f32, (B, H, N), lse))
+                  and (prm is None or (_plain(index, f32, (H,), prm[0], prm[1], prm[2])
+                                       and (prm[3] is None or _plain(index, f32, (H,), prm[3]))))
+                  and _cache_ok(index, k_pages, v_pages, block_table, cache_lens, draft_lens,
+                                parents, ws, B, N))
+        except AttributeError:
+            ok = False
+        if not ok:
+            dev = _device(q)
+            bf, f32s, outs, _ = _dt()
+            _check_tensors((("q", q, (B, H, N, 64), bf, False),
+                            ("o", o, (B, H, N, 64), outs, False),
+                            ("lse", lse, (B, H, N), f32s, True))
+                           + _cache_specs(k_pages, v_pages, block_table, cache_lens, draft_lens,
+                                          parents, B, N) + _param_specs(params, H), dev)
+            _check_ws(ws, dev)
+            raise ValueError("argument check failed")
     st = load_library().bam_attn_decode_tree_paged(
-        _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(cache_lens),
-        _ptr(draft_lens), _ptr(parents), _ptr(o), o_fp32, _ptr(lse), B, H, Hkv, N, page,
-        block_table.shape[1], num_pages, D, ctypes.byref(params), _ptr(ws), ws.numel(),
-        _stream(stream))
-    _check(st, "bam_attn_decode_tree_paged")
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+        cache_lens.data_ptr(), _address(draft_lens), _address(parents), o.data_ptr(),
+        1 if out is torch.float32 else 0, _address(lse), B, H, Hkv, N, page,
+        block_table.shape[1], num_pages, D, ctypes.byref(params), ws.data_ptr(), ws.numel(),
+        _raw_stream(stream, index))
+    if st:
+        _check(st, "bam_attn_decode_tree_paged")
 
 
 def bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, parents, accepted,
@@ -565,21 +658,34 @@ def bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, par
     num_pages, Hkv, page, D = k_pages.shape
     B = block_table.shape[0]
     N = parents.shape[1] if parents is not None else BAM_TREE_MAX_NODES
+    index = k_pages.get_device()
+    if parents is None and draft_lens is None:
+        raise ValueError("draft_lens is required without parents")
     if check:
-        dev = _device(k_pages, "k_pages")
-        i32 = _dt()[3]
-        if parents is None and draft_lens is None:
-            raise ValueError("draft_lens is required without parents")
-        _check_tensors(_cache_specs(k_pages, v_pages, block_table, cache_lens, draft_lens, parents,
-                                    B, N)
-                       + (("accepted", accepted, (B,), i32, False),
-                          ("new_lens", new_lens, (B,), i32, False)), dev)
-        _check_ws(ws, dev)
+        import torch
+        try:
+            ok = (index >= 0 and index == _current_device()
+                  and _plain(index, torch.int32, (B,), accepted, new_lens)
+                  and _cache_ok(index, k_pages, v_pages, block_table, cache_lens, draft_lens,
+                                parents, ws, B, N))
+        except AttributeError:
+            ok = False
+        if not ok:
+            dev = _device(k_pages, "k_pages")
+            i32 = _dt()[3]
+            _check_tensors(_cache_specs(k_pages, v_pages, block_table, cache_lens, draft_lens,
+                                        parents, B, N)
+                           + (("accepted", accepted, (B,), i32, False),
+                              ("new_lens", new_lens, (B,), i32, False)), dev)
+            _check_ws(ws, dev)
+            raise ValueError("argument check failed")
     st = load_library().bam_kv_keep_paged(
-        _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(cache_lens), _ptr(draft_lens),
-        _ptr(parents), _ptr(accepted), _ptr(new_lens), B, Hkv, N, page, block_table.shape[1],
-        num_pages, D, _ptr(ws), ws.numel(), _stream(stream))
-    _check(st, "bam_kv_keep_paged")
+        k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(),
+        _address(draft_lens), _address(parents), accepted.data_ptr(), new_lens.data_ptr(), B, Hkv,
+        N, page, block_table.shape[1], num_pages, D, ws.data_ptr(), ws.numel(),
+        _raw_stream(stream, index))
+    if st:
+        _check(st, "bam_kv_keep_paged")
 
 
 def bam_attn_selftest_wait(ws, stream=None) -> None:
