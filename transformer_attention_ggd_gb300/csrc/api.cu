@@ -468,10 +468,14 @@ bam_status bam_kv_append_paged(const void* k, const void* v, const void* q, void
       return BAM_ERR_INVALID_ARG;
     a.dims = rope->dims;
     a.interleaved = rope->interleaved;
-    for (int f = 0; f < rope->dims / 2; ++f) {
-      double turns = std::pow(rope->base, -2.0 * f / rope->dims) / 6.283185307179586477;
-      turns -= std::floor(turns);  // only the fraction of a turn per position matters
-      if (!(turns < 1.0)) turns = 0.0;
+    // base^(-2 f / dims) by repeated products: their 2^-48 is 2^-23 turns at
+    // position 2^28.
+    const double ratio = std::pow(rope->base, -2.0 / rope->dims);
+    double per = 1.0 / 6.283185307179586477;
+    for (int f = 0; f < rope->dims / 2; ++f, per *= ratio) {
+      // Only the fraction of a turn per position matters.
+      double turns = per - std::floor(per);
+      if (!(turns < 1.0)) turns = 0.0;  // also when base is extreme
       a.freq[f] = static_cast<uint64_t>(turns * 18446744073709551616.0);
     }
   }

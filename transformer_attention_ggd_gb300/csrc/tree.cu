@@ -912,13 +912,15 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   const uint32_t tm = sm.tmem_base;
   // The plan, the table and the status words come from the previous kernel
   // (a wait that looks at an abort word before it is cleared would give up).
-  grid_dep_wait();
+  // With few sequences the producer makes the plan itself, and its first loads
+  // of keys and queries, which no kernel of the call writes, do not wait.
   grid_dep_trigger();
+  if (warp != kProducer || c.B > 32) grid_dep_wait();
 
   if (warp == kProducer) {
     // ---------------------------------------------------------------- producer
-    bool ok = *reinterpret_cast<volatile int*>(&c.status->abort) == 0;
-    bool args_ok = true;
+    bool ok = true, args_ok = true;
+    bool early = c.B <= 32;  // the previous kernel has not been waited for
     // 32 sequences a time, one a lane: where they begin and end, their lengths.
     int b = 0, b0 = 0, len_l = 0, n_l = 0;
     int64_t beg_l = 0, end_l = 0;
@@ -928,15 +930,30 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       end_l = __ldcg(a.plan + y + 1);
       cache_lengths(c, y, &len_l, &n_l);
     };
-    if (c.B <= 32) fetch();
-    const int64_t all = __ldcg(a.plan + c.B);
+    int64_t all;
+    if (early) {
+      if (lane < c.B) cache_lengths(c, lane, &len_l, &n_l);
+      end_l = n_l > 0 ? static_cast<int64_t>(c.Hkv) * ((a.group * n_l + kRows - 1) / kRows) *
+                            ((len_l + n_l + kTile - 1) / kTile + kItemCost)
+                      : 0;
+      beg_l = end_l;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, end_l, off);
+        if (lane >= off) end_l += y;
+      }
+      beg_l = end_l - beg_l;
+      all = __shfl_sync(0xffffffffu, end_l, 31);
+    } else {
+      all = __ldcg(a.plan + c.B);
+    }
     const int active = active_ctas(all, a.ctas, a.least), cta = blockIdx.x;
     int64_t x = 0, end = 0;
     if (all > 0 && cta < active) {
       x = range_beg(all, active, cta);
       end = range_beg(all, active, cta + 1);
     }
-    if (c.B > 32 && x < end) {
+    if (!early && x < end) {
       // The sequence that unit x lies in: how many end at or before it.
       int hi = c.B;
       while (hi - b > 32) {
@@ -990,6 +1007,16 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const float* trow = a.table + static_cast<size_t>(it.hk * a.group + g0) * a.tab_len;
       const int y0 = a.tab_zero - (len + n - 1);  // entry of key 0 for the last position
       const int nwin = window_floats(kTile, n);
+      // The table windows of tile t into slot sl.
+      auto issue_windows = [&](int t, int sl) {
+        for (int g = lane; g < heads; g += 32) {
+          const float* tr = trow + static_cast<size_t>(g) * a.tab_len;
+          ok &= bulk_load_checked(win + sl * a.win_stage + g * nwin, tr + ((y0 + t * kTile) & ~3),
+                                  nwin * 4, &sm.k_full[sl], tr, tr + a.tab_len, c.status, ab,
+                                  kSiteTreeTable);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      };
       // Tiles are issued as slots are free; `wait` waits for them.  The last
       // tiles come first: where the prior falls off with distance, as it mostly
       // does, the first tiles then hold the largest logits, and O is hardly
@@ -1036,13 +1063,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
                             (t * kTile + x2 * kBox) % c.page, plane[x2]);
           }
           __syncwarp();
-          for (int g = lane; g < heads; g += 32) {
-            const float* tr = trow + static_cast<size_t>(g) * a.tab_len;
-            ok &= bulk_load_checked(win + s * a.win_stage + g * nwin, tr + ((y0 + t * kTile) & ~3),
-                                    nwin * 4, &sm.k_full[s], tr, tr + a.tab_len, c.status, ab,
-                                    kSiteTreeTable);
-          }
-          ok = __all_sync(0xffffffffu, ok);
+          if (!early) issue_windows(t, s);
           if (ok && wait && issued >= a.stages)
             ok = warp_wait(&sm.v_empty[s], phase, c.status, ab, kSiteTreeProducer);
           // (after a give-up the slot's V copy is still armed, so that the
@@ -1071,6 +1092,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       }
       if (!ok) break;
       if (it.t1 == 0) {
+        if (early) grid_dep_wait();
+        early = false;
         if (lane == 0) {
           *info.it = it;
           mbar_arrive(&sm.item_full[k & 1]);
@@ -1097,6 +1120,17 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           for (node += 4; node >= n; node -= n) ++hg;
         }
       }
+      if (it.b != last_b) {
+        tree ^= 1;
+        args_ok &= tree_info(c, it.b, n, a.nodes, tree_view(a, v, tree), jump_view(a, v));
+        last_b = it.b;
+      }
+      it.tree = tree;
+      if (early) {
+        grid_dep_wait();
+        early = false;
+        for (int i = 0; i < issued; ++i) issue_windows(it.t1 - 1 - i, i);
+      }
       // Some tile holds drafted keys: their distances' table entries.
       if (it.t1 * kTile > len) {
         for (int h = 0; h < heads; ++h)
@@ -1104,12 +1138,6 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             cp_async4(smem_u32(info.near + h * n + y),
                       trow + static_cast<size_t>(h) * a.tab_len + a.tab_zero - y);
       }
-      if (it.b != last_b) {
-        tree ^= 1;
-        args_ok &= tree_info(c, it.b, n, a.nodes, tree_view(a, v, tree), jump_view(a, v));
-        last_b = it.b;
-      }
-      it.tree = tree;
 #pragma unroll
       for (int rr = lane; rr < kRows; rr += 32) {
         const int r = it.r0 + rr;
