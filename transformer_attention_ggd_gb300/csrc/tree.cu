@@ -145,13 +145,16 @@ __global__ void __launch_bounds__(256) bam_tree_prep_kernel(const TreeArgs a) {
   far = __reduce_max_sync(0xffffffffu, far);
   if ((tid & 31) == 0) atomicMax(&most, far);
   __syncthreads();
-  const int d = blockIdx.x * 256 + tid;
-  const int h = blockIdx.y;
-  if (d > min(most, a.tab_zero)) return;
-  float b, g1, g2;
-  bias_terms<false>(d, a.alpha[h], a.beta[h], a.mu[h], a.eps, a.prior, &b, &g1, &g2);
-  a.table[static_cast<size_t>(h) * a.tab_len + a.tab_zero - d] =
-      to_f32_finite(b * static_cast<float>(kLog2e));
+  const int far_d = min(most, a.tab_zero);  // farthest distance
+  for (int h = blockIdx.y; h < a.H; h += gridDim.y) {
+    const float al = __ldg(a.alpha + h), be = __ldg(a.beta + h), mu = __ldg(a.mu + h);
+    float* row = a.table + static_cast<size_t>(h) * a.tab_len + a.tab_zero;
+    for (int d = blockIdx.x * 256 + tid; d <= far_d; d += gridDim.x * 256) {
+      float b, g1, g2;
+      bias_terms<false>(d, al, be, mu, a.eps, a.prior, &b, &g1, &g2);
+      row[-d] = to_f32_finite(b * static_cast<float>(kLog2e));
+    }
+  }
 }
 
 // ---------------------------------------------------------------- walking the plan
@@ -161,29 +164,38 @@ __device__ __forceinline__ int active_ctas(int64_t all, int ctas, int least) {
   const int64_t n = (all + least - 1) / least;
   return n < 1 ? 1 : n < ctas ? static_cast<int>(n) : ctas;
 }
+// (A 64-bit division is a hundred instructions; all * cta fits 32 bits in all
+// but the largest calls.)
 __device__ __forceinline__ int64_t range_beg(int64_t all, int active, int cta) {
+  if (all < (1 << 22))
+    return static_cast<uint32_t>(all) * static_cast<uint32_t>(cta) / static_cast<uint32_t>(active);
   return all * cta / active;
 }
 // The CTA whose range holds unit x.
 __device__ __forceinline__ int range_owner(int64_t all, int active, int64_t x) {
+  if (all < (1 << 22))
+    return static_cast<int>((static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(active) - 1) /
+                            static_cast<uint32_t>(all));
   return static_cast<int>(((x + 1) * active - 1) / all);
 }
 
-// Depth and ancestors of the n nodes of sequence b, by one warp, for `nodes`
-// (a multiple of 32) entries, up to four a lane.  Each round doubles the
-// chains that the jump pointers span.  Returns false in a lane that met a
-// parent outside [-1, i).
-__device__ __noinline__ bool tree_info(const CacheArgs& c, int b, int n, int nodes,
-                                       const TreeInfo& ti, int* jump) {
-  constexpr int kPer = kTreeMax / 32;
+constexpr int kPer = kTreeMax / 32;  // nodes of a lane
+
+// This lane's parents: of nodes lane, lane + 32, ... (-1 behind node n - 1).
+__device__ __forceinline__ void tree_parents(const CacheArgs& c, int b, int n, int* par) {
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) {
+    const int i = 32 * x + (threadIdx.x & 31);
+    par[x] = c.parents && i < n ? __ldg(c.parents + static_cast<size_t>(b) * c.N + i) : -1;
+  }
+}
+// Depth and ancestors of a sequence's nodes, by one warp, for `nodes` (a
+// multiple of 32) entries.  Each round doubles the chains that the jump
+// pointers span.  Returns false in a lane that met a parent outside [-1, i).
+__device__ __forceinline__ bool tree_info(bool chain, const int* par, int nodes,
+                                          const TreeInfo& ti, int* jump) {
   const int lane = threadIdx.x & 31;
   bool ok = true, more = false;
-  int par[kPer];
-#pragma unroll
-  for (int x = 0; x < kPer; ++x)
-    par[x] = c.parents && 32 * x + lane < n
-                 ? __ldg(c.parents + static_cast<size_t>(b) * c.N + 32 * x + lane)
-                 : -1;
   __syncwarp();
 #pragma unroll
   for (int x = 0; x < kPer; ++x) {
@@ -193,7 +205,7 @@ __device__ __noinline__ bool tree_info(const CacheArgs& c, int b, int n, int nod
     int p = par[x], d;
 #pragma unroll
     for (int y = 0; y < kPer; ++y) w[y] = x == y ? 1u << lane : 0u;
-    if (!c.parents) {
+    if (chain) {
       d = i;
 #pragma unroll
       for (int y = 0; y < kPer; ++y) w[y] = x > y ? ~0u : x == y ? ~0u >> (31 - lane) : 0u;
@@ -989,7 +1001,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         const int64_t local = x - __shfl_sync(0xffffffffu, beg_l, b - b0);
         it.tiles = (it.len + it.n + kTile - 1) / kTile;
         const int unit = it.tiles + kItemCost;
-        const int idx = static_cast<int>(local / unit);
+        const int idx = local < (1 << 30) ? static_cast<int>(local) / unit
+                                          : static_cast<int>(local / unit);
         const int at = static_cast<int>(local - static_cast<int64_t>(idx) * unit);
         const int nrb = (a.group * it.n + kRows - 1) / kRows;
         it.hk = idx / nrb;
@@ -1085,6 +1098,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           if (!ok) return;
         }
       };
+      // What the item's preparation needs is on its way while tiles are issued.
+      int par[kPer];
+      if (it.t1 && it.b != last_b) tree_parents(c, it.b, n, par);
+      const float s_lane =
+          a.ssmax && lane < heads ? __ldg(a.s + it.hk * a.group + g0 + lane) : 1.0f;
       issue_tiles(false);
       if (k >= 2) {
         ok = ok && warp_wait(&sm.item_empty[k & 1], (k / 2 - 1) & 1, c.status, ab, kSiteTreeItem);
@@ -1109,6 +1127,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             a.q + (static_cast<size_t>(it.b) * a.H + it.hk * a.group) * c.N * kHeadDim;
         const int ch = lane & 7, padded = (nrows + 31) & ~31;
         int hg = (it.r0 + (lane >> 3)) / n, node = it.r0 + (lane >> 3) - hg * n;
+#pragma unroll 2
         for (int rr = lane >> 3; rr < padded; rr += 4) {
           const bool live = rr < nrows;
           const uint16_t* src = base + (live ? static_cast<size_t>(hg) * c.N + node : 0) * kHeadDim + 8 * ch;
@@ -1122,7 +1141,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       }
       if (it.b != last_b) {
         tree ^= 1;
-        args_ok &= tree_info(c, it.b, n, a.nodes, tree_view(a, v, tree), jump_view(a, v));
+        args_ok &= tree_info(!c.parents, par, a.nodes, tree_view(a, v, tree), jump_view(a, v));
         last_b = it.b;
       }
       it.tree = tree;
@@ -1138,15 +1157,17 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             cp_async4(smem_u32(info.near + h * n + y),
                       trow + static_cast<size_t>(h) * a.tab_len + a.tab_zero - y);
       }
-#pragma unroll
+#pragma unroll 1
       for (int rr = lane; rr < kRows; rr += 32) {
         const int r = it.r0 + rr;
         const bool live = rr < nrows;
         const int hg = live ? r / n : g0, node = live ? r - hg * n : 0;
         float sc = 0.125f * static_cast<float>(kLog2e);
-        if (a.ssmax)
-          sc *= __ldg(a.s + it.hk * a.group + hg) *
+        if (a.ssmax) {
+          const float sh = __shfl_sync(0xffffffffu, s_lane, (hg - g0) & 31);
+          sc *= (hg - g0 < 32 ? sh : __ldg(a.s + it.hk * a.group + hg)) *
                 logf(static_cast<float>(len + tree_view(a, v, tree).depth[node] + 1));
+        }
         info.row[rr] = live ? (hg - g0) * kTreeMax + node : -1;
         info.scale[rr] = sc;
       }
@@ -1409,12 +1430,16 @@ bool tree_config(TreeArgs* a, int sms) {
   a->stages = static_cast<int>((budget - fixed) / stage);
   if (a->stages > kMaxStages) a->stages = kMaxStages;
   a->ctas = per_sm * sms < kTreeCtas ? per_sm * sms : kTreeCtas;
-  a->least = 1 + kItemCost;
+  a->least = 2;
   return a->stages >= 2 && a->ctas >= 1;
 }
 
 cudaError_t launch_tree_prep(const TreeArgs& a, cudaStream_t st) {
-  return launch_k(bam_tree_prep_kernel, dim3(a.tab_zero / 256 + 1, a.H), dim3(256), 0, st, false, a);
+  // At most about four blocks an SM, however long the table is: the attention
+  // kernel starts when the last block has started.
+  const int want = a.tab_zero / 256 + 1, y = a.H < 608 ? a.H : 608;
+  const int most = (608 + y - 1) / y;
+  return launch_k(bam_tree_prep_kernel, dim3(want < most ? want : most, y), dim3(256), 0, st, false, a);
 }
 
 cudaError_t launch_tree(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a,
