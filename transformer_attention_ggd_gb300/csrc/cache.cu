@@ -11,14 +11,16 @@ namespace bam {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendTokens = 32;  // most tokens of one CTA
-constexpr int kAppendRows = 4;     // rows of a thread in flight
+constexpr int kAppendTokens = 16;  // most tokens of a unit
+constexpr int kAppendRows = 4;     // rows of a thread
+constexpr int kAppendPass = kAppendThreads / 4;  // rows in flight per load: four lanes a row
+constexpr int kAppendResident = 2;  // CTAs of an SM in a long call
 
 // One rotated pair: (a, b) -> (a cos - b sin, b cos + a sin), in fp32, rounded
 // once to bf16 by the caller.
-__device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
-  const float x = a * cs.x - b * cs.y;
-  b = b * cs.x + a * cs.y;
+__device__ __forceinline__ void turn(float& a, float& b, float co, float si) {
+  const float x = a * co - b * si;
+  b = b * co + a * si;
   a = x;
 }
 
@@ -35,116 +37,207 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-// One CTA: up to 32 tokens of one sequence and a run of its heads (queries,
-// then keys, then values).  The cosines and sines of the tokens are computed
-// once and serve all heads.  Four lanes hold a row, 32 bytes each: for pairs
+// A unit is up to 16 tokens of one sequence and a run of the heads of its
+// queries, keys or values, 256 rows at most: four lanes hold a row, 32 bytes
+// each, and a thread has up to four rows, of one token.  For pairs
 // (x_f, x_{f + dims/2}) a lane takes the two 16-byte chunks that pair up.
-__global__ void __launch_bounds__(kAppendThreads) bam_kv_append_kernel(const AppendArgs a) {
+struct AppendUnit {
+  int b, tile;
+  int kind, h0, heads;  // kind: 0 queries, 1 keys, 2 values
+};
+__device__ __forceinline__ AppendUnit append_unit(const AppendArgs& a, int64_t bt, int part) {
+  AppendUnit x;
+  x.b = static_cast<int>(bt / a.tiles);
+  x.tile = static_cast<int>(bt - static_cast<int64_t>(x.b) * a.tiles);
+  x.kind = part < a.q_parts ? 0 : part < a.q_parts + a.kv_parts ? 1 : 2;
+  const int i = part - (x.kind == 0 ? 0 : x.kind == 1 ? a.q_parts : a.q_parts + a.kv_parts);
+  x.h0 = i * a.heads;
+  x.heads = min(a.heads, (x.kind == 0 ? a.H : a.c.Hkv) - x.h0);
+  return x;
+}
+// Committed length and tokens of sequence b, clamped; false if out of range.
+__device__ __forceinline__ bool append_lengths(const CacheArgs& c, int b, int& len, int& n) {
+  const int cap = c.page * c.max_blocks;
+  const int raw = __ldg(c.lens + b);
+  const int rawn = c.draft_lens ? __ldg(c.draft_lens + b) : c.N;
+  len = min(max(raw, 0), cap);
+  n = min(max(rawn, 0), c.N);
+  return raw == len && rawn == n;
+}
+
+// The parent of this thread's node of sequence b.
+__device__ __forceinline__ int append_parent(const CacheArgs& c, int b) {
+  return c.parents && threadIdx.x < c.N
+             ? __ldg(c.parents + static_cast<size_t>(b) * c.N + threadIdx.x)
+             : -1;
+}
+
+// This thread's place in a unit: token t, heads h, h + step, ...
+struct AppendLane {
+  int t, h, step, c0, c1;
+};
+// Loads this thread's rows of a unit whose tokens below n count.
+__device__ __forceinline__ void append_load(const AppendArgs& a, const AppendUnit& x, int n,
+                                            const AppendLane& ln, uint4 (&w)[kAppendRows][2]) {
+  const int tok = x.tile * a.tokens + ln.t;
+  if (tok >= n) return;
+  const uint16_t* base = x.kind == 0 ? a.q : x.kind == 1 ? a.k : a.v;
+  const int64_t* st = x.kind == 0 ? a.qs : x.kind == 1 ? a.ks : a.vs;
+  const uint16_t* src = base + x.b * st[0] + (x.h0 + ln.h) * st[1] + tok * st[2];
+  const int64_t step = ln.step * st[1];
+#pragma unroll
+  for (int y = 0; y < kAppendRows; ++y, src += step) {
+    if (ln.h + y * ln.step >= x.heads) break;
+    w[y][0] = *reinterpret_cast<const uint4*>(src + 8 * ln.c0);
+    w[y][1] = *reinterpret_cast<const uint4*>(src + 8 * ln.c1);
+  }
+}
+
+// A CTA takes every gridDim-th token tile (ragged prompts then load all SMs
+// alike), its heads one unit after the other, so that the tile's slots and
+// angles serve them all; the next unit's rows are on their way while this
+// one's are turned and stored.  A call of so few units that each has a CTA
+// loads all N tokens' rows before it knows which count: the lengths, slots,
+// depths and angles then take no time of their own.
+template <bool kRun>
+__global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_kernel(const AppendArgs a) {
   __shared__ float2 cs[kAppendTokens][kHeadDim / 2];
   __shared__ int64_t slot_row[kAppendTokens];  // row of head 0 in the pages, -1: not written
   __shared__ int depth[kTreeMax], jump[kTreeMax];
   const CacheArgs& c = a.c;
-  const int tiles = (c.N + a.tokens - 1) / a.tokens;
-  const int b = blockIdx.x / tiles;
-  const int t0 = (blockIdx.x % tiles) * a.tokens;
+  const int u4 = threadIdx.x & 3, nh = a.dims / 16, half = a.dims / 2;
+  const bool rotated = u4 < nh;
+  AppendLane ln;
+  ln.t = (threadIdx.x >> 2) & (a.tokens - 1);  // a.tokens is a power of two
+  ln.h = (threadIdx.x >> 2) / a.tokens;
+  ln.step = kAppendPass / a.tokens;
+  ln.c0 = a.interleaved || !rotated ? 2 * u4 : u4;
+  ln.c1 = a.interleaved || !rotated ? 2 * u4 + 1 : u4 + nh;
   const int cap = c.page * c.max_blocks;
-  const int raw = __ldg(c.lens + b);
-  const int rawn = c.draft_lens ? __ldg(c.draft_lens + b) : c.N;
-  const int len = min(max(raw, 0), cap);
-  const int n = min(max(rawn, 0), c.N);
-  bool ok = raw == len && rawn == n;
-  const int nt = min(a.tokens, n - t0);
-  if (nt <= 0) {
-    if (!ok && t0 == 0 && blockIdx.y == 0 && threadIdx.x == 0) record_bad_arg(c.status);
-    return;
+  const int split = a.q_parts + 2 * a.kv_parts;
+  int64_t bt = kRun ? blockIdx.x : blockIdx.x / split;
+  int part = kRun ? 0 : static_cast<int>(blockIdx.x - bt * split);
+  const int64_t tiles = static_cast<int64_t>(c.B) * a.tiles;
+  AppendUnit x = append_unit(a, bt, part);
+  uint4 w[kAppendRows][2], wn[kAppendRows][2];
+  int len, n, par = -1, last_b = -1, last_tile = -1;
+  if (!kRun) {
+    append_load(a, x, c.N, ln, w);
+    par = append_parent(c, x.b);
   }
-  if (c.parents) ok &= tree_depths(c.parents + static_cast<size_t>(b) * c.N, n, jump, depth);
-  for (int x = threadIdx.x; x < nt; x += kAppendThreads) {
-    const int64_t slot = static_cast<int64_t>(len) + t0 + x;
-    int64_t row = -1;
-    if (slot < cap) {
-      const int pg = __ldg(c.block_table + static_cast<size_t>(b) * c.max_blocks + slot / c.page);
-      if (pg >= 0 && pg < c.num_pages)
-        row = static_cast<int64_t>(pg) * c.Hkv * c.page + slot % c.page;
-    }
-    ok &= row >= 0;
-    slot_row[x] = row;
-  }
-  if (!ok && blockIdx.y == 0) record_bad_arg(c.status);
-  const int half = a.dims / 2;
-  for (int x = threadIdx.x; x < nt * half; x += kAppendThreads) {
-    const int t = x / half, f = x % half;
-    const uint64_t pos = static_cast<uint64_t>(len) + (c.parents ? depth[t0 + t] : t0 + t);
-    // The phase wraps modulo 2^64, one turn: an exact reduction.  Its top 32
-    // bits, signed, are the angle in units of 2^-31 half turns.
-    const int top = static_cast<int>((pos * a.freq[f]) >> 32);
-    float s, co;
-    sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &co);
-    cs[t][f] = make_float2(co, s);
-  }
-  __syncthreads();
-
-  const int heads = a.H + 2 * c.Hkv;
-  const int h0 = blockIdx.y * a.heads;
-  const int nrow = nt * min(a.heads, heads - h0);
-  const int u = threadIdx.x & 3;
-  const int nh = a.dims / 16;
-  const int c0 = a.interleaved || u >= nh ? 2 * u : u;
-  const int c1 = a.interleaved || u >= nh ? 2 * u + 1 : u + nh;
-  const bool rotated = u < nh;
-  for (int r0 = threadIdx.x >> 2; r0 < nrow; r0 += kAppendRows * (kAppendThreads / 4)) {
-    uint4 w[kAppendRows][2];
-#pragma unroll
-    for (int x = 0; x < kAppendRows; ++x) {
-      const int r = r0 + x * (kAppendThreads / 4);
-      if (r >= nrow) break;
-      const int h = h0 + r / nt, t = t0 + r % nt;
-      const uint16_t* src;
-      if (h < a.H)
-        src = a.q + b * a.qs[0] + h * a.qs[1] + t * a.qs[2];
-      else if (h < a.H + c.Hkv)
-        src = a.k + b * a.ks[0] + (h - a.H) * a.ks[1] + t * a.ks[2];
-      else
-        src = a.v + b * a.vs[0] + (h - a.H - c.Hkv) * a.vs[1] + t * a.vs[2];
-      w[x][0] = *reinterpret_cast<const uint4*>(src + 8 * c0);
-      w[x][1] = *reinterpret_cast<const uint4*>(src + 8 * c1);
-    }
-#pragma unroll
-    for (int x = 0; x < kAppendRows; ++x) {
-      const int r = r0 + x * (kAppendThreads / 4);
-      if (r >= nrow) break;
-      const int h = h0 + r / nt, t = r % nt;
-      if (rotated && h < a.H + c.Hkv) {
-        float f0[8], f1[8];
-        unpack8(w[x][0], f0);
-        unpack8(w[x][1], f1);
-        if (a.interleaved) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            turn(f0[2 * y], f0[2 * y + 1], cs[t][8 * u + y]);
-            turn(f1[2 * y], f1[2 * y + 1], cs[t][8 * u + 4 + y]);
-          }
-        } else {
-#pragma unroll
-          for (int y = 0; y < 8; ++y) turn(f0[y], f1[y], cs[t][8 * u + y]);
-        }
-        w[x][0] = pack8(f0);
-        w[x][1] = pack8(f1);
+  bool ok = append_lengths(c, x.b, len, n);
+  if (kRun) append_load(a, x, n, ln, w);
+  for (;;) {
+    // The unit after this one.
+    AppendUnit xn = x;
+    int len_n = len, n_n = n;
+    bool more = false;
+    if (kRun) {
+      if (++part == split) {
+        part = 0;
+        bt += gridDim.x;
       }
+      more = bt < tiles;
+      if (more) {
+        xn = append_unit(a, bt, part);
+        if (xn.b != x.b) ok &= append_lengths(c, xn.b, len_n, n_n);
+        append_load(a, xn, n_n, ln, wn);
+      }
+    }
+    const int t0 = x.tile * a.tokens, nt = min(a.tokens, n - t0);
+    if (nt > 0 && (x.b != last_b || x.tile != last_tile)) {
+      if (last_b >= 0) __syncthreads();  // the last tile's slots and angles are no longer read
+      const int64_t slot = static_cast<int64_t>(len) + t0 + threadIdx.x;
+      const int blk = static_cast<int>(slot) / c.page;
+      int pg = -1;
+      if (threadIdx.x < nt && slot < cap)
+        pg = __ldg(c.block_table + static_cast<size_t>(x.b) * c.max_blocks + blk);
+      if (c.parents && x.b != last_b) {
+        if (kRun) par = append_parent(c, x.b);
+        ok &= tree_depths(par, n, jump, depth);
+      }
+      if (threadIdx.x < nt) {
+        int64_t row = -1;
+        if (pg >= 0 && pg < c.num_pages)
+          row = static_cast<int64_t>(pg) * c.Hkv * c.page + (static_cast<int>(slot) - blk * c.page);
+        ok &= row >= 0;
+        slot_row[threadIdx.x] = row;
+      }
+      for (int y = threadIdx.x; y < nt * (kHeadDim / 2); y += kAppendThreads) {
+        const int t = y / (kHeadDim / 2), f = y % (kHeadDim / 2);
+        if (f >= half) continue;
+        const uint64_t pos = static_cast<uint64_t>(len) + (c.parents ? depth[t0 + t] : t0 + t);
+        // The phase wraps modulo 2^64, one turn: an exact reduction.  Its top
+        // 32 bits, signed, are the angle in units of 2^-31 half turns.
+        const int top = static_cast<int>((pos * a.freq[f]) >> 32);
+        float s, co;
+        sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &co);
+        cs[t][f] = make_float2(co, s);
+      }
+      __syncthreads();
+      last_b = x.b;
+      last_tile = x.tile;
+    }
+    const int64_t row = ln.t < nt ? (x.kind == 0 ? 0 : slot_row[ln.t]) : -1;
+    if (row >= 0) {
       uint16_t* dst;
-      if (h < a.H) {
-        dst = a.q_out + ((static_cast<int64_t>(b) * a.H + h) * c.N + t0 + t) * kHeadDim;
+      int64_t hs;  // elements from a head to the next
+      if (x.kind == 0) {
+        hs = static_cast<int64_t>(c.N) * kHeadDim;
+        dst = a.q_out + (static_cast<int64_t>(x.b) * a.H + x.h0 + ln.h) * hs +
+              static_cast<int64_t>(t0 + ln.t) * kHeadDim;
       } else {
-        const int64_t row = slot_row[t];
-        if (row < 0) continue;
-        const int hk = h < a.H + c.Hkv ? h - a.H : h - a.H - c.Hkv;
-        dst = (h < a.H + c.Hkv ? a.k_pages : a.v_pages) +
-              (row + static_cast<int64_t>(hk) * c.page) * kHeadDim;
+        hs = static_cast<int64_t>(c.page) * kHeadDim;
+        dst = (x.kind == 1 ? a.k_pages : a.v_pages) + row * kHeadDim + (x.h0 + ln.h) * hs;
       }
-      *reinterpret_cast<uint4*>(dst + 8 * c0) = w[x][0];
-      *reinterpret_cast<uint4*>(dst + 8 * c1) = w[x][1];
+      hs *= ln.step;
+      if (rotated && x.kind < 2) {
+        float4 r[4];  // eight (cosine, sine) pairs
+#pragma unroll
+        for (int y = 0; y < 4; ++y) r[y] = reinterpret_cast<const float4*>(cs[ln.t] + 8 * u4)[y];
+#pragma unroll
+        for (int y = 0; y < kAppendRows; ++y) {
+          if (ln.h + y * ln.step >= x.heads) break;
+          float f0[8], f1[8];
+          unpack8(w[y][0], f0);
+          unpack8(w[y][1], f1);
+          if (a.interleaved) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              turn(f0[4 * z], f0[4 * z + 1], r[z].x, r[z].y);
+              turn(f0[4 * z + 2], f0[4 * z + 3], r[z].z, r[z].w);
+              turn(f1[4 * z], f1[4 * z + 1], r[2 + z].x, r[2 + z].y);
+              turn(f1[4 * z + 2], f1[4 * z + 3], r[2 + z].z, r[2 + z].w);
+            }
+          } else {
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              turn(f0[2 * z], f1[2 * z], r[z].x, r[z].y);
+              turn(f0[2 * z + 1], f1[2 * z + 1], r[z].z, r[z].w);
+            }
+          }
+          w[y][0] = pack8(f0);
+          w[y][1] = pack8(f1);
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < kAppendRows; ++y, dst += hs) {
+        if (ln.h + y * ln.step >= x.heads) break;
+        *reinterpret_cast<uint4*>(dst + 8 * ln.c0) = w[y][0];
+        *reinterpret_cast<uint4*>(dst + 8 * ln.c1) = w[y][1];
+      }
+    }
+    if (!more) break;
+    x = xn;
+    len = len_n;
+    n = n_n;
+#pragma unroll
+    for (int y = 0; y < kAppendRows; ++y) {
+      w[y][0] = wn[y][0];
+      w[y][1] = wn[y][1];
     }
   }
+  if (!ok) record_bad_arg(c.status);
 }
 
 constexpr int kKeepThreads = 256;
@@ -156,11 +249,13 @@ constexpr int kKeepBatch = 16;  // rows that a warp holds in registers
 // (a_m' >= m' > m), so a warp that reads a batch of rows before it writes
 // them, batches in order, moves them in place.
 __global__ void __launch_bounds__(kKeepThreads) bam_kv_keep_kernel(const KeepArgs a) {
-  __shared__ int path[kTreeMax];
+  __shared__ int par[kTreeMax], path[kTreeMax];
   __shared__ int64_t src_row[kTreeMax], dst_row[kTreeMax];
   __shared__ int count;
   const CacheArgs& c = a.c;
   const int b = blockIdx.y;
+  if (c.parents && threadIdx.x < c.N)
+    par[threadIdx.x] = __ldg(c.parents + static_cast<size_t>(b) * c.N + threadIdx.x);
   int len, n;
   bool ok = cache_lengths(c, b, &len, &n);
   int acc = __ldg(a.accepted + b);
@@ -168,14 +263,14 @@ __global__ void __launch_bounds__(kKeepThreads) bam_kv_keep_kernel(const KeepArg
     ok = false;
     acc = -1;
   }
+  __syncthreads();
   if (threadIdx.x == 0) {
     // Root to node, from the deep end: the depth is known after the walk.
-    const int* par = c.parents ? c.parents + static_cast<size_t>(b) * c.N : nullptr;
     int m = 0;
-    if (par) {
+    if (c.parents) {
       for (int i = acc; i >= 0;) {
         path[m++] = i;
-        const int p = __ldg(par + i);
+        const int p = par[i];
         if (p < -1 || p >= i) ok = false;
         i = p < i ? p : -1;
       }
@@ -237,20 +332,25 @@ __global__ void __launch_bounds__(kKeepThreads) bam_kv_keep_kernel(const KeepArg
 
 cudaError_t launch_append(const AppendArgs& args, cudaStream_t st) {
   AppendArgs a = args;
-  const int heads = a.H + 2 * a.c.Hkv;
-  // Tokens and heads of a CTA: about four rows a thread once there are enough
-  // rows for two CTAs per SM.
-  a.tokens = a.c.N < kAppendTokens ? a.c.N : kAppendTokens;
-  const int tiles = (a.c.N + a.tokens - 1) / a.tokens;
-  const int64_t ctas = static_cast<int64_t>(a.c.B) * tiles;
-  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  int split = 1;
-  while (split < heads && ctas * split < 2 * 152 &&
-         static_cast<int64_t>(a.tokens) * ((heads + split - 1) / split) > kAppendThreads / 4)
-    ++split;
-  a.heads = (heads + split - 1) / split;
-  dim3 grid(static_cast<unsigned>(ctas), (heads + a.heads - 1) / a.heads);
-  return launch_k(bam_kv_append_kernel, grid, dim3(kAppendThreads), 0, st, false, a);
+  a.tokens = 1;
+  while (a.tokens < a.c.N && a.tokens < kAppendTokens) a.tokens *= 2;
+  a.tiles = (a.c.N + a.tokens - 1) / a.tokens;
+  // Heads of a unit: what fits, in equal parts.
+  const int most = kAppendRows * kAppendPass / a.tokens;
+  const int big = a.H > a.c.Hkv ? a.H : a.c.Hkv, parts = (big + most - 1) / most;
+  a.heads = (big + parts - 1) / parts;
+  a.q_parts = (a.H + a.heads - 1) / a.heads;
+  a.kv_parts = (a.c.Hkv + a.heads - 1) / a.heads;
+  const int64_t tiles = static_cast<int64_t>(a.c.B) * a.tiles;
+  const int64_t units = tiles * (a.q_parts + 2 * a.kv_parts);
+  // Token tiles dealt to resident CTAs once there are enough of them.
+  const int64_t run = static_cast<int64_t>(sm_count()) * kAppendResident;
+  if (tiles > run)
+    return launch_k(bam_kv_append_kernel<true>, dim3(static_cast<unsigned>(run)),
+                    dim3(kAppendThreads), 0, st, false, a);
+  if (units > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  return launch_k(bam_kv_append_kernel<false>, dim3(static_cast<unsigned>(units)),
+                  dim3(kAppendThreads), 0, st, false, a);
 }
 
 cudaError_t launch_keep(const KeepArgs& a, cudaStream_t st) {

@@ -30,7 +30,9 @@ struct AppendArgs {
   int64_t ks[3], vs[3], qs[3];  // element strides over batch, head, token
   int H;                        // query heads (0 without q)
   int dims, interleaved;
-  int tokens, heads;            // tokens and heads of one CTA
+  int tokens, heads;            // tokens (a power of two) and heads of a unit of work
+  int tiles;                    // token tiles of a sequence
+  int q_parts, kv_parts;        // units of a token tile: of its queries, of its keys
   uint64_t freq[kHeadDim / 2];  // turns per position of pair f, times 2^64
 };
 
@@ -128,24 +130,16 @@ __device__ __forceinline__ bool cache_lengths(const CacheArgs& c, int b, int* le
 }
 
 // Depths of the first n <= kTreeMax nodes, by all threads of a block of at
-// least kTreeMax threads: each round doubles the distance that a node's jump
-// pointer spans, so the deepest chain takes log2(depth) rounds.  `jump` holds
-// kTreeMax ints of shared memory, as `depth`.  Ends with a block barrier.
-// Returns false in a thread whose node had a parent outside [-1, i).
-__device__ __forceinline__ bool tree_depths(const int* parents, int n, int* jump, int* depth) {
+// least kTreeMax threads, thread i with node i's parent: each round doubles
+// the distance that a node's jump pointer spans, so the deepest chain takes
+// log2(depth) rounds.  `jump` holds kTreeMax ints of shared memory, as
+// `depth`.  Ends with a block barrier.  Returns false in a thread whose node
+// had a parent outside [-1, i).
+__device__ __forceinline__ bool tree_depths(int parent, int n, int* jump, int* depth) {
   const int i = threadIdx.x;
-  bool ok = true;
-  int p = -1;
-  if (i < n) {
-    p = parents ? __ldg(parents + i) : i - 1;
-    ok = p >= -1 && p < i;
-    if (!ok) p = -1;
-  }
+  const bool ok = i >= n || (parent >= -1 && parent < i);
+  int p = i < n && ok ? parent : -1;
   int d = p >= 0 ? 1 : 0;
-  if (!parents) {
-    d = i;
-    p = -1;
-  }
   if (i < kTreeMax) {
     jump[i] = p;
     depth[i] = d;
