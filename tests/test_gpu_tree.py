@@ -177,6 +177,87 @@ def test_tree_many_query_heads_per_key_head():
                True, False, "fp32")
 
 
+@pytest.mark.parametrize("H,N,out", [(128, 1, "bf16"), (200, 1, "fp32"), (130, 2, "bf16"),
+                                     (16, 8, "bf16"), (24, 3, "fp32")])
+def test_tree_one_key_head(H, N, out):
+    """All query heads share one key head: row blocks that hold many heads."""
+    rng = np.random.default_rng(H)
+    lens, new = [700, 0, 129], [N, 1, N]
+    _tree_case(H, 3, H, 1, N, 64, lens, new, [random_tree(rng, n) for n in new], True, False, out)
+
+
+def test_tree_without_any_node_and_without_lse():
+    """No sequence has a node: nothing is written.  A call without lse."""
+    B, H, N = 5, 4, 3
+    c = Cache(121, 2, 64, [70] * B, 2)
+    t = [dev_f32(_prm(c.rng, H, False)[n]) for n in ("alpha", "beta", "mu", "s")]
+    q = _normal(c.gen, B, H, N, 64)
+    o, lse = torch.full((B, H, N, 64), 5.0, device="cuda"), torch.full((B, H, N), 5.0, device="cuda")
+    ws = ba.tree_workspace(B, H, 2, N, 128)
+    prm = ba.make_params(*t, 1e-5, True, True)
+    args = (q, c.k, c.v, c.table, _i32([60] * B))
+    ba.bam_attn_decode_tree_paged(*args, _i32([0] * B), None, o, lse, prm, ws)
+    assert ba.bam_attn_check_status(ws) == ba.BAM_OK
+    assert torch.all(o == 5.0) and torch.all(lse == 5.0)
+    ba.bam_attn_decode_tree_paged(*args, None, None, o, lse, prm, ws)
+    o2 = torch.full_like(o, NAN)
+    ba.bam_attn_decode_tree_paged(*args, None, None, o2, None, prm, ws)
+    assert torch.equal(o, o2) and torch.isfinite(o).all()
+
+
+def test_tree_infinities_among_committed_keys_reach_every_node():
+    """A committed value is seen by every node: an infinity in it reaches all of
+    them, in its dimension alone."""
+    B, H, N, ln = 1, 3, 5, 300
+    for where in (3, 299):
+        c = Cache(131, H, 64, [ln + N], 5)
+        prm = _prm(c.rng, H, False)
+        prm["beta"] = np.zeros(H, np.float32)  # every weight is of the same order
+        t = [dev_f32(prm[n]) for n in ("alpha", "beta", "mu", "s")]
+        q = _normal(c.gen, B, H, N, 64)
+        c.v[int(c.table[0, where // 64]), :, where % 64, 7] = float("-inf")
+        for dt in (torch.bfloat16, torch.float32):
+            o, _ = ba.attention_decode_tree_paged(q, c.k, c.v, c.table, _i32([ln]), *t, o_dtype=dt)
+            assert torch.all(o[..., 7] == float("-inf"))
+            assert torch.isfinite(o[..., :7]).all() and torch.isfinite(o[..., 8:]).all()
+
+
+def test_refusals_on_the_gpu_leave_the_context_usable():
+    B, H, N = 2, 4, 3
+    c = Cache(141, 2, 64, [40, 50], 1)
+    t = [dev_f32(_prm(c.rng, H, False)[n]) for n in ("alpha", "beta", "mu", "s")]
+    q = _normal(c.gen, B, H, N, 64)
+    ln = _i32([30, 40])
+    good = (q, c.k, c.v, c.table, ln)
+    for i, bad in [(0, q.float()), (0, q.transpose(1, 2)), (0, q[:, :3]), (1, c.k[:, :1]),
+                   (1, c.k.transpose(0, 1)), (2, c.v[..., :32]), (3, c.table.long()),
+                   (3, c.table[:1]), (4, ln.float()), (4, ln[:1])]:
+        args = list(good)
+        args[i] = bad
+        with pytest.raises((ValueError, ba.BamError)):
+            ba.attention_decode_tree_paged(*args, *t)
+        if i:
+            with pytest.raises((ValueError, ba.BamError)):
+                ba.kv_append_paged(_normal(c.gen, B, 2, N, 64), _normal(c.gen, B, 2, N, 64), *args[1:])
+    for kw in (dict(draft_lens=_i32([1])), dict(parents=_i32([[-1, 0]] * 2)),
+               dict(parents=torch.zeros(B, N, device="cuda"))):
+        with pytest.raises(ValueError):
+            ba.attention_decode_tree_paged(*good, *t, **kw)
+    with pytest.raises(ValueError, match="aligned rows"):
+        x = _normal(c.gen, B, 2, N, 72)[..., 4:68]
+        ba.kv_append_paged(x, x, *good[1:])
+    with pytest.raises(ValueError, match="go together"):
+        k = _normal(c.gen, B, 2, N, 64)
+        ba.bam_kv_append_paged(k, k, *good[1:], None, None, q, None, None, ba.cache_workspace())
+    with pytest.raises(ba.BamError, match="unsupported"):
+        big = _normal(c.gen, B, H, 129, 64)
+        ba.attention_decode_tree_paged(big, *good[1:], *t, ws=torch.zeros(1 << 24, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ba.BamError, match="workspace"):
+        ba.attention_decode_tree_paged(*good, *t, ws=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    o, _ = ba.attention_decode_tree_paged(*good, *t)
+    assert torch.isfinite(o).all()
+
+
 def test_tree_masked_nan_and_inf_have_no_effect():
     """A drafted key or value that a node does not see may hold NaN or
     infinities: only the nodes that see it get them."""

@@ -542,7 +542,10 @@ __device__ __forceinline__ void soft_finish(const TreeArgs& a, TreeSmem& sm, con
   --st.t;
   st.first = false;
 }
-// Two weights and their bf16 parts; l2 gathers the exact ones.
+// Two weights and their bf16 parts; l2 gathers the exact ones.  Three parts
+// are cut off, not rounded: 8 bits each are the weight's 24, and none is
+// negative, nor zero behind a weight that is not, so that an infinite value
+// meets no product that turns it into NaN.
 template <int PARTS, int N>
 __device__ __forceinline__ void soft_weights(uint64_t z, uint64_t negm2, uint64_t& l2,
                                              uint32_t (*pk)[N], int y) {
@@ -551,14 +554,17 @@ __device__ __forceinline__ void soft_weights(uint64_t z, uint64_t negm2, uint64_
   p0 = ex2_approx(p0);
   p1 = ex2_approx(p1);
   l2 = fadd2(l2, f2_pack(p0, p1));
+  if (PARTS == 1) {
+    pk[0][y] = pack_bf16x2(p0, p1);
+    return;
+  }
+  constexpr float kTiny = 1.1754944e-38f;
 #pragma unroll
   for (int part = 0; part < PARTS; ++part) {
-    const uint32_t u = pack_bf16x2(p0, p1);
-    pk[part][y] = u;
-    if (part + 1 < PARTS) {
-      p0 -= __uint_as_float(u << 16);
-      p1 -= __uint_as_float(u & 0xFFFF0000u);
-    }
+    const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+    pk[part][y] = __byte_perm(u0, u1, 0x7632);
+    p0 = fmaxf(p0 - __uint_as_float(u0 & 0xFFFF0000u), kTiny);
+    p1 = fmaxf(p1 - __uint_as_float(u1 & 0xFFFF0000u), kTiny);
   }
 }
 
