@@ -54,7 +54,7 @@ enum : int {
 // One CTA's share of an item: rows r0 .. r1 - 1 of sequence b and key head
 // hk against tiles t0 .. t1 - 1 of its len + n keys.
 struct Item {
-  int b, hk, r0, r1;
+  int b, hk, r0, r1, g0;  // g0: head of row r0
   int len, n;
   int t0, t1, tiles;  // t1 == 0: no more items
   int tree;           // which of the two TreeInfo buffers
@@ -70,9 +70,8 @@ struct TreeInfo {
 // What the producer prepares of an item besides its queries.
 struct ItemInfo {
   Item* it;
-  int* row;      // of each row: head within the item * kTreeMax + node; -1: no row
-  float* scale;  // logit scale, log2 units
-  float* near;   // [head of the item's][distance < n] table entries
+  float* s;     // the Scalable-Softmax factor of each of its heads
+  float* near;  // [head of the item's][distance < n] table entries
 };
 
 struct __align__(16) TreeSmem {
@@ -85,7 +84,7 @@ struct __align__(16) TreeSmem {
   uint64_t item_empty[2];      // the softmax warps are done with them
   uint64_t s_full;             // S is complete
   uint64_t p_full, pv_done;    // P is in Tensor Memory; P V is done
-  uint64_t merge_full, merge_free;  // half the item's parts are in shared memory; are read
+  uint64_t merge[2];           // what two copies, then two pairs, exchange is there
   uint64_t mma_final;
   uint32_t odd[2][kTreeMax / 32];  // nodes whose value is not finite, by item parity
   uint32_t tmem_base;
@@ -402,8 +401,8 @@ struct View {
   TreeSmem* sm;
   uint8_t* nodes;   // TreeInfo [2], jump
   float* near;      // [2][near]
-  int* rows;        // row and scale [2][kRows] each
-  float2* merge_ml; // [128 - kRows]
+  float* s;         // [2][kRows]
+  float2* merge_ml; // [kRowsMax]
 };
 template <class S>
 __device__ __forceinline__ View smem_view(const TreeArgs& a) {
@@ -415,8 +414,8 @@ __device__ __forceinline__ View smem_view(const TreeArgs& a) {
   v.sm = reinterpret_cast<TreeSmem*>(v.win + a.stages * a.win_stage);
   v.nodes = reinterpret_cast<uint8_t*>(v.sm + 1);
   v.near = reinterpret_cast<float*>(v.nodes + a.nodes * 44);
-  v.rows = reinterpret_cast<int*>(v.near + 2 * a.near);
-  v.merge_ml = reinterpret_cast<float2*>(v.rows + 4 * S::kRows);
+  v.s = v.near + 2 * a.near;
+  v.merge_ml = reinterpret_cast<float2*>(v.s + 2 * S::kRows);
   return v;
 }
 __device__ __forceinline__ TreeInfo tree_view(const TreeArgs& a, const View& v, int which) {
@@ -429,8 +428,7 @@ __device__ __forceinline__ int* jump_view(const TreeArgs& a, const View& v) {
 template <class S>
 __device__ __forceinline__ ItemInfo info_view(const TreeArgs& a, const View& v, int k) {
   const int x = k & 1;
-  return ItemInfo{v.sm->item + x, v.rows + 2 * x * S::kRows,
-                  reinterpret_cast<float*>(v.rows + (2 * x + 1) * S::kRows), v.near + x * a.near};
+  return ItemInfo{v.sm->item + x, v.s + x * S::kRows, v.near + x * a.near};
 }
 
 // What a softmax warp carries from tile to tile.
@@ -463,12 +461,13 @@ __device__ __forceinline__ SoftRow soft_row(const TreeArgs& a, const View& v, in
   r.k0 = r.copy * S::kCols;
   r.lanes = sm.tmem_base + tmem_lane_base(warp);
   r.warp_live = it.r0 + 32 * (warp % S::kGroups) < it.r1;
-  const int row = info.row[r.rr];
-  r.live = row >= 0;
-  r.node = r.live ? row % kTreeMax : 0;
-  r.hrel = r.live ? row / kTreeMax : 0;
+  r.live = it.r0 + r.rr < it.r1;
+  const int head = r.live ? (it.r0 + r.rr) / n : it.g0;
+  r.node = r.live ? it.r0 + r.rr - head * n : 0;
+  r.hrel = head - it.g0;
   r.depth = tree_view(a, v, it.tree).depth[r.node];
-  r.cs = info.scale[r.rr];
+  r.cs = 0.125f * static_cast<float>(kLog2e);
+  if (a.ssmax) r.cs *= info.s[r.hrel] * logf(static_cast<float>(it.len + r.depth + 1));
   r.woff = r.hrel * window_floats(S::kTile, n) + ((a.tab_zero - (it.len + n - 1)) & 3) +
            (n - 1 - r.depth) + r.k0;
   return r;
@@ -621,8 +620,39 @@ __device__ __forceinline__ void soft_tile(const TreeArgs& a, const View& v, cons
   soft_finish(a, sm, row, st, scale);
 }
 
-// A tile with keys that not every row sees: 16 columns at a time, S read
-// twice, so that this rarer code takes few registers from the other.
+// 16 logits of a tile with keys that not every row sees, from column kk on.
+// nc: committed keys among the copy's columns (not clamped); the n nodes of
+// the draft follow them.
+__device__ __forceinline__ void tail_logits(uint32_t taddr, const SoftRow& row, const float* w,
+                                            const float* near, const int* depth, uint64_t vis,
+                                            int kk, int nc, int n, float* z) {
+  if (kk >= nc + n) {  // behind the draft
+#pragma unroll
+    for (int y = 0; y < 16; ++y) z[y] = -INFINITY;
+    return;
+  }
+  uint32_t sv[16];
+  tmem_ld_cols<16>(taddr + kk, sv);
+  if (kk + 16 <= nc) {  // committed
+#pragma unroll
+    for (int y = 0; y < 16; ++y) z[y] = fmaf(__uint_as_float(sv[y]), row.cs, w[kk + y]);
+    return;
+  }
+  const uint32_t bits = static_cast<uint32_t>(vis >> kk);
+#pragma unroll
+  for (int y = 0; y < 16; ++y) {
+    // A column outside the draft reads a neighbouring word of shared memory as
+    // its depth; kept within the table it stays harmless, and is not used.
+    const unsigned back = min(static_cast<unsigned>(depth[kk + y - nc]),
+                              static_cast<unsigned>(row.depth));
+    const float* from = kk + y < nc ? w + kk + y : near - back;
+    const float x = fmaf(__uint_as_float(sv[y]), row.cs, *from);
+    z[y] = bits >> y & 1 ? x : -INFINITY;
+  }
+}
+
+// A tile with keys that not every row sees.  Many columns are read twice, 16 at
+// a time, so that this rarer code takes few registers from the other.
 template <int PARTS, int KS>
 __device__ __forceinline__ void soft_tail(const TreeArgs& a, const View& v, const SoftRow& row,
                                           SoftState& st, int k) {
@@ -637,92 +667,123 @@ __device__ __forceinline__ void soft_tail(const TreeArgs& a, const View& v, cons
   const float* w = v.win + st.s * a.win_stage + row.woff;
   const float* near = info.near + row.hrel * n + row.depth;  // of an ancestor: near[-its depth]
   const uint64_t vis = row.live ? tile_mask(ti.seen[row.node], j0 + row.k0, len) : 0;
-  auto logits = [&](int q, uint64_t* z) __attribute__((always_inline)) {
-    uint32_t sv[16];
-    tmem_ld_cols<16>(row.lanes + row.k0 + 16 * q, sv);
-#pragma unroll
-    for (int y = 0; y < 8; ++y) {
-      float e[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int kk = 16 * q + 2 * y + h, i = j0 + row.k0 + kk - len;
-        // Loads of keys out of sight stay in range and are not used.
-        const int back = min(ti.depth[min(max(i, 0), n - 1)], row.depth);
-        const float bias = i < 0 ? w[kk] : near[-back];
-        const float x = fmaf(__uint_as_float(sv[2 * y + h]), row.cs, bias);
-        e[h] = vis >> kk & 1 ? x : -INFINITY;
-      }
-      z[y] = f2_pack(e[0], e[1]);
-    }
-  };
+  const int nc = len - j0 - row.k0;
+  constexpr bool kOnce = S::kCols * PARTS <= 48;
+  constexpr int kBlocks = S::kCols / 16;
+  float z[kOnce ? S::kCols : 16];
   float mx = kNoMax, scale;
   if (row.warp_live) {
-#pragma unroll 1
-    for (int q = 0; q < S::kCols / 16; ++q) {
-      uint64_t z[8];
-      logits(q, z);
+    if constexpr (kOnce) {
 #pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        float lo, hi;
-        f2_unpack(z[y], lo, hi);
-        mx = fmax3(mx, lo, hi);
+      for (int q = 0; q < kBlocks; ++q)
+        tail_logits(row.lanes + row.k0, row, w, near, ti.depth, vis, 16 * q, nc, n, z + 16 * q);
+#pragma unroll
+      for (int y = 0; y < S::kCols; y += 2) mx = fmax3(mx, z[y], z[y + 1]);
+    } else {
+#pragma unroll 1
+      for (int q = 0; q < kBlocks; ++q) {
+        tail_logits(row.lanes + row.k0, row, w, near, ti.depth, vis, 16 * q, nc, n, z);
+#pragma unroll
+        for (int y = 0; y < 16; y += 2) mx = fmax3(mx, z[y], z[y + 1]);
       }
     }
   }
+  if (kOnce) soft_free_s(sm, st);
   // Rows of V behind the draft hold anything, and a drafted value that is not
   // finite must not meet the weight 0 of a row that does not see it: zeros
   // here, a quarter of the rows by each warp.  The latter are added to O at
   // the item's end.
   st.ok = warp_wait(&sm.v_full[st.s], st.phase, a.c.status, ab, kSiteTreeSoftK);
   if (!st.ok) return;
-  bool any = false;
+  {
+    constexpr int kQuarter = S::kTile / kSoftWarps;
+    const int first = j0 + kQuarter * warp - len;  // node of the quarter's first row
+    uint8_t* const rows = v.sv + st.s * S::kTileBytes + kQuarter * warp * 128 + 16 * (lane & 7);
+    bool any = false;
 #pragma unroll 2
-  for (int y = 0; y < S::kTile / 16; ++y) {
-    const int key = S::kTile / kSoftWarps * warp + 4 * y + (lane >> 3), i = j0 + key - len;
-    if (i < 0) continue;
-    uint4* p = reinterpret_cast<uint4*>(v.sv + st.s * S::kTileBytes + key * 128 + 16 * (lane & 7));
-    uint4 x = *p;
-    uint32_t* u = reinterpret_cast<uint32_t*>(&x);
-    bool fix = i >= n;
+    for (int y = lane >> 3; y < kQuarter; y += 4) {
+      const int i = first + y;
+      if (i < 0) continue;
+      uint4* const p = reinterpret_cast<uint4*>(rows + y * 128);
+      if (i >= n) {
+        *p = make_uint4(0, 0, 0, 0);
+        any = true;
+        continue;
+      }
+      uint4 x = *p;
+      uint32_t* u = reinterpret_cast<uint32_t*>(&x);
+      bool fix = false;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      uint32_t keep = i >= n ? 0u : 0xFFFFFFFFu;
-      if (odd_exp(u[h])) keep &= 0xFFFF0000u;
-      if (odd_exp(u[h] >> 16)) keep &= 0x0000FFFFu;
-      fix |= keep != 0xFFFFFFFFu;
-      if (i < n && keep != 0xFFFFFFFFu) atomicOr(&sm.odd[k & 1][i >> 5], 1u << (i & 31));
-      u[h] &= keep;
+      for (int h = 0; h < 4; ++h) {
+        const bool lo = odd_exp(u[h]), hi = odd_exp(u[h] >> 16);
+        fix |= lo | hi;
+        u[h] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
+      }
+      if (fix) {
+        atomicOr(&sm.odd[k & 1][i >> 5], 1u << (i & 31));
+        *p = x;
+        any = true;
+      }
     }
-    if (fix) *p = x;
-    any |= fix;
+    if (any) fence_proxy_async_smem();
+    __syncwarp();
   }
-  if (any) fence_proxy_async_smem();
-  __syncwarp();
   if (!soft_max(a, sm, row, st, mx, scale)) return;
   if (row.warp_live) {
-    const uint64_t negm2 = f2_pack(-st.m, -st.m);
     uint64_t l2 = 0ull;
-#pragma unroll 1
-    for (int q = 0; q < S::kCols / 16; ++q) {
-      uint64_t z[8];
+    const uint64_t negm2 = f2_pack(-st.m, -st.m);
+    auto weights = [&](const float* zz, int q) __attribute__((always_inline)) {
       uint32_t pk[PARTS][8];
-      logits(q, z);
 #pragma unroll
-      for (int y = 0; y < 8; ++y) soft_weights<PARTS, 8>(z[y], negm2, l2, pk, y);
+      for (int y = 0; y < 8; ++y)
+        soft_weights<PARTS, 8>(f2_pack(zz[2 * y], zz[2 * y + 1]), negm2, l2, pk, y);
 #pragma unroll
       for (int part = 0; part < PARTS; ++part)
         tmem_st_pairs<16>(row.lanes + S::kColP + row.k0 / 2 + S::kPCols * part + 8 * q, pk[part]);
+    };
+    if constexpr (kOnce) {
+#pragma unroll
+      for (int q = 0; q < kBlocks; ++q) weights(z + 16 * q, q);
+    } else {
+#pragma unroll 1
+      for (int q = 0; q < kBlocks; ++q) {
+        tail_logits(row.lanes + row.k0, row, w, near, ti.depth, vis, 16 * q, nc, n, z);
+        weights(z, q);
+      }
     }
     float b0, b1;
     f2_unpack(l2, b0, b1);
     st.l += b0 + b1;
   }
-  soft_free_s(sm, st);
+  if (!kOnce) soft_free_s(sm, st);
   soft_finish(a, sm, row, st, scale);
 }
 
-// The item's end: the copies are joined, 32 columns at a time, through the
-// buffer of its queries, which its products no longer read.
+// o += x g, x being 4 N floats that another copy has handed over: chunks of 16
+// bytes, swizzled by the row.
+template <int N>
+__device__ __forceinline__ void join_row(const uint8_t* row, int swz, float g, float* o) {
+#pragma unroll
+  for (int y = 0; y < N; ++y) {
+    const float4 x = *reinterpret_cast<const float4*>(row + ((y ^ swz) << 4));
+    o[4 * y] = fmaf(x.x, g, o[4 * y]);
+    o[4 * y + 1] = fmaf(x.y, g, o[4 * y + 1]);
+    o[4 * y + 2] = fmaf(x.z, g, o[4 * y + 2]);
+    o[4 * y + 3] = fmaf(x.w, g, o[4 * y + 3]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void hand_row(uint8_t* row, int swz, const float* o) {
+#pragma unroll
+  for (int y = 0; y < N; ++y)
+    *reinterpret_cast<float4*>(row + ((y ^ swz) << 4)) =
+        make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+}
+
+// The item's end.  The copies of a row join by halves, through the buffer of
+// the item's queries, which its products no longer read: two copies exchange
+// 32 columns, and with four copies two pairs then exchange 16 (in the places
+// that they have read), so that each ends with 64 / KS columns of the sum.
 template <int PARTS, int KS>
 __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const SoftRow& row,
                                          const SoftState& st, int k) {
@@ -731,126 +792,125 @@ __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const
   const CacheArgs& c = a.c;
   volatile int* ab = &sm.abort_flag;
   const int lane = threadIdx.x & 31;
-  const Item& it = sm.item[k & 1];
-  const TreeInfo ti = tree_view(a, v, it.tree);
-  const int n = it.n, hk = it.hk, bb = it.b, t0 = it.t0;
+  constexpr int kOwn = 64 / KS < 32 ? 64 / KS : 32;  // columns at a time
   if (!warp_wait(&sm.pv_done, (st.g - 1) & 1, c.status, ab, kSiteTreeSoftEnd)) return false;
   tc_fence_after();
-  const bool whole = t0 == 0 && it.t1 == it.tiles;
-  const size_t orow =
-      (static_cast<size_t>(bb) * a.H + hk * a.group + it.r0 / n + row.hrel) * c.N + row.node;
-  const size_t prow = static_cast<size_t>(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * S::kRows + row.rr;
+  const Item& it = sm.item[k & 1];
+  const bool whole = it.t0 == 0 && it.t1 == it.tiles;
   const uint32_t* odd = sm.odd[k & 1];
   const bool any_odd = (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
-  uint8_t* const merge = v.sq + (k & 1) * kQBytes;  // [KS - 1][kRows] rows of 128 bytes, swizzled
-  float M = st.m, L = st.l, f[KS];
-  f[0] = 1.0f;
-  if (KS > 1 && row.copy > 0 && row.warp_live)
-    v.merge_ml[(row.copy - 1) * S::kRows + row.rr] = make_float2(st.m, st.l);
-#pragma unroll 1
-  for (int q = 0; q < 4; ++q) {
-    uint32_t ov[16];
-    float* o = reinterpret_cast<float*>(ov);
-    if (row.warp_live) tmem_ld_cols<16>(row.lanes + kColO + 16 * q, ov);
-    if (KS > 1) {
-      if ((q & 1) == 0) {
-        if (row.copy > 0 && row.warp_live) {
-          const int mr = (row.copy - 1) * S::kRows + row.rr;
-          uint32_t o2[16];
-          tmem_ld_cols<16>(row.lanes + kColO + 16 * q + 16, o2);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            *reinterpret_cast<uint4*>(merge + mr * 128 + ((y ^ (mr & 7)) << 4)) =
-                make_uint4(ov[4 * y], ov[4 * y + 1], ov[4 * y + 2], ov[4 * y + 3]);
-            *reinterpret_cast<uint4*>(merge + mr * 128 + (((y + 4) ^ (mr & 7)) << 4)) =
-                make_uint4(o2[4 * y], o2[4 * y + 1], o2[4 * y + 2], o2[4 * y + 3]);
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.merge_full);
-        if (!warp_wait(&sm.merge_full, q >> 1, c.status, ab, kSiteTreeMerge)) return false;
-        if (q == 0 && row.copy == 0 && row.live) {
-#pragma unroll
-          for (int y = 1; y < KS; ++y) M = fmaxf(M, v.merge_ml[(y - 1) * S::kRows + row.rr].x);
-          f[0] = ex2_approx(st.m - M);
-          L *= f[0];
-#pragma unroll
-          for (int y = 1; y < KS; ++y) {
-            const float2 ml = v.merge_ml[(y - 1) * S::kRows + row.rr];
-            f[y] = ex2_approx(ml.x - M);
-            L += ml.y * f[y];
-          }
-        }
-      }
-      if (row.copy == 0 && row.live) {
-#pragma unroll
-        for (int y = 0; y < 16; ++y) o[y] *= f[0];
-#pragma unroll
-        for (int cp = 1; cp < KS; ++cp) {
-          const int mr = (cp - 1) * S::kRows + row.rr;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float4 x = *reinterpret_cast<const float4*>(
-                merge + mr * 128 + (((y + 4 * (q & 1)) ^ (mr & 7)) << 4));
-            o[4 * y] = fmaf(x.x, f[cp], o[4 * y]);
-            o[4 * y + 1] = fmaf(x.y, f[cp], o[4 * y + 1]);
-            o[4 * y + 2] = fmaf(x.z, f[cp], o[4 * y + 2]);
-            o[4 * y + 3] = fmaf(x.w, f[cp], o[4 * y + 3]);
-          }
-        }
-      }
-      if (q == 1) {
-        // The second half may overwrite the first.
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.merge_free);
-        if (!warp_wait(&sm.merge_free, k & 1, c.status, ab, kSiteTreeMerge)) return false;
-      }
-    }
-    if (row.copy > 0 || !row.live) continue;
+  const size_t orow =
+      (static_cast<size_t>(it.b) * a.H + it.hk * a.group + it.g0 + row.hrel) * c.N + row.node;
+  const size_t prow = static_cast<size_t>(2 * blockIdx.x + (it.t0 == 0 ? 1 : 0)) * S::kRows + row.rr;
+  float M = st.m, L = st.l;
+  // Columns col .. col + kOwn - 1 of the row's output.
+  auto put = [&](float* o, int col) __attribute__((always_inline)) {
     if (any_odd) {
       // Values that are not finite, for the nodes that see them.
+      const TreeInfo ti = tree_view(a, v, it.tree);
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) {
+      for (int i = 0; i < it.n; ++i) {
         if (!(odd[i >> 5] >> (i & 31) & 1) || !tree_sees(ti, row.node, i)) continue;
-        const int slot = it.len + i;
-        int pg = __ldg(c.block_table + static_cast<size_t>(bb) * c.max_blocks + slot / c.page);
+        const int at = it.len + i;
+        int pg = __ldg(c.block_table + static_cast<size_t>(it.b) * c.max_blocks + at / c.page);
         if (pg < 0 || pg >= c.num_pages) pg = 0;
         const uint32_t* vr = reinterpret_cast<const uint32_t*>(
-            a.v_pages + ((static_cast<size_t>(pg) * c.Hkv + hk) * c.page + slot % c.page) * kHeadDim +
-            16 * q);
+            a.v_pages + ((static_cast<size_t>(pg) * c.Hkv + it.hk) * c.page + at % c.page) * kHeadDim +
+            col);
 #pragma unroll
-        for (int y = 0; y < 8; ++y) {
+        for (int y = 0; y < kOwn / 2; ++y) {
           const uint32_t u = __ldg(vr + y);
           if (odd_exp(u)) o[2 * y] += __uint_as_float(u << 16);
           if (odd_exp(u >> 16)) o[2 * y + 1] += __uint_as_float(u & 0xFFFF0000u);
         }
       }
     }
-    if (!whole) {
-      float4* dst = reinterpret_cast<float4*>(a.part + prow * kHeadDim + 16 * q);
+    if (!whole) {  // left to the combine kernel
+      float4* dst = reinterpret_cast<float4*>(a.part + prow * kHeadDim + col);
 #pragma unroll
-      for (int y = 0; y < 4; ++y)
+      for (int y = 0; y < kOwn / 4; ++y)
         dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-      if (q == 0) a.part_ml[prow] = make_float2(M, L);
+      if (col == 0) a.part_ml[prow] = make_float2(M, L);
+      return;
+    }
+    const float inv = 1.0f / L;
+    if (PARTS > 1) {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kHeadDim + col);
+#pragma unroll
+      for (int y = 0; y < kOwn / 4; ++y)
+        dst[y] = make_float4(o[4 * y] * inv, o[4 * y + 1] * inv, o[4 * y + 2] * inv,
+                             o[4 * y + 3] * inv);
     } else {
-      const float inv = 1.0f / L;
-      if (PARTS > 1) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kHeadDim + 16 * q);
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * kHeadDim + col);
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
-          dst[y] = make_float4(o[4 * y] * inv, o[4 * y + 1] * inv, o[4 * y + 2] * inv,
-                               o[4 * y + 3] * inv);
-      } else {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * kHeadDim + 16 * q);
+      for (int y = 0; y < kOwn / 8; ++y) {
+        const float* e = o + 8 * y;
+        dst[y] = make_uint4(pack_bf16x2(e[0] * inv, e[1] * inv), pack_bf16x2(e[2] * inv, e[3] * inv),
+                            pack_bf16x2(e[4] * inv, e[5] * inv), pack_bf16x2(e[6] * inv, e[7] * inv));
+      }
+    }
+    if (col == 0 && a.lse) a.lse[orow] = (M + log2f(L)) * kLn2f;
+  };
+  uint32_t ov[32];
+  float* o = reinterpret_cast<float*>(ov);
+  if (KS == 1) {
+#pragma unroll 1
+    for (int col = 0; col < 64 && row.warp_live; col += 32) {
+      tmem_ld_cols<32>(row.lanes + kColO + col, ov);
+      if (row.live) put(o, col);
+    }
+  } else {
+    uint8_t* const merge = v.sq + (k & 1) * kQBytes;  // 128 rows of 128 bytes
+    const int mine = threadIdx.x, other = mine ^ S::kRows, swz = mine & 7;
+    int col = 32 * (row.copy & 1);  // of o[0]
+    if (row.warp_live) {
+      tmem_ld_cols<32>(row.lanes + kColO + (col ^ 32), ov);
+      hand_row<8>(merge + mine * 128, swz, o);
+      v.merge_ml[mine] = make_float2(M, L);
+      tmem_ld_cols<32>(row.lanes + kColO + col, ov);
+    }
+    // The next maximum and sum, and what is kept of both.
+    auto join = [&](int from, float& f, float& g) {
+      const float2 ml = v.merge_ml[from];
+      const float m2 = fmaxf(M, ml.x);
+      f = ex2_approx(M - m2);
+      g = ex2_approx(ml.x - m2);
+      L = L * f + ml.y * g;
+      M = m2;
+    };
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.merge[0]);
+    if (!warp_wait(&sm.merge[0], k & 1, c.status, ab, kSiteTreeMerge)) return false;
+    float f, g;
+    if (row.warp_live) {
+      join(other, f, g);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float* e = o + 8 * y;
-          dst[y] = make_uint4(pack_bf16x2(e[0] * inv, e[1] * inv), pack_bf16x2(e[2] * inv, e[3] * inv),
-                              pack_bf16x2(e[4] * inv, e[5] * inv), pack_bf16x2(e[6] * inv, e[7] * inv));
+      for (int y = 0; y < 32; ++y) o[y] *= f;
+      join_row<8>(merge + other * 128, swz, g, o);
+    }
+    if (KS == 4) {
+      if (row.warp_live) {
+        v.merge_ml[other] = make_float2(M, L);
+        if (row.copy & 2) {
+          hand_row<4>(merge + other * 128, swz, o);
+#pragma unroll
+          for (int y = 0; y < 16; ++y) o[y] = o[y + 16];
+          col += 16;
+        } else {
+          hand_row<4>(merge + other * 128, swz, o + 16);
         }
       }
-      if (q == 0 && a.lse) a.lse[orow] = (M + log2f(L)) * kLn2f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.merge[1]);
+      if (!warp_wait(&sm.merge[1], k & 1, c.status, ab, kSiteTreeMerge)) return false;
+      if (row.warp_live) {
+        join(other ^ 64, f, g);
+#pragma unroll
+        for (int y = 0; y < 16; ++y) o[y] *= f;
+        join_row<4>(merge + (other ^ 64) * 128, swz, g, o);
+      }
     }
+    if (row.live) put(o, col);
   }
   // O has been read before the next item's products overwrite it: they wait
   // for its p_full, on which every warp arrives after this.
@@ -914,8 +974,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     }
     mbar_init(&sm.p_full, kSoftWarps);
     mbar_init(&sm.pv_done, 1);
-    mbar_init(&sm.merge_full, kSoftWarps);
-    mbar_init(&sm.merge_free, kSoftWarps);
+    mbar_init(&sm.merge[0], kSoftWarps);
+    mbar_init(&sm.merge[1], kSoftWarps);
     mbar_init(&sm.mma_final, 1);
     fence_barrier_init();
     sm.abort_flag = 0;
@@ -985,44 +1045,60 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       fetch();
     }
     int issued = 0, s = 0, phase = 1, k = 0, last_b = -1, tree = 1;
+    Item it;
+    int64_t seq_end = x;  // of the sequence that the last item was of
     for (;; ++k) {
       const ItemInfo info = info_view<S>(a, v, k);
       if (!ok) break;
-      Item it;
       it.t0 = it.t1 = 0;
-      while (x < end) {
-        // The sequence of unit x, at b or behind it.
-        for (;;) {
-          const unsigned ends = __ballot_sync(0xffffffffu, b0 + lane >= b && end_l > x);
-          if (ends) {
-            b = b0 + __ffs(ends) - 1;
-            break;
+      if (x < end) {
+        int at = 0;  // place of unit x in its item
+        if (x < seq_end) {
+          it.r0 += kRows;
+          if (it.r0 >= a.group * it.n) {
+            it.r0 = 0;
+            ++it.hk;
           }
-          b = b0 += 32;
-          fetch();
+        } else {
+          // The sequence of unit x, at b or behind it.
+          for (;;) {
+            const unsigned ends = __ballot_sync(0xffffffffu, b0 + lane >= b && end_l > x);
+            if (ends) {
+              b = b0 + __ffs(ends) - 1;
+              break;
+            }
+            b = b0 += 32;
+            fetch();
+          }
+          it.b = b;
+          it.len = __shfl_sync(0xffffffffu, len_l, b - b0);
+          it.n = __shfl_sync(0xffffffffu, n_l, b - b0);
+          seq_end = __shfl_sync(0xffffffffu, end_l, b - b0);
+          const int64_t local = x - __shfl_sync(0xffffffffu, beg_l, b - b0);
+          it.tiles = (it.len + it.n + kTile - 1) / kTile;
+          it.hk = it.r0 = 0;
+          if (local > 0) {
+            const int unit = it.tiles + kItemCost;
+            const int idx = local < (1 << 30) ? static_cast<int>(local) / unit
+                                              : static_cast<int>(local / unit);
+            at = static_cast<int>(local - static_cast<int64_t>(idx) * unit);
+            const int nrb = (a.group * it.n + kRows - 1) / kRows;
+            it.hk = idx / nrb;
+            it.r0 = (idx - it.hk * nrb) * kRows;
+          }
         }
-        it.b = b;
-        it.len = __shfl_sync(0xffffffffu, len_l, b - b0);
-        it.n = __shfl_sync(0xffffffffu, n_l, b - b0);
-        const int64_t local = x - __shfl_sync(0xffffffffu, beg_l, b - b0);
-        it.tiles = (it.len + it.n + kTile - 1) / kTile;
-        const int unit = it.tiles + kItemCost;
-        const int idx = local < (1 << 30) ? static_cast<int>(local) / unit
-                                          : static_cast<int>(local / unit);
-        const int at = static_cast<int>(local - static_cast<int64_t>(idx) * unit);
-        const int nrb = (a.group * it.n + kRows - 1) / kRows;
-        it.hk = idx / nrb;
-        it.r0 = (idx - it.hk * nrb) * kRows;
         it.r1 = min(it.r0 + kRows, a.group * it.n);
-        const int stop = static_cast<int>(min(static_cast<int64_t>(unit), at + (end - x)));
+        const int stop = static_cast<int>(
+            min(static_cast<int64_t>(it.tiles + kItemCost), at + (end - x)));
+        x += stop - at;
         it.t0 = max(at - kItemCost, 0);
         it.t1 = max(stop - kItemCost, 0);
-        x += stop - at;
-        if (it.t1 > it.t0) break;
-        it.t1 = 0;  // only the fixed cost of an item whose tiles are another CTA's
+        // (none: only the fixed cost of an item whose tiles are the next CTA's)
+        if (it.t1 <= it.t0) it.t1 = 0;
       }
       const int n = it.n, len = it.len;
       const int g0 = it.t1 ? it.r0 / n : 0, heads = it.t1 ? (it.r1 - 1) / n - g0 + 1 : 0;
+      it.g0 = g0;
       const float* trow = a.table + static_cast<size_t>(it.hk * a.group + g0) * a.tab_len;
       const int y0 = a.tab_zero - (len + n - 1);  // entry of key 0 for the last position
       const int nwin = window_floats(kTile, n);
@@ -1124,10 +1200,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         }
         break;
       }
-      const int nrows = it.r1 - it.r0;
       // Queries: the item's rows, once for each copy, 16-byte chunks swizzled
       // as the product reads them; eight lanes a row.
       {
+        const int nrows = it.r1 - it.r0;
         const uint32_t dst = smem_u32(sq + (k & 1) * kQBytes);
         const uint16_t* base =
             a.q + (static_cast<size_t>(it.b) * a.H + it.hk * a.group) * c.N * kHeadDim;
@@ -1136,7 +1212,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 #pragma unroll 2
         for (int rr = lane >> 3; rr < padded; rr += 4) {
           const bool live = rr < nrows;
-          const uint16_t* src = base + (live ? static_cast<size_t>(hg) * c.N + node : 0) * kHeadDim + 8 * ch;
+          const uint16_t* src =
+              base + (live ? static_cast<size_t>(hg) * c.N + node : 0) * kHeadDim + 8 * ch;
 #pragma unroll
           for (int cp = 0; cp < KS; ++cp) {
             const int row = cp * kRows + rr;
@@ -1144,6 +1221,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           }
           for (node += 4; node >= n; node -= n) ++hg;
         }
+      }
+      if (a.ssmax) {
+        if (lane < heads) info.s[lane] = s_lane;
+        for (int h = lane + 32; h < heads; h += 32)
+          info.s[h] = __ldg(a.s + it.hk * a.group + g0 + h);
       }
       if (it.b != last_b) {
         tree ^= 1;
@@ -1162,20 +1244,6 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           for (int y = lane; y < n; y += 32)
             cp_async4(smem_u32(info.near + h * n + y),
                       trow + static_cast<size_t>(h) * a.tab_len + a.tab_zero - y);
-      }
-#pragma unroll 1
-      for (int rr = lane; rr < kRows; rr += 32) {
-        const int r = it.r0 + rr;
-        const bool live = rr < nrows;
-        const int hg = live ? r / n : g0, node = live ? r - hg * n : 0;
-        float sc = 0.125f * static_cast<float>(kLog2e);
-        if (a.ssmax) {
-          const float sh = __shfl_sync(0xffffffffu, s_lane, (hg - g0) & 31);
-          sc *= (hg - g0 < 32 ? sh : __ldg(a.s + it.hk * a.group + hg)) *
-                logf(static_cast<float>(len + tree_view(a, v, tree).depth[node] + 1));
-        }
-        info.row[rr] = live ? (hg - g0) * kTreeMax + node : -1;
-        info.scale[rr] = sc;
       }
       if (lane == 0) *info.it = it;
       if (lane < kTreeMax / 32) sm.odd[k & 1][lane] = 0;
@@ -1380,7 +1448,7 @@ constexpr size_t kSmemOne = 227 * 1024;
 // Shared memory of a CTA besides its ring stages, and of one stage.
 size_t smem_fixed(const TreeArgs& a) {
   return 1024 + 2 * kQBytes + sizeof(TreeSmem) + 44 * static_cast<size_t>(a.nodes) +
-         8 * static_cast<size_t>(a.near) + 16 * a.rows + 8 * (kRowsMax - a.rows);
+         8 * static_cast<size_t>(a.near) + 8 * a.rows + 8 * kRowsMax;
 }
 size_t smem_stage(const TreeArgs& a) {
   return 2 * static_cast<size_t>(a.tile) * kHeadDim * 2 + static_cast<size_t>(a.win_stage) * 4;
@@ -1399,7 +1467,7 @@ cudaError_t launch_copies(const CUtensorMap& tk, const CUtensorMap& tv, const Tr
 
 template <int PARTS>
 cudaError_t launch_parts(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a,
-                         cudaStream_t st) {
+                          cudaStream_t st) {
   switch (a.rows) {
     case 32:
       return launch_copies<PARTS, 4>(tk, tv, a, st);
@@ -1449,7 +1517,7 @@ cudaError_t launch_tree_prep(const TreeArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_tree(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a,
-                        cudaStream_t st) {
+                          cudaStream_t st) {
   return a.o_fp32 ? launch_parts<3>(tk, tv, a, st) : launch_parts<1>(tk, tv, a, st);
 }
 
