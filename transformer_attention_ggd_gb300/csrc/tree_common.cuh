@@ -51,7 +51,7 @@ struct KeepArgs {
 // the plan is the running sum of the sequences' units over all their items,
 // and CTA c of `active` takes units [W c / active, W (c+1) / active) of the W
 // in all.
-constexpr int kItemCost = 5;     // an item's fixed cost, in tiles
+constexpr int kItemCost = 4;     // an item's fixed cost, in tiles
 constexpr int kTreeCtas = 304;   // most CTAs (two per SM)
 
 struct TreeArgs {
