@@ -51,7 +51,10 @@ struct KeepArgs {
 // the plan is the running sum of the sequences' units over all their items,
 // and CTA c of `active` takes units [W c / active, W (c+1) / active) of the W
 // in all.
-constexpr int kItemCost = 4;     // an item's fixed cost, in tiles
+// An item's fixed cost, in tiles.  3, 4 and 7 measured 55.4, 54.0 and 53.9 us
+// (13 sequences of 9001 keys, 21 nodes), 104.7, 105.6 and 107.6 (32 of 16384,
+// single tokens), 33.5, 33.5 and 35.1 (8 of 4096, fp32 output).
+constexpr int kItemCost = 4;
 constexpr int kTreeCtas = 304;   // most CTAs (two per SM)
 
 struct TreeArgs {
@@ -72,14 +75,18 @@ struct TreeArgs {
   int H, group, prior, ssmax, o_fp32;
   int tab_len, tab_zero;
   int rows;           // rows of an item, at most: 32, 64 or 128
-  int tile;           // keys of a tile: 64 with 128 rows, else 128
+  int tile;           // keys of a tile, 64 or 128
   int ctas, least;    // CTAs of the launch; units that one gets at least
   int stages;         // ring stages
   int win_stage;      // floats of a stage's table windows
   int nodes, near;    // nodes (a multiple of 32) and table entries that an item keeps
 };
 
-// Rows of an item for `rows` (head, node) pairs.
+// Rows of an item for `rows` (head, node) pairs: Tensor Memory's 128, or the half
+// or quarter that holds them all; they then stand there two or four times, each
+// copy with its part of the keys.  Against 128 always, a call: 455 and 575 us
+// with 32 rows and 64 sequences of 32768 keys, 105 and 133 with 4 rows and
+// 16384 keys, 106 and 113 with 64 rows and 131072.
 inline int tree_rows(int64_t rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 // Table row: distances 0 .. Tmax at entries Tmax .. 0 and, behind entry
 // Tmax, room for windows that reach past the last key.
