@@ -298,6 +298,32 @@ def test_tree_masked_nan_and_inf_have_no_effect():
                 assert torch.equal(o[:, :, n, 9:], o2[:, :, n, 9:])
 
 
+@pytest.mark.parametrize("ln", [0, 61, 5000])
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (8, 2), (10, 1)])
+def test_tree_infinite_drafted_values_in_every_layout(H, Hkv, ln):
+    """12, 48 and 120 rows a key head, on one CTA and cut: an infinite drafted
+    value reaches the nodes that see it, in its dimensions, and changes no
+    other bit."""
+    N, page = 12, 64
+    parents = [np.array([-1, 0, 0, 1, 1, 2, 2, 3, 4, 5, 6, 6])]
+    c = Cache(23, Hkv, page, [ln + N], -(-(ln + N) // page), NAN)
+    t = [dev_f32(_prm(np.random.default_rng(3), H, False)[n]) for n in ("alpha", "beta", "mu", "s")]
+    q = _normal(c.gen, 1, H, N, 64)
+    args = (c.table, _i32([ln]), *t)
+    clean = c.v.clone()
+    bad = {4: (float("inf"), [0, 20, 33]), 6: (float("-inf"), [15, 47, 63])}
+    for i, (value, dims) in bad.items():
+        c.v[int(c.table[0, (ln + i) // page]), :, (ln + i) % page, dims] = value
+    for out in (torch.float32, torch.bfloat16):
+        kw = dict(parents=_i32(parents), ssmax=True, o_dtype=out)
+        o, lse = ba.attention_decode_tree_paged(q, c.k, c.v, *args, **kw)
+        want, lse2 = ba.attention_decode_tree_paged(q, c.k, clean, *args, **kw)
+        for n in range(N):
+            for i in set(path_to(parents[0], n)) & set(bad):
+                want[:, :, n, bad[i][1]] = bad[i][0]
+        assert torch.equal(o, want) and torch.equal(lse, lse2)
+
+
 def test_tree_of_one_node_is_the_paged_decode():
     """A single node behind len keys is a decode over len + 1 keys, and the
     oracle's decode over them."""
@@ -600,6 +626,33 @@ def test_serving_step_on_another_stream():
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
         _serve(2, s)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_helpers_clear_their_outputs_on_the_stream_they_are_given(raw):
+    """The current stream is busy for some milliseconds: what the helpers clear
+    before the kernels write it must not wait behind that."""
+    B, H, N = 2, 3, 4
+    c = Cache(161, H, 64, [70 + N] * B, 2)
+    t = [dev_f32(_prm(c.rng, H, False)[n]) for n in ("alpha", "beta", "mu", "s")]
+    q, k, v = (_normal(c.gen, B, H, N, 64) for _ in range(3))
+    lens, new = _i32([70] * B), _i32([N, N - 1])
+    par, acc = _i32([[-1, 0, 0, 2]] * B), _i32([3, 2])
+
+    def step(stream):
+        q2 = ba.kv_append_paged(k, v, c.k, c.v, c.table, lens, new, par, q, ba.make_rope(),
+                                stream=stream)
+        o, lse = ba.attention_decode_tree_paged(q2, c.k, c.v, c.table, lens, *t, draft_lens=new,
+                                                parents=par, stream=stream)
+        return q2, o, lse, ba.kv_keep_paged(c.k, c.v, c.table, lens, acc, par, new, stream=stream)
+
+    want = step(None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)
+    got = step(s.cuda_stream if raw else s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
 def test_captured_step_replays_with_new_lengths():

@@ -22,6 +22,7 @@ and workspace with torch and then call the same entry points.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -853,6 +854,18 @@ def attention_decode_paged(q, k_pages, v_pages, block_table, cache_lens, alpha, 
     return o, lse
 
 
+def _on(stream):
+    """Makes `stream` (a torch stream, a raw handle or None) the current one: what
+    is allocated and cleared for a call is then ready when its kernels run, and
+    is not given to another stream before they are done."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
 def kv_append_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_lens=None, parents=None,
                     q=None, rope=None, ws=None, stream=None):
     """Append k, v [B, Hkv, N, 64] to the pages behind cache_lens committed
@@ -863,9 +876,11 @@ def kv_append_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_lens=No
     if q is not None:
         # rows behind new_lens are not written: no uninitialised memory in them
         make = torch.empty if new_lens is None else torch.zeros
-        q_out = make(q.shape, dtype=q.dtype, device=q.device)
+        with _on(stream):
+            q_out = make(q.shape, dtype=q.dtype, device=q.device)
     if ws is None:
-        ws = cache_workspace(k_pages.device)
+        with _on(stream):
+            ws = cache_workspace(k_pages.device)
     bam_kv_append_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_lens, parents, q,
                         q_out, rope, ws, stream)
     return q_out
@@ -880,11 +895,12 @@ def attention_decode_tree_paged(q, k_pages, v_pages, block_table, cache_lens, al
     import torch
     B, H, N, D = q.shape
     make = torch.empty if draft_lens is None else torch.zeros
-    o = make((B, H, N, D), dtype=o_dtype or torch.float32, device=q.device)
-    lse = make((B, H, N), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = tree_workspace(B, H, k_pages.shape[1], N, k_pages.shape[2] * block_table.shape[1],
-                            q.device)
+    with _on(stream):
+        o = make((B, H, N, D), dtype=o_dtype or torch.float32, device=q.device)
+        lse = make((B, H, N), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = tree_workspace(B, H, k_pages.shape[1], N, k_pages.shape[2] * block_table.shape[1],
+                                q.device)
     prm = make_params(alpha, beta, mu, s, eps, True, ssmax, prior)
     bam_attn_decode_tree_paged(q, k_pages, v_pages, block_table, cache_lens, draft_lens, parents,
                                o, lse, prm, ws, stream)
@@ -896,10 +912,11 @@ def kv_keep_paged(k_pages, v_pages, block_table, cache_lens, accepted, parents, 
     """Keep the accepted path of each draft; returns the new lengths (written
     to new_lens, which may be cache_lens, if given)."""
     import torch
-    if new_lens is None:
-        new_lens = torch.empty_like(cache_lens)
-    if ws is None:
-        ws = cache_workspace(k_pages.device)
+    with _on(stream):
+        if new_lens is None:
+            new_lens = torch.empty_like(cache_lens)
+        if ws is None:
+            ws = cache_workspace(k_pages.device)
     bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, parents, accepted,
                       new_lens, ws, stream)
     return new_lens
