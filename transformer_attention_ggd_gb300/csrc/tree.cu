@@ -102,6 +102,20 @@ struct __align__(16) TreeSmem {
 
 // ---------------------------------------------------------------- plan and table
 
+// Units of an item: its fixed cost, then one for a tile of committed keys and
+// tail_cost for one that holds drafted keys.  A tile belongs to the CTA that
+// its last unit is dealt to.
+__device__ __forceinline__ int item_units(int tile, int tail_cost, int len, int n) {
+  const int tiles = (len + n + tile - 1) / tile;
+  return kItemCost + tiles + (tail_cost - 1) * (tiles - len / tile);
+}
+// Tiles of an item that end at or before its unit `at`; `plain` of them hold
+// committed keys alone.
+__device__ __forceinline__ int tiles_before(int tail_cost, int plain, int at) {
+  const int y = at - kItemCost;
+  return y <= 0 ? 0 : y <= plain ? y : plain + (y - plain) / tail_cost;
+}
+
 // Block (0, 0) starts the call and sums the sequences' tiles; the blocks
 // together write the table of b_h(d) for the distances that occur.
 __global__ void __launch_bounds__(256) bam_tree_prep_kernel(const TreeArgs a) {
@@ -124,7 +138,7 @@ __global__ void __launch_bounds__(256) bam_tree_prep_kernel(const TreeArgs a) {
         ok &= cache_lengths(c, b0 + tid, &len, &n);
         if (n > 0)
           x = static_cast<int64_t>(c.Hkv) * ((a.group * n + a.rows - 1) / a.rows) *
-              ((len + n + a.tile - 1) / a.tile + kItemCost);
+              item_units(a.tile, a.tail_cost, len, n);
       }
       sum[tid] = x;
       __syncthreads();
@@ -167,9 +181,9 @@ __global__ void __launch_bounds__(256) bam_tree_prep_kernel(const TreeArgs a) {
 
 // ---------------------------------------------------------------- walking the plan
 
-// CTAs that take part: each gets at least `least` units.
+// CTAs that take part: each gets at least `least` units, if there are as many.
 __device__ __forceinline__ int active_ctas(int64_t all, int ctas, int least) {
-  const int64_t n = (all + least - 1) / least;
+  const int64_t n = all / least;
   return n < 1 ? 1 : n < ctas ? static_cast<int>(n) : ctas;
 }
 // (A 64-bit division is a hundred instructions; all * cta fits 32 bits in all
@@ -389,6 +403,15 @@ __host__ __device__ constexpr int tree_tile(int parts, int ks) {
   return parts == 1 && ks > 1 ? 128 : 64;
 }
 
+// A tile with drafted keys keeps its logits in registers where they are few;
+// else they go back to Tensor Memory between the maximum and the weights.
+__host__ __device__ constexpr bool tree_once(int parts, int ks) {
+  return tree_tile(parts, ks) / ks * parts <= 48;
+}
+__host__ __device__ constexpr int tree_tail_cost(int parts, int ks) {
+  return tree_once(parts, ks) ? 1 : kTailCost;
+}
+
 // Sizes of a kernel with PARTS parts of a weight and KS copies of a row.
 template <int PARTS, int KS>
 struct Shape {
@@ -396,6 +419,8 @@ struct Shape {
   static constexpr int kGroups = kRows / 32;         // warps of a copy
   static constexpr int kTile = tree_tile(PARTS, KS);  // keys of a tile
   static constexpr int kCols = kTile / KS;           // of which one copy's
+  static constexpr bool kOnce = tree_once(PARTS, KS);
+  static constexpr int kTailCost = tree_tail_cost(PARTS, KS);
   static constexpr int kTileBytes = kTile * kHeadDim * 2;
   static constexpr int kPCols = kTile / 2;           // columns of a part of P
   static constexpr uint32_t kColP = kTile;
@@ -663,8 +688,7 @@ __device__ __forceinline__ void tail_logits(uint32_t taddr, const SoftRow& row, 
   }
 }
 
-// A tile with keys that not every row sees.  Many columns are read twice, 16 at
-// a time, so that this rarer code takes few registers from the other.
+// A tile with keys that not every row sees, 16 columns at a time.
 template <int PARTS, int KS>
 __device__ __forceinline__ void soft_tail(const TreeArgs& a, const View& v, const SoftRow& row,
                                           SoftState& st, int k) {
@@ -680,7 +704,7 @@ __device__ __forceinline__ void soft_tail(const TreeArgs& a, const View& v, cons
   const float* near = info.near + row.hrel * n + row.depth;  // of an ancestor: near[-its depth]
   const uint64_t vis = row.live ? tile_mask(ti.seen[row.node], j0 + row.k0, len) : 0;
   const int nc = len - j0 - row.k0;
-  constexpr bool kOnce = S::kCols * PARTS <= 48;
+  constexpr bool kOnce = S::kOnce;
   constexpr int kBlocks = S::kCols / 16;
   float z[kOnce ? S::kCols : 16];
   float mx = kNoMax, scale;
@@ -695,9 +719,11 @@ __device__ __forceinline__ void soft_tail(const TreeArgs& a, const View& v, cons
 #pragma unroll 1
       for (int q = 0; q < kBlocks; ++q) {
         tail_logits(row.lanes + row.k0, row, w, near, ti.depth, vis, 16 * q, nc, n, z);
+        tmem_st_32x32b_x16(row.lanes + row.k0 + 16 * q, reinterpret_cast<const uint32_t*>(z));
 #pragma unroll
         for (int y = 0; y < 16; y += 2) mx = fmax3(mx, z[y], z[y + 1]);
       }
+      tmem_st_wait();
     }
   }
   if (kOnce) soft_free_s(sm, st);
@@ -759,7 +785,7 @@ __device__ __forceinline__ void soft_tail(const TreeArgs& a, const View& v, cons
     } else {
 #pragma unroll 1
       for (int q = 0; q < kBlocks; ++q) {
-        tail_logits(row.lanes + row.k0, row, w, near, ti.depth, vis, 16 * q, nc, n, z);
+        tmem_ld_cols<16>(row.lanes + row.k0 + 16 * q, reinterpret_cast<uint32_t*>(z));
         weights(z, q);
       }
     }
@@ -1028,7 +1054,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     if (early) {
       if (lane < c.B) cache_lengths(c, lane, &len_l, &n_l);
       end_l = n_l > 0 ? static_cast<int64_t>(c.Hkv) * ((a.group * n_l + kRows - 1) / kRows) *
-                            ((len_l + n_l + kTile - 1) / kTile + kItemCost)
+                            item_units(kTile, S::kTailCost, len_l, n_l)
                       : 0;
       beg_l = end_l;
 #pragma unroll
@@ -1062,6 +1088,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     }
     int issued = 0, s = 0, phase = 1, k = 0, last_b = -1, tree = 1;
     Item it;
+    int units = 0, plain = 0;  // of an item of the sequence
     int64_t seq_end = x;  // of the sequence that the last item was of
     for (;; ++k) {
       const ItemInfo info = info_view<S>(a, v, k);
@@ -1092,24 +1119,24 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           seq_end = __shfl_sync(0xffffffffu, end_l, b - b0);
           const int64_t local = x - __shfl_sync(0xffffffffu, beg_l, b - b0);
           it.tiles = (it.len + it.n + kTile - 1) / kTile;
+          plain = it.len / kTile;
+          units = item_units(kTile, S::kTailCost, it.len, it.n);
           it.hk = it.r0 = 0;
           if (local > 0) {
-            const int unit = it.tiles + kItemCost;
-            const int idx = local < (1 << 30) ? static_cast<int>(local) / unit
-                                              : static_cast<int>(local / unit);
-            at = static_cast<int>(local - static_cast<int64_t>(idx) * unit);
+            const int idx = local < (1 << 30) ? static_cast<int>(local) / units
+                                              : static_cast<int>(local / units);
+            at = static_cast<int>(local - static_cast<int64_t>(idx) * units);
             const int nrb = (a.group * it.n + kRows - 1) / kRows;
             it.hk = idx / nrb;
             it.r0 = (idx - it.hk * nrb) * kRows;
           }
         }
         it.r1 = min(it.r0 + kRows, a.group * it.n);
-        const int stop = static_cast<int>(
-            min(static_cast<int64_t>(it.tiles + kItemCost), at + (end - x)));
+        const int stop = static_cast<int>(min(static_cast<int64_t>(units), at + (end - x)));
         x += stop - at;
-        it.t0 = max(at - kItemCost, 0);
-        it.t1 = max(stop - kItemCost, 0);
-        // (none: only the fixed cost of an item whose tiles are the next CTA's)
+        it.t0 = tiles_before(S::kTailCost, plain, at);
+        it.t1 = tiles_before(S::kTailCost, plain, stop);
+        // (none: the share ends before the end of the item's next tile)
         if (it.t1 <= it.t0) it.t1 = 0;
       }
       const int n = it.n, len = it.len;
@@ -1420,31 +1447,53 @@ __global__ void __launch_bounds__(256) bam_tree_combine_kernel(const TreeArgs a)
     } else {
       const int g = h % a.group, r = g * n + t, rb = r / a.rows;
       const int nrb = (a.group * n + a.rows - 1) / a.rows;
-      const int tiles = (len + n + a.tile - 1) / a.tile;
-      const int64_t first = __ldcg(a.plan + b) + kItemCost +
-                            static_cast<int64_t>(h / a.group * nrb + rb) * (tiles + kItemCost);
-      const int c0 = range_owner(all, active, first);
-      const int c1 = range_owner(all, active, first + tiles - 1);
+      const int units = item_units(a.tile, a.tail_cost, len, n);
+      const int64_t first =
+          __ldcg(a.plan + b) + static_cast<int64_t>(h / a.group * nrb + rb) * units;
+      // the CTAs of its first and last tile
+      const int c0 = range_owner(all, active,
+                                 first + kItemCost + (len < a.tile ? a.tail_cost - 1 : 0));
+      const int c1 = range_owner(all, active, first + units - 1);
       if (c0 == c1) continue;
       const int rr = r - rb * a.rows;
       auto part_row = [&](int cta) {
         return static_cast<size_t>(2 * cta + (cta == c0 ? 1 : 0)) * a.rows + rr;
       };
+      // 32 parts at a time: their maxima and sums one a lane, and the outputs
+      // eight in flight.
       float M = kNoMax, L = 0.0f;
-      for (int x = c0 + lane; x <= c1; x += 32) M = fmaxf(M, __ldcg(a.part_ml + part_row(x)).x);
-#pragma unroll
-      for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
       v = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-      for (int x = c0; x <= c1; ++x) {
-        const size_t pr = part_row(x);
-        const float2 ml = __ldcg(a.part_ml + pr);
-        const float2 y = __ldcg(reinterpret_cast<const float2*>(a.part + pr * kHeadDim) + lane);
-        const float f = ex2_approx(ml.x - M);
-        L += ml.y * f;
-        v.x += y.x * f;
-        v.y += y.y * f;
+      for (int x0 = c0; x0 <= c1; x0 += 32) {
+        const int parts = min(32, c1 + 1 - x0);
+        const float2 ml =
+            lane < parts ? __ldcg(a.part_ml + part_row(x0 + lane)) : make_float2(kNoMax, 0.0f);
+        float m = fmaxf(M, ml.x);
+#pragma unroll
+        for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        const float old = ex2_approx(M - m), f = lane < parts ? ex2_approx(ml.x - m) : 0.0f;
+        M = m;
+        L = L * old + ml.y * f;  // (of this lane's parts)
+        v.x *= old;
+        v.y *= old;
+        for (int i = 0; i < parts; i += 8) {
+          float2 y[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (i + u < parts)
+              y[u] = __ldcg(reinterpret_cast<const float2*>(a.part + part_row(x0 + i + u) * kHeadDim) +
+                            lane);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const float g = __shfl_sync(0xffffffffu, f, (i + u) & 31);
+            if (i + u < parts) {
+              v.x += y[u].x * g;
+              v.y += y[u].y * g;
+            }
+          }
+        }
       }
+#pragma unroll
+      for (int off = 16; off; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
       v.x /= L;
       v.y /= L;
       lse = (M + log2f(L)) * kLn2f;
@@ -1520,7 +1569,9 @@ bool tree_config(TreeArgs* a, int sms) {
   a->stages = static_cast<int>((budget - fixed) / stage);
   if (a->stages > kMaxStages) a->stages = kMaxStages;
   a->ctas = per_sm * sms < kTreeCtas ? per_sm * sms : kTreeCtas;
-  a->least = 2;
+  // Every CTA between an item's first and last gets one of its tiles.
+  a->tail_cost = tree_tail_cost(a->o_fp32 ? 3 : 1, kRowsMax / a->rows);
+  a->least = a->tail_cost > 2 ? a->tail_cost : 2;
   return a->stages >= 2 && a->ctas >= 1;
 }
 

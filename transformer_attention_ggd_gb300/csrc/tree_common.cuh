@@ -47,14 +47,20 @@ struct KeepArgs {
 // Tree attention: the rows of a (sequence, key head) are its group * n
 // (query head, node) pairs, row r = (head r / n, node r % n), taken `rows` at
 // a time; such an item reads the tiles of 64 or 128 keys that hold the sequence's
-// len + n keys.  An item counts as its tiles and kItemCost units before them;
+// len + n keys.  An item counts as kItemCost units and those of its tiles;
 // the plan is the running sum of the sequences' units over all their items,
 // and CTA c of `active` takes units [W c / active, W (c+1) / active) of the W
 // in all.
-// An item's fixed cost, in tiles.  3, 4 and 7 measured 55.4, 54.0 and 53.9 us
-// (13 sequences of 9001 keys, 21 nodes), 104.7, 105.6 and 107.6 (32 of 16384,
-// single tokens), 33.5, 33.5 and 35.1 (8 of 4096, fp32 output).
+// An item's fixed cost, in units of a tile of committed keys.  3, 4 and 7
+// measured 55.4, 54.0 and 53.9 us (13 sequences of 9001 keys, 21 nodes), 104.7,
+// 105.6 and 107.6 (32 of 16384, single tokens), 33.5, 33.5 and 35.1 (8 of 4096,
+// fp32 output).
 constexpr int kItemCost = 4;
+// Units of a tile with drafted keys where its logits do not stay in registers.
+// 1, 2 and 3 measured 83.0, 80.4 and 79.7 us (4 chains of 128 nodes, 20000
+// keys), 52.5, 51.5 and 51.6 (13 of 9001, 21 nodes), 146, 148 and 151 (100 of
+// 600, 40 nodes, 8 heads a key head, fp32 output).
+constexpr int kTailCost = 2;
 constexpr int kTreeCtas = 304;   // most CTAs (two per SM)
 
 struct TreeArgs {
@@ -76,6 +82,7 @@ struct TreeArgs {
   int tab_len, tab_zero;
   int rows;           // rows of an item, at most: 32, 64 or 128
   int tile;           // keys of a tile, 64 or 128
+  int tail_cost;      // units of a tile that holds drafted keys
   int ctas, least;    // CTAs of the launch; units that one gets at least
   int stages;         // ring stages
   int win_stage;      // floats of a stage's table windows
