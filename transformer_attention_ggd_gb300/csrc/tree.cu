@@ -181,9 +181,11 @@ __global__ void __launch_bounds__(256) bam_tree_prep_kernel(const TreeArgs a) {
 
 // ---------------------------------------------------------------- walking the plan
 
-// CTAs that take part: each gets at least `least` units, if there are as many.
-__device__ __forceinline__ int active_ctas(int64_t all, int ctas, int least) {
-  const int64_t n = all / least;
+// CTAs that take part: each gets two units or more, if there are as many, so that
+// every CTA between the first and the last of an item gets one of its tiles.
+static_assert(kTailCost <= 2, "a CTA could get no tile of an item between its first and last");
+__device__ __forceinline__ int active_ctas(int64_t all, int ctas) {
+  const int64_t n = all >> 1;
   return n < 1 ? 1 : n < ctas ? static_cast<int>(n) : ctas;
 }
 // (A 64-bit division is a hundred instructions; all * cta fits 32 bits in all
@@ -1067,7 +1069,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     } else {
       all = __ldcg(a.plan + c.B);
     }
-    const int active = active_ctas(all, a.ctas, a.least), cta = blockIdx.x;
+    const int active = active_ctas(all, a.ctas), cta = blockIdx.x;
     int64_t x = 0, end = 0;
     if (all > 0 && cta < active) {
       x = range_beg(all, active, cta);
@@ -1159,7 +1161,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       // tiles come first: where the prior falls off with distance, as it mostly
       // does, the first tiles then hold the largest logits, and O is hardly
       // ever rescaled.
-      int t = it.t1 - 1, pages = 0;
+      int t = it.t1 - 1, pages = 0, page_rows = 0;
       auto issue_tiles = [&](bool wait) {
         for (; t >= it.t0; --t) {
           if (issued >= a.stages) {
@@ -1174,11 +1176,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           constexpr int kBoxes = kTile / kBox, kAhead = 32 / kBoxes;
           const int ahead = (it.t1 - 1 - t) % kAhead;
           if (ahead == 0) {
-            // page numbers of the boxes of the next tiles, one a lane
+            // pages of the boxes of the next tiles and their rows in them, one a lane
             const int tl = t - lane / kBoxes, key = tl * kTile + lane % kBoxes * kBox;
-            pages = 0;
+            pages = page_rows = 0;
             if (tl >= it.t0 && key < len + n) {
-              pages = __ldg(c.block_table + static_cast<size_t>(it.b) * c.max_blocks + key / c.page);
+              const int blk = key / c.page;
+              page_rows = key - blk * c.page;
+              pages = __ldg(c.block_table + static_cast<size_t>(it.b) * c.max_blocks + blk);
               if (pages < 0 || pages >= c.num_pages) {
                 args_ok = false;
                 pages = 0;
@@ -1188,17 +1192,19 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           // Boxes that hold no key are not loaded: their rows of S are out of
           // sight and their rows of V are made zero.
           const int boxes = min(kBoxes, (len + n - t * kTile + kBox - 1) / kBox);
-          int plane[kBoxes];
+          int plane[kBoxes], row[kBoxes];
 #pragma unroll
-          for (int x2 = 0; x2 < kBoxes; ++x2)
+          for (int x2 = 0; x2 < kBoxes; ++x2) {
             plane[x2] = __shfl_sync(0xffffffffu, pages, ahead * kBoxes + x2) * c.Hkv + it.hk;
+            row[x2] = __shfl_sync(0xffffffffu, page_rows, ahead * kBoxes + x2);
+          }
           if (lane == 0) {
             mbar_arrive_expect_tx(&sm.k_full[s], boxes * kBoxBytes + heads * nwin * 4);
 #pragma unroll
             for (int x2 = 0; x2 < kBoxes; ++x2)
               if (x2 < boxes)
                 tma_load_3d(sk + s * kTileBytes + x2 * kBoxBytes, &tk, &sm.k_full[s], 0,
-                            (t * kTile + x2 * kBox) % c.page, plane[x2]);
+                            row[x2], plane[x2]);
           }
           __syncwarp();
           if (!early) issue_windows(t, s);
@@ -1212,7 +1218,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             for (int x2 = 0; x2 < kBoxes; ++x2)
               if (ok && x2 < boxes)
                 tma_load_3d(sv_ring + s * kTileBytes + x2 * kBoxBytes, &tv, &sm.v_full[s], 0,
-                            (t * kTile + x2 * kBox) % c.page, plane[x2]);
+                            row[x2], plane[x2]);
           }
           __syncwarp();
           ++issued;
@@ -1244,25 +1250,32 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         break;
       }
       // Queries: the item's rows, once for each copy, 16-byte chunks swizzled
-      // as the product reads them; eight lanes a row.
+      // as the product reads them; eight lanes a row.  Without shared heads, or
+      // with all N nodes drafted, the rows lie one after the other.
       {
-        const int nrows = it.r1 - it.r0;
-        const uint32_t dst = smem_u32(sq + (k & 1) * kQBytes);
+        const int nrows = it.r1 - it.r0, padded = (nrows + 31) & ~31;
+        const int ch = lane & 7, r4 = lane >> 3;
+        const uint32_t dst = smem_u32(sq + (k & 1) * kQBytes) + r4 * 128 + ((ch ^ r4) << 4);
         const uint16_t* base =
-            a.q + (static_cast<size_t>(it.b) * a.H + it.hk * a.group) * c.N * kHeadDim;
-        const int ch = lane & 7, padded = (nrows + 31) & ~31;
-        int hg = (it.r0 + (lane >> 3)) / n, node = it.r0 + (lane >> 3) - hg * n;
-#pragma unroll 2
-        for (int rr = lane >> 3; rr < padded; rr += 4) {
-          const bool live = rr < nrows;
-          const uint16_t* src =
-              base + (live ? static_cast<size_t>(hg) * c.N + node : 0) * kHeadDim + 8 * ch;
+            a.q + (static_cast<size_t>(it.b) * a.H + it.hk * a.group) * c.N * kHeadDim + 8 * ch;
+        // Row rr = r4 + 4 x of the item, from `src` (any address if it is none).
+        auto copy = [&](int rr, const uint16_t* src) __attribute__((always_inline)) {
+          const uint32_t d = (dst ^ ((rr & 4) << 4)) + (rr - r4) * 128;
 #pragma unroll
-          for (int cp = 0; cp < KS; ++cp) {
-            const int row = cp * kRows + rr;
-            cp_async16(dst + row * 128 + ((ch ^ (row & 7)) << 4), src, live);
+          for (int cp = 0; cp < KS; ++cp) cp_async16(d + cp * kRows * 128, src, rr < nrows);
+        };
+        if (a.group == 1 || n == c.N) {
+          const uint16_t* src = base + static_cast<size_t>(it.r0 + r4) * kHeadDim;
+#pragma unroll 4
+          for (int rr = r4; rr < padded; rr += 4, src += 4 * kHeadDim)
+            copy(rr, rr < nrows ? src : base);
+        } else {
+          int hg = (it.r0 + r4) / n, node = it.r0 + r4 - hg * n;
+#pragma unroll 2
+          for (int rr = r4; rr < padded; rr += 4) {
+            copy(rr, rr < nrows ? base + (static_cast<size_t>(hg) * c.N + node) * kHeadDim : base);
+            for (node += 4; node >= n; node -= n) ++hg;
           }
-          for (node += 4; node >= n; node -= n) ++hg;
         }
       }
       if (a.ssmax) {
@@ -1430,7 +1443,7 @@ __global__ void __launch_bounds__(256) bam_tree_combine_kernel(const TreeArgs a)
   const int lane = threadIdx.x & 31;
   const int64_t rows = static_cast<int64_t>(c.B) * a.H * c.N;
   const int64_t all = __ldcg(a.plan + c.B);
-  const int active = active_ctas(all, a.ctas, a.least);
+  const int active = active_ctas(all, a.ctas);
   const bool gave_up = *reinterpret_cast<volatile int*>(&c.status->abort) != 0;
   for (int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5); row < rows; row += gridDim.x * 8ll) {
     const int t = static_cast<int>(row % c.N);
@@ -1569,9 +1582,7 @@ bool tree_config(TreeArgs* a, int sms) {
   a->stages = static_cast<int>((budget - fixed) / stage);
   if (a->stages > kMaxStages) a->stages = kMaxStages;
   a->ctas = per_sm * sms < kTreeCtas ? per_sm * sms : kTreeCtas;
-  // Every CTA between an item's first and last gets one of its tiles.
   a->tail_cost = tree_tail_cost(a->o_fp32 ? 3 : 1, kRowsMax / a->rows);
-  a->least = a->tail_cost > 2 ? a->tail_cost : 2;
   return a->stages >= 2 && a->ctas >= 1;
 }
 

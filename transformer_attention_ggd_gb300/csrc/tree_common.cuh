@@ -83,7 +83,7 @@ struct TreeArgs {
   int rows;           // rows of an item, at most: 32, 64 or 128
   int tile;           // keys of a tile, 64 or 128
   int tail_cost;      // units of a tile that holds drafted keys
-  int ctas, least;    // CTAs of the launch; units that one gets at least
+  int ctas;           // CTAs of the launch
   int stages;         // ring stages
   int win_stage;      // floats of a stage's table windows
   int nodes, near;    // nodes (a multiple of 32) and table entries that an item keeps
