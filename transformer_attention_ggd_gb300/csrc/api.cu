@@ -169,7 +169,7 @@ DecWs dec_ws(int B, int H, int Tkv) {
 }
 
 struct TreeWs {
-  size_t plan, table, ml, part, total;
+  size_t plan, table, ml, cut, part, total;
   int rows;
 };
 TreeWs tree_ws(int B, int H, int Hkv, int N, int Tmax) {
@@ -178,7 +178,8 @@ TreeWs tree_ws(int B, int H, int Hkv, int N, int Tmax) {
   w.plan = kStatusBytes;
   w.table = w.plan + align256((static_cast<size_t>(B) + 1) * 8);
   w.ml = w.table + align256(static_cast<size_t>(H) * tree_table_len(Tmax) * 4);
-  w.part = w.ml + align256(2 * kTreeCtas * static_cast<size_t>(w.rows) * 8);
+  w.cut = w.ml + align256(2 * kTreeCtas * static_cast<size_t>(w.rows) * 8);
+  w.part = w.cut + align256(kTreeCtas * sizeof(CutItem));
   w.total = w.part + align256(2 * kTreeCtas * static_cast<size_t>(w.rows) * kHeadDim * 4);
   return w;
 }
@@ -548,6 +549,7 @@ bam_status bam_attn_decode_tree_paged(const void* q, const void* k_pages, const 
   a.plan = reinterpret_cast<int64_t*>(wsb + w.plan);
   a.table = reinterpret_cast<float*>(wsb + w.table);
   a.part_ml = reinterpret_cast<float2*>(wsb + w.ml);
+  a.cut = reinterpret_cast<CutItem*>(wsb + w.cut);
   a.part = reinterpret_cast<float*>(wsb + w.part);
   a.eps = p->eps;
   a.H = H;

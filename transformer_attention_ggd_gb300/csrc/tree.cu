@@ -841,7 +841,7 @@ __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const
   const bool any_odd = (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
   const size_t orow =
       (static_cast<size_t>(it.b) * a.H + it.hk * a.group + it.g0 + row.hrel) * c.N + row.node;
-  const size_t prow = static_cast<size_t>(2 * blockIdx.x + (it.t0 == 0 ? 1 : 0)) * S::kRows + row.rr;
+  const size_t part = 2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
   float M = st.m, L = st.l;
   // Columns col .. col + kOwn - 1 of the row's output.
   auto put = [&](float* o, int col) __attribute__((always_inline)) {
@@ -866,11 +866,11 @@ __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const
       }
     }
     if (!whole) {  // left to the combine kernel
-      float4* dst = reinterpret_cast<float4*>(a.part + prow * kHeadDim + col);
+      float4* dst = reinterpret_cast<float4*>(a.part) + (part * 16 + col / 4) * S::kRows + row.rr;
 #pragma unroll
       for (int y = 0; y < kOwn / 4; ++y)
-        dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-      if (col == 0) a.part_ml[prow] = make_float2(M, L);
+        dst[y * S::kRows] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+      if (col == 0) a.part_ml[part * S::kRows + row.rr] = make_float2(M, L);
       return;
     }
     const float inv = 1.0f / L;
@@ -1091,6 +1091,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     int issued = 0, s = 0, phase = 1, k = 0, last_b = -1, tree = 1;
     Item it;
     int units = 0, plain = 0;  // of an item of the sequence
+    CutItem cut{0, 0, 0, 0, 0, 0};
     int64_t seq_end = x;  // of the sequence that the last item was of
     for (;; ++k) {
       const ItemInfo info = info_view<S>(a, v, k);
@@ -1140,6 +1141,14 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         it.t1 = tiles_before(S::kTailCost, plain, stop);
         // (none: the share ends before the end of the item's next tile)
         if (it.t1 <= it.t0) it.t1 = 0;
+        if (it.t0 == 0 && it.t1 > 0) {  // do other CTAs go on with it?
+          cut.n = 0;
+          if (stop < units)
+            cut = CutItem{it.b, it.hk, it.r0, it.n, cta,
+                          range_owner(all, active, x + (units - stop) - 1)};
+          if (a.by_item && lane == 0)
+            a.cut[(it.b * c.Hkv + it.hk) * a.nrb_most + it.r0 / kRows] = cut;
+        }
       }
       const int n = it.n, len = it.len;
       const int g0 = it.t1 ? it.r0 / n : 0, heads = it.t1 ? (it.r1 - 1) / n - g0 + 1 : 0;
@@ -1244,6 +1253,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         if (early) grid_dep_wait();
         early = false;
         if (lane == 0) {
+          if (!a.by_item && cta < active) a.cut[cta] = cut;
           *info.it = it;
           mbar_arrive(&sm.item_full[k & 1]);
         }
@@ -1436,88 +1446,118 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   }
 }
 
-// One warp per row (b, h, t): joins the parts of an item that was cut.
-__global__ void __launch_bounds__(256) bam_tree_combine_kernel(const TreeArgs a) {
-  grid_dep_wait();
+// Joins the parts of the items that were cut: blocks (x, .) the one of record x.
+// A warp takes half the columns of four rows, a lane four columns (a chunk) of
+// one row, of every kSplit-th part.  kSplit 4 is for items of many parts: one
+// sequence of 131072 keys, 12 heads (26 parts an item) 98 us with 1, 89 with 4;
+// 4 chains of 128 nodes over 20000 keys (7 parts) 74.6 with 1, 82 with 4.
+constexpr int kJoinThreads = 128, kJoinParts = 8;  // parts in flight
+constexpr int kJoinRows = kJoinThreads / 16;       // rows of a block
+template <int kSplit>
+__global__ void __launch_bounds__(kJoinThreads* kSplit) bam_tree_combine_kernel(const TreeArgs a) {
   const CacheArgs& c = a.c;
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = static_cast<int64_t>(c.B) * a.H * c.N;
-  const int64_t all = __ldcg(a.plan + c.B);
-  const int active = active_ctas(all, a.ctas);
-  const bool gave_up = *reinterpret_cast<volatile int*>(&c.status->abort) != 0;
-  for (int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5); row < rows; row += gridDim.x * 8ll) {
-    const int t = static_cast<int>(row % c.N);
-    const int h = static_cast<int>(row / c.N % a.H);
-    const int b = static_cast<int>(row / c.N / a.H);
+  const int tid = threadIdx.x % kJoinThreads, split = threadIdx.x / kJoinThreads;
+  const int warp = tid >> 5, lane = tid & 31;
+  bool used = true;  // the record is of an item that there is
+  if (a.by_item) {
     int len, n;
-    cache_lengths(c, b, &len, &n);
-    if (t >= n) continue;
-    float2 v;
-    float lse;
-    if (gave_up) {
-      lse = __int_as_float(0x7fc00000);
-      v = make_float2(lse, lse);
-    } else {
-      const int g = h % a.group, r = g * n + t, rb = r / a.rows;
-      const int nrb = (a.group * n + a.rows - 1) / a.rows;
-      const int units = item_units(a.tile, a.tail_cost, len, n);
-      const int64_t first =
-          __ldcg(a.plan + b) + static_cast<int64_t>(h / a.group * nrb + rb) * units;
-      // the CTAs of its first and last tile
-      const int c0 = range_owner(all, active,
-                                 first + kItemCost + (len < a.tile ? a.tail_cost - 1 : 0));
-      const int c1 = range_owner(all, active, first + units - 1);
-      if (c0 == c1) continue;
-      const int rr = r - rb * a.rows;
-      auto part_row = [&](int cta) {
-        return static_cast<size_t>(2 * cta + (cta == c0 ? 1 : 0)) * a.rows + rr;
-      };
-      // 32 parts at a time: their maxima and sums one a lane, and the outputs
-      // eight in flight.
-      float M = kNoMax, L = 0.0f;
-      v = make_float2(0.0f, 0.0f);
-      for (int x0 = c0; x0 <= c1; x0 += 32) {
-        const int parts = min(32, c1 + 1 - x0);
-        const float2 ml =
-            lane < parts ? __ldcg(a.part_ml + part_row(x0 + lane)) : make_float2(kNoMax, 0.0f);
-        float m = fmaxf(M, ml.x);
-#pragma unroll
-        for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        const float old = ex2_approx(M - m), f = lane < parts ? ex2_approx(ml.x - m) : 0.0f;
-        M = m;
-        L = L * old + ml.y * f;  // (of this lane's parts)
-        v.x *= old;
-        v.y *= old;
-        for (int i = 0; i < parts; i += 8) {
-          float2 y[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            if (i + u < parts)
-              y[u] = __ldcg(reinterpret_cast<const float2*>(a.part + part_row(x0 + i + u) * kHeadDim) +
-                            lane);
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const float g = __shfl_sync(0xffffffffu, f, (i + u) & 31);
-            if (i + u < parts) {
-              v.x += y[u].x * g;
-              v.y += y[u].y * g;
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int off = 16; off; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-      v.x /= L;
-      v.y /= L;
-      lse = (M + log2f(L)) * kLn2f;
-    }
-    if (a.o_fp32)
-      reinterpret_cast<float2*>(static_cast<float*>(a.o) + row * kHeadDim)[lane] = v;
-    else
-      reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + row * kHeadDim)[lane] =
-          pack_bf16x2(v.x, v.y);
-    if (a.lse && lane == 0) a.lse[row] = lse;
+    cache_lengths(c, blockIdx.x / a.nrb_most / c.Hkv, &len, &n);
+    used = static_cast<int>(blockIdx.x % a.nrb_most) * a.rows < a.group * n;
   }
+  grid_dep_wait();
+  if (*reinterpret_cast<volatile int*>(&c.status->abort) != 0) {
+    // A wait of the call gave up: NaN in every row.
+    const float nan = __int_as_float(0x7fc00000);
+    const int64_t rows = static_cast<int64_t>(c.B) * a.H * c.N;
+    const int64_t first = static_cast<int64_t>(blockIdx.y * gridDim.x + blockIdx.x) * 4 + warp;
+    for (int64_t row = first; split == 0 && row < rows; row += static_cast<int64_t>(gridDim.x) * gridDim.y * 4) {
+      int len, n;
+      cache_lengths(c, static_cast<int>(row / c.N / a.H), &len, &n);
+      if (row % c.N >= n) continue;
+      if (a.o_fp32)
+        reinterpret_cast<float2*>(a.o)[row * 32 + lane] = make_float2(nan, nan);
+      else
+        reinterpret_cast<uint32_t*>(a.o)[row * 32 + lane] = pack_bf16x2(nan, nan);
+      if (a.lse && lane == 0) a.lse[row] = nan;
+    }
+    return;
+  }
+  if (!used) return;
+  const CutItem it = a.cut[blockIdx.x];
+  if (!a.by_item && blockIdx.x >= active_ctas(__ldcg(a.plan + c.B), a.ctas)) return;
+  if (it.n == 0) return;
+  const int c0 = it.first;
+  const int rr = kJoinRows * blockIdx.y + 4 * (warp >> 1) + (lane & 3);
+  const int chunk = 8 * (warp & 1) + (lane >> 2);
+  const int r = it.r0 + rr, rows = a.group * it.n;
+  const bool on = r < rows;
+  float M = kNoMax, L = 0.0f;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float4* part = reinterpret_cast<const float4*>(a.part);
+  for (int x0 = c0 + split; on && x0 <= it.last; x0 += kJoinParts * kSplit) {
+    float2 ml[kJoinParts];
+    float4 p[kJoinParts];
+#pragma unroll
+    for (int u = 0; u < kJoinParts; ++u) {
+      ml[u] = make_float2(kNoMax, 0.0f);
+      const int x = x0 + u * kSplit;
+      if (x > it.last) continue;
+      const size_t at = 2 * x + (x == c0 ? 1 : 0);
+      ml[u] = __ldcg(a.part_ml + at * a.rows + rr);
+      p[u] = __ldcg(part + (at * 16 + chunk) * a.rows + rr);
+    }
+    float m = M;
+#pragma unroll
+    for (int u = 0; u < kJoinParts; ++u) m = fmaxf(m, ml[u].x);
+    const float old = ex2_approx(M - m);
+    M = m;
+    L *= old;
+    v = make_float4(v.x * old, v.y * old, v.z * old, v.w * old);
+#pragma unroll
+    for (int u = 0; u < kJoinParts; ++u) {
+      if (x0 + u * kSplit > it.last) continue;
+      const float f = ex2_approx(ml[u].x - m);
+      L = fmaf(ml[u].y, f, L);
+      v.x = fmaf(p[u].x, f, v.x);
+      v.y = fmaf(p[u].y, f, v.y);
+      v.z = fmaf(p[u].z, f, v.z);
+      v.w = fmaf(p[u].w, f, v.w);
+    }
+  }
+  if (kSplit > 1) {
+    __shared__ float4 sv[kSplit][kJoinThreads];
+    __shared__ float2 sml[kSplit][kJoinThreads];
+    sv[split][tid] = v;
+    sml[split][tid] = make_float2(M, L);
+    __syncthreads();
+    if (split > 0) return;
+    float m = M;
+#pragma unroll
+    for (int u = 1; u < kSplit; ++u) m = fmaxf(m, sml[u][tid].x);
+    const float old = ex2_approx(M - m);
+    L *= old;
+    v = make_float4(v.x * old, v.y * old, v.z * old, v.w * old);
+    M = m;
+#pragma unroll
+    for (int u = 1; u < kSplit; ++u) {
+      const float2 ml = sml[u][tid];
+      const float4 p = sv[u][tid];
+      const float f = ex2_approx(ml.x - m);
+      L = fmaf(ml.y, f, L);
+      v = make_float4(fmaf(p.x, f, v.x), fmaf(p.y, f, v.y), fmaf(p.z, f, v.z), fmaf(p.w, f, v.w));
+    }
+  }
+  if (!on) return;
+  const float inv = 1.0f / L;
+  const int h = r / it.n;
+  const size_t orow = (static_cast<size_t>(it.b) * a.H + it.hk * a.group + h) * c.N + (r - h * it.n);
+  if (a.o_fp32)
+    reinterpret_cast<float4*>(a.o)[orow * 16 + chunk] =
+        make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  else
+    reinterpret_cast<uint2*>(a.o)[orow * 16 + chunk] =
+        make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+  if (a.lse && chunk == 0) a.lse[orow] = (M + log2f(L)) * kLn2f;
 }
 
 constexpr size_t kSmemTwo = 113 * 1024;  // a CTA's share when two fit an SM
@@ -1582,6 +1622,9 @@ bool tree_config(TreeArgs* a, int sms) {
   a->stages = static_cast<int>((budget - fixed) / stage);
   if (a->stages > kMaxStages) a->stages = kMaxStages;
   a->ctas = per_sm * sms < kTreeCtas ? per_sm * sms : kTreeCtas;
+  // Records of the items or of the CTAs, whichever are fewer.
+  a->nrb_most = (a->group * a->c.N + a->rows - 1) / a->rows;
+  a->by_item = static_cast<int64_t>(a->c.B) * a->c.Hkv * a->nrb_most <= a->ctas;
   a->tail_cost = tree_tail_cost(a->o_fp32 ? 3 : 1, kRowsMax / a->rows);
   return a->stages >= 2 && a->ctas >= 1;
 }
@@ -1600,10 +1643,11 @@ cudaError_t launch_tree(const CUtensorMap& tk, const CUtensorMap& tv, const Tree
 }
 
 cudaError_t launch_tree_combine(const TreeArgs& a, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(a.c.B) * a.H * a.c.N;
-  const int64_t want = (rows + 7) / 8;
-  const int grid = static_cast<int>(want < 152 * 8 ? want : 152 * 8);
-  return launch_k(bam_tree_combine_kernel, dim3(grid), dim3(256), 0, st, true, a);
+  const int records = a.by_item ? a.c.B * a.c.Hkv * a.nrb_most : a.ctas;
+  const dim3 grid(records, a.rows / kJoinRows);
+  if (records * 8 < a.ctas)  // mostly more than eight parts an item
+    return launch_k(bam_tree_combine_kernel<4>, grid, dim3(4 * kJoinThreads), 0, st, true, a);
+  return launch_k(bam_tree_combine_kernel<1>, grid, dim3(kJoinThreads), 0, st, true, a);
 }
 
 }  // namespace bam

@@ -63,6 +63,13 @@ constexpr int kItemCost = 4;
 constexpr int kTailCost = 2;
 constexpr int kTreeCtas = 304;   // most CTAs (two per SM)
 
+// An item that lies in CTAs `first` to `last`; n is 0 if it lies in one.  In a call
+// of few items there is a record of each (by_item), in one of many a record of
+// the one that begins in each CTA and goes on in others.
+struct CutItem {
+  int b, hk, r0, n, first, last;
+};
+
 struct TreeArgs {
   CacheArgs c;
   const uint16_t* q;  // [B, H, N, 64]
@@ -75,8 +82,10 @@ struct TreeArgs {
   float* lse;
   int64_t* plan;      // [B + 1] first unit of each sequence, and W
   float* table;       // [H, tab_len]: entry y is b_h(tab_zero - y) * log2(e)
-  float* part;        // [2 * kTreeCtas, rows, 64] partial outputs
+  float* part;        // [2 * kTreeCtas, 16, rows, 4] partial outputs, by four columns
   float2* part_ml;    // [2 * kTreeCtas, rows]: maximum (log2 units), sum
+  CutItem* cut;       // [kTreeCtas]
+  int by_item, nrb_most;  // nrb_most: items of a sequence and key head, at most
   float eps;
   int H, group, prior, ssmax, o_fp32;
   int tab_len, tab_zero;
