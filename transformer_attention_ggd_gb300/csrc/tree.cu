@@ -323,6 +323,18 @@ __device__ __forceinline__ void umma_ts_lanes(uint32_t d_tmem, uint32_t a_tmem, 
 
 // ---------------------------------------------------------------- attention
 
+// True when phase `parity` is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // As mbar_wait, without its call: the slow path of a call would keep the
 // caller's live registers (a row of S, here) in local memory.
 __device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, DevStatus* st,
@@ -333,6 +345,7 @@ __device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, DevSta
     return false;
   }
 #endif
+  if (mbar_test(bar, parity)) return true;
   uint64_t t0 = 0;
 #pragma unroll 1
   for (uint32_t it = 1; !mbar_try_wait_sleep(bar, parity, kWaitSleepNs); ++it) {
@@ -382,18 +395,6 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
-// True when phase `parity` is complete, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 
 // Keys of a tile: as many as S and the parts of P leave Tensor Memory for, and no
