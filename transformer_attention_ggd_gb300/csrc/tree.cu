@@ -525,8 +525,9 @@ __device__ __forceinline__ void tmem_st_pairs(uint32_t taddr, const uint32_t* r)
 // The start of a tile: S and the windows are there.
 __device__ __forceinline__ bool soft_begin(const TreeArgs& a, TreeSmem& sm, SoftState& st) {
   volatile int* ab = &sm.abort_flag;
-  st.ok = warp_wait(&sm.s_full, st.g & 1, a.c.status, ab, kSiteTreeSoftS) &&
-          warp_wait(&sm.k_full[st.s], st.phase, a.c.status, ab, kSiteTreeSoftK);
+  st.ok = __all_sync(0xffffffffu,
+                     tree_wait(&sm.s_full, st.g & 1, a.c.status, ab, kSiteTreeSoftS) &&
+                         tree_wait(&sm.k_full[st.s], st.phase, a.c.status, ab, kSiteTreeSoftK));
   if (st.ok) tc_fence_after();
   return st.ok;
 }
