@@ -20,11 +20,11 @@
 // leaves a partial maximum, sum and output per CTA, which the combine kernel
 // joins.  Ragged batches and a single long sequence keep every SM busy alike.
 //
-// Measured (HBM copy 6.70 TB/s, L2 129 MB; a call with its three kernels): 64
-// sequences of 32768 keys at most, 12 heads, 32 nodes 455 us (3.2 GB, 7.1 TB/s
-// with what L2 keeps); 32 of 16384, 8 key heads, one node, 4 heads a key head
-// 105 us (537 MB); one of 131072, 12 heads, 64 nodes 106 us (403 MB); 4 of
-// 20000, 12 heads, 128 nodes 86 us (249 MB); one of 500, 7 nodes 15.7 us.
+// Measured (HBM copy 6.70 TB/s, L2 129 MB; a call with its three kernels, in a
+// graph): 64 sequences of 32768 keys at most, 12 heads, 32 nodes 441 us (3.2 GB,
+// 7.3 TB/s with what L2 keeps); 32 of 16384, 8 key heads, one node, 4 heads a
+// key head 101 us (537 MB); one of 131072, 12 heads, 64 nodes 87 us (403 MB); 4
+// of 20000, 12 heads, 128 nodes 71 us (249 MB); one of 500, 7 nodes 13.0 us.
 #include "table_eval.cuh"
 #include "tree_common.cuh"
 
@@ -399,9 +399,9 @@ __device__ __forceinline__ void cp_async_wait() {
 
 // Keys of a tile: as many as S and the parts of P leave Tensor Memory for, and no
 // more than 64 columns a thread.  128 against 64 keys where both fit, a call:
-// 455 and 532 us with 64 sequences of 32768 keys and 32 rows, 105 and 125 with
-// 4 rows and 16384 keys, 106 and 109 with 64 rows and 131072 keys; 117 and 115
-// with 64 rows and 1000 keys, 15.7 and 15.1 with 500.
+// 441 and 456 us with 64 sequences of 32768 keys and 32 rows, 87 and 89 with 64
+// rows and 131072 keys, 48 and 58 with 8 rows and 100 keys, 101 and 101 with 4
+// rows and 16384; 13.0 and 11.9 with 7 rows and one sequence of 500.
 __host__ __device__ constexpr int tree_tile(int parts, int ks) {
   return parts == 1 && ks > 1 ? 128 : 64;
 }
@@ -969,8 +969,8 @@ __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const
 //   MMA thread      S = Q K^T  (128 x tile x 64, Q and K from shared memory),
 //                   O += P V   (128 x 64 x tile, P from Tensor Memory);
 //   softmax warps   four, a thread per lane of Tensor Memory.
-// Queries come by asynchronous copies of 16 bytes: TMA boxes of 32 rows took
-// 169 instead of 173 us with 100 nodes, but 111 instead of 110 with one.
+// Queries come by asynchronous copies of 16 bytes; TMA boxes of 32 rows were 2%
+// faster with 100 nodes and 2% slower with one.
 // All 128 lanes are computed whatever the number of rows: the two products of
 // 64 keys take 256 cycles of an SM's tensor core, its share of HBM delivers
 // their 16 KB in about 700.  S runs a tile ahead of the softmax.
@@ -980,7 +980,7 @@ __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const
 // tile, with its own maximum, sum and output, which are joined at the item's
 // end.  The products cost the same (a step of P V adds to the lanes of its
 // keys' copy only), and the softmax takes a KS-th of the time.  With copies a
-// tile is 128 keys: a tile's hand-offs (about 1500 cycles) then weigh half.
+// tile is 128 keys: a tile's hand-offs (about 1000 cycles) then weigh half.
 // The softmax needs no exchange between threads; O is rescaled only when a
 // row's maximum grows by more than 8.
 //
@@ -1036,8 +1036,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   // (a wait that looks at an abort word before it is cleared would give up).
   // With few sequences (one a lane) the producer makes the plan itself, and its
   // first loads of keys and queries, which no kernel of the call writes, do not
-  // wait: 20.2 instead of 22.2 us for 16 sequences of 360 keys, 15.7 instead of
-  // 16.8 for one of 500; no difference at 32 of 16384.
+  // wait: 16.8 instead of 17.9 us for 16 sequences of 360 keys, 13.0 instead of
+  // 14.3 for one of 500; 101.1 against 100.5 at 32 of 16384, 44.1 against 43.0 at
+  // 13 of 9001.
   grid_dep_trigger();
   if (warp != kProducer || c.B > 32) grid_dep_wait();
 
