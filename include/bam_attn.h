@@ -239,7 +239,7 @@ bam_status bam_kv_append_paged(const void* k, const void* v, const void* q, void
  * The weights enter the product with V as sums of bf16 parts: one part for
  * bf16 output, three (24 bits) for fp32 output.  A page number out of range
  * reads page 0 and is reported.  If a device wait of the call gives up, the
- * rows of o and lse are written as NaN. */
+ * rows of o and lse are written as NaN.  o does not overlap q. */
 bam_status bam_attn_decode_tree_paged(const void* q, const void* k_pages, const void* v_pages,
                                       const int* block_table, const int* cache_lens,
                                       const int* draft_lens, const int* parents, void* o,
@@ -267,10 +267,21 @@ bam_status bam_kv_keep_paged(void* k_pages, void* v_pages, const int* block_tabl
                              int max_blocks, int num_pages, int D, void* ws, size_t ws_bytes,
                              cudaStream_t stream);
 
+/* The three operators above for bindings whose foreign calls cost time for each
+ * argument: `words` holds the arguments of operator `op` in order, a 64-bit
+ * word each (pointers and structs by address, integers as they are).  In the
+ * place of the append's strides stands 0 (NULL) or 1: nine stride words then
+ * follow the last argument.  Checks, results and errors are the operator's; an
+ * integer that does not fit its parameter or an unknown op is
+ * BAM_ERR_INVALID_ARG. */
+enum { BAM_CALL_KV_APPEND = 0, BAM_CALL_DECODE_TREE = 1, BAM_CALL_KV_KEEP = 2 };
+bam_status bam_paged_call(int op, const void* words);
+
 /* Synchronises `stream`, then reads and clears the device status word of
  * `ws`.  Returns BAM_OK, BAM_ERR_TIMEOUT (a device wait gave up),
- * BAM_ERR_INVALID_ARG (a device-read argument was out of range: a ragged or
- * paged decode's cache length or page number), BAM_ERR_BOUNDS (debug build:
+ * BAM_ERR_INVALID_ARG (a device-read argument was out of range: a length or
+ * page number of a ragged or paged cache, a draft's length, parent or accepted
+ * node), BAM_ERR_BOUNDS (debug build:
  * a bulk copy failed its bounds check and was not issued; the call's outputs
  * are then invalid) or BAM_ERR_CUDA.  The result is the first error recorded
  * by any call on `ws` since the previous check (errors are not cleared by

@@ -3,6 +3,7 @@ keep): every call here returns before anything is launched, so no GPU is
 needed.  Also pins the tests' 64-bit tree attention on the oracle."""
 
 import ctypes
+import struct
 
 import numpy as np
 import pytest
@@ -167,3 +168,36 @@ def test_reference_tree_attention_is_a_decode_over_each_path(theta, ssmax):
             np.testing.assert_allclose(o[b, :, t].numpy(), oref[0], rtol=0, atol=1e-10)
             np.testing.assert_allclose(lse[b, :, t].numpy(), lref[0], rtol=0, atol=1e-10)
     assert float(oerr[:, :, 0].max()) < 1e-3
+
+
+WORDS = {"append": [FAKE, FAKE, FAKE, FAKE, 0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE,
+                    2, 4, 2, 3, 64, 4, 8, 64, 0, FAKE, 1 << 30, 0],
+         "tree": [FAKE] * 8 + [0, FAKE, 2, 4, 2, 3, 64, 4, 8, 64, 0, FAKE, 1 << 30, 0],
+         "keep": [FAKE] * 8 + [2, 2, 3, 64, 4, 8, 64, FAKE, 1 << 30, 0]}
+
+
+@pytest.mark.parametrize("op,at,value,want", [
+    ("append", 11, 0, "INVALID_ARG"), ("append", 12, 3, "INVALID_ARG"), ("append", 14, 129, "UNSUPPORTED"),
+    ("append", 15, 32, "INVALID_ARG"), ("append", 18, 128, "UNSUPPORTED"), ("append", 2, 0, "INVALID_ARG"),
+    ("append", 0, FAKE + 8, "INVALID_ARG"), ("append", 21, 100, "WORKSPACE"), ("append", 4, 2, "INVALID_ARG"),
+    ("append", 11, (1 << 32) + 2, "INVALID_ARG"), ("append", 10, FAKE + 1, "INVALID_ARG"),
+    ("tree", 10, 0, "INVALID_ARG"), ("tree", 12, 3, "INVALID_ARG"), ("tree", 17, 128, "UNSUPPORTED"),
+    ("tree", 18, 0, "INVALID_ARG"), ("tree", 13, 129, "UNSUPPORTED"), ("tree", 8, 1 << 32, "INVALID_ARG"),
+    ("tree", 16, 1 << 33, "INVALID_ARG"), ("tree", 3, 0, "INVALID_ARG"),
+    ("keep", 8, 0, "INVALID_ARG"), ("keep", 10, 129, "UNSUPPORTED"), ("keep", 11, 96, "INVALID_ARG"),
+    ("keep", 6, 0, "INVALID_ARG"), ("keep", 7, FAKE + 2, "INVALID_ARG"), ("keep", 16, 100, "WORKSPACE"),
+    ("keep", 15, 0, "WORKSPACE"), ("keep", 13, -(1 << 32) + 8, "INVALID_ARG")])
+def test_refusals_of_calls_by_words(lib, op, at, value, want):
+    words = list(WORDS[op])
+    words[at] = value
+    number = list(WORDS).index(op)
+    assert lib.bam_paged_call(number, struct.pack(f"{len(words)}q", *words)) == getattr(ba, "BAM_ERR_" + want)
+
+
+def test_calls_by_words_need_an_operator_and_words(lib):
+    words = struct.pack("32q", *([0] * 32))
+    for op in (-1, 3, 1 << 20):
+        assert lib.bam_paged_call(op, words) == ba.BAM_ERR_INVALID_ARG
+    assert lib.bam_paged_call(0, None) == ba.BAM_ERR_INVALID_ARG
+    with pytest.raises(TypeError):
+        ba._struct_address(object(), ba.BamRope)

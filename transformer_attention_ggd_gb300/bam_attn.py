@@ -25,6 +25,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -79,6 +80,7 @@ EXPORTED = (
     "bam_attn_decode_tree_paged",
     "bam_attn_tree_workspace_size",
     "bam_kv_keep_paged",
+    "bam_paged_call",
 )
 
 # Size of the fixed device scratch of bam_attn_decode_noalloc.
@@ -115,8 +117,6 @@ class BamRope(ctypes.Structure):
         ("interleaved", ctypes.c_int),
     ]
 
-
-_Strides9 = ctypes.c_int64 * 9
 
 _lib = None
 _lock = threading.Lock()
@@ -184,6 +184,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.bam_attn_tree_workspace_size.argtypes = [i] * 6
         lib.bam_kv_keep_paged.restype = i
         lib.bam_kv_keep_paged.argtypes = [vp] * 8 + [i] * 7 + [vp, sz, vp]
+        lib.bam_paged_call.restype = i
+        lib.bam_paged_call.argtypes = [i, ctypes.c_char_p]
         _lib = lib
         return lib
 
@@ -519,28 +521,43 @@ def _raw_stream(stream, index):
 
 
 def _address(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
-def _plain(index, dtype, shape, *tensors):
-    """Every tensor is contiguous, on CUDA device `index`, of this dtype and shape."""
-    for t in tensors:
-        if not (t.dtype is dtype and t.get_device() == index and t.shape == shape
-                and t.is_contiguous()):
-            return False
-    return True
+def _struct_address(x, kind):
+    if x is None:
+        return 0
+    if not isinstance(x, kind):
+        raise TypeError(f"expected {kind.__name__}, got {type(x).__name__}")
+    return ctypes.addressof(x)
 
 
-def _cache_ok(index, k_pages, v_pages, block_table, cache_lens, draft_lens, parents, ws, B, N):
+# The words of bam_paged_call: a foreign call with 22 arguments takes 5 us, one
+# with its words packed 1 us.
+_append_words = struct.Struct("32q").pack
+_tree_words = struct.Struct("22q").pack
+_keep_words = struct.Struct("18q").pack
+
+
+def _all_ok(index, pool, k_pages, v_pages, table, block_table, cache_lens, draft_lens, parents, ws,
+            B, N, specs):
+    """The cache's tensors and those of specs (tensor, dtype, shape) are contiguous, on CUDA
+    device `index`, of their dtypes and shapes.  pool, table: the shapes of k_pages and
+    block_table."""
     import torch
-    i32 = torch.int32
-    return (_plain(index, torch.bfloat16, k_pages.shape, k_pages, v_pages)
-            and k_pages.shape[3] == 64 and block_table.dim() == 2
-            and _plain(index, i32, (B, block_table.shape[1]), block_table)
-            and _plain(index, i32, (B,), cache_lens)
-            and (draft_lens is None or _plain(index, i32, (B,), draft_lens))
-            and (parents is None or _plain(index, i32, (B, N), parents))
-            and ws.dim() == 1 and _plain(index, torch.uint8, ws.shape, ws))
+    bf, i32, lens = torch.bfloat16, torch.int32, (B,)
+    specs += ((k_pages, bf, pool), (v_pages, bf, pool), (block_table, i32, table),
+              (cache_lens, i32, lens))
+    if draft_lens is not None:
+        specs += ((draft_lens, i32, lens),)
+    if parents is not None:
+        specs += ((parents, i32, (B, N)),)
+    for t, dtype, shape in specs:
+        if (t.dtype is not dtype or t.get_device() != index or t.shape != shape
+                or not t.is_contiguous()):
+            return False
+    return (pool[3] == 64 and len(table) == 2 and table[0] == B and ws.dtype is torch.uint8
+            and ws.get_device() == index and ws.dim() == 1 and ws.is_contiguous())
 
 
 def _rows_ok(index, shape, t):
@@ -565,7 +582,8 @@ def bam_kv_append_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_len
     follow; q [B, H, N, 64] -> q_out (contiguous) or both None: queries rotated
     on the way; rope: make_rope(...) or None."""
     B, Hkv, N, D = shape = k.shape
-    num_pages, pool_heads, page, _ = k_pages.shape
+    num_pages, pool_heads, page, _ = pool = k_pages.shape
+    table = block_table.shape
     index = k.get_device()
     H = Hkv
     strides = k.stride()[:3] + v.stride()[:3]
@@ -578,10 +596,10 @@ def bam_kv_append_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_len
             ok = (index >= 0 and index == _current_device() and D == 64 and pool_heads == Hkv
                   and _rows_ok(index, shape, k) and _rows_ok(index, shape, v)
                   and (q is None) == (q_out is None)
-                  and (q is None or (_rows_ok(index, (B, H, N, 64), q)
-                                     and _plain(index, torch.bfloat16, (B, H, N, 64), q_out)))
-                  and _cache_ok(index, k_pages, v_pages, block_table, cache_lens, new_lens,
-                                parents, ws, B, N))
+                  and (q is None or _rows_ok(index, (B, H, N, 64), q))
+                  and _all_ok(index, pool, k_pages, v_pages, table, block_table, cache_lens,
+                              new_lens, parents, ws, B, N,
+                              () if q is None else ((q_out, torch.bfloat16, (B, H, N, 64)),)))
         except AttributeError:
             ok = False
         if not ok:
@@ -597,12 +615,14 @@ def bam_kv_append_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_len
                            + (("q_out", q_out, (B, H, N, 64), _dt()[0], True),), dev)
             _check_ws(ws, dev)
             raise ValueError("argument check failed")
-    st = load_library().bam_kv_append_paged(
+    if q is None:
+        strides += (0, 0, 0)
+    st = load_library().bam_paged_call(0, _append_words(
         k.data_ptr(), v.data_ptr(), _address(q), _address(q_out),
-        _Strides9(*strides), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+        1, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
         cache_lens.data_ptr(), _address(new_lens), _address(parents), B, H, Hkv, N, page,
-        block_table.shape[1], num_pages, D, None if rope is None else ctypes.byref(rope),
-        ws.data_ptr(), ws.numel(), _raw_stream(stream, index))
+        table[1], num_pages, D, _struct_address(rope, BamRope), ws.data_ptr(),
+        ws.numel(), _raw_stream(stream, index), *strides))
     if st:
         _check(st, "bam_kv_append_paged")
 
@@ -615,21 +635,25 @@ def bam_attn_decode_tree_paged(q, k_pages, v_pages, block_table, cache_lens, dra
     [B, N] or None (a chain); lse [B, H, N] or None."""
     import torch
     B, H, N, D = shape = q.shape
-    num_pages, Hkv, page, _ = k_pages.shape
+    num_pages, Hkv, page, _ = pool = k_pages.shape
+    table = block_table.shape
     index = q.get_device()
     out = o.dtype
     if check:
         f32 = torch.float32
         try:
             prm = getattr(params, "tensors", None)
+            specs = ((q, torch.bfloat16, shape), (o, out, shape))
+            if lse is not None:
+                specs += ((lse, f32, (B, H, N)),)
+            if prm is not None:
+                specs += ((prm[0], f32, (H,)), (prm[1], f32, (H,)), (prm[2], f32, (H,)))
+                if prm[3] is not None:
+                    specs += ((prm[3], f32, (H,)),)
             ok = (index >= 0 and index == _current_device() and D == 64
                   and (out is torch.bfloat16 or out is f32)
-                  and _plain(index, torch.bfloat16, shape, q) and _plain(index, out, shape, o)
-                  and (lse is None or _plain(index, f32, (B, H, N), lse))
-                  and (prm is None or (_plain(index, f32, (H,), prm[0], prm[1], prm[2])
-                                       and (prm[3] is None or _plain(index, f32, (H,), prm[3]))))
-                  and _cache_ok(index, k_pages, v_pages, block_table, cache_lens, draft_lens,
-                                parents, ws, B, N))
+                  and _all_ok(index, pool, k_pages, v_pages, table, block_table, cache_lens,
+                              draft_lens, parents, ws, B, N, specs))
         except AttributeError:
             ok = False
         if not ok:
@@ -642,12 +666,12 @@ def bam_attn_decode_tree_paged(q, k_pages, v_pages, block_table, cache_lens, dra
                                           parents, B, N) + _param_specs(params, H), dev)
             _check_ws(ws, dev)
             raise ValueError("argument check failed")
-    st = load_library().bam_attn_decode_tree_paged(
+    st = load_library().bam_paged_call(1, _tree_words(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
         cache_lens.data_ptr(), _address(draft_lens), _address(parents), o.data_ptr(),
         1 if out is torch.float32 else 0, _address(lse), B, H, Hkv, N, page,
-        block_table.shape[1], num_pages, D, ctypes.byref(params), ws.data_ptr(), ws.numel(),
-        _raw_stream(stream, index))
+        table[1], num_pages, D, _struct_address(params, BamParams), ws.data_ptr(),
+        ws.numel(), _raw_stream(stream, index)))
     if st:
         _check(st, "bam_attn_decode_tree_paged")
 
@@ -656,8 +680,9 @@ def bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, par
                       new_lens, ws, stream=None, check=True) -> None:
     """Keep the path from the root to node accepted[b] (int32 [B], -1: none)
     of each draft; new_lens int32 [B] (may be cache_lens) gets the lengths."""
-    num_pages, Hkv, page, D = k_pages.shape
-    B = block_table.shape[0]
+    num_pages, Hkv, page, D = pool = k_pages.shape
+    table = block_table.shape
+    B = table[0]
     N = parents.shape[1] if parents is not None else BAM_TREE_MAX_NODES
     index = k_pages.get_device()
     if parents is None and draft_lens is None:
@@ -666,9 +691,9 @@ def bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, par
         import torch
         try:
             ok = (index >= 0 and index == _current_device()
-                  and _plain(index, torch.int32, (B,), accepted, new_lens)
-                  and _cache_ok(index, k_pages, v_pages, block_table, cache_lens, draft_lens,
-                                parents, ws, B, N))
+                  and _all_ok(index, pool, k_pages, v_pages, table, block_table, cache_lens,
+                              draft_lens, parents, ws, B, N,
+                              ((accepted, torch.int32, (B,)), (new_lens, torch.int32, (B,)))))
         except AttributeError:
             ok = False
         if not ok:
@@ -680,11 +705,11 @@ def bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, par
                               ("new_lens", new_lens, (B,), i32, False)), dev)
             _check_ws(ws, dev)
             raise ValueError("argument check failed")
-    st = load_library().bam_kv_keep_paged(
+    st = load_library().bam_paged_call(2, _keep_words(
         k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(),
         _address(draft_lens), _address(parents), accepted.data_ptr(), new_lens.data_ptr(), B, Hkv,
-        N, page, block_table.shape[1], num_pages, D, ws.data_ptr(), ws.numel(),
-        _raw_stream(stream, index))
+        N, page, table[1], num_pages, D, ws.data_ptr(), ws.numel(),
+        _raw_stream(stream, index)))
     if st:
         _check(st, "bam_kv_keep_paged")
 

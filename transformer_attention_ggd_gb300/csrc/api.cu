@@ -594,6 +594,47 @@ bam_status bam_kv_keep_paged(void* k_pages, void* v_pages, const int* block_tabl
       launch_kernel(BAM_KERNEL_KV_KEEP, stream, [&] { return launch_keep(a, stream); }));
 }
 
+bam_status bam_paged_call(int op, const void* words) {
+  constexpr int kWords[] = {23, 22, 18}, kStrides = 4;  // place of the append's strides
+  if (!words || op < BAM_CALL_KV_APPEND || op > BAM_CALL_KV_KEEP) return BAM_ERR_INVALID_ARG;
+  int64_t w[23], strides[9];
+  std::memcpy(w, words, kWords[op] * sizeof(int64_t));
+  bool fits = true;
+  auto p = [&](int x) { return reinterpret_cast<void*>(static_cast<uintptr_t>(w[x])); };
+  auto ip = [&](int x) { return static_cast<const int*>(p(x)); };
+  auto n = [&](int x) {
+    fits &= w[x] == static_cast<int>(w[x]);
+    return static_cast<int>(w[x]);
+  };
+  auto st = [&](int x) { return static_cast<cudaStream_t>(p(x)); };
+  auto sz = [&](int x) { return static_cast<size_t>(w[x]); };
+  int i[8];
+  const int first = op == BAM_CALL_KV_APPEND ? 11 : op == BAM_CALL_DECODE_TREE ? 10 : 8;
+  const int ints = op == BAM_CALL_KV_KEEP ? 7 : 8;
+  for (int x = 0; x < ints; ++x) i[x] = n(first + x);
+  const int o_fp32 = op == BAM_CALL_DECODE_TREE ? n(8) : 0;
+  if (!fits) return BAM_ERR_INVALID_ARG;
+  switch (op) {
+    case BAM_CALL_KV_APPEND:
+      if (w[kStrides] != 0 && w[kStrides] != 1) return BAM_ERR_INVALID_ARG;
+      if (w[kStrides])
+        std::memcpy(strides, static_cast<const char*>(words) + sizeof(w), sizeof(strides));
+      return bam_kv_append_paged(p(0), p(1), p(2), p(3), w[kStrides] ? strides : nullptr, p(5), p(6),
+                                 ip(7), ip(8), ip(9), ip(10), i[0], i[1], i[2], i[3], i[4], i[5],
+                                 i[6], i[7], static_cast<const bam_rope*>(p(19)), p(20), sz(21),
+                                 st(22));
+    case BAM_CALL_DECODE_TREE:
+      return bam_attn_decode_tree_paged(p(0), p(1), p(2), ip(3), ip(4), ip(5), ip(6), p(7), o_fp32,
+                                        static_cast<float*>(p(9)), i[0], i[1], i[2], i[3], i[4],
+                                        i[5], i[6], i[7], static_cast<const bam_params*>(p(18)),
+                                        p(19), sz(20), st(21));
+    default:
+      return bam_kv_keep_paged(p(0), p(1), ip(2), ip(3), ip(4), ip(5), ip(6),
+                               static_cast<int*>(p(7)), i[0], i[1], i[2], i[3], i[4], i[5], i[6],
+                               p(15), sz(16), st(17));
+  }
+}
+
 bam_status bam_attn_bwd(const void* q, const void* k, const void* v, const void* o, int o_fp32,
                         const float* lse, const void* dO, void* dq, void* dk, void* dv,
                         float* dalpha, float* dbeta, float* dmu, float* ds, int B, int H, int T,
