@@ -23,7 +23,7 @@
 // Measured (HBM copy 6.70 TB/s, L2 129 MB; a call with its three kernels, in a
 // graph): 64 sequences of 32768 keys at most, 12 heads, 32 nodes 441 us (3.2 GB,
 // 7.3 TB/s with what L2 keeps); 32 of 16384, 8 key heads, one node, 4 heads a
-// key head 101 us (537 MB); one of 131072, 12 heads, 64 nodes 87 us (403 MB); 4
+// key head 100 us (537 MB); one of 131072, 12 heads, 64 nodes 85 us (403 MB); 4
 // of 20000, 12 heads, 128 nodes 71 us (249 MB); one of 500, 7 nodes 13.0 us.
 #include "table_eval.cuh"
 #include "tree_common.cuh"
