@@ -171,6 +171,17 @@ def test_tree_many_sequences():
     _tree_case(4, B, 2, 1, 3, 64, lens, new, parents, False, False, "bf16")
 
 
+@pytest.mark.parametrize("B,out", [(37, "fp32"), (38, "bf16"), (39, "fp32"), (39, "bf16")])
+def test_tree_about_as_many_items_as_ctas(B, out):
+    """A few items less and more than CTAs, cut in different places, some of
+    them empty: what was cut is recorded by item, or by CTA."""
+    rng = np.random.default_rng(B)
+    lens, new = rng.integers(0, 900, B), rng.integers(0, 6, B)
+    lens[3], new[3], new[5], new[B - 1] = 5000, 5, 0, 0
+    parents = [random_tree(rng, n) for n in new]
+    _tree_case(5, B, 16, 8, 5, 64, lens, new, parents, True, False, out)
+
+
 def test_tree_many_query_heads_per_key_head():
     rng = np.random.default_rng(6)
     _tree_case(8, 2, 64, 1, 5, 64, [300, 10], [5, 3], [random_tree(rng, 5), random_tree(rng, 3)],
