@@ -584,8 +584,10 @@ __device__ __forceinline__ void soft_finish(const TreeArgs& a, TreeSmem& sm, con
 }
 // Two weights and their bf16 parts; l2 gathers the exact ones.  Three parts
 // are cut off, not rounded: 8 bits each are the weight's 24, and none is
-// negative, nor zero behind a weight that is not, so that an infinite value
-// meets no product that turns it into NaN.
+// negative.  None is less than 2^-26 of the weight (two such floors are half of
+// its last place), so that an infinite value meets no zero that turns it into
+// NaN; those of a weight of zero are zero, so that a key out of sight adds
+// nothing, however large its value.
 template <int PARTS, int N>
 __device__ __forceinline__ void soft_weights(uint64_t z, uint64_t negm2, uint64_t& l2,
                                              uint32_t (*pk)[N], int y) {
@@ -598,13 +600,13 @@ __device__ __forceinline__ void soft_weights(uint64_t z, uint64_t negm2, uint64_
     pk[0][y] = pack_bf16x2(p0, p1);
     return;
   }
-  constexpr float kTiny = 1.1754944e-38f;
+  const float least0 = p0 * 0x1p-26f, least1 = p1 * 0x1p-26f;
 #pragma unroll
   for (int part = 0; part < PARTS; ++part) {
     const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
     pk[part][y] = __byte_perm(u0, u1, 0x7632);
-    p0 = fmaxf(p0 - __uint_as_float(u0 & 0xFFFF0000u), kTiny);
-    p1 = fmaxf(p1 - __uint_as_float(u1 & 0xFFFF0000u), kTiny);
+    p0 = fmaxf(p0 - __uint_as_float(u0 & 0xFFFF0000u), least0);
+    p1 = fmaxf(p1 - __uint_as_float(u1 & 0xFFFF0000u), least1);
   }
 }
 
