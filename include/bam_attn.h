@@ -233,7 +233,8 @@ bam_status bam_kv_append_paged(const void* k, const void* v, const void* q, void
  * cache_lens[b] + depth(t) - j, an ancestor i at depth(t) - depth(i), and
  * n = cache_lens[b] + depth(t) + 1 for Scalable-Softmax.  A key that a node
  * does not see has no effect on it, whatever it holds (NaN and infinities
- * included).  A tree of one node is bam_attn_decode_paged with that token's
+ * included); an infinity or NaN in the value of a drafted key that it does see
+ * reaches it, however small that key's weight.  A tree of one node is bam_attn_decode_paged with that token's
  * length counted.  o: [B, H, N, D], fp32 when o_fp32 != 0, else bf16; lse:
  * fp32 [B, H, N] or NULL; rows behind draft_lens[b] are left as they were.
  * The weights enter the product with V as sums of bf16 parts: one part for

@@ -1,5 +1,6 @@
 """Tree attention where values are extreme: what a node does not see, or weighs
-with nothing, leaves no trace."""
+with nothing, leaves no trace; an infinity that it sees reaches it however the
+work was dealt."""
 
 import numpy as np
 import pytest
@@ -68,4 +69,34 @@ def test_large_values_of_vanishing_weight(H, Hkv, ln):
         kw = dict(parents=_i32(TREE[None]), o_dtype=out)
         o, lse = ba.attention_decode_tree_paged(q, c.k, c.v, *args, **kw)
         want, lse2 = ba.attention_decode_tree_paged(q, c.k, clean, *args, **kw)
+        assert torch.equal(o, want) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("B", [1, 400])
+@pytest.mark.parametrize("ln", [100, 5000])
+@pytest.mark.parametrize("H,Hkv", LAYOUTS)
+def test_drafted_infinities_of_vanishing_weight(H, Hkv, ln, B):
+    """The first 100 committed keys lie 128 above all others, so the weights of
+    the drafted ones are 0 beside them.  An infinite drafted value reaches the
+    nodes that see it all the same, whether the sequence is cut (alone, its
+    tiles go to many CTAs) or not (among 400 that share its pages)."""
+    N, page = len(TREE), 64
+    c = Cache(33, Hkv, page, [ln + N], -(-(ln + N) // page), NAN)
+    for j in range(ln + N):
+        c.k[int(c.table[0, j // page]), :, j % page] = 4.0 if j < 100 else 0.0
+    table, lens = c.table.expand(B, -1).contiguous(), _i32([ln] * B)
+    q = torch.full((B, H, N, 64), 4.0, dtype=torch.bfloat16, device="cuda")
+    args = (table, lens, *_flat(H))
+    clean = c.v.clone()
+    bad = {4: (float("inf"), [0, 20, 33]), 6: (float("-inf"), [15, 47, 63])}
+    for i, (value, dims) in bad.items():
+        c.v[int(c.table[0, (ln + i) // page]), :, (ln + i) % page, dims] = value
+    for out in (torch.float32, torch.bfloat16):
+        kw = dict(parents=_i32(np.tile(TREE, (B, 1))), o_dtype=out)
+        o, lse = ba.attention_decode_tree_paged(q, c.k, c.v, *args, **kw)
+        want, lse2 = ba.attention_decode_tree_paged(q, c.k, clean, *args, **kw)
+        assert torch.isfinite(want).all()
+        for n in range(N):
+            for i in set(path_to(TREE, n)) & set(bad):
+                want[:, :, n, bad[i][1]] = bad[i][0]
         assert torch.equal(o, want) and torch.equal(lse, lse2)

@@ -803,6 +803,25 @@ __device__ __forceinline__ void soft_tail(const TreeArgs& a, const View& v, cons
   soft_finish(a, sm, row, st, scale);
 }
 
+// o += the infinities and NaN among 2 W columns of the value of node i (zeros
+// stood for them in the products), from column col on.
+template <int W>
+__device__ __forceinline__ void add_odd(const TreeArgs& a, int b, int hk, int len, int i, int col,
+                                        float* o) {
+  const CacheArgs& c = a.c;
+  const int at = len + i;
+  int pg = __ldg(c.block_table + static_cast<size_t>(b) * c.max_blocks + at / c.page);
+  if (pg < 0 || pg >= c.num_pages) pg = 0;
+  const uint32_t* vr = reinterpret_cast<const uint32_t*>(
+      a.v_pages + ((static_cast<size_t>(pg) * c.Hkv + hk) * c.page + at % c.page) * kHeadDim + col);
+#pragma unroll
+  for (int y = 0; y < W; ++y) {
+    const uint32_t u = __ldg(vr + y);
+    if (odd_exp(u)) o[2 * y] += __uint_as_float(u << 16);
+    if (odd_exp(u >> 16)) o[2 * y + 1] += __uint_as_float(u & 0xFFFF0000u);
+  }
+}
+
 // o += x g, x being 4 N floats that another copy has handed over: chunks of 16
 // bytes, swizzled by the row.
 template <int N>
@@ -842,40 +861,29 @@ __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const
   const Item& it = sm.item[k & 1];
   const bool whole = it.t0 == 0 && it.t1 == it.tiles;
   const uint32_t* odd = sm.odd[k & 1];
-  const bool any_odd = (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
+  auto any_odd = [&]() { return (odd[0] | odd[1] | odd[2] | odd[3]) != 0; };
   const size_t orow =
       (static_cast<size_t>(it.b) * a.H + it.hk * a.group + it.g0 + row.hrel) * c.N + row.node;
   const size_t part = 2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
   float M = st.m, L = st.l;
   // Columns col .. col + kOwn - 1 of the row's output.
   auto put = [&](float* o, int col) __attribute__((always_inline)) {
-    if (any_odd) {
-      // Values that are not finite, for the nodes that see them.
-      const TreeInfo ti = tree_view(a, v, it.tree);
-#pragma unroll 1
-      for (int i = 0; i < it.n; ++i) {
-        if (!(odd[i >> 5] >> (i & 31) & 1) || !tree_sees(ti, row.node, i)) continue;
-        const int at = it.len + i;
-        int pg = __ldg(c.block_table + static_cast<size_t>(it.b) * c.max_blocks + at / c.page);
-        if (pg < 0 || pg >= c.num_pages) pg = 0;
-        const uint32_t* vr = reinterpret_cast<const uint32_t*>(
-            a.v_pages + ((static_cast<size_t>(pg) * c.Hkv + it.hk) * c.page + at % c.page) * kHeadDim +
-            col);
-#pragma unroll
-        for (int y = 0; y < kOwn / 2; ++y) {
-          const uint32_t u = __ldg(vr + y);
-          if (odd_exp(u)) o[2 * y] += __uint_as_float(u << 16);
-          if (odd_exp(u >> 16)) o[2 * y + 1] += __uint_as_float(u & 0xFFFF0000u);
-        }
-      }
-    }
     if (!whole) {  // left to the combine kernel
       float4* dst = reinterpret_cast<float4*>(a.part) + (part * 16 + col / 4) * S::kRows + row.rr;
 #pragma unroll
       for (int y = 0; y < kOwn / 4; ++y)
         dst[y * S::kRows] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-      if (col == 0) a.part_ml[part * S::kRows + row.rr] = make_float2(M, L);
+      // A sum with its sign bit set: drafted values that are not finite are
+      // still to be added (here their part's factor could turn them into NaN).
+      if (col == 0) a.part_ml[part * S::kRows + row.rr] = make_float2(M, any_odd() ? -L : L);
       return;
+    }
+    if (any_odd()) {
+      const TreeInfo ti = tree_view(a, v, it.tree);
+#pragma unroll 1
+      for (int i = 0; i < it.n; ++i)
+        if ((odd[i >> 5] >> (i & 31) & 1) && tree_sees(ti, row.node, i))
+          add_odd<kOwn / 2>(a, it.b, it.hk, it.len, i, col, o);
     }
     const float inv = 1.0f / L;
     if (PARTS > 1) {
@@ -1497,6 +1505,7 @@ __global__ void __launch_bounds__(kJoinThreads* kSplit) bam_tree_combine_kernel(
   const int r = it.r0 + rr, rows = a.group * it.n;
   const bool on = r < rows;
   float M = kNoMax, L = 0.0f;
+  unsigned odd = 0;  // its top bit: the sign of a part's sum
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const float4* part = reinterpret_cast<const float4*>(a.part);
   for (int x0 = c0 + split; on && x0 <= it.last; x0 += kJoinParts * kSplit) {
@@ -1522,7 +1531,8 @@ __global__ void __launch_bounds__(kJoinThreads* kSplit) bam_tree_combine_kernel(
     for (int u = 0; u < kJoinParts; ++u) {
       if (x0 + u * kSplit > it.last) continue;
       const float f = ex2_approx(ml[u].x - m);
-      L = fmaf(ml[u].y, f, L);
+      odd |= __float_as_uint(ml[u].y);
+      L = fmaf(fabsf(ml[u].y), f, L);
       v.x = fmaf(p[u].x, f, v.x);
       v.y = fmaf(p[u].y, f, v.y);
       v.z = fmaf(p[u].z, f, v.z);
@@ -1533,7 +1543,7 @@ __global__ void __launch_bounds__(kJoinThreads* kSplit) bam_tree_combine_kernel(
     __shared__ float4 sv[kSplit][kJoinThreads];
     __shared__ float2 sml[kSplit][kJoinThreads];
     sv[split][tid] = v;
-    sml[split][tid] = make_float2(M, L);
+    sml[split][tid] = make_float2(M, odd >> 31 ? -L : L);
     __syncthreads();
     if (split > 0) return;
     float m = M;
@@ -1548,13 +1558,24 @@ __global__ void __launch_bounds__(kJoinThreads* kSplit) bam_tree_combine_kernel(
       const float2 ml = sml[u][tid];
       const float4 p = sv[u][tid];
       const float f = ex2_approx(ml.x - m);
-      L = fmaf(ml.y, f, L);
+      odd |= __float_as_uint(ml.y);
+      L = fmaf(fabsf(ml.y), f, L);
       v = make_float4(fmaf(p.x, f, v.x), fmaf(p.y, f, v.y), fmaf(p.z, f, v.z), fmaf(p.w, f, v.w));
     }
   }
   if (!on) return;
   const float inv = 1.0f / L;
   const int h = r / it.n;
+  if (odd >> 31) {
+    // The row's node and its ancestors.
+    int len, n, i = r - h * it.n;
+    cache_lengths(c, it.b, &len, &n);
+    while (i >= 0) {
+      add_odd<2>(a, it.b, it.hk, len, i, 4 * chunk, reinterpret_cast<float*>(&v));
+      const int p = c.parents ? __ldg(c.parents + static_cast<size_t>(it.b) * c.N + i) : i - 1;
+      i = p < i ? p : -1;
+    }
+  }
   const size_t orow = (static_cast<size_t>(it.b) * a.H + it.hk * a.group + h) * c.N + (r - h * it.n);
   if (a.o_fp32)
     reinterpret_cast<float4*>(a.o)[orow * 16 + chunk] =
