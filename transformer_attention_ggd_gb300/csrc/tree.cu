@@ -415,6 +415,17 @@ __host__ __device__ constexpr int tree_tail_cost(int parts, int ks) {
   return tree_once(parts, ks) ? 1 : kTailCost;
 }
 
+// The tensor core cuts off the last place of O in every step of a product (16
+// keys, a part of their weights), toward zero, so that over thousands of steps
+// the sum falls short: with positive values of like weight, 304 sequences, by
+// 4e-4 after 512 tiles of three parts and 6e-3 after 16384 tiles of one.  After a
+// run of tiles O is therefore added to a sum in fp32 outside of Tensor Memory.
+// Tiles of a run for each copy, that is 96 steps or 256 to 512: what is lost is then
+// below 1e-5 and 3e-5 (bf16 output rounds by 2^-9 to 2^-8).  Runs of 4, 8 and 16 and no end
+// of a run took 139, 131, 128 and 121 us with three parts (131072 keys, 64 nodes); with
+// one part 64 cost nothing that shows (442 us for 64 sequences of 32768 keys), 16 cost 10%.
+constexpr int kRunParts = 8, kRunOne = 64;
+
 // Sizes of a kernel with PARTS parts of a weight and KS copies of a row.
 template <int PARTS, int KS>
 struct Shape {
@@ -426,8 +437,10 @@ struct Shape {
   static constexpr int kTailCost = tree_tail_cost(PARTS, KS);
   static constexpr int kTileBytes = kTile * kHeadDim * 2;
   static constexpr int kPCols = kTile / 2;           // columns of a part of P
+  static constexpr int kRun = (PARTS > 1 ? kRunParts : kRunOne) * KS;
   static constexpr uint32_t kColP = kTile;
   static_assert(kColP + kPCols * PARTS <= kColO, "Tensor Memory");
+  static_assert((kRun & (kRun - 1)) == 0 && kRun > kTreeMax / kTile + 1, "a tail lies in one run");
 };
 
 // The CTA's shared memory.  What grows with the nodes of a draft is laid out
@@ -478,6 +491,13 @@ struct SoftState {
   float m, l;       // running maximum (log2 units) and sum of the weights
   bool first;       // the item's first tile
   bool ok;
+};
+
+// The sum of an item's tiles before the run in Tensor Memory: output, weights, and
+// the maximum that they are relative to.  In local memory (the indexes vary), as
+// a thread has no 64 registers left.
+struct SoftSum {
+  float o[64], l, m;
 };
 
 // A softmax thread's row of the item in buffer k & 1.
@@ -581,6 +601,42 @@ __device__ __forceinline__ void soft_finish(const TreeArgs& a, TreeSmem& sm, con
   ++st.g;
   --st.t;
   st.first = false;
+}
+// Between two tiles, at the end of a run: adds O and l to the sum of the runs
+// before (if `held`).  The next product overwrites O; it waits for the next
+// tile's p_full.  kAhead, for short runs: what was held is on its way while the
+// last product ends and while columns are added (131 against 136 us with three
+// parts, 131072 keys and 64 nodes; with one part the code costs more than it saves).
+template <bool kAhead>
+__device__ __forceinline__ void soft_hold(const TreeArgs& a, TreeSmem& sm, const SoftRow& row,
+                                          SoftState& st, SoftSum& sum, bool held) {
+  constexpr int kCols = kAhead ? 32 : 16;
+  float o[kCols];
+  auto fetch = [&](int col) __attribute__((always_inline)) {
+#pragma unroll
+    for (int y = 0; y < kCols; ++y) o[y] = held ? sum.o[col + y] : 0.0f;
+  };
+  if (kAhead) fetch(0);
+  st.ok = warp_wait(&sm.pv_done, (st.g - 1) & 1, a.c.status, &sm.abort_flag, kSiteTreeSoftPV);
+  if (!st.ok) return;
+  tc_fence_after();
+  if (row.warp_live) {
+    const float f = held ? ex2_approx(sum.m - st.m) : 0.0f;
+#pragma unroll 1
+    for (int col = 0; col < 64; col += kCols) {
+      if (!kAhead) fetch(col);
+      uint32_t ov[kCols];
+      tmem_ld_cols<kCols>(row.lanes + kColO + col, ov);
+#pragma unroll
+      for (int y = 0; y < kCols; ++y)
+        sum.o[col + y] = fmaf(o[y], f, __uint_as_float(ov[y]));
+      if (kAhead) fetch((col + kCols) & 63);
+    }
+    sum.l = held ? fmaf(sum.l, f, st.l) : st.l;
+    sum.m = st.m;
+    st.l = 0.0f;
+  }
+  tc_fence_before();
 }
 // Two weights and their bf16 parts; l2 gathers the exact ones.  Three parts
 // are cut off, not rounded: 8 bits each are the weight's 24, and none is
@@ -849,7 +905,7 @@ __device__ __forceinline__ void hand_row(uint8_t* row, int swz, const float* o) 
 // that they have read), so that each ends with 64 / KS columns of the sum.
 template <int PARTS, int KS>
 __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const SoftRow& row,
-                                         const SoftState& st, int k) {
+                                         const SoftState& st, const SoftSum& sum, int k) {
   using S = Shape<PARTS, KS>;
   TreeSmem& sm = *v.sm;
   const CacheArgs& c = a.c;
@@ -866,6 +922,18 @@ __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const
       (static_cast<size_t>(it.b) * a.H + it.hk * a.group + it.g0 + row.hrel) * c.N + row.node;
   const size_t part = 2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
   float M = st.m, L = st.l;
+  const bool held = it.t1 - it.t0 > S::kRun;
+  const float kept = held ? ex2_approx(sum.m - M) : 0.0f;
+  if (held) L = fmaf(sum.l, kept, L);
+  // 32 columns of this lane's output, with what the runs before left of them.
+  auto load = [&](int col, uint32_t* ov) __attribute__((always_inline)) {
+    tmem_ld_cols<32>(row.lanes + kColO + col, ov);
+    if (held) {
+#pragma unroll
+      for (int y = 0; y < 32; ++y)
+        ov[y] = __float_as_uint(fmaf(sum.o[col + y], kept, __uint_as_float(ov[y])));
+    }
+  };
   // Columns col .. col + kOwn - 1 of the row's output.
   auto put = [&](float* o, int col) __attribute__((always_inline)) {
     if (!whole) {  // left to the combine kernel
@@ -908,7 +976,7 @@ __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const
   if (KS == 1) {
 #pragma unroll 1
     for (int col = 0; col < 64 && row.warp_live; col += 32) {
-      tmem_ld_cols<32>(row.lanes + kColO + col, ov);
+      load(col, ov);
       if (row.live) put(o, col);
     }
   } else {
@@ -916,10 +984,10 @@ __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const
     const int mine = threadIdx.x, other = mine ^ S::kRows, swz = mine & 7;
     int col = 32 * (row.copy & 1);  // of o[0]
     if (row.warp_live) {
-      tmem_ld_cols<32>(row.lanes + kColO + (col ^ 32), ov);
+      load(col ^ 32, ov);
       hand_row<8>(merge + mine * 128, swz, o);
       v.merge_ml[mine] = make_float2(M, L);
-      tmem_ld_cols<32>(row.lanes + kColO + col, ov);
+      load(col, ov);
     }
     // The next maximum and sum, and what is kept of both.
     auto join = [&](int from, float& f, float& g) {
@@ -1352,14 +1420,14 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       // Two places in the same sequence of tiles: S runs ahead of P V.
       struct Place {
         int k, left, g, s, phase;  // item, its tiles to come, tile, ring slot and phase
-        bool first;
+        int run;                   // tiles of the item that O is to take on
       };
-      Place ps{-1, 0, 0, 0, 0, true}, pv{-1, 0, 0, 0, 0, true};
+      Place ps{-1, 0, 0, 0, 0, 0}, pv{-1, 0, 0, 0, 0, 0};
       bool ok = true;
       auto advance = [&](Place& p) {
         --p.left;
         ++p.g;
-        p.first = false;
+        p.run = (p.run + 1) & (S::kRun - 1);
         if (++p.s == a.stages) {
           p.s = 0;
           p.phase ^= 1;
@@ -1369,7 +1437,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       auto enter = [&](Place& p) {
         if (p.left > 0) return true;
         ++p.k;
-        p.first = true;
+        p.run = 0;
         ok = ok && tree_wait(&sm.item_full[p.k & 1], (p.k >> 1) & 1, c.status, ab, kSiteTreeMmaItem);
         if (!ok) return false;
         const Item& it = sm.item[p.k & 1];
@@ -1416,7 +1484,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             constexpr int kSteps = kTile / 16 / KS;
             umma_ts_lanes<KS>(tm + kColO, tm + S::kColP + S::kPCols * part + 8 * kk,
                               vd + kSlotDesc * pv.s + 128 * kk, id_o,
-                              (!pv.first || part > 0 || kk % kSteps > 0) ? 1u : 0u, kk / kSteps);
+                              (pv.run > 0 || part > 0 || kk % kSteps > 0) ? 1u : 0u, kk / kSteps);
           }
         umma_commit(&sm.pv_done);
         umma_commit(&sm.v_empty[pv.s]);
@@ -1432,6 +1500,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   } else {
     // ---------------------------------------------------------------- softmax
     SoftState st{0, 0, 0, 0, 0.0f, 0.0f, true, true};
+    SoftSum sum;
     for (int k = 0;; ++k) {
       st.ok = warp_wait(&sm.item_full[k & 1], (k >> 1) & 1, c.status, ab, kSiteTreeSoftItem);
       if (!st.ok) break;
@@ -1443,9 +1512,16 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       st.l = 0.0f;
       st.first = true;
       const SoftRow row = soft_row<S>(a, v, k);
+      // (the tail ends within the first run)
+      int stop = st.t - S::kRun;
       while (st.ok && st.t >= max(plain, t0)) soft_tail<PARTS, KS>(a, v, row, st, k);
-      while (st.ok && st.t >= t0) soft_tile<PARTS, KS>(a, v, row, st);
-      if (!st.ok || !soft_end<PARTS, KS>(a, v, row, st, k)) break;
+      for (bool held = false; st.ok; held = true, stop -= S::kRun) {
+        const int last = max(stop + 1, t0);
+        while (st.ok && st.t >= last) soft_tile<PARTS, KS>(a, v, row, st);
+        if (!st.ok || st.t < t0) break;
+        soft_hold<(PARTS > 1)>(a, sm, row, st, sum, held);
+      }
+      if (!st.ok || !soft_end<PARTS, KS>(a, v, row, st, sum, k)) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
     }
