@@ -106,7 +106,7 @@ __device__ __forceinline__ void append_load(const AppendArgs& a, const AppendUni
 // depths and angles then take no time of their own.
 template <bool kRun>
 __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_kernel(const AppendArgs a) {
-  __shared__ float2 cs[kAppendTokens][kHeadDim / 2];
+  __shared__ float4 cs[kAppendTokens][kHeadDim / 4];  // two (cosine, sine) pairs each
   __shared__ int64_t slot_row[kAppendTokens];  // row of head 0 in the pages, -1: not written
   __shared__ int depth[kTreeMax], jump[kTreeMax];
   const CacheArgs& c = a.c;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
         const int top = static_cast<int>((pos * a.freq[f]) >> 32);
         float s, co;
         sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &co);
-        cs[t][f] = make_float2(co, s);
+        reinterpret_cast<float2*>(cs[t])[f] = make_float2(co, s);
       }
       __syncthreads();
       last_b = x.b;
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
       if (rotated && x.kind < 2) {
         float4 r[4];  // eight (cosine, sine) pairs
 #pragma unroll
-        for (int y = 0; y < 4; ++y) r[y] = reinterpret_cast<const float4*>(cs[ln.t] + 8 * u4)[y];
+        for (int y = 0; y < 4; ++y) r[y] = cs[ln.t][4 * u4 + y];
 #pragma unroll
         for (int y = 0; y < kAppendRows; ++y) {
           if (ln.h + y * ln.step >= x.heads) break;
