@@ -287,15 +287,13 @@ __global__ void __launch_bounds__(kKeepThreads) bam_kv_keep_kernel(const KeepArg
   __syncthreads();
   const int m = count;
   bool pages_ok = true;
-  if (c.parents) {
-    for (int x = threadIdx.x; x < m; x += kKeepThreads) {
-      const int s = len + path[m - 1 - x], d = len + x;
-      const int ps = __ldg(c.block_table + static_cast<size_t>(b) * c.max_blocks + s / c.page);
-      const int pd = __ldg(c.block_table + static_cast<size_t>(b) * c.max_blocks + d / c.page);
-      pages_ok &= ps >= 0 && ps < c.num_pages && pd >= 0 && pd < c.num_pages;
-      src_row[x] = static_cast<int64_t>(ps) * c.Hkv * c.page + s % c.page;
-      dst_row[x] = static_cast<int64_t>(pd) * c.Hkv * c.page + d % c.page;
-    }
+  for (int x = threadIdx.x; x < m; x += kKeepThreads) {
+    const int s = len + (c.parents ? path[m - 1 - x] : x), d = len + x;
+    const int ps = __ldg(c.block_table + static_cast<size_t>(b) * c.max_blocks + s / c.page);
+    const int pd = __ldg(c.block_table + static_cast<size_t>(b) * c.max_blocks + d / c.page);
+    pages_ok &= ps >= 0 && ps < c.num_pages && pd >= 0 && pd < c.num_pages;
+    src_row[x] = static_cast<int64_t>(ps) * c.Hkv * c.page + s % c.page;
+    dst_row[x] = static_cast<int64_t>(pd) * c.Hkv * c.page + d % c.page;
   }
   pages_ok = __syncthreads_and(pages_ok);
   if (blockIdx.x == 0 && threadIdx.x == 0 && !(ok && pages_ok)) record_bad_arg(c.status);
