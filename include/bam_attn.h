@@ -194,7 +194,7 @@ bam_status bam_attn_decode_paged(const void* q, const void* k_pages, const void*
  * multiple of 16 from 0 (no rotation) to 64.  Angles are reduced exactly (a
  * 64-bit fraction of a turn), so far positions keep their accuracy. */
 typedef struct {
-  double base;     /* > 0, finite; for example 10000                         */
+  double base;     /* >= 1, finite; for example 10000                        */
   int dims;
   int interleaved; /* 0: pair f is (x[f], x[f + dims/2]); 1: (x[2f], x[2f+1]) */
 } bam_rope;

@@ -201,3 +201,12 @@ def test_calls_by_words_need_an_operator_and_words(lib):
     assert lib.bam_paged_call(0, None) == ba.BAM_ERR_INVALID_ARG
     with pytest.raises(TypeError):
         ba._struct_address(object(), ba.BamRope)
+
+
+@pytest.mark.parametrize("base", [1.0 - 2.0 ** -53, 0.5, 1e-12, 1e-300, -1.0])
+def test_a_rotation_needs_a_base_of_at_least_one(lib, base):
+    """Below it a position is many turns, of which 64 bits hold no fraction that
+    is right at far positions (none at all for 1e-300)."""
+    assert _append(lib, rope=ba.BamRope(base, 64, 0)) == ba.BAM_ERR_INVALID_ARG
+    with pytest.raises(ValueError, match="at least 1"):
+        ba.make_rope(base)

@@ -473,8 +473,8 @@ def make_rope(base=10000.0, dims=64, interleaved=False) -> BamRope:
     (f, f + dims/2)."""
     if not 0 <= int(dims) <= 64 or int(dims) % 16:
         raise ValueError("dims must be a multiple of 16 from 0 to 64")
-    if not 0.0 < float(base) < float("inf"):
-        raise ValueError("base must be positive and finite")
+    if not 1.0 <= float(base) < float("inf"):
+        raise ValueError("base must be at least 1 and finite")
     return BamRope(float(base), int(dims), int(bool(interleaved)))
 
 

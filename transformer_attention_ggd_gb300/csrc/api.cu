@@ -464,9 +464,9 @@ bam_status bam_kv_append_paged(const void* k, const void* v, const void* q, void
   AppendArgs a = {};
   if (rope && rope->dims != 0) {
     if (rope->dims < 0 || rope->dims > kHeadDim || rope->dims % 16 != 0 ||
-        (rope->interleaved != 0 && rope->interleaved != 1) || !(rope->base > 0.0) ||
+        (rope->interleaved != 0 && rope->interleaved != 1) || !(rope->base >= 1.0) ||
         !std::isfinite(rope->base))
-      return BAM_ERR_INVALID_ARG;
+      return BAM_ERR_INVALID_ARG;  // (below 1, turns per position exceed what a double's fraction holds)
     a.dims = rope->dims;
     a.interleaved = rope->interleaved;
     // base^(-2 f / dims) by repeated products: their 2^-48 is 2^-23 turns at
@@ -474,10 +474,8 @@ bam_status bam_kv_append_paged(const void* k, const void* v, const void* q, void
     const double ratio = std::pow(rope->base, -2.0 / rope->dims);
     double per = 1.0 / 6.283185307179586477;
     for (int f = 0; f < rope->dims / 2; ++f, per *= ratio) {
-      // Only the fraction of a turn per position matters.
-      double turns = per - std::floor(per);
-      if (!(turns < 1.0)) turns = 0.0;  // also when base is extreme
-      a.freq[f] = static_cast<uint64_t>(turns * 18446744073709551616.0);
+      // (per is below 1: base is at least 1)
+      a.freq[f] = static_cast<uint64_t>(per * 18446744073709551616.0);
     }
   }
   for (int x = 0; x < 9; ++x) {
