@@ -238,7 +238,10 @@ bam_status bam_kv_append_paged(const void* k, const void* v, const void* q, void
  * length counted.  o: [B, H, N, D], fp32 when o_fp32 != 0, else bf16; lse:
  * fp32 [B, H, N] or NULL; rows behind draft_lens[b] are left as they were.
  * The weights enter the product with V as sums of bf16 parts: one part for
- * bf16 output, three (24 bits) for fp32 output.  A page number out of range
+ * bf16 output, three (24 bits) for fp32 output.  Products and weights are summed
+ * in fp32, with weights of up to 2^8 (they are relative to the largest logit met
+ * so far): values of seen keys that add up to more than 1e36 may overflow.  A
+ * page number out of range
  * reads page 0 and is reported.  If a device wait of the call gives up, the
  * rows of o and lse are written as NaN.  o does not overlap q. */
 bam_status bam_attn_decode_tree_paged(const void* q, const void* k_pages, const void* v_pages,

@@ -895,7 +895,8 @@ def kv_append_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_lens=No
                     q=None, rope=None, ws=None, stream=None):
     """Append k, v [B, Hkv, N, 64] to the pages behind cache_lens committed
     keys, rotated by position when rope is given; returns the rotated q (None
-    without q).  cache_lens is not changed."""
+    without q).  cache_lens is not changed.  Without ws, tokens that had no
+    slot go unreported (bam_attn_check_status(ws))."""
     import torch
     q_out = None
     if q is not None:
@@ -916,7 +917,9 @@ def attention_decode_tree_paged(q, k_pages, v_pages, block_table, cache_lens, al
                                 o_dtype=None, ws=None, stream=None, prior=BAM_PRIOR_ALPHA):
     """Attention of drafted tokens q bf16 [B,H,N,64] over a paged cache that
     already holds their keys and values behind cache_lens committed ones ->
-    (o [B,H,N,64], lse [B,H,N]); rows behind draft_lens are zero."""
+    (o [B,H,N,64], lse [B,H,N]); rows behind draft_lens are zero.  o_dtype:
+    fp32 by default; bf16 is faster.  Without ws (tree_workspace(...)) each call
+    clears one of its own, and what it would report is lost with it."""
     import torch
     B, H, N, D = q.shape
     make = torch.empty if draft_lens is None else torch.zeros
@@ -935,7 +938,8 @@ def attention_decode_tree_paged(q, k_pages, v_pages, block_table, cache_lens, al
 def kv_keep_paged(k_pages, v_pages, block_table, cache_lens, accepted, parents, draft_lens=None,
                   new_lens=None, ws=None, stream=None):
     """Keep the accepted path of each draft; returns the new lengths (written
-    to new_lens, which may be cache_lens, if given)."""
+    to new_lens, which may be cache_lens, if given).  Without ws, paths that
+    could not be kept go unreported."""
     import torch
     with _on(stream):
         if new_lens is None:

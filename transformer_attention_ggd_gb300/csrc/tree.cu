@@ -21,10 +21,12 @@
 // joins.  Ragged batches and a single long sequence keep every SM busy alike.
 //
 // Measured (HBM copy 6.70 TB/s, L2 129 MB; a call with its three kernels, in a
-// graph): 64 sequences of 32768 keys at most, 12 heads, 32 nodes 441 us (3.2 GB,
+// graph): 64 sequences of 32768 keys at most, 12 heads, 32 nodes 442 us (3.2 GB,
 // 7.3 TB/s with what L2 keeps); 32 of 16384, 8 key heads, one node, 4 heads a
-// key head 100 us (537 MB); one of 131072, 12 heads, 64 nodes 85 us (403 MB); 4
-// of 20000, 12 heads, 128 nodes 71 us (249 MB); one of 500, 7 nodes 13.0 us.
+// key head 101 us (537 MB); one of 131072, 12 heads, 64 nodes 87 us (403 MB); 4
+// of 20000, 12 heads, 128 nodes 72 us (249 MB); one of 500, 7 nodes 13.4 us.
+// fp32 output: 8 of 4096, 16 nodes 29 us (51 MB); 131 and 102 us for the third
+// and the fourth.
 #include "table_eval.cuh"
 #include "tree_common.cuh"
 
@@ -399,9 +401,9 @@ __device__ __forceinline__ void cp_async_wait() {
 
 // Keys of a tile: as many as S and the parts of P leave Tensor Memory for, and no
 // more than 64 columns a thread.  128 against 64 keys where both fit, a call:
-// 441 and 456 us with 64 sequences of 32768 keys and 32 rows, 87 and 89 with 64
-// rows and 131072 keys, 48 and 58 with 8 rows and 100 keys, 101 and 101 with 4
-// rows and 16384; 13.0 and 11.9 with 7 rows and one sequence of 500.
+// 442 and 463 us with 64 sequences of 32768 keys and 32 rows, 87 and 88 with 64
+// rows and 131072 keys, 50 and 59 with 8 rows and 100 keys, 101 and 103 with 4
+// rows and 16384; 13.4 and 12.6 with 7 rows and one sequence of 500.
 __host__ __device__ constexpr int tree_tile(int parts, int ks) {
   return parts == 1 && ks > 1 ? 128 : 64;
 }
@@ -423,7 +425,8 @@ __host__ __device__ constexpr int tree_tail_cost(int parts, int ks) {
 // Tiles of a run for each copy, that is 96 steps or 256 to 512: what is lost is then
 // below 1e-5 and 3e-5 (bf16 output rounds by 2^-9 to 2^-8).  Runs of 4, 8 and 16 and no end
 // of a run took 139, 131, 128 and 121 us with three parts (131072 keys, 64 nodes); with
-// one part 64 cost nothing that shows (442 us for 64 sequences of 32768 keys), 16 cost 10%.
+// one part 64 and 16 took 442 and 461 (64 sequences of 32768 keys), 71.7 and 79.0 (4
+// chains of 128 nodes, 20000 keys).
 constexpr int kRunParts = 8, kRunOne = 64;
 
 // Sizes of a kernel with PARTS parts of a weight and KS copies of a row.
@@ -1065,6 +1068,9 @@ __device__ __forceinline__ bool soft_end(const TreeArgs& a, const View& v, const
 // PARTS: bf16 parts of a weight in the product with V.  One rounds a weight by
 // at most 2^-8, which moves an output by as much as its own rounding to bf16
 // does; three carry 24 bits, for fp32 output.  Sums are of the exact weights.
+// Measured against 64 bits: 0.0017 to 0.0020 relative for bf16 output (0.0016 to
+// 0.0017 are its own rounding), 4e-7 to 1e-6 for fp32 output, up to 7e-6 where
+// thousands of positive values have about the same weight (kRunParts).
 template <int PARTS, int KS>
 __global__ void __launch_bounds__(kTreeThreads, 2)
     bam_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -1114,8 +1120,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   // (a wait that looks at an abort word before it is cleared would give up).
   // With few sequences (one a lane) the producer makes the plan itself, and its
   // first loads of keys and queries, which no kernel of the call writes, do not
-  // wait: 16.8 instead of 17.9 us for 16 sequences of 360 keys, 13.0 instead of
-  // 14.3 for one of 500; 101.1 against 100.5 at 32 of 16384, 44.1 against 43.0 at
+  // wait: 17.4 instead of 18.5 us for 16 sequences of 360 keys, 13.4 instead of
+  // 14.5 for one of 500, 86.8 instead of 89.6 for one of 131072; 44.0 against 43.7 at
   // 13 of 9001.
   grid_dep_trigger();
   if (warp != kProducer || c.B > 32) grid_dep_wait();
@@ -1538,8 +1544,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 // Joins the parts of the items that were cut: blocks (x, .) the one of record x.
 // A warp takes half the columns of four rows, a lane four columns (a chunk) of
 // one row, of every kSplit-th part.  kSplit 4 is for items of many parts: one
-// sequence of 131072 keys, 12 heads (26 parts an item) 98 us with 1, 89 with 4;
-// 4 chains of 128 nodes over 20000 keys (7 parts) 74.6 with 1, 82 with 4.
+// sequence of 131072 keys, 12 heads (26 parts an item) 95 us with 1, 87 with 4;
+// 4 chains of 128 nodes over 20000 keys (7 parts) 71.6 with 1, 78.6 with 4.
 constexpr int kJoinThreads = 128, kJoinParts = 8;  // parts in flight
 constexpr int kJoinRows = kJoinThreads / 16;       // rows of a block
 template <int kSplit>
@@ -1701,7 +1707,10 @@ cudaError_t launch_parts(const CUtensorMap& tk, const CUtensorMap& tv, const Tre
 }  // namespace
 
 // Ring and grid of the call, from its sizes.  Returns false when a stage does
-// not fit (more heads share a key head than its windows have room for).
+// not fit (more heads share a key head than its windows have room for).  From 16
+// query heads a key head on, with few nodes, the windows of 128-key tiles leave
+// room for one CTA an SM instead of two: 64 single tokens over 16384 keys take
+// 169 us with 64 query and 4 key heads, 108 with 32 and 4.
 bool tree_config(TreeArgs* a, int sms) {
   a->tile = tree_tile(a->o_fp32 ? 3 : 1, kRowsMax / a->rows);
   // Most heads and floats that a stage's windows hold, over the node counts.
@@ -1733,7 +1742,7 @@ bool tree_config(TreeArgs* a, int sms) {
 
 cudaError_t launch_tree_prep(const TreeArgs& a, cudaStream_t st) {
   // It asks for the attention kernel's division of an SM's memory, whose CTAs can
-  // then start beside it: 84.8 instead of 87.2 us with 131072 keys.
+  // then start beside it: 86.8 instead of 88.8 us with 131072 keys.
   static bool divided[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

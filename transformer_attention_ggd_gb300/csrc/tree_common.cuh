@@ -52,15 +52,14 @@ struct KeepArgs {
 // and CTA c of `active` takes units [W c / active, W (c+1) / active) of the W
 // in all.
 // An item's fixed cost, in units of a tile of committed keys.  3, 4 and 7
-// measured 45.1, 44.2 and 44.8 us (13 sequences of 9001 keys, 21 nodes), 100.3,
-// 101.1 and 103.2 (32 of 16384, single tokens), 28.8, 28.6 and 30.2 (8 of 4096,
-// fp32 output).
+// measured 45.3, 44.0 and 44.5 us (13 sequences of 9001 keys, 21 nodes), 100.6,
+// 101.4 and 103.5 (32 of 16384, single tokens), 29.4, 29.4 and 31.1 (8 of 4096,
+// fp32 output), 13.8, 13.4 and 13.2 (one of 500, 7 nodes).
 constexpr int kItemCost = 4;
 // Units of a tile with drafted keys where its logits do not stay in registers.
-// 1, 2 and 3 measured 73.7, 71.4 and 70.6 us (4 chains of 128 nodes, 20000
-// keys), 44.7, 44.2 and 43.6 (13 of 9001, 21 nodes), 108.2, 108.2 and 111.1 (100
-// of 600, 40 nodes, 8 heads a key head, fp32 output), 13.0, 13.0 and 14.2 (one of
-// 500, 7 nodes).
+// 1 and 2 measured 74.2 and 71.7 us (4 chains of 128 nodes, 20000 keys), 45.2 and
+// 44.0 (13 of 9001, 21 nodes), 116.3 and 118.3 (100 of 600, 40 nodes, 8 heads a
+// key head, fp32 output).
 constexpr int kTailCost = 2;
 constexpr int kTreeCtas = 304;   // most CTAs (two per SM)
 
@@ -84,7 +83,7 @@ struct TreeArgs {
   int64_t* plan;      // [B + 1] first unit of each sequence, and W
   float* table;       // [H, tab_len]: entry y is b_h(tab_zero - y) * log2(e)
   float* part;        // [2 * kTreeCtas, 16, rows, 4] partial outputs, by four columns
-  float2* part_ml;    // [2 * kTreeCtas, rows]: maximum (log2 units), sum
+  float2* part_ml;    // [2 * kTreeCtas, rows]: maximum (log2 units), sum (sign bit: odd values to come)
   CutItem* cut;       // [kTreeCtas]
   int by_item, nrb_most;  // nrb_most: items of a sequence and key head, at most
   float eps;
@@ -101,10 +100,10 @@ struct TreeArgs {
 
 // Rows of an item for `rows` (head, node) pairs: Tensor Memory's 128, or the half
 // or quarter that holds them all; they then stand there two or four times, each
-// copy with its part of the keys.  Against 128 always, a call: 441 and 498 us
-// with 32 rows and 64 sequences of 32768 keys, 101 and 110 with 4 rows and
-// 16384 keys, 87 and 90 with 64 rows and 131072, 48 and 74 with 8 rows and 256
-// sequences of 100; 13.0 and 12.3 with 7 rows and one sequence of 500.
+// copy with its part of the keys.  Against 128 always, a call: 442 and 515 us
+// with 32 rows and 64 sequences of 32768 keys, 101 and 112 with 4 rows and
+// 16384 keys, 87 and 91 with 64 rows and 131072, 50 and 78 with 8 rows and 256
+// sequences of 100; 13.4 and 12.8 with 7 rows and one sequence of 500.
 inline int tree_rows(int64_t rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 // Table row: distances 0 .. Tmax at entries Tmax .. 0 and, behind entry
 // Tmax, room for windows that reach past the last key.
