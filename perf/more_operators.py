@@ -214,6 +214,7 @@ def prepare(case, seed):
         st["q_out"] = torch.zeros(B, H, N, D, dtype=torch.bfloat16, device="cuda")
         st["lens"], st["new"], st["pos"] = i32(lens), i32(new), None
         if case["marked"]:
+            st["span"] = 200000
             # the sequences have been longer than what is left of them
             st["pos"] = i32(lens + rng.integers(0, 100000, B))
             st["key_pos"] = torch.zeros(num, Hkv, page, dtype=torch.int32, device="cuda")
@@ -258,7 +259,7 @@ def prepare(case, seed):
     out, num = _tables(rng, -(-np.minimum(lens, budget) // page), -(-min(budget, T) // page), num)
     _cache(st, gen, B, Hkv, page, num, table)
     st["lens"], st["out"], st["new_lens"] = i32(lens), i32(out), i32(np.zeros(B))
-    _marks(st, gen, case, lens, 0, 2)
+    st["span"] = _marks(st, gen, case, lens, 0, 2) + 1
     return st
 
 
@@ -446,7 +447,7 @@ def run(state):
         else:
             kept.update(ws=ba.cache_workspace())
     if "key_pos" in state and not kept.get("marks"):
-        kept.update(marks=ba.make_marks(state["key_pos"], state["key_weight"]))
+        kept.update(marks=ba.make_marks(state["key_pos"], state["key_weight"], state["span"]))
     if op == "qk_norm":
         ba.bam_qk_norm_fwd(state["q"], state["k"], state["q_out"], state["k_out"], state["positions"],
                            kept["norm"], kept["rope"])
@@ -468,7 +469,7 @@ def run(state):
             Pmax = state["prefix"].numel() * case["page"] if case["P"] else 0
             kept.update(prm=ba.make_params(*state["prm"], EPS, True, case["ssmax"], prior),
                         ws=ba.shared_workspace(case["B"], case["H"], case["Hkv"], Pmax, Tmax,
-                                               case["marked"]))
+                                               state["span"] if case["marked"] else 0))
         ba.bam_attn_decode_shared_paged(state["q"], *cache, state.get("prefix"), state.get("prefix_len"),
                                         state["q_pos"], kept.get("marks"), 1.0, state["o"], state["lse"],
                                         kept["prm"], kept["ws"])
