@@ -271,14 +271,180 @@ bam_status bam_kv_keep_paged(void* k_pages, void* v_pages, const int* block_tabl
                              int max_blocks, int num_pages, int D, void* ws, size_t ws_bytes,
                              cudaStream_t stream);
 
-/* The three operators above for bindings whose foreign calls cost time for each
+/* ---------------------------------------------------------------------------
+ * Norms of queries and keys
+ *
+ * Every head vector x of the queries and of the keys is normalised and then
+ * rotated by its position:
+ *
+ *     y = R(pos) ( w * x / sqrt(mean(x^2) + eps) ),
+ *
+ * with weights w for the queries and for the keys, in fp32, rounded once to
+ * bf16.  Gradients: with dn = R(-pos) dy and n = x / sqrt(mean(x^2) + eps),
+ * dw = sum dn n and dx = (w dn - n mean(w dn n)) / sqrt(mean(x^2) + eps).
+ * ------------------------------------------------------------------------- */
+
+typedef struct {
+  const float* q_weight; /* device fp32 [64], or [H, 64] with per_head; 16-byte aligned */
+  const float* k_weight; /* device fp32 [64], or [Hkv, 64] with per_head     */
+  float eps;             /* >= 1e-30, finite; for example 1e-6               */
+  int per_head;          /* 0: one weight vector for all heads               */
+} bam_qk_norm;
+
+/* q: bf16 [B, H, T, D] and k: bf16 [B, Hkv, T, D] -> q_out, k_out of the same
+ * shapes, ready for bam_attn_fwd (Hkv may be any number).  positions: device
+ * int32 [B, T], any values; NULL: token t has position t.  rope: NULL or dims
+ * 0: no rotation.  strides: element strides over batch, head and token of q,
+ * k, q_out and k_out (twelve values, multiples of 8, >= 0; rows of an output
+ * must not overlap), so that slices of a projection's output need no copy;
+ * NULL when all are dense.  q_out may be q itself with the same strides, and
+ * k_out k; otherwise outputs overlap no input and no other output.  No
+ * workspace; one launch. */
+bam_status bam_qk_norm_fwd(const void* q, const void* k, void* q_out, void* k_out,
+                           const int64_t* strides, const int* positions, int B, int H, int Hkv,
+                           int T, int D, const bam_qk_norm* norm, const bam_rope* rope,
+                           cudaStream_t stream);
+
+/* Gradients of bam_qk_norm_fwd.  q, k: its inputs; dq_out, dk_out: bf16
+ * gradients of its outputs; dq, dk: bf16 gradients of q and k; strides: of q,
+ * k, dq_out, dk_out, dq and dk (eighteen values as above).  dq may be dq_out or q
+ * itself with the same strides, and dk likewise.  dq_weight, dk_weight: fp32,
+ * shaped as the weights, overwritten; their sums run in a fixed order. */
+bam_status bam_qk_norm_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                           void* dq, void* dk, const int64_t* strides, float* dq_weight,
+                           float* dk_weight, const int* positions, int B, int H, int Hkv, int T,
+                           int D, const bam_qk_norm* norm, const bam_rope* rope, void* ws,
+                           size_t ws_bytes, cudaStream_t stream);
+
+/* Bytes of workspace of bam_qk_norm_bwd (it holds no status words).  Returns 0
+ * for invalid sizes.  Host-only. */
+size_t bam_qk_norm_workspace_size(int B, int H, int Hkv, int T, int D);
+
+/* ---------------------------------------------------------------------------
+ * A long, bounded cache
+ *
+ * The prior depends on the distance between positions.  While a paged cache
+ * holds every key of its sequence, slots tell positions; once keys have left
+ * it, each key needs its own.  Marks are pages [num_pages, Hkv, page] beside
+ * those of keys and values, under the same block table: the position of each
+ * key and the attention weight that it has gathered so far.
+ * bam_kv_append_norm_paged writes them, bam_attn_decode_shared_paged reads the
+ * positions and adds to the weights, bam_kv_evict_paged keeps the keys of the
+ * largest weights.
+ * ------------------------------------------------------------------------- */
+
+typedef struct {
+  int* key_pos;      /* device int32 [num_pages, Hkv, page], 16-byte aligned */
+  float* key_weight; /* device fp32 [num_pages, Hkv, page], 16-byte aligned  */
+  int max_pos;       /* positions lie in [0, max_pos); 1 to 2^28             */
+} bam_marks;
+
+/* bam_kv_append_paged for heads with norms and caches with marks: keys, and
+ * queries if given, are normalised (norm; NULL: not) before they are rotated.
+ * first_pos: device int32 [B], the position of each sequence's token 0 (with
+ * parents: of depth 0), in [0, 2^28]; NULL: cache_lens.  marks (or NULL): each
+ * written key gets its position and the weight 0; a position of max_pos or
+ * more is written and reported.  All else, the workspace too, is as in
+ * bam_kv_append_paged. */
+bam_status bam_kv_append_norm_paged(const void* k, const void* v, const void* q, void* q_out,
+                                    const int64_t* strides, void* k_pages, void* v_pages,
+                                    const int* block_table, const int* cache_lens,
+                                    const int* new_lens, const int* parents, int B, int H, int Hkv,
+                                    int N, int page, int max_blocks, int num_pages, int D,
+                                    const bam_qk_norm* norm, const bam_rope* rope,
+                                    const int* first_pos, const bam_marks* marks, void* ws,
+                                    size_t ws_bytes, cudaStream_t stream);
+
+/* Decode of one query per sequence over a prefix that the whole batch shares and
+ * the sequence's own keys.  q: bf16 [B, H, D]; query head h reads key head
+ * h / (H / Hkv).
+ *
+ * prefix_table: device int32 [prefix_blocks], prefix_len: device int32 [1];
+ * the shared prefix is the first prefix_len keys of these pages, at positions
+ * 0 .. P-1.  Its keys and values are read once for all sequences.  Both NULL
+ * and prefix_blocks 0: no prefix.  block_table, cache_lens: the own keys, 0 or
+ * more.  A sequence without any key gets o = 0 and lse = -infinity.
+ *
+ * Without marks (marks and q_pos NULL), own key j has position P + j and the
+ * query P + cache_lens[b] - 1: the own keys include the new token's.  With
+ * marks, own keys have the positions of key_pos and the query has q_pos[b]
+ * (device int32 [B]); key_weight of each own key becomes
+ *
+ *     decay * key_weight + sum over the group's heads of exp(z - lse),
+ *
+ * 0 <= decay <= 1, while the prefix gathers nothing.  Scalable-Softmax's n is
+ * the query's position + 1.  Prefix lengths, cache lengths and q_pos out of
+ * range are clamped, a key behind the query counts as at the query's position,
+ * and a page number out of range reads page 0; all are reported by
+ * bam_attn_check_status as BAM_ERR_INVALID_ARG.  Sequences with marks share
+ * own pages with no other sequence of the call.
+ *
+ * What lies behind a sequence's keys has no effect, whatever it holds.  A NaN
+ * in a key reaches o, lse and the weights of its head; NaN and infinities in a
+ * value reach o.  Products and weights are summed in fp32, the weights of the
+ * product with V as sums of bf16 parts (16 bits for bf16 output, 24 for fp32).
+ * If a device wait of the call gives up, o and lse are written as NaN and no
+ * weight changes.  o: [B, H, D], fp32 when o_fp32 != 0, else bf16; lse: fp32
+ * [B, H] or NULL.  p->causal is ignored.  Every output is bitwise repeatable. */
+bam_status bam_attn_decode_shared_paged(const void* q, const void* k_pages, const void* v_pages,
+                                        const int* block_table, const int* cache_lens,
+                                        const int* prefix_table, const int* prefix_len,
+                                        const int* q_pos, const bam_marks* marks, float decay,
+                                        void* o, int o_fp32, float* lse, int B, int H, int Hkv,
+                                        int page, int max_blocks, int prefix_blocks, int num_pages,
+                                        int D, const bam_params* p, void* ws, size_t ws_bytes,
+                                        cudaStream_t stream);
+
+/* Bytes of workspace of bam_attn_decode_shared_paged: Pmax = prefix_blocks *
+ * page, Tmax = max_blocks * page, max_pos of the marks (0 without).  Returns 0
+ * for invalid sizes.  Host-only. */
+size_t bam_attn_shared_workspace_size(int B, int H, int Hkv, int Pmax, int Tmax, int max_pos, int D);
+
+/* Eviction: of every sequence that has more than `budget` own keys, each key
+ * head keeps the first `sink` keys, the last `recent` ones and, of the others,
+ * those with the largest key_weight (a NaN counts as largest; among equals the
+ * lowest slots), `budget` in all.  They move, with their positions and weights,
+ * in order to slots 0 .. budget-1; other sequences keep their keys as they
+ * are.  new_lens: device int32 [B], min(cache_lens, budget); it may be
+ * cache_lens itself.  budget >= 1, sink, recent >= 0, sink + recent <= budget.
+ *
+ * out_table NULL (out_blocks 0): in place; slots behind new_lens hold what is
+ * left.  Else device int32 [B, out_blocks], out_blocks * page >= budget (or
+ * all of max_blocks * page): the keys kept, of every sequence, go to these
+ * pages, which belong to no block_table row, and the old pages stay as they
+ * were (for sequences whose pages are shared with others).
+ *
+ * A length out of range is clamped; a sequence with a page number out of range
+ * in a used block keeps all its pages as they were and its length; both are
+ * reported.  In place, sequences share no pages.  Two launches. */
+bam_status bam_kv_evict_paged(void* k_pages, void* v_pages, const int* block_table,
+                              const int* cache_lens, const bam_marks* marks, const int* out_table,
+                              int* new_lens, int B, int Hkv, int page, int max_blocks,
+                              int out_blocks, int num_pages, int D, int budget, int sink,
+                              int recent, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Bytes of workspace of bam_kv_evict_paged (Tmax = max_blocks * page).  Returns
+ * 0 for invalid sizes.  Host-only. */
+size_t bam_kv_evict_workspace_size(int B, int Hkv, int Tmax, int budget);
+
+/* The operators above for bindings whose foreign calls cost time for each
  * argument: `words` holds the arguments of operator `op` in order, a 64-bit
- * word each (pointers and structs by address, integers as they are).  In the
- * place of the append's strides stands 0 (NULL) or 1: nine stride words then
- * follow the last argument.  Checks, results and errors are the operator's; an
- * integer that does not fit its parameter or an unknown op is
+ * word each (pointers and structs by address, integers as they are, decay as
+ * the bits of a float).  In the place of the strides of an append or a norm
+ * stands 0 (NULL) or 1: nine (norms: twelve forward, eighteen backward) stride
+ * words then follow the last argument.  Checks, results and errors are the
+ * operator's; an integer that does not fit its parameter or an unknown op is
  * BAM_ERR_INVALID_ARG. */
-enum { BAM_CALL_KV_APPEND = 0, BAM_CALL_DECODE_TREE = 1, BAM_CALL_KV_KEEP = 2 };
+enum {
+  BAM_CALL_KV_APPEND = 0,
+  BAM_CALL_DECODE_TREE = 1,
+  BAM_CALL_KV_KEEP = 2,
+  BAM_CALL_KV_APPEND_NORM = 3,
+  BAM_CALL_QK_NORM_FWD = 4,
+  BAM_CALL_QK_NORM_BWD = 5,
+  BAM_CALL_DECODE_SHARED = 6,
+  BAM_CALL_KV_EVICT = 7
+};
 bam_status bam_paged_call(int op, const void* words);
 
 /* Synchronises `stream`, then reads and clears the device status word of
@@ -383,7 +549,16 @@ enum {
   BAM_KERNEL_TREE = 9,         /* tree attention                              */
   BAM_KERNEL_TREE_COMBINE = 10,
   BAM_KERNEL_KV_KEEP = 11,
-  BAM_KERNEL_COUNT = 12
+  BAM_KERNEL_QK_NORM = 12,
+  BAM_KERNEL_QK_NORM_BWD = 13,
+  BAM_KERNEL_QK_NORM_FINISH = 14, /* sums of the weights' gradients         */
+  BAM_KERNEL_SHARED_PREP = 15,    /* shared decode                          */
+  BAM_KERNEL_SHARED = 16,
+  BAM_KERNEL_SHARED_JOIN = 17,
+  BAM_KERNEL_SHARED_WEIGH = 18,   /* accumulated weights                    */
+  BAM_KERNEL_EVICT_SELECT = 19,
+  BAM_KERNEL_EVICT_MOVE = 20,
+  BAM_KERNEL_COUNT = 21
 };
 
 /* Instrumentation: while set, every launch of kernel `which` is bracketed

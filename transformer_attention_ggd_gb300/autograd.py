@@ -53,3 +53,32 @@ def bam_attention(q, k, v, alpha, beta, mu, s=None, *, causal=True, ssmax=False,
     o_dtype = o_dtype or torch.bfloat16
     return BamAttention.apply(q, k, v, alpha, beta, mu, s if ssmax else None, bool(causal),
                               bool(ssmax), int(prior), float(eps), o_dtype)
+
+
+class QkNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, rope, eps):
+        out = ba.qk_norm_forward(q, k, q_weight, k_weight, positions, rope, eps)
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions)
+        ctx.cfg = (rope, eps)
+        return out
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, positions = ctx.saved_tensors
+        rope, eps = ctx.cfg
+        g = (x.to(torch.bfloat16).contiguous() for x in (dq_out, dk_out))
+        dq, dk, dqw, dkw = ba.qk_norm_backward(q, k, *g, q_weight, k_weight, positions, rope, eps)
+        return dq, dk, dqw, dkw, None, None, None
+
+
+def qk_norm(q, k, q_weight, k_weight, positions=None, rope=None, eps=1e-6):
+    """Norms of queries and keys for each head and their rotation, with autograd.
+
+    q: bf16 CUDA tensor [B, H, T, 64], k: [B, Hkv, T, 64], rows of 64 contiguous
+    and 16-byte aligned (slices of a projection's output need no copy).
+    q_weight, k_weight: fp32 [64], or [H, 64] and [Hkv, 64].  positions: int32
+    [B, T] or None (0, 1, ..); rope: ``bam_attn.make_rope(...)`` or None.
+    Returns contiguous (q_out, k_out), as ``bam_attention`` takes them.
+    """
+    return QkNorm.apply(q, k, q_weight, k_weight, positions, rope, float(eps))

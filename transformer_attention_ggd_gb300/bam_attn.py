@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -55,7 +56,16 @@ BAM_KERNEL_TREE_PREP = 8
 BAM_KERNEL_TREE = 9
 BAM_KERNEL_TREE_COMBINE = 10
 BAM_KERNEL_KV_KEEP = 11
-BAM_KERNEL_COUNT = 12
+BAM_KERNEL_QK_NORM = 12
+BAM_KERNEL_QK_NORM_BWD = 13
+BAM_KERNEL_QK_NORM_FINISH = 14
+BAM_KERNEL_SHARED_PREP = 15
+BAM_KERNEL_SHARED = 16
+BAM_KERNEL_SHARED_JOIN = 17
+BAM_KERNEL_SHARED_WEIGH = 18
+BAM_KERNEL_EVICT_SELECT = 19
+BAM_KERNEL_EVICT_MOVE = 20
+BAM_KERNEL_COUNT = 21
 
 # Every symbol that include/bam_attn.h declares.
 EXPORTED = (
@@ -81,11 +91,19 @@ EXPORTED = (
     "bam_attn_tree_workspace_size",
     "bam_kv_keep_paged",
     "bam_paged_call",
+    "bam_qk_norm_fwd",
+    "bam_qk_norm_bwd",
+    "bam_qk_norm_workspace_size",
+    "bam_kv_append_norm_paged",
+    "bam_attn_decode_shared_paged",
+    "bam_attn_shared_workspace_size",
+    "bam_kv_evict_paged",
+    "bam_kv_evict_workspace_size",
 )
 
 # Size of the fixed device scratch of bam_attn_decode_noalloc.
 BAM_DECODE_NOALLOC_SCRATCH_BYTES = 4 << 20
-# Workspace of bam_kv_append_paged and bam_kv_keep_paged (status words only).
+# Workspace of the appends and of bam_kv_keep_paged (status words only).
 BAM_CACHE_WORKSPACE_BYTES = 256
 # Most nodes of a draft with parents (tree attention, keep).
 BAM_TREE_MAX_NODES = 128
@@ -115,6 +133,23 @@ class BamRope(ctypes.Structure):
         ("base", ctypes.c_double),
         ("dims", ctypes.c_int),
         ("interleaved", ctypes.c_int),
+    ]
+
+
+class BamQkNorm(ctypes.Structure):
+    _fields_ = [
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("per_head", ctypes.c_int),
+    ]
+
+
+class BamMarks(ctypes.Structure):
+    _fields_ = [
+        ("key_pos", ctypes.c_void_p),
+        ("key_weight", ctypes.c_void_p),
+        ("max_pos", ctypes.c_int),
     ]
 
 
@@ -184,6 +219,26 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.bam_attn_tree_workspace_size.argtypes = [i] * 6
         lib.bam_kv_keep_paged.restype = i
         lib.bam_kv_keep_paged.argtypes = [vp] * 8 + [i] * 7 + [vp, sz, vp]
+        np_, mp = ctypes.POINTER(BamQkNorm), ctypes.POINTER(BamMarks)
+        rp = ctypes.POINTER(BamRope)
+        lib.bam_qk_norm_fwd.restype = i
+        lib.bam_qk_norm_fwd.argtypes = [vp] * 4 + [lp, vp] + [i] * 5 + [np_, rp, vp]
+        lib.bam_qk_norm_bwd.restype = i
+        lib.bam_qk_norm_bwd.argtypes = [vp] * 6 + [lp, vp, vp, vp] + [i] * 5 + [np_, rp, vp, sz, vp]
+        lib.bam_qk_norm_workspace_size.restype = sz
+        lib.bam_qk_norm_workspace_size.argtypes = [i] * 5
+        lib.bam_kv_append_norm_paged.restype = i
+        lib.bam_kv_append_norm_paged.argtypes = [vp] * 4 + [lp] + [vp] * 6 + [i] * 8 + [
+            np_, rp, vp, mp, vp, sz, vp]
+        lib.bam_attn_decode_shared_paged.restype = i
+        lib.bam_attn_decode_shared_paged.argtypes = [vp] * 8 + [mp, ctypes.c_float, vp, i, vp] + [
+            i] * 8 + [pp, vp, sz, vp]
+        lib.bam_attn_shared_workspace_size.restype = sz
+        lib.bam_attn_shared_workspace_size.argtypes = [i] * 7
+        lib.bam_kv_evict_paged.restype = i
+        lib.bam_kv_evict_paged.argtypes = [vp] * 4 + [mp, vp, vp] + [i] * 10 + [vp, sz, vp]
+        lib.bam_kv_evict_workspace_size.restype = sz
+        lib.bam_kv_evict_workspace_size.argtypes = [i] * 4
         lib.bam_paged_call.restype = i
         lib.bam_paged_call.argtypes = [i, ctypes.c_char_p]
         _lib = lib
@@ -325,6 +380,19 @@ def bam_status_string(status: int) -> str:
 
 def bam_attn_tree_workspace_size(B: int, H: int, Hkv: int, N: int, Tmax: int, D: int = 64) -> int:
     return int(load_library().bam_attn_tree_workspace_size(B, H, Hkv, N, Tmax, D))
+
+
+def bam_qk_norm_workspace_size(B: int, H: int, Hkv: int, T: int, D: int = 64) -> int:
+    return int(load_library().bam_qk_norm_workspace_size(B, H, Hkv, T, D))
+
+
+def bam_attn_shared_workspace_size(B: int, H: int, Hkv: int, Pmax: int, Tmax: int,
+                                   max_pos: int = 0, D: int = 64) -> int:
+    return int(load_library().bam_attn_shared_workspace_size(B, H, Hkv, Pmax, Tmax, max_pos, D))
+
+
+def bam_kv_evict_workspace_size(B: int, Hkv: int, Tmax: int, budget: int) -> int:
+    return int(load_library().bam_kv_evict_workspace_size(B, Hkv, Tmax, budget))
 
 
 def bam_attn_workspace_size(op: int, B: int, H: int, T: int, D: int = 64) -> int:
@@ -714,6 +782,336 @@ def bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, par
         _check(st, "bam_kv_keep_paged")
 
 
+# ---------------------------------------------------------------- norms of queries and keys
+
+def make_qk_norm(q_weight, k_weight, eps=1e-6) -> BamQkNorm:
+    """Norms of the heads' queries and keys: weights fp32 [64], or [H, 64] and
+    [Hkv, 64], contiguous CUDA tensors, which the returned struct keeps alive."""
+    import torch
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if not isinstance(t, torch.Tensor) or t.dim() not in (1, 2) or t.shape[-1] != 64:
+            raise ValueError(f"{name} must be a tensor [64] or [heads, 64]")
+        _require(t, name, t.shape, (torch.float32,), q_weight.device)
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name} must be 16-byte aligned")
+    if q_weight.dim() != k_weight.dim():
+        raise ValueError("q_weight and k_weight are both [64] or both [heads, 64]")
+    if not 1e-30 <= float(eps) < float("inf"):
+        raise ValueError("eps must be at least 1e-30 and finite")
+    norm = BamQkNorm(q_weight.data_ptr(), k_weight.data_ptr(), float(eps), int(q_weight.dim() == 2))
+    norm.tensors = (q_weight, k_weight)
+    return norm
+
+
+def make_marks(key_pos, key_weight, max_pos) -> BamMarks:
+    """Marks of a paged cache: key_pos int32 and key_weight fp32, contiguous
+    CUDA tensors [num_pages, Hkv, page], which the returned struct keeps alive;
+    positions lie in [0, max_pos)."""
+    import torch
+    if not isinstance(key_pos, torch.Tensor) or key_pos.dim() != 3:
+        raise ValueError("key_pos must be a tensor [num_pages, Hkv, page]")
+    _require(key_pos, "key_pos", key_pos.shape, (torch.int32,), key_pos.device)
+    _require(key_weight, "key_weight", key_pos.shape, (torch.float32,), key_pos.device)
+    if key_pos.data_ptr() % 16 or key_weight.data_ptr() % 16:
+        raise ValueError("key_pos and key_weight must be 16-byte aligned")
+    if not 1 <= int(max_pos) <= 1 << 28:
+        raise ValueError("max_pos must lie in [1, 2^28]")
+    marks = BamMarks(key_pos.data_ptr(), key_weight.data_ptr(), int(max_pos))
+    marks.tensors = (key_pos, key_weight)
+    return marks
+
+
+_append_norm_words = struct.Struct("35q").pack
+_norm_fwd_words = struct.Struct("26q").pack
+_norm_bwd_words = struct.Struct("38q").pack
+_shared_words = struct.Struct("25q").pack
+_evict_words = struct.Struct("20q").pack
+_float_bits = functools.lru_cache(64)(lambda x: struct.unpack("<i", struct.pack("<f", x))[0])
+
+
+def _norm_fits(norm, index, H, Hkv):
+    """A norm's weights lie on CUDA device `index` and fit the heads (a struct built
+    by hand from raw pointers: the caller vouches for them)."""
+    tensors = getattr(norm, "tensors", None)
+    if tensors is None:
+        return True
+    q, k = tensors
+    return (q.get_device() == index and k.get_device() == index
+            and (q.dim() == 1 or (q.shape[0] == H and k.shape[0] == Hkv)))
+
+
+def _marks_fit(marks, index, pool):
+    tensors = getattr(marks, "tensors", None)
+    return tensors is None or (tensors[0].get_device() == index and tensors[1].get_device() == index
+                               and tensors[0].shape == pool[:3])
+
+
+def _check_norm_marks(norm, marks, index, H, Hkv, pool):
+    if norm is not None and not _norm_fits(norm, index, H, Hkv):
+        raise ValueError(f"the norm's weights must be on cuda:{index}, [64] or [{H}, 64] and [{Hkv}, 64]")
+    if marks is not None and not _marks_fit(marks, index, pool):
+        raise ValueError(f"the marks must be on cuda:{index}, shaped {tuple(pool[:3])}")
+
+
+def _check_norm_rows(rows, positions, B, T, norm, H, Hkv):
+    """The detailed checks of a norm's tensors: rows (name, tensor, shape)."""
+    dev = _device(rows[0][1], rows[0][0])
+    for name, t, shape in rows:
+        _check_rows(t, name, shape, dev)
+    _check_tensors((("positions", positions, (B, T), _dt()[3], True),), dev)
+    _check_norm_marks(norm, None, dev.index, H, Hkv, None)
+    return dev
+
+
+def bam_qk_norm_fwd(q, k, q_out, k_out, positions, norm: BamQkNorm, rope=None, stream=None,
+                    check=True) -> None:
+    """q [B, H, T, 64], k [B, Hkv, T, 64] normalised by head and rotated by
+    positions (int32 [B, T], or None: 0, 1, ..) into q_out, k_out; rows of 64
+    contiguous and 16-byte aligned, other strides free."""
+    B, H, T, D = qs = q.shape
+    Hkv = k.shape[1]
+    ks = (B, Hkv, T, D)
+    index = q.get_device()
+    if check:
+        import torch
+        try:
+            ok = (index >= 0 and index == _current_device() and D == 64 and _rows_ok(index, qs, q)
+                  and _rows_ok(index, ks, k) and _rows_ok(index, qs, q_out)
+                  and _rows_ok(index, ks, k_out) and _norm_fits(norm, index, H, Hkv)
+                  and (positions is None or (positions.dtype is torch.int32
+                                             and positions.get_device() == index
+                                             and positions.shape == (B, T)
+                                             and positions.is_contiguous())))
+        except AttributeError:
+            ok = False
+        if not ok:
+            qs, ks = (B, H, T, 64), (B, Hkv, T, 64)
+            _check_norm_rows((("q", q, qs), ("k", k, ks), ("q_out", q_out, qs), ("k_out", k_out, ks)),
+                             positions, B, T, norm, H, Hkv)
+            raise ValueError("argument check failed")
+    st = load_library().bam_paged_call(4, _norm_fwd_words(
+        q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), 1, _address(positions), B, H,
+        Hkv, T, D, _struct_address(norm, BamQkNorm), _struct_address(rope, BamRope),
+        _raw_stream(stream, index), *q.stride()[:3], *k.stride()[:3], *q_out.stride()[:3],
+        *k_out.stride()[:3]))
+    if st:
+        _check(st, "bam_qk_norm_fwd")
+
+
+def bam_qk_norm_bwd(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, positions, norm: BamQkNorm,
+                    rope, ws, stream=None, check=True) -> None:
+    """Gradients of bam_qk_norm_fwd: of q and k (dq, dk, any strides) and of the
+    weights (fp32, shaped as they are)."""
+    B, H, T, D = qs = q.shape
+    Hkv = k.shape[1]
+    ks = (B, Hkv, T, D)
+    index = q.get_device()
+    if check:
+        import torch
+        wq, wk = ((H, 64), (Hkv, 64)) if norm.per_head else ((64,), (64,))
+        try:
+            ok = (index >= 0 and index == _current_device() and D == 64 and _rows_ok(index, qs, q)
+                  and _rows_ok(index, ks, k) and _rows_ok(index, qs, dq_out)
+                  and _rows_ok(index, ks, dk_out) and _rows_ok(index, qs, dq)
+                  and _rows_ok(index, ks, dk) and _norm_fits(norm, index, H, Hkv))
+            for t, dtype, shape in ((dq_weight, torch.float32, wq), (dk_weight, torch.float32, wk),
+                                    (positions, torch.int32, (B, T))):
+                if t is not None or dtype is torch.float32:
+                    ok = ok and (t.dtype is dtype and t.get_device() == index and t.shape == shape
+                                 and t.is_contiguous())
+            ok = ok and (ws.dtype is torch.uint8 and ws.get_device() == index and ws.dim() == 1
+                         and ws.is_contiguous())
+        except AttributeError:
+            ok = False
+        if not ok:
+            qs, ks = (B, H, T, 64), (B, Hkv, T, 64)
+            dev = _check_norm_rows((("q", q, qs), ("k", k, ks), ("dq_out", dq_out, qs),
+                                    ("dk_out", dk_out, ks), ("dq", dq, qs), ("dk", dk, ks)),
+                                   positions, B, T, norm, H, Hkv)
+            f32 = _dt()[1]
+            _check_tensors((("dq_weight", dq_weight, wq, f32, False),
+                            ("dk_weight", dk_weight, wk, f32, False)), dev)
+            _check_ws(ws, dev)
+            raise ValueError("argument check failed")
+    st = load_library().bam_paged_call(5, _norm_bwd_words(
+        q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), 1, dq_weight.data_ptr(), dk_weight.data_ptr(), _address(positions), B, H, Hkv,
+        T, D, _struct_address(norm, BamQkNorm), _struct_address(rope, BamRope), ws.data_ptr(),
+        ws.numel(), _raw_stream(stream, index), *q.stride()[:3], *k.stride()[:3],
+        *dq_out.stride()[:3], *dk_out.stride()[:3], *dq.stride()[:3], *dk.stride()[:3]))
+    if st:
+        _check(st, "bam_qk_norm_bwd")
+
+
+# ---------------------------------------------------------------- a long, bounded cache
+
+def bam_kv_append_norm_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_lens, parents, q,
+                             q_out, norm, rope, first_pos, marks, ws, stream=None,
+                             check=True) -> None:
+    """bam_kv_append_paged with the norms of make_qk_norm (or None), positions
+    that start at first_pos (int32 [B], or None: cache_lens) and the marks of
+    make_marks (or None), which get each written key's position and weight 0."""
+    B, Hkv, N, D = shape = k.shape
+    num_pages, pool_heads, page, _ = pool = k_pages.shape
+    table = block_table.shape
+    index = k.get_device()
+    H = Hkv
+    strides = k.stride()[:3] + v.stride()[:3]
+    if q is not None:
+        H = q.shape[1]
+        strides += q.stride()[:3]
+    if check:
+        import torch
+        specs = () if q is None else ((q_out, torch.bfloat16, (B, H, N, 64)),)
+        if first_pos is not None:
+            specs += ((first_pos, torch.int32, (B,)),)
+        try:
+            ok = (index >= 0 and index == _current_device() and D == 64 and pool_heads == Hkv
+                  and _rows_ok(index, shape, k) and _rows_ok(index, shape, v)
+                  and (q is None) == (q_out is None)
+                  and (q is None or _rows_ok(index, (B, H, N, 64), q))
+                  and (norm is None or _norm_fits(norm, index, H, Hkv))
+                  and (marks is None or _marks_fit(marks, index, pool))
+                  and _all_ok(index, pool, k_pages, v_pages, table, block_table, cache_lens,
+                              new_lens, parents, ws, B, N, specs))
+        except AttributeError:
+            ok = False
+        if not ok:
+            dev = _device(k, "k")
+            _check_rows(k, "k", (B, pool_heads, N, 64), dev)
+            _check_rows(v, "v", shape, dev)
+            if (q is None) != (q_out is None):
+                raise ValueError("q and q_out go together")
+            if q is not None:
+                _check_rows(q, "q", (B, H, N, 64), dev)
+            bf, _, _, i32 = _dt()
+            _check_tensors(_cache_specs(k_pages, v_pages, block_table, cache_lens, new_lens,
+                                        parents, B, N)
+                           + (("q_out", q_out, (B, H, N, 64), bf, True),
+                              ("first_pos", first_pos, (B,), i32, True)), dev)
+            _check_norm_marks(norm, marks, dev.index, H, Hkv, pool)
+            _check_ws(ws, dev)
+            raise ValueError("argument check failed")
+    if q is None:
+        strides += (0, 0, 0)
+    st = load_library().bam_paged_call(3, _append_norm_words(
+        k.data_ptr(), v.data_ptr(), _address(q), _address(q_out),
+        1, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+        cache_lens.data_ptr(), _address(new_lens), _address(parents), B, H, Hkv, N, page,
+        table[1], num_pages, D, _struct_address(norm, BamQkNorm), _struct_address(rope, BamRope),
+        _address(first_pos), _struct_address(marks, BamMarks), ws.data_ptr(), ws.numel(),
+        _raw_stream(stream, index), *strides))
+    if st:
+        _check(st, "bam_kv_append_norm_paged")
+
+
+def bam_attn_decode_shared_paged(q, k_pages, v_pages, block_table, cache_lens, prefix_table,
+                                 prefix_len, q_pos, marks, decay, o, lse, params: BamParams, ws,
+                                 stream=None, check=True) -> None:
+    """q, o [B, H, 64] over the prefix of prefix_table int32 [blocks] and
+    prefix_len int32 [1] (both None: no prefix) and the own keys of block_table
+    and cache_lens int32 [B].  marks: make_marks(...) with q_pos int32 [B], or
+    both None; the marks' weights decay by `decay` and gather this step's.  lse
+    [B, H] or None."""
+    import torch
+    B, H, D = shape = q.shape
+    num_pages, Hkv, page, _ = pool = k_pages.shape
+    table = block_table.shape
+    index = q.get_device()
+    out = o.dtype
+    blocks = 0 if prefix_table is None else prefix_table.shape[0]
+    if (prefix_table is None) != (prefix_len is None):
+        raise ValueError("prefix_table and prefix_len go together")
+    if (marks is None) != (q_pos is None):
+        raise ValueError("marks and q_pos go together")
+    if check:
+        f32 = torch.float32
+        try:
+            prm = getattr(params, "tensors", None)
+            specs = ((q, torch.bfloat16, shape), (o, out, shape))
+            if lse is not None:
+                specs += ((lse, f32, (B, H)),)
+            if blocks:
+                specs += ((prefix_table, torch.int32, (blocks,)), (prefix_len, torch.int32, (1,)))
+            if q_pos is not None:
+                specs += ((q_pos, torch.int32, (B,)),)
+            if prm is not None:
+                specs += ((prm[0], f32, (H,)), (prm[1], f32, (H,)), (prm[2], f32, (H,)))
+                if prm[3] is not None:
+                    specs += ((prm[3], f32, (H,)),)
+            ok = (index >= 0 and index == _current_device() and D == 64
+                  and (out is torch.bfloat16 or out is f32)
+                  and (prefix_table is None or blocks > 0)
+                  and (marks is None or _marks_fit(marks, index, pool))
+                  and _all_ok(index, pool, k_pages, v_pages, table, block_table, cache_lens, None,
+                              None, ws, B, 1, specs))
+        except AttributeError:
+            ok = False
+        if not ok:
+            dev = _device(q)
+            bf, f32s, outs, i32 = _dt()
+            _check_tensors((("q", q, (B, H, 64), bf, False), ("o", o, (B, H, 64), outs, False),
+                            ("lse", lse, (B, H), f32s, True),
+                            ("prefix_table", prefix_table, (max(blocks, 1),), i32, True),
+                            ("prefix_len", prefix_len, (1,), i32, True),
+                            ("q_pos", q_pos, (B,), i32, True))
+                           + _cache_specs(k_pages, v_pages, block_table, cache_lens, None, None, B,
+                                          1) + _param_specs(params, H), dev)
+            _check_norm_marks(None, marks, dev.index, H, Hkv, pool)
+            _check_ws(ws, dev)
+            raise ValueError("argument check failed")
+    st = load_library().bam_paged_call(6, _shared_words(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+        cache_lens.data_ptr(), _address(prefix_table), _address(prefix_len), _address(q_pos),
+        _struct_address(marks, BamMarks), _float_bits(decay), o.data_ptr(),
+        1 if out is torch.float32 else 0, _address(lse), B, H, Hkv, page, table[1], blocks, num_pages,
+        D, _struct_address(params, BamParams), ws.data_ptr(), ws.numel(),
+        _raw_stream(stream, index)))
+    if st:
+        _check(st, "bam_attn_decode_shared_paged")
+
+
+def bam_kv_evict_paged(k_pages, v_pages, block_table, cache_lens, marks: BamMarks, out_table,
+                       new_lens, budget: int, sink: int, recent: int, ws, stream=None,
+                       check=True) -> None:
+    """Each key head of a sequence with more than `budget` keys keeps its first
+    `sink`, its last `recent` and the heaviest of the others; new_lens int32 [B]
+    (may be cache_lens) gets the lengths.  out_table int32 [B, blocks]: pages for
+    the kept keys; None: in place."""
+    num_pages, Hkv, page, D = pool = k_pages.shape
+    table = block_table.shape
+    B = table[0]
+    index = k_pages.get_device()
+    out_blocks = 0 if out_table is None else out_table.shape[-1]
+    if check:
+        import torch
+        specs = ((new_lens, torch.int32, (B,)),)
+        if out_table is not None:
+            specs += ((out_table, torch.int32, (B, out_blocks)),)
+        try:
+            ok = (index >= 0 and index == _current_device() and _marks_fit(marks, index, pool)
+                  and _all_ok(index, pool, k_pages, v_pages, table, block_table, cache_lens, None,
+                              None, ws, B, 1, specs))
+        except AttributeError:
+            ok = False
+        if not ok:
+            dev = _device(k_pages, "k_pages")
+            i32 = _dt()[3]
+            _check_tensors(_cache_specs(k_pages, v_pages, block_table, cache_lens, None, None, B, 1)
+                           + (("new_lens", new_lens, (B,), i32, False),
+                              ("out_table", out_table, (B, out_blocks), i32, True)), dev)
+            _check_norm_marks(None, marks, dev.index, Hkv, Hkv, pool)
+            _check_ws(ws, dev)
+            raise ValueError("argument check failed")
+    st = load_library().bam_paged_call(7, _evict_words(
+        k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(),
+        _struct_address(marks, BamMarks), _address(out_table), new_lens.data_ptr(), B, Hkv, page,
+        table[1], out_blocks, num_pages, D, budget, sink, recent, ws.data_ptr(), ws.numel(),
+        _raw_stream(stream, index)))
+    if st:
+        _check(st, "bam_kv_evict_paged")
+
+
 def bam_attn_selftest_wait(ws, stream=None) -> None:
     """Launch the failure-detection self-test: a bounded wait that runs out
     and records BAM_ERR_TIMEOUT in the status word of `ws` (about 2 s)."""
@@ -797,9 +1195,34 @@ def tree_workspace(B: int, H: int, Hkv: int, N: int, Tmax: int, device="cuda"):
 
 
 def cache_workspace(device="cuda"):
-    """Workspace of bam_kv_append_paged and bam_kv_keep_paged."""
+    """Workspace of the appends and of bam_kv_keep_paged."""
     import torch
     return torch.zeros(BAM_CACHE_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+
+
+def _zeros(n, name, device):
+    import torch
+    if n == 0:
+        raise BamError(BAM_ERR_INVALID_ARG, name)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def qk_norm_workspace(B: int, H: int, Hkv: int, T: int, device="cuda"):
+    """Workspace of bam_qk_norm_bwd."""
+    return _zeros(bam_qk_norm_workspace_size(B, H, Hkv, T), "bam_qk_norm_workspace_size", device)
+
+
+def shared_workspace(B: int, H: int, Hkv: int, Pmax: int, Tmax: int, max_pos: int = 0, device="cuda"):
+    """Workspace of bam_attn_decode_shared_paged (Pmax = prefix blocks * page, Tmax =
+    max_blocks * page; max_pos of the marks, 0 without)."""
+    return _zeros(bam_attn_shared_workspace_size(B, H, Hkv, Pmax, Tmax, max_pos),
+                  "bam_attn_shared_workspace_size", device)
+
+
+def evict_workspace(B: int, Hkv: int, Tmax: int, budget: int, device="cuda"):
+    """Workspace of bam_kv_evict_paged (Tmax = max_blocks * page)."""
+    return _zeros(bam_kv_evict_workspace_size(B, Hkv, Tmax, budget), "bam_kv_evict_workspace_size",
+                  device)
 
 
 def attention_forward(q, k, v, alpha, beta, mu, s=None, eps=1e-5, causal=True, ssmax=False,
@@ -948,4 +1371,95 @@ def kv_keep_paged(k_pages, v_pages, block_table, cache_lens, accepted, parents, 
             ws = cache_workspace(k_pages.device)
     bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, parents, accepted,
                       new_lens, ws, stream)
+    return new_lens
+
+
+def qk_norm_forward(q, k, q_weight, k_weight, positions=None, rope=None, eps=1e-6, stream=None):
+    """Norms and rotation of q [B, H, T, 64] and k [B, Hkv, T, 64] (any batch,
+    head and token strides) -> contiguous (q_out, k_out)."""
+    import torch
+    with _on(stream):
+        q_out, k_out = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
+    bam_qk_norm_fwd(q, k, q_out, k_out, positions, make_qk_norm(q_weight, k_weight, eps), rope, stream)
+    return q_out, k_out
+
+
+def qk_norm_backward(q, k, dq_out, dk_out, q_weight, k_weight, positions=None, rope=None, eps=1e-6,
+                     ws=None, stream=None):
+    """Gradients of qk_norm_forward: (dq, dk, dq_weight, dk_weight), dq and dk contiguous."""
+    import torch
+    B, H, T, _ = q.shape
+    with _on(stream):
+        dq, dk = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
+        dqw, dkw = torch.empty_like(q_weight), torch.empty_like(k_weight)
+        if ws is None:
+            ws = torch.empty(bam_qk_norm_workspace_size(B, H, k.shape[1], T), dtype=torch.uint8,
+                             device=q.device)
+    bam_qk_norm_bwd(q, k, dq_out, dk_out, dq, dk, dqw, dkw, positions,
+                    make_qk_norm(q_weight, k_weight, eps), rope, ws, stream)
+    return dq, dk, dqw, dkw
+
+
+def kv_append_norm_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_lens=None, parents=None,
+                         q=None, norm=None, rope=None, first_pos=None, marks=None, ws=None,
+                         stream=None):
+    """kv_append_paged with norms, positions from first_pos on and marks (see
+    bam_kv_append_norm_paged); returns the normalised and rotated q."""
+    import torch
+    q_out = None
+    if q is not None:
+        make = torch.empty if new_lens is None else torch.zeros
+        with _on(stream):
+            q_out = make(q.shape, dtype=q.dtype, device=q.device)
+    if ws is None:
+        with _on(stream):
+            ws = cache_workspace(k_pages.device)
+    bam_kv_append_norm_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_lens, parents, q,
+                             q_out, norm, rope, first_pos, marks, ws, stream)
+    return q_out
+
+
+def attention_decode_shared_paged(q, k_pages, v_pages, block_table, cache_lens, alpha, beta, mu,
+                                  s=None, prefix_table=None, prefix_len=None, q_pos=None, marks=None,
+                                  decay=1.0, eps=1e-5, ssmax=False, o_dtype=None, ws=None,
+                                  stream=None, prior=BAM_PRIOR_ALPHA):
+    """Decode of q bf16 [B, H, 64] over a prefix that the batch shares and each
+    sequence's own keys -> (o [B, H, 64], lse [B, H]).  With marks and q_pos the
+    own keys have positions and gather weights.  o_dtype: fp32 by default.
+    Without ws (shared_workspace(...)) each call clears one of its own, and what it would
+    report is lost with it."""
+    import torch
+    B, H, D = q.shape
+    page = k_pages.shape[2]
+    with _on(stream):
+        o = torch.empty((B, H, D), dtype=o_dtype or torch.float32, device=q.device)
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = shared_workspace(B, H, k_pages.shape[1],
+                                  0 if prefix_table is None else prefix_table.shape[0] * page,
+                                  block_table.shape[1] * page, 0 if marks is None else marks.max_pos,
+                                  q.device)
+    prm = make_params(alpha, beta, mu, s, eps, True, ssmax, prior)
+    bam_attn_decode_shared_paged(q, k_pages, v_pages, block_table, cache_lens, prefix_table, prefix_len,
+                                 q_pos, marks, decay, o, lse, prm, ws, stream)
+    return o, lse
+
+
+def kv_evict_paged(k_pages, v_pages, block_table, cache_lens, marks, budget, sink=4, recent=None,
+                   out_table=None, new_lens=None, ws=None, stream=None):
+    """Evict the keys of the least weight from caches of more than `budget` keys;
+    returns the new lengths (written to new_lens, which may be cache_lens, if
+    given).  recent: keys at the end that stay (default: a quarter of the
+    budget).  Without ws, sequences that could not be evicted go unreported."""
+    import torch
+    if recent is None:
+        recent = min(budget // 4, budget - sink)
+    with _on(stream):
+        if new_lens is None:
+            new_lens = torch.empty_like(cache_lens)
+        if ws is None:
+            ws = evict_workspace(cache_lens.shape[0], k_pages.shape[1],
+                                 block_table.shape[1] * k_pages.shape[2], budget, k_pages.device)
+    bam_kv_evict_paged(k_pages, v_pages, block_table, cache_lens, marks, out_table, new_lens, budget,
+                       sink, recent, ws, stream)
     return new_lens

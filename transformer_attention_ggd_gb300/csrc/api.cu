@@ -6,11 +6,14 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include <cudaTypedefs.h>
 
 #include "../../include/bam_attn.h"
 #include "bam_common.cuh"
+#include "norm_common.cuh"
+#include "shared_common.cuh"
 #include "tree_common.cuh"
 
 static_assert(BAM_PRIOR_THETA == bam::kPriorTheta, "prior codes of the ABI and the kernels");
@@ -206,6 +209,142 @@ bam_status check_cache(int B, int H, int Hkv, int N, int page, int max_blocks, i
   return BAM_OK;
 }
 
+// False when the rotation is not a valid one (null: none).
+bool fill_rope(const bam_rope* rope, RopeArgs* a) {
+  a->dims = a->interleaved = 0;
+  if (!rope || rope->dims == 0) return true;
+  if (rope->dims < 0 || rope->dims > kHeadDim || rope->dims % 16 != 0 ||
+      (rope->interleaved != 0 && rope->interleaved != 1) || !(rope->base >= 1.0) ||
+      !std::isfinite(rope->base))
+    return false;  // (below 1, turns per position exceed what a double's fraction holds)
+  a->dims = rope->dims;
+  a->interleaved = rope->interleaved;
+  // base^(-2 f / dims) by repeated products: their 2^-48 is 2^-23 turns at
+  // position 2^28.
+  const double ratio = std::pow(rope->base, -2.0 / rope->dims);
+  double per = 1.0 / 6.283185307179586477;
+  for (int f = 0; f < rope->dims / 2; ++f, per *= ratio) {
+    // (per is below 1: base is at least 1)
+    a->freq[f] = static_cast<uint64_t>(per * 18446744073709551616.0);
+  }
+  return true;
+}
+
+// The smallest eps of a norm: below it, squares that fp32 loses would count.
+constexpr float kNormEpsMin = 1e-30f;
+
+bool norm_ok(const bam_qk_norm* n) {
+  return n && n->q_weight && n->k_weight && aligned(n->q_weight, 16) && aligned(n->k_weight, 16) &&
+         n->eps >= kNormEpsMin && std::isfinite(n->eps) && (n->per_head == 0 || n->per_head == 1);
+}
+
+// Three element strides (batch, head, token) of a tensor of rows of 64; an output's
+// rows must not overlap: sorted by stride, each spans what lies below it.
+bool strides_ok(const int64_t* st, const int64_t* dims, bool output) {
+  for (int x = 0; x < 3; ++x)
+    if (st[x] < 0 || st[x] % 8 != 0) return false;
+  if (!output) return true;
+  int order[3] = {0, 1, 2};
+  for (int x = 0; x < 2; ++x)
+    for (int y = 0; y < 2; ++y)
+      if (st[order[y]] > st[order[y + 1]]) std::swap(order[y], order[y + 1]);
+  int64_t span = kHeadDim;
+  for (int x : order) {
+    if (dims[x] == 1) continue;
+    if (st[x] < span) return false;
+    span = st[x] * (dims[x] - 1) + span;
+  }
+  return true;
+}
+
+// The sides of a norm: x, g (backward), y from `ptrs` (queries', keys'), strides from
+// `strides` in the same order (null: dense).
+bam_status fill_norm(NormArgs* a, const void* const (*ptrs)[2], int tensors, const int64_t* strides,
+                     const int* positions, int B, int H, int Hkv, int T, int D,
+                     const bam_qk_norm* norm, const bam_rope* rope) {
+  if (B < 1 || H < 1 || Hkv < 1 || T < 1 || D < 1) return BAM_ERR_INVALID_ARG;
+  if (D != kHeadDim) return BAM_ERR_UNSUPPORTED;
+  if (H > 65535 || Hkv > 65535 || static_cast<int64_t>(B) * T > 0x7FFFFFFF) return BAM_ERR_UNSUPPORTED;
+  if (!norm_ok(norm) || !fill_rope(rope, &a->rope) || !aligned(positions, 4)) return BAM_ERR_INVALID_ARG;
+  for (int x = 0; x < tensors; ++x) {
+    for (int k = 0; k < 2; ++k) {
+      if (!ptrs[x][k] || !aligned(ptrs[x][k], 16)) return BAM_ERR_INVALID_ARG;
+      NormSide& s = a->side[k];
+      s.heads = k ? Hkv : H;
+      int64_t* st = x == 0 ? s.xs : x == tensors - 1 ? s.ys : s.gs;
+      const int64_t dims[3] = {B, s.heads, T};
+      const int64_t dense[3] = {static_cast<int64_t>(s.heads) * T * kHeadDim,
+                                static_cast<int64_t>(T) * kHeadDim, kHeadDim};
+      std::memcpy(st, strides ? strides + 3 * (2 * x + k) : dense, sizeof(dense));
+      if (!strides_ok(st, dims, x == tensors - 1)) return BAM_ERR_INVALID_ARG;
+    }
+  }
+  for (int k = 0; k < 2; ++k) {
+    NormSide& s = a->side[k];
+    s.x = static_cast<const uint16_t*>(ptrs[0][k]);
+    s.g = static_cast<const uint16_t*>(ptrs[1][k]);
+    s.y = static_cast<uint16_t*>(const_cast<void*>(ptrs[tensors - 1][k]));
+    s.w = k ? norm->k_weight : norm->q_weight;
+  }
+  a->positions = positions;
+  a->tokens = static_cast<unsigned>(static_cast<int64_t>(B) * T);
+  a->T = T;
+  a->eps = norm->eps;
+  a->per_head = norm->per_head;
+  return BAM_OK;
+}
+
+// Workspace of the norms' backward: sums of every CTA it may have.
+size_t norm_ws(int H, int Hkv) {
+  const int64_t all = static_cast<int64_t>(H) + Hkv, parts = (all + 3) / 4;
+  const int64_t ctas = parts > kNormMaxCtas ? parts : kNormMaxCtas;
+  const int64_t rows = all < kNormMaxHeads ? (all + 3) / 4 * 4 : kNormMaxHeads;
+  return align256(static_cast<size_t>(ctas * rows) * kHeadDim * 4);
+}
+
+struct SharedWs {
+  size_t ml, part, z, total;
+};
+SharedWs shared_ws(const SharedArgs& a, bool marked) {
+  SharedWs w;
+  const size_t rows = static_cast<size_t>(a.c.B) * a.H;
+  w.ml = kStatusBytes;
+  w.part = w.ml + align256(rows * a.slots * 8);
+  w.z = w.part + align256(rows * a.slots * kHeadDim * 4);
+  w.total = w.z + (marked ? align256(rows * a.zstride * 4) : 0);
+  return w;
+}
+
+// Sizes of a decode over a shared prefix of up to Pmax keys and Tmax own ones.
+bam_status check_shared(int64_t B, int64_t H, int64_t Hkv, int64_t Pmax, int64_t Tmax, int64_t max_pos,
+                        int D, SharedArgs* a) {
+  if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || Pmax < 0 || Tmax < 1 || max_pos < 0 || D < 1)
+    return BAM_ERR_INVALID_ARG;
+  if (D != kHeadDim) return BAM_ERR_UNSUPPORTED;
+  if (Pmax + Tmax > (1 << 28) || max_pos > (1 << 28) || B > 65535 || H > 65535 || B * H > (1 << 24))
+    return BAM_ERR_UNSUPPORTED;
+  a->c.B = static_cast<int>(B);
+  a->c.Hkv = static_cast<int>(Hkv);
+  a->H = static_cast<int>(H);
+  a->group = static_cast<int>(H / Hkv);
+  a->max_pos = static_cast<int>(max_pos);
+  a->zstride = (Tmax + 63) / 64 * 64;
+  shared_split(a, Pmax, Tmax);
+  return BAM_OK;
+}
+
+struct EvictWs {
+  size_t count, list, total;
+};
+EvictWs evict_ws(int B, int Hkv, int budget) {
+  EvictWs w;
+  const size_t rows = static_cast<size_t>(B) * Hkv;
+  w.count = kStatusBytes;
+  w.list = w.count + align256(rows * 8);
+  w.total = w.list + align256(rows * budget * 4);
+  return w;
+}
+
 inline bam_status cuda_status(cudaError_t e) { return e == cudaSuccess ? BAM_OK : BAM_ERR_CUDA; }
 
 }  // namespace
@@ -277,6 +416,68 @@ bam_status decode_impl(const void* q, const void* kc, const void* vc, const int*
   e = launch_kernel(BAM_KERNEL_DECODE_COMBINE, stream,
                     [&] { return launch_decode_combine(da, stream); });
   return cuda_status(e);
+}
+
+bool marks_ok(const bam_marks* m) {
+  return m && m->key_pos && m->key_weight && aligned(m->key_pos, 16) && aligned(m->key_weight, 16) &&
+         m->max_pos >= 1 && m->max_pos <= kMaxPosition;
+}
+
+// bam_kv_append_paged, and with `extended` bam_kv_append_norm_paged.
+bam_status append_impl(const void* k, const void* v, const void* q, void* q_out,
+                       const int64_t* strides, void* k_pages, void* v_pages, const int* block_table,
+                       const int* cache_lens, const int* new_lens, const int* parents, int B, int H,
+                       int Hkv, int N, int page, int max_blocks, int num_pages, int D,
+                       const bam_qk_norm* norm, const bam_rope* rope, const int* first_pos,
+                       const bam_marks* marks, bool extended, void* ws, size_t ws_bytes,
+                       cudaStream_t stream) {
+  bam_status s = check_cache(B, H, Hkv, N, page, max_blocks, num_pages, D, block_table, cache_lens,
+                             new_lens, parents);
+  if (s != BAM_OK) return s;
+  if (!k || !v || !k_pages || !v_pages || !q != !q_out) return BAM_ERR_INVALID_ARG;
+  for (const void* x : {k, v, q, static_cast<const void*>(q_out),
+                        static_cast<const void*>(k_pages), static_cast<const void*>(v_pages)})
+    if (!aligned(x, 16)) return BAM_ERR_INVALID_ARG;
+  if (parents && N > kTreeMax) return BAM_ERR_UNSUPPORTED;
+  AppendArgs a = {};
+  if (!fill_rope(rope, &a.rope)) return BAM_ERR_INVALID_ARG;
+  for (int x = 0; x < 9; ++x) {
+    const int h = x < 6 ? Hkv : H;
+    const int64_t dense[3] = {static_cast<int64_t>(h) * N * kHeadDim,
+                              static_cast<int64_t>(N) * kHeadDim, kHeadDim};
+    const int64_t v64 = strides ? strides[x] : dense[x % 3];
+    if (x >= 6 && !q) break;
+    if (v64 < 0 || v64 % 8 != 0) return BAM_ERR_INVALID_ARG;
+    (x < 3 ? a.ks : x < 6 ? a.vs : a.qs)[x % 3] = v64;
+  }
+  if (norm && !norm_ok(norm)) return BAM_ERR_INVALID_ARG;
+  if (marks && !marks_ok(marks)) return BAM_ERR_INVALID_ARG;
+  if (!aligned(first_pos, 4)) return BAM_ERR_INVALID_ARG;
+  if ((s = check_ws(ws, ws_bytes, BAM_CACHE_WORKSPACE_BYTES)) != BAM_OK) return s;
+  if (norm) {
+    a.q_weight = norm->q_weight;
+    a.k_weight = norm->k_weight;
+    a.norm_eps = norm->eps;
+    a.per_head = norm->per_head;
+  }
+  if (marks) {
+    a.key_pos = marks->key_pos;
+    a.key_weight = marks->key_weight;
+    a.max_pos = marks->max_pos;
+  }
+  a.first_pos = first_pos;
+  a.extended = extended;
+  a.c = CacheArgs{block_table, cache_lens, new_lens, parents, static_cast<DevStatus*>(ws),
+                  B, Hkv, N, page, max_blocks, num_pages};
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_pages = static_cast<uint16_t*>(k_pages);
+  a.v_pages = static_cast<uint16_t*>(v_pages);
+  a.H = q ? H : 0;
+  return cuda_status(
+      launch_kernel(BAM_KERNEL_KV_APPEND, stream, [&] { return launch_append(a, stream); }));
 }
 
 }  // namespace
@@ -453,52 +654,187 @@ bam_status bam_kv_append_paged(const void* k, const void* v, const void* q, void
                                int N, int page, int max_blocks, int num_pages, int D,
                                const bam_rope* rope, void* ws, size_t ws_bytes,
                                cudaStream_t stream) {
-  bam_status s = check_cache(B, H, Hkv, N, page, max_blocks, num_pages, D, block_table, cache_lens,
-                             new_lens, parents);
+  return append_impl(k, v, q, q_out, strides, k_pages, v_pages, block_table, cache_lens, new_lens,
+                     parents, B, H, Hkv, N, page, max_blocks, num_pages, D, nullptr, rope, nullptr,
+                     nullptr, false, ws, ws_bytes, stream);
+}
+
+bam_status bam_kv_append_norm_paged(const void* k, const void* v, const void* q, void* q_out,
+                                    const int64_t* strides, void* k_pages, void* v_pages,
+                                    const int* block_table, const int* cache_lens,
+                                    const int* new_lens, const int* parents, int B, int H, int Hkv,
+                                    int N, int page, int max_blocks, int num_pages, int D,
+                                    const bam_qk_norm* norm, const bam_rope* rope,
+                                    const int* first_pos, const bam_marks* marks, void* ws,
+                                    size_t ws_bytes, cudaStream_t stream) {
+  return append_impl(k, v, q, q_out, strides, k_pages, v_pages, block_table, cache_lens, new_lens,
+                     parents, B, H, Hkv, N, page, max_blocks, num_pages, D, norm, rope, first_pos,
+                     marks, true, ws, ws_bytes, stream);
+}
+
+bam_status bam_qk_norm_fwd(const void* q, const void* k, void* q_out, void* k_out,
+                           const int64_t* strides, const int* positions, int B, int H, int Hkv,
+                           int T, int D, const bam_qk_norm* norm, const bam_rope* rope,
+                           cudaStream_t stream) {
+  NormArgs a = {};
+  const void* ptrs[2][2] = {{q, k}, {q_out, k_out}};
+  const bam_status s = fill_norm(&a, ptrs, 2, strides, positions, B, H, Hkv, T, D, norm, rope);
   if (s != BAM_OK) return s;
-  if (!k || !v || !k_pages || !v_pages || !q != !q_out) return BAM_ERR_INVALID_ARG;
-  for (const void* x : {k, v, q, static_cast<const void*>(q_out),
-                        static_cast<const void*>(k_pages), static_cast<const void*>(v_pages)})
-    if (!aligned(x, 16)) return BAM_ERR_INVALID_ARG;
-  if (parents && N > kTreeMax) return BAM_ERR_UNSUPPORTED;
-  AppendArgs a = {};
-  if (rope && rope->dims != 0) {
-    if (rope->dims < 0 || rope->dims > kHeadDim || rope->dims % 16 != 0 ||
-        (rope->interleaved != 0 && rope->interleaved != 1) || !(rope->base >= 1.0) ||
-        !std::isfinite(rope->base))
-      return BAM_ERR_INVALID_ARG;  // (below 1, turns per position exceed what a double's fraction holds)
-    a.dims = rope->dims;
-    a.interleaved = rope->interleaved;
-    // base^(-2 f / dims) by repeated products: their 2^-48 is 2^-23 turns at
-    // position 2^28.
-    const double ratio = std::pow(rope->base, -2.0 / rope->dims);
-    double per = 1.0 / 6.283185307179586477;
-    for (int f = 0; f < rope->dims / 2; ++f, per *= ratio) {
-      // (per is below 1: base is at least 1)
-      a.freq[f] = static_cast<uint64_t>(per * 18446744073709551616.0);
-    }
-  }
-  for (int x = 0; x < 9; ++x) {
-    const int h = x < 6 ? Hkv : H;
-    const int64_t dense[3] = {static_cast<int64_t>(h) * N * kHeadDim,
-                              static_cast<int64_t>(N) * kHeadDim, kHeadDim};
-    const int64_t v64 = strides ? strides[x] : dense[x % 3];
-    if (x >= 6 && !q) break;
-    if (v64 < 0 || v64 % 8 != 0) return BAM_ERR_INVALID_ARG;
-    (x < 3 ? a.ks : x < 6 ? a.vs : a.qs)[x % 3] = v64;
-  }
-  if ((s = check_ws(ws, ws_bytes, BAM_CACHE_WORKSPACE_BYTES)) != BAM_OK) return s;
-  a.c = CacheArgs{block_table, cache_lens, new_lens, parents, static_cast<DevStatus*>(ws),
-                  B, Hkv, N, page, max_blocks, num_pages};
-  a.k = static_cast<const uint16_t*>(k);
-  a.v = static_cast<const uint16_t*>(v);
+  return cuda_status(
+      launch_kernel(BAM_KERNEL_QK_NORM, stream, [&] { return launch_norm_fwd(a, stream); }));
+}
+
+size_t bam_qk_norm_workspace_size(int B, int H, int Hkv, int T, int D) {
+  if (B < 1 || H < 1 || Hkv < 1 || T < 1 || D != kHeadDim || H > 65535 || Hkv > 65535 ||
+      static_cast<int64_t>(B) * T > 0x7FFFFFFF)
+    return 0;
+  return norm_ws(H, Hkv);
+}
+
+bam_status bam_qk_norm_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                           void* dq, void* dk, const int64_t* strides, float* dq_weight,
+                           float* dk_weight, const int* positions, int B, int H, int Hkv, int T,
+                           int D, const bam_qk_norm* norm, const bam_rope* rope, void* ws,
+                           size_t ws_bytes, cudaStream_t stream) {
+  NormArgs a = {};
+  const void* ptrs[3][2] = {{q, k}, {dq_out, dk_out}, {dq, dk}};
+  bam_status s = fill_norm(&a, ptrs, 3, strides, positions, B, H, Hkv, T, D, norm, rope);
+  if (s != BAM_OK) return s;
+  if (!dq_weight || !dk_weight || !aligned(dq_weight, 4) || !aligned(dk_weight, 4))
+    return BAM_ERR_INVALID_ARG;
+  if ((s = check_ws(ws, ws_bytes, norm_ws(H, Hkv))) != BAM_OK) return s;
+  a.side[0].dw = dq_weight;
+  a.side[1].dw = dk_weight;
+  a.part = static_cast<float*>(ws);
+  norm_bwd_config(&a, sm_count());
+  cudaError_t e =
+      launch_kernel(BAM_KERNEL_QK_NORM_BWD, stream, [&] { return launch_norm_bwd(a, stream); });
+  if (e != cudaSuccess) return BAM_ERR_CUDA;
+  return cuda_status(launch_kernel(BAM_KERNEL_QK_NORM_FINISH, stream,
+                                   [&] { return launch_norm_bwd_finish(a, stream); }));
+}
+
+size_t bam_attn_shared_workspace_size(int B, int H, int Hkv, int Pmax, int Tmax, int max_pos, int D) {
+  SharedArgs a = {};
+  if (check_shared(B, H, Hkv, Pmax, Tmax, max_pos, D, &a) != BAM_OK) return 0;
+  return shared_ws(a, max_pos > 0).total;
+}
+
+bam_status bam_attn_decode_shared_paged(const void* q, const void* k_pages, const void* v_pages,
+                                        const int* block_table, const int* cache_lens,
+                                        const int* prefix_table, const int* prefix_len,
+                                        const int* q_pos, const bam_marks* marks, float decay,
+                                        void* o, int o_fp32, float* lse, int B, int H, int Hkv,
+                                        int page, int max_blocks, int prefix_blocks, int num_pages,
+                                        int D, const bam_params* p, void* ws, size_t ws_bytes,
+                                        cudaStream_t stream) {
+  bam_status s = check_cache(B, H, Hkv, 1, page, max_blocks, num_pages, D, block_table, cache_lens,
+                             nullptr, nullptr);
+  if (s != BAM_OK) return s;
+  if ((s = check_params(p)) != BAM_OK) return s;
+  if (!q || !k_pages || !v_pages || !o) return BAM_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16) ||
+      !aligned(lse, 4) || !aligned(prefix_table, 4) || !aligned(prefix_len, 4) || !aligned(q_pos, 4))
+    return BAM_ERR_INVALID_ARG;
+  if (!prefix_table != !prefix_len || !prefix_table != (prefix_blocks == 0) || prefix_blocks < 0)
+    return BAM_ERR_INVALID_ARG;
+  if (!marks != !q_pos || (marks && !marks_ok(marks)) || !(decay >= 0.0f && decay <= 1.0f))
+    return BAM_ERR_INVALID_ARG;
+  SharedArgs a = {};
+  if ((s = check_shared(B, H, Hkv, static_cast<int64_t>(prefix_blocks) * page,
+                        static_cast<int64_t>(max_blocks) * page, marks ? marks->max_pos : 0, D, &a)) !=
+      BAM_OK)
+    return s;
+  const SharedWs w = shared_ws(a, marks != nullptr);
+  if ((s = check_ws(ws, ws_bytes, w.total)) != BAM_OK) return s;
+  CUtensorMap tk, tv;
+  if (!encode_rows(&tk, k_pages, num_pages * Hkv, page, 64) ||
+      !encode_rows(&tv, v_pages, num_pages * Hkv, page, 64))
+    return BAM_ERR_CUDA;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  a.c = CacheArgs{block_table, cache_lens, nullptr, nullptr, static_cast<DevStatus*>(ws),
+                  B, Hkv, 1, page, max_blocks, num_pages};
   a.q = static_cast<const uint16_t*>(q);
-  a.q_out = static_cast<uint16_t*>(q_out);
+  a.prefix_table = prefix_table;
+  a.prefix_len = prefix_len;
+  a.prefix_blocks = prefix_blocks;
+  a.q_pos = q_pos;
+  if (marks) {
+    a.key_pos = marks->key_pos;
+    a.key_weight = marks->key_weight;
+    a.z = reinterpret_cast<float*>(wsb + w.z);
+  }
+  a.decay = decay;
+  a.alpha = p->alpha;
+  a.beta = p->beta;
+  a.mu = p->mu;
+  a.s = p->s;
+  a.eps = p->eps;
+  a.prior = p->prior;
+  a.ssmax = p->ssmax;
+  a.o = o;
+  a.o_fp32 = o_fp32 ? 1 : 0;
+  a.lse = lse;
+  a.ml = reinterpret_cast<float2*>(wsb + w.ml);
+  a.part = reinterpret_cast<float*>(wsb + w.part);
+  cudaError_t e =
+      launch_kernel(BAM_KERNEL_SHARED_PREP, stream, [&] { return launch_shared_prep(a, stream); });
+  if (e != cudaSuccess) return BAM_ERR_CUDA;
+  e = launch_kernel(BAM_KERNEL_SHARED, stream, [&] { return launch_shared(tk, tv, a, stream); });
+  if (e != cudaSuccess) return BAM_ERR_CUDA;
+  e = launch_kernel(BAM_KERNEL_SHARED_JOIN, stream, [&] { return launch_shared_join(a, stream); });
+  if (e != cudaSuccess || !marks) return cuda_status(e);
+  return cuda_status(
+      launch_kernel(BAM_KERNEL_SHARED_WEIGH, stream, [&] { return launch_shared_weigh(a, stream); }));
+}
+
+size_t bam_kv_evict_workspace_size(int B, int Hkv, int Tmax, int budget) {
+  if (B < 1 || Hkv < 1 || Tmax < 1 || budget < 1 || B > 65535 || Hkv > 65535 || Tmax > (1 << 28))
+    return 0;
+  return evict_ws(B, Hkv, budget < Tmax ? budget : Tmax).total;
+}
+
+bam_status bam_kv_evict_paged(void* k_pages, void* v_pages, const int* block_table,
+                              const int* cache_lens, const bam_marks* marks, const int* out_table,
+                              int* new_lens, int B, int Hkv, int page, int max_blocks,
+                              int out_blocks, int num_pages, int D, int budget, int sink,
+                              int recent, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  bam_status s = check_cache(B, Hkv, Hkv, 1, page, max_blocks, num_pages, D, block_table, cache_lens,
+                             nullptr, nullptr);
+  if (s != BAM_OK) return s;
+  if (!k_pages || !v_pages || !new_lens || !aligned(k_pages, 16) || !aligned(v_pages, 16) ||
+      !aligned(new_lens, 4) || !aligned(out_table, 4) || !marks_ok(marks))
+    return BAM_ERR_INVALID_ARG;
+  if (budget < 1 || sink < 0 || recent < 0 || static_cast<int64_t>(sink) + recent > budget)
+    return BAM_ERR_INVALID_ARG;
+  const int Tmax = page * max_blocks;
+  if (budget > Tmax) budget = Tmax;  // no sequence is longer: nothing leaves
+  if (!out_table != (out_blocks == 0) || out_blocks < 0 ||
+      (out_table && static_cast<int64_t>(out_blocks) * page < budget))
+    return BAM_ERR_INVALID_ARG;
+  const EvictWs w = evict_ws(B, Hkv, budget);
+  if ((s = check_ws(ws, ws_bytes, w.total)) != BAM_OK) return s;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  EvictArgs a = {};
+  a.c = CacheArgs{block_table, cache_lens, nullptr, nullptr, static_cast<DevStatus*>(ws),
+                  B, Hkv, 1, page, max_blocks, num_pages};
   a.k_pages = static_cast<uint16_t*>(k_pages);
   a.v_pages = static_cast<uint16_t*>(v_pages);
-  a.H = q ? H : 0;
+  a.key_pos = marks->key_pos;
+  a.key_weight = marks->key_weight;
+  a.out_table = out_table;
+  a.out_blocks = out_blocks;
+  a.new_lens = new_lens;
+  a.budget = budget;
+  a.sink = sink;
+  a.recent = recent;
+  a.count = reinterpret_cast<int2*>(wsb + w.count);
+  a.list = reinterpret_cast<int*>(wsb + w.list);
+  cudaError_t e =
+      launch_kernel(BAM_KERNEL_EVICT_SELECT, stream, [&] { return launch_evict_select(a, stream); });
+  if (e != cudaSuccess) return BAM_ERR_CUDA;
   return cuda_status(
-      launch_kernel(BAM_KERNEL_KV_APPEND, stream, [&] { return launch_append(a, stream); }));
+      launch_kernel(BAM_KERNEL_EVICT_MOVE, stream, [&] { return launch_evict_move(a, stream); }));
 }
 
 size_t bam_attn_tree_workspace_size(int B, int H, int Hkv, int N, int Tmax, int D) {
@@ -592,8 +928,69 @@ bam_status bam_kv_keep_paged(void* k_pages, void* v_pages, const int* block_tabl
       launch_kernel(BAM_KERNEL_KV_KEEP, stream, [&] { return launch_keep(a, stream); }));
 }
 
+static bam_status bounded_call(int op, const void* words) {
+  // Words of each operator, the place of its strides' flag (-1: none) and their number.
+  constexpr int kWords[] = {26, 14, 20, 25, 20}, kFlag[] = {4, 4, 6, -1, -1}, kSteps[] = {9, 12, 18, 0, 0};
+  const int x = op - BAM_CALL_KV_APPEND_NORM, flag = kFlag[x];
+  int64_t w[26], steps[18];
+  std::memcpy(w, words, kWords[x] * sizeof(int64_t));
+  const int64_t* strides = nullptr;
+  if (flag >= 0) {
+    if (w[flag] != 0 && w[flag] != 1) return BAM_ERR_INVALID_ARG;
+    if (w[flag]) {
+      std::memcpy(steps, static_cast<const char*>(words) + kWords[x] * sizeof(int64_t),
+                  kSteps[x] * sizeof(int64_t));
+      strides = steps;
+    }
+  }
+  bool fits = true;
+  auto p = [&](int i) { return reinterpret_cast<void*>(static_cast<uintptr_t>(w[i])); };
+  auto ip = [&](int i) { return static_cast<int*>(p(i)); };
+  auto fp = [&](int i) { return static_cast<float*>(p(i)); };
+  auto n = [&](int i) {
+    fits &= w[i] == static_cast<int>(w[i]);
+    return static_cast<int>(w[i]);
+  };
+  auto norm = [&](int i) { return static_cast<const bam_qk_norm*>(p(i)); };
+  auto rope = [&](int i) { return static_cast<const bam_rope*>(p(i)); };
+  auto marks = [&](int i) { return static_cast<const bam_marks*>(p(i)); };
+  auto st = [&](int i) { return static_cast<cudaStream_t>(p(i)); };
+  auto sz = [&](int i) { return static_cast<size_t>(w[i]); };
+  constexpr int kFirst[] = {11, 6, 10, 13, 7}, kInts[] = {8, 5, 5, 8, 10};
+  int i[10];
+  for (int y = 0; y < kInts[x]; ++y) i[y] = n(kFirst[x] + y);
+  const int o_fp32 = op == BAM_CALL_DECODE_SHARED ? n(11) : 0;
+  float decay = 0.0f;
+  if (op == BAM_CALL_DECODE_SHARED) {  // its bits
+    const int bits = n(9);
+    std::memcpy(&decay, &bits, sizeof(decay));
+  }
+  if (!fits) return BAM_ERR_INVALID_ARG;
+  switch (op) {
+    case BAM_CALL_KV_APPEND_NORM:
+      return bam_kv_append_norm_paged(p(0), p(1), p(2), p(3), strides, p(5), p(6), ip(7), ip(8), ip(9),
+                                      ip(10), i[0], i[1], i[2], i[3], i[4], i[5], i[6], i[7], norm(19),
+                                      rope(20), ip(21), marks(22), p(23), sz(24), st(25));
+    case BAM_CALL_QK_NORM_FWD:
+      return bam_qk_norm_fwd(p(0), p(1), p(2), p(3), strides, ip(5), i[0], i[1], i[2], i[3], i[4],
+                             norm(11), rope(12), st(13));
+    case BAM_CALL_QK_NORM_BWD:
+      return bam_qk_norm_bwd(p(0), p(1), p(2), p(3), p(4), p(5), strides, fp(7), fp(8), ip(9), i[0],
+                             i[1], i[2], i[3], i[4], norm(15), rope(16), p(17), sz(18), st(19));
+    case BAM_CALL_DECODE_SHARED:
+      return bam_attn_decode_shared_paged(p(0), p(1), p(2), ip(3), ip(4), ip(5), ip(6), ip(7), marks(8),
+                                          decay, p(10), o_fp32, fp(12), i[0], i[1], i[2], i[3], i[4],
+                                          i[5], i[6], i[7], static_cast<const bam_params*>(p(21)), p(22),
+                                          sz(23), st(24));
+    default:
+      return bam_kv_evict_paged(p(0), p(1), ip(2), ip(3), marks(4), ip(5), ip(6), i[0], i[1], i[2], i[3],
+                                i[4], i[5], i[6], i[7], i[8], i[9], p(17), sz(18), st(19));
+  }
+}
+
 bam_status bam_paged_call(int op, const void* words) {
   constexpr int kWords[] = {23, 22, 18}, kStrides = 4;  // place of the append's strides
+  if (words && op > BAM_CALL_KV_KEEP && op <= BAM_CALL_KV_EVICT) return bounded_call(op, words);
   if (!words || op < BAM_CALL_KV_APPEND || op > BAM_CALL_KV_KEEP) return BAM_ERR_INVALID_ARG;
   int64_t w[23], strides[9];
   std::memcpy(w, words, kWords[op] * sizeof(int64_t));

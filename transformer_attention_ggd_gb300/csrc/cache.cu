@@ -21,27 +21,6 @@ constexpr int kAppendPass = kAppendThreads / 4;  // rows in flight per load: fou
 // of up to 8192 tokens, 12 heads, 8 sequences (453 MB: 68 us).
 constexpr int kAppendResident = 2;
 
-// One rotated pair: (a, b) -> (a cos - b sin, b cos + a sin), in fp32, rounded
-// once to bf16 by the caller.
-__device__ __forceinline__ void turn(float& a, float& b, float co, float si) {
-  const float x = a * co - b * si;
-  b = b * co + a * si;
-  a = x;
-}
-
-__device__ __forceinline__ void unpack8(const uint4& w, float* f) {
-  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(x[i] << 16);
-    f[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
-}
-
 // A unit is up to 16 tokens of one sequence and a run of the heads of its
 // queries, keys or values, 256 rows at most: four lanes hold a row, 32 bytes
 // each, and a thread has up to four rows, of one token.  For pairs
@@ -68,6 +47,16 @@ __device__ __forceinline__ bool append_lengths(const CacheArgs& c, int b, int& l
   len = min(max(raw, 0), cap);
   n = min(max(rawn, 0), c.N);
   return raw == len && rawn == n;
+}
+
+// Position of the first appended token of sequence b whose committed length is
+// len; false if it is out of range.
+__device__ __forceinline__ bool append_first(const AppendArgs& a, int b, int len, int& first) {
+  first = len;
+  if (!a.first_pos) return true;
+  const int raw = __ldg(a.first_pos + b);
+  first = min(max(raw, 0), kMaxPosition);
+  return raw == first;
 }
 
 // The parent of this thread's node of sequence b.
@@ -98,26 +87,61 @@ __device__ __forceinline__ void append_load(const AppendArgs& a, const AppendUni
   }
 }
 
+// Norm and rotation of a unit's rows in registers, rounded once; by whole
+// warps (rows that were not loaded are turned for nothing).
+__device__ __forceinline__ void append_turn(const AppendArgs& a, const AppendUnit& x,
+                                            const AppendLane& ln, bool rotated, const float4* cs,
+                                            uint4 (&w)[kAppendRows][2]) {
+  const float* weight = x.kind == 0 ? a.q_weight : a.k_weight;
+  float4 r[4];  // eight (cosine, sine) pairs
+  if (rotated) {
+#pragma unroll
+    for (int y = 0; y < 4; ++y) r[y] = cs[y];
+  }
+#pragma unroll
+  for (int y = 0; y < kAppendRows; ++y) {
+    if (y * ln.step >= x.heads) break;
+    float f[16];
+    unpack8(w[y][0], f);
+    unpack8(w[y][1], f + 8);
+    if (weight) {
+      float scale;
+      const float inv = row_rms_inv(f, a.norm_eps, &scale);
+      const int h = min(x.h0 + ln.h + y * ln.step, (x.kind == 0 ? a.H : a.c.Hkv) - 1);
+      const float* p = weight + (a.per_head ? h * kHeadDim : 0);
+#pragma unroll
+      for (int z = 0; z < 16; ++z) f[z] = f[z] * inv * __ldg(p + 8 * (z < 8 ? ln.c0 : ln.c1) + (z & 7));
+    }
+    if (rotated) turn_row(f, f + 8, r, a.rope.interleaved, 1.0f);
+    w[y][0] = pack8(f);
+    w[y][1] = pack8(f + 8);
+  }
+}
+
 // A CTA takes every gridDim-th token tile (ragged prompts then load all SMs
 // alike), its heads one unit after the other, so that the tile's slots and
 // angles serve them all; the next unit's rows are on their way while this
 // one's are turned and stored.  A call of so few units that each has a CTA
 // loads all N tokens' rows before it knows which count: the lengths, slots,
 // depths and angles then take no time of their own.
-template <bool kRun>
+//
+// kNorm: queries and keys are normalised on the way (4 lanes sum a row's
+// squares), positions may start anywhere, and the keys' positions and weights
+// are written beside them.
+template <bool kRun, bool kNorm>
 __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_kernel(const AppendArgs a) {
   __shared__ float4 cs[kAppendTokens][kHeadDim / 4];  // two (cosine, sine) pairs each
   __shared__ int64_t slot_row[kAppendTokens];  // row of head 0 in the pages, -1: not written
   __shared__ int depth[kTreeMax], jump[kTreeMax];
   const CacheArgs& c = a.c;
-  const int u4 = threadIdx.x & 3, nh = a.dims / 16, half = a.dims / 2;
+  const int u4 = threadIdx.x & 3, nh = a.rope.dims / 16, half = a.rope.dims / 2;
   const bool rotated = u4 < nh;
   AppendLane ln;
   ln.t = (threadIdx.x >> 2) & (a.tokens - 1);  // a.tokens is a power of two
   ln.h = (threadIdx.x >> 2) / a.tokens;
   ln.step = kAppendPass / a.tokens;
-  ln.c0 = a.interleaved || !rotated ? 2 * u4 : u4;
-  ln.c1 = a.interleaved || !rotated ? 2 * u4 + 1 : u4 + nh;
+  ln.c0 = a.rope.interleaved || !rotated ? 2 * u4 : u4;
+  ln.c1 = a.rope.interleaved || !rotated ? 2 * u4 + 1 : u4 + nh;
   const int cap = c.page * c.max_blocks;
   const int split = a.q_parts + 2 * a.kv_parts;
   int64_t bt = kRun ? blockIdx.x : blockIdx.x / split;
@@ -125,17 +149,23 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
   const int64_t tiles = static_cast<int64_t>(c.B) * a.tiles;
   AppendUnit x = append_unit(a, bt, part);
   uint4 w[kAppendRows][2], wn[kAppendRows][2];
+  if (kNorm) {
+#pragma unroll
+    for (int y = 0; y < kAppendRows; ++y) w[y][0] = w[y][1] = wn[y][0] = wn[y][1] = make_uint4(0, 0, 0, 0);
+  }
   int len, n, par = -1, last_b = -1, last_tile = -1;
   if (!kRun) {
     append_load(a, x, c.N, ln, w);
     par = append_parent(c, x.b);
   }
   bool ok = append_lengths(c, x.b, len, n);
+  int first = len;  // position of token 0
+  if (kNorm) ok &= append_first(a, x.b, len, first);
   if (kRun) append_load(a, x, n, ln, w);
   for (;;) {
     // The unit after this one.
     AppendUnit xn = x;
-    int len_n = len, n_n = n;
+    int len_n = len, n_n = n, first_n = first;
     bool more = false;
     if (kRun) {
       if (++part == split) {
@@ -145,7 +175,11 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
       more = bt < tiles;
       if (more) {
         xn = append_unit(a, bt, part);
-        if (xn.b != x.b) ok &= append_lengths(c, xn.b, len_n, n_n);
+        if (xn.b != x.b) {
+          ok &= append_lengths(c, xn.b, len_n, n_n);
+          first_n = len_n;
+          if (kNorm) ok &= append_first(a, xn.b, len_n, first_n);
+        }
         append_load(a, xn, n_n, ln, wn);
       }
     }
@@ -171,19 +205,24 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
       for (int y = threadIdx.x; y < nt * (kHeadDim / 2); y += kAppendThreads) {
         const int t = y / (kHeadDim / 2), f = y % (kHeadDim / 2);
         if (f >= half) continue;
-        const uint64_t pos = static_cast<uint64_t>(len) + (c.parents ? depth[t0 + t] : t0 + t);
-        // The phase wraps modulo 2^64, one turn: an exact reduction.  Its top
-        // 32 bits, signed, are the angle in units of 2^-31 half turns.
-        const int top = static_cast<int>((pos * a.freq[f]) >> 32);
-        float s, co;
-        sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &co);
-        reinterpret_cast<float2*>(cs[t])[f] = make_float2(co, s);
+        const uint64_t pos = static_cast<uint64_t>(kNorm ? first : len) + (c.parents ? depth[t0 + t] : t0 + t);
+        reinterpret_cast<float2*>(cs[t])[f] = rope_angle(pos, a.rope.freq[f]);
       }
       __syncthreads();
       last_b = x.b;
       last_tile = x.tile;
     }
+    if (kNorm && x.kind < 2 && nt > 0) append_turn(a, x, ln, rotated, cs[ln.t] + 4 * u4, w);
     const int64_t row = ln.t < nt ? (x.kind == 0 ? 0 : slot_row[ln.t]) : -1;
+    if (kNorm && a.key_pos && x.kind == 1 && row >= 0 && u4 == 0) {
+      const int pos = first + (c.parents ? depth[t0 + ln.t] : t0 + ln.t);
+      ok &= pos < a.max_pos;
+      for (int h = ln.h; h < x.heads; h += ln.step) {
+        const int64_t at = row + static_cast<int64_t>(x.h0 + h) * c.page;
+        a.key_pos[at] = pos;
+        a.key_weight[at] = 0.0f;
+      }
+    }
     if (row >= 0) {
       uint16_t* dst;
       int64_t hs;  // elements from a head to the next
@@ -196,7 +235,7 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
         dst = (x.kind == 1 ? a.k_pages : a.v_pages) + row * kHeadDim + (x.h0 + ln.h) * hs;
       }
       hs *= ln.step;
-      if (rotated && x.kind < 2) {
+      if (!kNorm && rotated && x.kind < 2) {
         float4 r[4];  // eight (cosine, sine) pairs
 #pragma unroll
         for (int y = 0; y < 4; ++y) r[y] = cs[ln.t][4 * u4 + y];
@@ -206,21 +245,7 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
           float f0[8], f1[8];
           unpack8(w[y][0], f0);
           unpack8(w[y][1], f1);
-          if (a.interleaved) {
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              turn(f0[4 * z], f0[4 * z + 1], r[z].x, r[z].y);
-              turn(f0[4 * z + 2], f0[4 * z + 3], r[z].z, r[z].w);
-              turn(f1[4 * z], f1[4 * z + 1], r[2 + z].x, r[2 + z].y);
-              turn(f1[4 * z + 2], f1[4 * z + 3], r[2 + z].z, r[2 + z].w);
-            }
-          } else {
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              turn(f0[2 * z], f1[2 * z], r[z].x, r[z].y);
-              turn(f0[2 * z + 1], f1[2 * z + 1], r[z].z, r[z].w);
-            }
-          }
+          turn_row(f0, f1, r, a.rope.interleaved, 1.0f);
           w[y][0] = pack8(f0);
           w[y][1] = pack8(f1);
         }
@@ -236,6 +261,7 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
     x = xn;
     len = len_n;
     n = n_n;
+    first = first_n;
 #pragma unroll
     for (int y = 0; y < kAppendRows; ++y) {
       w[y][0] = wn[y][0];
@@ -352,11 +378,11 @@ cudaError_t launch_append(const AppendArgs& args, cudaStream_t st) {
   // single tokens and 11.1 instead of 10.1 for 64 drafts of 48 nodes.
   const int64_t run = static_cast<int64_t>(sm_count()) * kAppendResident;
   if (tiles > run)
-    return launch_k(bam_kv_append_kernel<true>, dim3(static_cast<unsigned>(run)),
-                    dim3(kAppendThreads), 0, st, false, a);
+    return launch_k(a.extended ? bam_kv_append_kernel<true, true> : bam_kv_append_kernel<true, false>,
+                    dim3(static_cast<unsigned>(run)), dim3(kAppendThreads), 0, st, false, a);
   if (units > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  return launch_k(bam_kv_append_kernel<false>, dim3(static_cast<unsigned>(units)),
-                  dim3(kAppendThreads), 0, st, false, a);
+  return launch_k(a.extended ? bam_kv_append_kernel<false, true> : bam_kv_append_kernel<false, false>,
+                  dim3(static_cast<unsigned>(units)), dim3(kAppendThreads), 0, st, false, a);
 }
 
 cudaError_t launch_keep(const KeepArgs& a, cudaStream_t st) {

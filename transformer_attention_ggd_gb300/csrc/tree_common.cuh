@@ -3,11 +3,12 @@
 // reads, and the depths and ancestors of a draft's nodes.
 #pragma once
 
-#include "bam_common.cuh"
+#include "row_ops.cuh"
 
 namespace bam {
 
 constexpr int kTreeMax = 128;  // nodes of a draft with parents
+constexpr int kMaxPosition = 1 << 28;  // positions of keys and queries stay below
 
 // A paged cache and the drafts behind its committed keys.
 struct CacheArgs {
@@ -29,11 +30,18 @@ struct AppendArgs {
   uint16_t* v_pages;
   int64_t ks[3], vs[3], qs[3];  // element strides over batch, head, token
   int H;                        // query heads (0 without q)
-  int dims, interleaved;
   int tokens, heads;            // tokens (a power of two) and heads of a unit of work
   int tiles;                    // token tiles of a sequence
   int q_parts, kv_parts;        // units of a token tile: of its queries, of its keys
-  uint64_t freq[kHeadDim / 2];  // turns per position of pair f, times 2^64
+  RopeArgs rope;
+  // With `extended` alone:
+  const float* q_weight;        // norms (null: none), [64] or [heads, 64]
+  const float* k_weight;
+  const int* first_pos;         // [B] position of each sequence's token 0, or null: lens
+  int* key_pos;                 // [num_pages, Hkv, page] or null
+  float* key_weight;
+  float norm_eps;
+  int per_head, max_pos, extended;
 };
 
 struct KeepArgs {
