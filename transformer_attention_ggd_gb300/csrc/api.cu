@@ -277,6 +277,14 @@ bam_status fill_norm(NormArgs* a, const void* const (*ptrs)[2], int tensors, con
                                 static_cast<int64_t>(T) * kHeadDim, kHeadDim};
       std::memcpy(st, strides ? strides + 3 * (2 * x + k) : dense, sizeof(dense));
       if (!strides_ok(st, dims, x == tensors - 1)) return BAM_ERR_INVALID_ARG;
+      // (a walk goes up to a pass past the last head)
+      unsigned __int128 most = 0;
+      for (int y = 0; y < 3; ++y) {
+        st[y] /= 8;
+        most += static_cast<unsigned __int128>(st[y]) * (dims[y] + (y == 1 ? 2 * kNormPass : 0));
+      }
+      if (most >> 32) a->large = 1;
+      if (most >> 60) return BAM_ERR_INVALID_ARG;
     }
   }
   for (int k = 0; k < 2; ++k) {
@@ -289,6 +297,7 @@ bam_status fill_norm(NormArgs* a, const void* const (*ptrs)[2], int tensors, con
   a->positions = positions;
   a->tokens = static_cast<unsigned>(static_cast<int64_t>(B) * T);
   a->T = T;
+  a->by_T = divisor_of(a->T);
   a->eps = norm->eps;
   a->per_head = norm->per_head;
   return BAM_OK;
@@ -296,9 +305,9 @@ bam_status fill_norm(NormArgs* a, const void* const (*ptrs)[2], int tensors, con
 
 // Workspace of the norms' backward: sums of every CTA it may have.
 size_t norm_ws(int H, int Hkv) {
-  const int64_t all = static_cast<int64_t>(H) + Hkv, parts = (all + 3) / 4;
-  const int64_t ctas = parts > kNormMaxCtas ? parts : kNormMaxCtas;
-  const int64_t rows = all < kNormMaxHeads ? (all + 3) / 4 * 4 : kNormMaxHeads;
+  const int64_t all = (H + kNormPass - 1) / kNormPass + (Hkv + kNormPass - 1) / kNormPass;
+  const int64_t ctas = all > kNormMaxCtas ? all : kNormMaxCtas;  // (each part has one at least)
+  const int64_t rows = kNormPass * (all < kNormMaxPasses ? all : kNormMaxPasses);
   return align256(static_cast<size_t>(ctas * rows) * kHeadDim * 4);
 }
 

@@ -88,33 +88,29 @@ __device__ __forceinline__ void append_load(const AppendArgs& a, const AppendUni
 }
 
 // Norm and rotation of a unit's rows in registers, rounded once; by whole
-// warps (rows that were not loaded are turned for nothing).
+// warps (rows that were not loaded are turned for nothing).  cos, sin: of this lane's token.
+template <int kTurn>
 __device__ __forceinline__ void append_turn(const AppendArgs& a, const AppendUnit& x,
-                                            const AppendLane& ln, bool rotated, const float4* cs,
-                                            uint4 (&w)[kAppendRows][2]) {
+                                            const AppendLane& ln, const RowLane& rl, const float* cos,
+                                            const float* sin, uint4 (&w)[kAppendRows][2]) {
   const float* weight = x.kind == 0 ? a.q_weight : a.k_weight;
-  float4 r[4];  // eight (cosine, sine) pairs
-  if (rotated) {
-#pragma unroll
-    for (int y = 0; y < 4; ++y) r[y] = cs[y];
-  }
+  const int most = (x.kind == 0 ? a.H : a.c.Hkv) - 1;
+  F2x8 wt;
+  if (weight && !a.per_head) load_weight(weight, rl, wt);
 #pragma unroll
   for (int y = 0; y < kAppendRows; ++y) {
     if (y * ln.step >= x.heads) break;
-    float f[16];
-    unpack8(w[y][0], f);
-    unpack8(w[y][1], f + 8);
+    F2x8 f;
+    unpack_row(w[y], f);
     if (weight) {
       float scale;
-      const float inv = row_rms_inv(f, a.norm_eps, &scale);
-      const int h = min(x.h0 + ln.h + y * ln.step, (x.kind == 0 ? a.H : a.c.Hkv) - 1);
-      const float* p = weight + (a.per_head ? h * kHeadDim : 0);
+      const uint64_t inv = f2_both(row_rms_inv(f, a.norm_eps, &scale));
+      if (a.per_head) load_weight(weight + min(x.h0 + ln.h + y * ln.step, most) * kHeadDim, rl, wt);
 #pragma unroll
-      for (int z = 0; z < 16; ++z) f[z] = f[z] * inv * __ldg(p + 8 * (z < 8 ? ln.c0 : ln.c1) + (z & 7));
+      for (int z = 0; z < 8; ++z) f[z] = fmul2(fmul2(f[z], inv), wt[z]);
     }
-    if (rotated) turn_row(f, f + 8, r, a.rope.interleaved, 1.0f);
-    w[y][0] = pack8(f);
-    w[y][1] = pack8(f + 8);
+    turn_values<kTurn>(f, cos, sin, rl);
+    pack_row(f, w[y]);
   }
 }
 
@@ -128,11 +124,14 @@ __device__ __forceinline__ void append_turn(const AppendArgs& a, const AppendUni
 // kNorm: queries and keys are normalised on the way (4 lanes sum a row's
 // squares), positions may start anywhere, and the keys' positions and weights
 // are written beside them.
-template <bool kRun, bool kNorm>
+template <bool kRun, bool kNorm, int kTurn>
 __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_kernel(const AppendArgs a) {
   __shared__ float4 cs[kAppendTokens][kHeadDim / 4];  // two (cosine, sine) pairs each
   __shared__ int64_t slot_row[kAppendTokens];  // row of head 0 in the pages, -1: not written
   __shared__ int depth[kTreeMax], jump[kTreeMax];
+  // kNorm: the same memory as rows of 32 cosines and, behind them, of sines
+  float* const cosines = reinterpret_cast<float*>(cs);
+  float* const sines = cosines + kAppendTokens * (kHeadDim / 2);
   const CacheArgs& c = a.c;
   const int u4 = threadIdx.x & 3, nh = a.rope.dims / 16, half = a.rope.dims / 2;
   const bool rotated = u4 < nh;
@@ -140,8 +139,11 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
   ln.t = (threadIdx.x >> 2) & (a.tokens - 1);  // a.tokens is a power of two
   ln.h = (threadIdx.x >> 2) / a.tokens;
   ln.step = kAppendPass / a.tokens;
-  ln.c0 = a.rope.interleaved || !rotated ? 2 * u4 : u4;
-  ln.c1 = a.rope.interleaved || !rotated ? 2 * u4 + 1 : u4 + nh;
+  const RowLane rl = row_lane<kTurn>(u4, a.rope.dims);
+  ln.c0 = kNorm ? rl.c0 : a.rope.interleaved || !rotated ? 2 * u4 : u4;
+  ln.c1 = kNorm ? rl.c1 : a.rope.interleaved || !rotated ? 2 * u4 + 1 : u4 + nh;
+  // (read once: lanes read the launch's arguments one after the other)
+  const uint64_t freq = a.rope.freq[threadIdx.x % (kHeadDim / 2)];
   const int cap = c.page * c.max_blocks;
   const int split = a.q_parts + 2 * a.kv_parts;
   int64_t bt = kRun ? blockIdx.x : blockIdx.x / split;
@@ -206,13 +208,20 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
         const int t = y / (kHeadDim / 2), f = y % (kHeadDim / 2);
         if (f >= half) continue;
         const uint64_t pos = static_cast<uint64_t>(kNorm ? first : len) + (c.parents ? depth[t0 + t] : t0 + t);
-        reinterpret_cast<float2*>(cs[t])[f] = rope_angle(pos, a.rope.freq[f]);
+        const float2 angle = rope_angle(pos, freq);
+        if (kNorm) {
+          cosines[t * (kHeadDim / 2) + f] = angle.x;
+          sines[t * (kHeadDim / 2) + f] = angle.y;
+        } else {
+          reinterpret_cast<float2*>(cs[t])[f] = angle;
+        }
       }
       __syncthreads();
       last_b = x.b;
       last_tile = x.tile;
     }
-    if (kNorm && x.kind < 2 && nt > 0) append_turn(a, x, ln, rotated, cs[ln.t] + 4 * u4, w);
+    if (kNorm && x.kind < 2 && nt > 0)
+      append_turn<kTurn>(a, x, ln, rl, cosines + ln.t * (kHeadDim / 2), sines + ln.t * (kHeadDim / 2), w);
     const int64_t row = ln.t < nt ? (x.kind == 0 ? 0 : slot_row[ln.t]) : -1;
     if (kNorm && a.key_pos && x.kind == 1 && row >= 0 && u4 == 0) {
       const int pos = first + (c.parents ? depth[t0 + ln.t] : t0 + ln.t);
@@ -267,6 +276,138 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
       w[y][0] = wn[y][0];
       w[y][1] = wn[y][1];
     }
+  }
+  if (!ok) record_bad_arg(c.status);
+}
+
+// Prompts with norms: a CTA walks over tiles of eight tokens of one sequence, four heads (a
+// warp each) a pass: the queries', the keys' and the values'; the next pass's rows are on
+// their way while one is turned and stored.  A tile's angles and slots serve all its heads.
+// 8 prompts of up to 8192 tokens, 12 heads: 97 us (472 MB); in the units of the kernel
+// above, whose four rows a thread leave too few registers, 122.  6, 8 and 10 CTAs an SM
+// take 104, 97 and 103.
+constexpr int kRunWarps = 4, kRunThreads = 32 * kRunWarps, kRunTokens = 8, kRunResident = 8;
+
+struct RunTile {
+  unsigned tile;
+  int b, t0, len, n, first;
+};
+// The first tile from w.tile on, in steps of the grid, that holds a token; false if none.
+__device__ __forceinline__ bool run_tile(const AppendArgs& a, unsigned tiles, RunTile& w, bool& ok) {
+  const unsigned each = (a.c.N + kRunTokens - 1) / kRunTokens;
+  for (; w.tile < tiles; w.tile += gridDim.x) {
+    w.b = static_cast<int>(w.tile / each);
+    w.t0 = static_cast<int>(w.tile - w.b * each) * kRunTokens;
+    ok &= append_lengths(a.c, w.b, w.len, w.n);
+    ok &= append_first(a, w.b, w.len, w.first);
+    if (w.t0 < w.n) return true;
+  }
+  return false;
+}
+
+template <int kTurn>
+__global__ void __launch_bounds__(kRunThreads, kRunResident) bam_kv_append_run_kernel(const AppendArgs a) {
+  __shared__ __align__(16) float cosines[kRunTokens][kHeadDim / 2], sines[kRunTokens][kHeadDim / 2];
+  const CacheArgs& c = a.c;
+  const RowLane l = row_lane<kTurn>(threadIdx.x & 3, a.rope.dims);
+  const int lt = (threadIdx.x >> 2) & 7, lh = threadIdx.x >> 5;
+  // (read once: lanes read the launch's arguments one after the other)
+  const uint64_t freq = a.rope.freq[threadIdx.x % (kHeadDim / 2)];
+  const int q_passes = (a.H + kRunWarps - 1) / kRunWarps, kv_passes = (c.Hkv + kRunWarps - 1) / kRunWarps;
+  const int passes = q_passes + 2 * kv_passes;
+  const unsigned tiles = c.B * ((static_cast<unsigned>(c.N) + kRunTokens - 1) / kRunTokens);
+  const int cap = c.page * c.max_blocks;
+  bool ok = true;
+  RunTile at;
+  at.tile = blockIdx.x;
+  if (!run_tile(a, tiles, at, ok)) {
+    if (!ok) record_bad_arg(c.status);
+    return;
+  }
+  RunTile ahead = at;
+  bool more = true;
+  int next = 0;  // pass of the rows on their way
+  uint4 x[2] = {};
+  auto load = [&]() {
+    const int kind = next < q_passes ? 0 : next < q_passes + kv_passes ? 1 : 2;
+    const int h = kRunWarps * (next - (kind == 0 ? 0 : kind == 1 ? q_passes : q_passes + kv_passes)) + lh;
+    const int t = ahead.t0 + lt;
+    if (!more || t >= ahead.n || h >= (kind == 0 ? a.H : c.Hkv)) return;
+    const int64_t* st = kind == 0 ? a.qs : kind == 1 ? a.ks : a.vs;
+    const uint4* src = reinterpret_cast<const uint4*>((kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
+                                                      (ahead.b * st[0] + h * st[1] + t * st[2]));
+    x[0] = src[l.c0];
+    x[1] = src[l.c1];
+  };
+  load();
+  for (;;) {
+    // This thread's token and its slot.
+    const int t = at.t0 + lt;
+    const bool live = t < at.n;
+    int64_t row = -1;
+    if (live) {
+      const int64_t slot = static_cast<int64_t>(at.len) + t;
+      if (slot < cap) {
+        const int blk = static_cast<int>(slot) / c.page;
+        const int pg = __ldg(c.block_table + static_cast<size_t>(at.b) * c.max_blocks + blk);
+        if (pg >= 0 && pg < c.num_pages)
+          row = static_cast<int64_t>(pg) * c.Hkv * c.page + (static_cast<int>(slot) - blk * c.page);
+      }
+      ok &= row >= 0;
+    }
+    if (kTurn != kNoTurn) {
+      __syncthreads();  // the last tile's angles are no longer read
+      for (int y = threadIdx.x; y < kRunTokens * (kHeadDim / 2); y += kRunThreads) {
+        const int f = y % (kHeadDim / 2), ty = y / (kHeadDim / 2);
+        if (2 * f >= a.rope.dims) continue;
+        const float2 r = rope_angle(static_cast<uint64_t>(at.first + at.t0 + ty), freq);
+        cosines[ty][f] = r.x;
+        sines[ty][f] = r.y;
+      }
+      __syncthreads();
+    }
+    for (int pass = 0; pass < passes; ++pass) {
+      const int kind = pass < q_passes ? 0 : pass < q_passes + kv_passes ? 1 : 2;
+      const int h = kRunWarps * (pass - (kind == 0 ? 0 : kind == 1 ? q_passes : q_passes + kv_passes)) + lh;
+      const int heads = kind == 0 ? a.H : c.Hkv;
+      uint4 w[2] = {x[0], x[1]};
+      if (++next == passes) {
+        next = 0;
+        ahead.tile += gridDim.x;
+        more = run_tile(a, tiles, ahead, ok);
+      }
+      load();
+      if (kind < 2) {
+        F2x8 f;
+        unpack_row(w, f);
+        const float* weight = kind == 0 ? a.q_weight : a.k_weight;
+        if (weight) {
+          F2x8 wt;
+          load_weight(weight + (a.per_head ? min(h, heads - 1) * kHeadDim : 0), l, wt);
+          float scale;
+          const uint64_t inv = f2_both(row_rms_inv(f, a.norm_eps, &scale));
+#pragma unroll
+          for (int z = 0; z < 8; ++z) f[z] = fmul2(fmul2(f[z], inv), wt[z]);
+        }
+        turn_values<kTurn>(f, cosines[lt], sines[lt], l);
+        pack_row(f, w);
+      }
+      if (!live || h >= heads || (kind && row < 0)) continue;
+      uint16_t* base = kind == 0 ? a.q_out : kind == 1 ? a.k_pages : a.v_pages;
+      const int64_t to = kind == 0 ? (static_cast<int64_t>(at.b) * a.H + h) * c.N + t
+                                   : row + static_cast<int64_t>(h) * c.page;
+      uint4* dst = reinterpret_cast<uint4*>(base) + 8 * to;
+      dst[l.c0] = w[0];
+      dst[l.c1] = w[1];
+      if (kind == 1 && a.key_pos && l.u4 == 0) {
+        const int pos = at.first + t;
+        ok &= pos < a.max_pos;
+        a.key_pos[to] = pos;
+        a.key_weight[to] = 0.0f;
+      }
+    }
+    if (!more) break;
+    at = ahead;
   }
   if (!ok) record_bad_arg(c.status);
 }
@@ -377,12 +518,29 @@ cudaError_t launch_append(const AppendArgs& args, cudaStream_t st) {
   // 20.3 for 200 drafts of 48 nodes; resident CTAs take 4.2 instead of 3.0 for 8
   // single tokens and 11.1 instead of 10.1 for 64 drafts of 48 nodes.
   const int64_t run = static_cast<int64_t>(sm_count()) * kAppendResident;
+  typedef void (*Kernel)(AppendArgs);
+  if (a.extended) {
+    const int turned = a.rope.dims == 0 ? kNoTurn : a.rope.interleaved ? kPairs : kHalves;
+    const int64_t run_tiles = static_cast<int64_t>(a.c.B) * ((a.c.N + kRunTokens - 1) / kRunTokens);
+    if (tiles > run && !a.c.parents && run_tiles <= 0x7FFFFFFF) {
+      constexpr Kernel runs[] = {bam_kv_append_run_kernel<kNoTurn>, bam_kv_append_run_kernel<kHalves>,
+                                 bam_kv_append_run_kernel<kPairs>};
+      int64_t ctas = static_cast<int64_t>(sm_count()) * kRunResident;
+      if (ctas > run_tiles) ctas = run_tiles;
+      return launch_k(runs[turned], dim3(static_cast<unsigned>(ctas)), dim3(kRunThreads), 0, st, false, a);
+    }
+    if (units > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    constexpr Kernel normed[] = {bam_kv_append_kernel<false, true, kNoTurn>,
+                                 bam_kv_append_kernel<false, true, kHalves>,
+                                 bam_kv_append_kernel<false, true, kPairs>};
+    return launch_k(normed[turned], dim3(static_cast<unsigned>(units)), dim3(kAppendThreads), 0, st, false, a);
+  }
   if (tiles > run)
-    return launch_k(a.extended ? bam_kv_append_kernel<true, true> : bam_kv_append_kernel<true, false>,
-                    dim3(static_cast<unsigned>(run)), dim3(kAppendThreads), 0, st, false, a);
+    return launch_k(bam_kv_append_kernel<true, false, kNoTurn>, dim3(static_cast<unsigned>(run)),
+                    dim3(kAppendThreads), 0, st, false, a);
   if (units > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  return launch_k(a.extended ? bam_kv_append_kernel<false, true> : bam_kv_append_kernel<false, false>,
-                  dim3(static_cast<unsigned>(units)), dim3(kAppendThreads), 0, st, false, a);
+  return launch_k(bam_kv_append_kernel<false, false, kNoTurn>, dim3(static_cast<unsigned>(units)),
+                  dim3(kAppendThreads), 0, st, false, a);
 }
 
 cudaError_t launch_keep(const KeepArgs& a, cudaStream_t st) {

@@ -4,336 +4,422 @@
 //   dn = R(-pos) dy,  dw = sum dn n,  dx = r (w dn - n mean(w dn n))
 //
 // per head vector x of 64 values.  A row is read and written once: 256 bytes
-// forward, 384 backward, against some 500 and 1000 instructions of a lane, so
-// both are bound by HBM.  1 / rms is computed again in the backward pass (x is
-// read there anyway), so nothing is kept between the passes.
+// forward, 384 backward, so both are bound by HBM as far as their instructions
+// let them: some 200 and 300 of a warp for eight rows, where a copy has 30.  1 / rms is
+// computed again in the backward pass (x is read there anyway), so nothing is
+// kept between the passes.
 //
-// Four lanes hold a row, 16 values each; a tile is 16 tokens, whose angles are
-// computed once for the heads of a unit (a sine and cosine cost as much as a
-// value's whole path).
+// Four lanes hold a row, 16 values each, as pairs for f32x2 arithmetic; a tile is 8 or 16
+// tokens, whose angles are computed once for all heads (a sine and cosine cost as
+// much as a value's whole path), and a CTA goes through the heads of a token in
+// order, as they lie in a projection's output.
+//
+// Measured on the device: 4 x 16383 tokens, 32 and 8 heads, out of a projection's output:
+// forward 112 us (0.67 GB, 6.0 TB/s; a copy along the same path takes 101), backward
+// 192 us (1.0 GB, 5.2 TB/s); 8 x 512 tokens, 12 and 12 heads: 9.0 and 15 us.
 #include "norm_common.cuh"
 
 namespace bam {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTokens = 16;       // of a tile
-constexpr int kPass = 4;          // heads of a pass: 64 rows of 4 lanes
-constexpr int kFwdRows = 4;       // passes of a forward unit, loaded at once
+// Tokens of a thread in a tile, eight apart: two share a head's weights and, backward, the
+// sum of its gradient.
+constexpr int kFwdSlots = 1, kBwdSlots = 2;
+constexpr int kPass = kNormPass;  // heads of a pass, a warp of eight rows each
+constexpr int kThreads = 32 * kPass;
 constexpr int kFinishThreads = 1024;
+// Resident CTAs of an SM (forward 3, 4 and 5 took 126, 113 and 136 us in the first case
+// above, with eight warps a CTA).
+constexpr int kFwdResident = 32 / kNormPass, kBwdResident = 16 / kNormPass;
 
-// This thread's place: token t of the tile, head h of each pass, its chunks.
-struct Lane {
-  int t, h, u4, c0, c1;
-  bool rotated;
+// This thread's place: tokens t and t + 8 of the tile, head h of each pass.
+struct Lane : RowLane {
+  int t, h;
 };
+template <int kTurn>
 __device__ __forceinline__ Lane lane_of(const RopeArgs& r) {
-  Lane l;
-  l.u4 = threadIdx.x & 3;
-  l.t = (threadIdx.x >> 2) & (kTokens - 1);
-  l.h = threadIdx.x / (4 * kTokens);
-  const int nh = r.dims / 16;
-  l.rotated = l.u4 < nh;
-  const bool apart = l.rotated && !r.interleaved;
-  l.c0 = apart ? l.u4 : 2 * l.u4;
-  l.c1 = apart ? l.u4 + nh : 2 * l.u4 + 1;
-  return l;
+  return Lane{row_lane<kTurn>(threadIdx.x & 3, r.dims), static_cast<int>(threadIdx.x >> 2) & 7,
+              static_cast<int>(threadIdx.x >> 5)};
 }
 
-// Cosines and sines of a tile's tokens, by the whole block.
-__device__ __forceinline__ void tile_angles(const NormArgs& a, unsigned tile,
-                                            float4 (*cs)[kHeadDim / 4]) {
+// Cosines and sines (times `sign`) of a tile's tokens, by the whole block.
+template <int kSlots>
+struct Angles {
+  float cos[8 * kSlots][kHeadDim / 2];
+  float sin[8 * kSlots][kHeadDim / 2];
+};
+template <int kSlots>
+__device__ __forceinline__ void tile_angles(const NormArgs& a, unsigned tile, float sign,
+                                            uint64_t freq, Angles<kSlots>& cs) {
+  constexpr int kTokens = 8 * kSlots;
   const int half = a.rope.dims / 2;
   for (int y = threadIdx.x; y < kTokens * (kHeadDim / 2); y += kThreads) {
     const int t = y / (kHeadDim / 2), f = y % (kHeadDim / 2);
     const unsigned n = tile * kTokens + t;
     if (f >= half) continue;
     // (places behind the last token hold zeros, which any angle leaves zero)
-    const int pos = n >= a.tokens ? 0 : a.positions ? __ldg(a.positions + n) : static_cast<int>(n % a.T);
-    reinterpret_cast<float2*>(cs[t])[f] =
-        rope_angle(static_cast<uint64_t>(static_cast<int64_t>(pos)), a.rope.freq[f]);
+    const int pos = n >= a.tokens ? 0
+                    : a.positions ? __ldg(a.positions + n)
+                                  : static_cast<int>(n - a.T * divide(n, a.by_T));
+    const float2 x = rope_angle(static_cast<uint64_t>(static_cast<int64_t>(pos)), freq);
+    cs.cos[t][f] = x.x;
+    cs.sin[t][f] = sign * x.y;
   }
+}
+
+// A CTA's tiles, every `step`-th from `tile` on, and passes; the queries' passes come
+// first.
+struct Span {
+  unsigned tile, tiles, step;
+  int first, last, nq;
+};
+template <int kSlots>
+__device__ __forceinline__ Span span_of(const NormArgs& a) {
+  constexpr int kTokens = 8 * kSlots;
+  Span s;
+  s.tiles = (a.tokens + kTokens - 1) / kTokens;
+  s.tile = blockIdx.x / a.parts;
+  s.step = a.ctas / a.parts;
+  s.nq = (a.side[0].heads + kPass - 1) / kPass;
+  s.first = static_cast<int>(blockIdx.x - s.tile * a.parts) * a.passes;
+  s.last = min(s.first + a.passes, s.nq + (a.side[1].heads + kPass - 1) / kPass);
+  return s;
+}
+
+// A walk over them: places of this thread's rows in kN tensors, in 16-byte words (32 bits
+// where that is enough: fewer registers, see launch_norm_fwd).  `strides` gives those of
+// a side's tensor.  A pass further on a side is kPass heads further; places are worked
+// out anew for a tile and for a side.
+template <int kN, int kSlots, class Off>
+struct Walk {
+  unsigned tile;
+  int pass, side, h;
+  bool live[kSlots];
+  Off at[kN][kSlots];
+  __device__ __forceinline__ bool on(const NormArgs& a, int y) const {
+    return live[y] && h < a.side[side].heads;
+  }
+};
+template <int kN, int kSlots, class Off, class F>
+__device__ __forceinline__ void walk_to(Walk<kN, kSlots, Off>& w, const NormArgs& a, const Span& s,
+                                        const Lane& l, F strides) {
+  w.side = w.pass >= s.nq;
+  w.h = kPass * (w.pass - (w.side ? s.nq : 0)) + l.h;
+#pragma unroll
+  for (int y = 0; y < kSlots; ++y) {
+    const unsigned n = 8 * (w.tile * kSlots + y) + l.t;
+    w.live[y] = w.tile < s.tiles && n < a.tokens;
+    const unsigned b = w.live[y] ? divide(n, a.by_T) : 0, t = w.live[y] ? n - b * a.T : 0;
+#pragma unroll
+    for (int x = 0; x < kN; ++x) {
+      const int64_t* st = strides(a.side[w.side], x);
+      w.at[x][y] = static_cast<Off>(st[0]) * b + static_cast<Off>(st[1]) * w.h + static_cast<Off>(st[2]) * t;
+    }
+  }
+}
+template <int kN, int kSlots, class Off, class F>
+__device__ __forceinline__ void walk_on(Walk<kN, kSlots, Off>& w, const NormArgs& a, const Span& s,
+                                        const Lane& l, F strides) {
+  ++w.pass;
+  if (w.pass != s.last && w.pass != s.nq) {
+    w.h += kPass;
+#pragma unroll
+    for (int x = 0; x < kN; ++x) {
+      const Off step = static_cast<Off>(strides(a.side[w.side], x)[1]) * kPass;
+#pragma unroll
+      for (int y = 0; y < kSlots; ++y) w.at[x][y] += step;
+    }
+    return;
+  }
+  if (w.pass == s.last) {
+    w.pass = s.first;
+    w.tile += s.step;
+  }
+  walk_to(w, a, s, l, strides);
 }
 
 struct Row {
   uint4 v[2];
 };
-__device__ __forceinline__ Row load_row(const uint16_t* p, const int64_t* st, unsigned b, int h,
-                                        unsigned t, const Lane& l) {
-  const uint16_t* src = p + b * st[0] + h * st[1] + t * st[2];
-  Row r;
-  r.v[0] = *reinterpret_cast<const uint4*>(src + 8 * l.c0);
-  r.v[1] = *reinterpret_cast<const uint4*>(src + 8 * l.c1);
-  return r;
+template <class Off>
+__device__ __forceinline__ void load_row(const uint16_t* p, Off at, bool on, const Lane& l, Row& r) {
+  r.v[0] = r.v[1] = make_uint4(0, 0, 0, 0);
+  if (!on) return;
+  const uint4* src = reinterpret_cast<const uint4*>(p) + at;
+  r.v[0] = src[l.c0];
+  r.v[1] = src[l.c1];
 }
-__device__ __forceinline__ void store_row(uint16_t* p, const int64_t* st, unsigned b, int h,
-                                          unsigned t, const Lane& l, const float* f) {
-  uint16_t* dst = p + b * st[0] + h * st[1] + t * st[2];
-  *reinterpret_cast<uint4*>(dst + 8 * l.c0) = pack8(f);
-  *reinterpret_cast<uint4*>(dst + 8 * l.c1) = pack8(f + 8);
+template <class Off>
+__device__ __forceinline__ void store_row(uint16_t* p, Off at, const Lane& l, const F2x8& f) {
+  uint4 v[2];
+  pack_row(f, v);
+  uint4* dst = reinterpret_cast<uint4*>(p) + at;
+  dst[l.c0] = v[0];
+  dst[l.c1] = v[1];
 }
-__device__ __forceinline__ void load_weight(const NormArgs& a, const NormSide& s, int h,
-                                            const Lane& l, float* w) {
-  const float* p = s.w + (a.per_head ? h * kHeadDim : 0);
+// A CTA takes its tiles and passes in turn (Span); the rows of the next passes are on their way while one is turned and stored.
+template <int kTurn, class Off>
+__global__ void __launch_bounds__(kThreads, kFwdResident) bam_qk_norm_fwd_kernel(const NormArgs a) {
+  __shared__ __align__(16) Angles<kFwdSlots> cs;
+  const Lane l = lane_of<kTurn>(a.rope);
+  // this thread's frequency (read once: lanes read the launch's arguments one after the other)
+  const uint64_t freq = a.rope.freq[threadIdx.x % (kHeadDim / 2)];
+  const Span sp = span_of<kFwdSlots>(a);
+  auto xs = [](const NormSide& s, int) { return s.xs; };
+  auto ys = [](const NormSide& s, int) { return s.ys; };
+  constexpr int kSlots = kFwdSlots;
+  Walk<1, kSlots, Off> at, ahead;
+  at.tile = ahead.tile = sp.tile;
+  at.pass = ahead.pass = sp.first;
+  walk_to(ahead, a, sp, l, xs);
+  walk_to(at, a, sp, l, ys);
+  Row x[kSlots];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const float4* q = reinterpret_cast<const float4*>(p + 8 * (c ? l.c1 : l.c0));
-    const float4 x = __ldg(q), y = __ldg(q + 1);
-    w[8 * c] = x.x, w[8 * c + 1] = x.y, w[8 * c + 2] = x.z, w[8 * c + 3] = x.w;
-    w[8 * c + 4] = y.x, w[8 * c + 5] = y.y, w[8 * c + 6] = y.z, w[8 * c + 7] = y.w;
-  }
-}
-
-// A unit is a tile of tokens and up to 16 heads (the queries' and then the
-// keys', in one row of numbers); all its rows are on their way before its angles are
-// computed.
-__global__ void __launch_bounds__(kThreads, 4) bam_qk_norm_fwd_kernel(const NormArgs a) {
-  __shared__ float4 cs[kTokens][kHeadDim / 4];
-  const Lane l = lane_of(a.rope);
-  const unsigned tile = blockIdx.x / a.parts;
-  const int part = static_cast<int>(blockIdx.x - tile * a.parts);
-  const unsigned n = tile * kTokens + l.t;
-  const bool live = n < a.tokens;
-  const unsigned b = live ? n / a.T : 0, t = n - b * a.T;
-  const int h0 = part * a.heads + l.h, H = a.side[0].heads;
-  const int end = min((part + 1) * a.heads, H + a.side[1].heads);
-  Row x[kFwdRows];
-#pragma unroll
-  for (int y = 0; y < kFwdRows; ++y) {
-    const int hh = h0 + kPass * y;
-    if (!live || hh >= end) continue;
-    const NormSide& s = a.side[hh >= H];
-    x[y] = load_row(s.x, s.xs, b, hh >= H ? hh - H : hh, t, l);
-  }
-  if (a.rope.dims) {
-    tile_angles(a, tile, cs);
-    __syncthreads();
-  }
-  float4 r[4];
-  if (l.rotated) {
-#pragma unroll
-    for (int z = 0; z < 4; ++z) r[z] = cs[l.t][4 * l.u4 + z];
-  }
-#pragma unroll
-  for (int y = 0; y < kFwdRows; ++y) {
-    const int hh = h0 + kPass * y;
-    if (__all_sync(0xffffffffu, hh >= end)) break;
-    const bool on = live && hh < end;
-    float f[16];
-    if (!on) x[y].v[0] = x[y].v[1] = make_uint4(0, 0, 0, 0);
-    unpack8(x[y].v[0], f);
-    unpack8(x[y].v[1], f + 8);
-    float scale;
-    const float inv = row_rms_inv(f, a.eps, &scale);
-    if (!on) continue;
-    const NormSide& s = a.side[hh >= H];
-    const int h = hh >= H ? hh - H : hh;
-    float w[16];
-    load_weight(a, s, h, l, w);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = f[i] * inv * w[i];
-    if (l.rotated) turn_row(f, f + 8, r, a.rope.interleaved, 1.0f);
-    store_row(s.y, s.ys, b, h, t, l, f);
-  }
-}
-
-// A CTA takes every (ctas / parts)-th tile of one part of the heads, a pass of
-// four heads after the other with the next pass's rows on their way, and sums
-// the weights' gradients in shared memory: a warp's eight rows belong to one
-// head, so they are joined by shuffles (halving the values each lane holds), and
-// a place in shared memory has one warp that adds to it.  The order of every sum
-// is fixed.
-__global__ void __launch_bounds__(kThreads, 2) bam_qk_norm_bwd_kernel(const NormArgs a) {
-  extern __shared__ __align__(16) float acc[];  // [rows][2 token halves][64]
-  __shared__ float4 cs[kTokens][kHeadDim / 4];
-  grid_dep_trigger();
-  const Lane l = lane_of(a.rope);
-  const int lane = threadIdx.x & 31, wt = (threadIdx.x >> 5) & 1;
-  const int part = blockIdx.x % a.parts, H = a.side[0].heads;
-  const int first = part * a.heads, end = min(first + a.heads, H + a.side[1].heads);
-  const int passes = (end - first + kPass - 1) / kPass;
-  const int acc_rows = a.per_head ? a.heads : 2 * kPass;
-  for (int y = threadIdx.x; y < acc_rows * 2 * kHeadDim; y += kThreads) acc[y] = 0.0f;
-  const unsigned tiles = (a.tokens + kTokens - 1) / kTokens;
-  const unsigned step = a.ctas / a.parts;
-  unsigned tile = blockIdx.x / a.parts;
-  int pass = 0;
-  Row x, g;
-  auto load = [&](unsigned tl, int ps, Row& xr, Row& gr) {
-    const unsigned n = tl * kTokens + l.t;
-    const int hh = first + kPass * ps + l.h;
-    if (tl >= tiles || n >= a.tokens || hh >= end) {
-      xr.v[0] = xr.v[1] = gr.v[0] = gr.v[1] = make_uint4(0, 0, 0, 0);
-      return;
-    }
-    const unsigned b = n / a.T, t = n - b * a.T;
-    const NormSide& s = a.side[hh >= H];
-    const int h = hh >= H ? hh - H : hh;
-    xr = load_row(s.x, s.xs, b, h, t, l);
-    gr = load_row(s.g, s.gs, b, h, t, l);
-  };
-  load(tile, 0, x, g);
-  float4 r[4];
-  while (tile < tiles) {
-    const int next_pass = pass + 1 == passes ? 0 : pass + 1;
-    const unsigned next_tile = next_pass ? tile : tile + step;
-    Row xn, gn;
-    load(next_tile, next_pass, xn, gn);
-    if (pass == 0) {
-      __syncthreads();  // the last tile's angles are no longer read; the sums are zeroed
-      if (a.rope.dims) tile_angles(a, tile, cs);
+  for (int y = 0; y < kSlots; ++y) load_row(a.side[ahead.side].x, ahead.at[0][y], ahead.on(a, y), l, x[y]);
+  while (at.tile < sp.tiles) {
+    walk_on(ahead, a, sp, l, xs);
+    if (kTurn != kNoTurn && at.pass == sp.first) {
+      __syncthreads();  // the last tile's angles are no longer read
+      tile_angles(a, at.tile, 1.0f, freq, cs);
       __syncthreads();
-      if (l.rotated) {
+    }
+    F2x8 w;
+    load_weight(a.side[at.side].w + (a.per_head && at.on(a, 0) ? at.h * kHeadDim : 0), l, w);
 #pragma unroll
-        for (int z = 0; z < 4; ++z) r[z] = cs[l.t][4 * l.u4 + z];
+    for (int y = 0; y < kSlots; ++y) {
+      F2x8 f;
+      unpack_row(x[y].v, f);
+      load_row(a.side[ahead.side].x, ahead.at[0][y], ahead.on(a, y), l, x[y]);
+      float scale;
+      const float inv = row_rms_inv(f, a.eps, &scale);
+      const uint64_t inv2 = f2_both(inv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = fmul2(fmul2(f[i], inv2), w[i]);
+      turn_values<kTurn>(f, cs.cos[8 * y + l.t], cs.sin[8 * y + l.t], l);
+      if (at.on(a, y)) store_row(a.side[at.side].y, at.at[0][y], l, f);
+    }
+    walk_on(at, a, sp, l, ys);
+  }
+}
+
+// Sum of a warp's eight rows of 16 values (f32x2 pairs): each step hands over half of
+// them; this lane ends with the pair whose number is made of its lane bits 4, 3, 2.
+__device__ __forceinline__ uint64_t sum_rows(F2x8& v, int lane) {
+#pragma unroll
+  for (int n = 4, bit = 16; n >= 1; n >>= 1, bit >>= 1) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const bool up = lane & bit;
+      const uint64_t send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = fadd2(keep, __shfl_xor_sync(0xffffffffu, send, bit));
+    }
+  }
+  return v[0];
+}
+
+// As the forward kernel.  With r = 1 / rms, d = dn r and u = w d:
+// dw gathers d x, and dx = u - x r^2 mean(u x).  The sums of the weights'
+// gradients stay in registers as long as they belong to one row of them (a
+// side's passes of a tile, or one pass with weights of each head); a warp's eight rows
+// are then joined by shuffles and added to shared memory, where every place has
+// one warp that adds to it.  The order of every sum is fixed.
+template <int kTurn, class Off>
+__global__ void __launch_bounds__(kThreads, kBwdResident) bam_qk_norm_bwd_kernel(const NormArgs a) {
+  extern __shared__ __align__(16) float acc[];  // [rows][64], a warp adds to each
+  __shared__ __align__(16) Angles<kBwdSlots> cs;
+  grid_dep_trigger();
+  const Lane l = lane_of<kTurn>(a.rope);
+  const int lane = threadIdx.x & 31;
+  // this thread's frequency (read once: lanes read the launch's arguments one after the other)
+  const uint64_t freq = a.rope.freq[threadIdx.x % (kHeadDim / 2)];
+  const int acc_rows = kPass * (a.per_head ? a.passes : 2);
+  // (each place is zeroed by a thread of the warp that adds to it)
+  for (int y = 0; y < acc_rows / kPass; ++y)
+    reinterpret_cast<uint64_t*>(acc + (kPass * y + l.h) * kHeadDim)[lane] = 0;
+  __syncwarp();
+  const Span sp = span_of<kBwdSlots>(a);
+  auto xs = [](const NormSide& s, int x) { return x ? s.gs : s.xs; };
+  auto ys = [](const NormSide& s, int) { return s.ys; };
+  constexpr int kSlots = kBwdSlots;
+  Walk<2, kSlots, Off> ahead;
+  Walk<1, kSlots, Off> at;
+  at.tile = ahead.tile = sp.tile;
+  at.pass = ahead.pass = sp.first;
+  walk_to(ahead, a, sp, l, xs);
+  walk_to(at, a, sp, l, ys);
+  Row x[kSlots], g[kSlots];
+  auto load = [&](int y) {
+    const bool on = ahead.on(a, y);
+    load_row(a.side[ahead.side].x, ahead.at[0][y], on, l, x[y]);
+    load_row(a.side[ahead.side].g, ahead.at[1][y], on, l, g[y]);
+  };
+#pragma unroll
+  for (int y = 0; y < kSlots; ++y) load(y);
+  F2x8 sum;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] = 0;
+  while (at.tile < sp.tiles) {
+    walk_on(ahead, a, sp, l, xs);
+    if (kTurn != kNoTurn && at.pass == sp.first) {
+      __syncthreads();  // the last tile's angles are no longer read
+      tile_angles(a, at.tile, -1.0f, freq, cs);
+      __syncthreads();
+    }
+    F2x8 w;
+    load_weight(a.side[at.side].w + (a.per_head && at.on(a, 0) ? at.h * kHeadDim : 0), l, w);
+#pragma unroll
+    for (int y = 0; y < kSlots; ++y) {
+      F2x8 f, d;
+      unpack_row(x[y].v, f);
+      unpack_row(g[y].v, d);
+      load(y);
+      float scale;
+      const float inv = row_rms_inv(f, a.eps, &scale);
+      turn_values<kTurn>(d, cs.cos[8 * y + l.t], cs.sin[8 * y + l.t], l);
+      const uint64_t inv2 = f2_both(inv);
+      uint64_t dot0 = 0, dot1 = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        d[i] = fmul2(d[i], inv2);
+        sum[i] = ffma2(d[i], f[i], sum[i]);
+        d[i] = fmul2(d[i], w[i]);
+        if (i & 1)
+          dot1 = ffma2(d[i], f[i], dot1);
+        else
+          dot0 = ffma2(d[i], f[i], dot0);
       }
-    }
-    const unsigned n = tile * kTokens + l.t;
-    const int hh = first + kPass * pass + l.h;
-    const bool on = n < a.tokens && hh < end;
-    const NormSide& s = a.side[hh >= H];
-    const int h = hh >= H ? hh - H : hh;
-    float f[16], d[16], w[16];
-    unpack8(x.v[0], f);
-    unpack8(x.v[1], f + 8);
-    unpack8(g.v[0], d);
-    unpack8(g.v[1], d + 8);
-    float scale;
-    const float inv = row_rms_inv(f, a.eps, &scale);
-    if (l.rotated) turn_row(d, d + 8, r, a.rope.interleaved, -1.0f);
-    if (on)
-      load_weight(a, s, h, l, w);
-    else
+      const float dot = row_sum(f2_sum(fadd2(dot0, dot1))) * (1.0f / kHeadDim);
+      const uint64_t back = f2_both(-dot * inv * inv);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = 0.0f;
-    float dot = 0.0f, v[16];
+      for (int i = 0; i < 8; ++i) d[i] = ffma2(f[i], back, d[i]);
+      if (__any_sync(0xffffffffu, scale != 1.0f)) {
+        const uint64_t s2 = f2_both(scale);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      f[i] *= inv;         // n
-      v[i] = d[i] * f[i];  // dn n: this row's part of dw
-      d[i] *= w[i];
-      dot = fmaf(d[i], f[i], dot);
+        for (int i = 0; i < 8; ++i) d[i] = fmul2(d[i], s2);
+      }
+      if (at.on(a, y)) store_row(a.side[at.side].y, at.at[0][y], l, d);
     }
-    dot = row_sum(dot) * (1.0f / kHeadDim);
-    if (on) {
-      const float back = inv * scale;
-      float dx[16];
+    const int pass = at.pass, side = at.side;
+    walk_on(at, a, sp, l, ys);
+    if (a.per_head || at.pass == sp.first || at.side != side) {
+      const uint64_t v = sum_rows(sum, lane);
+      const int row = kPass * (a.per_head ? pass - sp.first : side) + l.h;
+      const int pair = (lane & 16 ? 4 : 0) + (lane & 8 ? 2 : 0) + (lane & 4 ? 1 : 0);
+      uint64_t* p = reinterpret_cast<uint64_t*>(acc + row * kHeadDim + 8 * (pair >= 4 ? l.c1 : l.c0) +
+                                                2 * (pair & 3));
+      *p = fadd2(*p, v);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) dx[i] = back * (d[i] - f[i] * dot);
-      const unsigned b = n / a.T;
-      store_row(s.y, s.ys, b, h, n - b * a.T, l, dx);
+      for (int i = 0; i < 8; ++i) sum[i] = 0;
     }
-    // Sum of the warp's eight rows: each step hands over half of the values.
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float send = lane & 16 ? v[i] : v[i + 8];
-      const float keep = lane & 16 ? v[i + 8] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float send = lane & 8 ? v[i] : v[i + 4];
-      const float keep = lane & 8 ? v[i + 4] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 8);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float send = lane & 4 ? v[i] : v[i + 2];
-      const float keep = lane & 4 ? v[i + 2] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 4);
-    }
-    if (hh < end) {
-      const int row = a.per_head ? hh - first : (hh >= H ? kPass : 0) + l.h;
-      const int chunk = lane & 16 ? l.c1 : l.c0;
-      float* p = acc + (2 * row + wt) * kHeadDim + 8 * chunk + (lane & 8 ? 4 : 0) + (lane & 4 ? 2 : 0);
-      p[0] += v[0];
-      p[1] += v[1];
-    }
-    x = xn;
-    g = gn;
-    pass = next_pass;
-    tile = next_tile;
   }
   __syncthreads();
   const int rows = norm_part_rows(a);
   float* out = a.part + static_cast<int64_t>(blockIdx.x) * rows * kHeadDim;
   for (int y = threadIdx.x; y < rows * kHeadDim; y += kThreads) {
     const int row = y / kHeadDim, d = y % kHeadDim;
-    float sum = 0.0f;
-    if (a.per_head) {
-      sum = acc[2 * row * kHeadDim + d] + acc[(2 * row + 1) * kHeadDim + d];
-    } else {
-#pragma unroll
-      for (int z = 0; z < 2 * kPass; ++z) sum += acc[(2 * kPass * row + z) * kHeadDim + d];
-    }
-    out[y] = sum;
+    float total = 0.0f;
+    const int from = a.per_head ? row : kPass * row, n = a.per_head ? 1 : kPass;
+    for (int z = from; z < from + n; ++z) total += acc[z * kHeadDim + d];
+    out[y] = total;
   }
 }
 
-// One block a row of the weights' gradients: the CTAs' sums, in 64 bits.
+// Sum with the rounding errors carried along (TwoSum).
+__device__ __forceinline__ void add_carried(float& sum, float& err, float x) {
+  const float t = sum + x, z = t - sum;
+  err += (sum - (t - z)) + (x - z);
+  sum = t;
+}
+
+constexpr int kFinishDims = 16;  // of a block
+
+// A block takes 16 places of a row of the weights' gradients: the CTAs' sums, as if in 48
+// bits (fp64 would take 10 us here).
 __global__ void __launch_bounds__(kFinishThreads) bam_qk_norm_finish_kernel(const NormArgs a) {
-  __shared__ double sums[kFinishThreads];
+  __shared__ float2 sums[kFinishThreads];
   grid_dep_wait();
-  const int H = a.side[0].heads, d = threadIdx.x % kHeadDim, group = threadIdx.x / kHeadDim;
-  constexpr int kGroups = kFinishThreads / kHeadDim;
+  constexpr int kBlocks = kHeadDim / kFinishDims, kGroups = kFinishThreads / kFinishDims;
+  const int out = blockIdx.x / kBlocks;  // row of the weights: queries' first
+  const int d = blockIdx.x % kBlocks * kFinishDims + threadIdx.x % kFinishDims;
+  const int group = threadIdx.x / kFinishDims, H = a.side[0].heads;
   const int rows = norm_part_rows(a);
-  const int hh = blockIdx.x;  // the head, or q or k
-  const int part = a.per_head ? hh / a.heads : 0, step = a.per_head ? a.parts : 1;
-  const int row = a.per_head ? hh % a.heads : hh;
-  double sum = 0.0;
-#pragma unroll 4
+  const int k = out >= (a.per_head ? H : 1);  // side, and the head of its weights
+  const int h = a.per_head ? out - (k ? H : 0) : 0;
+  const int pass = (k ? (H + kPass - 1) / kPass : 0) + h / kPass;
+  const int part = a.per_head ? pass / a.passes : 0, step = a.per_head ? a.parts : 1;
+  const int row = a.per_head ? kPass * (pass % a.passes) + h % kPass : k;
+  float sum = 0.0f, err = 0.0f;
+#pragma unroll 8
   for (int c = part + group * step; c < a.ctas; c += kGroups * step)
-    sum += a.part[(static_cast<int64_t>(c) * rows + row) * kHeadDim + d];
-  sums[threadIdx.x] = sum;
+    add_carried(sum, err, a.part[(static_cast<int64_t>(c) * rows + row) * kHeadDim + d]);
+  // a warp's two groups, then the warps' sums
+  add_carried(sum, err, __shfl_down_sync(0xffffffffu, sum, kFinishDims));
+  err += __shfl_down_sync(0xffffffffu, err, kFinishDims);
+  sums[threadIdx.x] = make_float2(sum, err);
   __syncthreads();
   if (group == 0) {
-    for (int y = 1; y < kGroups; ++y) sum += sums[y * kHeadDim + d];
-    const int k = a.per_head ? hh >= H : hh;
-    const int h = a.per_head ? (hh >= H ? hh - H : hh) : 0;
-    a.side[k].dw[h * kHeadDim + d] = static_cast<float>(sum);
+#pragma unroll 8
+    for (int y = 2; y < kGroups; y += 2) {
+      const float2 x = sums[y * kFinishDims + threadIdx.x];
+      add_carried(sum, err, x.x);
+      err += x.y;
+    }
+    a.side[k].dw[h * kHeadDim + d] = sum + err;
   }
 }
 
-int round4(int x) { return (x + kPass - 1) / kPass * kPass; }
+// A launch of at most `resident` CTAs an SM: as many passes a part as leave every CTA
+// a part of a tile, so that angles serve many heads.
+void split_passes(NormArgs* a, int slots, int sms, int resident, int most_ctas) {
+  int all = 0;
+  for (int k = 0; k < 2; ++k) all += (a->side[k].heads + kPass - 1) / kPass;
+  const int64_t tiles = (static_cast<int64_t>(a->tokens) + 8 * slots - 1) / (8 * slots);
+  int most = resident * sms;
+  if (most > most_ctas) most = most_ctas;
+  if (most < 1) most = 1;
+  a->passes = all < kNormMaxPasses ? all : kNormMaxPasses;
+  while (a->passes > 1 && tiles * ((all + a->passes - 1) / a->passes) < most)
+    a->passes = (a->passes + 1) / 2;
+  a->parts = (all + a->passes - 1) / a->passes;
+  int64_t each = most / a->parts;
+  if (each > tiles) each = tiles;
+  if (each < 1) each = 1;
+  each = (tiles + (tiles + each - 1) / each - 1) / ((tiles + each - 1) / each);  // no more than the longest needs
+  a->ctas = static_cast<unsigned>(each) * a->parts;
+}
+
+typedef void (*Kernel)(NormArgs);
+template <class Off>
+constexpr Kernel fwd_kernel[] = {bam_qk_norm_fwd_kernel<kNoTurn, Off>,
+                                 bam_qk_norm_fwd_kernel<kHalves, Off>, bam_qk_norm_fwd_kernel<kPairs, Off>};
+template <class Off>
+constexpr Kernel bwd_kernel[] = {bam_qk_norm_bwd_kernel<kNoTurn, Off>,
+                                 bam_qk_norm_bwd_kernel<kHalves, Off>, bam_qk_norm_bwd_kernel<kPairs, Off>};
+Kernel pick_kernel(const NormArgs& a, const Kernel (&small)[3], const Kernel (&large)[3]) {
+  const int turn = a.rope.dims == 0 ? kNoTurn : a.rope.interleaved ? kPairs : kHalves;
+  return a.large ? large[turn] : small[turn];
+}
 
 }  // namespace
 
 cudaError_t launch_norm_fwd(const NormArgs& args, cudaStream_t st) {
   NormArgs a = args;
-  const int all = a.side[0].heads + a.side[1].heads, most = kPass * kFwdRows;
-  a.parts = (all + most - 1) / most;
-  a.heads = round4((all + a.parts - 1) / a.parts);
-  a.parts = (all + a.heads - 1) / a.heads;
-  const int64_t units = (a.tokens + kTokens - 1) / kTokens * a.parts;
-  if (units > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  return launch_k(bam_qk_norm_fwd_kernel, dim3(static_cast<unsigned>(units)), dim3(kThreads), 0, st,
-                  false, a);
+  split_passes(&a, kFwdSlots, sm_count(), kFwdResident, 1 << 30);
+  return launch_k(pick_kernel(a, fwd_kernel<uint32_t>, fwd_kernel<uint64_t>), dim3(a.ctas),
+                  dim3(kThreads), 0, st, false, a);
 }
 
-void norm_bwd_config(NormArgs* a, int sms) {
-  const int all = a->side[0].heads + a->side[1].heads;
-  const int64_t tiles = (a->tokens + kTokens - 1) / kTokens;
-  int most = 2 * sms;
-  if (most > kNormMaxCtas) most = kNormMaxCtas;
-  // As many heads a unit as leave every CTA a few units.
-  a->heads = round4(all < kNormMaxHeads ? all : kNormMaxHeads);
-  while (a->heads > kPass && tiles * ((all + a->heads - 1) / a->heads) < 2 * most)
-    a->heads = round4(a->heads / 2);
-  a->parts = (all + a->heads - 1) / a->heads;
-  int64_t per_part = most / a->parts;
-  if (per_part > tiles) per_part = tiles;
-  if (per_part < 1) per_part = 1;
-  a->ctas = static_cast<int>(per_part) * a->parts;
-}
+void norm_bwd_config(NormArgs* a, int sms) { split_passes(a, kBwdSlots, sms, kBwdResident, kNormMaxCtas); }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t st) {
-  const size_t smem = static_cast<size_t>(a.per_head ? a.heads : 2 * kPass) * 2 * kHeadDim * 4;
-  return launch_k(bam_qk_norm_bwd_kernel, dim3(a.ctas), dim3(kThreads), smem, st, false, a);
+  const size_t smem = static_cast<size_t>(kPass * (a.per_head ? a.passes : 2)) * kHeadDim * 4;
+  return launch_k(pick_kernel(a, bwd_kernel<uint32_t>, bwd_kernel<uint64_t>), dim3(a.ctas),
+                  dim3(kThreads), smem, st, false, a);
 }
 
 cudaError_t launch_norm_bwd_finish(const NormArgs& a, cudaStream_t st) {
   const int rows = a.per_head ? a.side[0].heads + a.side[1].heads : 2;
-  return launch_k(bam_qk_norm_finish_kernel, dim3(rows), dim3(kFinishThreads), 0, st, true, a);
+  return launch_k(bam_qk_norm_finish_kernel, dim3(rows * (kHeadDim / kFinishDims)), dim3(kFinishThreads), 0, st, true, a);
 }
 
 }  // namespace bam

@@ -12,9 +12,32 @@ struct NormSide {
   uint16_t* y;         // output, or the gradient of x
   const float* w;      // [64] or [heads, 64]
   float* dw;           // backward
-  int64_t xs[3], gs[3], ys[3];  // element strides over batch, head, token
+  int64_t xs[3], gs[3], ys[3];  // strides over batch, head, token, in 16-byte words
   int heads;
 };
+
+// Division of 32-bit numbers by a divisor that the host knows: the quotient is
+// (t + (n - t >> s1)) >> s2 with t the high word of n times `factor` (Granlund and
+// Montgomery, "Division by invariant integers using multiplication").
+struct Divisor {
+  unsigned factor;
+  int s1, s2;
+};
+inline Divisor divisor_of(unsigned d) {
+  int l = 0;
+  while (l < 32 && (1ull << l) < d) ++l;
+  Divisor x;
+  x.factor = static_cast<unsigned>((((1ull << l) - d) << 32) / d + 1);
+  x.s1 = l < 1 ? l : 1;
+  x.s2 = l < 1 ? 0 : l - 1;
+  return x;
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ unsigned divide(unsigned n, const Divisor& d) {
+  const unsigned t = __umulhi(n, d.factor);
+  return (t + ((n - t) >> d.s1)) >> d.s2;
+}
+#endif
 
 struct NormArgs {
   NormSide side[2];
@@ -23,22 +46,27 @@ struct NormArgs {
   unsigned tokens;       // B * T
   float eps;
   unsigned T;
+  Divisor by_T;
   int per_head;
-  int heads;             // of a unit: q then k heads, a multiple of 4
-  int parts;             // units of a token tile
-  int ctas;              // backward: CTAs of the launch, a multiple of parts
+  int large;             // some place needs more than 32 bits
+  int passes;            // of a part, eight heads each: the queries' and then the keys'
+  unsigned parts;        // of a tile's passes
+  unsigned ctas;         // of the launch, a multiple of parts
   RopeArgs rope;
 };
 
+constexpr int kNormPass = 4;  // heads of a pass
 // Rows of a CTA's sums of the weights' gradients: its heads, or q and k.
-__host__ __device__ inline int norm_part_rows(const NormArgs& a) { return a.per_head ? a.heads : 2; }
+__host__ __device__ inline int norm_part_rows(const NormArgs& a) {
+  return a.per_head ? kNormPass * a.passes : 2;
+}
 
-// The most CTAs of a backward launch and the most heads of its units.
-constexpr int kNormMaxCtas = 152 * 3;
-constexpr int kNormMaxHeads = 64;
+// The most CTAs of a backward launch and the most passes of a part.
+constexpr int kNormMaxCtas = 152 * 16 / kNormPass;
+constexpr int kNormMaxPasses = 64 / kNormPass;
 
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t st);
-// Chooses heads, parts and ctas for `sms` SMs.
+// Chooses passes, parts and CTAs for `sms` SMs.
 void norm_bwd_config(NormArgs* a, int sms);
 cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_norm_bwd_finish(const NormArgs& a, cudaStream_t st);

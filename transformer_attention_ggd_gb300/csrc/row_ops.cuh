@@ -75,31 +75,145 @@ __device__ __forceinline__ float row_sum(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
+constexpr float kBigSquares = 1e38f;
+constexpr float kDownScale = 0x1p-68f;
+
+// How a lane's two chunks of 8 values are turned: not at all, as pairs (x_f,
+// x_{f + dims/2}) that lie across them, or as neighbouring pairs inside each.
+enum : int { kNoTurn = 0, kHalves = 1, kPairs = 2 };
+
+// A lane's 16 values as f32x2 pairs.
+typedef uint64_t F2x8[8];
+__device__ __forceinline__ void unpack_row(const uint4* v, F2x8& f) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[4 * c + i] = f2_pack(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
+  }
+}
+__device__ __forceinline__ void pack_row(const F2x8& f, uint4* v) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      f2_unpack(f[4 * c + i], lo, hi);
+      x[i] = pack_bf16x2(lo, hi);
+    }
+    v[c] = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+}
+__device__ __forceinline__ uint64_t f2_both(float x) { return f2_pack(x, x); }
+__device__ __forceinline__ float f2_sum(uint64_t x) {
+  float lo, hi;
+  f2_unpack(x, lo, hi);
+  return lo + hi;
+}
+// One of the four lanes of a row: its two chunks of 8 values (where it can, one of the
+// row's first and one of its last four: an access then covers 64 bytes of the row.
+// Chunks side by side took twice the sectors: 164 instead of 139 us forward, 4 x 16383
+// tokens, 40 heads), and which of them are turned (kHalves: turn0 for both).
+struct RowLane {
+  int u4, c0, c1;
+  bool turn0, turn1;
+};
+template <int kTurn>
+__device__ __forceinline__ RowLane row_lane(int u4, int dims) {
+  RowLane l = {u4, u4, u4 + 4, false, false};
+  if (kTurn == kHalves) {
+    const int nh = dims / 16;
+    l.turn0 = u4 < nh;
+    l.c0 = l.turn0 ? u4 : 2 * u4;
+    l.c1 = l.turn0 ? u4 + nh : 2 * u4 + 1;
+  }
+  if (kTurn == kPairs) {
+    l.turn0 = 8 * l.c0 < dims;
+    l.turn1 = 8 * l.c1 < dims;
+  }
+  return l;
+}
+
+// Turns a lane's values by its token's angles, 32 cosines and 32 sines in shared memory
+// (they are read for every row: in registers they would take 32).
+template <int kTurn>
+__device__ __forceinline__ void turn_values(F2x8& f, const float* cos, const float* sin,
+                                            const RowLane& l) {
+  if (kTurn == kHalves) {
+    if (!l.turn0) return;
+    const float* pc = cos + 8 * l.u4;
+    const float* ps = sin + 8 * l.u4;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      uint64_t c[2], s[2];
+      ld_f2x2(pc + 2 * i, c[0], c[1]);
+      ld_f2x2(ps + 2 * i, s[0], s[1]);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const uint64_t x0 = f[i + y], x1 = f[4 + i + y];
+        f[i + y] = ffma2(x1, s[y] ^ 0x8000000080000000ull, fmul2(x0, c[y]));
+        f[4 + i + y] = ffma2(x0, s[y], fmul2(x1, c[y]));
+      }
+    }
+  }
+  if (kTurn == kPairs) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!(h ? l.turn1 : l.turn0)) continue;
+      const float4 c = *reinterpret_cast<const float4*>(cos + 4 * (h ? l.c1 : l.c0));
+      const float4 s = *reinterpret_cast<const float4*>(sin + 4 * (h ? l.c1 : l.c0));
+      const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        float x0, x1;
+        f2_unpack(f[4 * h + y], x0, x1);
+        turn(x0, x1, cv[y], sv[y]);
+        f[4 * h + y] = f2_pack(x0, x1);
+      }
+    }
+  }
+}
+
 // 1 / sqrt(mean(x^2) + eps) of each row, by whole warps.  A row whose squares
 // leave fp32 (values above 1e18) is scaled by 2^-68 first; the values in f are
 // then scaled too and *scale is 2^-68, else 1: f * result is the normalised row
 // either way, and result * *scale is 1 / rms.
-__device__ __forceinline__ float row_rms_inv(float (&f)[16], float eps, float* scale) {
-  float ss = 0.0f;
+__device__ __forceinline__ float row_rms_inv(F2x8& f, float eps, float* scale) {
+  uint64_t s0 = fmul2(f[0], f[0]), s1 = fmul2(f[1], f[1]);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) ss = fmaf(f[i], f[i], ss);
-  ss = row_sum(ss);
+  for (int i = 2; i < 8; i += 2) {
+    s0 = ffma2(f[i], f[i], s0);
+    s1 = ffma2(f[i + 1], f[i + 1], s1);
+  }
+  float ss = row_sum(f2_sum(fadd2(s0, s1)));
   *scale = 1.0f;
-  const bool big = ss > 1e38f;
+  const bool big = ss > kBigSquares;
   if (__any_sync(0xffffffffu, big)) {
-    constexpr float kDown = 3.3881317890172014e-21f;  // 2^-68
-    const float down = big ? kDown : 1.0f;
-    float s2 = 0.0f;
+    const float down = big ? kDownScale : 1.0f;
+    const uint64_t d2 = f2_both(down);
+    uint64_t s2 = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      f[i] *= down;
-      s2 = fmaf(f[i], f[i], s2);
+    for (int i = 0; i < 8; ++i) {
+      f[i] = fmul2(f[i], d2);
+      s2 = ffma2(f[i], f[i], s2);
     }
-    ss = row_sum(s2);
+    ss = row_sum(f2_sum(s2));
     eps *= down * down;
     *scale = down;
   }
   return rsqrtf(ss * (1.0f / kHeadDim) + eps);
+}
+
+// A row's weights.
+__device__ __forceinline__ void load_weight(const float* p, const RowLane& l, F2x8& w) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const float* q = p + 8 * (c ? l.c1 : l.c0);
+    ld_f2x2(q, w[4 * c], w[4 * c + 1]);
+    ld_f2x2(q + 4, w[4 * c + 2], w[4 * c + 3]);
+  }
 }
 
 #endif  // __CUDACC__
