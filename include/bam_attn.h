@@ -373,16 +373,18 @@ bam_status bam_kv_append_norm_paged(const void* k, const void* v, const void* q,
  *     decay * key_weight + sum over the group's heads of exp(z - lse),
  *
  * 0 <= decay <= 1, while the prefix gathers nothing.  Scalable-Softmax's n is
- * the query's position + 1.  Prefix lengths, cache lengths and q_pos out of
- * range are clamped, a key behind the query counts as at the query's position,
+ * the query's position + 1.  Prefix lengths, cache lengths and q_pos (at least
+ * P - 1) out of range are clamped, a key behind the query counts as at its position,
  * and a page number out of range reads page 0; all are reported by
  * bam_attn_check_status as BAM_ERR_INVALID_ARG.  Sequences with marks share
  * own pages with no other sequence of the call.
  *
  * What lies behind a sequence's keys has no effect, whatever it holds.  A NaN
  * in a key reaches o, lse and the weights of its head; NaN and infinities in a
- * value reach o.  Products and weights are summed in fp32, the weights of the
- * product with V as sums of bf16 parts (16 bits for bf16 output, 24 for fp32).
+ * value reach o (an infinity of the prefix as itself or as NaN).  Products and
+ * weights are summed in fp32; the weights enter the product with V as sums of
+ * bf16 parts: 24 bits for fp32 output; for bf16 output 16, or 8 over a prefix
+ * that more than 16 rows of a key head share.
  * If a device wait of the call gives up, o and lse are written as NaN and no
  * weight changes.  o: [B, H, D], fp32 when o_fp32 != 0, else bf16; lse: fp32
  * [B, H] or NULL.  p->causal is ignored.  Every output is bitwise repeatable. */
@@ -558,7 +560,8 @@ enum {
   BAM_KERNEL_SHARED_WEIGH = 18,   /* accumulated weights                    */
   BAM_KERNEL_EVICT_SELECT = 19,
   BAM_KERNEL_EVICT_MOVE = 20,
-  BAM_KERNEL_COUNT = 21
+  BAM_KERNEL_PREFIX = 21,         /* shared decode: the prefix in tiles     */
+  BAM_KERNEL_COUNT = 22
 };
 
 /* Instrumentation: while set, every launch of kernel `which` is bracketed

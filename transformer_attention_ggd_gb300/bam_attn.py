@@ -65,7 +65,8 @@ BAM_KERNEL_SHARED_JOIN = 17
 BAM_KERNEL_SHARED_WEIGH = 18
 BAM_KERNEL_EVICT_SELECT = 19
 BAM_KERNEL_EVICT_MOVE = 20
-BAM_KERNEL_COUNT = 21
+BAM_KERNEL_PREFIX = 21
+BAM_KERNEL_COUNT = 22
 
 # Every symbol that include/bam_attn.h declares.
 EXPORTED = (

@@ -24,7 +24,7 @@ LIB = os.path.join(BUILD, "libbam_attn.so")
 DEBUG_BUILD = os.path.join(BUILD, "debug")
 DEBUG_LIB = os.path.join(BUILD, "libbam_attn_debug.so")
 SOURCES = ["api.cu", "table.cu", "fwd.cu", "bwd.cu", "decode.cu", "decode_noalloc.cu",
-           "cache.cu", "tree.cu", "norm.cu", "shared.cu", "evict.cu", "selftest.cu"]
+           "cache.cu", "tree.cu", "norm.cu", "shared.cu", "prefix.cu", "evict.cu", "selftest.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          f"-I{os.path.join(ROOT, 'include')}"]

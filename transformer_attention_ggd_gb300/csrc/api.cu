@@ -312,7 +312,7 @@ size_t norm_ws(int H, int Hkv) {
 }
 
 struct SharedWs {
-  size_t ml, part, z, total;
+  size_t ml, part, z, table, total;
 };
 SharedWs shared_ws(const SharedArgs& a, bool marked) {
   SharedWs w;
@@ -320,7 +320,10 @@ SharedWs shared_ws(const SharedArgs& a, bool marked) {
   w.ml = kStatusBytes;
   w.part = w.ml + align256(rows * a.slots * 8);
   w.z = w.part + align256(rows * a.slots * kHeadDim * 4);
-  w.total = w.z + (marked ? align256(rows * a.zstride * 4) : 0);
+  w.table = w.z + (marked ? align256(rows * a.zstride * 4) : 0);
+  w.total = w.table;
+  if (a.copies)
+    w.total += align256((kTabCopies * static_cast<size_t>(a.H) * a.tab_len + kTabPadFloats) * 4);
   return w;
 }
 
@@ -786,9 +789,14 @@ bam_status bam_attn_decode_shared_paged(const void* q, const void* k_pages, cons
   a.lse = lse;
   a.ml = reinterpret_cast<float2*>(wsb + w.ml);
   a.part = reinterpret_cast<float*>(wsb + w.part);
+  if (a.copies) a.table = reinterpret_cast<float*>(wsb + w.table);
   cudaError_t e =
       launch_kernel(BAM_KERNEL_SHARED_PREP, stream, [&] { return launch_shared_prep(a, stream); });
   if (e != cudaSuccess) return BAM_ERR_CUDA;
+  if (a.copies) {
+    e = launch_kernel(BAM_KERNEL_PREFIX, stream, [&] { return launch_prefix(tk, tv, a, stream); });
+    if (e != cudaSuccess) return BAM_ERR_CUDA;
+  }
   e = launch_kernel(BAM_KERNEL_SHARED, stream, [&] { return launch_shared(tk, tv, a, stream); });
   if (e != cudaSuccess) return BAM_ERR_CUDA;
   e = launch_kernel(BAM_KERNEL_SHARED_JOIN, stream, [&] { return launch_shared_join(a, stream); });

@@ -59,33 +59,39 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Committed length of sequence b and of the prefix, clamped.
-__device__ __forceinline__ int own_len(const SharedArgs& a, int b, bool* ok) {
-  const int cap = a.c.page * a.c.max_blocks, raw = __ldg(a.c.lens + b);
-  const int len = min(max(raw, 0), cap);
-  *ok &= raw == len;
-  return len;
-}
-__device__ __forceinline__ int prefix_len(const SharedArgs& a, bool* ok) {
-  if (!a.prefix_table) return 0;
-  const int cap = a.c.page * a.prefix_blocks, raw = __ldg(a.prefix_len);
-  const int len = min(max(raw, 0), cap);
-  *ok &= raw == len;
-  return len;
-}
-// Position of the query of sequence b (-1 when there is no key at all).
-__device__ __forceinline__ int query_pos(const SharedArgs& a, int b, int P, bool* ok) {
-  if (a.q_pos) {
-    const int raw = __ldg(a.q_pos + b), pos = min(max(raw, 0), a.max_pos - 1);
-    *ok &= raw == pos;
-    return pos;
-  }
-  return P + own_len(a, b, ok) - 1;
-}
+constexpr int kPrepThreads = 256;
 
-__global__ void bam_shared_prep_kernel(const SharedArgs a) {
+// Starts the call and, for the prefix in tiles, fills the table over the distances that its
+// keys have from the queries.
+__global__ void __launch_bounds__(kPrepThreads) bam_shared_prep_kernel(const SharedArgs a) {
+  __shared__ int2 range;
   grid_dep_trigger();
-  if (blockIdx.x == 0 && threadIdx.x == 0) status_begin_call(a.c.status);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) status_begin_call(a.c.status);
+  if (!a.table) return;
+  bool ok = true;
+  const int P = prefix_len(a, &ok);
+  if (P == 0) return;
+  if (threadIdx.x == 0) range = make_int2(0x7FFFFFFF, -1);
+  __syncthreads();
+  int lo = 0x7FFFFFFF, hi = -1;
+  for (int b = threadIdx.x; b < a.c.B; b += kPrepThreads) {
+    const int pos = query_pos(a, b, P, &ok);
+    lo = min(lo, pos);
+    hi = max(hi, pos);
+  }
+  atomicMin(&range.x, lo);
+  atomicMax(&range.y, hi);
+  __syncthreads();
+  const int h = blockIdx.y, from = range.x - P + 1;
+  const float alpha = a.alpha[h], beta = a.beta[h], mu = a.mu[h];
+  for (int d = from + blockIdx.x * kPrepThreads + threadIdx.x; d <= range.y; d += gridDim.x * kPrepThreads) {
+    float b, g1, g2;
+    bias_terms<false>(d, alpha, beta, mu, a.eps, a.prior, &b, &g1, &g2);
+    b = to_f32_finite(b * static_cast<float>(kLog2e));
+#pragma unroll
+    for (int k = 0; k < kTabCopies; ++k)
+      a.table[(static_cast<int64_t>(k) * a.H + h) * a.tab_len + (a.tab_top - d) + k] = b;
+  }
 }
 
 // An item is up to 16 rows (the heads of one sequence that share a key head, or rows
@@ -100,18 +106,16 @@ __global__ void __launch_bounds__(kThreads) bam_shared_kernel(const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hkv = a.c.Hkv;
   // The item.
-  const int64_t prefix_rows = static_cast<int64_t>(a.c.B) * a.group;
-  const int pblocks = static_cast<int>((prefix_rows + kRows - 1) / kRows);
-  const int64_t pitems = static_cast<int64_t>(a.npsplit) * Hkv * pblocks;
+  const bool few = a.npsplit && a.copies == 0;  // the prefix's rows are one item's
+  const int64_t pitems = few ? static_cast<int64_t>(a.npsplit) * Hkv : 0;
   int64_t item = blockIdx.x;
   const bool prefix = item < pitems;
   int sp, hk, b = 0, r0, nrows;
   if (prefix) {
     sp = static_cast<int>(item % a.npsplit);
-    item /= a.npsplit;
-    r0 = static_cast<int>(item % pblocks) * kRows;
-    hk = static_cast<int>(item / pblocks);
-    nrows = static_cast<int>(min(static_cast<int64_t>(kRows), prefix_rows - r0));
+    hk = static_cast<int>(item / a.npsplit);
+    r0 = 0;
+    nrows = a.c.B * a.group;
   } else {
     item -= pitems;
     const int blocks = (a.group + kRows - 1) / kRows;
@@ -126,8 +130,8 @@ __global__ void __launch_bounds__(kThreads) bam_shared_kernel(const __grid_const
   bool ok_arg = true;
   const int P = prefix_len(a, &ok_arg);
   const int len = prefix ? P : own_len(a, b, &ok_arg);
-  const int kbeg = sp * (prefix ? a.pchunk : a.chunk);
-  const int kend = min(len, kbeg + (prefix ? a.pchunk : a.chunk));
+  const int chunk = prefix ? part_keys(len, a.npsplit, kPrefixLeast) : part_keys(len, a.nsplit, kOwnLeast);
+  const int kbeg = min(len, sp * chunk), kend = min(len, kbeg + chunk);
   const int nst = kend > kbeg ? (kend - kbeg + kKeys - 1) / kKeys : 0;
   const bool marked = !prefix && a.key_pos;
   volatile int* ab = &sm.abort_flag;
@@ -142,14 +146,14 @@ __global__ void __launch_bounds__(kThreads) bam_shared_kernel(const __grid_const
       r.alpha = __ldg(a.alpha + h);
       r.beta = __ldg(a.beta + h);
       r.mu = __ldg(a.mu + h);
-      const float c = a.ssmax ? __ldg(a.s + h) * logf(static_cast<float>(r.pos + 1)) : 1.0f;
-      r.c = c * (0.125f * 1.44269504088896341f);
+      r.c = shared_scale(a, h, r.pos);
       r.row = rb * a.H + h;
     }
     sm.rows[i] = r;
   }
   if (threadIdx.x == 0) {
-    grid_dep_wait();
+    // Behind the prefix in tiles: the kernel before has waited for the call's start.
+    if (!a.copies) grid_dep_wait();
     sm.abort_flag = *reinterpret_cast<volatile int*>(&a.c.status->abort);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.full[s], 1);
@@ -345,6 +349,8 @@ __global__ void __launch_bounds__(kThreads) bam_shared_kernel(const __grid_const
     if (bad_pos) record_bad_arg(a.c.status);
   }
   __syncthreads();
+  // The prefix's parts are written when this grid ends: the join waits for this grid alone.
+  if (a.copies && blockIdx.x == gridDim.x - 1) grid_dep_wait();
   grid_dep_trigger();
   if (*ab) return;
   // Join the four warps in the ring's memory: every copy into it has been waited for.
@@ -409,6 +415,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) bam_shared_join_kernel(const 
 #pragma unroll 4
   for (int s = warp; s < a.slots; s += kJoinWarps) {
     const float2 ml = a.ml[base + s];
+    if (ml.y == 0.0f) continue;  // no key, or no weight
     const float2 o = reinterpret_cast<const float2*>(a.part + (base + s) * kHeadDim)[lane];
     const float f = ex2_approx(ml.x - M);
     L += ml.y * f;
@@ -484,17 +491,26 @@ __global__ void __launch_bounds__(kWeighThreads) bam_shared_weigh_kernel(const S
 
 void shared_split(SharedArgs* a, int64_t Pmax, int64_t Tmax) {
   const int blocks = (a->group + kRows - 1) / kRows;
-  decode_split(a->c.B * a->c.Hkv * blocks, static_cast<int>(Tmax), &a->nsplit, &a->chunk);
-  a->npsplit = a->pchunk = 0;
+  int chunk;
+  decode_split(a->c.B * a->c.Hkv * blocks, static_cast<int>(Tmax), &a->nsplit, &chunk);
+  a->npsplit = a->copies = a->tab_len = 0;
   if (Pmax > 0) {
-    const int64_t pblocks = (static_cast<int64_t>(a->c.B) * a->group + kRows - 1) / kRows;
-    decode_split(static_cast<int>(a->c.Hkv * pblocks), static_cast<int>(Pmax), &a->npsplit, &a->pchunk);
+    if (static_cast<int64_t>(a->c.B) * a->group <= kFewRows)
+      decode_split(a->c.Hkv, static_cast<int>(Pmax), &a->npsplit, &chunk);
+    else
+      prefix_split(a, Pmax, Tmax);
   }
-  a->slots = a->nsplit + a->npsplit;
+  a->slots = a->nsplit + a->npsplit * (a->copies > 1 ? a->copies : 1);
 }
 
 cudaError_t launch_shared_prep(const SharedArgs& a, cudaStream_t st) {
-  return launch_k(bam_shared_prep_kernel, dim3(1), dim3(32), 0, st, false, a);
+  dim3 grid(1, 1);
+  if (a.table) {
+    const int64_t blocks = (static_cast<int64_t>(a.tab_top) + kPrepThreads) / kPrepThreads;
+    const int64_t most = (8 * sm_count() + a.H - 1) / a.H;
+    grid = dim3(static_cast<unsigned>(blocks < most ? blocks : most), a.H);
+  }
+  return launch_k(bam_shared_prep_kernel, grid, dim3(kPrepThreads), 0, st, false, a);
 }
 
 template <bool kTwo, int kParts>
@@ -511,11 +527,11 @@ cudaError_t launch_main(const CUtensorMap& tk, const CUtensorMap& tv, const Shar
 cudaError_t launch_shared(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArgs& a,
                           cudaStream_t st) {
   const int blocks = (a.group + kRows - 1) / kRows;
-  const int64_t rows = static_cast<int64_t>(a.c.B) * a.group;
+  const bool few = a.npsplit && a.copies == 0;
   const int64_t items = static_cast<int64_t>(a.nsplit) * a.c.B * a.c.Hkv * blocks +
-                        static_cast<int64_t>(a.npsplit) * a.c.Hkv * ((rows + kRows - 1) / kRows);
+                        (few ? static_cast<int64_t>(a.npsplit) * a.c.Hkv : 0);
   if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const bool two = a.group > 8 || (a.npsplit && rows > 8);
+  const bool two = a.group > 8 || (few && a.c.B * a.group > 8);
   if (a.o_fp32)
     return two ? launch_main<true, 3>(tk, tv, a, items, st) : launch_main<false, 3>(tk, tv, a, items, st);
   return two ? launch_main<true, 2>(tk, tv, a, items, st) : launch_main<false, 2>(tk, tv, a, items, st);

@@ -30,13 +30,59 @@ struct SharedArgs {
   float* part;               // [B * H, slots, 64]: its unnormalised output
   float* z;                  // [B, H, zstride] logits (log2 units) of own keys, with key_pos
   int H, group;
-  int nsplit, chunk;         // parts of the own keys, keys of a part
-  int npsplit, pchunk;       // of the prefix
-  int slots;                 // nsplit + npsplit
+  int nsplit;                // parts of a sequence's own keys
+  int npsplit;               // of the prefix
+  int copies;                // of a row, each with its part of a tile's keys; 0: few rows, no tiles
+  int slots;                 // of a row: nsplit + npsplit * max(copies, 1)
   int64_t zstride;           // max_blocks * page
+  // Tiles: the table of b_h(d) log2(e).  Entry y of copy k of head h, at
+  // [(k * H + h) * tab_len + y + k], holds d = tab_top - y.
+  float* table;
+  int tab_top, tab_len;
 };
 
+// Keys of part `sp` of `parts` of n keys: whole tiles of 64, `least` at least.
+__host__ __device__ inline int part_keys(int n, int parts, int least) {
+  const int each = (n + parts - 1) / parts;
+  return ((each > least ? each : least) + 63) / 64 * 64;
+}
+constexpr int kOwnLeast = 256;    // keys of a part of own keys, at least
+constexpr int kPrefixLeast = 128; // and of the prefix
+constexpr int kFewRows = 16;      // of a key head over the prefix, at most, without tiles
+
 constexpr float kNoMax = -3.4e38f;  // below every logit (the bias is clamped at -3e38)
+
+#ifdef __CUDACC__
+// Own length of sequence b and length of the prefix, clamped.
+__device__ __forceinline__ int own_len(const SharedArgs& a, int b, bool* ok) {
+  const int cap = a.c.page * a.c.max_blocks, raw = __ldg(a.c.lens + b);
+  const int len = min(max(raw, 0), cap);
+  *ok &= raw == len;
+  return len;
+}
+__device__ __forceinline__ int prefix_len(const SharedArgs& a, bool* ok) {
+  if (!a.prefix_table) return 0;
+  const int cap = a.c.page * a.prefix_blocks, raw = __ldg(a.prefix_len);
+  const int len = min(max(raw, 0), cap);
+  *ok &= raw == len;
+  return len;
+}
+// Position of the query of sequence b (-1 when there is no key at all), not before the
+// prefix's last key.
+__device__ __forceinline__ int query_pos(const SharedArgs& a, int b, int P, bool* ok) {
+  if (a.q_pos) {
+    const int raw = __ldg(a.q_pos + b), pos = max(min(raw, a.max_pos - 1), max(P - 1, 0));
+    *ok &= raw == pos;
+    return pos;
+  }
+  return P + own_len(a, b, ok) - 1;
+}
+// Logit scale of head h at position pos, log2 units.
+__device__ __forceinline__ float shared_scale(const SharedArgs& a, int h, int pos) {
+  const float c = a.ssmax ? __ldg(a.s + h) * logf(static_cast<float>(pos + 1)) : 1.0f;
+  return c * (0.125f * 1.44269504088896341f);
+}
+#endif
 
 struct EvictArgs {
   CacheArgs c;
@@ -58,8 +104,12 @@ cudaError_t launch_shared(const CUtensorMap& tk, const CUtensorMap& tv, const Sh
                           cudaStream_t st);
 cudaError_t launch_shared_join(const SharedArgs& a, cudaStream_t st);
 cudaError_t launch_shared_weigh(const SharedArgs& a, cudaStream_t st);
-// Splits of the own and prefix keys; fills nsplit, chunk, npsplit, pchunk, slots.
+cudaError_t launch_prefix(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArgs& a,
+                          cudaStream_t st);
+// Splits of the own and prefix keys and the table's size; fills nsplit, npsplit, copies,
+// slots, tab_top, tab_len.
 void shared_split(SharedArgs* a, int64_t Pmax, int64_t Tmax);
+void prefix_split(SharedArgs* a, int64_t Pmax, int64_t Tmax);
 
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st);
 cudaError_t launch_evict_move(const EvictArgs& a, cudaStream_t st);
