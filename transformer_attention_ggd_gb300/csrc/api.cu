@@ -322,8 +322,8 @@ SharedWs shared_ws(const SharedArgs& a, bool marked) {
   w.z = w.part + align256(rows * a.slots * kHeadDim * 4);
   w.table = w.z + (marked ? align256(rows * a.zstride * 4) : 0);
   w.total = w.table;
-  if (a.copies)
-    w.total += align256((kTabCopies * static_cast<size_t>(a.H) * a.tab_len + kTabPadFloats) * 4);
+  if (a.use_table)
+    w.total += align256(((a.copies ? kTabCopies : 1) * static_cast<size_t>(a.H) * a.tab_len + kTabPadFloats) * 4);
   return w;
 }
 
@@ -342,6 +342,8 @@ bam_status check_shared(int64_t B, int64_t H, int64_t Hkv, int64_t Pmax, int64_t
   a->max_pos = static_cast<int>(max_pos);
   a->zstride = (Tmax + 63) / 64 * 64;
   shared_split(a, Pmax, Tmax);
+  // (windows are found by 32 bits of 16-byte words)
+  if (a->copies && static_cast<int64_t>(a->H) * a->tab_len > INT64_C(0x7FFFFFFF)) return BAM_ERR_UNSUPPORTED;
   return BAM_OK;
 }
 
@@ -759,9 +761,12 @@ bam_status bam_attn_decode_shared_paged(const void* q, const void* k_pages, cons
     return s;
   const SharedWs w = shared_ws(a, marks != nullptr);
   if ((s = check_ws(ws, ws_bytes, w.total)) != BAM_OK) return s;
-  CUtensorMap tk, tv;
-  if (!encode_rows(&tk, k_pages, num_pages * Hkv, page, 64) ||
-      !encode_rows(&tv, v_pages, num_pages * Hkv, page, 64))
+  // Pages in boxes of 32 keys, and of a tile of 64 for the prefix.
+  CUtensorMap tk, tv, tk64, tv64;
+  if (!encode_rows(&tk, k_pages, num_pages * Hkv, page, 32) ||
+      !encode_rows(&tv, v_pages, num_pages * Hkv, page, 32) ||
+      (a.copies && (!encode_rows(&tk64, k_pages, num_pages * Hkv, page, 64) ||
+                    !encode_rows(&tv64, v_pages, num_pages * Hkv, page, 64))))
     return BAM_ERR_CUDA;
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   a.c = CacheArgs{block_table, cache_lens, nullptr, nullptr, static_cast<DevStatus*>(ws),
@@ -789,12 +794,12 @@ bam_status bam_attn_decode_shared_paged(const void* q, const void* k_pages, cons
   a.lse = lse;
   a.ml = reinterpret_cast<float2*>(wsb + w.ml);
   a.part = reinterpret_cast<float*>(wsb + w.part);
-  if (a.copies) a.table = reinterpret_cast<float*>(wsb + w.table);
+  if (a.use_table) a.table = reinterpret_cast<float*>(wsb + w.table);
   cudaError_t e =
       launch_kernel(BAM_KERNEL_SHARED_PREP, stream, [&] { return launch_shared_prep(a, stream); });
   if (e != cudaSuccess) return BAM_ERR_CUDA;
   if (a.copies) {
-    e = launch_kernel(BAM_KERNEL_PREFIX, stream, [&] { return launch_prefix(tk, tv, a, stream); });
+    e = launch_kernel(BAM_KERNEL_PREFIX, stream, [&] { return launch_prefix(tk64, tv64, a, stream); });
     if (e != cudaSuccess) return BAM_ERR_CUDA;
   }
   e = launch_kernel(BAM_KERNEL_SHARED, stream, [&] { return launch_shared(tk, tv, a, stream); });

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
   const int rb = blockIdx.x / a.npsplit % blocks, hk = blockIdx.x / a.npsplit / blocks;
   bool ok_arg = true;
   const int P = prefix_len(a, &ok_arg);
-  const int chunk = part_keys(P, a.npsplit, kPrefixLeast);
+  const int chunk = part_keys(P, a.npsplit);
   const int kbeg = min(P, sp * chunk), kend = min(P, kbeg + chunk);
   const int tiles = (kend - kbeg + kTile - 1) / kTile;
   const int64_t row0 = static_cast<int64_t>(rb) * S::kRows;
@@ -169,24 +169,33 @@ __global__ void __launch_bounds__(kThreads, kResident)
     // ------------------------------------------------------------ copies
     constexpr int kChunks = kCols / 4, kStep = 32 / kChunks;  // 16-byte words of a window; windows at a time
     const int chunk = lane % kChunks;
-    const uint4* table = reinterpret_cast<const uint4*>(a.table) + chunk;
+    const uint4* src = reinterpret_cast<const uint4*>(a.table) + chunk;
+    uint32_t win[kLanes / kStep];
+#pragma unroll
+    for (int x = 0; x < kLanes / kStep; ++x) win[x] = bars.win[lane / kChunks + kStep * x];
+    const uint32_t dst = smem_u32(ring + 2 * kBoxBytes) + 16 * chunk + lane / kChunks * S::kWinStride * 4;
     bool bad_page = false;
-    int issued = 0;
+    int issued = 0, blk = kbeg / a.c.page, in = kbeg - blk * a.c.page;
+    int next = tiles ? __ldg(a.prefix_table + blk) : 0;  // the next tile's page, on its way
     for (int it = 0; it < tiles; ++it) {
       const int s = it % kStages;
       if (it >= kStages && !warp_wait(&bars.empty[s], (it / kStages - 1) & 1, status, ab, kSitePrefixProducer))
         break;
-      uint8_t* stage = ring + s * S::kStageBytes;
       if (lane == 0) {
-        const int kb = kbeg + it * kTile;
-        int pg = __ldg(a.prefix_table + kb / a.c.page);
+        uint8_t* stage = ring + s * S::kStageBytes;
+        int pg = next;
         if (pg < 0 || pg >= a.c.num_pages) {
           bad_page = true;
           pg = 0;
         }
         mbar_arrive_expect_tx(&bars.kv_full[s], 2 * kBoxBytes);
-        tma_load_3d(stage, &tk, &bars.kv_full[s], 0, kb % a.c.page, pg * a.c.Hkv + hk);
-        tma_load_3d(stage + kBoxBytes, &tv, &bars.kv_full[s], 0, kb % a.c.page, pg * a.c.Hkv + hk);
+        tma_load_3d(stage, &tk, &bars.kv_full[s], 0, in, pg * a.c.Hkv + hk);
+        tma_load_3d(stage + kBoxBytes, &tv, &bars.kv_full[s], 0, in, pg * a.c.Hkv + hk);
+        in += kTile;
+        if (in == a.c.page) {
+          in = 0;
+          if (it + 1 < tiles) next = __ldg(a.prefix_table + ++blk);
+        }
       }
       issued = it + 1;
       if (it == 0) {
@@ -194,18 +203,17 @@ __global__ void __launch_bounds__(kThreads, kResident)
         grid_dep_trigger();
       }
       __syncwarp();
-      const uint32_t dst = smem_u32(stage + 2 * kBoxBytes) + 16 * chunk;
-#pragma unroll 8
-      for (int row = lane / kChunks; row < kLanes; row += kStep) {
-        const uint4* src = table + bars.win[row] + it * (kTile / 4);
+#pragma unroll
+      for (int x = 0; x < kLanes / kStep; ++x) {
 #ifdef BAM_DEBUG
-        if (src + 1 > reinterpret_cast<const uint4*>(a.table) + static_cast<int64_t>(a.H) * a.tab_len) {
+        if (src + win[x] + 1 > reinterpret_cast<const uint4*>(a.table) + static_cast<int64_t>(a.H) * a.tab_len) {
           raise_error(status, ab, kSitePrefixTable, BAM_DEV_BOUNDS);
           continue;
         }
 #endif
-        copy16(dst + row * S::kWinStride * 4, src);
+        copy16(dst + s * S::kStageBytes + x * kStep * S::kWinStride * 4, src + win[x]);
       }
+      src += kTile / 4;
       arrive_copied(&bars.win_full[s]);
     }
     if (tiles == 0) {
@@ -388,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
         m = mx;
       }
       const uint64_t negm2 = f2_pack(-m, -m);
+      const uint64_t minus = f2_pack(-1.0f, -1.0f);
       uint64_t sum[2] = {0, 0};
       constexpr int kStep = kCols / 2 < 8 ? kCols / 2 : 8;  // pairs at a time
 #pragma unroll
@@ -400,19 +409,17 @@ __global__ void __launch_bounds__(kThreads, kResident)
           p0 = ex2_approx(p0);
           p1 = ex2_approx(p1);
           sum[y & 1] = fadd2(sum[y & 1], f2_pack(p0, p1));
-          // Parts but the last are cut off, and none is negative or, where the weight is not,
-          // zero (an infinite value then stays one: no inf - inf, no 0 * inf).
-          float least0 = p0 * 0x1p-28f, least1 = p1 * 0x1p-28f;
+          // Each part is the rounding of what the last left.
+          uint64_t left = f2_pack(p0, p1);
 #pragma unroll
-          for (int p = 0; p < kParts - 1; ++p) {
-            const uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
-            pk[p][y] = __byte_perm(w0, w1, 0x7632);
-            p0 = fmaxf(p0 - __uint_as_float(w0 & 0xFFFF0000u), least0);
-            p1 = fmaxf(p1 - __uint_as_float(w1 & 0xFFFF0000u), least1);
-            least0 *= 0x1p-8f;
-            least1 *= 0x1p-8f;
+          for (int p = 0; p < kParts; ++p) {
+            const uint32_t w = pack_bf16x2(p0, p1);
+            pk[p][y] = w;
+            if (p + 1 < kParts) {
+              left = ffma2(f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)), minus, left);
+              f2_unpack(left, p0, p1);
+            }
           }
-          pk[kParts - 1][y] = pack_bf16x2(p0, p1);
         }
 #pragma unroll
         for (int p = 0; p < kParts; ++p)
@@ -473,7 +480,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArg
 
 }  // namespace
 
-void prefix_split(SharedArgs* a, int64_t Pmax, int64_t Tmax) {
+void prefix_split(SharedArgs* a, int64_t Pmax) {
   const int64_t rows = static_cast<int64_t>(a->c.B) * a->group;
   a->copies = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
   const int64_t base = (rows * a->copies + kLanes - 1) / kLanes * a->c.Hkv;
@@ -482,17 +489,13 @@ void prefix_split(SharedArgs* a, int64_t Pmax, int64_t Tmax) {
   const int64_t ctas = 152 * kResident, tiles = (Pmax + kTile - 1) / kTile;
   int64_t best = INT64_MAX;
   a->npsplit = 1;
-  for (int64_t n = 1; n <= 2 * ctas && n * kPrefixLeast < Pmax + kPrefixLeast; ++n) {
+  for (int64_t n = 1; n <= 2 * ctas && n * kLeastKeys < Pmax + kLeastKeys; ++n) {
     const int64_t cost = (base * n + ctas - 1) / ctas * ((tiles + n - 1) / n + kItemCost);
     if (cost < best) {
       best = cost;
       a->npsplit = static_cast<int>(n);
     }
   }
-  // Distances of the prefix's keys, and behind them windows that reach past the last key.
-  const int64_t top = a->max_pos > 0 ? (a->max_pos > Pmax ? a->max_pos : Pmax) : Pmax + Tmax;
-  a->tab_top = static_cast<int>(top - 1);
-  a->tab_len = static_cast<int>((top + kTile + 8 + 63) / 64 * 64);
 }
 
 cudaError_t launch_prefix(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArgs& a,

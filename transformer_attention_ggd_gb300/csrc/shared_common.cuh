@@ -35,19 +35,18 @@ struct SharedArgs {
   int copies;                // of a row, each with its part of a tile's keys; 0: few rows, no tiles
   int slots;                 // of a row: nsplit + npsplit * max(copies, 1)
   int64_t zstride;           // max_blocks * page
-  // Tiles: the table of b_h(d) log2(e).  Entry y of copy k of head h, at
-  // [(k * H + h) * tab_len + y + k], holds d = tab_top - y.
+  // The table of b_h(d) log2(e), or null.  Entry y of copy k of head h, at
+  // [(k * H + h) * tab_len + y + k], holds d = tab_top - y.  One copy without tiles.
   float* table;
-  int tab_top, tab_len;
+  int tab_top, tab_len, use_table;
 };
 
-// Keys of part `sp` of `parts` of n keys: whole tiles of 64, `least` at least.
-__host__ __device__ inline int part_keys(int n, int parts, int least) {
-  const int each = (n + parts - 1) / parts;
-  return ((each > least ? each : least) + 63) / 64 * 64;
+constexpr int kLeastKeys = 64;    // of a part, at least
+// Keys of each of `parts` parts of n keys: whole tiles of 64.
+__host__ __device__ inline int part_keys(int n, int parts) {
+  const int each = ((n + parts - 1) / parts + 63) / 64 * 64;
+  return each > kLeastKeys ? each : kLeastKeys;
 }
-constexpr int kOwnLeast = 256;    // keys of a part of own keys, at least
-constexpr int kPrefixLeast = 128; // and of the prefix
 constexpr int kFewRows = 16;      // of a key head over the prefix, at most, without tiles
 
 constexpr float kNoMax = -3.4e38f;  // below every logit (the bias is clamped at -3e38)
@@ -109,7 +108,7 @@ cudaError_t launch_prefix(const CUtensorMap& tk, const CUtensorMap& tv, const Sh
 // Splits of the own and prefix keys and the table's size; fills nsplit, npsplit, copies,
 // slots, tab_top, tab_len.
 void shared_split(SharedArgs* a, int64_t Pmax, int64_t Tmax);
-void prefix_split(SharedArgs* a, int64_t Pmax, int64_t Tmax);
+void prefix_split(SharedArgs* a, int64_t Pmax);
 
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st);
 cudaError_t launch_evict_move(const EvictArgs& a, cudaStream_t st);
