@@ -829,6 +829,8 @@ bam_status bam_kv_evict_paged(void* k_pages, void* v_pages, const int* block_tab
     return BAM_ERR_INVALID_ARG;
   if (budget < 1 || sink < 0 || recent < 0 || static_cast<int64_t>(sink) + recent > budget)
     return BAM_ERR_INVALID_ARG;
+  // (rows of the pages are numbered with 32 bits: more than any device holds)
+  if (static_cast<int64_t>(num_pages) * Hkv > 0xFFFFFFFFll / page) return BAM_ERR_UNSUPPORTED;
   const int Tmax = page * max_blocks;
   if (budget > Tmax) budget = Tmax;  // no sequence is longer: nothing leaves
   if (!out_table != (out_blocks == 0) || out_blocks < 0 ||
@@ -851,7 +853,8 @@ bam_status bam_kv_evict_paged(void* k_pages, void* v_pages, const int* block_tab
   a.sink = sink;
   a.recent = recent;
   a.count = reinterpret_cast<int2*>(wsb + w.count);
-  a.list = reinterpret_cast<int*>(wsb + w.list);
+  a.list = reinterpret_cast<unsigned*>(wsb + w.list);
+  a.by_page = divisor_of(static_cast<unsigned>(page));
   cudaError_t e =
       launch_kernel(BAM_KERNEL_EVICT_SELECT, stream, [&] { return launch_evict_select(a, stream); });
   if (e != cudaSuccess) return BAM_ERR_CUDA;

@@ -163,6 +163,29 @@ __device__ __forceinline__ void grid_dep_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Division of 32-bit numbers by a divisor that the host knows: the quotient is
+// (t + (n - t >> s1)) >> s2 with t the high word of n times `factor` (Granlund and
+// Montgomery, "Division by invariant integers using multiplication").
+struct Divisor {
+  unsigned factor;
+  int s1, s2;
+};
+inline Divisor divisor_of(unsigned d) {
+  int l = 0;
+  while (l < 32 && (1ull << l) < d) ++l;
+  Divisor x;
+  x.factor = static_cast<unsigned>((((1ull << l) - d) << 32) / d + 1);
+  x.s1 = l < 1 ? l : 1;
+  x.s2 = l < 1 ? 0 : l - 1;
+  return x;
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ unsigned divide(unsigned n, const Divisor& d) {
+  const unsigned t = __umulhi(n, d.factor);
+  return (t + ((n - t) >> d.s1)) >> d.s2;
+}
+#endif
+
 // Streaming multiprocessors of the current device (queried once per device).
 inline int sm_count() {
   static int cached[64] = {};

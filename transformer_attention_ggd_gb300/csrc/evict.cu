@@ -1,16 +1,41 @@
 // Eviction from a paged cache: of each sequence and key head the first keys, the
 // last ones and, of the rest, those of the largest accumulated weight stay, in
 // order.
+//
+// It reads the weights once (4 bytes a key) and moves the keys, values, positions
+// and weights that stay (264 bytes a key, read and written): bound by HBM, with
+// the choice of the keys before it.
+//
+// Choice: the weight of the last key that stays is found digit by digit (11, 11
+// and 10 bits, from the highest) in histograms of the weights, which stay in shared
+// memory; keys of exactly that weight stay from the lowest slot on.  Long
+// sequences are dealt to a cluster of CTAs, a run of slots each.
 #include "shared_common.cuh"
 
 namespace bam {
 namespace {
 
 constexpr int kSelThreads = 512;
-constexpr int kSelPer = 4;        // slots of a thread in a chunk
-constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 8;      // rows of a thread in a wave
-constexpr int kMoveWave = kMoveThreads / 8 * kMoveRows;
+constexpr int kSelPer = 4;                          // slots of a thread in a chunk
+constexpr int kSelChunk = kSelThreads * kSelPer;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kCacheMost = 40960;                   // weights in shared memory, at most
+constexpr int kSlotsCta = 4096;                     // of a CTA of a cluster, at least
+constexpr int kMoveRows = 8;                        // rows of a thread in a wave
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The int at `p` of this CTA's shared memory in CTA `rank` of the cluster.
+__device__ __forceinline__ int cluster_load(const int* p, int rank) {
+  uint32_t at;
+  int x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
 
 // Order of the weights as unsigned numbers: NaN above everything, -0 as 0.
 __device__ __forceinline__ uint32_t weight_order(float w) {
@@ -41,101 +66,171 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* warp_sums, 
   return before + s - x;
 }
 
-// One block a sequence and key head: the weight of the last kept key by a radix
-// search from the highest bits, then the list of the slots that stay.
-__global__ void __launch_bounds__(kSelThreads) bam_kv_evict_select_kernel(const EvictArgs a) {
-  __shared__ int hist[256];
+// A cluster chooses the keys of a sequence and key head.
+__global__ void __launch_bounds__(kSelThreads, 2) bam_kv_evict_select_kernel(const EvictArgs a) {
+  extern __shared__ __align__(16) uint32_t cache[];  // orders of this CTA's weights
+  __shared__ __align__(16) int hist[kBins];
   __shared__ uint64_t warp_sums[kSelThreads / 32];
-  __shared__ int s_bin, s_need;
+  __shared__ int s_bin, s_need, s_over, s_ties, s_first;
   grid_dep_trigger();
   const CacheArgs& c = a.c;
-  const int hk = blockIdx.x, b = blockIdx.y;
+  const int rank = blockIdx.x % a.cluster, hk = blockIdx.x / a.cluster, b = blockIdx.y;
   const int cap = c.page * c.max_blocks, raw = __ldg(c.lens + b);
   const int len = min(max(raw, 0), cap), kept = min(len, a.budget);
-  bool ok = raw == len, pages_ok = true;
   const int* table = c.block_table + static_cast<size_t>(b) * c.max_blocks;
   const int* out = a.out_table ? a.out_table + static_cast<size_t>(b) * a.out_blocks : nullptr;
-  for (int i = threadIdx.x; i * static_cast<int64_t>(c.page) < len; i += kSelThreads) {
-    const int pg = __ldg(table + i);
+  // Pages of all used blocks, by every CTA: all of a sequence's CTAs decide alike.
+  bool pages_ok = true;
+  const int blocks = static_cast<int>(divide(len + c.page - 1, a.by_page));
+  const int out_blocks = out ? static_cast<int>(divide(kept + c.page - 1, a.by_page)) : 0;
+  for (int i = threadIdx.x; i < blocks + out_blocks; i += kSelThreads) {
+    const int pg = __ldg(i < blocks ? table + i : out + (i - blocks));
     pages_ok &= pg >= 0 && pg < c.num_pages;
   }
-  if (out) {
-    for (int i = threadIdx.x; i * static_cast<int64_t>(c.page) < kept; i += kSelThreads) {
-      const int pg = __ldg(out + i);
-      pages_ok &= pg >= 0 && pg < c.num_pages;
-    }
-  }
   pages_ok = __syncthreads_and(pages_ok);
-  int2* count = a.count + static_cast<int64_t>(b) * c.Hkv + hk;
-  if (threadIdx.x == 0 && !(ok && pages_ok)) record_bad_arg(c.status);
-  int* list = a.list + (static_cast<int64_t>(b) * c.Hkv + hk) * a.budget;
-  if (!pages_ok || len <= a.budget) {
-    if (threadIdx.x == 0) *count = make_int2(pages_ok ? len : -1 - len, out ? 0 : len);
+  const int64_t head = static_cast<int64_t>(b) * c.Hkv + hk;
+  if (threadIdx.x == 0 && rank == 0 && !(raw == len && pages_ok)) record_bad_arg(c.status);
+  unsigned* list = a.list + head * a.budget;
+  // Row of a slot in the pages.
+  auto row_of = [&](int slot) {
+    const unsigned blk = divide(slot, a.by_page);
+    return (static_cast<unsigned>(__ldg(table + blk)) * c.Hkv + hk) * c.page + (slot - blk * c.page);
+  };
+  if (!pages_ok || len <= a.budget) {  // (the same in every CTA of the cluster)
+    if (threadIdx.x == 0 && rank == 0) a.count[head] = make_int2(pages_ok ? len : -1 - len, out ? 0 : len);
     if (pages_ok && out)
-      for (int i = threadIdx.x; i < len; i += kSelThreads) list[i] = i;
+      for (int i = rank * kSelThreads + threadIdx.x; i < len; i += a.cluster * kSelThreads) list[i] = row_of(i);
     return;
   }
-  auto weight = [&](int slot) {
-    const int pg = __ldg(table + slot / c.page);
-    return weight_order(a.key_weight[(static_cast<int64_t>(pg) * c.Hkv + hk) * c.page + slot % c.page]);
-  };
-  const int lo = a.sink, hi = len - a.recent;
-  int need = a.budget - a.sink - a.recent;  // of [lo, hi), which holds more
-  uint32_t prefix = 0;                      // the threshold's leading bits
-  if (need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int i = lo + threadIdx.x; i < hi; i += kSelThreads) {
-        const uint32_t w = weight(i);
-        if (shift == 24 || (w >> (shift + 8)) == (prefix >> (shift + 8)))
-          atomicAdd(&hist[(w >> shift) & 255], 1);
-      }
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        int left = need, bin = 255;
-        while (hist[bin] < left) left -= hist[bin--];
-        s_bin = bin;
-        s_need = left;
-      }
-      __syncthreads();
-      prefix |= static_cast<uint32_t>(s_bin) << shift;
-      need = s_need;
+  // This CTA's slots: a run of whole fours.
+  const int per = ((len + a.cluster - 1) / a.cluster + kSelPer - 1) / kSelPer * kSelPer;
+  const int begin = min(len, rank * per), end = min(len, begin + per);
+  const int lo = a.sink, hi = len - a.recent;   // the candidates
+  int need = a.budget - a.sink - a.recent;      // of them
+  // Orders of four slots from i on, which lie in one page.
+  auto orders = [&](int i, bool first) {
+    uint4 w;
+    if (!first && i - begin < a.cached) {
+      w = *reinterpret_cast<const uint4*>(cache + (i - begin));
+    } else {
+      const float4 f = *reinterpret_cast<const float4*>(a.key_weight + row_of(i));
+      w = make_uint4(weight_order(f.x), weight_order(f.y), weight_order(f.z), weight_order(f.w));
+      if (first && i - begin < a.cached) *reinterpret_cast<uint4*>(cache + (i - begin)) = w;
     }
+    return w;
+  };
+  uint32_t threshold = 0;
+  int shift = 32;
+#pragma unroll 1
+  for (int pass = 0; pass < 3 && need > 0; ++pass) {
+    const int bits = pass < 2 ? 11 : 10, up = shift;  // bits above `up` are known
+    shift -= bits;
+    for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    for (int i = begin + kSelPer * threadIdx.x; i < end; i += kSelChunk) {
+      const uint4 q = orders(i, pass == 0);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (i + x >= lo && i + x < hi && i + x < end && (pass == 0 || ((w[x] ^ threshold) >> up) == 0))
+          atomicAdd(&hist[(w[x] >> shift) & ((1 << bits) - 1)], 1);
+    }
+    if (a.cluster > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    // Thread 0 has the highest four bins.
+    int n[4], sum = 0;
+    const int top = kBins - 1 - 4 * threadIdx.x;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      n[x] = 0;
+      if (a.cluster > 1) {
+        for (int r = 0; r < a.cluster; ++r) n[x] += cluster_load(&hist[top - x], r);
+      } else {
+        n[x] = hist[top - x];
+      }
+      sum += n[x];
+    }
+    uint64_t total;
+    int above = static_cast<int>(block_scan(static_cast<uint64_t>(sum), warp_sums, &total));
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (above < need && need <= above + n[x]) {
+        s_bin = top - x;
+        s_need = need - above;
+      }
+      above += n[x];
+    }
+    if (a.cluster > 1)
+      cluster_sync();  // (the histograms are no longer read)
+    else
+      __syncthreads();
+    threshold |= static_cast<uint32_t>(s_bin) << shift;
+    need = s_need;
+    __syncthreads();
   }
-  // `need` of the keys whose weight is the threshold stay, the lowest slots first.
-  const bool none = a.budget == a.sink + a.recent;
-  int at = 0, ties = 0, first = len;
-  for (int base = 0; base < len; base += kSelThreads * kSelPer) {
-    const int i0 = base + threadIdx.x * kSelPer;
-    bool over[kSelPer], tie[kSelPer];
-    int n = 0, t = 0;
+  // `need` of the keys whose weight is the threshold stay, the lowest slots first (none of the
+  // candidates if none is needed).
+  const bool any = a.budget > a.sink + a.recent;
+  auto classify = [&](int i0, bool (&over)[kSelPer], bool (&tie)[kSelPer]) {
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (i0 < end && any) q = orders(i0, false);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int x = 0; x < kSelPer; ++x) {
       const int i = i0 + x;
-      over[x] = tie[x] = false;
-      if (i < lo || (i >= hi && i < len)) {
-        over[x] = true;
-      } else if (i < len && !none) {
-        const uint32_t w = weight(i);
-        over[x] = w > prefix;
-        tie[x] = w == prefix;
-      }
-      n += over[x];
-      t += tie[x];
+      const bool in = i < end, candidate = in && i >= lo && i < hi;
+      over[x] = in && (candidate ? any && w[x] > threshold : true);
+      tie[x] = candidate && any && w[x] == threshold;
     }
+  };
+  int at = 0, ties = 0;
+  if (a.cluster > 1) {
+    // What the CTAs before this one keep.
+    int n = 0, t = 0;
+    for (int i0 = begin + kSelPer * threadIdx.x; i0 < end; i0 += kSelChunk) {
+      bool over[kSelPer], tie[kSelPer];
+      classify(i0, over, tie);
+#pragma unroll
+      for (int x = 0; x < kSelPer; ++x) n += over[x], t += tie[x];
+    }
+    uint64_t total;
+    block_scan(static_cast<uint64_t>(n) << 32 | static_cast<uint32_t>(t), warp_sums, &total);
+    if (threadIdx.x == 0) {
+      s_over = static_cast<int>(total >> 32);
+      s_ties = static_cast<int>(total & 0xFFFFFFFFu);
+    }
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      at += cluster_load(&s_over, r);
+      ties += cluster_load(&s_ties, r);
+    }
+  }
+  if (threadIdx.x == 0) s_first = len;
+  int first = len;
+  for (int base = begin; base < end; base += kSelChunk) {
+    const int i0 = base + threadIdx.x * kSelPer;
+    bool over[kSelPer], tie[kSelPer];
+    classify(i0, over, tie);
+    int n = 0, t = 0;
+#pragma unroll
+    for (int x = 0; x < kSelPer; ++x) n += over[x], t += tie[x];
     uint64_t total;
     const uint64_t scan =
         block_scan(static_cast<uint64_t>(n) << 32 | static_cast<uint32_t>(t), warp_sums, &total);
     int tie_rank = ties + static_cast<int>(scan & 0xFFFFFFFFu);
-    int dst = at + static_cast<int>(scan >> 32) + min(tie_rank, need) ;
+    int dst = at + static_cast<int>(scan >> 32) + min(tie_rank, need);
+    if (n + t > 0) {
+      const unsigned row = row_of(i0);
 #pragma unroll
-    for (int x = 0; x < kSelPer; ++x) {
-      const bool keep = over[x] || (tie[x] && tie_rank < need);
-      tie_rank += tie[x];
-      if (keep) {
-        if (dst != i0 + x && first == len) first = dst;
-        list[dst++] = i0 + x;
+      for (int x = 0; x < kSelPer; ++x) {
+        const bool keep = over[x] || (tie[x] && tie_rank < need);
+        tie_rank += tie[x];
+        if (keep) {
+          if (dst != i0 + x && first == len) first = dst;
+          list[dst++] = row + x;
+        }
       }
     }
     at += static_cast<int>(total >> 32);
@@ -143,83 +238,122 @@ __global__ void __launch_bounds__(kSelThreads) bam_kv_evict_select_kernel(const 
   }
   // The first key that moves.
   __syncthreads();
-  if (threadIdx.x == 0) s_need = len;
-  __syncthreads();
-  atomicMin(&s_need, first);
-  __syncthreads();
-  if (threadIdx.x == 0) *count = make_int2(kept, out ? 0 : min(s_need, kept));
+  if (first < len) atomicMin(&s_first, first);
+  if (a.cluster > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (threadIdx.x == 0 && rank == 0) {
+    int f = s_first;
+    for (int r = 1; r < a.cluster; ++r) f = min(f, cluster_load(&s_first, r));
+    a.count[head] = make_int2(kept, out ? 0 : min(f, kept));
+  }
+  if (a.cluster > 1) cluster_sync();  // (no CTA ends while another reads it)
 }
 
-// A cluster moves the keys (z 0) or the values (z 1) of one sequence and key head,
-// in waves: every CTA reads its rows of the wave, the cluster meets, and they are
-// written.  Row m goes from slot list[m] >= m to slot m, so a row that is written
-// was the source of an earlier row, if of any, which has been read.
-__global__ void __launch_bounds__(kMoveThreads) bam_kv_evict_move_kernel(const EvictArgs a) {
+// CTAs move the keys (z 0) or the values (z 1) of one sequence and key head.  In place they
+// are a cluster and go in waves: every CTA reads its rows of the wave, the
+// cluster meets, and they are written.  Row m goes from a slot >= m to slot m, so
+// that a row that is written was the source of an earlier row, if of any, which has
+// been read; the next wave's rows are on their way while this one's are written.
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) bam_kv_evict_move_kernel(const EvictArgs a) {
+  constexpr int kStep = kThreads / 8, kWave = kStep * kMoveRows;  // eight lanes a row
   grid_dep_wait();
   const CacheArgs& c = a.c;
   const int rank = blockIdx.x % a.cluster, hk = blockIdx.x / a.cluster, b = blockIdx.y;
   const bool values = blockIdx.z;
-  const int2 cnt = a.count[static_cast<int64_t>(b) * c.Hkv + hk];
+  const int64_t head = static_cast<int64_t>(b) * c.Hkv + hk;
+  const int2 cnt = a.count[head];
   if (blockIdx.x == 0 && !values && threadIdx.x == 0) a.new_lens[b] = cnt.x >= 0 ? cnt.x : -1 - cnt.x;
-  const int* table = c.block_table + static_cast<size_t>(b) * c.max_blocks;
-  const int* dst_table = a.out_table ? a.out_table + static_cast<size_t>(b) * a.out_blocks : table;
-  const int* list = a.list + (static_cast<int64_t>(b) * c.Hkv + hk) * a.budget;
+  const int* table = a.out_table ? a.out_table + static_cast<size_t>(b) * a.out_blocks
+                                 : c.block_table + static_cast<size_t>(b) * c.max_blocks;
+  const unsigned* list = a.list + head * a.budget;
   uint4* pool = reinterpret_cast<uint4*>(values ? a.v_pages : a.k_pages);
   uint32_t* side = values ? reinterpret_cast<uint32_t*>(a.key_weight) : reinterpret_cast<uint32_t*>(a.key_pos);
-  const int u = threadIdx.x & 7;
-  for (int64_t m0 = cnt.y; m0 < cnt.x; m0 += static_cast<int64_t>(kMoveWave) * a.cluster) {
-    uint4 w[kMoveRows];
-    uint32_t mark[kMoveRows];
-    const int64_t first = m0 + rank * kMoveWave + (threadIdx.x >> 3);
+  const int u = threadIdx.x & 7, n = cnt.x, step = kWave * a.cluster;
+  uint4 w[kMoveRows];
+  uint32_t mark[kMoveRows];
+  unsigned src[kMoveRows];
+  auto fetch = [&](int64_t m) {  // rows' places
+#pragma unroll
+    for (int x = 0; x < kMoveRows; ++x) src[x] = m + x * kStep < n ? __ldg(list + m + x * kStep) : 0;
+  };
+  int64_t m0 = cnt.y + static_cast<int64_t>(rank) * kWave + (threadIdx.x >> 3);
+  fetch(m0);
+  // (every CTA of a cluster goes through as many waves)
+  for (int64_t wave = cnt.y; wave < n; wave += step, m0 += step) {
 #pragma unroll
     for (int x = 0; x < kMoveRows; ++x) {
-      const int64_t m = first + x * (kMoveThreads / 8);
-      if (m >= cnt.x) break;
-      const int slot = list[m];
-      const int pg = __ldg(table + slot / c.page);
-      const int64_t row = (static_cast<int64_t>(pg) * c.Hkv + hk) * c.page + slot % c.page;
-      w[x] = pool[row * 8 + u];
-      if (u == 0) mark[x] = side[row];
+      if (m0 + x * kStep >= n) break;
+      w[x] = pool[static_cast<int64_t>(src[x]) * 8 + u];
+      if (u == 0) mark[x] = side[src[x]];
     }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    fetch(m0 + step);
+    if (!a.out_table) cluster_sync();
 #pragma unroll
     for (int x = 0; x < kMoveRows; ++x) {
-      const int64_t m = first + x * (kMoveThreads / 8);
-      if (m >= cnt.x) break;
-      const int slot = static_cast<int>(m);
-      const int pg = __ldg(dst_table + slot / c.page);
-      const int64_t row = (static_cast<int64_t>(pg) * c.Hkv + hk) * c.page + slot % c.page;
+      const int64_t m = m0 + x * kStep;
+      if (m >= n) break;
+      const unsigned blk = divide(static_cast<unsigned>(m), a.by_page);
+      const int64_t row = (static_cast<int64_t>(__ldg(table + blk)) * c.Hkv + hk) * c.page + (m - blk * c.page);
       pool[row * 8 + u] = w[x];
       if (u == 0) side[row] = mark[x];
     }
   }
 }
 
-}  // namespace
-
-cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st) {
-  return launch_k(bam_kv_evict_select_kernel, dim3(a.c.Hkv, a.c.B), dim3(kSelThreads), 0, st, false, a);
-}
-
-cudaError_t launch_evict_move(const EvictArgs& args, cudaStream_t st) {
-  EvictArgs a = args;
-  a.cluster = 1;
-  while (a.cluster < 8 && 2 * static_cast<int64_t>(a.c.B) * a.c.Hkv * a.cluster < 4 * sm_count()) a.cluster *= 2;
+template <class F>
+cudaError_t launch_cluster(F* kernel, dim3 grid, int threads, size_t smem, int cluster, bool pdl,
+                           const EvictArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.cluster * a.c.Hkv, a.c.B, 2);
-  cfg.blockDim = dim3(kMoveThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.cluster;
+  attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, bam_kv_evict_move_kernel, a);
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace
+
+cudaError_t launch_evict_select(const EvictArgs& args, cudaStream_t st) {
+  EvictArgs a = args;
+  const int64_t heads = static_cast<int64_t>(a.c.B) * a.c.Hkv, cap = static_cast<int64_t>(a.c.page) * a.c.max_blocks;
+  a.cluster = 1;
+  while (a.cluster < kMaxCluster &&
+         (cap > static_cast<int64_t>(kCacheMost) * a.cluster ||
+          (heads * a.cluster < 2 * sm_count() && cap > static_cast<int64_t>(2 * kSlotsCta) * a.cluster)))
+    a.cluster *= 2;
+  const int64_t per = ((cap + a.cluster - 1) / a.cluster + kSelPer - 1) / kSelPer * kSelPer;
+  a.cached = static_cast<int>(per < kCacheMost ? per : kCacheMost);
+  static bool limit_set[64] = {};
+  const cudaError_t e = smem_limit_once(bam_kv_evict_select_kernel, kCacheMost * 4, limit_set);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(bam_kv_evict_select_kernel, dim3(a.c.Hkv * a.cluster, a.c.B), kSelThreads,
+                        static_cast<size_t>(a.cached) * 4, a.cluster, false, a, st);
+}
+
+cudaError_t launch_evict_move(const EvictArgs& args, cudaStream_t st) {
+  EvictArgs a = args;
+  // Small CTAs where there are many chains; else large ones, and as many a chain as a cluster takes.
+  const int64_t chains = 2 * static_cast<int64_t>(a.c.B) * a.c.Hkv;
+  const bool many = chains >= 4 * sm_count();
+  a.cluster = 1;
+  while (a.cluster < kMaxCluster && chains * a.cluster < 2 * sm_count() &&
+         a.budget > 512 * static_cast<int64_t>(a.cluster))
+    a.cluster *= 2;
+  const dim3 grid(a.cluster * a.c.Hkv, a.c.B, 2);
+  if (many) return launch_cluster(bam_kv_evict_move_kernel<128>, grid, 128, 0, a.cluster, true, a, st);
+  return launch_cluster(bam_kv_evict_move_kernel<512>, grid, 512, 0, a.cluster, true, a, st);
 }
 
 }  // namespace bam

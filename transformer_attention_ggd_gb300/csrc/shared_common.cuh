@@ -93,9 +93,13 @@ struct EvictArgs {
   int out_blocks;
   int* new_lens;
   int budget, sink, recent;
-  int* list;             // [B, Hkv, budget] slots kept, ascending
-  int2* count;           // [B, Hkv] kept keys (-1: left as they were) and the first that moves
-  int cluster;           // CTAs that share a chain of moves
+  Divisor by_page;
+  // Of each sequence and key head: the rows of the pages that stay, in order, how many they are
+  // (-1 - length: the sequence stays as it is) and the first that moves.
+  unsigned* list;        // [B, Hkv, budget]
+  int2* count;           // [B, Hkv]
+  int cluster;           // CTAs that share a sequence and key head (of its keys or values, moving)
+  int cached;            // weights of a selecting CTA that stay in shared memory
 };
 
 cudaError_t launch_shared_prep(const SharedArgs& a, cudaStream_t st);
