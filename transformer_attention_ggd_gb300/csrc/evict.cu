@@ -15,9 +15,11 @@
 namespace bam {
 namespace {
 
-constexpr int kSelThreads = 512;
+// Threads of a selecting CTA for short runs of slots and for long ones (16384 of them take
+// 53 us with the few, 40 with 512).
+constexpr int kSelFew = 256, kSelMany = 512;
+constexpr int kSelRun = 8192;                       // slots, at most, for the few
 constexpr int kSelPer = 4;                          // slots of a thread in a chunk
-constexpr int kSelChunk = kSelThreads * kSelPer;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kCacheMost = 40960;                   // weights in shared memory, at most
@@ -37,6 +39,17 @@ __device__ __forceinline__ int cluster_load(const int* p, int rank) {
   return x;
 }
 
+__device__ __forceinline__ int4 cluster_load4(const int* p, int rank) {
+  uint32_t at;
+  int4 x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(at)
+               : "memory");
+  return x;
+}
+
 // Order of the weights as unsigned numbers: NaN above everything, -0 as 0.
 __device__ __forceinline__ uint32_t weight_order(float w) {
   if (w != w) return 0xFFFFFFFFu;
@@ -45,6 +58,7 @@ __device__ __forceinline__ uint32_t weight_order(float w) {
 }
 
 // Exclusive prefix sums over the block of two counts packed in a 64-bit word.
+template <int kSelThreads>
 __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* warp_sums, uint64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint64_t s = x;
@@ -67,7 +81,11 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* warp_sums, 
 }
 
 // A cluster chooses the keys of a sequence and key head.
-__global__ void __launch_bounds__(kSelThreads, 2) bam_kv_evict_select_kernel(const EvictArgs a) {
+template <int kSelThreads>
+__global__ void __launch_bounds__(kSelThreads, 1280 / kSelThreads) bam_kv_evict_select_kernel(const EvictArgs a) {
+  constexpr int kSelChunk = kSelThreads * kSelPer;
+  constexpr int kBinThreads = kSelThreads < kBins / 4 ? kSelThreads : kBins / 4;
+  constexpr int kThreadBins = kBins / kBinThreads;  // in fours
   extern __shared__ __align__(16) uint32_t cache[];  // orders of this CTA's weights
   __shared__ __align__(16) int hist[kBins];
   __shared__ uint64_t warp_sums[kSelThreads / 32];
@@ -106,6 +124,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) bam_kv_evict_select_kernel(con
   const int per = ((len + a.cluster - 1) / a.cluster + kSelPer - 1) / kSelPer * kSelPer;
   const int begin = min(len, rank * per), end = min(len, begin + per);
   const int lo = a.sink, hi = len - a.recent;   // the candidates
+  const int inner = min(hi, end);               // end of those of this CTA
   int need = a.budget - a.sink - a.recent;      // of them
   // Orders of four slots from i on, which lie in one page.
   auto orders = [&](int i, bool first) {
@@ -130,34 +149,45 @@ __global__ void __launch_bounds__(kSelThreads, 2) bam_kv_evict_select_kernel(con
     for (int i = begin + kSelPer * threadIdx.x; i < end; i += kSelChunk) {
       const uint4 q = orders(i, pass == 0);
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      const bool all = i >= lo && i + 4 <= inner;
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (i + x >= lo && i + x < hi && i + x < end && (pass == 0 || ((w[x] ^ threshold) >> up) == 0))
-          atomicAdd(&hist[(w[x] >> shift) & ((1 << bits) - 1)], 1);
+      for (int x = 0; x < 4; ++x) {
+        if (!all && (i + x < lo || i + x >= inner)) continue;
+        if (pass > 0 && ((w[x] ^ threshold) >> up) != 0) continue;
+        atomicAdd(&hist[(w[x] >> shift) & ((1 << bits) - 1)], 1);
+      }
     }
     if (a.cluster > 1)
       cluster_sync();
     else
       __syncthreads();
-    // Thread 0 has the highest four bins.
-    int n[4], sum = 0;
-    const int top = kBins - 1 - 4 * threadIdx.x;
+    // Thread 0 has the highest bins.
+    int n[kThreadBins], sum = 0;  // from the highest on
+    const int top = kBins - kThreadBins * static_cast<int>(threadIdx.x + 1);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      n[x] = 0;
+    for (int x = 0; x < kThreadBins; x += 4) {
+      n[x] = n[x + 1] = n[x + 2] = n[x + 3] = 0;
+      if (top < 0) continue;
+      const int* p = hist + top + kThreadBins - 4 - x;
+      int4 v = *reinterpret_cast<const int4*>(p);
       if (a.cluster > 1) {
-        for (int r = 0; r < a.cluster; ++r) n[x] += cluster_load(&hist[top - x], r);
-      } else {
-        n[x] = hist[top - x];
+        int4 y[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          y[r] = r < a.cluster ? cluster_load4(p, r) : make_int4(0, 0, 0, 0);
+        v = make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) v.x += y[r].x, v.y += y[r].y, v.z += y[r].z, v.w += y[r].w;
       }
-      sum += n[x];
+      n[x] = v.w, n[x + 1] = v.z, n[x + 2] = v.y, n[x + 3] = v.x;
+      sum += v.x + v.y + v.z + v.w;
     }
     uint64_t total;
-    int above = static_cast<int>(block_scan(static_cast<uint64_t>(sum), warp_sums, &total));
+    int above = static_cast<int>(block_scan<kSelThreads>(static_cast<uint64_t>(sum), warp_sums, &total));
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < kThreadBins; ++x) {
       if (above < need && need <= above + n[x]) {
-        s_bin = top - x;
+        s_bin = top + kThreadBins - 1 - x;
         s_need = need - above;
       }
       above += n[x];
@@ -177,12 +207,17 @@ __global__ void __launch_bounds__(kSelThreads, 2) bam_kv_evict_select_kernel(con
     uint4 q = make_uint4(0, 0, 0, 0);
     if (i0 < end && any) q = orders(i0, false);
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const bool all = i0 >= lo && i0 + kSelPer <= inner && any;
 #pragma unroll
     for (int x = 0; x < kSelPer; ++x) {
       const int i = i0 + x;
-      const bool in = i < end, candidate = in && i >= lo && i < hi;
-      over[x] = in && (candidate ? any && w[x] > threshold : true);
-      tie[x] = candidate && any && w[x] == threshold;
+      over[x] = w[x] > threshold;
+      tie[x] = w[x] == threshold;
+      if (!all) {
+        const bool in = i < end, candidate = in && i >= lo && i < hi;
+        over[x] = in && (!candidate || (any && over[x]));
+        tie[x] = candidate && any && tie[x];
+      }
     }
   };
   int at = 0, ties = 0;
@@ -196,7 +231,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) bam_kv_evict_select_kernel(con
       for (int x = 0; x < kSelPer; ++x) n += over[x], t += tie[x];
     }
     uint64_t total;
-    block_scan(static_cast<uint64_t>(n) << 32 | static_cast<uint32_t>(t), warp_sums, &total);
+    block_scan<kSelThreads>(static_cast<uint64_t>(n) << 32 | static_cast<uint32_t>(t), warp_sums, &total);
     if (threadIdx.x == 0) {
       s_over = static_cast<int>(total >> 32);
       s_ties = static_cast<int>(total & 0xFFFFFFFFu);
@@ -218,7 +253,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) bam_kv_evict_select_kernel(con
     for (int x = 0; x < kSelPer; ++x) n += over[x], t += tie[x];
     uint64_t total;
     const uint64_t scan =
-        block_scan(static_cast<uint64_t>(n) << 32 | static_cast<uint32_t>(t), warp_sums, &total);
+        block_scan<kSelThreads>(static_cast<uint64_t>(n) << 32 | static_cast<uint32_t>(t), warp_sums, &total);
     int tie_rank = ties + static_cast<int>(scan & 0xFFFFFFFFu);
     int dst = at + static_cast<int>(scan >> 32) + min(tie_rank, need);
     if (n + t > 0) {
@@ -335,19 +370,29 @@ cudaError_t launch_evict_select(const EvictArgs& args, cudaStream_t st) {
     a.cluster *= 2;
   const int64_t per = ((cap + a.cluster - 1) / a.cluster + kSelPer - 1) / kSelPer * kSelPer;
   a.cached = static_cast<int>(per < kCacheMost ? per : kCacheMost);
-  static bool limit_set[64] = {};
-  const cudaError_t e = smem_limit_once(bam_kv_evict_select_kernel, kCacheMost * 4, limit_set);
+  static bool few_set[64] = {}, many_set[64] = {};
+  const bool few = per <= kSelRun;
+  const cudaError_t e = few ? smem_limit_once(bam_kv_evict_select_kernel<kSelFew>, kCacheMost * 4, few_set)
+                            : smem_limit_once(bam_kv_evict_select_kernel<kSelMany>, kCacheMost * 4, many_set);
   if (e != cudaSuccess) return e;
-  return launch_cluster(bam_kv_evict_select_kernel, dim3(a.c.Hkv * a.cluster, a.c.B), kSelThreads,
-                        static_cast<size_t>(a.cached) * 4, a.cluster, false, a, st);
+  const dim3 grid(a.c.Hkv * a.cluster, a.c.B);
+  const size_t smem = static_cast<size_t>(a.cached) * 4;
+  return few ? launch_cluster(bam_kv_evict_select_kernel<kSelFew>, grid, kSelFew, smem, a.cluster, false, a, st)
+             : launch_cluster(bam_kv_evict_select_kernel<kSelMany>, grid, kSelMany, smem, a.cluster, false, a, st);
 }
 
 cudaError_t launch_evict_move(const EvictArgs& args, cudaStream_t st) {
   EvictArgs a = args;
-  // Small CTAs where there are many chains; else large ones, and as many a chain as a cluster takes.
   const int64_t chains = 2 * static_cast<int64_t>(a.c.B) * a.c.Hkv;
-  const bool many = chains >= 4 * sm_count();
   a.cluster = 1;
+  if (a.out_table) {
+    // Nothing that is read is written: any number of CTAs.
+    while (a.cluster < 64 && chains * a.cluster < 8 * sm_count() && a.budget > 128 * static_cast<int64_t>(a.cluster))
+      a.cluster *= 2;
+    return launch_k(bam_kv_evict_move_kernel<128>, dim3(a.cluster * a.c.Hkv, a.c.B, 2), dim3(128), 0, st, true, a);
+  }
+  // Small CTAs where there are many chains; else large ones, and as many a chain as a cluster takes.
+  const bool many = chains >= 4 * sm_count();
   while (a.cluster < kMaxCluster && chains * a.cluster < 2 * sm_count() &&
          a.budget > 512 * static_cast<int64_t>(a.cluster))
     a.cluster *= 2;
