@@ -16,12 +16,60 @@ constexpr int kBoxBytes = kKeys * kHeadDim * 2;
 constexpr int kBiasStride = kKeys + 8;       // floats: 8-byte reads of four rows hit all banks
 constexpr float kRescale = 8.0f;
 
+// A row's prior for biases that are evaluated in the attention kernel itself:
+//   b log2(e) = -log2(e) 2^y,  y = beta (log2 u - log2 alpha),  u = |d - mu| (at least eps where beta <= 0),
+// or, with the theta prior, y = theta_beta log2(|d - mu| + eps) + theta_alpha log2(e).
+struct __align__(16) BiasRow {
+  float beta, mu;
+  float least, add;  // u = max(|d - mu|, least) + add
+  float e, l;        // log2 alpha: integer part and the rest
+  float hi, lo;      // theta_alpha log2(e) as a sum of two floats
+};
+__device__ __forceinline__ BiasRow bias_row(const SharedArgs& a, int h) {
+  BiasRow r;
+  const float alpha = __ldg(a.alpha + h);
+  r.beta = __ldg(a.beta + h);
+  r.mu = __ldg(a.mu + h);
+  r.least = r.add = r.e = r.l = r.hi = r.lo = 0.0f;
+  if (a.prior == kPriorTheta) {
+    r.mu = 2.0f * sinhf(r.mu);
+    r.add = a.eps;
+    constexpr float kL2eHi = 1.44269502162933349609375f, kL2eLo = 1.925962989091e-08f;  // log2(e)
+    r.hi = alpha * kL2eHi;
+    r.lo = fmaf(alpha, kL2eHi, -r.hi) + alpha * kL2eLo;
+  } else {
+    if (r.beta <= 0.0f) r.least = a.eps;
+    int e;
+    const float m = frexpf(alpha, &e);
+    r.e = static_cast<float>(e);
+    r.l = log2f(m);
+  }
+  return r;
+}
+// b(d) log2(e) to a few 1e-7 relative: the exponent y is a sum of two floats (its large part beta times
+// an integer is split exactly), and 2^y is 2^n, exact, times exp2 of the rest.
+__device__ __forceinline__ float bias_value(float d, const BiasRow& r) {
+  const float u = fmaxf(fabsf(d - r.mu), r.least) + r.add;
+  const int bits = __float_as_int(u);
+  const float e = static_cast<float>((bits >> 23) - 126) - r.e;
+  const float l = __log2f(__int_as_float((bits & 0x007FFFFF) | 0x3F000000)) - r.l;  // u's mantissa in [1/2, 1)
+  const float p = r.beta * e, q = fmaf(r.beta, e, -p), t = r.beta * l;
+  const float s1 = p + t, v1 = s1 - p, e1 = (p - (s1 - v1)) + (t - v1);
+  const float s2 = s1 + r.hi, v2 = s2 - s1, e2 = (s1 - (s2 - v2)) + (r.hi - v2);
+  const float y = fminf(fmaxf(s2, -120.0f), 400.0f), n = floorf(y);
+  const float f = (y - n) + (e1 + e2 + q + r.lo);
+  const float scale = __int_as_float((static_cast<int>(fminf(n, 127.0f)) + 127) << 23);
+  const float b = -ex2_approx(f) * scale * (n > 127.0f ? 3.0e38f : 1.0f) * 1.44269504088896341f;
+  return u == 0.0f ? 0.0f : fmaxf(b, -3.0e38f);
+}
+
 template <bool kTwo>
 struct __align__(1024) SharedSmem {
   uint8_t k[kWarps][kStages][kBoxBytes];
   uint8_t v[kWarps][kStages][kBoxBytes];
   int kpos[kWarps][kStages][kKeys];
   float bias[kWarps][kTwo ? kRows : kRows / 2][kBiasStride];
+  BiasRow rows[kWarps][kRows];
   uint64_t full[kWarps][kStages];
   int abort_flag;
 };
@@ -233,17 +281,16 @@ __global__ void __launch_bounds__(kThreads, kResident)
     bool have_next = false;
     Item next = cur;
     // Rows: lane i holds row i's parameters; products take the queries of rows rq and rq + 8.
-    float alpha = 1.0f, beta = 0.0f, mu = 0.0f, scale = 0.0f;
+    float scale = 0.0f;
     int pos = 0, row = -1;
     if (lane < cur.nrows) {
       int b, h;
       row = item_row(a, cur, lane, &b, &h);
       pos = query_pos(a, b, cur.P, &ok_arg);
-      alpha = __ldg(a.alpha + h);
-      beta = __ldg(a.beta + h);
-      mu = __ldg(a.mu + h);
       scale = shared_scale(a, h, pos);
+      if (!a.table) sm.rows[warp][lane] = bias_row(a, h);
     }
+    __syncwarp();
     const bool tile_marked = marked && !cur.prefix;
     uint32_t qf[4][4];
     float c[2];
@@ -287,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const int valid = cur.kend - kb;
+      const bool full = valid >= kKeys;
       // The bias.  Out of the table: each lane that of its logits.  Else it is evaluated, a key a
       // lane and rows in turn, and handed over in shared memory.
       const int kfirst = (cur.prefix ? 0 : cur.P) + kb;  // position of the tile's first key, without marks
@@ -295,14 +343,11 @@ __global__ void __launch_bounds__(kThreads, kResident)
 #pragma unroll 2
         for (int r = 0; r < cur.nrows; ++r) {
           int d = __shfl_sync(0xffffffffu, pos, r) - kp;
-          if (d < 0) {
+          if (d < 0 || (tile_marked && kp < 0)) {
             bad_pos |= lane < valid;
-            d = 0;
+            d = max(d, 0);
           }
-          float bb, g1, g2;
-          bias_terms<false>(d, __shfl_sync(0xffffffffu, alpha, r), __shfl_sync(0xffffffffu, beta, r),
-                            __shfl_sync(0xffffffffu, mu, r), a.eps, a.prior, &bb, &g1, &g2);
-          sm.bias[warp][r][lane] = to_f32_finite(bb * static_cast<float>(kLog2e));
+          sm.bias[warp][r][lane] = bias_value(static_cast<float>(d), sm.rows[warp][r]);
         }
         __syncwarp();
       }
@@ -321,7 +366,12 @@ __global__ void __launch_bounds__(kThreads, kResident)
               const int2 kp = *reinterpret_cast<const int2*>(&sm.kpos[warp][s][8 * oc + cq]);
               k0 = max(min(kp.x, rpos[x]), 0);
               k1 = max(min(kp.y, rpos[x]), 0);
-              bad_pos |= (kp.x > rpos[x] && 8 * oc + cq < valid) || (kp.y > rpos[x] && 8 * oc + cq + 1 < valid);
+              if (full) {
+                bad_pos |= k0 != kp.x;
+                bad_pos |= k1 != kp.y;
+              } else {
+                bad_pos |= (k0 != kp.x && 8 * oc + cq < valid) || (k1 != kp.y && 8 * oc + cq + 1 < valid);
+              }
             }
             bi = make_float2(__ldg(brow[x] + k0), __ldg(brow[x] + k1));
           }
@@ -351,8 +401,10 @@ __global__ void __launch_bounds__(kThreads, kResident)
         for (int oc = 0; oc < 4; ++oc) {
           float z0 = fmaf(sacc[oc][2 * x], c[x], bias[x][oc].x);
           float z1 = fmaf(sacc[oc][2 * x + 1], c[x], bias[x][oc].y);
-          if (8 * oc + cq >= valid) z0 = -INFINITY;
-          if (8 * oc + cq + 1 >= valid) z1 = -INFINITY;
+          if (!full) {
+            if (8 * oc + cq >= valid) z0 = -INFINITY;
+            if (8 * oc + cq + 1 >= valid) z1 = -INFINITY;
+          }
           mx = fmax3(mx, z0, z1);
           if (zrow[x]) *reinterpret_cast<float2*>(zrow[x] + kb + 8 * oc + cq) = make_float2(z0, z1);
           sacc[oc][2 * x] = z0;
@@ -378,26 +430,32 @@ __global__ void __launch_bounds__(kThreads, kResident)
         }
       }
       // Weights as bf16 parts: all but the last cut off, none of them negative or, where
-      // the weight is not, zero (an infinite value then stays one: no inf - inf, no 0 * inf).
+      // the weight is not, zero (an infinite value then stays one: no inf - inf, no 0 * inf).  The last
+      // bit of a weight, set, makes sure of the second part; a third has a least value.
       uint32_t pf[2][kParts][4];  // of 16 keys each
 #pragma unroll
       for (int oc = 0; oc < 4; ++oc)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           uint32_t(&w)[kParts][4] = pf[oc >> 1];
-          float p0 = kTwo || x == 0 ? sacc[oc][2 * x] : 0.0f;
-          float p1 = kTwo || x == 0 ? sacc[oc][2 * x + 1] : 0.0f;
-          float least0 = p0 * 0x1p-28f, least1 = p1 * 0x1p-28f;
+          const int at = 2 * (oc & 1) + x;
+          if (!kTwo && x) {
+#pragma unroll
+            for (int y = 0; y < kParts; ++y) w[y][at] = 0;
+            continue;
+          }
+          uint32_t w0 = __float_as_uint(sacc[oc][2 * x]) | 1u, w1 = __float_as_uint(sacc[oc][2 * x + 1]) | 1u;
+          float p0 = __uint_as_float(w0), p1 = __uint_as_float(w1);
+          const float least0 = p0 * 0x1p-36f, least1 = p1 * 0x1p-36f;
 #pragma unroll
           for (int y = 0; y < kParts - 1; ++y) {
-            const uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
-            w[y][2 * (oc & 1) + x] = __byte_perm(w0, w1, 0x7632);
-            p0 = fmaxf(p0 - __uint_as_float(w0 & 0xFFFF0000u), least0);
-            p1 = fmaxf(p1 - __uint_as_float(w1 & 0xFFFF0000u), least1);
-            least0 *= 0x1p-8f;
-            least1 *= 0x1p-8f;
+            w[y][at] = __byte_perm(w0, w1, 0x7632);
+            p0 -= __uint_as_float(w0 & 0xFFFF0000u);
+            p1 -= __uint_as_float(w1 & 0xFFFF0000u);
+            if (y == 1) p0 = fmaxf(p0, least0), p1 = fmaxf(p1, least1);
+            w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
           }
-          w[kParts - 1][2 * (oc & 1) + x] = pack_bf16x2(p0, p1);
+          w[kParts - 1][at] = pack_bf16x2(p0, p1);
         }
       // What lies behind the last key (anything) has no effect: weight 0 times 0.
       if (valid < kKeys) {
@@ -416,13 +474,22 @@ __global__ void __launch_bounds__(kThreads, kResident)
         }
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (kParts < 3) {
 #pragma unroll
-          for (int p = kParts - 1; p >= 0; --p)
+            for (int p = kParts - 1; p >= 0; --p)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) mma_bf16(t, pf[h][p], vf[h][2 * y], vf[h][2 * y + 1]);
+              for (int h = 0; h < 2; ++h) mma_bf16(o[2 * dd + y], pf[h][p], vf[h][2 * y], vf[h][2 * y + 1]);
+          } else {
+            // The tensor core's sums cut off their last place in every step: for fp32 output a
+            // tile's are added outside.
+            float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int x = 0; x < 4; ++x) o[2 * dd + y][x] += t[x];
+            for (int p = kParts - 1; p >= 0; --p)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) mma_bf16(t, pf[h][p], vf[h][2 * y], vf[h][2 * y + 1]);
+#pragma unroll
+            for (int x = 0; x < (kTwo ? 4 : 2); ++x) o[2 * dd + y][x] += t[x];
+          }
         }
       }
       __syncwarp();
@@ -458,31 +525,27 @@ __global__ void __launch_bounds__(kThreads, kResident)
   if (a.copies && blockIdx.x == gridDim.x - 1) grid_dep_wait();
 }
 
-constexpr int kJoinThreads = 256;
-constexpr int kJoinFew = 16;  // slots of a row, at most, that one warp joins
-
-// Joins the parts of a row's keys: eight rows a block, a warp each, or one row.
-template <int kWarpsRow>
-__global__ void __launch_bounds__(kJoinThreads) bam_shared_join_kernel(const SharedArgs a) {
-  constexpr int kRowsBlock = kJoinThreads / 32 / kWarpsRow;
-  __shared__ float red_m[kJoinThreads / 32], red_l[kJoinThreads / 32];
-  __shared__ float2 red_o[kJoinThreads / 32][32];
+// Joins the parts of a row's keys: kWarpsRow warps a row, kRowsBlock rows a block.
+template <int kWarpsRow, int kRowsBlock>
+__global__ void __launch_bounds__(32 * kWarpsRow * kRowsBlock) bam_shared_join_kernel(const SharedArgs a) {
+  __shared__ float red_m[kRowsBlock][kWarpsRow], red_l[kRowsBlock][kWarpsRow];
+  __shared__ float2 red_o[kRowsBlock][kWarpsRow][32];
   grid_dep_wait();
   grid_dep_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % kWarpsRow;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsBlock + warp / kWarpsRow;
-  if (row >= static_cast<int64_t>(a.c.B) * a.H) return;  // (whole blocks if a row has one)
-  const int64_t base = row * a.slots;
+  const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) % kWarpsRow, rb = (threadIdx.x >> 5) / kWarpsRow;
+  const int64_t rows = static_cast<int64_t>(a.c.B) * a.H;
+  const int64_t row_raw = static_cast<int64_t>(blockIdx.x) * kRowsBlock + rb;
+  const int64_t row = min(row_raw, rows - 1), base = row * a.slots;
   const bool aborted = *reinterpret_cast<volatile int*>(&a.c.status->abort) != 0;
   float M = kNoMax;
   for (int s = 32 * part + lane; s < a.slots; s += 32 * kWarpsRow) M = fmaxf(M, a.ml[base + s].x);
 #pragma unroll
   for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
   if (kWarpsRow > 1) {
-    if (lane == 0) red_m[warp] = M;
+    if (lane == 0) red_m[rb][part] = M;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarpsRow; ++w) M = fmaxf(M, red_m[w]);
+    for (int w = 0; w < kWarpsRow; ++w) M = fmaxf(M, red_m[rb][w]);
   }
   float L = 0.0f, o0 = 0.0f, o1 = 0.0f;
 #pragma unroll 8
@@ -496,18 +559,18 @@ __global__ void __launch_bounds__(kJoinThreads) bam_shared_join_kernel(const Sha
     o1 = none ? o1 : fmaf(o.y, f, o1);
   }
   if (kWarpsRow > 1) {
-    if (lane == 0) red_l[warp] = L;
-    red_o[warp][lane] = make_float2(o0, o1);
+    if (lane == 0) red_l[rb][part] = L;
+    red_o[rb][part][lane] = make_float2(o0, o1);
     __syncthreads();
-    if (warp) return;
     L = o0 = o1 = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarpsRow; ++w) {
-      L += red_l[w];
-      o0 += red_o[w][lane].x;
-      o1 += red_o[w][lane].y;
+      L += red_l[rb][w];
+      o0 += red_o[rb][w][lane].x;
+      o1 += red_o[rb][w][lane].y;
     }
   }
+  if (part || row_raw >= rows) return;
   float lse2 = M + __log2f(L), inv = 1.0f / L;
   if (L == 0.0f) {
     bool ok = true;
@@ -532,44 +595,70 @@ __global__ void __launch_bounds__(kJoinThreads) bam_shared_join_kernel(const Sha
 }
 
 constexpr int kWeighThreads = 256;
-constexpr int kWeighKeys = 4 * kWeighThreads;
+constexpr int kWeighFours = 2;  // of a thread
+constexpr int kWeighKeys = 4 * kWeighFours * kWeighThreads;
 
 // w_j <- decay w_j + sum over the heads of the group of exp(z_j - lse).
 __global__ void __launch_bounds__(kWeighThreads) bam_shared_weigh_kernel(const SharedArgs a) {
-  grid_dep_wait();
-  if (*reinterpret_cast<volatile int*>(&a.c.status->abort)) return;
   const int hk = blockIdx.y, b = blockIdx.z;
   bool ok = true;
-  const int len = own_len(a, b, &ok);
-  const int j = blockIdx.x * kWeighKeys + 4 * threadIdx.x;
-  if (j >= len) return;
-  float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int len = own_len(a, b, &ok), j0 = blockIdx.x * kWeighKeys + 4 * threadIdx.x;
+  // What no kernel of the call writes is on its way before the logits are there.
+  float* at[kWeighFours];
+  float4 old[kWeighFours];
+#pragma unroll
+  for (int x = 0; x < kWeighFours; ++x) {
+    const int j = j0 + 4 * kWeighThreads * x;
+    at[x] = nullptr;
+    if (j >= len) continue;
+    const int pg = __ldg(a.c.block_table + static_cast<size_t>(b) * a.c.max_blocks + j / a.c.page);
+    if (pg < 0 || pg >= a.c.num_pages) continue;
+    at[x] = a.key_weight + (static_cast<int64_t>(pg) * a.c.Hkv + hk) * a.c.page + j % a.c.page;
+    old[x] = *reinterpret_cast<const float4*>(at[x]);
+  }
+  grid_dep_wait();
+  if (*reinterpret_cast<volatile int*>(&a.c.status->abort)) return;
+  float w[kWeighFours][4] = {};
   for (int g = 0; g < a.group; ++g) {
     const int64_t row = static_cast<int64_t>(b) * a.H + hk * a.group + g;
     const float lse = a.ml[row * a.slots].x;
-    const float4 z = *reinterpret_cast<const float4*>(a.z + row * a.zstride + j);
-    w[0] += ex2_approx(z.x - lse);
-    w[1] += ex2_approx(z.y - lse);
-    w[2] += ex2_approx(z.z - lse);
-    w[3] += ex2_approx(z.w - lse);
-  }
-  const int pg = __ldg(a.c.block_table + static_cast<size_t>(b) * a.c.max_blocks + j / a.c.page);
-  if (pg < 0 || pg >= a.c.num_pages) return;
-  float* dst = a.key_weight + (static_cast<int64_t>(pg) * a.c.Hkv + hk) * a.c.page + j % a.c.page;
 #pragma unroll
-  for (int x = 0; x < 4; ++x)
-    if (j + x < len) dst[x] = fmaf(a.decay, dst[x], w[x]);
+    for (int x = 0; x < kWeighFours; ++x) {
+      if (!at[x]) continue;
+      const float4 z = *reinterpret_cast<const float4*>(a.z + row * a.zstride + j0 + 4 * kWeighThreads * x);
+      w[x][0] += ex2_approx(z.x - lse);
+      w[x][1] += ex2_approx(z.y - lse);
+      w[x][2] += ex2_approx(z.z - lse);
+      w[x][3] += ex2_approx(z.w - lse);
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < kWeighFours; ++x) {
+    if (!at[x]) continue;
+    const float o[4] = {old[x].x, old[x].y, old[x].z, old[x].w};
+    const int left = len - (j0 + 4 * kWeighThreads * x);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) w[x][y] = fmaf(a.decay, o[y], w[x][y]);
+    if (left >= 4) {
+      *reinterpret_cast<float4*>(at[x]) = make_float4(w[x][0], w[x][1], w[x][2], w[x][3]);
+    } else {
+#pragma unroll
+      for (int y = 0; y < 3; ++y)
+        if (y < left) at[x][y] = w[x][y];
+    }
+  }
 }
 
 }  // namespace
 
 // Parts of up to `most` keys of each of `rows` item rows: two items a warp, or up to six of 512
 // keys and more, so that the last ones end alike.
+constexpr int kItemsFew = 2, kItemsMany = 6, kItemKeys = 512;
 static int split_keys(int64_t rows, int64_t most) {
   const int64_t warps = 152 * kResident * kWarps;
-  const int64_t two = (2 * warps + rows - 1) / rows, six = (6 * warps + rows - 1) / rows;
-  int64_t n = most / 512 > two ? most / 512 : two;
-  if (n > six) n = six;
+  const int64_t few = (kItemsFew * warps + rows - 1) / rows, many = (kItemsMany * warps + rows - 1) / rows;
+  int64_t n = most / kItemKeys > few ? most / kItemKeys : few;
+  if (n > many) n = many;
   const int64_t cap = (most + kLeastKeys - 1) / kLeastKeys;
   return static_cast<int>(n < cap ? n : cap);
 }
@@ -634,12 +723,14 @@ cudaError_t launch_shared(const CUtensorMap& tk, const CUtensorMap& tv, const Sh
 
 cudaError_t launch_shared_join(const SharedArgs& a, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(a.c.B) * a.H;
-  constexpr int kWide = kJoinThreads / 32;
-  if (a.slots <= kJoinFew)
-    return launch_k(bam_shared_join_kernel<1>, dim3(static_cast<unsigned>((rows + kWide - 1) / kWide)),
-                    dim3(kJoinThreads), 0, st, true, a);
-  return launch_k(bam_shared_join_kernel<kWide>, dim3(static_cast<unsigned>(rows)), dim3(kJoinThreads), 0,
-                  st, true, a);
+  auto launch = [&](auto* kernel, int warps, int block) {
+    return launch_k(kernel, dim3(static_cast<unsigned>((rows + block - 1) / block)), dim3(32 * warps * block), 0,
+                    st, true, a);
+  };
+  // (8192 rows of 7 parts: 7 us by a warp each, 12 by four; 768 rows of 55: 10 and 7)
+  if (a.slots <= 4 || (a.slots <= 16 && rows > 2048)) return launch(bam_shared_join_kernel<1, 8>, 1, 8);
+  if (a.slots <= 64) return launch(bam_shared_join_kernel<4, 2>, 4, 2);
+  return launch(bam_shared_join_kernel<32, 1>, 32, 1);
 }
 
 cudaError_t launch_shared_weigh(const SharedArgs& a, cudaStream_t st) {
