@@ -322,8 +322,8 @@ SharedWs shared_ws(const SharedArgs& a, bool marked) {
   w.z = w.part + align256(rows * a.slots * kHeadDim * 4);
   w.table = w.z + (marked ? align256(rows * a.zstride * 4) : 0);
   w.total = w.table;
-  if (a.use_table)
-    w.total += align256(((a.copies ? kTabCopies : 1) * static_cast<size_t>(a.H) * a.tab_len + kTabPadFloats) * 4);
+  if (a.copies)
+    w.total += align256((kTabCopies * static_cast<size_t>(a.H) * a.tab_len + kTabPadFloats) * 4);
   return w;
 }
 
@@ -794,7 +794,7 @@ bam_status bam_attn_decode_shared_paged(const void* q, const void* k_pages, cons
   a.lse = lse;
   a.ml = reinterpret_cast<float2*>(wsb + w.ml);
   a.part = reinterpret_cast<float*>(wsb + w.part);
-  if (a.use_table) a.table = reinterpret_cast<float*>(wsb + w.table);
+  if (a.copies) a.table = reinterpret_cast<float*>(wsb + w.table);
   cudaError_t e =
       launch_kernel(BAM_KERNEL_SHARED_PREP, stream, [&] { return launch_shared_prep(a, stream); });
   if (e != cudaSuccess) return BAM_ERR_CUDA;

@@ -8,9 +8,10 @@
 // tcgen05.  Rows stand at positions of their own, so that each has its own window of its
 // head's table of biases: 4 bytes a row and key out of L2, staged with the keys.
 //
-// Warps 0-3: softmax, one thread a row (its lane of Tensor Memory).  Warp 4: K and V by TMA and
-// the windows by asynchronous 16-byte copies, into a ring (a bulk copy per window took 4.4 us a
-// tile).  Warp 5, one thread: S = Q K^T (Q in Tensor Memory) and O += P V (P in Tensor Memory).
+// Warps 0-7: softmax, two threads a row (its lane of Tensor Memory), each with half of a tile's
+// keys; they exchange their maxima.  Warp 8: K and V by TMA and the windows by
+// asynchronous 16-byte copies, into a ring (a bulk copy per window took 4.4 us a tile).
+// Warp 9, one thread: S = Q K^T (Q in Tensor Memory) and O += P V (P in Tensor Memory).
 //
 // With up to 64 rows a row stands in two or four lanes, each with its part of a tile's keys and
 // zeros for the weights of the others.
@@ -19,14 +20,15 @@
 namespace bam {
 namespace {
 
-constexpr int kSoftWarps = 4;
+constexpr int kSoftWarps = 8;
+constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
 constexpr int kThreads = 32 * (kSoftWarps + 2);
 constexpr int kTile = 64;                      // keys
 constexpr int kLanes = 128;
 constexpr int kBoxBytes = kTile * kHeadDim * 2;
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 5;
 constexpr int kResident = 2;                   // CTAs of an SM
-constexpr int kSmemMost = 112 * 1024;
+constexpr int kSmemMost = 111 * 1024;
 constexpr float kRescale = 8.0f;               // log2 units by which a weight may exceed 1
 
 // Tensor Memory columns: S, O, P (up to three parts), Q.
@@ -41,22 +43,31 @@ enum : int {
   kSitePrefixS = 99,
   kSitePrefixWin = 100,
   kSitePrefixPV = 101,
-  kSitePrefixTable = 102  // debug build: bounds of a copy of a window
+  kSitePrefixPair = 102,
+  kSitePrefixTable = 103  // debug build: bounds of a copy of a window
 };
 
 template <int kCopies>
 struct Shape {
-  static constexpr int kCols = kTile / kCopies;      // keys of a lane in a tile
+  static constexpr int kWin = kTile / kCopies;       // keys of a lane in a tile
+  static constexpr int kCols = kWin / 2;             // of a thread
   static constexpr int kRows = kLanes / kCopies;     // rows of an item
-  static constexpr int kWinStride = kCols + 4;       // floats: 16-byte reads of eight rows hit all banks
-  static constexpr int kStageBytes = 2 * kBoxBytes + kLanes * kWinStride * 4;
-  static constexpr int kStages =
-      kSmemMost / kStageBytes < kMaxStages ? kSmemMost / kStageBytes : kMaxStages;
+  static constexpr int kWinStride = kWin + 4;        // floats: 16-byte reads of eight rows hit all banks
+  static constexpr int kWinBytes = kLanes * kWinStride * 4;
+  // Rings: windows are free again when they have been read, K when S is there, V last.
+  static constexpr int kWinStages = 2;
+  static constexpr int kBoxes = (kSmemMost - kWinStages * kWinBytes) / kBoxBytes;
+  static constexpr int kVStages = (kBoxes + 1) / 2 < kMaxStages ? (kBoxes + 1) / 2 : kMaxStages;
+  static constexpr int kKStages = kBoxes / 2 < kMaxStages ? kBoxes / 2 : kMaxStages;
+  static constexpr int kV = kKStages * kBoxBytes, kW = kV + kVStages * kBoxBytes;  // behind the K ring
+  static constexpr int kSmem = kW + kWinStages * kWinBytes;
 };
 
 struct PrefixBars {
-  uint64_t kv_full[kMaxStages], win_full[kMaxStages], empty[kMaxStages];
-  uint64_t q_full, s_full, s_free, p_full, pv_done, final;
+  uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
+  uint64_t win_full[2], win_empty[2];
+  uint64_t q_full, s_full, s_free, p_full, pv_done, final, pair[4];
+  float max[2][2][kLanes];  // of a row's halves, by the tile's parity
   uint32_t win[kLanes];  // where each lane's window begins in the table, in 16-byte words
   uint32_t tmem;
   int abort_flag;
@@ -78,18 +89,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, DevSta
 
 template <int kN>
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* r) {
-  if constexpr (kN == 64) {
-    tmem_ld_32x32b_x32(at, r);
-    tmem_ld_32x32b_x32(at + 32, r + 32);
-  } else if constexpr (kN == 32) {
-    tmem_ld_32x32b_x32(at, r);
-  } else {
-    tmem_ld_32x32b_x16(at, r);
-  }
+  if constexpr (kN == 32) tmem_ld_32x32b_x32(at, r);
+  if constexpr (kN == 16) tmem_ld_32x32b_x16(at, r);
+  if constexpr (kN == 8) tmem_ld_32x32b_x8(at, r);
   tmem_ld_wait();
-  if constexpr (kN >= 32) reg_fence32(r);
-  if constexpr (kN == 64) reg_fence32(r + 32);
+  if constexpr (kN == 32) reg_fence32(r);
   if constexpr (kN == 16) reg_fence16(r);
+  if constexpr (kN == 8) reg_fence8(r);
 }
 // A row of the item: query head h of sequence b, or none.
 struct RowAt {
@@ -111,7 +117,8 @@ __global__ void __launch_bounds__(kThreads, kResident)
     bam_prefix_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                       const SharedArgs a) {
   using S = Shape<kCopies>;
-  constexpr int kCols = S::kCols, kStages = S::kStages, kFlush = kParts == 3 ? 8 : 128;
+  constexpr int kCols = S::kCols, kFlush = kParts == 3 ? 8 : 128;
+  constexpr int kKStages = S::kKStages, kVStages = S::kVStages, kWinStages = S::kWinStages;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ PrefixBars bars;
   uint8_t* const ring = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
@@ -132,10 +139,17 @@ __global__ void __launch_bounds__(kThreads, kResident)
 
   if (threadIdx.x == 0) {
     bars.abort_flag = 0;
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars.kv_full[s], 1);
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(&bars.k_full[s], 1);
+      mbar_init(&bars.k_empty[s], 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(&bars.v_full[s], 1);
+      mbar_init(&bars.v_empty[s], 1);
+    }
+    for (int s = 0; s < kWinStages; ++s) {
       mbar_init(&bars.win_full[s], 32);
-      mbar_init(&bars.empty[s], 1 + kSoftWarps);
+      mbar_init(&bars.win_empty[s], kSoftWarps);
     }
     mbar_init(&bars.q_full, kSoftWarps);
     mbar_init(&bars.s_full, 1);
@@ -143,20 +157,21 @@ __global__ void __launch_bounds__(kThreads, kResident)
     mbar_init(&bars.p_full, kSoftWarps);
     mbar_init(&bars.pv_done, 1);
     mbar_init(&bars.final, 1);
+    for (int x = 0; x < 4; ++x) mbar_init(&bars.pair[x], 2);
     fence_barrier_init();
   }
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tmem_alloc(&bars.tmem, kTmemCols);
     tmem_relinquish();
   }
   // A lane's row and window: it begins on a 16-byte boundary in the copy of the table that is
   // shifted by as much as is missing.
-  const int ln = threadIdx.x, c = ln / S::kRows;
+  const int ln = threadIdx.x % kLanes, half = threadIdx.x / kLanes, c = ln / S::kRows;
   const RowAt r = row_at(a, hk, row0 + ln % S::kRows);
   int pos = 0;
   if (warp < kSoftWarps) {
     pos = r.on ? query_pos(a, r.b, P, &ok_arg) : 0;
-    const int y = a.tab_top - (r.on ? pos : max(P - 1, 0)) + kbeg + c * kCols, k = (4 - (y & 3)) & 3;
+    const int y = a.tab_top - (r.on ? pos : max(P - 1, 0)) + kbeg + c * S::kWin, k = (4 - (y & 3)) & 3;
     bars.win[ln] = static_cast<uint32_t>((static_cast<int64_t>(k) * a.H + (r.on ? r.h : 0)) * (a.tab_len / 4) +
                                          (y + k) / 4);
   }
@@ -165,39 +180,49 @@ __global__ void __launch_bounds__(kThreads, kResident)
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
 
-  if (warp == 4) {
+  if (warp == kCopyWarp) {
     // ------------------------------------------------------------ copies
-    constexpr int kChunks = kCols / 4, kStep = 32 / kChunks;  // 16-byte words of a window; windows at a time
+    constexpr int kChunks = S::kWin / 4, kStep = 32 / kChunks;  // 16-byte words of a window; windows at a time
     const int chunk = lane % kChunks;
     const uint4* src = reinterpret_cast<const uint4*>(a.table) + chunk;
     uint32_t win[kLanes / kStep];
 #pragma unroll
     for (int x = 0; x < kLanes / kStep; ++x) win[x] = bars.win[lane / kChunks + kStep * x];
-    const uint32_t dst = smem_u32(ring + 2 * kBoxBytes) + 16 * chunk + lane / kChunks * S::kWinStride * 4;
+    const uint32_t dst = smem_u32(ring + S::kW) + 16 * chunk + lane / kChunks * S::kWinStride * 4;
     bool bad_page = false;
-    int issued = 0, blk = kbeg / a.c.page, in = kbeg - blk * a.c.page;
+    int k_issued = 0, v_issued = 0, blk = kbeg / a.c.page, in = kbeg - blk * a.c.page;
     int next = tiles ? __ldg(a.prefix_table + blk) : 0;  // the next tile's page, on its way
     for (int it = 0; it < tiles; ++it) {
-      const int s = it % kStages;
-      if (it >= kStages && !warp_wait(&bars.empty[s], (it / kStages - 1) & 1, status, ab, kSitePrefixProducer))
+      const int ks = it % kKStages, vs = it % kVStages, s = it % kWinStages;
+      if (it >= kKStages &&
+          !warp_wait(&bars.k_empty[ks], (it / kKStages - 1) & 1, status, ab, kSitePrefixProducer))
+        break;
+      int pg = next;
+      if (pg < 0 || pg >= a.c.num_pages) {
+        bad_page = true;
+        pg = 0;
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars.k_full[ks], kBoxBytes);
+        tma_load_3d(ring + ks * kBoxBytes, &tk, &bars.k_full[ks], 0, in, pg * a.c.Hkv + hk);
+      }
+      k_issued = it + 1;
+      if (it >= kVStages &&
+          !warp_wait(&bars.v_empty[vs], (it / kVStages - 1) & 1, status, ab, kSitePrefixProducer))
         break;
       if (lane == 0) {
-        uint8_t* stage = ring + s * S::kStageBytes;
-        int pg = next;
-        if (pg < 0 || pg >= a.c.num_pages) {
-          bad_page = true;
-          pg = 0;
-        }
-        mbar_arrive_expect_tx(&bars.kv_full[s], 2 * kBoxBytes);
-        tma_load_3d(stage, &tk, &bars.kv_full[s], 0, in, pg * a.c.Hkv + hk);
-        tma_load_3d(stage + kBoxBytes, &tv, &bars.kv_full[s], 0, in, pg * a.c.Hkv + hk);
-        in += kTile;
-        if (in == a.c.page) {
-          in = 0;
-          if (it + 1 < tiles) next = __ldg(a.prefix_table + ++blk);
-        }
+        mbar_arrive_expect_tx(&bars.v_full[vs], kBoxBytes);
+        tma_load_3d(ring + S::kV + vs * kBoxBytes, &tv, &bars.v_full[vs], 0, in, pg * a.c.Hkv + hk);
       }
-      issued = it + 1;
+      v_issued = it + 1;
+      in += kTile;
+      if (in == a.c.page) {
+        in = 0;
+        if (it + 1 < tiles) next = __ldg(a.prefix_table + ++blk);
+      }
+      if (it >= kWinStages &&
+          !warp_wait(&bars.win_empty[s], (it / kWinStages - 1) & 1, status, ab, kSitePrefixProducer))
+        break;
       if (it == 0) {
         grid_dep_wait();  // the table, and the call's start
         grid_dep_trigger();
@@ -211,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
           continue;
         }
 #endif
-        copy16(dst + s * S::kStageBytes + x * kStep * S::kWinStride * 4, src + win[x]);
+        copy16(dst + s * S::kWinBytes + x * kStep * S::kWinStride * 4, src + win[x]);
       }
       src += kTile / 4;
       arrive_copied(&bars.win_full[s]);
@@ -221,25 +246,29 @@ __global__ void __launch_bounds__(kThreads, kResident)
       grid_dep_trigger();
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (lane == 0)
-      for (int it = max(0, issued - kStages); it < issued; ++it)
-        mbar_drain(&bars.kv_full[it % kStages], (it / kStages) & 1);
+    if (lane == 0) {
+      for (int it = max(0, k_issued - kKStages); it < k_issued; ++it)
+        mbar_drain(&bars.k_full[it % kKStages], (it / kKStages) & 1);
+      for (int it = max(0, v_issued - kVStages); it < v_issued; ++it)
+        mbar_drain(&bars.v_full[it % kVStages], (it / kVStages) & 1);
+    }
     __syncwarp();
     if (bad_page) record_bad_arg(status);
-  } else if (warp == 5) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
     if (lane == 0) {
       const uint32_t idS = idesc_bf16(kLanes, kTile, false, false);
       const uint32_t idO = idesc_bf16(kLanes, kHeadDim, false, true);
       auto issue_s = [&](int it) {
-        const int s = it % kStages;
-        if (!mbar_wait(&bars.kv_full[s], (it / kStages) & 1, status, ab, kSitePrefixK)) return false;
+        const int s = it % kKStages;
+        if (!mbar_wait(&bars.k_full[s], (it / kKStages) & 1, status, ab, kSitePrefixK)) return false;
         tc_fence_after();
-        const uint64_t kd = sdesc_sw128(smem_u32(ring + s * S::kStageBytes), 16, 1024);
+        const uint64_t kd = sdesc_sw128(smem_u32(ring + s * kBoxBytes), 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < kHeadDim / 16; ++kk)
           umma_ts(tmem + kColS, tmem + kColQ + 8 * kk, kd + 2 * kk, idS, kk > 0);
         umma_commit(&bars.s_full);
+        umma_commit(&bars.k_empty[s]);
         return true;
       };
       bool ok = tiles == 0 || mbar_wait(&bars.q_full, 0, status, ab, kSitePrefixQ);
@@ -251,11 +280,12 @@ __global__ void __launch_bounds__(kThreads, kResident)
           if (ok) ok = issue_s(it + 1);
           if (!ok) break;
         }
-        ok = mbar_wait(&bars.p_full, it & 1, status, ab, kSitePrefixP);
+        const int s = it % kVStages;
+        ok = mbar_wait(&bars.v_full[s], (it / kVStages) & 1, status, ab, kSitePrefixK) &&
+             mbar_wait(&bars.p_full, it & 1, status, ab, kSitePrefixP);
         if (!ok) break;
         tc_fence_after();
-        const int s = it % kStages;
-        const uint64_t vd = sdesc_sw128(smem_u32(ring + s * S::kStageBytes + kBoxBytes), 16384, 1024);
+        const uint64_t vd = sdesc_sw128(smem_u32(ring + S::kV + s * kBoxBytes), 16384, 1024);
 #pragma unroll
         for (int p = kParts - 1; p >= 0; --p)
 #pragma unroll
@@ -263,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
             umma_ts(tmem + kColO, tmem + kColP + 32 * p + 8 * kk, vd + 128 * kk, idO,
                     it % kFlush != 0 || p < kParts - 1 || kk > 0);
         umma_commit(&bars.pv_done);
-        umma_commit(&bars.empty[s]);
+        umma_commit(&bars.v_empty[s]);
       }
       // Every product is done before Tensor Memory is freed.
       umma_commit(&bars.final);
@@ -283,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, kResident)
                              : make_uint4(0, 0, 0, 0);
         q[4 * x] = w.x, q[4 * x + 1] = w.y, q[4 * x + 2] = w.z, q[4 * x + 3] = w.w;
       }
-      tmem_st_32x32b_x32(tl + kColQ, q);
-      if (kCopies > 1) {  // weights of the other copies' keys
+      if (half == 0) tmem_st_32x32b_x32(tl + kColQ, q);
+      if (kCopies > 1 && half == 1) {  // weights of the other copies' keys
         uint32_t zero[32];
 #pragma unroll
         for (int x = 0; x < 32; ++x) zero[x] = 0;
@@ -300,15 +330,15 @@ __global__ void __launch_bounds__(kThreads, kResident)
     const int64_t slot = row * a.slots + a.nsplit + sp * kCopies + c;
     float m = kNoMax, l = 0.0f, m_out = kNoMax;  // m_out: the maximum that what has left O is relative to
     bool first = true, ok = true;
-    // Adds O to this row's partial output.
+    // Adds this half of O's columns to the row's partial output.
     auto flush = [&]() {
-      float4* out = reinterpret_cast<float4*>(a.part + slot * kHeadDim);
+      float4* out = reinterpret_cast<float4*>(a.part + slot * kHeadDim) + 8 * half;
       const float f = ex2_approx(m_out - m);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
+      for (int x = 0; x < 2; ++x) {
         uint32_t o[16];
         __syncwarp();
-        tmem_ld<16>(tl + kColO + 16 * x, o);
+        tmem_ld<16>(tl + kColO + 32 * half + 16 * x, o);
         if (r.on) {
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
@@ -326,19 +356,21 @@ __global__ void __launch_bounds__(kThreads, kResident)
       m_out = m;
       first = false;
     };
+    const int col = c * S::kWin + half * kCols;  // this thread's first key in a tile
+    uint64_t* const pair = &bars.pair[warp & 3];
     const uint64_t cr2 = f2_pack(cr, cr);
     for (int it = 0; it < tiles; ++it) {
-      const int s = it % kStages;
-      const uint8_t* stage = ring + s * S::kStageBytes;
+      const int s = it % kWinStages, vs = it % kVStages;
       ok = warp_wait(&bars.s_full, it & 1, status, ab, kSitePrefixS) &&
-           warp_wait(&bars.win_full[s], (it / kStages) & 1, status, ab, kSitePrefixWin);
+           warp_wait(&bars.win_full[s], (it / kWinStages) & 1, status, ab, kSitePrefixWin);
       if (!ok) break;
       tc_fence_after();
       uint64_t z[kCols / 2];
       {
         uint32_t sv[kCols];
-        tmem_ld<kCols>(tl + kColS + c * kCols, sv);
-        const float* win = reinterpret_cast<const float*>(stage + 2 * kBoxBytes) + ln * S::kWinStride;
+        tmem_ld<kCols>(tl + kColS + col, sv);
+        const float* win =
+            reinterpret_cast<const float*>(ring + S::kW + s * S::kWinBytes) + ln * S::kWinStride + half * kCols;
 #pragma unroll
         for (int x = 0; x < kCols / 2; x += 2) {
           uint64_t b0, b1;
@@ -351,20 +383,20 @@ __global__ void __launch_bounds__(kThreads, kResident)
       const int valid = kend - kbeg - it * kTile;  // keys of the tile
       if (valid < kTile) {
         // What lies behind the last key (anything) has no effect: weight 0 times 0.
-        ok = warp_wait(&bars.kv_full[s], (it / kStages) & 1, status, ab, kSitePrefixK);
+        ok = warp_wait(&bars.v_full[vs], (it / kVStages) & 1, status, ab, kSitePrefixK);
         if (!ok) break;
-        for (int y = ln; y < (kTile - valid) * 8; y += 32 * kSoftWarps)
-          *reinterpret_cast<uint4*>(ring + s * S::kStageBytes + kBoxBytes + valid * 128 + 16 * y) =
+        for (int y = threadIdx.x; y < (kTile - valid) * 8; y += 32 * kSoftWarps)
+          *reinterpret_cast<uint4*>(ring + S::kV + vs * kBoxBytes + valid * 128 + 16 * y) =
               make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
       }
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&bars.s_free);
-        mbar_arrive(&bars.empty[s]);
+        mbar_arrive(&bars.win_empty[s]);
       }
       if (valid < kTile) {
-        const int lim = valid - c * kCols;
+        const int lim = valid - col;
 #pragma unroll
         for (int x = 0; x < kCols / 2; ++x) {
           float z0, z1;
@@ -372,14 +404,24 @@ __global__ void __launch_bounds__(kThreads, kResident)
           z[x] = f2_pack(2 * x < lim ? z0 : -INFINITY, 2 * x + 1 < lim ? z1 : -INFINITY);
         }
       }
-      float mq[4];
+      constexpr int kChains = kCols / 2 < 4 ? kCols / 2 : 4;
+      float mq[kChains];
 #pragma unroll
       for (int x = 0; x < kCols / 2; ++x) {
         float z0, z1;
         f2_unpack(z[x], z0, z1);
-        mq[x & 3] = x < 4 ? fmaxf(z0, z1) : fmax3(mq[x & 3], z0, z1);
+        mq[x % kChains] = x < kChains ? fmaxf(z0, z1) : fmax3(mq[x % kChains], z0, z1);
       }
-      const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+      float mx = mq[0];
+#pragma unroll
+      for (int x = 1; x < kChains; ++x) mx = fmaxf(mx, mq[x]);
+      // The row's maximum: of both halves.
+      bars.max[it & 1][half][ln] = mx;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair);
+      ok = warp_wait(pair, it & 1, status, ab, kSitePrefixPair);
+      if (!ok) break;
+      mx = fmaxf(mx, bars.max[it & 1][half ^ 1][ln]);
       if (it > 0) {
         // P V of the last tile: it has read P, and O is at rest.
         ok = warp_wait(&bars.pv_done, (it - 1) & 1, status, ab, kSitePrefixPV);
@@ -398,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
       const uint64_t negm2 = f2_pack(-m, -m);
       const uint64_t minus = f2_pack(-1.0f, -1.0f);
       uint64_t sum[2] = {0, 0};
-      constexpr int kStep = kCols / 2 < 8 ? kCols / 2 : 8;  // pairs at a time
+      constexpr int kStep = kCols / 2 < 8 ? kCols / 2 : 8;  // pairs at a time (4 or 8)
 #pragma unroll
       for (int q = 0; q < kCols / 2; q += kStep) {
         uint32_t pk[kParts][kStep];
@@ -423,22 +465,22 @@ __global__ void __launch_bounds__(kThreads, kResident)
         }
 #pragma unroll
         for (int p = 0; p < kParts; ++p)
-          tmem_st_32x32b_x8(tl + kColP + 32 * p + c * (kCols / 2) + q, pk[p]);
+          if constexpr (kStep == 8)
+            tmem_st_32x32b_x8(tl + kColP + 32 * p + col / 2 + q, pk[p]);
+          else
+            tmem_st_32x32b_x4(tl + kColP + 32 * p + col / 2 + q, pk[p]);
       }
       {
         float s0, s1;
         f2_unpack(fadd2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
       }
-      if (!fresh && __any_sync(0xffffffffu, grow)) {
+      if (!fresh && __any_sync(0xffffffffu, grow)) {  // each half its columns of O
+        uint32_t o[32];
+        tmem_ld<32>(tl + kColO + 32 * half, o);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t o[32];
-          tmem_ld<32>(tl + kColO + 32 * x, o);
-#pragma unroll
-          for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * scale);
-          tmem_st_32x32b_x32(tl + kColO + 32 * x, o);
-        }
+        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * scale);
+        tmem_st_32x32b_x32(tl + kColO + 32 * half, o);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -450,7 +492,14 @@ __global__ void __launch_bounds__(kThreads, kResident)
       tc_fence_after();
       if (ok) flush();
     }
-    if (ok && r.on) a.ml[slot] = make_float2(m, l);
+    if (ok) {
+      // The row's sum: of both halves.
+      if (half == 1) bars.max[tiles & 1][1][ln] = l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair);
+      ok = warp_wait(pair, tiles & 1, status, ab, kSitePrefixPair);
+      if (ok && r.on && half == 0) a.ml[slot] = make_float2(m, l + bars.max[tiles & 1][1][ln]);
+    }
     if (!ok_arg) {
       grid_dep_wait();  // (the call's start clears what fresh memory held)
       record_bad_arg(status);
@@ -458,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -470,7 +519,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArg
   const int64_t blocks = (static_cast<int64_t>(a.c.B) * a.group + S::kRows - 1) / S::kRows;
   const int64_t items = blocks * a.c.Hkv * a.npsplit;
   if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const size_t smem = S::kStages * S::kStageBytes + 1024;
+  const size_t smem = S::kSmem + 1024;
   static bool limit_set[64] = {};
   const cudaError_t e = smem_limit_once(bam_prefix_kernel<kCopies, kParts>, smem, limit_set);
   if (e != cudaSuccess) return e;
@@ -480,7 +529,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArg
 
 }  // namespace
 
-void prefix_split(SharedArgs* a, int64_t Pmax) {
+void prefix_split(SharedArgs* a, int64_t Pmax, int64_t Tmax) {
   const int64_t rows = static_cast<int64_t>(a->c.B) * a->group;
   a->copies = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
   const int64_t base = (rows * a->copies + kLanes - 1) / kLanes * a->c.Hkv;
@@ -496,6 +545,10 @@ void prefix_split(SharedArgs* a, int64_t Pmax) {
       a->npsplit = static_cast<int>(n);
     }
   }
+  // Distances of the prefix's keys, and behind them windows that reach past the last key.
+  const int64_t top = a->max_pos > 0 ? (a->max_pos > Pmax ? a->max_pos : Pmax) : Pmax + Tmax;
+  a->tab_top = static_cast<int>(top - 1);
+  a->tab_len = static_cast<int>((top + kTile + 8 + 63) / 64 * 64);
 }
 
 cudaError_t launch_prefix(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArgs& a,

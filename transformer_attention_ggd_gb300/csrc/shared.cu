@@ -1,22 +1,11 @@
 // Decode over a paged cache whose first keys a whole batch shares and whose own
 // keys may carry positions and accumulated weights, on sm_103a.
 #include "shared_common.cuh"
-#include "table_eval.cuh"
 
 namespace bam {
 namespace {
 
-constexpr int kWarps = 4;                    // of a CTA, each on items of its own
-constexpr int kThreads = 32 * kWarps;
-constexpr int kResident = 3;                 // CTAs of an SM
-constexpr int kStages = 2;                   // of a warp's ring
-constexpr int kKeys = 32;                    // of a stage
-constexpr int kRows = 16;                    // of an item
-constexpr int kBoxBytes = kKeys * kHeadDim * 2;
-constexpr int kBiasStride = kKeys + 8;       // floats: 8-byte reads of four rows hit all banks
-constexpr float kRescale = 8.0f;
-
-// A row's prior for biases that are evaluated in the attention kernel itself:
+// A row's prior, ready to be evaluated:
 //   b log2(e) = -log2(e) 2^y,  y = beta (log2 u - log2 alpha),  u = |d - mu| (at least eps where beta <= 0),
 // or, with the theta prior, y = theta_beta log2(|d - mu| + eps) + theta_alpha log2(e).
 struct __align__(16) BiasRow {
@@ -63,6 +52,16 @@ __device__ __forceinline__ float bias_value(float d, const BiasRow& r) {
   return u == 0.0f ? 0.0f : fmaxf(b, -3.0e38f);
 }
 
+constexpr int kWarps = 4;                    // of a CTA, each on items of its own
+constexpr int kThreads = 32 * kWarps;
+constexpr int kResident = 3;                 // CTAs of an SM
+constexpr int kStages = 2;                   // of a warp's ring
+constexpr int kKeys = 32;                    // of a stage
+constexpr int kRows = 16;                    // of an item
+constexpr int kBoxBytes = kKeys * kHeadDim * 2;
+constexpr int kBiasStride = kKeys + 8;       // floats: 8-byte reads of four rows hit all banks
+constexpr float kRescale = 8.0f;
+
 template <bool kTwo>
 struct __align__(1024) SharedSmem {
   uint8_t k[kWarps][kStages][kBoxBytes];
@@ -107,9 +106,10 @@ static_assert(sizeof(DevStatus) <= 128 && kStatusBytes >= 256, "place of the ite
 
 constexpr int kPrepThreads = 256;
 
-// Starts the call and fills the table, if there is one, up to the largest distance.
+// Starts the call and, for a prefix in tiles, fills its table over the distances that its keys have
+// from the queries.
 __global__ void __launch_bounds__(kPrepThreads) bam_shared_prep_kernel(const SharedArgs a) {
-  __shared__ int most;  // position of any query, at most
+  __shared__ int least, most;  // position of any query
   grid_dep_trigger();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
     status_begin_call(a.c.status);
@@ -118,20 +118,31 @@ __global__ void __launch_bounds__(kPrepThreads) bam_shared_prep_kernel(const Sha
   if (!a.table) return;
   bool ok = true;
   const int P = prefix_len(a, &ok);
-  if (threadIdx.x == 0) most = -1;
+  if (P == 0) return;
+  if (threadIdx.x == 0) least = 0x7FFFFFFF, most = -1;
   __syncthreads();
-  int hi = -1;
-  for (int b = threadIdx.x; b < a.c.B; b += kPrepThreads) hi = max(hi, query_pos(a, b, P, &ok));
-  atomicMax(&most, hi);
+  int lo = 0x7FFFFFFF, hi = -1;
+  for (int b = threadIdx.x; b < a.c.B; b += kPrepThreads) {
+    const int pos = query_pos(a, b, P, &ok);
+    lo = min(lo, pos);
+    hi = max(hi, pos);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if ((threadIdx.x & 31) == 0) {
+    atomicMin(&least, lo);
+    atomicMax(&most, hi);
+  }
   __syncthreads();
-  const int h = blockIdx.y, copies = a.copies ? kTabCopies : 1;
-  const float alpha = a.alpha[h], beta = a.beta[h], mu = a.mu[h];
-  for (int d = blockIdx.x * kPrepThreads + threadIdx.x; d <= most; d += gridDim.x * kPrepThreads) {
-    float b, g1, g2;
-    bias_terms<false>(d, alpha, beta, mu, a.eps, a.prior, &b, &g1, &g2);
-    b = to_f32_finite(b * static_cast<float>(kLog2e));
-    for (int k = 0; k < copies; ++k)
-      a.table[(static_cast<int64_t>(k) * a.H + h) * a.tab_len + (a.tab_top - d) + k] = b;
+  const int h = blockIdx.y;
+  const BiasRow row = bias_row(a, h);
+  float* tab = a.table + static_cast<int64_t>(h) * a.tab_len + a.tab_top;
+  const int64_t copy = static_cast<int64_t>(a.H) * a.tab_len + 1;
+  for (int d = least - P + 1 + blockIdx.x * kPrepThreads + threadIdx.x; d <= most;
+       d += gridDim.x * kPrepThreads) {
+    const float b = bias_value(static_cast<float>(d), row);
+#pragma unroll
+    for (int k = 0; k < kTabCopies; ++k) tab[k * copy - d] = b;
   }
 }
 
@@ -191,8 +202,8 @@ __device__ __forceinline__ int64_t item_slot(const SharedArgs& a, const Item& x,
 // Every warp takes items by itself, from a counter that the call's first kernel sets to 0 (which warp
 // computes an item changes nothing in it), and runs through their keys in tiles of 32; the next
 // tiles, of the next item too, are on their way meanwhile.  Nothing is joined in
-// a CTA: items of a few hundred keys, whose start a CTA of its own each paid for, took 24 instead of
-// XX us (64 sequences of up to 512 keys, 12 heads).  kTwo: more than 8 rows.  kParts: bf16 parts of
+// a CTA: items of a few hundred keys, whose start a CTA of its own each paid for, took 24 us (64
+// sequences of up to 512 keys, 12 heads).  kTwo: more than 8 rows.  kParts: bf16 parts of
 // a weight.
 template <bool kTwo, int kParts>
 __global__ void __launch_bounds__(kThreads, kResident)
@@ -288,23 +299,18 @@ __global__ void __launch_bounds__(kThreads, kResident)
       row = item_row(a, cur, lane, &b, &h);
       pos = query_pos(a, b, cur.P, &ok_arg);
       scale = shared_scale(a, h, pos);
-      if (!a.table) sm.rows[warp][lane] = bias_row(a, h);
+      sm.rows[warp][lane] = bias_row(a, h);
     }
     __syncwarp();
     const bool tile_marked = marked && !cur.prefix;
     uint32_t qf[4][4];
     float c[2];
     float* zrow[2];
-    const float* brow[2];
-    int rpos[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int r = __shfl_sync(0xffffffffu, row, rq + 8 * x);
       c[x] = __shfl_sync(0xffffffffu, scale, rq + 8 * x);
       zrow[x] = tile_marked && r >= 0 ? a.z + r * a.zstride : nullptr;
-      rpos[x] = __shfl_sync(0xffffffffu, pos, rq + 8 * x);
-      brow[x] = a.table && r >= 0 ? a.table + static_cast<int64_t>(r % a.H) * a.tab_len + (a.tab_top - rpos[x])
-                                  : nullptr;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + static_cast<int64_t>(r) * kHeadDim);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
@@ -335,11 +341,11 @@ __global__ void __launch_bounds__(kThreads, kResident)
       if (!ok) break;
       const int valid = cur.kend - kb;
       const bool full = valid >= kKeys;
-      // The bias.  Out of the table: each lane that of its logits.  Else it is evaluated, a key a
-      // lane and rows in turn, and handed over in shared memory.
-      const int kfirst = (cur.prefix ? 0 : cur.P) + kb;  // position of the tile's first key, without marks
-      if (!a.table) {
-        const int kp = tile_marked ? sm.kpos[warp][s][lane] : kfirst + lane;
+      // The bias, a key a lane and rows in turn, handed over in shared memory.  (Out of a table that
+      // the call's first kernel fills it took 160 instead of 151 us for 64 caches of 8192 keys, and 80
+      // instead of 66 for one of 131072.)
+      {
+        const int kp = tile_marked ? sm.kpos[warp][s][lane] : (cur.prefix ? 0 : cur.P) + kb + lane;
 #pragma unroll 2
         for (int r = 0; r < cur.nrows; ++r) {
           int d = __shfl_sync(0xffffffffu, pos, r) - kp;
@@ -350,33 +356,6 @@ __global__ void __launch_bounds__(kThreads, kResident)
           sm.bias[warp][r][lane] = bias_value(static_cast<float>(d), sm.rows[warp][r]);
         }
         __syncwarp();
-      }
-      float2 bias[kTwo ? 2 : 1][4];
-#pragma unroll
-      for (int x = 0; x < (kTwo ? 2 : 1); ++x) {
-#pragma unroll
-        for (int oc = 0; oc < 4; ++oc) {
-          float2 bi = make_float2(0.0f, 0.0f);
-          if (!a.table) {
-            bi = *reinterpret_cast<const float2*>(&sm.bias[warp][rq + 8 * x][8 * oc + cq]);
-          } else if (brow[x]) {
-            // brow: this row's table at the query's position; a key's entry is its position further.
-            int k0 = kfirst + 8 * oc + cq, k1 = k0 + 1;
-            if (tile_marked) {
-              const int2 kp = *reinterpret_cast<const int2*>(&sm.kpos[warp][s][8 * oc + cq]);
-              k0 = max(min(kp.x, rpos[x]), 0);
-              k1 = max(min(kp.y, rpos[x]), 0);
-              if (full) {
-                bad_pos |= k0 != kp.x;
-                bad_pos |= k1 != kp.y;
-              } else {
-                bad_pos |= (k0 != kp.x && 8 * oc + cq < valid) || (k1 != kp.y && 8 * oc + cq + 1 < valid);
-              }
-            }
-            bi = make_float2(__ldg(brow[x] + k0), __ldg(brow[x] + k1));
-          }
-          bias[x][oc] = bi;
-        }
       }
       const uint32_t kt = smem_u32(sm.k[warp][s]), vt = smem_u32(sm.v[warp][s]);
       // S
@@ -399,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, kResident)
         float mx = -INFINITY;
 #pragma unroll
         for (int oc = 0; oc < 4; ++oc) {
-          float z0 = fmaf(sacc[oc][2 * x], c[x], bias[x][oc].x);
-          float z1 = fmaf(sacc[oc][2 * x + 1], c[x], bias[x][oc].y);
+          const float2 bi = *reinterpret_cast<const float2*>(&sm.bias[warp][rq + 8 * x][8 * oc + cq]);
+          float z0 = fmaf(sacc[oc][2 * x], c[x], bi.x), z1 = fmaf(sacc[oc][2 * x + 1], c[x], bi.y);
           if (!full) {
             if (8 * oc + cq >= valid) z0 = -INFINITY;
             if (8 * oc + cq + 1 >= valid) z1 = -INFINITY;
@@ -666,22 +645,14 @@ static int split_keys(int64_t rows, int64_t most) {
 void shared_split(SharedArgs* a, int64_t Pmax, int64_t Tmax) {
   const int blocks = (a->group + kRows - 1) / kRows;
   a->nsplit = split_keys(static_cast<int64_t>(a->c.B) * a->c.Hkv * blocks, Tmax);
-  a->npsplit = a->copies = 0;
+  a->npsplit = a->copies = a->tab_len = 0;
   if (Pmax > 0) {
     if (static_cast<int64_t>(a->c.B) * a->group <= kFewRows)
       a->npsplit = split_keys(a->c.Hkv, Pmax);
     else
-      prefix_split(a, Pmax);
+      prefix_split(a, Pmax, Tmax);
   }
   a->slots = a->nsplit + a->npsplit * (a->copies > 1 ? a->copies : 1);
-  // The table holds every distance below `top`, and room for windows that reach past the last
-  // key.  Where it would hold more than a few keys have (one long sequence; positions far
-  // beyond what a bounded cache holds), the bias of each key is evaluated instead: XX
-  const int64_t reach = Pmax + Tmax;
-  const int64_t top = a->max_pos > 0 ? (a->max_pos > Pmax ? a->max_pos : Pmax) : reach;
-  a->use_table = a->copies || top <= 8192 || 4 * top <= a->c.B * reach;
-  a->tab_top = static_cast<int>(top - 1);
-  a->tab_len = static_cast<int>((top + 72 + 63) / 64 * 64);
 }
 
 cudaError_t launch_shared_prep(const SharedArgs& a, cudaStream_t st) {

@@ -35,10 +35,10 @@ struct SharedArgs {
   int copies;                // of a row, each with its part of a tile's keys; 0: few rows, no tiles
   int slots;                 // of a row: nsplit + npsplit * max(copies, 1)
   int64_t zstride;           // max_blocks * page
-  // The table of b_h(d) log2(e), or null.  Entry y of copy k of head h, at
-  // [(k * H + h) * tab_len + y + k], holds d = tab_top - y.  One copy without tiles.
+  // For a prefix in tiles: the table of b_h(d) log2(e).  Entry y of copy k of head h, at
+  // [(k * H + h) * tab_len + y + k], holds d = tab_top - y.
   float* table;
-  int tab_top, tab_len, use_table;
+  int tab_top, tab_len;
 };
 
 constexpr int kLeastKeys = 64;    // of a part, at least
@@ -112,7 +112,7 @@ cudaError_t launch_prefix(const CUtensorMap& tk, const CUtensorMap& tv, const Sh
 // Splits of the own and prefix keys and the table's size; fills nsplit, npsplit, copies,
 // slots, tab_top, tab_len.
 void shared_split(SharedArgs* a, int64_t Pmax, int64_t Tmax);
-void prefix_split(SharedArgs* a, int64_t Pmax);
+void prefix_split(SharedArgs* a, int64_t Pmax, int64_t Tmax);
 
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st);
 cudaError_t launch_evict_move(const EvictArgs& a, cudaStream_t st);
