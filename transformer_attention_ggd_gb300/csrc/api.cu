@@ -312,7 +312,7 @@ size_t norm_ws(int H, int Hkv) {
 }
 
 struct SharedWs {
-  size_t ml, part, z, table, total;
+  size_t ml, part, z, spill, table, total;
 };
 SharedWs shared_ws(const SharedArgs& a, bool marked) {
   SharedWs w;
@@ -320,7 +320,8 @@ SharedWs shared_ws(const SharedArgs& a, bool marked) {
   w.ml = kStatusBytes;
   w.part = w.ml + align256(rows * a.slots * 8);
   w.z = w.part + align256(rows * a.slots * kHeadDim * 4);
-  w.table = w.z + (marked ? align256(rows * a.zstride * 4) : 0);
+  w.spill = w.z + (marked ? align256(rows * a.zstride * 4) : 0);
+  w.table = w.spill + align256(rows * a.spills * kHeadDim * 4);
   w.total = w.table;
   if (a.copies)
     w.total += align256((kTabCopies * static_cast<size_t>(a.H) * a.tab_len + kTabPadFloats) * 4);
@@ -794,7 +795,10 @@ bam_status bam_attn_decode_shared_paged(const void* q, const void* k_pages, cons
   a.lse = lse;
   a.ml = reinterpret_cast<float2*>(wsb + w.ml);
   a.part = reinterpret_cast<float*>(wsb + w.part);
-  if (a.copies) a.table = reinterpret_cast<float*>(wsb + w.table);
+  if (a.copies) {
+    a.spill = reinterpret_cast<float*>(wsb + w.spill);
+    a.table = reinterpret_cast<float*>(wsb + w.table);
+  }
   cudaError_t e =
       launch_kernel(BAM_KERNEL_SHARED_PREP, stream, [&] { return launch_shared_prep(a, stream); });
   if (e != cudaSuccess) return BAM_ERR_CUDA;

@@ -645,14 +645,14 @@ static int split_keys(int64_t rows, int64_t most) {
 void shared_split(SharedArgs* a, int64_t Pmax, int64_t Tmax) {
   const int blocks = (a->group + kRows - 1) / kRows;
   a->nsplit = split_keys(static_cast<int64_t>(a->c.B) * a->c.Hkv * blocks, Tmax);
-  a->npsplit = a->copies = a->tab_len = 0;
+  a->npsplit = a->copies = a->tab_len = a->spills = 0;
   if (Pmax > 0) {
     if (static_cast<int64_t>(a->c.B) * a->group <= kFewRows)
       a->npsplit = split_keys(a->c.Hkv, Pmax);
     else
       prefix_split(a, Pmax, Tmax);
   }
-  a->slots = a->nsplit + a->npsplit * (a->copies > 1 ? a->copies : 1);
+  a->slots = a->nsplit + a->npsplit;
 }
 
 cudaError_t launch_shared_prep(const SharedArgs& a, cudaStream_t st) {

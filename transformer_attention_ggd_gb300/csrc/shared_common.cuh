@@ -33,8 +33,10 @@ struct SharedArgs {
   int nsplit;                // parts of a sequence's own keys
   int npsplit;               // of the prefix
   int copies;                // of a row, each with its part of a tile's keys; 0: few rows, no tiles
-  int slots;                 // of a row: nsplit + npsplit * max(copies, 1)
+  int slots;                 // of a row: nsplit + npsplit
   int64_t zstride;           // max_blocks * page
+  float* spill;              // [B * H, spills, 64]: what leaves the accumulators of a prefix in tiles
+  int spills;
   // For a prefix in tiles: the table of b_h(d) log2(e).  Entry y of copy k of head h, at
   // [(k * H + h) * tab_len + y + k], holds d = tab_top - y.
   float* table;
@@ -110,7 +112,7 @@ cudaError_t launch_shared_weigh(const SharedArgs& a, cudaStream_t st);
 cudaError_t launch_prefix(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArgs& a,
                           cudaStream_t st);
 // Splits of the own and prefix keys and the table's size; fills nsplit, npsplit, copies,
-// slots, tab_top, tab_len.
+// slots, spills, tab_top, tab_len.
 void shared_split(SharedArgs* a, int64_t Pmax, int64_t Tmax);
 void prefix_split(SharedArgs* a, int64_t Pmax, int64_t Tmax);
 
