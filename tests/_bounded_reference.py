@@ -68,7 +68,7 @@ def decode(q, k_pages, v_pages, table, lens, prefix, P, key_pos, q_pos, prm, ssm
     a logit is off by at most delta, a weight by its delta and the mean delta
     relative.  The weights enter the product with V with 24 bits (2^-22 covers the
     parts) for fp32 output, and for bf16 output with 16 bits (2^-16) or, over a
-    prefix that more than 16 rows of a key head share, rounded to 8 (half a
+    prefix that more than 8 rows of a key head share, rounded to 8 (half a
     step: 2^-8)."""
     B, H, D = q.shape
     Hkv = k_pages.shape[1]
@@ -113,7 +113,7 @@ def decode(q, k_pages, v_pages, table, lens, prefix, P, key_pos, q_pos, prm, ssm
         lse[b] = torch.logsumexp(z, 1)
         mag = torch.einsum("hl,hld->hd", w, v.abs())
         wd = (w * delta).sum(1)
-        parts = (BF16 if P and B * G > 16 else 2.0 ** -16) if bf16_out else 2.0 ** -22
+        parts = (BF16 if P and B * G > 8 else 2.0 ** -16) if bf16_out else 2.0 ** -22
         e = torch.einsum("hl,hld->hd", w * delta, v.abs()) + wd[:, None] * mag \
             + (L * 2.0 ** -24 + parts) * mag
         oerr[b] = e + (BF16 if bf16_out else 2.0 ** -24) * (o[b].abs() + e) + 1e-38

@@ -102,6 +102,7 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ unsigned* item_counter(DevStatus* st) {
   return reinterpret_cast<unsigned*>(st) + 32;
 }
+static_assert(kFewRows <= kRows / 2);
 static_assert(sizeof(DevStatus) <= 128 && kStatusBytes >= 256, "place of the item counter");
 
 constexpr int kPrepThreads = 256;
@@ -146,8 +147,8 @@ __global__ void __launch_bounds__(kPrepThreads) bam_shared_prep_kernel(const Sha
   }
 }
 
-// An item: up to 16 rows (the heads of one sequence that share a key head, or all rows of a
-// few over the prefix) and one part of their keys.
+// An item: up to 16 rows (the heads of one sequence that share a key head, or all rows over the
+// prefix, up to 8) and one part of their keys.
 struct Item {
   bool on, prefix;
   int sp, hk, b, r0, nrows;
@@ -202,8 +203,8 @@ __device__ __forceinline__ int64_t item_slot(const SharedArgs& a, const Item& x,
 // Every warp takes items by itself, from a counter that the call's first kernel sets to 0 (which warp
 // computes an item changes nothing in it), and runs through their keys in tiles of 32; the next
 // tiles, of the next item too, are on their way meanwhile.  Nothing is joined in
-// a CTA: items of a few hundred keys, whose start a CTA of its own each paid for, took 24 us (64
-// sequences of up to 512 keys, 12 heads).  kTwo: more than 8 rows.  kParts: bf16 parts of
+// a CTA: items of a few hundred keys, whose start a CTA of its own each paid for, took 24 us
+// where these take 15 (64 sequences of up to 512 keys, 12 heads).  kTwo: more than 8 rows.  kParts: bf16 parts of
 // a weight.
 template <bool kTwo, int kParts>
 __global__ void __launch_bounds__(kThreads, kResident)
@@ -686,7 +687,7 @@ cudaError_t launch_shared(const CUtensorMap& tk, const CUtensorMap& tv, const Sh
   const int64_t items = static_cast<int64_t>(a.nsplit) * a.c.B * a.c.Hkv * blocks +
                         (few ? static_cast<int64_t>(a.npsplit) * a.c.Hkv : 0);
   if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const bool two = a.group > 8 || (few && a.c.B * a.group > 8);
+  const bool two = a.group > 8;
   if (a.o_fp32)
     return two ? launch_main<true, 3>(tk, tv, a, items, st) : launch_main<false, 3>(tk, tv, a, items, st);
   return two ? launch_main<true, 2>(tk, tv, a, items, st) : launch_main<false, 2>(tk, tv, a, items, st);

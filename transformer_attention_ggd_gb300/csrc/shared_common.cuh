@@ -49,7 +49,10 @@ __host__ __device__ inline int part_keys(int n, int parts) {
   const int each = ((n + parts - 1) / parts + 63) / 64 * 64;
   return each > kLeastKeys ? each : kLeastKeys;
 }
-constexpr int kFewRows = 16;      // of a key head over the prefix, at most, without tiles
+// Rows of a key head over the prefix, at most, that go with the own keys instead of in tiles.  8 rows, 12
+// key heads and 1024, 8192 and 65536 keys: 12, 16 and 54 us without tiles, 14, 19 and 62 with them;
+// 12 rows and 1024 and 8192: 14 and 23, 15 and 21; 16 rows, 32768: 58 and 38.
+constexpr int kFewRows = 8;
 
 constexpr float kNoMax = -3.4e38f;  // below every logit (the bias is clamped at -3e38)
 
