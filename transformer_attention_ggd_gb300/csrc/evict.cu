@@ -8,15 +8,21 @@
 //
 // Choice: the weight of the last key that stays is found digit by digit (11, 11
 // and 10 bits, from the highest) in histograms of the weights, which stay in shared
-// memory; keys of exactly that weight stay from the lowest slot on.  Long
-// sequences are dealt to a cluster of CTAs, a run of slots each.
+// memory; keys of exactly that weight stay from the lowest slot on.  Then every warp
+// counts what it keeps of a run of slots, and writes their rows behind what the
+// warps before it keep.  Long sequences are dealt to a cluster of CTAs, a run of slots each.
+//
+// Measured: 64 sequences, 12 heads, 4352 -> 4096 keys, to other pages: 290 us, of which 25 for
+// the choice (1.66 GB moved at 6.3 TB/s); one sequence, 12 heads, 131072 -> 65536: 104 us, 33 for the
+// choice, which is a chain of latencies: three digits of 5 us, each of a histogram and two meetings
+// of the cluster; 8 sequences of 600 -> 512: 10 us, two kernels of dependent steps.
 #include "shared_common.cuh"
 
 namespace bam {
 namespace {
 
-// Threads of a selecting CTA for short runs of slots and for long ones (16384 of them take
-// 53 us with the few, 40 with 512).
+// Threads of a selecting CTA for short runs of slots and for long ones (96 CTAs with 16384 each take
+// 48 us with the few, 33 with the many; 768 with 4352 each 25 and 36).
 constexpr int kSelFew = 256, kSelMany = 512;
 constexpr int kSelRun = 8192;                       // slots, at most, for the few
 constexpr int kSelPer = 4;                          // slots of a thread in a chunk
@@ -57,38 +63,37 @@ __device__ __forceinline__ uint32_t weight_order(float w) {
   return x & 0x80000000u ? ~x : x | 0x80000000u;
 }
 
-// Exclusive prefix sums over the block of two counts packed in a 64-bit word.
+// Exclusive prefix sums over the block.
 template <int kSelThreads>
-__device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* warp_sums, uint64_t* total) {
+__device__ __forceinline__ int block_scan(int x, int* warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t s = x;
+  int s = x;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const uint64_t y = __shfl_up_sync(0xffffffffu, s, d);
+    const int y = __shfl_up_sync(0xffffffffu, s, d);
     if (lane >= d) s += y;
   }
   if (lane == 31) warp_sums[warp] = s;
   __syncthreads();
-  uint64_t before = 0, all = 0;
+  int before = 0;
 #pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w) {
+  for (int w = 0; w < kSelThreads / 32; ++w)
     if (w < warp) before += warp_sums[w];
-    all += warp_sums[w];
-  }
   __syncthreads();
-  *total = all;
   return before + s - x;
 }
 
 // A cluster chooses the keys of a sequence and key head.
 template <int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads, 1280 / kSelThreads) bam_kv_evict_select_kernel(const EvictArgs a) {
-  constexpr int kSelChunk = kSelThreads * kSelPer;
+  constexpr int kSelChunk = kSelThreads * kSelPer, kSelWarps = kSelThreads / 32;
+  constexpr int kSelAhead = kSelThreads == kSelFew ? 2 : 4;  // chunks whose weights are on their way
   constexpr int kBinThreads = kSelThreads < kBins / 4 ? kSelThreads : kBins / 4;
   constexpr int kThreadBins = kBins / kBinThreads;  // in fours
   extern __shared__ __align__(16) uint32_t cache[];  // orders of this CTA's weights
   __shared__ __align__(16) int hist[kBins];
-  __shared__ uint64_t warp_sums[kSelThreads / 32];
+  __shared__ int warp_sums[kSelWarps];
+  __shared__ int2 kept_by[kSelWarps];
   __shared__ int s_bin, s_need, s_over, s_ties, s_first;
   grid_dep_trigger();
   const CacheArgs& c = a.c;
@@ -127,16 +132,12 @@ __global__ void __launch_bounds__(kSelThreads, 1280 / kSelThreads) bam_kv_evict_
   const int inner = min(hi, end);               // end of those of this CTA
   int need = a.budget - a.sink - a.recent;      // of them
   // Orders of four slots from i on, which lie in one page.
-  auto orders = [&](int i, bool first) {
-    uint4 w;
-    if (!first && i - begin < a.cached) {
-      w = *reinterpret_cast<const uint4*>(cache + (i - begin));
-    } else {
-      const float4 f = *reinterpret_cast<const float4*>(a.key_weight + row_of(i));
-      w = make_uint4(weight_order(f.x), weight_order(f.y), weight_order(f.z), weight_order(f.w));
-      if (first && i - begin < a.cached) *reinterpret_cast<uint4*>(cache + (i - begin)) = w;
-    }
-    return w;
+  auto orders_of = [](const float4& f) {
+    return make_uint4(weight_order(f.x), weight_order(f.y), weight_order(f.z), weight_order(f.w));
+  };
+  auto orders = [&](int i) {
+    return i - begin < a.cached ? *reinterpret_cast<const uint4*>(cache + (i - begin))
+                                : orders_of(*reinterpret_cast<const float4*>(a.key_weight + row_of(i)));
   };
   uint32_t threshold = 0;
   int shift = 32;
@@ -146,8 +147,7 @@ __global__ void __launch_bounds__(kSelThreads, 1280 / kSelThreads) bam_kv_evict_
     shift -= bits;
     for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
-    for (int i = begin + kSelPer * threadIdx.x; i < end; i += kSelChunk) {
-      const uint4 q = orders(i, pass == 0);
+    auto add = [&](int i, const uint4& q) {
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
       const bool all = i >= lo && i + 4 <= inner;
 #pragma unroll
@@ -156,6 +156,26 @@ __global__ void __launch_bounds__(kSelThreads, 1280 / kSelThreads) bam_kv_evict_
         if (pass > 0 && ((w[x] ^ threshold) >> up) != 0) continue;
         atomicAdd(&hist[(w[x] >> shift) & ((1 << bits) - 1)], 1);
       }
+    };
+    if (pass == 0) {
+      // The weights, some on their way at a time.
+      for (int i = begin + kSelPer * threadIdx.x; i < end; i += kSelAhead * kSelChunk) {
+        float4 f[kSelAhead];
+#pragma unroll
+        for (int y = 0; y < kSelAhead; ++y)
+          if (i + y * kSelChunk < end)
+            f[y] = *reinterpret_cast<const float4*>(a.key_weight + row_of(i + y * kSelChunk));
+#pragma unroll
+        for (int y = 0; y < kSelAhead; ++y) {
+          const int j = i + y * kSelChunk;
+          if (j >= end) break;
+          const uint4 w = orders_of(f[y]);
+          if (j - begin < a.cached) *reinterpret_cast<uint4*>(cache + (j - begin)) = w;
+          add(j, w);
+        }
+      }
+    } else {
+      for (int i = begin + kSelPer * threadIdx.x; i < end; i += kSelChunk) add(i, orders(i));
     }
     if (a.cluster > 1)
       cluster_sync();
@@ -182,8 +202,7 @@ __global__ void __launch_bounds__(kSelThreads, 1280 / kSelThreads) bam_kv_evict_
       n[x] = v.w, n[x + 1] = v.z, n[x + 2] = v.y, n[x + 3] = v.x;
       sum += v.x + v.y + v.z + v.w;
     }
-    uint64_t total;
-    int above = static_cast<int>(block_scan<kSelThreads>(static_cast<uint64_t>(sum), warp_sums, &total));
+    int above = block_scan<kSelThreads>(sum, warp_sums);
 #pragma unroll
     for (int x = 0; x < kThreadBins; ++x) {
       if (above < need && need <= above + n[x]) {
@@ -205,7 +224,7 @@ __global__ void __launch_bounds__(kSelThreads, 1280 / kSelThreads) bam_kv_evict_
   const bool any = a.budget > a.sink + a.recent;
   auto classify = [&](int i0, bool (&over)[kSelPer], bool (&tie)[kSelPer]) {
     uint4 q = make_uint4(0, 0, 0, 0);
-    if (i0 < end && any) q = orders(i0, false);
+    if (i0 < end && any) q = orders(i0);
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
     const bool all = i0 >= lo && i0 + kSelPer <= inner && any;
 #pragma unroll
@@ -220,43 +239,58 @@ __global__ void __launch_bounds__(kSelThreads, 1280 / kSelThreads) bam_kv_evict_
       }
     }
   };
+  // Each warp has a run of slots; what is kept before it is counted first.
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int run = ((per + kSelWarps - 1) / kSelWarps + 127) / 128 * 128;
+  const int wbegin = min(end, begin + warp * run), wend = min(end, wbegin + run);
   int at = 0, ties = 0;
-  if (a.cluster > 1) {
-    // What the CTAs before this one keep.
+  {
     int n = 0, t = 0;
-    for (int i0 = begin + kSelPer * threadIdx.x; i0 < end; i0 += kSelChunk) {
+    for (int i0 = wbegin + kSelPer * lane; i0 < wend; i0 += 32 * kSelPer) {
       bool over[kSelPer], tie[kSelPer];
       classify(i0, over, tie);
 #pragma unroll
       for (int x = 0; x < kSelPer; ++x) n += over[x], t += tie[x];
     }
-    uint64_t total;
-    block_scan<kSelThreads>(static_cast<uint64_t>(n) << 32 | static_cast<uint32_t>(t), warp_sums, &total);
-    if (threadIdx.x == 0) {
-      s_over = static_cast<int>(total >> 32);
-      s_ties = static_cast<int>(total & 0xFFFFFFFFu);
+    n = __reduce_add_sync(0xffffffffu, n);
+    t = __reduce_add_sync(0xffffffffu, t);
+    if (lane == 0) kept_by[warp] = make_int2(n, t);
+    if (threadIdx.x == 0) s_first = len;
+    __syncthreads();
+    n = t = 0;
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) {
+      const int2 k = kept_by[w];
+      if (w < warp) at += k.x, ties += k.y;
+      n += k.x, t += k.y;
     }
-    cluster_sync();
-    for (int r = 0; r < rank; ++r) {
-      at += cluster_load(&s_over, r);
-      ties += cluster_load(&s_ties, r);
+    if (a.cluster > 1) {
+      if (threadIdx.x == 0) s_over = n, s_ties = t;
+      cluster_sync();
+      const bool before = lane < rank;
+      at += __reduce_add_sync(0xffffffffu, before ? cluster_load(&s_over, lane) : 0);
+      ties += __reduce_add_sync(0xffffffffu, before ? cluster_load(&s_ties, lane) : 0);
     }
   }
-  if (threadIdx.x == 0) s_first = len;
   int first = len;
-  for (int base = begin; base < end; base += kSelChunk) {
-    const int i0 = base + threadIdx.x * kSelPer;
+  for (int base = wbegin; base < wend; base += 32 * kSelPer) {
+    const int i0 = base + lane * kSelPer;
     bool over[kSelPer], tie[kSelPer];
     classify(i0, over, tie);
-    int n = 0, t = 0;
+    int n = 0;  // of both, 16 bits each
 #pragma unroll
-    for (int x = 0; x < kSelPer; ++x) n += over[x], t += tie[x];
-    uint64_t total;
-    const uint64_t scan =
-        block_scan<kSelThreads>(static_cast<uint64_t>(n) << 32 | static_cast<uint32_t>(t), warp_sums, &total);
-    int tie_rank = ties + static_cast<int>(scan & 0xFFFFFFFFu);
-    int dst = at + static_cast<int>(scan >> 32) + min(tie_rank, need);
-    if (n + t > 0) {
+    for (int x = 0; x < kSelPer; ++x) n += over[x] + (tie[x] << 16);
+    int scan = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, scan, d);
+      if (lane >= d) scan += y;
+    }
+    const int total = __shfl_sync(0xffffffffu, scan, 31);
+    scan -= n;
+    int tie_rank = ties + (scan >> 16);
+    int dst = at + (scan & 0xFFFF) + min(tie_rank, need);
+    if (n > 0) {
       const unsigned row = row_of(i0);
 #pragma unroll
       for (int x = 0; x < kSelPer; ++x) {
@@ -268,8 +302,8 @@ __global__ void __launch_bounds__(kSelThreads, 1280 / kSelThreads) bam_kv_evict_
         }
       }
     }
-    at += static_cast<int>(total >> 32);
-    ties += static_cast<int>(total & 0xFFFFFFFFu);
+    at += total & 0xFFFF;
+    ties += total >> 16;
   }
   // The first key that moves.
   __syncthreads();
@@ -363,6 +397,8 @@ cudaError_t launch_cluster(F* kernel, dim3 grid, int threads, size_t smem, int c
 cudaError_t launch_evict_select(const EvictArgs& args, cudaStream_t st) {
   EvictArgs a = args;
   const int64_t heads = static_cast<int64_t>(a.c.B) * a.c.Hkv, cap = static_cast<int64_t>(a.c.page) * a.c.max_blocks;
+  // A cluster for what shared memory does not hold, and where CTAs are few (12 heads of 131072 slots: 33 us
+  // with eight CTAs each, 40 with the four that hold them).
   a.cluster = 1;
   while (a.cluster < kMaxCluster &&
          (cap > static_cast<int64_t>(kCacheMost) * a.cluster ||
@@ -391,8 +427,9 @@ cudaError_t launch_evict_move(const EvictArgs& args, cudaStream_t st) {
       a.cluster *= 2;
     return launch_k(bam_kv_evict_move_kernel<128>, dim3(a.cluster * a.c.Hkv, a.c.B, 2), dim3(128), 0, st, true, a);
   }
-  // Small CTAs where there are many chains; else large ones, and as many a chain as a cluster takes.
-  const bool many = chains >= 4 * sm_count();
+  // Small CTAs for many short chains (16000 of 512 rows: 282 us, with large ones 345; 16 of them 21 and 15);
+  // else large ones (1536 of 4096 rows: 124 us, with small ones 133), and as many a chain as a cluster takes.
+  const bool many = chains >= 4 * sm_count() && a.budget <= 2048;
   while (a.cluster < kMaxCluster && chains * a.cluster < 2 * sm_count() &&
          a.budget > 512 * static_cast<int64_t>(a.cluster))
     a.cluster *= 2;
