@@ -162,6 +162,44 @@ def test_shared_batch_sizes(B):
     _case(B, 3, 3, 64, rng.integers(0, 70, B).tolist(), 150, B % 2 == 1)
 
 
+@pytest.mark.parametrize("B", [8, 9, 32, 64, 128])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_shared_rows_that_fill_a_variant(B, out):
+    _case(B, 3, 3, 64, [i % 5 for i in range(B)], 777, False, out=out, prefix_slack=40)
+
+
+@pytest.mark.parametrize("out,P", [("fp32", 14000), ("bf16", 140000)])
+@pytest.mark.parametrize("flat", [False, True])
+def test_shared_sums_that_leave_tensor_memory(out, P, flat):
+    """75 blocks of rows, each in two parts that are longer than an accumulator takes
+    on (of three chains of 8 tiles, four of 128), more than once; with equal keys and
+    positive values every step rounds to the same side.  Against some of the
+    sequences."""
+    B, H = 600, 16
+    c = Cache(P, 1, 64, [1] * B, P)
+    if flat:
+        c.k[c.prefix.long()] = 0
+        c.v.copy_(c.v.abs())
+    t = [dev_f32(x) for x in ([5.0] * H, [0.3] * H, [1.0] * H, [1.0] * H)]
+    q = _normal(c.gen, B, H, 64)
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    lens = _i32([1] * B)
+    ws = ba.shared_workspace(B, H, 1, c.prefix.numel() * 64, 64)
+    ws.fill_(0xFF)
+    o, lse = ba.attention_decode_shared_paged(q, c.k, c.v, c.table, lens, *t, prefix_table=c.prefix,
+                                              prefix_len=_i32([P]), o_dtype=dt, ws=ws)
+    assert ba.bam_attn_check_status(ws) == ba.BAM_OK
+    some = [0, 7, 8, 300, 599]
+    oref, lref, _, oerr, lerr, _ = decode(q[some], c.k, c.v, c.table[some], [1] * len(some), c.prefix, P, None,
+                                          None, t, False, False, out == "bf16")
+    for got, want, bound in ((o, oref, oerr), (lse, lref, lerr)):
+        d = (got[some].double() - want).abs()
+        assert torch.all(d <= bound), float((d / bound).max())
+    again, lagain = ba.attention_decode_shared_paged(q, c.k, c.v, c.table, lens, *t, prefix_table=c.prefix,
+                                                     prefix_len=_i32([P]), o_dtype=dt, ws=ws)
+    assert torch.equal(o, again) and torch.equal(lse, lagain)
+
+
 @pytest.mark.parametrize("lens,P,H,Hkv,marked", [([9000], 0, 8, 2, True), ([0], 9000, 4, 4, False),
                                                  ([20000, 5], 70, 4, 2, True), ([1] * 40, 20001, 8, 2, False),
                                                  ([0, 1], 40000, 2, 1, True)])
