@@ -198,6 +198,70 @@ def test_norm_is_repeatable_and_runs_on_streams_and_in_graphs():
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
 
 
+def test_norm_gradients_in_a_graph():
+    """Forward and gradients by autograd, captured after the eager graphs are gone."""
+    g = _gen(6)
+    q, k, gq, gk = (_normal(g, 2, h, 90, 64) for h in (3, 1, 3, 1))
+    wq, wk = _weights(g, 3, 1, True)
+    leaves = [x.requires_grad_() for x in (q, k, wq, wk)]
+
+    def step():
+        return torch.autograd.grad(qk_norm(*leaves, rope=ba.make_rope()), leaves, (gq, gk))
+
+    want = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for x in got:
+        x.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_norm_has_gradients_of_the_first_order_only():
+    g = _gen(7)
+    leaves = [x.requires_grad_() for x in (*(_normal(g, 1, 2, 5, 64) for _ in range(2)), *_weights(g, 2, 2, False))]
+    grads = torch.autograd.grad(sum(x.float().pow(2).sum() for x in qk_norm(*leaves)), leaves, create_graph=True)
+    with pytest.raises(RuntimeError):
+        grads[0].float().sum().backward()
+
+
+def test_norm_of_a_broadcast_input():
+    """A batch of one, expanded: each copy's gradient, summed by autograd."""
+    g = _gen(8)
+    q, k = (_normal(g, 1, 2, 40, 64).requires_grad_() for _ in range(2))
+    wq, wk = (x.requires_grad_() for x in _weights(g, 2, 2, False))
+    gq, gk = _normal(g, 3, 2, 40, 64), _normal(g, 3, 2, 40, 64)
+    wide = [x.expand(3, -1, -1, -1) for x in (q, k)]
+    got = torch.autograd.grad(qk_norm(*wide, wq, wk), (wide[0], wide[1], wq, wk), (gq, gk))
+    dense = [x.detach().expand(3, -1, -1, -1).contiguous() for x in (q, k)]
+    want = ba.qk_norm_backward(*dense, gq, gk, wq.detach(), wk.detach())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    dq, = torch.autograd.grad(qk_norm(*(x.expand(3, -1, -1, -1) for x in (q, k)), wq, wk)[0], q, gq)
+    assert dq.shape == q.shape and torch.isfinite(dq).all()
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+def test_norm_of_places_beyond_32_bits(per_head):
+    """The stride of a batch of one may be anything: its places then take 64 bits."""
+    g = _gen(9)
+    H, Hkv, T = 9, 2, 130
+    q, k, gq, gk = (_normal(g, 1, h, T, 64) for h in (H, Hkv, H, Hkv))
+    far = [x.as_strided(x.shape, (1 << 40,) + x.stride()[1:]) for x in (q, k, gq, gk)]
+    wq, wk = _weights(g, H, Hkv, per_head)
+    rope = ba.make_rope(10000.0, 32)
+    pos = torch.arange(T, 0, -1, dtype=torch.int32, device="cuda")[None].contiguous()
+    want = ba.qk_norm_forward(q, k, wq, wk, pos, rope) + ba.qk_norm_backward(q, k, gq, gk, wq, wk, pos, rope)
+    got = ba.qk_norm_forward(*far[:2], wq, wk, pos, rope) + ba.qk_norm_backward(*far, wq, wk, pos, rope)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_norm_then_attention_trains_all_parameters():
     """The training path: norms, attention and their gradients, against the same
     step in 64 bits."""

@@ -64,6 +64,7 @@ class QkNorm(torch.autograd.Function):
         return out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, q_weight, k_weight, positions = ctx.saved_tensors
         rope, eps = ctx.cfg
@@ -79,6 +80,13 @@ def qk_norm(q, k, q_weight, k_weight, positions=None, rope=None, eps=1e-6):
     and 16-byte aligned (slices of a projection's output need no copy).
     q_weight, k_weight: fp32 [64], or [H, 64] and [Hkv, 64].  positions: int32
     [B, T] or None (0, 1, ..); rope: ``bam_attn.make_rope(...)`` or None.
-    Returns contiguous (q_out, k_out), as ``bam_attention`` takes them.
+    Returns contiguous (q_out, k_out), as ``bam_attention`` takes them.  Gradients
+    are of the first order.
+
+    Captured into a CUDA graph, take the gradients inside the capture with
+    ``torch.autograd.grad``, and let go of every eager graph of the same leaves
+    before: PyTorch ties a leaf's accumulation to the stream of the oldest graph
+    that is alive, and a captured backward that reaches for that stream fails, which
+    can end the process.
     """
     return QkNorm.apply(q, k, q_weight, k_weight, positions, rope, float(eps))
