@@ -403,6 +403,48 @@ def test_shared_two_streams_and_two_graphs():
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_offsets_beyond_32_bits():
+    """Pages behind the first 5 GB of a pool, and logits behind the first 8 GB of a
+    workspace: appends, decoding and evictions equal those of a small pool and table."""
+    B, H, Hkv, page, P = 64, 32, 2, 64, 100
+    lens, extra = [70 + b % 50 for b in range(B)], 300000
+    c = Cache(23, Hkv, page, lens, P)
+    t = [dev_f32(_prm(c.rng, H, False)[n]) for n in ("alpha", "beta", "mu", "s")]
+    q, k, v = _normal(c.gen, B, H, 64), _normal(c.gen, B, Hkv, 1, 64), _normal(c.gen, B, Hkv, 1, 64)
+    room = torch.full((B, 1), -1, dtype=torch.int32, device="cuda")
+    n = c.k.shape[0]
+    outs = []
+    for far in (False, True):
+        pools = [c.k, c.v, c.pos, c.w]
+        table, prefix = c.table, c.prefix
+        if far:
+            pools = [torch.empty((extra + n,) + x.shape[1:], dtype=x.dtype, device="cuda") for x in pools]
+            for x, y in zip(pools, (c.k, c.v, c.pos, c.w)):
+                x[extra:].copy_(y)
+            table = torch.where(table < 0, table, table + extra)
+            table = torch.cat([table, room.expand(B, 16384)], 1).contiguous()
+            prefix = prefix + extra
+        else:
+            pools = [x.clone() for x in pools]
+        kp, vp, pos, w = pools
+        assert not far or kp.numel() * 2 > 4 << 30
+        marks = ba.make_marks(pos, w, c.max_pos)
+        at = _i32([m - 1 for m in lens])  # the last key again
+        ba.kv_append_norm_paged(k, v, kp, vp, table, at, first_pos=c.q_pos, marks=marks)
+        ws = ba.shared_workspace(B, H, Hkv, prefix.numel() * page, table.shape[1] * page, c.max_pos)
+        o, lse = ba.attention_decode_shared_paged(q, kp, vp, table, _i32(lens), *t, prefix_table=prefix,
+                                                  prefix_len=_i32([P]), q_pos=c.q_pos, marks=marks, ws=ws)
+        assert ba.bam_attn_check_status(ws) == ba.BAM_OK
+        assert not far or ws.numel() > 8 << 30
+        del ws
+        new = ba.kv_evict_paged(kp, vp, table, _i32(lens), marks, 64, 3, 20)
+        outs.append([o, lse, new] + [x[-n:].clone() for x in pools])
+    for x, y in zip(*outs):
+        if x.dtype == torch.bfloat16:
+            x, y = x.view(torch.int16), y.view(torch.int16)
+        torch.testing.assert_close(x, y, rtol=1e-4, atol=1e-4, equal_nan=True)
+
+
 def test_serving_with_a_bounded_cache():
     """A shared document, prompts that enter the cache through norms and rotation,
     decoding steps that gather weights, evictions whenever the caches are full,

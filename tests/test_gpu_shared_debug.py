@@ -91,3 +91,32 @@ def test_giveup(at, marked):
     again = call()
     assert again[3] == ba.BAM_OK
     assert all(torch.equal(x, y) for x, y in zip(again[:3], good[:3]))
+
+
+@debug_only
+@pytest.mark.parametrize("B,out", [(20, "bf16"), (50, "fp32"), (130, "bf16")])
+@pytest.mark.parametrize("at", [1, 40, 700, 4000])
+def test_giveup_of_every_prefix_variant(at, B, out):
+    H, P = 2, 9000
+    rng = np.random.default_rng(at)
+    lens = [b % 3 for b in range(B)]
+    c = Cache(4, H, 64, lens, P)
+    t = [dev_f32(_prm(rng, H, False)[n]) for n in ("alpha", "beta", "mu", "s")]
+    prm = ba.make_params(*t, 1e-5, True, True)
+    q = _normal(c.gen, B, H, 64)
+    ws = ba.shared_workspace(B, H, H, c.prefix.numel() * 64, c.table.shape[1] * 64)
+
+    def call():
+        o = torch.full((B, H, 64), 3.0, device="cuda", dtype=torch.bfloat16 if out == "bf16" else torch.float32)
+        ba.bam_attn_decode_shared_paged(q, c.k, c.v, c.table, _i32(lens), c.prefix, _i32([P]), None, None, 1.0, o,
+                                        None, prm, ws)
+        return o, ba.bam_attn_check_status(ws)
+
+    good, st = call()
+    assert st == ba.BAM_OK
+    assert ba.bam_attn_debug_arm_giveup(ws, at) == ba.BAM_OK
+    o, st = call()
+    ba.bam_attn_debug_arm_giveup(ws, 0)
+    assert st == ba.BAM_ERR_TIMEOUT and torch.isnan(o).all()
+    o, st = call()
+    assert st == ba.BAM_OK and torch.equal(o, good)
