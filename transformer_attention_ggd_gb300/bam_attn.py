@@ -582,8 +582,15 @@ def _check_rows(t, name, shape, device):
 # a handful of attribute reads per tensor, and only a call that fails them goes
 # through the detailed ones above, which say what is wrong.
 
-def _raw_stream(stream, index):
+torch = None  # bound by the first call of one of them
+
+
+def _use_torch():
+    global torch
     import torch
+
+
+def _raw_stream(stream, index):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -613,7 +620,6 @@ def _all_ok(index, pool, k_pages, v_pages, table, block_table, cache_lens, draft
     """The cache's tensors and those of specs (tensor, dtype, shape) are contiguous, on CUDA
     device `index`, of their dtypes and shapes.  pool, table: the shapes of k_pages and
     block_table."""
-    import torch
     bf, i32, lens = torch.bfloat16, torch.int32, (B,)
     specs += ((k_pages, bf, pool), (v_pages, bf, pool), (block_table, i32, table),
               (cache_lens, i32, lens))
@@ -630,15 +636,30 @@ def _all_ok(index, pool, k_pages, v_pages, table, block_table, cache_lens, draft
 
 
 def _rows_ok(index, shape, t):
-    import torch
     if t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape:
         return False
     a, b, c, d = t.stride()
     return d == 1 and not (a | b | c) & 7 and not t.data_ptr() & 15
 
 
+def _row_words(index, shape, t):
+    """Address and strides over batch, head and token of a tensor for which
+    _rows_ok holds; else None."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape:
+        return None
+    a, b, c, d = t.stride()
+    p = t.data_ptr()
+    return (p, a, b, c) if d == 1 and not (a | b | c) & 7 and not p & 15 else None
+
+
+_no_rows = (0, 0, 0, 0)
+
+
+def _unchecked_words(t):
+    return (t.data_ptr(), *t.stride()[:3])
+
+
 def _current_device():
-    import torch
     return torch._C._cuda_getDevice()
 
 
@@ -650,6 +671,8 @@ def bam_kv_append_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_len
     each sequence; parents int32 [B, N] or None: the tree that positions
     follow; q [B, H, N, 64] -> q_out (contiguous) or both None: queries rotated
     on the way; rope: make_rope(...) or None."""
+    if torch is None:
+        _use_torch()
     B, Hkv, N, D = shape = k.shape
     num_pages, pool_heads, page, _ = pool = k_pages.shape
     table = block_table.shape
@@ -660,7 +683,6 @@ def bam_kv_append_paged(k, v, k_pages, v_pages, block_table, cache_lens, new_len
         H = q.shape[1]
         strides += q.stride()[:3]
     if check:
-        import torch
         try:
             ok = (index >= 0 and index == _current_device() and D == 64 and pool_heads == Hkv
                   and _rows_ok(index, shape, k) and _rows_ok(index, shape, v)
@@ -702,7 +724,8 @@ def bam_attn_decode_tree_paged(q, k_pages, v_pages, block_table, cache_lens, dra
     sequence's committed keys and, behind them, its draft's; cache_lens int32
     [B] (committed keys); draft_lens int32 [B] or None (N each); parents int32
     [B, N] or None (a chain); lse [B, H, N] or None."""
-    import torch
+    if torch is None:
+        _use_torch()
     B, H, N, D = shape = q.shape
     num_pages, Hkv, page, _ = pool = k_pages.shape
     table = block_table.shape
@@ -749,6 +772,8 @@ def bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, par
                       new_lens, ws, stream=None, check=True) -> None:
     """Keep the path from the root to node accepted[b] (int32 [B], -1: none)
     of each draft; new_lens int32 [B] (may be cache_lens) gets the lengths."""
+    if torch is None:
+        _use_torch()
     num_pages, Hkv, page, D = pool = k_pages.shape
     table = block_table.shape
     B = table[0]
@@ -757,7 +782,6 @@ def bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, par
     if parents is None and draft_lens is None:
         raise ValueError("draft_lens is required without parents")
     if check:
-        import torch
         try:
             ok = (index >= 0 and index == _current_device()
                   and _all_ok(index, pool, k_pages, v_pages, table, block_table, cache_lens,
@@ -869,16 +893,19 @@ def bam_qk_norm_fwd(q, k, q_out, k_out, positions, norm: BamQkNorm, rope=None, s
     """q [B, H, T, 64], k [B, Hkv, T, 64] normalised by head and rotated by
     positions (int32 [B, T], or None: 0, 1, ..) into q_out, k_out; rows of 64
     contiguous and 16-byte aligned, other strides free."""
+    if torch is None:
+        _use_torch()
     B, H, T, D = qs = q.shape
     Hkv = k.shape[1]
     ks = (B, Hkv, T, D)
     index = q.get_device()
+    rows = None
     if check:
-        import torch
         try:
-            ok = (index >= 0 and index == _current_device() and D == 64 and _rows_ok(index, qs, q)
-                  and _rows_ok(index, ks, k) and _rows_ok(index, qs, q_out)
-                  and _rows_ok(index, ks, k_out) and _norm_fits(norm, index, H, Hkv)
+            rows = (_row_words(index, qs, q), _row_words(index, ks, k), _row_words(index, qs, q_out),
+                    _row_words(index, ks, k_out))
+            ok = (index >= 0 and index == _current_device() and D == 64 and None not in rows
+                  and _norm_fits(norm, index, H, Hkv)
                   and (positions is None or (positions.dtype is torch.int32
                                              and positions.get_device() == index
                                              and positions.shape == (B, T)
@@ -890,11 +917,10 @@ def bam_qk_norm_fwd(q, k, q_out, k_out, positions, norm: BamQkNorm, rope=None, s
             _check_norm_rows((("q", q, qs), ("k", k, ks), ("q_out", q_out, qs), ("k_out", k_out, ks)),
                              positions, B, T, norm, H, Hkv)
             raise ValueError("argument check failed")
+    w = rows or [_unchecked_words(t) for t in (q, k, q_out, k_out)]
     st = load_library().bam_paged_call(4, _norm_fwd_words(
-        q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), 1, _address(positions), B, H,
-        Hkv, T, D, _struct_address(norm, BamQkNorm), _struct_address(rope, BamRope),
-        _raw_stream(stream, index), *q.stride()[:3], *k.stride()[:3], *q_out.stride()[:3],
-        *k_out.stride()[:3]))
+        w[0][0], w[1][0], w[2][0], w[3][0], 1, _address(positions), B, H, Hkv, T, D, _struct_address(norm, BamQkNorm), _struct_address(rope, BamRope),
+        _raw_stream(stream, index), *w[0][1:], *w[1][1:], *w[2][1:], *w[3][1:]))
     if st:
         _check(st, "bam_qk_norm_fwd")
 
@@ -903,18 +929,20 @@ def bam_qk_norm_bwd(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, position
                     rope, ws, stream=None, check=True) -> None:
     """Gradients of bam_qk_norm_fwd: of q and k (dq, dk, any strides) and of the
     weights (fp32, shaped as they are)."""
+    if torch is None:
+        _use_torch()
     B, H, T, D = qs = q.shape
     Hkv = k.shape[1]
     ks = (B, Hkv, T, D)
     index = q.get_device()
+    rows = None
     if check:
-        import torch
         wq, wk = ((H, 64), (Hkv, 64)) if norm.per_head else ((64,), (64,))
         try:
-            ok = (index >= 0 and index == _current_device() and D == 64 and _rows_ok(index, qs, q)
-                  and _rows_ok(index, ks, k) and _rows_ok(index, qs, dq_out)
-                  and _rows_ok(index, ks, dk_out) and _rows_ok(index, qs, dq)
-                  and _rows_ok(index, ks, dk) and _norm_fits(norm, index, H, Hkv))
+            rows = (_row_words(index, qs, q), _row_words(index, ks, k), _row_words(index, qs, dq_out),
+                    _row_words(index, ks, dk_out), _row_words(index, qs, dq), _row_words(index, ks, dk))
+            ok = (index >= 0 and index == _current_device() and D == 64 and None not in rows
+                  and _norm_fits(norm, index, H, Hkv))
             for t, dtype, shape in ((dq_weight, torch.float32, wq), (dk_weight, torch.float32, wk),
                                     (positions, torch.int32, (B, T))):
                 if t is not None or dtype is torch.float32:
@@ -934,12 +962,12 @@ def bam_qk_norm_bwd(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, position
                             ("dk_weight", dk_weight, wk, f32, False)), dev)
             _check_ws(ws, dev)
             raise ValueError("argument check failed")
+    w = rows or [_unchecked_words(t) for t in (q, k, dq_out, dk_out, dq, dk)]
     st = load_library().bam_paged_call(5, _norm_bwd_words(
-        q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(),
-        dk.data_ptr(), 1, dq_weight.data_ptr(), dk_weight.data_ptr(), _address(positions), B, H, Hkv,
+        w[0][0], w[1][0], w[2][0], w[3][0], w[4][0], w[5][0], 1, dq_weight.data_ptr(), dk_weight.data_ptr(), _address(positions), B, H, Hkv,
         T, D, _struct_address(norm, BamQkNorm), _struct_address(rope, BamRope), ws.data_ptr(),
-        ws.numel(), _raw_stream(stream, index), *q.stride()[:3], *k.stride()[:3],
-        *dq_out.stride()[:3], *dk_out.stride()[:3], *dq.stride()[:3], *dk.stride()[:3]))
+        ws.numel(), _raw_stream(stream, index), *w[0][1:], *w[1][1:], *w[2][1:],
+        *w[3][1:], *w[4][1:], *w[5][1:]))
     if st:
         _check(st, "bam_qk_norm_bwd")
 
@@ -952,25 +980,25 @@ def bam_kv_append_norm_paged(k, v, k_pages, v_pages, block_table, cache_lens, ne
     """bam_kv_append_paged with the norms of make_qk_norm (or None), positions
     that start at first_pos (int32 [B], or None: cache_lens) and the marks of
     make_marks (or None), which get each written key's position and weight 0."""
+    if torch is None:
+        _use_torch()
     B, Hkv, N, D = shape = k.shape
     num_pages, pool_heads, page, _ = pool = k_pages.shape
     table = block_table.shape
     index = k.get_device()
     H = Hkv
-    strides = k.stride()[:3] + v.stride()[:3]
+    rows = None
     if q is not None:
         H = q.shape[1]
-        strides += q.stride()[:3]
     if check:
-        import torch
         specs = () if q is None else ((q_out, torch.bfloat16, (B, H, N, 64)),)
         if first_pos is not None:
             specs += ((first_pos, torch.int32, (B,)),)
         try:
+            rows = (_row_words(index, shape, k), _row_words(index, shape, v),
+                    _no_rows if q is None else _row_words(index, (B, H, N, 64), q))
             ok = (index >= 0 and index == _current_device() and D == 64 and pool_heads == Hkv
-                  and _rows_ok(index, shape, k) and _rows_ok(index, shape, v)
-                  and (q is None) == (q_out is None)
-                  and (q is None or _rows_ok(index, (B, H, N, 64), q))
+                  and None not in rows and (q is None) == (q_out is None)
                   and (norm is None or _norm_fits(norm, index, H, Hkv))
                   and (marks is None or _marks_fit(marks, index, pool))
                   and _all_ok(index, pool, k_pages, v_pages, table, block_table, cache_lens,
@@ -993,15 +1021,14 @@ def bam_kv_append_norm_paged(k, v, k_pages, v_pages, block_table, cache_lens, ne
             _check_norm_marks(norm, marks, dev.index, H, Hkv, pool)
             _check_ws(ws, dev)
             raise ValueError("argument check failed")
-    if q is None:
-        strides += (0, 0, 0)
+    kw, vw, qw = rows or [_no_rows if t is None else _unchecked_words(t) for t in (k, v, q)]
     st = load_library().bam_paged_call(3, _append_norm_words(
-        k.data_ptr(), v.data_ptr(), _address(q), _address(q_out),
+        kw[0], vw[0], qw[0], _address(q_out),
         1, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
         cache_lens.data_ptr(), _address(new_lens), _address(parents), B, H, Hkv, N, page,
         table[1], num_pages, D, _struct_address(norm, BamQkNorm), _struct_address(rope, BamRope),
         _address(first_pos), _struct_address(marks, BamMarks), ws.data_ptr(), ws.numel(),
-        _raw_stream(stream, index), *strides))
+        _raw_stream(stream, index), *kw[1:], *vw[1:], *qw[1:]))
     if st:
         _check(st, "bam_kv_append_norm_paged")
 
@@ -1014,7 +1041,8 @@ def bam_attn_decode_shared_paged(q, k_pages, v_pages, block_table, cache_lens, p
     and cache_lens int32 [B].  marks: make_marks(...) with q_pos int32 [B], or
     both None; the marks' weights decay by `decay` and gather this step's.  lse
     [B, H] or None."""
-    import torch
+    if torch is None:
+        _use_torch()
     B, H, D = shape = q.shape
     num_pages, Hkv, page, _ = pool = k_pages.shape
     table = block_table.shape
@@ -1079,13 +1107,14 @@ def bam_kv_evict_paged(k_pages, v_pages, block_table, cache_lens, marks: BamMark
     `sink`, its last `recent` and the heaviest of the others; new_lens int32 [B]
     (may be cache_lens) gets the lengths.  out_table int32 [B, blocks]: pages for
     the kept keys; None: in place."""
+    if torch is None:
+        _use_torch()
     num_pages, Hkv, page, D = pool = k_pages.shape
     table = block_table.shape
     B = table[0]
     index = k_pages.get_device()
     out_blocks = 0 if out_table is None else out_table.shape[-1]
     if check:
-        import torch
         specs = ((new_lens, torch.int32, (B,)),)
         if out_table is not None:
             specs += ((out_table, torch.int32, (B, out_blocks)),)
