@@ -26,7 +26,7 @@ struct NormArgs {
   Divisor by_T;
   int per_head;
   int large;             // some place needs more than 32 bits
-  int passes;            // of a part, eight heads each: the queries' and then the keys'
+  int passes;            // of a part, kNormPass heads each: the queries' and then the keys'
   unsigned parts;        // of a tile's passes
   unsigned ctas;         // of the launch, a multiple of parts
   RopeArgs rope;
