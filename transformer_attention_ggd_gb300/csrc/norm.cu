@@ -27,6 +27,7 @@ namespace {
 constexpr int kFwdSlots = 1, kBwdSlots = 2;
 constexpr int kPass = kNormPass;  // heads of a pass, a warp of eight rows each
 constexpr int kThreads = 32 * kPass;
+constexpr int kFwdStages = 3, kBwdStages = 2;  // passes whose rows are on their way
 constexpr int kFinishThreads = 1024;
 // Resident CTAs of an SM (forward 3, 4 and 5 took 126, 113 and 136 us in the first case
 // above, with eight warps a CTA).
@@ -138,16 +139,31 @@ __device__ __forceinline__ void walk_on(Walk<kN, kSlots, Off>& w, const NormArgs
   walk_to(w, a, s, l, strides);
 }
 
-struct Row {
-  uint4 v[2];
+// Rows on their way: every thread copies its own chunks into a ring and reads them back, kStages passes
+// later (in registers, one pass ahead, backward took 192 us in the first case above).
+template <int kN, int kSlots, int kStages>
+struct Ring {
+  uint4 v[kStages][kSlots][kN][2][kThreads];
 };
+// A chunk of 16 bytes, global -> shared, asynchronously; zeros where it is not `on`.
+__device__ __forceinline__ void copy_chunk(uint4* dst, const uint4* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
 template <class Off>
-__device__ __forceinline__ void load_row(const uint16_t* p, Off at, bool on, const Lane& l, Row& r) {
-  r.v[0] = r.v[1] = make_uint4(0, 0, 0, 0);
-  if (!on) return;
-  const uint4* src = reinterpret_cast<const uint4*>(p) + at;
-  r.v[0] = src[l.c0];
-  r.v[1] = src[l.c1];
+__device__ __forceinline__ void copy_row(uint4 (&dst)[2][kThreads], const uint16_t* p, Off at, bool on, const Lane& l) {
+  const uint4* src = reinterpret_cast<const uint4*>(p) + (on ? at : 0);
+  copy_chunk(&dst[0][threadIdx.x], src + (on ? l.c0 : 0), on);
+  copy_chunk(&dst[1][threadIdx.x], src + (on ? l.c1 : 0), on);
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ void read_row(const uint4 (&src)[2][kThreads], F2x8& f) {
+  const uint4 v[2] = {src[0][threadIdx.x], src[1][threadIdx.x]};
+  unpack_row(v, f);
 }
 template <class Off>
 __device__ __forceinline__ void store_row(uint16_t* p, Off at, const Lane& l, const F2x8& f) {
@@ -157,10 +173,12 @@ __device__ __forceinline__ void store_row(uint16_t* p, Off at, const Lane& l, co
   dst[l.c0] = v[0];
   dst[l.c1] = v[1];
 }
-// A CTA takes its tiles and passes in turn (Span); the rows of the next passes are on their way while one is turned and stored.
+// A CTA takes its tiles and passes in turn (Span); the rows of the next passes are on their way
+// while one is turned and stored.
 template <int kTurn, class Off>
 __global__ void __launch_bounds__(kThreads, kFwdResident) bam_qk_norm_fwd_kernel(const NormArgs a) {
   __shared__ __align__(16) Angles<kFwdSlots> cs;
+  __shared__ __align__(16) Ring<1, kFwdSlots, kFwdStages> ring;
   const Lane l = lane_of<kTurn>(a.rope);
   // this thread's frequency (read once: lanes read the launch's arguments one after the other)
   const uint64_t freq = a.rope.freq[threadIdx.x % (kHeadDim / 2)];
@@ -173,11 +191,17 @@ __global__ void __launch_bounds__(kThreads, kFwdResident) bam_qk_norm_fwd_kernel
   at.pass = ahead.pass = sp.first;
   walk_to(ahead, a, sp, l, xs);
   walk_to(at, a, sp, l, ys);
-  Row x[kSlots];
+  auto load = [&](int stage) {  // of the next pass
 #pragma unroll
-  for (int y = 0; y < kSlots; ++y) load_row(a.side[ahead.side].x, ahead.at[0][y], ahead.on(a, y), l, x[y]);
-  while (at.tile < sp.tiles) {
+    for (int y = 0; y < kSlots; ++y)
+      copy_row(ring.v[stage][y][0], a.side[ahead.side].x, ahead.at[0][y], ahead.on(a, y), l);
+    copies_commit();
     walk_on(ahead, a, sp, l, xs);
+  };
+#pragma unroll
+  for (int stage = 0; stage < kFwdStages; ++stage) load(stage);
+  int stage = 0;
+  while (at.tile < sp.tiles) {
     if (kTurn != kNoTurn && at.pass == sp.first) {
       __syncthreads();  // the last tile's angles are no longer read
       tile_angles(a, at.tile, 1.0f, freq, cs);
@@ -185,11 +209,15 @@ __global__ void __launch_bounds__(kThreads, kFwdResident) bam_qk_norm_fwd_kernel
     }
     F2x8 w;
     load_weight(a.side[at.side].w + (a.per_head && at.on(a, 0) ? at.h * kHeadDim : 0), l, w);
+    copies_wait<kFwdStages - 1>();
+    F2x8 x[kSlots];
+#pragma unroll
+    for (int y = 0; y < kSlots; ++y) read_row(ring.v[stage][y][0], x[y]);
+    load(stage);
+    if (++stage == kFwdStages) stage = 0;
 #pragma unroll
     for (int y = 0; y < kSlots; ++y) {
-      F2x8 f;
-      unpack_row(x[y].v, f);
-      load_row(a.side[ahead.side].x, ahead.at[0][y], ahead.on(a, y), l, x[y]);
+      F2x8& f = x[y];
       float scale;
       const float inv = row_rms_inv(f, a.eps, &scale);
       const uint64_t inv2 = f2_both(inv);
@@ -227,6 +255,7 @@ template <int kTurn, class Off>
 __global__ void __launch_bounds__(kThreads, kBwdResident) bam_qk_norm_bwd_kernel(const NormArgs a) {
   extern __shared__ __align__(16) float acc[];  // [rows][64], a warp adds to each
   __shared__ __align__(16) Angles<kBwdSlots> cs;
+  __shared__ __align__(16) Ring<2, kBwdSlots, kBwdStages> ring;
   grid_dep_trigger();
   const Lane l = lane_of<kTurn>(a.rope);
   const int lane = threadIdx.x & 31;
@@ -247,19 +276,23 @@ __global__ void __launch_bounds__(kThreads, kBwdResident) bam_qk_norm_bwd_kernel
   at.pass = ahead.pass = sp.first;
   walk_to(ahead, a, sp, l, xs);
   walk_to(at, a, sp, l, ys);
-  Row x[kSlots], g[kSlots];
-  auto load = [&](int y) {
-    const bool on = ahead.on(a, y);
-    load_row(a.side[ahead.side].x, ahead.at[0][y], on, l, x[y]);
-    load_row(a.side[ahead.side].g, ahead.at[1][y], on, l, g[y]);
+  auto load = [&](int stage) {  // of the next pass
+#pragma unroll
+    for (int y = 0; y < kSlots; ++y) {
+      const bool on = ahead.on(a, y);
+      copy_row(ring.v[stage][y][0], a.side[ahead.side].x, ahead.at[0][y], on, l);
+      copy_row(ring.v[stage][y][1], a.side[ahead.side].g, ahead.at[1][y], on, l);
+    }
+    copies_commit();
+    walk_on(ahead, a, sp, l, xs);
   };
 #pragma unroll
-  for (int y = 0; y < kSlots; ++y) load(y);
+  for (int stage = 0; stage < kBwdStages; ++stage) load(stage);
+  int stage = 0;
   F2x8 sum;
 #pragma unroll
   for (int i = 0; i < 8; ++i) sum[i] = 0;
   while (at.tile < sp.tiles) {
-    walk_on(ahead, a, sp, l, xs);
     if (kTurn != kNoTurn && at.pass == sp.first) {
       __syncthreads();  // the last tile's angles are no longer read
       tile_angles(a, at.tile, -1.0f, freq, cs);
@@ -267,12 +300,12 @@ __global__ void __launch_bounds__(kThreads, kBwdResident) bam_qk_norm_bwd_kernel
     }
     F2x8 w;
     load_weight(a.side[at.side].w + (a.per_head && at.on(a, 0) ? at.h * kHeadDim : 0), l, w);
+    copies_wait<kBwdStages - 1>();
 #pragma unroll
     for (int y = 0; y < kSlots; ++y) {
       F2x8 f, d;
-      unpack_row(x[y].v, f);
-      unpack_row(g[y].v, d);
-      load(y);
+      read_row(ring.v[stage][y][0], f);
+      read_row(ring.v[stage][y][1], d);
       float scale;
       const float inv = row_rms_inv(f, a.eps, &scale);
       turn_values<kTurn>(d, cs.cos[8 * y + l.t], cs.sin[8 * y + l.t], l);
@@ -299,6 +332,8 @@ __global__ void __launch_bounds__(kThreads, kBwdResident) bam_qk_norm_bwd_kernel
       }
       if (at.on(a, y)) store_row(a.side[at.side].y, at.at[0][y], l, d);
     }
+    load(stage);
+    if (++stage == kBwdStages) stage = 0;
     const int pass = at.pass, side = at.side;
     walk_on(at, a, sp, l, ys);
     if (a.per_head || at.pass == sp.first || at.side != side) {
