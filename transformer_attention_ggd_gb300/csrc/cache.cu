@@ -281,12 +281,12 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
 }
 
 // Prompts with norms: a CTA walks over tiles of eight tokens of one sequence, four heads (a
-// warp each) a pass: the queries', the keys' and the values'; the next pass's rows are on
-// their way while one is turned and stored.  A tile's angles and slots serve all its heads.
-// 8 prompts of up to 8192 tokens, 12 heads: 97 us (472 MB); in the units of the kernel
-// above, whose four rows a thread leave too few registers, 122.  6, 8 and 10 CTAs an SM
-// take 104, 97 and 103.
-constexpr int kRunWarps = 4, kRunThreads = 32 * kRunWarps, kRunTokens = 8, kRunResident = 8;
+// warp each) a pass: the queries', the keys' and the values'; the next two passes' rows are on
+// their way, in a ring in shared memory, while one is turned and stored.  A tile's angles and slots
+// serve all its heads.  8 prompts of up to 8192 tokens, 12 heads: 81 us (472 MB, 5.8 TB/s); with one
+// pass ahead in registers 97, in the units of the kernel above, whose four rows a thread leave too few
+// registers, 122.  4, 5, 7 and 8 CTAs an SM take 102, 86, 84 and 87.
+constexpr int kRunWarps = 4, kRunThreads = 32 * kRunWarps, kRunTokens = 8, kRunResident = 6;
 
 struct RunTile {
   unsigned tile;
@@ -308,6 +308,7 @@ __device__ __forceinline__ bool run_tile(const AppendArgs& a, unsigned tiles, Ru
 template <int kTurn>
 __global__ void __launch_bounds__(kRunThreads, kRunResident) bam_kv_append_run_kernel(const AppendArgs a) {
   __shared__ __align__(16) float cosines[kRunTokens][kHeadDim / 2], sines[kRunTokens][kHeadDim / 2];
+  __shared__ uint4 ring[2][2][kRunThreads];
   const CacheArgs& c = a.c;
   const RowLane l = row_lane<kTurn>(threadIdx.x & 3, a.rope.dims);
   const int lt = (threadIdx.x >> 2) & 7, lh = threadIdx.x >> 5;
@@ -324,22 +325,32 @@ __global__ void __launch_bounds__(kRunThreads, kRunResident) bam_kv_append_run_k
     if (!ok) record_bad_arg(c.status);
     return;
   }
+  // Every thread copies its chunks of the next two passes into a ring and reads them back.
   RunTile ahead = at;
   bool more = true;
-  int next = 0;  // pass of the rows on their way
-  uint4 x[2] = {};
-  auto load = [&]() {
+  int next = 0, stage = 0;  // pass of the rows copied last
+  auto issue = [&](int into) {
     const int kind = next < q_passes ? 0 : next < q_passes + kv_passes ? 1 : 2;
     const int h = kRunWarps * (next - (kind == 0 ? 0 : kind == 1 ? q_passes : q_passes + kv_passes)) + lh;
     const int t = ahead.t0 + lt;
-    if (!more || t >= ahead.n || h >= (kind == 0 ? a.H : c.Hkv)) return;
+    const bool on = more && t < ahead.n && h < (kind == 0 ? a.H : c.Hkv);
     const int64_t* st = kind == 0 ? a.qs : kind == 1 ? a.ks : a.vs;
-    const uint4* src = reinterpret_cast<const uint4*>((kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
-                                                      (ahead.b * st[0] + h * st[1] + t * st[2]));
-    x[0] = src[l.c0];
-    x[1] = src[l.c1];
+    const uint4* src = reinterpret_cast<const uint4*>(
+        on ? (kind == 0 ? a.q : kind == 1 ? a.k : a.v) + (ahead.b * st[0] + h * st[1] + t * st[2]) : a.k);
+    copy_chunk(&ring[into][0][threadIdx.x], src + (on ? l.c0 : 0), on);
+    copy_chunk(&ring[into][1][threadIdx.x], src + (on ? l.c1 : 0), on);
+    copies_commit();
   };
-  load();
+  auto load = [&](int into) {
+    if (more && ++next == passes) {
+      next = 0;
+      ahead.tile += gridDim.x;
+      more = run_tile(a, tiles, ahead, ok);
+    }
+    issue(into);
+  };
+  issue(0);
+  load(1);
   for (;;) {
     // This thread's token and its slot.
     const int t = at.t0 + lt;
@@ -370,13 +381,10 @@ __global__ void __launch_bounds__(kRunThreads, kRunResident) bam_kv_append_run_k
       const int kind = pass < q_passes ? 0 : pass < q_passes + kv_passes ? 1 : 2;
       const int h = kRunWarps * (pass - (kind == 0 ? 0 : kind == 1 ? q_passes : q_passes + kv_passes)) + lh;
       const int heads = kind == 0 ? a.H : c.Hkv;
-      uint4 w[2] = {x[0], x[1]};
-      if (++next == passes) {
-        next = 0;
-        ahead.tile += gridDim.x;
-        more = run_tile(a, tiles, ahead, ok);
-      }
-      load();
+      copies_wait<1>();
+      uint4 w[2] = {ring[stage][0][threadIdx.x], ring[stage][1][threadIdx.x]};
+      load(stage);  // (a tile has two passes at least: what is copied belongs to it or to the next one)
+      stage ^= 1;
       if (kind < 2) {
         F2x8 f;
         unpack_row(w, f);

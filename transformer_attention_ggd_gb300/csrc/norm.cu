@@ -15,8 +15,8 @@
 // order, as they lie in a projection's output.
 //
 // Measured on the device: 4 x 16383 tokens, 32 and 8 heads, out of a projection's output:
-// forward 112 us (0.67 GB, 6.0 TB/s; a copy along the same path takes 101), backward
-// 192 us (1.0 GB, 5.2 TB/s); 8 x 512 tokens, 12 and 12 heads: 9.0 and 15 us.
+// forward 111 us (0.67 GB, 6.0 TB/s; a copy along the same path takes 101), backward
+// 168 us (1.0 GB, 6.0 TB/s); 8 x 512 tokens, 12 and 12 heads: 21 us both calls.
 #include "norm_common.cuh"
 
 namespace bam {
@@ -29,8 +29,8 @@ constexpr int kPass = kNormPass;  // heads of a pass, a warp of eight rows each
 constexpr int kThreads = 32 * kPass;
 constexpr int kFwdStages = 3, kBwdStages = 2;  // passes whose rows are on their way
 constexpr int kFinishThreads = 1024;
-// Resident CTAs of an SM (forward 3, 4 and 5 took 126, 113 and 136 us in the first case
-// above, with eight warps a CTA).
+// Resident CTAs of an SM (forward 6, 7 and 8 take 111, 112 and 111 us in the first case
+// above, backward 3, 4 and 5 174, 168 and 182).
 constexpr int kFwdResident = 32 / kNormPass, kBwdResident = 16 / kNormPass;
 
 // This thread's place: tokens t and t + 8 of the tile, head h of each pass.
@@ -145,21 +145,11 @@ template <int kN, int kSlots, int kStages>
 struct Ring {
   uint4 v[kStages][kSlots][kN][2][kThreads];
 };
-// A chunk of 16 bytes, global -> shared, asynchronously; zeros where it is not `on`.
-__device__ __forceinline__ void copy_chunk(uint4* dst, const uint4* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
-               : "memory");
-}
 template <class Off>
 __device__ __forceinline__ void copy_row(uint4 (&dst)[2][kThreads], const uint16_t* p, Off at, bool on, const Lane& l) {
   const uint4* src = reinterpret_cast<const uint4*>(p) + (on ? at : 0);
   copy_chunk(&dst[0][threadIdx.x], src + (on ? l.c0 : 0), on);
   copy_chunk(&dst[1][threadIdx.x], src + (on ? l.c1 : 0), on);
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 __device__ __forceinline__ void read_row(const uint4 (&src)[2][kThreads], F2x8& f) {
   const uint4 v[2] = {src[0][threadIdx.x], src[1][threadIdx.x]};
@@ -403,8 +393,8 @@ __global__ void __launch_bounds__(kFinishThreads) bam_qk_norm_finish_kernel(cons
   }
 }
 
-// A launch of at most `resident` CTAs an SM: as many passes a part as leave every CTA
-// a part of a tile, so that angles serve many heads.
+// A launch of at most `resident` CTAs an SM: as many passes a part as leave a quarter of them a part of a
+// tile, so that angles serve many heads (8 x 512 tokens, both calls: 21 us; all of them 25, half 22).
 void split_passes(NormArgs* a, int slots, int sms, int resident, int most_ctas) {
   int all = 0;
   for (int k = 0; k < 2; ++k) all += (a->side[k].heads + kPass - 1) / kPass;
@@ -413,7 +403,7 @@ void split_passes(NormArgs* a, int slots, int sms, int resident, int most_ctas) 
   if (most > most_ctas) most = most_ctas;
   if (most < 1) most = 1;
   a->passes = all < kNormMaxPasses ? all : kNormMaxPasses;
-  while (a->passes > 1 && tiles * ((all + a->passes - 1) / a->passes) < most)
+  while (a->passes > 1 && tiles * ((all + a->passes - 1) / a->passes) < most / 4)
     a->passes = (a->passes + 1) / 2;
   a->parts = (all + a->passes - 1) / a->passes;
   int64_t each = most / a->parts;

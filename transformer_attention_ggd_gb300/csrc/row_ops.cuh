@@ -206,6 +206,17 @@ __device__ __forceinline__ float row_rms_inv(F2x8& f, float eps, float* scale) {
   return rsqrtf(ss * (1.0f / kHeadDim) + eps);
 }
 
+// A chunk of 16 bytes, global -> shared, asynchronously; zeros where it is not `on`.
+__device__ __forceinline__ void copy_chunk(uint4* dst, const uint4* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
 // A row's weights.
 __device__ __forceinline__ void load_weight(const float* p, const RowLane& l, F2x8& w) {
 #pragma unroll
