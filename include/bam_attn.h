@@ -556,12 +556,11 @@ enum {
   BAM_KERNEL_QK_NORM_FINISH = 14, /* sums of the weights' gradients         */
   BAM_KERNEL_SHARED_PREP = 15,    /* shared decode                          */
   BAM_KERNEL_SHARED = 16,
-  BAM_KERNEL_SHARED_JOIN = 17,
-  BAM_KERNEL_SHARED_WEIGH = 18,   /* accumulated weights                    */
+  BAM_KERNEL_SHARED_END = 17,     /* parts joined, weights added to         */
+  BAM_KERNEL_PREFIX = 18,         /* shared decode: the prefix in tiles     */
   BAM_KERNEL_EVICT_SELECT = 19,
   BAM_KERNEL_EVICT_MOVE = 20,
-  BAM_KERNEL_PREFIX = 21,         /* shared decode: the prefix in tiles     */
-  BAM_KERNEL_COUNT = 22
+  BAM_KERNEL_COUNT = 21
 };
 
 /* Instrumentation: while set, every launch of kernel `which` is bracketed

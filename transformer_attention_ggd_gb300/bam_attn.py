@@ -61,12 +61,11 @@ BAM_KERNEL_QK_NORM_BWD = 13
 BAM_KERNEL_QK_NORM_FINISH = 14
 BAM_KERNEL_SHARED_PREP = 15
 BAM_KERNEL_SHARED = 16
-BAM_KERNEL_SHARED_JOIN = 17
-BAM_KERNEL_SHARED_WEIGH = 18
+BAM_KERNEL_SHARED_END = 17
+BAM_KERNEL_PREFIX = 18
 BAM_KERNEL_EVICT_SELECT = 19
 BAM_KERNEL_EVICT_MOVE = 20
-BAM_KERNEL_PREFIX = 21
-BAM_KERNEL_COUNT = 22
+BAM_KERNEL_COUNT = 21
 
 # Every symbol that include/bam_attn.h declares.
 EXPORTED = (

@@ -808,10 +808,8 @@ bam_status bam_attn_decode_shared_paged(const void* q, const void* k_pages, cons
   }
   e = launch_kernel(BAM_KERNEL_SHARED, stream, [&] { return launch_shared(tk, tv, a, stream); });
   if (e != cudaSuccess) return BAM_ERR_CUDA;
-  e = launch_kernel(BAM_KERNEL_SHARED_JOIN, stream, [&] { return launch_shared_join(a, stream); });
-  if (e != cudaSuccess || !marks) return cuda_status(e);
   return cuda_status(
-      launch_kernel(BAM_KERNEL_SHARED_WEIGH, stream, [&] { return launch_shared_weigh(a, stream); }));
+      launch_kernel(BAM_KERNEL_SHARED_END, stream, [&] { return launch_shared_end(a, stream); }));
 }
 
 size_t bam_kv_evict_workspace_size(int B, int Hkv, int Tmax, int budget) {

@@ -9,14 +9,15 @@
 // which stay in L2).  The first kernel starts the call and fills the prefix's table of biases;
 // the prefix goes in tiles (prefix.cu) where nine or more rows share it; the main kernel takes
 // what is left on mma.sync, whose 16 rows the heads of a group fill as far as they do; the
-// join adds up the parts of a row, and the last kernel the weights, which need every lse.
+// last one joins the parts of a row and, in blocks of its own, adds to the weights, which need every lse:
+// each takes it from the parts (two kernels in turn took 2.5 us longer in small calls).
 //
 // Positions of kept keys are any numbers, so that the own keys' biases are evaluated where they
 // are needed (20 instructions and two special functions; windows of a table in order of
 // positions took 160 us where this takes 151).
 //
-// Measured: 64 caches of 8192 keys, 12 heads, with weights 151 us (0.85 GB, 5.7 TB/s); one of
-// 131072, 32 and 8 heads, fp32, 65 us; 4 sequences of 40 keys behind 1000, 12 heads, 11.5 us.
+// Measured: 64 caches of 8192 keys, 12 heads, with weights 150 us (0.85 GB, 5.7 TB/s); one of
+// 131072, 32 and 8 heads, fp32, 64 us; 4 sequences of 40 keys behind 1000, 12 heads, 11 us.
 #include "shared_common.cuh"
 
 namespace bam {
@@ -522,16 +523,20 @@ __global__ void __launch_bounds__(kThreads, kResident)
   if (a.copies && blockIdx.x == gridDim.x - 1) grid_dep_wait();
 }
 
-// Joins the parts of a row's keys: kWarpsRow warps a row, kRowsBlock rows a block.
-template <int kWarpsRow, int kRowsBlock>
-__global__ void __launch_bounds__(32 * kWarpsRow * kRowsBlock) bam_shared_join_kernel(const SharedArgs a) {
+constexpr int kEndThreads = 256;
+constexpr int kEndWarps = kEndThreads / 32;
+
+// Joins the parts of a row's keys, kWarpsRow warps a row.
+template <int kWarpsRow>
+__device__ __forceinline__ void join_rows(const SharedArgs& a, int64_t block) {
+  constexpr int kRowsBlock = kEndWarps / kWarpsRow;
   __shared__ float red_m[kRowsBlock][kWarpsRow], red_l[kRowsBlock][kWarpsRow];
   __shared__ float2 red_o[kRowsBlock][kWarpsRow][32];
-  grid_dep_wait();
-  grid_dep_trigger();
-  const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) % kWarpsRow, rb = (threadIdx.x >> 5) / kWarpsRow;
   const int64_t rows = static_cast<int64_t>(a.c.B) * a.H;
-  const int64_t row_raw = static_cast<int64_t>(blockIdx.x) * kRowsBlock + rb;
+  if (block * kRowsBlock >= rows) return;
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) % kWarpsRow, rb = (threadIdx.x >> 5) / kWarpsRow;
+  const int64_t row_raw = block * kRowsBlock + rb;
   const int64_t row = min(row_raw, rows - 1), base = row * a.slots;
   const bool aborted = *reinterpret_cast<volatile int*>(&a.c.status->abort) != 0;
   float M = kNoMax;
@@ -584,28 +589,28 @@ __global__ void __launch_bounds__(32 * kWarpsRow * kRowsBlock) bam_shared_join_k
     reinterpret_cast<float2*>(static_cast<float*>(a.o) + row * kHeadDim)[lane] = make_float2(o0, o1);
   else
     reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + row * kHeadDim)[lane] = pack_bf16x2(o0, o1);
-  if (lane == 0) {
-    if (a.lse) a.lse[row] = lse2 * kLn2f;
-    // for the weights, in the first part's place
-    if (a.z) a.ml[base] = make_float2(lse2, 0.0f);
-  }
+  if (a.lse && lane == 0) a.lse[row] = lse2 * kLn2f;
 }
 
-constexpr int kWeighThreads = 256;
 constexpr int kWeighFours = 2;  // of a thread
-constexpr int kWeighKeys = 4 * kWeighFours * kWeighThreads;
+constexpr int kWeighKeys = 4 * kWeighFours * kEndThreads;
+constexpr int kWeighRows = 64;  // whose lse is at hand at a time
 
-// w_j <- decay w_j + sum over the heads of the group of exp(z_j - lse).
-__global__ void __launch_bounds__(kWeighThreads) bam_shared_weigh_kernel(const SharedArgs a) {
-  const int hk = blockIdx.y, b = blockIdx.z;
+// w_j <- decay w_j + sum over the heads of the group of exp(z_j - lse), for a run of a sequence's keys.
+__device__ __forceinline__ void weigh_keys(const SharedArgs& a, unsigned block) {
+  __shared__ float lse[kWeighRows];
+  const int hk = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
   bool ok = true;
-  const int len = own_len(a, b, &ok), j0 = blockIdx.x * kWeighKeys + 4 * threadIdx.x;
+  const int len = own_len(a, b, &ok);
+  const int64_t begin = static_cast<int64_t>(block) * kWeighKeys;
+  if (begin >= len) return;
+  const int j0 = static_cast<int>(begin) + 4 * threadIdx.x;
   // What no kernel of the call writes is on its way before the logits are there.
   float* at[kWeighFours];
   float4 old[kWeighFours];
 #pragma unroll
   for (int x = 0; x < kWeighFours; ++x) {
-    const int j = j0 + 4 * kWeighThreads * x;
+    const int j = j0 + 4 * kEndThreads * x;
     at[x] = nullptr;
     if (j >= len) continue;
     const int pg = __ldg(a.c.block_table + static_cast<size_t>(b) * a.c.max_blocks + j / a.c.page);
@@ -615,25 +620,53 @@ __global__ void __launch_bounds__(kWeighThreads) bam_shared_weigh_kernel(const S
   }
   grid_dep_wait();
   if (*reinterpret_cast<volatile int*>(&a.c.status->abort)) return;
+  const int64_t row0 = static_cast<int64_t>(b) * a.H + hk * a.group;
   float w[kWeighFours][4] = {};
-  for (int g = 0; g < a.group; ++g) {
-    const int64_t row = static_cast<int64_t>(b) * a.H + hk * a.group + g;
-    const float lse = a.ml[row * a.slots].x;
+  float4 z[kWeighFours];
+  auto load = [&](int g) {
 #pragma unroll
-    for (int x = 0; x < kWeighFours; ++x) {
-      if (!at[x]) continue;
-      const float4 z = *reinterpret_cast<const float4*>(a.z + row * a.zstride + j0 + 4 * kWeighThreads * x);
-      w[x][0] += ex2_approx(z.x - lse);
-      w[x][1] += ex2_approx(z.y - lse);
-      w[x][2] += ex2_approx(z.z - lse);
-      w[x][3] += ex2_approx(z.w - lse);
+    for (int x = 0; x < kWeighFours; ++x)
+      if (at[x]) z[x] = *reinterpret_cast<const float4*>(a.z + (row0 + g) * a.zstride + j0 + 4 * kEndThreads * x);
+  };
+  load(0);
+  for (int g0 = 0; g0 < a.group; g0 += kWeighRows) {
+    const int rows = min(kWeighRows, a.group - g0);
+    if (g0 > 0) __syncthreads();
+    for (int g = threadIdx.x >> 5; g < rows; g += kEndWarps) {
+      // From the row's parts, as the join has it (which runs beside this).
+      const float2* ml = a.ml + (row0 + g0 + g) * a.slots;
+      float M = kNoMax, L = 0.0f;
+#pragma unroll 4
+      for (int s = lane; s < a.slots; s += 32) M = fmaxf(M, ml[s].x);
+#pragma unroll
+      for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+#pragma unroll 4
+      for (int s = lane; s < a.slots; s += 32) {
+        const float2 p = ml[s];
+        L += p.y == 0.0f ? 0.0f : p.y * ex2_approx(p.x - M);
+      }
+#pragma unroll
+      for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+      if (lane == 0) lse[g] = M + __log2f(L);
+    }
+    __syncthreads();
+    for (int g = 0; g < rows; ++g) {
+#pragma unroll
+      for (int x = 0; x < kWeighFours; ++x) {
+        if (!at[x]) continue;
+        w[x][0] += ex2_approx(z[x].x - lse[g]);
+        w[x][1] += ex2_approx(z[x].y - lse[g]);
+        w[x][2] += ex2_approx(z[x].z - lse[g]);
+        w[x][3] += ex2_approx(z[x].w - lse[g]);
+      }
+      if (g0 + g + 1 < a.group) load(g0 + g + 1);
     }
   }
 #pragma unroll
   for (int x = 0; x < kWeighFours; ++x) {
     if (!at[x]) continue;
     const float o[4] = {old[x].x, old[x].y, old[x].z, old[x].w};
-    const int left = len - (j0 + 4 * kWeighThreads * x);
+    const int left = len - (j0 + 4 * kEndThreads * x);
 #pragma unroll
     for (int y = 0; y < 4; ++y) w[x][y] = fmaf(a.decay, o[y], w[x][y]);
     if (left >= 4) {
@@ -644,6 +677,17 @@ __global__ void __launch_bounds__(kWeighThreads) bam_shared_weigh_kernel(const S
         if (y < left) at[x][y] = w[x][y];
     }
   }
+}
+
+// The end of a call: blocks that join rows and, with weights, behind them blocks that add to them; both
+// need nothing but the parts.
+template <int kWarpsRow>
+__global__ void __launch_bounds__(kEndThreads) bam_shared_end_kernel(const SharedArgs a, unsigned joins) {
+  // (every sequence and key head has `joins` of the joining blocks)
+  if (blockIdx.x < joins)
+    join_rows<kWarpsRow>(a, (static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y) * joins + blockIdx.x);
+  else
+    weigh_keys(a, blockIdx.x - joins);
 }
 
 }  // namespace
@@ -710,21 +754,18 @@ cudaError_t launch_shared(const CUtensorMap& tk, const CUtensorMap& tv, const Sh
   return two ? launch_main<true, 2>(tk, tv, a, items, st) : launch_main<false, 2>(tk, tv, a, items, st);
 }
 
-cudaError_t launch_shared_join(const SharedArgs& a, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(a.c.B) * a.H;
-  auto launch = [&](auto* kernel, int warps, int block) {
-    return launch_k(kernel, dim3(static_cast<unsigned>((rows + block - 1) / block)), dim3(32 * warps * block), 0,
-                    st, true, a);
+cudaError_t launch_shared_end(const SharedArgs& a, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(a.c.B) * a.H, heads = a.z ? static_cast<int64_t>(a.c.B) * a.c.Hkv : 1;
+  auto launch = [&](auto* kernel, int warps) {
+    const int64_t blocks = (rows * warps + kEndWarps - 1) / kEndWarps, joins = (blocks + heads - 1) / heads;
+    const int64_t tiles = a.z ? (a.zstride + kWeighKeys - 1) / kWeighKeys : 0;
+    const dim3 grid(static_cast<unsigned>(joins + tiles), a.z ? a.c.Hkv : 1, a.z ? a.c.B : 1);
+    return launch_k(kernel, grid, dim3(kEndThreads), 0, st, true, a, static_cast<unsigned>(joins));
   };
   // (8192 rows of 7 parts: 7 us by a warp each, 12 by four; 768 rows of 55: 10 and 7)
-  if (a.slots <= 4 || (a.slots <= 16 && rows > 2048)) return launch(bam_shared_join_kernel<1, 8>, 1, 8);
-  if (a.slots <= 64) return launch(bam_shared_join_kernel<4, 2>, 4, 2);
-  return launch(bam_shared_join_kernel<32, 1>, 32, 1);
-}
-
-cudaError_t launch_shared_weigh(const SharedArgs& a, cudaStream_t st) {
-  const unsigned tiles = static_cast<unsigned>((a.zstride + kWeighKeys - 1) / kWeighKeys);
-  return launch_k(bam_shared_weigh_kernel, dim3(tiles, a.c.Hkv, a.c.B), dim3(kWeighThreads), 0, st, true, a);
+  if (a.slots <= 4 || (a.slots <= 16 && rows > 2048)) return launch(bam_shared_end_kernel<1>, 1);
+  if (a.slots <= 64) return launch(bam_shared_end_kernel<4>, 4);
+  return launch(bam_shared_end_kernel<8>, 8);
 }
 
 }  // namespace bam

@@ -110,8 +110,7 @@ struct EvictArgs {
 cudaError_t launch_shared_prep(const SharedArgs& a, cudaStream_t st);
 cudaError_t launch_shared(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArgs& a,
                           cudaStream_t st);
-cudaError_t launch_shared_join(const SharedArgs& a, cudaStream_t st);
-cudaError_t launch_shared_weigh(const SharedArgs& a, cudaStream_t st);
+cudaError_t launch_shared_end(const SharedArgs& a, cudaStream_t st);
 cudaError_t launch_prefix(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArgs& a,
                           cudaStream_t st);
 // Splits of the own and prefix keys and the table's size; fills nsplit, npsplit, copies,
