@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(kRunThreads, kRunResident) bam_kv_append_run_k
     if (!more) break;
     at = ahead;
   }
+  copies_wait<0>();  // (no copy outlives its block)
   if (!ok) record_bad_arg(c.status);
 }
 
@@ -530,7 +531,8 @@ cudaError_t launch_append(const AppendArgs& args, cudaStream_t st) {
   if (a.extended) {
     const int turned = a.rope.dims == 0 ? kNoTurn : a.rope.interleaved ? kPairs : kHalves;
     const int64_t run_tiles = static_cast<int64_t>(a.c.B) * ((a.c.N + kRunTokens - 1) / kRunTokens);
-    if (tiles > run && !a.c.parents && run_tiles <= 0x7FFFFFFF) {
+    // (2 prompts of 2000 tokens, 12 heads: 10.6 us in runs, 11.5 in units; 32 of 64 tokens 8.6 and 7.7)
+    if (tiles > run / 2 && !a.c.parents && run_tiles <= 0x7FFFFFFF) {
       constexpr Kernel runs[] = {bam_kv_append_run_kernel<kNoTurn>, bam_kv_append_run_kernel<kHalves>,
                                  bam_kv_append_run_kernel<kPairs>};
       int64_t ctas = static_cast<int64_t>(sm_count()) * kRunResident;

@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, kFwdResident) bam_qk_norm_fwd_kernel
     }
     walk_on(at, a, sp, l, ys);
   }
+  copies_wait<0>();  // (no copy outlives its block)
 }
 
 // Sum of a warp's eight rows of 16 values (f32x2 pairs): each step hands over half of
@@ -337,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, kBwdResident) bam_qk_norm_bwd_kernel
       for (int i = 0; i < 8; ++i) sum[i] = 0;
     }
   }
+  copies_wait<0>();  // (no copy outlives its block)
   __syncthreads();
   const int rows = norm_part_rows(a);
   float* out = a.part + static_cast<int64_t>(blockIdx.x) * rows * kHeadDim;
