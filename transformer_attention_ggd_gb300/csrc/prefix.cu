@@ -10,24 +10,22 @@
 //
 // A tile of 64 keys is a chain of S = Q K^T, softmax, O += P V, each of which waits for the one
 // before; so that a processor has more than one under way, its CTA takes a part's tiles in turn
-// with four chains (three with fp32 output), each with a maximum, a sum and an O of its own, which are
-// joined at the end.  A chain: four warps, a thread a row (its lane of Tensor Memory), which
+// with three chains, each with a maximum, a sum and an O of its own, which are joined at the end.  A chain: four warps, a thread a row (its lane of Tensor Memory), which
 // also copy their rows' windows; P lies over S, and the next S is issued right behind the
 // product that reads P, so that one wait and one arrival a tile are all that a chain needs.
 // One more warp copies K and V by TMA into rings, one issues the products.
 //
 // With up to 64 rows a row stands in two or four lanes, each with its part of a tile's keys and
-// zeros for the weights of the others: 32 rows over 32768 keys of 12 heads take 36 us with four
-// lanes a row, 44 with two, 69 with one; 64 rows 44 with two, 66 with one.
+// zeros for the weights of the others: 32 rows over 32768 keys of 12 heads take 33 us with four
+// lanes a row, 40 with two, 63 with one; 64 rows 40 with two, 61 with one.
 //
-// Measured, of the whole call: 64 sequences, 12 heads, 32768 keys: 50 us, of it 30 in this kernel
-// (100 MB at 3.4 TB/s); 256 sequences, 32 and 8 heads, 8111 keys, fp32: 104 us, of it 84 here, with
+// Measured, of the whole call: 64 sequences, 12 heads, 32768 keys: 47 us, of it 28 in this kernel
+// (100 MB at 3.6 TB/s); 256 sequences, 32 and 8 heads, 8111 keys, fp32: 104 us, of it 84 here, with
 // the tensor pipe busy for a fifth of it: the softmax of 128 rows is what lasts.  A tile takes 1.2 us a
-// processor there (bf16 0.9, of which 0.35 for the windows, which come at 5 TB/s out of L2
-// beside 2.5 TB/s of keys); of a chain's 7500 cycles a tile clocks gave 2000 to the windows' copies,
-// 1100 each to the logits, the maximum and the exponentials, 1000 to waits.  One chain a CTA and two CTAs a
-// processor took 52 and 109 us.  The issuing thread is chosen by elect.sync: chosen by its lane it
-// took 60 us where it takes 51.
+// processor there, with bf16 output 0.9; without the copies of the windows, which come at 5 TB/s out of
+// L2 beside 2.5 TB/s of keys, the calls take 45 and 93, and that with bf16 output 47 instead of 73.  One chain a
+// CTA and two CTAs a processor took 52 and 109 us.  The issuing thread is chosen by elect.sync: chosen
+// by its lane it took 60 us where it took 51.
 #include "shared_common.cuh"
 
 namespace bam {
@@ -38,6 +36,9 @@ constexpr int kLanes = 128;
 constexpr int kBoxBytes = kTile * kHeadDim * 2, kQBytes = kLanes * kHeadDim * 2;
 constexpr int kMaxStages = 8;
 constexpr int kSmemMost = 224 * 1024;
+constexpr int kChains = 3;                     // (four, with bf16 output: 50 us where three take 47)
+constexpr int kSoft = 4 * kChains;             // their warps
+constexpr int kThreads = 32 * (kSoft + 2);
 constexpr int kOutStride = kHeadDim + 4;       // floats
 constexpr float kRescale = 8.0f;               // log2 units by which a weight may exceed 1
 constexpr uint32_t kTmemCols = 512;
@@ -54,9 +55,6 @@ enum : int {
 // kParts: bf16 parts of a weight.
 template <int kCopies, int kParts>
 struct Shape {
-  static constexpr int kChains = kParts == 3 ? 3 : 4;
-  static constexpr int kSoft = 4 * kChains;          // warps
-  static constexpr int kThreads = 32 * (kSoft + 2);
   static constexpr int kWin = kTile / kCopies;       // keys of a lane in a tile
   static constexpr int kRows = kLanes / kCopies;     // rows of an item
   static constexpr int kWinStride = kWin + 4;        // floats: 16-byte reads of eight rows hit all banks
@@ -78,12 +76,10 @@ struct Shape {
 // O leaves the accumulator, which cuts off its last place in every step, after as many tiles (96
 // steps for fp32 output, 512 for bf16).
 __host__ __device__ constexpr int flush_tiles(bool fp32) { return fp32 ? 8 : 128; }
-constexpr int chain_count(bool fp32) { return fp32 ? Shape<1, 3>::kChains : Shape<1, 1>::kChains; }
-static_assert(chain_count(false) >= chain_count(true) && flush_tiles(false) >= flush_tiles(true));
 
 struct PrefixBars {
   uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
-  uint64_t q_full, s_full[4], p_full[4], final;
+  uint64_t q_full, s_full[kChains], p_full[kChains], final;
   uint32_t win[kLanes];  // where each lane's window begins in the table, in 16-byte words
   uint32_t tmem;
   int abort_flag;
@@ -142,11 +138,11 @@ struct Walk {
 };
 
 template <int kCopies, int kParts>
-__global__ void __launch_bounds__(Shape<kCopies, kParts>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     bam_prefix_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                       const SharedArgs a) {
   using S = Shape<kCopies, kParts>;
-  constexpr int kFlush = flush_tiles(kParts == 3), kChains = S::kChains, kWin = S::kWin;
+  constexpr int kFlush = flush_tiles(kParts == 3), kWin = S::kWin;
   constexpr int kKStages = S::kKStages, kVStages = S::kVStages;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ PrefixBars bars;
@@ -184,7 +180,7 @@ __global__ void __launch_bounds__(Shape<kCopies, kParts>::kThreads, 1)
     mbar_init(&bars.final, 1);
     fence_barrier_init();
   }
-  if (warp == S::kSoft) {
+  if (warp == kSoft) {
     tmem_alloc(&bars.tmem, kTmemCols);
     tmem_relinquish();
   }
@@ -193,7 +189,7 @@ __global__ void __launch_bounds__(Shape<kCopies, kParts>::kThreads, 1)
   const int ln = threadIdx.x % kLanes, c = ln / S::kRows;
   const RowAt r = row_at(a, hk, row0 + ln % S::kRows);
   int pos = 0;
-  if (warp < S::kSoft) {
+  if (warp < kSoft) {
     pos = r.on ? query_pos(a, r.b, P, &ok_arg) : 0;
     const int y = a.tab_top - (r.on ? pos : max(P - 1, 0)) + kbeg + c * kWin, k = (4 - (y & 3)) & 3;
     if (warp < 4)
@@ -205,7 +201,7 @@ __global__ void __launch_bounds__(Shape<kCopies, kParts>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
 
-  if (warp == S::kSoft + 1) {
+  if (warp == kSoft + 1) {
     // ------------------------------------------------------------ K and V, in the order of their use
     if (elect_one()) {
       bool bad_page = false, ok = true;
@@ -250,7 +246,7 @@ __global__ void __launch_bounds__(Shape<kCopies, kParts>::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == S::kSoft) {
+  } else if (warp == kSoft) {
     // ------------------------------------------------------------ products
     if (elect_one()) {
       const uint32_t idS = idesc_bf16(kLanes, kTile, false, false);
@@ -498,7 +494,7 @@ __global__ void __launch_bounds__(Shape<kCopies, kParts>::kThreads, 1)
       tc_fence_after();
     }
     copies_wait();
-    soft_sync(kSoftBarrier, 32 * S::kSoft);
+    soft_sync(kSoftBarrier, 32 * kSoft);
     float* const out = reinterpret_cast<float*>(smem);
     float2* const ml = reinterpret_cast<float2*>(smem + S::kMl);
     if (ok) {
@@ -514,9 +510,9 @@ __global__ void __launch_bounds__(Shape<kCopies, kParts>::kThreads, 1)
             *reinterpret_cast<float4*>(out + (g * kLanes + ln) * kOutStride + 16 * x + 4 * y) = v[y];
         }
     }
-    soft_sync(kSoftBarrier, 32 * S::kSoft);
+    soft_sync(kSoftBarrier, 32 * kSoft);
     if (ok) {
-      for (int i = threadIdx.x; i < S::kRows * (kHeadDim / 4); i += 32 * S::kSoft) {
+      for (int i = threadIdx.x; i < S::kRows * (kHeadDim / 4); i += 32 * kSoft) {
         const int lr = i / (kHeadDim / 4), x = i % (kHeadDim / 4);
         const RowAt ro = row_at(a, hk, row0 + lr);
         if (!ro.on) break;
@@ -542,7 +538,7 @@ __global__ void __launch_bounds__(Shape<kCopies, kParts>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == S::kSoft) {
+  if (warp == kSoft) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -558,7 +554,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArg
   static bool limit_set[64] = {};
   const cudaError_t e = smem_limit_once(bam_prefix_kernel<kCopies, kParts>, smem, limit_set);
   if (e != cudaSuccess) return e;
-  return launch_k(bam_prefix_kernel<kCopies, kParts>, dim3(static_cast<unsigned>(items)), dim3(S::kThreads),
+  return launch_k(bam_prefix_kernel<kCopies, kParts>, dim3(static_cast<unsigned>(items)), dim3(kThreads),
                   smem, st, true, tk, tv, a);
 }
 
@@ -581,8 +577,8 @@ void prefix_split(SharedArgs* a, int64_t Pmax, int64_t Tmax) {
     }
   }
   // (of either output: the workspace is one size)
-  a->spills = part_keys(static_cast<int>(Pmax), a->npsplit) > flush_tiles(true) * chain_count(true) * kTile
-                  ? a->npsplit * chain_count(false) * a->copies
+  a->spills = part_keys(static_cast<int>(Pmax), a->npsplit) > flush_tiles(true) * kChains * kTile
+                  ? a->npsplit * kChains * a->copies
                   : 0;
   // Distances of the prefix's keys, and behind them windows that reach past the last key.
   const int64_t top = a->max_pos > 0 ? (a->max_pos > Pmax ? a->max_pos : Pmax) : Pmax + Tmax;

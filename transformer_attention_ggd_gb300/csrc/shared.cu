@@ -523,11 +523,8 @@ __global__ void __launch_bounds__(kThreads, kResident)
   if (a.copies && blockIdx.x == gridDim.x - 1) grid_dep_wait();
 }
 
-constexpr int kEndThreads = 256;
-constexpr int kEndWarps = kEndThreads / 32;
-
-// Joins the parts of a row's keys, kWarpsRow warps a row.
-template <int kWarpsRow>
+// Joins the parts of a row's keys, kWarpsRow warps a row, kEndWarps a block.
+template <int kWarpsRow, int kEndWarps>
 __device__ __forceinline__ void join_rows(const SharedArgs& a, int64_t block) {
   constexpr int kRowsBlock = kEndWarps / kWarpsRow;
   __shared__ float red_m[kRowsBlock][kWarpsRow], red_l[kRowsBlock][kWarpsRow];
@@ -593,11 +590,13 @@ __device__ __forceinline__ void join_rows(const SharedArgs& a, int64_t block) {
 }
 
 constexpr int kWeighFours = 2;  // of a thread
-constexpr int kWeighKeys = 4 * kWeighFours * kEndThreads;
+constexpr int weigh_keys_of(int warps) { return 4 * kWeighFours * 32 * warps; }
 constexpr int kWeighRows = 64;  // whose lse is at hand at a time
 
 // w_j <- decay w_j + sum over the heads of the group of exp(z_j - lse), for a run of a sequence's keys.
+template <int kEndWarps>
 __device__ __forceinline__ void weigh_keys(const SharedArgs& a, unsigned block) {
+  constexpr int kEndThreads = 32 * kEndWarps, kWeighKeys = 4 * kWeighFours * kEndThreads;
   __shared__ float lse[kWeighRows];
   const int hk = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
   bool ok = true;
@@ -681,13 +680,13 @@ __device__ __forceinline__ void weigh_keys(const SharedArgs& a, unsigned block) 
 
 // The end of a call: blocks that join rows and, with weights, behind them blocks that add to them; both
 // need nothing but the parts.
-template <int kWarpsRow>
-__global__ void __launch_bounds__(kEndThreads) bam_shared_end_kernel(const SharedArgs a, unsigned joins) {
+template <int kWarpsRow, int kEndWarps>
+__global__ void __launch_bounds__(32 * kEndWarps) bam_shared_end_kernel(const SharedArgs a, unsigned joins) {
   // (every sequence and key head has `joins` of the joining blocks)
   if (blockIdx.x < joins)
-    join_rows<kWarpsRow>(a, (static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y) * joins + blockIdx.x);
+    join_rows<kWarpsRow, kEndWarps>(a, (static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y) * joins + blockIdx.x);
   else
-    weigh_keys(a, blockIdx.x - joins);
+    weigh_keys<kEndWarps>(a, blockIdx.x - joins);
 }
 
 }  // namespace
@@ -756,16 +755,19 @@ cudaError_t launch_shared(const CUtensorMap& tk, const CUtensorMap& tv, const Sh
 
 cudaError_t launch_shared_end(const SharedArgs& a, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(a.c.B) * a.H, heads = a.z ? static_cast<int64_t>(a.c.B) * a.c.Hkv : 1;
-  auto launch = [&](auto* kernel, int warps) {
-    const int64_t blocks = (rows * warps + kEndWarps - 1) / kEndWarps, joins = (blocks + heads - 1) / heads;
-    const int64_t tiles = a.z ? (a.zstride + kWeighKeys - 1) / kWeighKeys : 0;
+  auto launch = [&](auto* kernel, int warps, int block) {  // of a row, of a block
+    const int64_t blocks = (rows * warps + block - 1) / block, joins = (blocks + heads - 1) / heads;
+    const int64_t tiles = a.z ? (a.zstride + weigh_keys_of(block) - 1) / weigh_keys_of(block) : 0;
     const dim3 grid(static_cast<unsigned>(joins + tiles), a.z ? a.c.Hkv : 1, a.z ? a.c.B : 1);
-    return launch_k(kernel, grid, dim3(kEndThreads), 0, st, true, a, static_cast<unsigned>(joins));
+    return launch_k(kernel, grid, dim3(32 * block), 0, st, true, a, static_cast<unsigned>(joins));
   };
   // (8192 rows of 7 parts: 7 us by a warp each, 12 by four; 768 rows of 55: 10 and 7)
-  if (a.slots <= 4 || (a.slots <= 16 && rows > 2048)) return launch(bam_shared_end_kernel<1>, 1);
-  if (a.slots <= 64) return launch(bam_shared_end_kernel<4>, 4);
-  return launch(bam_shared_end_kernel<8>, 8);
+  if (a.slots <= 4 || (a.slots <= 16 && rows > 2048)) return launch(bam_shared_end_kernel<1, 8>, 1, 8);
+  if (a.slots <= 64) return launch(bam_shared_end_kernel<4, 8>, 4, 8);
+  // (96 rows of 8192 keys in 129 parts: 15.2 us with eight warps a row, 16.8 with 32; of 65536 in some
+  // hundred: 57 and 54)
+  if (a.slots <= 192) return launch(bam_shared_end_kernel<8, 8>, 8, 8);
+  return launch(bam_shared_end_kernel<32, 32>, 32, 32);
 }
 
 }  // namespace bam
