@@ -383,8 +383,7 @@ bam_status bam_kv_append_norm_paged(const void* k, const void* v, const void* q,
  * in a key reaches o, lse and the weights of its head; NaN and infinities in a
  * value reach o (an infinity of the prefix as itself or as NaN).  Products and
  * weights are summed in fp32; the weights enter the product with V as sums of
- * bf16 parts: 24 bits for fp32 output; for bf16 output 16, or 8 over a prefix
- * that more than 8 rows of a key head share.
+ * bf16 parts: 24 bits for fp32 output, 16 for bf16 output.
  * If a device wait of the call gives up, o and lse are written as NaN and no
  * weight changes.  o: [B, H, D], fp32 when o_fp32 != 0, else bf16; lse: fp32
  * [B, H] or NULL.  p->causal is ignored.  Every output is bitwise repeatable. */

@@ -200,6 +200,33 @@ def test_shared_sums_that_leave_tensor_memory(out, P, flat):
     assert torch.equal(o, again) and torch.equal(lse, lagain)
 
 
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,H,Hkv", [(4, 2, 1), (5, 2, 1), (20, 3, 1), (50, 1, 1), (150, 2, 2)])
+def test_shared_weights_have_as_many_bits_whoever_shares_the_prefix(B, H, Hkv, out):
+    """Values +1 and -1 of neighbouring keys nearly cancel, so that the output's own
+    rounding is small beside a weight's: 2^-16 of the sum of the weights (1) with bf16
+    output, over a prefix of few rows and of many."""
+    P, n = 70, 2
+    c = Cache(B, Hkv, 64, [n] * B, P)
+    sign = torch.randint(0, 2, (c.v.shape[0], Hkv, 32, 1, 64), generator=c.gen, device="cuda") * 2 - 1
+    sign = torch.cat([sign, -sign], 3).reshape(c.v.shape).to(torch.bfloat16)
+    c.v.copy_(torch.where(torch.isnan(c.v), c.v, sign))
+    for row in (c.prefix.long(), c.table.long().clamp(min=0)):
+        c.k[row] = 0
+    t = [dev_f32(x) for x in ([40.0] * H, [0.6] * H, [1.0] * H, [1.0] * H)]
+    q, lens = _normal(c.gen, B, H, 64), [n] * B
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    o, _ = ba.attention_decode_shared_paged(q, c.k, c.v, c.table, _i32(lens), *t, prefix_table=c.prefix,
+                                            prefix_len=_i32([P]), o_dtype=dt)
+    oref, _, _, oerr, _, _ = decode(q, c.k, c.v, c.table, lens, c.prefix, P, None, None, t, False, False, False)
+    bound = oerr  # with fp32 output: a weight's delta and 2^-22, and 2^-24 for each key's sum
+    if out == "bf16":
+        bound = oerr + 2.0 ** -16
+        bound = bound + 2.0 ** -8 * (oref.abs() + bound)
+    d = (o.double() - oref).abs()
+    assert torch.all(d <= bound), float((d / bound).max())
+
+
 @pytest.mark.parametrize("lens,P,H,Hkv,marked", [([9000], 0, 8, 2, True), ([0], 9000, 4, 4, False),
                                                  ([20000, 5], 70, 4, 2, True), ([1] * 40, 20001, 8, 2, False),
                                                  ([0, 1], 40000, 2, 1, True)])

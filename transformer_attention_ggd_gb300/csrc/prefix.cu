@@ -19,11 +19,16 @@
 // zeros for the weights of the others: 32 rows over 32768 keys of 12 heads take 33 us with four
 // lanes a row, 40 with two, 63 with one; 64 rows 40 with two, 61 with one.
 //
-// Measured, of the whole call: 64 sequences, 12 heads, 32768 keys: 47 us, of it 28 in this kernel
-// (100 MB at 3.6 TB/s); 256 sequences, 32 and 8 heads, 8111 keys, fp32: 104 us, of it 84 here, with
-// the tensor pipe busy for a fifth of it: the softmax of 128 rows is what lasts.  A tile takes 1.2 us a
-// processor there, with bf16 output 0.9; without the copies of the windows, which come at 5 TB/s out of
-// L2 beside 2.5 TB/s of keys, the calls take 45 and 93, and that with bf16 output 47 instead of 73.  One chain a
+// The weights enter P V as sums of bf16 parts: three for fp32 output, two (16 bits, as for own keys) for bf16
+// output.  One part, 8 bits, took 47.5 and 78.0 us where two take 49.0 and 81.4 (the cases below, bf16 output), and
+// put a sequence's error down to how many others it shares the prefix with.
+//
+// Measured, of the whole call: 64 sequences, 12 heads, 32768 keys: 49 us, of it 29 in this kernel
+// (100 MB at 3.5 TB/s); 256 sequences, 32 and 8 heads, 8111 keys: 81 us, of it 61 here, and with fp32 output 105
+// and 86, with the tensor pipe busy for a fifth of it: the softmax of 128 rows is what lasts.  A tile takes
+// 1.2 us a processor with fp32 output, with bf16 output and one part a weight 0.9; without the copies of the windows,
+// which come at 5 TB/s out of L2 beside 2.5 TB/s of keys, the first call took 45 instead of 47, the second 47
+// instead of 73 (one part) and 93 instead of 104 (fp32).  One chain a
 // CTA and two CTAs a processor took 52 and 109 us.  The issuing thread is chosen by elect.sync: chosen
 // by its lane it took 60 us where it took 51.
 #include "shared_common.cuh"
@@ -75,7 +80,7 @@ struct Shape {
 };
 // O leaves the accumulator, which cuts off its last place in every step, after as many tiles (96
 // steps for fp32 output, 512 for bf16).
-__host__ __device__ constexpr int flush_tiles(bool fp32) { return fp32 ? 8 : 128; }
+__host__ __device__ constexpr int flush_tiles(bool fp32) { return fp32 ? 8 : 64; }
 
 struct PrefixBars {
   uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
@@ -592,9 +597,9 @@ cudaError_t launch_prefix(const CUtensorMap& tk, const CUtensorMap& tv, const Sh
     return a.copies == 4   ? launch<4, 3>(tk, tv, a, st)
            : a.copies == 2 ? launch<2, 3>(tk, tv, a, st)
                            : launch<1, 3>(tk, tv, a, st);
-  return a.copies == 4   ? launch<4, 1>(tk, tv, a, st)
-         : a.copies == 2 ? launch<2, 1>(tk, tv, a, st)
-                         : launch<1, 1>(tk, tv, a, st);
+  return a.copies == 4   ? launch<4, 2>(tk, tv, a, st)
+         : a.copies == 2 ? launch<2, 2>(tk, tv, a, st)
+                         : launch<1, 2>(tk, tv, a, st);
 }
 
 }  // namespace bam
