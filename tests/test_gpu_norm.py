@@ -302,6 +302,14 @@ def test_norm_then_attention_trains_all_parameters():
         assert float(e) < GRAD_RTOL, float(e)
 
 
+@pytest.mark.parametrize("dims,pairs", [(0, False), (64, False), (32, True)])
+@pytest.mark.parametrize("B,H,Hkv,T", [(8, 32, 32, 512), (8, 64, 8, 512), (8, 48, 8, 512), (1, 64, 8, 1300),
+                                       (1, 40, 10, 2500), (1, 48, 4, 2500), (1, 70, 70, 2500)])
+def test_norm_of_many_heads_with_weights_of_their_own(B, H, Hkv, T, dims, pairs):
+    """So many tokens that a CTA takes 13 to 16 passes of heads, whose sums it holds all at once."""
+    _run(H + Hkv + dims, B, H, Hkv, T, dims, pairs, True, False)
+
+
 def test_norm_refusals():
     g = _gen(6)
     q, k = _normal(g, 2, 4, 8, 64), _normal(g, 2, 2, 8, 64)

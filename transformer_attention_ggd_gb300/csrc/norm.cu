@@ -415,16 +415,31 @@ void split_passes(NormArgs* a, int slots, int sms, int resident, int most_ctas) 
   a->ctas = static_cast<unsigned>(each) * a->parts;
 }
 
+constexpr int turn_of(const RopeArgs& r) { return r.dims == 0 ? kNoTurn : r.interleaved ? kPairs : kHalves; }
+
 typedef void (*Kernel)(NormArgs);
 template <class Off>
 constexpr Kernel fwd_kernel[] = {bam_qk_norm_fwd_kernel<kNoTurn, Off>,
                                  bam_qk_norm_fwd_kernel<kHalves, Off>, bam_qk_norm_fwd_kernel<kPairs, Off>};
+
+// The sums of the weights' gradients of 16 passes, and beside them the rings and angles, take 53 KB
+// of shared memory: more than a launch has without a limit of its own.
+template <int kTurn, class Off>
+cudaError_t launch_bwd(const NormArgs& a, cudaStream_t st) {
+  constexpr size_t kMost = static_cast<size_t>(kPass) * kNormMaxPasses * kHeadDim * 4;
+  static bool limit_set[64] = {};
+  const cudaError_t e = smem_limit_once(bam_qk_norm_bwd_kernel<kTurn, Off>, kMost, limit_set);
+  if (e != cudaSuccess) return e;
+  const size_t smem = static_cast<size_t>(kPass * (a.per_head ? a.passes : 2)) * kHeadDim * 4;
+  return launch_k(bam_qk_norm_bwd_kernel<kTurn, Off>, dim3(a.ctas), dim3(kThreads), smem, st, false, a);
+}
 template <class Off>
-constexpr Kernel bwd_kernel[] = {bam_qk_norm_bwd_kernel<kNoTurn, Off>,
-                                 bam_qk_norm_bwd_kernel<kHalves, Off>, bam_qk_norm_bwd_kernel<kPairs, Off>};
-Kernel pick_kernel(const NormArgs& a, const Kernel (&small)[3], const Kernel (&large)[3]) {
-  const int turn = a.rope.dims == 0 ? kNoTurn : a.rope.interleaved ? kPairs : kHalves;
-  return a.large ? large[turn] : small[turn];
+cudaError_t launch_bwd(const NormArgs& a, cudaStream_t st) {
+  switch (turn_of(a.rope)) {
+    case kHalves: return launch_bwd<kHalves, Off>(a, st);
+    case kPairs: return launch_bwd<kPairs, Off>(a, st);
+    default: return launch_bwd<kNoTurn, Off>(a, st);
+  }
 }
 
 }  // namespace
@@ -432,16 +447,15 @@ Kernel pick_kernel(const NormArgs& a, const Kernel (&small)[3], const Kernel (&l
 cudaError_t launch_norm_fwd(const NormArgs& args, cudaStream_t st) {
   NormArgs a = args;
   split_passes(&a, kFwdSlots, sm_count(), kFwdResident, 1 << 30);
-  return launch_k(pick_kernel(a, fwd_kernel<uint32_t>, fwd_kernel<uint64_t>), dim3(a.ctas),
+  const int turn = turn_of(a.rope);
+  return launch_k(a.large ? fwd_kernel<uint64_t>[turn] : fwd_kernel<uint32_t>[turn], dim3(a.ctas),
                   dim3(kThreads), 0, st, false, a);
 }
 
 void norm_bwd_config(NormArgs* a, int sms) { split_passes(a, kBwdSlots, sms, kBwdResident, kNormMaxCtas); }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t st) {
-  const size_t smem = static_cast<size_t>(kPass * (a.per_head ? a.passes : 2)) * kHeadDim * 4;
-  return launch_k(pick_kernel(a, bwd_kernel<uint32_t>, bwd_kernel<uint64_t>), dim3(a.ctas),
-                  dim3(kThreads), smem, st, false, a);
+  return a.large ? launch_bwd<uint64_t>(a, st) : launch_bwd<uint32_t>(a, st);
 }
 
 cudaError_t launch_norm_bwd_finish(const NormArgs& a, cudaStream_t st) {
