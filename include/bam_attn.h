@@ -264,7 +264,8 @@ size_t bam_attn_tree_workspace_size(int B, int H, int Hkv, int N, int Tmax, int 
  * behind the kept ones hold what is left of the draft.  1 <= N <= 128.  An
  * accepted node outside [-1, draft_lens[b]) counts as -1, and a sequence with
  * a page number out of range on its path keeps its pages as they were and its
- * length; both are reported.  One launch. */
+ * length; both are reported.  Caches with marks: bam_kv_keep_marks_paged.  One
+ * launch. */
 bam_status bam_kv_keep_paged(void* k_pages, void* v_pages, const int* block_table,
                              const int* cache_lens, const int* draft_lens, const int* parents,
                              const int* accepted, int* new_lens, int B, int Hkv, int N, int page,
@@ -329,8 +330,12 @@ size_t bam_qk_norm_workspace_size(int B, int H, int Hkv, int T, int D);
  * those of keys and values, under the same block table: the position of each
  * key and the attention weight that it has gathered so far.
  * bam_kv_append_norm_paged writes them, bam_attn_decode_shared_paged reads the
- * positions and adds to the weights, bam_kv_evict_paged keeps the keys of the
- * largest weights.
+ * positions and adds to the weights, bam_kv_keep_marks_paged and
+ * bam_kv_evict_paged move them with their keys, the latter keeps the keys of the
+ * largest weights.  No other operator knows them: bam_kv_keep_paged leaves the
+ * marks of a draft in its slots, and bam_attn_decode_paged and
+ * bam_attn_decode_tree_paged take slots as positions, which they are as long as
+ * no key has left and positions count up from 0.
  * ------------------------------------------------------------------------- */
 
 typedef struct {
@@ -424,6 +429,14 @@ bam_status bam_kv_evict_paged(void* k_pages, void* v_pages, const int* block_tab
                               int out_blocks, int num_pages, int D, int budget, int sink,
                               int recent, void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* bam_kv_keep_paged for a cache with marks: the positions and weights of the
+ * path's nodes move with their keys. */
+bam_status bam_kv_keep_marks_paged(void* k_pages, void* v_pages, const int* block_table,
+                                   const int* cache_lens, const int* draft_lens, const int* parents,
+                                   const int* accepted, int* new_lens, const bam_marks* marks, int B,
+                                   int Hkv, int N, int page, int max_blocks, int num_pages, int D,
+                                   void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* Bytes of workspace of bam_kv_evict_paged (Tmax = max_blocks * page).  Returns
  * 0 for invalid sizes.  Host-only. */
 size_t bam_kv_evict_workspace_size(int B, int Hkv, int Tmax, int budget);
@@ -444,7 +457,8 @@ enum {
   BAM_CALL_QK_NORM_FWD = 4,
   BAM_CALL_QK_NORM_BWD = 5,
   BAM_CALL_DECODE_SHARED = 6,
-  BAM_CALL_KV_EVICT = 7
+  BAM_CALL_KV_EVICT = 7,
+  BAM_CALL_KV_KEEP_MARKS = 8
 };
 bam_status bam_paged_call(int op, const void* words);
 

@@ -251,3 +251,28 @@ def test_reference_of_kept_slots():
     assert kept_slots(w, 7, 0, 1).tolist() == [0, 1, 2, 3, 6, 8, 9]
     assert kept_slots(w, 8, 0, 1).tolist() == [0, 1, 2, 3, 4, 6, 8, 9]
     assert kept_slots(w, 4, 2, 2).tolist() == [0, 1, 8, 9]
+
+
+KEEP = dict(kp=FAKE, vp=FAKE, bt=FAKE, lens=FAKE, draft=FAKE, par=FAKE, acc=FAKE, new=FAKE, marks=MARKS, B=2, Hkv=2,
+            N=8, page=64, mb=4, pages=8, D=64, ws=FAKE, ws_bytes=1 << 30, stream=0)
+
+
+@pytest.mark.parametrize("kw,want", CACHED + [
+    (dict(N=129), "UNSUPPORTED"), (dict(N=0), "INVALID_ARG"), (dict(acc=0), "INVALID_ARG"),
+    (dict(new=FAKE + 2), "INVALID_ARG"), (dict(marks=0), "INVALID_ARG"),
+    (dict(N=1 << 32), "INVALID_ARG")])
+def test_refusals_of_the_keep_with_marks(lib, kw, want):
+    args = {**KEEP, **kw}
+    assert len(args) == 19
+    words = [_addr(x) for x in args.values()]
+    assert lib.bam_paged_call(8, struct.pack("19q", *words)) == getattr(ba, "BAM_ERR_" + want)
+
+
+def test_binding_refuses_marks_on_the_host():
+    pages = torch.zeros(4, 2, 64, 64, dtype=torch.bfloat16)
+    i, table = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 2, dtype=torch.int32)
+    marks = ba.make_marks(torch.zeros(4, 2, 64, dtype=torch.int32), torch.zeros(4, 2, 64), 10)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        ba.bam_kv_keep_paged(pages, pages, table, i, i, None, i, i, torch.zeros(256, dtype=torch.uint8), marks=marks)
+    with pytest.raises(TypeError, match="BamMarks"):
+        ba._struct_address(object(), ba.BamMarks)

@@ -99,6 +99,7 @@ EXPORTED = (
     "bam_attn_shared_workspace_size",
     "bam_kv_evict_paged",
     "bam_kv_evict_workspace_size",
+    "bam_kv_keep_marks_paged",
 )
 
 # Size of the fixed device scratch of bam_attn_decode_noalloc.
@@ -237,6 +238,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.bam_attn_shared_workspace_size.argtypes = [i] * 7
         lib.bam_kv_evict_paged.restype = i
         lib.bam_kv_evict_paged.argtypes = [vp] * 4 + [mp, vp, vp] + [i] * 10 + [vp, sz, vp]
+        lib.bam_kv_keep_marks_paged.restype = i
+        lib.bam_kv_keep_marks_paged.argtypes = [vp] * 8 + [mp] + [i] * 7 + [vp, sz, vp]
         lib.bam_kv_evict_workspace_size.restype = sz
         lib.bam_kv_evict_workspace_size.argtypes = [i] * 4
         lib.bam_paged_call.restype = i
@@ -612,6 +615,7 @@ def _struct_address(x, kind):
 _append_words = struct.Struct("32q").pack
 _tree_words = struct.Struct("22q").pack
 _keep_words = struct.Struct("18q").pack
+_keep_marks_words = struct.Struct("19q").pack
 
 
 def _all_ok(index, pool, k_pages, v_pages, table, block_table, cache_lens, draft_lens, parents, ws,
@@ -768,9 +772,10 @@ def bam_attn_decode_tree_paged(q, k_pages, v_pages, block_table, cache_lens, dra
 
 
 def bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, parents, accepted,
-                      new_lens, ws, stream=None, check=True) -> None:
+                      new_lens, ws, stream=None, check=True, marks=None) -> None:
     """Keep the path from the root to node accepted[b] (int32 [B], -1: none)
-    of each draft; new_lens int32 [B] (may be cache_lens) gets the lengths."""
+    of each draft; new_lens int32 [B] (may be cache_lens) gets the lengths.
+    marks: make_marks(...) of a cache that has them; they move with their keys."""
     if torch is None:
         _use_torch()
     num_pages, Hkv, page, D = pool = k_pages.shape
@@ -783,6 +788,7 @@ def bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, par
     if check:
         try:
             ok = (index >= 0 and index == _current_device()
+                  and (marks is None or _marks_fit(marks, index, pool))
                   and _all_ok(index, pool, k_pages, v_pages, table, block_table, cache_lens,
                               draft_lens, parents, ws, B, N,
                               ((accepted, torch.int32, (B,)), (new_lens, torch.int32, (B,)))))
@@ -795,13 +801,16 @@ def bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, par
                                         parents, B, N)
                            + (("accepted", accepted, (B,), i32, False),
                               ("new_lens", new_lens, (B,), i32, False)), dev)
+            _check_norm_marks(None, marks, dev.index, Hkv, Hkv, pool)
             _check_ws(ws, dev)
             raise ValueError("argument check failed")
-    st = load_library().bam_paged_call(2, _keep_words(
-        k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(),
-        _address(draft_lens), _address(parents), accepted.data_ptr(), new_lens.data_ptr(), B, Hkv,
-        N, page, table[1], num_pages, D, ws.data_ptr(), ws.numel(),
-        _raw_stream(stream, index)))
+    head = (k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(),
+            _address(draft_lens), _address(parents), accepted.data_ptr(), new_lens.data_ptr())
+    tail = (B, Hkv, N, page, table[1], num_pages, D, ws.data_ptr(), ws.numel(), _raw_stream(stream, index))
+    if marks is None:
+        st = load_library().bam_paged_call(2, _keep_words(*head, *tail))
+    else:
+        st = load_library().bam_paged_call(8, _keep_marks_words(*head, _struct_address(marks, BamMarks), *tail))
     if st:
         _check(st, "bam_kv_keep_paged")
 
@@ -1388,10 +1397,10 @@ def attention_decode_tree_paged(q, k_pages, v_pages, block_table, cache_lens, al
 
 
 def kv_keep_paged(k_pages, v_pages, block_table, cache_lens, accepted, parents, draft_lens=None,
-                  new_lens=None, ws=None, stream=None):
+                  new_lens=None, ws=None, stream=None, marks=None):
     """Keep the accepted path of each draft; returns the new lengths (written
-    to new_lens, which may be cache_lens, if given).  Without ws, paths that
-    could not be kept go unreported."""
+    to new_lens, which may be cache_lens, if given).  marks: of a cache that has
+    them.  Without ws, paths that could not be kept go unreported."""
     import torch
     with _on(stream):
         if new_lens is None:
@@ -1399,7 +1408,7 @@ def kv_keep_paged(k_pages, v_pages, block_table, cache_lens, accepted, parents, 
         if ws is None:
             ws = cache_workspace(k_pages.device)
     bam_kv_keep_paged(k_pages, v_pages, block_table, cache_lens, draft_lens, parents, accepted,
-                      new_lens, ws, stream)
+                      new_lens, ws, stream, marks=marks)
     return new_lens
 
 

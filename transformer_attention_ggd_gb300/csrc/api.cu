@@ -495,6 +495,34 @@ bam_status append_impl(const void* k, const void* v, const void* q, void* q_out,
       launch_kernel(BAM_KERNEL_KV_APPEND, stream, [&] { return launch_append(a, stream); }));
 }
 
+// bam_kv_keep_paged, and with `marks` bam_kv_keep_marks_paged.
+bam_status keep_impl(void* k_pages, void* v_pages, const int* block_table, const int* cache_lens,
+                     const int* draft_lens, const int* parents, const int* accepted, int* new_lens,
+                     const bam_marks* marks, int B, int Hkv, int N, int page, int max_blocks, int num_pages,
+                     int D, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  bam_status s = check_cache(B, Hkv, Hkv, N, page, max_blocks, num_pages, D, block_table,
+                             cache_lens, draft_lens, parents);
+  if (s != BAM_OK) return s;
+  if (N > kTreeMax) return BAM_ERR_UNSUPPORTED;
+  if (!k_pages || !v_pages || !accepted || !new_lens || !aligned(k_pages, 16) ||
+      !aligned(v_pages, 16) || !aligned(accepted, 4) || !aligned(new_lens, 4))
+    return BAM_ERR_INVALID_ARG;
+  if ((s = check_ws(ws, ws_bytes, BAM_CACHE_WORKSPACE_BYTES)) != BAM_OK) return s;
+  KeepArgs a = {};
+  a.c = CacheArgs{block_table, cache_lens, draft_lens, parents, static_cast<DevStatus*>(ws),
+                  B, Hkv, N, page, max_blocks, num_pages};
+  a.k_pages = static_cast<uint16_t*>(k_pages);
+  a.v_pages = static_cast<uint16_t*>(v_pages);
+  a.accepted = accepted;
+  a.new_lens = new_lens;
+  if (marks) {
+    a.key_pos = marks->key_pos;
+    a.key_weight = marks->key_weight;
+  }
+  return cuda_status(
+      launch_kernel(BAM_KERNEL_KV_KEEP, stream, [&] { return launch_keep(a, stream); }));
+}
+
 }  // namespace
 
 // For bam_attn_decode_noalloc (decode_noalloc.cu): the argument checks, the
@@ -936,28 +964,24 @@ bam_status bam_kv_keep_paged(void* k_pages, void* v_pages, const int* block_tabl
                              const int* accepted, int* new_lens, int B, int Hkv, int N, int page,
                              int max_blocks, int num_pages, int D, void* ws, size_t ws_bytes,
                              cudaStream_t stream) {
-  bam_status s = check_cache(B, Hkv, Hkv, N, page, max_blocks, num_pages, D, block_table,
-                             cache_lens, draft_lens, parents);
-  if (s != BAM_OK) return s;
-  if (N > kTreeMax) return BAM_ERR_UNSUPPORTED;
-  if (!k_pages || !v_pages || !accepted || !new_lens || !aligned(k_pages, 16) ||
-      !aligned(v_pages, 16) || !aligned(accepted, 4) || !aligned(new_lens, 4))
-    return BAM_ERR_INVALID_ARG;
-  if ((s = check_ws(ws, ws_bytes, BAM_CACHE_WORKSPACE_BYTES)) != BAM_OK) return s;
-  KeepArgs a;
-  a.c = CacheArgs{block_table, cache_lens, draft_lens, parents, static_cast<DevStatus*>(ws),
-                  B, Hkv, N, page, max_blocks, num_pages};
-  a.k_pages = static_cast<uint16_t*>(k_pages);
-  a.v_pages = static_cast<uint16_t*>(v_pages);
-  a.accepted = accepted;
-  a.new_lens = new_lens;
-  return cuda_status(
-      launch_kernel(BAM_KERNEL_KV_KEEP, stream, [&] { return launch_keep(a, stream); }));
+  return keep_impl(k_pages, v_pages, block_table, cache_lens, draft_lens, parents, accepted, new_lens, nullptr,
+                   B, Hkv, N, page, max_blocks, num_pages, D, ws, ws_bytes, stream);
+}
+
+bam_status bam_kv_keep_marks_paged(void* k_pages, void* v_pages, const int* block_table,
+                                   const int* cache_lens, const int* draft_lens, const int* parents,
+                                   const int* accepted, int* new_lens, const bam_marks* marks, int B,
+                                   int Hkv, int N, int page, int max_blocks, int num_pages, int D,
+                                   void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!marks_ok(marks)) return BAM_ERR_INVALID_ARG;
+  return keep_impl(k_pages, v_pages, block_table, cache_lens, draft_lens, parents, accepted, new_lens, marks,
+                   B, Hkv, N, page, max_blocks, num_pages, D, ws, ws_bytes, stream);
 }
 
 static bam_status bounded_call(int op, const void* words) {
   // Words of each operator, the place of its strides' flag (-1: none) and their number.
-  constexpr int kWords[] = {26, 14, 20, 25, 20}, kFlag[] = {4, 4, 6, -1, -1}, kSteps[] = {9, 12, 18, 0, 0};
+  constexpr int kWords[] = {26, 14, 20, 25, 20, 19}, kFlag[] = {4, 4, 6, -1, -1, -1},
+                kSteps[] = {9, 12, 18, 0, 0, 0};
   const int x = op - BAM_CALL_KV_APPEND_NORM, flag = kFlag[x];
   int64_t w[26], steps[18];
   std::memcpy(w, words, kWords[x] * sizeof(int64_t));
@@ -983,7 +1007,7 @@ static bam_status bounded_call(int op, const void* words) {
   auto marks = [&](int i) { return static_cast<const bam_marks*>(p(i)); };
   auto st = [&](int i) { return static_cast<cudaStream_t>(p(i)); };
   auto sz = [&](int i) { return static_cast<size_t>(w[i]); };
-  constexpr int kFirst[] = {11, 6, 10, 13, 7}, kInts[] = {8, 5, 5, 8, 10};
+  constexpr int kFirst[] = {11, 6, 10, 13, 7, 9}, kInts[] = {8, 5, 5, 8, 10, 7};
   int i[10];
   for (int y = 0; y < kInts[x]; ++y) i[y] = n(kFirst[x] + y);
   const int o_fp32 = op == BAM_CALL_DECODE_SHARED ? n(11) : 0;
@@ -1009,6 +1033,9 @@ static bam_status bounded_call(int op, const void* words) {
                                           decay, p(10), o_fp32, fp(12), i[0], i[1], i[2], i[3], i[4],
                                           i[5], i[6], i[7], static_cast<const bam_params*>(p(21)), p(22),
                                           sz(23), st(24));
+    case BAM_CALL_KV_KEEP_MARKS:
+      return bam_kv_keep_marks_paged(p(0), p(1), ip(2), ip(3), ip(4), ip(5), ip(6), ip(7), marks(8), i[0], i[1],
+                                     i[2], i[3], i[4], i[5], i[6], p(16), sz(17), st(18));
     default:
       return bam_kv_evict_paged(p(0), p(1), ip(2), ip(3), marks(4), ip(5), ip(6), i[0], i[1], i[2], i[3],
                                 i[4], i[5], i[6], i[7], i[8], i[9], p(17), sz(18), st(19));
@@ -1017,7 +1044,7 @@ static bam_status bounded_call(int op, const void* words) {
 
 bam_status bam_paged_call(int op, const void* words) {
   constexpr int kWords[] = {23, 22, 18}, kStrides = 4;  // place of the append's strides
-  if (words && op > BAM_CALL_KV_KEEP && op <= BAM_CALL_KV_EVICT) return bounded_call(op, words);
+  if (words && op > BAM_CALL_KV_KEEP && op <= BAM_CALL_KV_KEEP_MARKS) return bounded_call(op, words);
   if (!words || op < BAM_CALL_KV_APPEND || op > BAM_CALL_KV_KEEP) return BAM_ERR_INVALID_ARG;
   int64_t w[23], strides[9];
   std::memcpy(w, words, kWords[op] * sizeof(int64_t));

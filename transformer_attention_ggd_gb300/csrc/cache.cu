@@ -424,7 +424,8 @@ __global__ void __launch_bounds__(kRunThreads, kRunResident) bam_kv_append_run_k
 constexpr int kKeepThreads = 256;
 constexpr int kKeepBatch = 16;  // rows that a warp holds in registers
 
-// One cluster per sequence; a warp takes one head of K or of V at a time.
+// One cluster per sequence; a warp takes one head of K or of V at a time, with marks the positions with
+// K and the weights with V.
 // Node m of the path moves from slot a_m to slot m <= a_m.  A slot that is
 // written may be an earlier node's source but never a later one's
 // (a_m' >= m' > m), so a warp that reads a batch of rows before it writes
@@ -480,21 +481,28 @@ __global__ void __launch_bounds__(kKeepThreads) bam_kv_keep_kernel(const KeepArg
     for (int hv = blockIdx.x * (kKeepThreads / 32) + (threadIdx.x >> 5); hv < 2 * c.Hkv;
          hv += warps) {
       uint16_t* pool = hv < c.Hkv ? a.k_pages : a.v_pages;
+      uint32_t* side = reinterpret_cast<uint32_t*>(hv < c.Hkv ? static_cast<void*>(a.key_pos) : a.key_weight);
       const int64_t head = static_cast<int64_t>(hv < c.Hkv ? hv : hv - c.Hkv) * c.page;
+      const bool marks = side && (lane & 7) == 0;
       for (int m0 = 0; m0 < m; m0 += kKeepBatch) {
         uint4 w[kKeepBatch / 4];
+        uint32_t mark[kKeepBatch / 4];
 #pragma unroll
         for (int x = 0; x < kKeepBatch / 4; ++x) {
           const int i = m0 + 4 * x + (lane >> 3);
-          if (i < m)
+          if (i < m) {
             w[x] = reinterpret_cast<const uint4*>(pool + (src_row[i] + head) * kHeadDim)[lane & 7];
+            if (marks) mark[x] = side[src_row[i] + head];
+          }
         }
         __syncwarp();
 #pragma unroll
         for (int x = 0; x < kKeepBatch / 4; ++x) {
           const int i = m0 + 4 * x + (lane >> 3);
-          if (i < m && src_row[i] != dst_row[i])
+          if (i < m && src_row[i] != dst_row[i]) {
             reinterpret_cast<uint4*>(pool + (dst_row[i] + head) * kHeadDim)[lane & 7] = w[x];
+            if (marks) side[dst_row[i] + head] = mark[x];
+          }
         }
         __syncwarp();
       }

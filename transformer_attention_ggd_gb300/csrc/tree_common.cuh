@@ -50,6 +50,8 @@ struct KeepArgs {
   uint16_t* v_pages;
   const int* accepted;
   int* new_lens;
+  int* key_pos;       // [num_pages, Hkv, page] or null: no marks
+  float* key_weight;
 };
 
 // Tree attention: the rows of a (sequence, key head) are its group * n
