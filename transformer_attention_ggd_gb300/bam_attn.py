@@ -863,14 +863,15 @@ _float_bits = functools.lru_cache(64)(lambda x: struct.unpack("<i", struct.pack(
 
 
 def _norm_fits(norm, index, H, Hkv):
-    """A norm's weights lie on CUDA device `index` and fit the heads (a struct built
-    by hand from raw pointers: the caller vouches for them)."""
+    """A norm's weights lie on CUDA device `index` and fit the heads (H None: no
+    queries, whose weights may be any; a struct built by hand from raw pointers: the
+    caller vouches for them)."""
     tensors = getattr(norm, "tensors", None)
     if tensors is None:
         return True
     q, k = tensors
     return (q.get_device() == index and k.get_device() == index
-            and (q.dim() == 1 or (q.shape[0] == H and k.shape[0] == Hkv)))
+            and (q.dim() == 1 or ((H is None or q.shape[0] == H) and k.shape[0] == Hkv)))
 
 
 def _marks_fit(marks, index, pool):
@@ -881,7 +882,8 @@ def _marks_fit(marks, index, pool):
 
 def _check_norm_marks(norm, marks, index, H, Hkv, pool):
     if norm is not None and not _norm_fits(norm, index, H, Hkv):
-        raise ValueError(f"the norm's weights must be on cuda:{index}, [64] or [{H}, 64] and [{Hkv}, 64]")
+        heads = "any number" if H is None else H
+        raise ValueError(f"the norm's weights must be on cuda:{index}, [64] or [{heads}, 64] and [{Hkv}, 64]")
     if marks is not None and not _marks_fit(marks, index, pool):
         raise ValueError(f"the marks must be on cuda:{index}, shaped {tuple(pool[:3])}")
 
@@ -1007,7 +1009,7 @@ def bam_kv_append_norm_paged(k, v, k_pages, v_pages, block_table, cache_lens, ne
                     _no_rows if q is None else _row_words(index, (B, H, N, 64), q))
             ok = (index >= 0 and index == _current_device() and D == 64 and pool_heads == Hkv
                   and None not in rows and (q is None) == (q_out is None)
-                  and (norm is None or _norm_fits(norm, index, H, Hkv))
+                  and (norm is None or _norm_fits(norm, index, None if q is None else H, Hkv))
                   and (marks is None or _marks_fit(marks, index, pool))
                   and _all_ok(index, pool, k_pages, v_pages, table, block_table, cache_lens,
                               new_lens, parents, ws, B, N, specs))
@@ -1026,7 +1028,7 @@ def bam_kv_append_norm_paged(k, v, k_pages, v_pages, block_table, cache_lens, ne
                                         parents, B, N)
                            + (("q_out", q_out, (B, H, N, 64), bf, True),
                               ("first_pos", first_pos, (B,), i32, True)), dev)
-            _check_norm_marks(norm, marks, dev.index, H, Hkv, pool)
+            _check_norm_marks(norm, marks, dev.index, None if q is None else H, Hkv, pool)
             _check_ws(ws, dev)
             raise ValueError("argument check failed")
     kw, vw, qw = rows or [_no_rows if t is None else _unchecked_words(t) for t in (k, v, q)]
