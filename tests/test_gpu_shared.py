@@ -572,3 +572,20 @@ def test_serving_with_a_bounded_cache():
     assert evictions >= 2
     for ws in (cws, sws, ews):
         assert ba.bam_attn_check_status(ws) == ba.BAM_OK
+
+
+def test_shared_decay_is_read_at_each_call():
+    """A number of any kind, of a tensor too, that changed between two calls."""
+    c = Cache(33, 2, 64, [70, 5], 0)
+    t = [dev_f32(x) for x in ([5.0] * 4, [1.0] * 4, [0.0] * 4, [1.0] * 4)]
+    q, lens, w0 = _normal(c.gen, 2, 4, 64), _i32([70, 5]), c.w.clone()
+    marks, box = ba.make_marks(c.pos, c.w, c.max_pos), torch.tensor(1.0)
+
+    def step(decay):
+        c.w.copy_(w0)
+        ba.attention_decode_shared_paged(q, c.k, c.v, c.table, lens, *t, q_pos=c.q_pos, marks=marks, decay=decay)
+        return c.w.view(torch.int32).clone()
+
+    for value in (1.0, 0.25, 0.0):
+        box.fill_(value)
+        assert torch.equal(step(box), step(value))

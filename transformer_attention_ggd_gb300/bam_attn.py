@@ -859,6 +859,7 @@ _norm_fwd_words = struct.Struct("26q").pack
 _norm_bwd_words = struct.Struct("38q").pack
 _shared_words = struct.Struct("25q").pack
 _evict_words = struct.Struct("20q").pack
+# (of a Python number alone: one that can change in place would be remembered by its identity)
 _float_bits = functools.lru_cache(64)(lambda x: struct.unpack("<i", struct.pack("<f", x))[0])
 
 
@@ -1102,7 +1103,7 @@ def bam_attn_decode_shared_paged(q, k_pages, v_pages, block_table, cache_lens, p
     st = load_library().bam_paged_call(6, _shared_words(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
         cache_lens.data_ptr(), _address(prefix_table), _address(prefix_len), _address(q_pos),
-        _struct_address(marks, BamMarks), _float_bits(decay), o.data_ptr(),
+        _struct_address(marks, BamMarks), _float_bits(float(decay)), o.data_ptr(),
         1 if out is torch.float32 else 0, _address(lse), B, H, Hkv, page, table[1], blocks, num_pages,
         D, _struct_address(params, BamParams), ws.data_ptr(), ws.numel(),
         _raw_stream(stream, index)))
