@@ -589,3 +589,29 @@ def test_shared_decay_is_read_at_each_call():
     for value in (1.0, 0.25, 0.0):
         box.fill_(value)
         assert torch.equal(step(box), step(value))
+
+
+def test_shared_weights_of_far_keys_add_up():
+    """Far from every key the logits are large (10^6, and the least that a bias may be):
+    what a step adds to a sequence's weights is 1 for each query head all the same.  A
+    weight and the sum that divides it have the same logits, so that only the
+    exponentials' 2^-22 each and the sums of n terms count."""
+    lens, H, Hkv = [70, 300, 1], 4, 2
+    for P in (0, 40):
+        c = Cache(31 + P, Hkv, 64, lens, P)
+        c.q_pos += 1000000
+        c.max_pos += 1000000
+        c.k[c.table.long().clamp(min=0)] = 0
+        prm = [dev_f32(x) for x in ([1.0] * H, [1.0, 1.0, 40.0, 40.0], [0.0] * H, [1.0] * H)]
+        marks = ba.make_marks(c.pos, c.w, c.max_pos)
+        for decay, old in ((0.0, 0.0), (1.0, 1.0)):
+            w0 = c.w.clone()
+            ba.attention_decode_shared_paged(_normal(c.gen, 3, H, 64), c.k, c.v, c.table, _i32(lens), *prm,
+                                             q_pos=c.q_pos, marks=marks, decay=decay)
+            for b, n in enumerate(lens):
+                s = torch.arange(n, device="cuda")
+                pg, row = c.table[b].long()[s // 64], s % 64
+                got, was = c.w[pg, :, row].double(), w0[pg, :, row].double()
+                added = got.sum(0) - old * was.sum(0)
+                bound = 2 * (n * 2.0 ** -24 + 2.0 ** -20) + 2.0 ** -24 * got.sum(0)
+                assert torch.all((added - H // Hkv).abs() <= bound), (decay, b, added.tolist())

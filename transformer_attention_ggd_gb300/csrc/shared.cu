@@ -9,7 +9,7 @@
 // which stay in L2).  The first kernel starts the call and fills the prefix's table of biases;
 // the prefix goes in tiles (prefix.cu) where nine or more rows share it; the main kernel takes
 // what is left on mma.sync, whose 16 rows the heads of a group fill as far as they do; the
-// last one joins the parts of a row and, in blocks of its own, adds to the weights, which need every lse:
+// last one joins the parts of a row and, in blocks of its own, adds to the weights, which need every row's sum:
 // each takes it from the parts (two kernels in turn took 2.5 us longer in small calls).
 //
 // Positions of kept keys are any numbers, so that the own keys' biases are evaluated where they
@@ -591,13 +591,15 @@ __device__ __forceinline__ void join_rows(const SharedArgs& a, int64_t block) {
 
 constexpr int kWeighFours = 2;  // of a thread
 constexpr int weigh_keys_of(int warps) { return 4 * kWeighFours * 32 * warps; }
-constexpr int kWeighRows = 64;  // whose lse is at hand at a time
+constexpr int kWeighRows = 64;  // whose sums are at hand at a time
 
-// w_j <- decay w_j + sum over the heads of the group of exp(z_j - lse), for a run of a sequence's keys.
+// w_j <- decay w_j + sum over the heads of the group of exp(z_j - lse), for a run of a sequence's keys.  A
+// row's maximum and sum stay apart: z less the maximum is as exact as z, while maximum + log2(sum) is a
+// number of the logits' size, whose last place may be more than log2(sum) (far from every key).
 template <int kEndWarps>
 __device__ __forceinline__ void weigh_keys(const SharedArgs& a, unsigned block) {
   constexpr int kEndThreads = 32 * kEndWarps, kWeighKeys = 4 * kWeighFours * kEndThreads;
-  __shared__ float lse[kWeighRows];
+  __shared__ float2 row_ml[kWeighRows];  // maximum, 1 / sum
   const int hk = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
   bool ok = true;
   const int len = own_len(a, b, &ok);
@@ -646,17 +648,18 @@ __device__ __forceinline__ void weigh_keys(const SharedArgs& a, unsigned block) 
       }
 #pragma unroll
       for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
-      if (lane == 0) lse[g] = M + __log2f(L);
+      if (lane == 0) row_ml[g] = make_float2(M, 1.0f / L);
     }
     __syncthreads();
     for (int g = 0; g < rows; ++g) {
+      const float2 ml = row_ml[g];
 #pragma unroll
       for (int x = 0; x < kWeighFours; ++x) {
         if (!at[x]) continue;
-        w[x][0] += ex2_approx(z[x].x - lse[g]);
-        w[x][1] += ex2_approx(z[x].y - lse[g]);
-        w[x][2] += ex2_approx(z[x].z - lse[g]);
-        w[x][3] += ex2_approx(z[x].w - lse[g]);
+        w[x][0] = fmaf(ex2_approx(z[x].x - ml.x), ml.y, w[x][0]);
+        w[x][1] = fmaf(ex2_approx(z[x].y - ml.x), ml.y, w[x][1]);
+        w[x][2] = fmaf(ex2_approx(z[x].z - ml.x), ml.y, w[x][2]);
+        w[x][3] = fmaf(ex2_approx(z[x].w - ml.x), ml.y, w[x][3]);
       }
       if (g0 + g + 1 < a.group) load(g0 + g + 1);
     }
