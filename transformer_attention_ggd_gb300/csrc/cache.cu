@@ -539,8 +539,17 @@ cudaError_t launch_append(const AppendArgs& args, cudaStream_t st) {
   if (a.extended) {
     const int turned = a.rope.dims == 0 ? kNoTurn : a.rope.interleaved ? kPairs : kHalves;
     const int64_t run_tiles = static_cast<int64_t>(a.c.B) * ((a.c.N + kRunTokens - 1) / kRunTokens);
-    // (2 prompts of 2000 tokens, 12 heads: 10.6 us in runs, 11.5 in units; 32 of 64 tokens 8.6 and 7.7)
-    if (tiles > run / 2 && !a.c.parents && run_tiles <= 0x7FFFFFFF) {
+    // In runs or in units, by what either takes in ns beyond a launch: a unit 5.7 and a row of it 1 / 30; a
+    // run's tile its passes one after the other, 600 each, and 1.36 a pass once two tiles an SM are under way.
+    // Measured in runs and units, us: one token each of 153, 1024 and 4096 sequences, 12 heads: 8.3 and 5.9,
+    // 16.8 and 21.3, 50 and 74; 64 and 16 heads: 18.4 and 6.2, 40 and 21, 133 and 81; 8 tokens, 64 and 16
+    // heads: 18.5 and 11.1, 44 and 48, 133 and 172; 2 prompts of 2000 tokens, 12 heads: 10.6 and 11.5.
+    const int64_t passes = (a.H + kRunWarps - 1) / kRunWarps + 2 * ((a.c.Hkv + kRunWarps - 1) / kRunWarps);
+    const int64_t rows = static_cast<int64_t>(a.c.B) * a.c.N * (a.H + 2 * a.c.Hkv);
+    const int64_t many = run_tiles - 2 * static_cast<int64_t>(sm_count());
+    const double in_units = 600.0 + 5.7 * units + rows / 30.0;
+    const double in_runs = passes * (600.0 + 1.36 * (many > 0 ? many : 0));
+    if (in_runs < in_units && !a.c.parents && run_tiles <= 0x7FFFFFFF) {
       constexpr Kernel runs[] = {bam_kv_append_run_kernel<kNoTurn>, bam_kv_append_run_kernel<kHalves>,
                                  bam_kv_append_run_kernel<kPairs>};
       int64_t ctas = static_cast<int64_t>(sm_count()) * kRunResident;
