@@ -123,9 +123,10 @@ __device__ __forceinline__ void append_turn(const AppendArgs& a, const AppendUni
 //
 // kNorm: queries and keys are normalised on the way (4 lanes sum a row's
 // squares), positions may start anywhere, and the keys' positions and weights
-// are written beside them.
+// are written beside them; it has one unit a CTA (long calls: the kernel below).
 template <bool kRun, bool kNorm, int kTurn>
 __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_kernel(const AppendArgs a) {
+  static_assert(!(kRun && kNorm), "positions of one unit's sequence alone");
   __shared__ float4 cs[kAppendTokens][kHeadDim / 4];  // two (cosine, sine) pairs each
   __shared__ int64_t slot_row[kAppendTokens];  // row of head 0 in the pages, -1: not written
   __shared__ int depth[kTreeMax], jump[kTreeMax];
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
   for (;;) {
     // The unit after this one.
     AppendUnit xn = x;
-    int len_n = len, n_n = n, first_n = first;
+    int len_n = len, n_n = n;
     bool more = false;
     if (kRun) {
       if (++part == split) {
@@ -177,11 +178,7 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
       more = bt < tiles;
       if (more) {
         xn = append_unit(a, bt, part);
-        if (xn.b != x.b) {
-          ok &= append_lengths(c, xn.b, len_n, n_n);
-          first_n = len_n;
-          if (kNorm) ok &= append_first(a, xn.b, len_n, first_n);
-        }
+        if (xn.b != x.b) ok &= append_lengths(c, xn.b, len_n, n_n);
         append_load(a, xn, n_n, ln, wn);
       }
     }
@@ -254,7 +251,7 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
           float f0[8], f1[8];
           unpack8(w[y][0], f0);
           unpack8(w[y][1], f1);
-          turn_row(f0, f1, r, a.rope.interleaved, 1.0f);
+          turn_row(f0, f1, r, a.rope.interleaved);
           w[y][0] = pack8(f0);
           w[y][1] = pack8(f1);
         }
@@ -270,7 +267,6 @@ __global__ void __launch_bounds__(kAppendThreads, kRun ? 2 : 3) bam_kv_append_ke
     x = xn;
     len = len_n;
     n = n_n;
-    first = first_n;
 #pragma unroll
     for (int y = 0; y < kAppendRows; ++y) {
       w[y][0] = wn[y][0];

@@ -47,24 +47,23 @@ __device__ __forceinline__ float2 rope_angle(uint64_t pos, uint64_t freq) {
   return make_float2(co, s);
 }
 
-// Turns a lane's 16 values (two chunks of 8) by the angles of its eight pairs;
-// `sign` -1 turns back.  r: the pairs' (cosine, sine), two in each float4.
+// Turns a lane's 16 values (two chunks of 8) by the angles of its eight pairs, r: their
+// (cosine, sine), two in each float4.
 // Interleaved pairs lie inside a chunk, the others across the two.
-__device__ __forceinline__ void turn_row(float* f0, float* f1, const float4* r, bool interleaved,
-                                         float sign) {
+__device__ __forceinline__ void turn_row(float* f0, float* f1, const float4* r, bool interleaved) {
   if (interleaved) {
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
-      turn(f0[4 * z], f0[4 * z + 1], r[z].x, sign * r[z].y);
-      turn(f0[4 * z + 2], f0[4 * z + 3], r[z].z, sign * r[z].w);
-      turn(f1[4 * z], f1[4 * z + 1], r[2 + z].x, sign * r[2 + z].y);
-      turn(f1[4 * z + 2], f1[4 * z + 3], r[2 + z].z, sign * r[2 + z].w);
+      turn(f0[4 * z], f0[4 * z + 1], r[z].x, r[z].y);
+      turn(f0[4 * z + 2], f0[4 * z + 3], r[z].z, r[z].w);
+      turn(f1[4 * z], f1[4 * z + 1], r[2 + z].x, r[2 + z].y);
+      turn(f1[4 * z + 2], f1[4 * z + 3], r[2 + z].z, r[2 + z].w);
     }
   } else {
 #pragma unroll
     for (int z = 0; z < 4; ++z) {
-      turn(f0[2 * z], f1[2 * z], r[z].x, sign * r[z].y);
-      turn(f0[2 * z + 1], f1[2 * z + 1], r[z].z, sign * r[z].w);
+      turn(f0[2 * z], f1[2 * z], r[z].x, r[z].y);
+      turn(f0[2 * z + 1], f1[2 * z + 1], r[z].z, r[z].w);
     }
   }
 }
