@@ -236,3 +236,39 @@ def test_evict_refusals():
         ba.make_marks(c.pos, c.w, 0)
     with pytest.raises(ValueError):
         ba.make_marks(c.pos, c.w.double(), 10)
+
+
+@pytest.mark.parametrize("bad", ["page", "out", "long", "negative"])
+def test_evict_goes_on_beside_a_bad_sequence(bad):
+    """The good sequence's keys are evicted as if it stood alone, and one whose length is
+    too long as if it filled its table."""
+    lens, budget, page, sink, recent = [200, 300], 100, 64, 4, 20
+    c = Cache(8, 2, page, lens, random_weights, spare=4)
+    before = c.host()
+    table, ln, out = c.table.copy(), list(lens), None
+    if bad == "page":
+        table[1, 2] = c.k.shape[0]
+    elif bad == "out":
+        out = np.stack([c.spare[:2], [c.spare[2], -3]])
+    elif bad == "long":
+        ln[1] = table.shape[1] * page + 7
+    else:
+        ln[1] = -1
+    new = ba.kv_evict_paged(c.k, c.v, _i32(table), _i32(ln), ba.make_marks(c.pos, c.w, 1 << 20), budget, sink, recent,
+                            None if out is None else _i32(out))
+    after, w = c.host(), before[3].view(torch.float32).numpy()
+    assert new[0] == budget
+    for b, n in [(0, 200)] + ([(1, table.shape[1] * page)] if bad == "long" else []):
+        dst = table[b] if out is None else out[b]
+        for h in range(2):
+            s, m = np.arange(n), np.arange(budget)
+            kept = kept_slots(w[table[b, s // page], h, s % page], budget, sink, recent)
+            for x, y in zip(after, before):
+                assert torch.equal(x[dst[m // page], h, m % page], y[table[b, kept // page], h, kept % page])
+
+
+@pytest.mark.parametrize("out", [False, True])
+def test_evict_of_more_slots_than_shared_memory_holds(out):
+    """8 CTAs hold 327680 weights; what lies behind is read from the pages each time."""
+    _evict(10 + out, 1, 256, [400003, 1000], 250001, 5, 1000, random_weights, out)
+    _evict(12 + out, 1, 64, [330001], 329000, 0, 0, few_values, out)
