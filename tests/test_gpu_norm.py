@@ -232,6 +232,24 @@ def test_norm_has_gradients_of_the_first_order_only():
         grads[0].float().sum().backward()
 
 
+def test_gradients_that_begin_anywhere():
+    """Outputs joined behind three other numbers: their gradients are slices whose rows lie
+    on no 16 bytes."""
+    g = _gen(11)
+    q, k = (_normal(g, 1, 2, 40, 64).requires_grad_() for _ in range(2))
+    wq, wk = (x.requires_grad_() for x in _weights(g, 2, 2, False))
+    prm = [torch.tensor(x, device="cuda").requires_grad_() for x in ([5.0, 20.0], [1.0, 0.5], [0.3, 2.5])]
+    v = _normal(g, 1, 2, 40, 64).requires_grad_()
+    up = _normal(g, 3 * 5120 + 3)
+    parts = [x.flatten() for x in (*qk_norm(q, k, wq, wk), bam_attention(v, v, v, *prm))]
+    leaves = (q, k, wq, wk, v, *prm)
+    got = torch.autograd.grad(torch.cat([torch.zeros_like(up[:3])] + parts), leaves, up, retain_graph=True)
+    want = torch.autograd.grad(parts, leaves, [up[3 + 5120 * i:][:5120].clone() for i in range(3)])
+    assert all(torch.equal(a, b) for a, b in zip(got[:4], want[:4]))
+    for a, b in zip(got[4:], want[4:]):  # dQ and the scalars' sums have no order of their own
+        torch.testing.assert_close(a.float(), b.float(), rtol=2.0 ** -6, atol=2.0 ** -6 * float(b.abs().max()))
+
+
 def test_norm_of_a_broadcast_input():
     """A batch of one, expanded: each copy's gradient, summed by autograd."""
     g = _gen(8)

@@ -18,6 +18,13 @@ import torch
 from . import bam_attn as ba
 
 
+def _rows_of(g):
+    """A gradient as the library reads it: bf16, contiguous, its first row on 16 bytes (one
+    of a slice may begin anywhere)."""
+    g = g.to(torch.bfloat16).contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 class BamAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, alpha, beta, mu, s, causal, ssmax, prior, eps, o_dtype):
@@ -31,9 +38,8 @@ class BamAttention(torch.autograd.Function):
     def backward(ctx, dO):
         q, k, v, o, lse, alpha, beta, mu, s = ctx.saved_tensors
         causal, ssmax, prior, eps = ctx.cfg
-        dO = dO.to(torch.bfloat16).contiguous()
         dq, dk, dv, da, db, dm, ds = ba.attention_backward(
-            q, k, v, o, lse, dO, alpha, beta, mu, s, eps=eps, causal=causal, ssmax=ssmax,
+            q, k, v, o, lse, _rows_of(dO), alpha, beta, mu, s, eps=eps, causal=causal, ssmax=ssmax,
             prior=prior)
         return (dq, dk, dv, da, db, dm, ds if s is not None else None,
                 None, None, None, None, None)
@@ -68,8 +74,8 @@ class QkNorm(torch.autograd.Function):
     def backward(ctx, dq_out, dk_out):
         q, k, q_weight, k_weight, positions = ctx.saved_tensors
         rope, eps = ctx.cfg
-        g = (x.to(torch.bfloat16).contiguous() for x in (dq_out, dk_out))
-        dq, dk, dqw, dkw = ba.qk_norm_backward(q, k, *g, q_weight, k_weight, positions, rope, eps)
+        dq, dk, dqw, dkw = ba.qk_norm_backward(q, k, _rows_of(dq_out), _rows_of(dk_out), q_weight, k_weight,
+                                               positions, rope, eps)
         return dq, dk, dqw, dkw, None, None, None
 
 
