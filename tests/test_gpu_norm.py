@@ -250,6 +250,27 @@ def test_gradients_that_begin_anywhere():
         torch.testing.assert_close(a.float(), b.float(), rtol=2.0 ** -6, atol=2.0 ** -6 * float(b.abs().max()))
 
 
+@pytest.mark.parametrize("per_head", [False, True])
+def test_infinite_gradients_reach_the_weights_as_themselves(per_head):
+    """dw is the sum of dn n: infinite where one of its terms is, NaN where two cancel, and
+    finite in every other place."""
+    g = _gen(12)
+    q, k = _normal(g, 2, 3, 700, 64), _normal(g, 2, 3, 700, 64)
+    wq, wk = _weights(g, 3, 3, per_head)
+    gq, gk = _normal(g, 2, 3, 700, 64), _normal(g, 2, 3, 700, 64)
+    q[1, 2, 650, 5], q[0, 1, 3, 9], q[1, 1, 600, 9], q[0, 2, 1, 20] = 1.0, 1.0, 1.0, -2.0
+    gq[1, 2, 650, 5] = gq[0, 1, 3, 9] = gq[0, 2, 1, 20] = float("inf")
+    gq[1, 1, 600, 9] = float("-inf")
+    _, _, dwq, dwk = ba.qk_norm_backward(q, k, gq, gk, wq, wk)
+    assert torch.isfinite(dwk).all()
+    want = torch.zeros(3, 64, device="cuda")
+    want[2, 5], want[1, 9], want[2, 20] = float("inf"), float("nan"), float("-inf")
+    want = want if per_head else want.sum(0)
+    bad = ~torch.isfinite(want)
+    torch.testing.assert_close(dwq[bad], want[bad], rtol=0, atol=0, equal_nan=True)
+    assert torch.isfinite(dwq[~bad]).all()
+
+
 def test_norm_of_a_broadcast_input():
     """A batch of one, expanded: each copy's gradient, summed by autograd."""
     g = _gen(8)

@@ -391,7 +391,8 @@ __global__ void __launch_bounds__(kFinishThreads) bam_qk_norm_finish_kernel(cons
       add_carried(sum, err, x.x);
       err += x.y;
     }
-    a.side[k].dw[h * kHeadDim + d] = sum + err;
+    // (the error of an infinite sum is NaN)
+    a.side[k].dw[h * kHeadDim + d] = isinf(sum) ? sum : sum + err;
   }
 }
 
