@@ -293,7 +293,8 @@ typedef struct {
 } bam_qk_norm;
 
 /* q: bf16 [B, H, T, D] and k: bf16 [B, Hkv, T, D] -> q_out, k_out of the same
- * shapes, ready for bam_attn_fwd (Hkv may be any number).  positions: device
+ * shapes; Hkv may be any number, and where it is H, dense outputs are what
+ * bam_attn_fwd takes.  positions: device
  * int32 [B, T], any values; NULL: token t has position t.  rope: NULL or dims
  * 0: no rotation.  strides: element strides over batch, head and token of q,
  * k, q_out and k_out (twelve values, multiples of 8, >= 0; rows of an output
@@ -335,7 +336,10 @@ size_t bam_qk_norm_workspace_size(int B, int H, int Hkv, int T, int D);
  * largest weights.  No other operator knows them: bam_kv_keep_paged leaves the
  * marks of a draft in its slots, and bam_attn_decode_paged and
  * bam_attn_decode_tree_paged take slots as positions, which they are as long as
- * no key has left and positions count up from 0.
+ * no key has left and positions count up from 0.  Weights are gathered by
+ * bam_attn_decode_shared_paged alone, one token a call: the tokens of a prompt
+ * have weight 0 until then, and an eviction right behind it keeps the lowest
+ * slots.
  * ------------------------------------------------------------------------- */
 
 typedef struct {
@@ -366,8 +370,8 @@ bam_status bam_kv_append_norm_paged(const void* k, const void* v, const void* q,
  *
  * prefix_table: device int32 [prefix_blocks], prefix_len: device int32 [1];
  * the shared prefix is the first prefix_len keys of these pages, at positions
- * 0 .. P-1.  Its keys and values are read once for all sequences.  Both NULL
- * and prefix_blocks 0: no prefix.  block_table, cache_lens: the own keys, 0 or
+ * 0 .. P-1.  Its keys and values are read once for every 128 rows (sequence and
+ * query head) of a key head.  Both NULL and prefix_blocks 0: no prefix.  block_table, cache_lens: the own keys, 0 or
  * more.  A sequence without any key gets o = 0 and lse = -infinity.
  *
  * Without marks (marks and q_pos NULL), own key j has position P + j and the
@@ -402,8 +406,10 @@ bam_status bam_attn_decode_shared_paged(const void* q, const void* k_pages, cons
                                         cudaStream_t stream);
 
 /* Bytes of workspace of bam_attn_decode_shared_paged: Pmax = prefix_blocks *
- * page, Tmax = max_blocks * page, max_pos of the marks (0 without).  Returns 0
- * for invalid sizes.  Host-only. */
+ * page, Tmax = max_blocks * page, max_pos of the marks (0 without).  More than 8
+ * rows of a key head over a prefix take 16 bytes for each query head and position:
+ * H times the larger of max_pos and Pmax (without marks Pmax + Tmax) has to stay
+ * below 2^31.  Returns 0 for invalid sizes.  Host-only. */
 size_t bam_attn_shared_workspace_size(int B, int H, int Hkv, int Pmax, int Tmax, int max_pos, int D);
 
 /* Eviction: of every sequence that has more than `budget` own keys, each key

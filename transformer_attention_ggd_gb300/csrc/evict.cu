@@ -15,7 +15,10 @@
 // Measured: 64 sequences, 12 heads, 4352 -> 4096 keys, to other pages: 290 us, of which 25 for
 // the choice (1.66 GB moved at 6.3 TB/s); one sequence, 12 heads, 131072 -> 65536: 104 us, 33 for the
 // choice, which is a chain of latencies: three digits of 5 us, each of a histogram and two meetings
-// of the cluster; 8 sequences of 600 -> 512: 10 us, two kernels of dependent steps.
+// of the cluster; 8 sequences of 600 -> 512: 10 us, two kernels of dependent steps.  In place, where keys
+// in front of the first that leaves stay where they are: 309 us with weights that all differ (94% of the rows
+// kept move: 1.5 GB), 125 where the ones that leave have equal weights and lie at the end (30%), 134 for the long
+// sequence (all), 18 for the small ones.
 #include "shared_common.cuh"
 
 namespace bam {
@@ -324,7 +327,8 @@ __global__ void __launch_bounds__(kSelThreads, 1280 / kSelThreads) bam_kv_evict_
 // are a cluster and go in waves: every CTA reads its rows of the wave, the
 // cluster meets, and they are written.  Row m goes from a slot >= m to slot m, so
 // that a row that is written was the source of an earlier row, if of any, which has
-// been read; the next wave's rows are on their way while this one's are written.
+// been read.  The numbers of the next wave's rows are on their way meanwhile; the rows
+// themselves are read behind this wave's writes.
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) bam_kv_evict_move_kernel(const EvictArgs a) {
   constexpr int kStep = kThreads / 8, kWave = kStep * kMoveRows;  // eight lanes a row
@@ -428,7 +432,8 @@ cudaError_t launch_evict_move(const EvictArgs& args, cudaStream_t st) {
     return launch_k(bam_kv_evict_move_kernel<128>, dim3(a.cluster * a.c.Hkv, a.c.B, 2), dim3(128), 0, st, true, a);
   }
   // Small CTAs for many short chains (16000 of 512 rows: 282 us, with large ones 345; 16 of them 21 and 15);
-  // else large ones (1536 of 4096 rows: 124 us, with small ones 133), and as many a chain as a cluster takes.
+  // else large ones (1536 of 4096 rows, 30% of which move: 125 us with the choice, with small ones 133), and as
+  // many a chain as a cluster takes.
   const bool many = chains >= 4 * sm_count() && a.budget <= 2048;
   while (a.cluster < kMaxCluster && chains * a.cluster < 2 * sm_count() &&
          a.budget > 512 * static_cast<int64_t>(a.cluster))

@@ -16,7 +16,7 @@
 //
 // Measured on the device: 4 x 16383 tokens, 32 and 8 heads, out of a projection's output:
 // forward 111 us (0.67 GB, 6.0 TB/s; a copy along the same path takes 101), backward
-// 168 us (1.0 GB, 6.0 TB/s); 8 x 512 tokens, 12 and 12 heads: 21 us both calls.
+// 167 us (1.0 GB, 6.0 TB/s); 8 x 512 tokens, 12 and 12 heads: 21 us both calls.
 #include "norm_common.cuh"
 
 namespace bam {

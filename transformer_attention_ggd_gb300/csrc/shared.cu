@@ -16,8 +16,8 @@
 // are needed (20 instructions and two special functions; windows of a table in order of
 // positions took 160 us where this takes 151).
 //
-// Measured: 64 caches of 8192 keys, 12 heads, with weights 150 us (0.85 GB, 5.7 TB/s); one of
-// 131072, 32 and 8 heads, fp32, 64 us; 4 sequences of 40 keys behind 1000, 12 heads, 11 us.
+// Measured: 64 caches of 8192 keys, 12 heads, with weights 151 us (0.85 GB, 5.7 TB/s); one of
+// 131072, 32 and 8 heads, 65 us, with fp32 output 71; 4 sequences of 40 keys behind 1000, 12 heads, 12 us.
 #include "shared_common.cuh"
 
 namespace bam {
